@@ -57,7 +57,8 @@ enum mla_device_error {
   MLA_DEVERR_TIMEOUT = 1,       /* a bounded on-chip wait gave up          */
   MLA_DEVERR_BAD_SEQ_LEN = 2,   /* seq_len > max_pages_per_seq*page_size   */
   MLA_DEVERR_BAD_BLOCK = 4,     /* block-table entry outside [0,num_blocks) */
-  MLA_DEVERR_BAD_QSL = 8        /* query_start_loc inconsistent with total_q */
+  MLA_DEVERR_BAD_QSL = 8,       /* query_start_loc inconsistent with total_q */
+  MLA_DEVERR_BAD_POSITION = 16  /* position outside the rotation table      */
 };
 
 /*
@@ -300,7 +301,7 @@ MLA_API int mla_v_up_proj(const void* o_lat, const void* w_uv, int64_t num_token
 
 /*
  * mla_proj_status -- copy the device error word of the projection kernels
- * (mla_q_absorb, mla_v_up_proj; OR of mla_device_error bits, 0 = clean) to
+ * (mla_q_absorb, mla_v_up_proj, mla_kv_up_proj; OR of mla_device_error bits, 0 = clean) to
  * *status, then clear it if `clear` is non-zero.  The word is shared by every
  * projection launched in the process on the current device.  Synchronises
  * `stream`.
@@ -401,6 +402,80 @@ MLA_API int mla_gather_cache(const void* cache, int64_t num_blocks, int page_siz
                              const int32_t* block_table, int max_pages_per_seq, const int32_t* cu_seq_lens,
                              const int32_t* seq_starts, int batch, void* dst, int64_t num_tokens, int32_t* status,
                              void* stream);
+
+/*
+ * mla_rope_cache_write -- append the latent rows of new tokens to the paged
+ * cache with the position rotation applied on the way, and rotate the rope
+ * part of the same tokens' queries.  With (cos_k, sin_k) = entries k and 32+k
+ * of row positions[t] of the table:
+ *
+ *   c_t         = kv_c_t                                        without norm_weight
+ *               = kv_c_t * norm_weight / sqrt(mean(kv_c_t^2) + norm_eps)   with it
+ *   rot(x)      : (x_i, x_j) -> (x_i cos_k - x_j sin_k, x_j cos_k + x_i sin_k), k < 32,
+ *                 (i, j) = (2k, 2k+1) if interleaved, else (k, k+32)
+ *   cache[slot] = [c_t | rot(k_pe_t)]     latent_t = [c_t | rot(k_pe_t)]
+ *   q_pe_out[t, h] = rot(q_pe[t, h])
+ *
+ * in float32, rounded once to the stored type (nearest even).
+ *   kv_c            bf16, 512 values per token at kv_c + t * kv_c_stride elements
+ *   k_pe            bf16, 64 values per token at k_pe + t * k_pe_stride (both may
+ *                   be column ranges of a wider projection output)
+ *   norm_weight     [512] bf16, or NULL: kv_c is stored as it is;  norm_eps
+ *                   finite and >= 0
+ *   positions       [num_tokens] int64.  A position outside [0, max_positions)
+ *                   sets MLA_DEVERR_BAD_POSITION in *status; nothing is written
+ *                   for that token
+ *   cos_sin         [max_positions, 64] float32, dense: 32 cosines, 32 sines
+ *   slot_mapping    [num_tokens] int64, as for mla_cache_write (a slot outside
+ *                   the cache is padding: no cache row is written, the latent
+ *                   row and the query still are).  Two tokens with the same slot
+ *                   in one call leave a row mixed of both
+ *   cache, num_blocks, page_size, cache_dtype, kv_scale: as for mla_cache_write;
+ *                   e4m3 codes are those of float32 value / kv_scale (the value
+ *                   is not rounded to bf16 first), saturated to +-448
+ *   latent          bf16 rows of 576 at latent + t * latent_stride, or NULL: the
+ *                   same rows for mla_kv_up_proj and mla_prefill (the layout of
+ *                   mla_gather_cache's dst).  May be the input rows themselves
+ *                   (latent == kv_c, k_pe == kv_c + 512, equal strides)
+ *   q_pe            bf16, 64 values of (t, h) at q_pe + t * q_token_stride +
+ *                   h * q_head_stride, or NULL (then q_pe_out is NULL too)
+ *   q_pe_out        the same with its own strides; may be q_pe itself (equal
+ *                   strides: in place), else it overlaps no other argument
+ *   status          one int32 on the device, or NULL: OR-ed into, never cleared
+ * All strides are multiples of 8 elements, all tensors 16-byte aligned.
+ * num_tokens in [0, 8388480]; 0 is a no-op.  One launch.
+ */
+MLA_API int mla_rope_cache_write(const void* kv_c, int64_t kv_c_stride, const void* k_pe, int64_t k_pe_stride,
+                                 const void* norm_weight, float norm_eps, const int64_t* positions,
+                                 const float* cos_sin, int64_t max_positions, int interleaved,
+                                 const int64_t* slot_mapping, int64_t num_tokens, void* cache, int64_t num_blocks,
+                                 int page_size, int cache_dtype, float kv_scale, void* latent,
+                                 int64_t latent_stride, const void* q_pe, int64_t q_token_stride,
+                                 int64_t q_head_stride, int num_heads, void* q_pe_out, int64_t q_out_token_stride,
+                                 int64_t q_out_head_stride, int* status, void* stream);
+
+/*
+ * mla_kv_up_proj -- every head's key and value from the shared latent rows,
+ * the first step of the expanded ("compute-friendly") form:
+ *
+ *   kv[t, n, d] = sum_l latent[t, l] * w[n, d, l]      l < 512
+ *
+ * float32 accumulation on the tensor cores, one rounding to bf16.
+ *   latent     bf16, 512 values per token at latent + t * latent_stride elements
+ *              (a multiple of 8, >= 512; 576 reads [kv_c | k_pe] rows as
+ *              mla_gather_cache and mla_rope_cache_write leave them)
+ *   w          [num_heads, head_dim, 512] bf16, dense: the weight of the
+ *              projection from the latent to all heads, one output row after the
+ *              other (for mla_prefill: 128 key rows, then 128 value rows a head)
+ *   kv         [num_tokens, num_heads, head_dim] bf16, dense; must not overlap
+ *              the inputs
+ *   head_dim   multiple of 8 in [8, 2048];  num_heads in [1, 1024];
+ *   num_tokens in [0, 8388480]; 0 is a no-op.  16-byte aligned tensors.
+ * One launch (a programmatic dependent of the previous kernel on `stream`).
+ * Device-side timeouts set MLA_DEVERR_TIMEOUT in the word mla_proj_status reads.
+ */
+MLA_API int mla_kv_up_proj(const void* latent, int64_t latent_stride, const void* w, int64_t num_tokens,
+                           int num_heads, int head_dim, void* kv, void* stream);
 
 /*
  * mla_set_decode_wait_test -- test aid for the failure detection of the

@@ -22,6 +22,7 @@ DEVERR_TIMEOUT = 1
 DEVERR_BAD_SEQ_LEN = 2
 DEVERR_BAD_BLOCK = 4
 DEVERR_BAD_QSL = 8
+DEVERR_BAD_POSITION = 16
 LKV = 512
 ROPE = 64
 DQK = 576
@@ -30,7 +31,8 @@ C_ABI_SYMBOLS = ("mla_cache_write", "mla_decode_workspace_size", "mla_decode", "
                  "mla_merge_states", "mla_last_error", "mla_device_sm_count", "mla_set_decode_timing_events",
                  "mla_decode_no_alloc", "mla_q_absorb", "mla_v_up_proj", "mla_proj_status",
                  "mla_gather_cache", "mla_quantize_fp8", "mla_decode_fp8q", "mla_set_decode_wait_test",
-                 "mla_decode_no_alloc_status", "mla_decode_step", "mla_decode_fp8q_step")
+                 "mla_decode_no_alloc_status", "mla_decode_step", "mla_decode_fp8q_step",
+                 "mla_rope_cache_write", "mla_kv_up_proj")
 NO_ALLOC_SCRATCH_BYTES = 96 << 20
 
 _lib = None
@@ -91,6 +93,11 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.mla_decode_step.restype = i32
     lib.mla_decode_step.argtypes = [P, P, P, i64, P, P, P, i64, i32, i32, f32, P, i32, P, i32, P, i32, i32, f32, i32,
                                     P, P, P, sz, P]
+    lib.mla_rope_cache_write.restype = i32
+    lib.mla_rope_cache_write.argtypes = [P, i64, P, i64, P, f32, P, P, i64, i32, P, i64, P, i64, i32, i32, f32, P, i64,
+                                         P, i64, i64, i32, P, i64, i64, P, P]
+    lib.mla_kv_up_proj.restype = i32
+    lib.mla_kv_up_proj.argtypes = [P, i64, P, i64, i32, i32, P, P]
     _lib = lib
     return lib
 
@@ -166,6 +173,90 @@ def cache_write(kv_c, k_pe, slot_mapping, cache, kv_scale: float = 1.0, stream=N
     _dense(k_pe, "k_pe", torch.bfloat16, (T, ROPE))
     _check(load().mla_cache_write(_ptr(kv_c), _ptr(k_pe), _ptr(slot_mapping), slot_mapping.numel(), _ptr(cache),
                                   nb, ps, _dtype_code(cache), float(kv_scale), _stream(stream)))
+
+
+def _rows(t, name: str, shape, writable: bool = False):
+    """Check a bf16 tensor whose last dimension is contiguous and whose other
+    dimensions may have any stride the library takes; returns those strides
+    (a dimension of size 1 counts as packed)."""
+    import torch
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be bfloat16, got {str(t.dtype).replace('torch.', '')}")
+    if t.dim() != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
+        exp = "[" + ", ".join("*" if w is None else str(w) for w in shape) + "]"
+        raise ValueError(f"{name} must have shape {exp}, got {tuple(t.shape)}")
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous, got strides {t.stride()}")
+    out, packed = [], t.shape[-1]
+    for d in range(t.dim() - 2, -1, -1):
+        n, st = t.shape[d], t.stride(d)
+        if n <= 1:
+            st = (packed + 7) // 8 * 8
+        elif st % 8 or (writable and st == 0):
+            raise ValueError(f"{name}'s strides must be multiples of 8 elements, got {t.stride()}")
+        out.append(st)
+        packed = max(packed, st * n)
+    return out[::-1]
+
+
+def _on_current_device(*tensors) -> None:
+    """Refuse tensors of another device than the current one: the call's
+    stream, tensor maps and launch belong to the current device."""
+    import torch
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"expected a CUDA tensor, got one on {t.device}")
+        if dev is None:
+            dev = torch.cuda.current_device()
+        if t.device.index != dev:
+            raise ValueError(f"every tensor must be on the current device cuda:{dev}, got one on {t.device}")
+
+
+def rope_cache_write(kv_c, k_pe, positions, cos_sin, slot_mapping, cache, *, q_pe=None, q_pe_out=None,
+                     norm_weight=None, norm_eps: float = 1e-6, interleaved: bool = True, kv_scale: float = 1.0,
+                     latent_out=None, status=None, stream=None) -> None:
+    """Append the latent rows of T new tokens to the cache, normalised (with
+    ``norm_weight`` [512]) and their shared key rotated by the token's
+    position; with ``q_pe`` [T, N, 64] the queries' rope parts are rotated into
+    ``q_pe_out`` (which may be ``q_pe`` itself), with ``latent_out`` [T, 576]
+    the rows are also written there in bf16.  ``kv_c`` [T, 512], ``k_pe`` [T, 64],
+    ``q_pe``, ``q_pe_out`` and ``latent_out`` may be column ranges of wider
+    tensors; ``cos_sin`` [max_positions, 64] float32 holds 32 cosines and 32
+    sines a row; ``positions`` and ``slot_mapping`` [T] are int64 (a negative
+    slot is padding).  A position outside the table sets DEVERR_BAD_POSITION in
+    ``status`` [1] int32 and nothing is written for its token."""
+    import torch
+    nb, ps, _ = _cache_checked(cache)
+    _dense(slot_mapping, "slot_mapping", torch.int64, dims=1)
+    T = slot_mapping.numel()
+    (kvs,) = _rows(kv_c, "kv_c", (T, LKV))
+    (pes,) = _rows(k_pe, "k_pe", (T, ROPE))
+    _dense(positions, "positions", torch.int64, (T,))
+    _dense(cos_sin, "cos_sin", torch.float32, (None, ROPE))
+    if norm_weight is not None:
+        _dense(norm_weight, "norm_weight", torch.bfloat16, (LKV,))
+    ls = 0
+    if latent_out is not None:
+        (ls,) = _rows(latent_out, "latent_out", (T, DQK), writable=True)
+    if (q_pe is None) != (q_pe_out is None):
+        raise ValueError("q_pe and q_pe_out are given together or not at all")
+    N, qs, qo = 0, (0, 0), (0, 0)
+    if q_pe is not None:
+        qs = _rows(q_pe, "q_pe", (T, None, ROPE))
+        N = q_pe.shape[1]
+        qo = _rows(q_pe_out, "q_pe_out", (T, N, ROPE), writable=True)
+    if status is not None:
+        _dense(status, "status", torch.int32, (1,))
+    _on_current_device(kv_c, k_pe, positions, cos_sin, slot_mapping, cache, q_pe, q_pe_out, norm_weight, latent_out,
+                       status)
+    _check(load().mla_rope_cache_write(_ptr(kv_c), kvs, _ptr(k_pe), pes, _ptr(norm_weight), float(norm_eps),
+                                       _ptr(positions), _ptr(cos_sin), cos_sin.shape[0], int(bool(interleaved)),
+                                       _ptr(slot_mapping), T, _ptr(cache), nb, ps, _dtype_code(cache),
+                                       float(kv_scale), _ptr(latent_out), ls, _ptr(q_pe), qs[0], qs[1], N,
+                                       _ptr(q_pe_out), qo[0], qo[1], _ptr(status), _stream(stream)))
 
 
 def decode_workspace_size(batch: int, total_q: int, num_heads: int, max_splits: int = 0) -> int:
@@ -352,6 +443,21 @@ def v_up_proj(o_lat, w_uv, out, stream=None) -> None:
     _dense(w_uv, "w_uv", torch.bfloat16, (N, LKV, None))
     _dense(out, "out", torch.bfloat16, (T, N, w_uv.shape[2]))
     _check(load().mla_v_up_proj(_ptr(o_lat), _ptr(w_uv), T, N, w_uv.shape[2], _ptr(out), _stream(stream)))
+
+
+def kv_up_proj(latent, w, kv, stream=None) -> None:
+    """kv[t, n, :] = w[n] @ latent[t] for every head (bf16): ``latent`` [T, 512]
+    (may be the first 512 columns of [kv_c | k_pe] rows), ``w`` [N, D, 512] (the
+    latent-to-heads projection's weight: for prefill D = 256, 128 key rows then
+    128 value rows a head), ``kv`` [T, N, D]."""
+    import torch
+    (ls,) = _rows(latent, "latent", (None, LKV))
+    T = latent.shape[0]
+    _dense(w, "w", torch.bfloat16, (None, None, LKV))
+    N, D = w.shape[0], w.shape[1]
+    _dense(kv, "kv", torch.bfloat16, (T, N, D))
+    _on_current_device(latent, w, kv)
+    _check(load().mla_kv_up_proj(_ptr(latent), ls, _ptr(w), T, N, D, _ptr(kv), _stream(stream)))
 
 
 def gather_cache(cache, block_table, cu_seq_lens, dst, seq_starts=None, kv_scale: float = 1.0, status=None,

@@ -471,8 +471,137 @@ int mla_quantize_fp8(const void* x, int64_t x_stride, int64_t rows, int width, f
 
 int mla_proj_status(int* status, int clear, void* stream) {
   if (!status) return fail(MLA_ERR_INVALID_ARG, "null pointer argument");
+  int kv = 0;
   cudaError_t e = mla::head_proj_status(status, clear, (cudaStream_t)stream);
+  if (e == cudaSuccess) e = mla::kv_proj_status(&kv, clear, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "projection status read");
+  *status |= kv;
+  return ok();
+}
+
+}  // extern "C"
+
+namespace {
+
+// [first byte, last byte + 1) of a strided tensor of `n0` x `n1` rows of
+// `width` elements (strides in elements).
+struct Extent {
+  uintptr_t lo, hi;
+};
+Extent extent(const void* p, int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t width, int64_t elem_bytes) {
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+  return Extent{lo, lo + (uintptr_t)(((n0 - 1) * s0 + (n1 - 1) * s1 + width) * elem_bytes)};
+}
+bool overlap(const Extent& a, const Extent& b) { return a.lo < b.hi && b.lo < a.hi; }
+
+constexpr int64_t kMaxStride = 1LL << 32;   // elements
+bool valid_stride(int64_t s, int64_t least) { return s >= least && s % 8 == 0 && s <= kMaxStride; }
+
+}  // namespace
+
+extern "C" {
+
+int mla_rope_cache_write(const void* kv_c, int64_t kv_c_stride, const void* k_pe, int64_t k_pe_stride,
+                         const void* norm_weight, float norm_eps, const int64_t* positions, const float* cos_sin,
+                         int64_t max_positions, int interleaved, const int64_t* slot_mapping, int64_t num_tokens,
+                         void* cache, int64_t num_blocks, int page_size, int cache_dtype, float kv_scale,
+                         void* latent, int64_t latent_stride, const void* q_pe, int64_t q_token_stride,
+                         int64_t q_head_stride, int num_heads, void* q_pe_out, int64_t q_out_token_stride,
+                         int64_t q_out_head_stride, int* status, void* stream) {
+  if (num_tokens < 0) return fail(MLA_ERR_INVALID_ARG, "num_tokens must be >= 0 (got %lld)", (long long)num_tokens);
+  if (num_tokens > 65535LL * 128) return fail(MLA_ERR_UNSUPPORTED, "num_tokens must be <= 8388480");
+  if (cache_dtype != MLA_BF16 && cache_dtype != MLA_FP8_E4M3)
+    return fail(MLA_ERR_INVALID_ARG, "cache_dtype must be MLA_BF16 or MLA_FP8_E4M3 (got %d)", cache_dtype);
+  if (page_size <= 0 || num_blocks <= 0 || num_blocks > (1LL << 40) / page_size)
+    return fail(MLA_ERR_INVALID_ARG, "page_size and num_blocks must be positive and num_blocks * page_size <= 2^40");
+  if (max_positions <= 0) return fail(MLA_ERR_INVALID_ARG, "max_positions must be positive");
+  if (cache_dtype == MLA_FP8_E4M3 && !(std::isfinite(kv_scale) && kv_scale > 0.f))
+    return fail(MLA_ERR_INVALID_ARG, "kv_scale must be finite and > 0 for an fp8 cache");
+  if (norm_weight && !(std::isfinite(norm_eps) && norm_eps >= 0.f))
+    return fail(MLA_ERR_INVALID_ARG, "norm_eps must be finite and >= 0");
+  if (!q_pe != !q_pe_out) return fail(MLA_ERR_INVALID_ARG, "q_pe and q_pe_out are given together or not at all");
+  if (q_pe && (num_heads < 1 || num_heads > 1024)) return fail(MLA_ERR_INVALID_ARG, "num_heads must be in [1, 1024]");
+  if (num_tokens == 0) return ok();
+  if (!kv_c || !k_pe || !positions || !cos_sin || !slot_mapping || !cache)
+    return fail(MLA_ERR_INVALID_ARG, "null pointer argument");
+  if (!aligned(kv_c, 16) || !aligned(k_pe, 16) || !aligned(cache, 16) || !aligned(cos_sin, 16) ||
+      !aligned(norm_weight, 16) || !aligned(latent, 16) || !aligned(q_pe, 16) || !aligned(q_pe_out, 16))
+    return fail(MLA_ERR_INVALID_ARG, "tensors must be 16-byte aligned");
+  if (!aligned(positions, 8) || !aligned(slot_mapping, 8) || !aligned(status, 4))
+    return fail(MLA_ERR_INVALID_ARG, "positions and slot_mapping must be 8-byte aligned, status 4-byte aligned");
+  if (!valid_stride(kv_c_stride, 0) || !valid_stride(k_pe_stride, 0))
+    return fail(MLA_ERR_INVALID_ARG, "kv_c_stride and k_pe_stride must be multiples of 8 in [0, 2^32]");
+  if (latent && !valid_stride(latent_stride, mla::kDqk))
+    return fail(MLA_ERR_INVALID_ARG, "latent_stride must be a multiple of 8 in [576, 2^32]");
+  const Extent ec = extent(cache, 1, 0, 1, 0, num_blocks * page_size * mla::kDqk, cache_dtype == MLA_BF16 ? 2 : 1);
+  const Extent ek = extent(kv_c, num_tokens, kv_c_stride, 1, 0, mla::kLkv, 2);
+  const Extent ep = extent(k_pe, num_tokens, k_pe_stride, 1, 0, mla::kRope, 2);
+  if (overlap(ec, ek) || overlap(ec, ep)) return fail(MLA_ERR_INVALID_ARG, "the cache must not overlap the inputs");
+  Extent el{0, 0};
+  if (latent) {
+    el = extent(latent, num_tokens, latent_stride, 1, 0, mla::kDqk, 2);
+    // in place: the latent rows are the input rows themselves
+    const bool same = latent == kv_c && static_cast<const char*>(k_pe) == static_cast<char*>(latent) + 2 * mla::kLkv &&
+                      (num_tokens == 1 || (latent_stride == kv_c_stride && latent_stride == k_pe_stride));
+    if (overlap(el, ec) || (!same && (overlap(el, ek) || overlap(el, ep))))
+      return fail(MLA_ERR_INVALID_ARG, "latent must not overlap the cache, nor the inputs unless it is their rows");
+  }
+  mla::RopeWriteArgs w{kv_c,          kv_c_stride,   k_pe,       k_pe_stride,
+                       norm_weight,   norm_eps,      positions,  cos_sin,
+                       max_positions, slot_mapping,  num_tokens, cache,
+                       num_blocks * page_size, kv_scale, latent, latent_stride,
+                       q_pe,          q_token_stride, q_head_stride, q_pe_out,
+                       q_out_token_stride, q_out_head_stride, num_heads, status};
+  if (q_pe) {
+    if (!valid_stride(q_token_stride, 0) || !valid_stride(q_head_stride, 0))
+      return fail(MLA_ERR_INVALID_ARG, "q_pe strides must be multiples of 8 in [0, 2^32]");
+    // the written rows lie apart: heads inside tokens or tokens inside heads
+    if (!valid_stride(q_out_token_stride, mla::kRope) || !valid_stride(q_out_head_stride, mla::kRope) ||
+        !(q_out_token_stride >= (num_heads - 1) * q_out_head_stride + mla::kRope || num_tokens == 1 ||
+          q_out_head_stride >= (num_tokens - 1) * q_out_token_stride + mla::kRope || num_heads == 1))
+      return fail(MLA_ERR_INVALID_ARG, "q_pe_out strides must be multiples of 8 that keep its rows of 64 apart");
+    const Extent eq = extent(q_pe, num_tokens, q_token_stride, num_heads, q_head_stride, mla::kRope, 2);
+    const Extent eo = extent(q_pe_out, num_tokens, q_out_token_stride, num_heads, q_out_head_stride, mla::kRope, 2);
+    const bool same = q_pe == q_pe_out && (num_tokens == 1 || q_token_stride == q_out_token_stride) &&
+                      (num_heads == 1 || q_head_stride == q_out_head_stride);
+    if ((!same && overlap(eq, eo)) || overlap(eo, ec) || overlap(eo, ek) || overlap(eo, ep) || overlap(eq, ec) ||
+        (latent && (overlap(el, eo) || overlap(el, eq))))
+      return fail(MLA_ERR_INVALID_ARG, "q_pe_out must be q_pe itself or overlap no other argument");
+  }
+  cudaError_t e = mla::launch_rope_write(w, cache_dtype == MLA_FP8_E4M3, interleaved != 0, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "rotated cache write launch");
+  return ok();
+}
+
+int mla_kv_up_proj(const void* latent, int64_t latent_stride, const void* w, int64_t num_tokens, int num_heads,
+                   int head_dim, void* kv, void* stream) {
+  if (num_tokens < 0) return fail(MLA_ERR_INVALID_ARG, "num_tokens must be >= 0 (got %lld)", (long long)num_tokens);
+  if (num_tokens > 65535LL * 128) return fail(MLA_ERR_UNSUPPORTED, "num_tokens must be <= 8388480");
+  if (num_heads < 1 || num_heads > 1024) return fail(MLA_ERR_INVALID_ARG, "num_heads must be in [1, 1024]");
+  if (head_dim < 8 || head_dim > 2048 || head_dim % 8 != 0)
+    return fail(MLA_ERR_UNSUPPORTED, "head_dim must be a multiple of 8 in [8, 2048] (got %d)", head_dim);
+  if (num_tokens == 0) return ok();
+  if (!latent || !w || !kv) return fail(MLA_ERR_INVALID_ARG, "null pointer argument");
+  if (!aligned(latent, 16) || !aligned(w, 16) || !aligned(kv, 16))
+    return fail(MLA_ERR_INVALID_ARG, "tensors must be 16-byte aligned");
+  if (!valid_stride(latent_stride, mla::kLkv))
+    return fail(MLA_ERR_INVALID_ARG, "latent_stride must be a multiple of 8 in [512, 2^32]");
+  const int64_t C = (int64_t)num_heads * head_dim;
+  const Extent ek = extent(kv, 1, 0, 1, 0, num_tokens * C, 2);
+  if (overlap(ek, extent(latent, num_tokens, latent_stride, 1, 0, mla::kLkv, 2)) ||
+      overlap(ek, extent(w, 1, 0, 1, 0, C * mla::kLkv, 2)))
+    return fail(MLA_ERR_INVALID_ARG, "kv must not overlap the inputs");
+  const int sms = sm_count();
+  if (sms < 1) return fail(MLA_ERR_CUDA, "cannot query the current device");
+  const mla::KvProjShape p = mla::kv_proj_shape(num_tokens, C, sms);
+  CUtensorMap tm_x, tm_w;
+  if (!mla::encode_tmap_2d(&tm_x, latent, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, mla::kLkv, (uint64_t)num_tokens,
+                           (uint64_t)latent_stride * 2, 64, (uint32_t)p.xrows, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !mla::encode_tmap_2d(&tm_w, w, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, mla::kLkv, (uint64_t)C, mla::kLkv * 2, 64,
+                           (uint32_t)p.bn, CU_TENSOR_MAP_SWIZZLE_128B))
+    return fail(MLA_ERR_CUDA, "cuTensorMapEncodeTiled rejected a tensor layout");
+  cudaError_t e = mla::launch_kv_proj(tm_x, tm_w, kv, num_tokens, C, p, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "key/value projection launch");
   return ok();
 }
 

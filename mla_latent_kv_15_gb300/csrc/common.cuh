@@ -161,7 +161,48 @@ struct QuantArgs {
   uint8_t* q8;
 };
 
+// A step's rows for mla_rope_cache_write: per token the raw latent row (kv_c
+// 512 bf16 at kv_c + t * kv_c_stride, k_pe 64 at k_pe + t * k_pe_stride), its
+// position (row of the [max_positions, 64] table of 32 cosines and 32 sines)
+// and cache slot; optional: the norm weight, the bf16 latent rows and the
+// query's rope parts.  Strides in elements.
+struct RopeWriteArgs {
+  const void* kv_c;
+  int64_t kv_c_stride;
+  const void* k_pe;
+  int64_t k_pe_stride;
+  const void* norm_weight;    // bf16 [512] or null: no norm
+  float norm_eps;
+  const int64_t* positions;
+  const float* cos_sin;
+  int64_t max_positions;
+  const int64_t* slots;
+  int64_t num_tokens;
+  void* cache;
+  int64_t num_slots;
+  float kv_scale;
+  void* latent;               // bf16 rows of 576 or null
+  int64_t latent_stride;
+  const void* q_pe;           // bf16 [tokens, heads, 64] strided, or null
+  int64_t q_token_stride, q_head_stride;
+  void* q_out;
+  int64_t qo_token_stride, qo_head_stride;
+  int num_heads;
+  int* status;                // OR of mla_device_error bits, or null
+};
+
+// Tile of mla_kv_up_proj for a shape: columns and token-box rows of a CTA.
+struct KvProjShape {
+  int bn, xrows;
+};
+
 // ---- launchers (return cudaError_t of the launch)
+cudaError_t launch_rope_write(const RopeWriteArgs& w, int fp8, int pairs, cudaStream_t s);
+KvProjShape kv_proj_shape(int64_t T, int64_t C, int sms);
+// y[t, c] = x[t, :] . w[c, :] (2-D tensor maps with 128-byte swizzle: x boxes
+// 64 x shape.xrows, w boxes 64 x shape.bn)
+cudaError_t launch_kv_proj(const CUtensorMap& tm_x, const CUtensorMap& tm_w, void* y, int64_t T, int64_t C,
+                           const KvProjShape& shape, cudaStream_t s);
 // group_rows: query rows per group, a power of two (128; 32 for the small-rows decode variant)
 // write: the step's cache rows, quant: the step's query quantisation, both
 // done by extra blocks of the same launch (nullptr: none; quant needs an
@@ -199,5 +240,6 @@ cudaError_t launch_gather(const void* cache, int64_t num_blocks, int page_size, 
                           const int32_t* seq_starts, int batch, void* dst, int64_t num_tokens, int32_t* status,
                           cudaStream_t s);
 cudaError_t head_proj_status(int* status, int clear, cudaStream_t s);
+cudaError_t kv_proj_status(int* status, int clear, cudaStream_t s);
 
 }  // namespace mla
