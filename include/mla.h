@@ -478,6 +478,68 @@ MLA_API int mla_kv_up_proj(const void* latent, int64_t latent_stride, const void
                            int num_heads, int head_dim, void* kv, void* stream);
 
 /*
+ * mla_prefill_workspace_size -- bytes of device workspace mla_prefill needs
+ * for `batch` sequences, `total_q` query rows in all, `num_heads` heads and a
+ * num_splits <= max_splits (0: automatic only).  Depends on sizes only.
+ */
+MLA_API size_t mla_prefill_workspace_size(int batch, int total_q, int num_heads, int max_splits);
+
+/*
+ * mla_prefill -- attention in the expanded form over packed sequences, for
+ * prompts, chunks of prompts and cached contexts: with query rows
+ * cu_q[b]..cu_q[b+1] and key rows cu_kv[b]..cu_kv[b+1] of sequence b (Sq and
+ * Sk of them), for every head h and local query row i
+ *
+ *   s_j  = scale * (q[i,h,:128] . kv[j,h,:128] + q[i,h,128:] . k_pe[j])
+ *   out  = sum_j softmax(s)_j kv[j,h,128:]       lse = ln sum_j exp(s_j)
+ *
+ * over keys j < Sk - Sq + 1 + i with `causal` (the last query row sees every
+ * key: new tokens behind a cached context, as in mla_decode) and j < Sk
+ * without (a context chunk, to be joined by mla_merge_states).  Rows that see
+ * no key get out = 0 and lse = -inf.  Query rows outside every sequence are
+ * not written.  Scores, softmax and sums are float32; the probabilities are
+ * rounded to bf16 for their product with the values.
+ *   q           bf16, the 192 values [nope | rotated] of (t, h) at
+ *               q + t * q_token_stride + h * q_head_stride
+ *   kv          bf16, the 256 values [k_nope | v] of (t, h) at
+ *               kv + t * kv_token_stride + h * kv_head_stride
+ *               (mla_kv_up_proj's output with head_dim 256: strides 256 * heads, 256)
+ *   k_pe        bf16, 64 rotated values per key row at k_pe + t * k_pe_stride,
+ *               shared by all heads (columns 512.. of latent rows: stride 576)
+ *               All strides in elements: multiples of 8 in [8, 2^32].
+ *   cu_q, cu_kv [batch + 1] int32 on the device, non-decreasing, within
+ *               [0, total_q] and [0, total_kv].  Otherwise MLA_DEVERR_BAD_QSL (cu_q)
+ *               or MLA_DEVERR_BAD_SEQ_LEN (cu_kv) is set and nothing is written
+ *   total_q, total_kv  rows of q and out, of kv and k_pe;  <= 2^30,
+ *               total_q * num_heads < 2^31
+ *   scale       finite and > 0
+ *   num_splits  0: long key ranges are split where that balances the SMs;
+ *               k > 0: every block of query rows is cut into min(k, tiles) pieces
+ *   out         [total_q, num_heads, 128] bf16, dense; overlaps no input
+ *   lse         [total_q, num_heads] float32, or NULL
+ *   workspace   >= mla_prefill_workspace_size(batch, total_q, num_heads,
+ *               num_splits) bytes, 256-byte aligned; scratch only.  Calls that
+ *               may overlap on the GPU need a workspace each
+ * A value that is not finite makes the rows that see its key not finite; in
+ * keys a row does not see it has no effect on the row.
+ * batch == 0 or total_q == 0 is a no-op.  Three launches (plan, attention,
+ * join), nothing of which depends on device data: a captured call may be
+ * replayed over other lengths.
+ */
+MLA_API int mla_prefill(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* kv,
+                        int64_t kv_token_stride, int64_t kv_head_stride, const void* k_pe, int64_t k_pe_stride,
+                        const int32_t* cu_q, const int32_t* cu_kv, int batch, int total_q, int total_kv,
+                        int num_heads, float scale, int causal, int num_splits, void* out, float* lse,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * mla_prefill_status -- copy the device error word of the last mla_prefill
+ * that used `workspace` (OR of mla_device_error bits; 0 = clean) to *status.
+ * Synchronises `stream`.  The word is cleared by every mla_prefill.
+ */
+MLA_API int mla_prefill_status(const void* workspace, int* status, void* stream);
+
+/*
  * mla_set_decode_wait_test -- test aid for the failure detection of the
  * decode kernels (the pages have no counterpart).  Every mbarrier wait inside
  * a decode is bounded in wall time; when one runs out, the CTA records

@@ -32,7 +32,8 @@ C_ABI_SYMBOLS = ("mla_cache_write", "mla_decode_workspace_size", "mla_decode", "
                  "mla_decode_no_alloc", "mla_q_absorb", "mla_v_up_proj", "mla_proj_status",
                  "mla_gather_cache", "mla_quantize_fp8", "mla_decode_fp8q", "mla_set_decode_wait_test",
                  "mla_decode_no_alloc_status", "mla_decode_step", "mla_decode_fp8q_step",
-                 "mla_rope_cache_write", "mla_kv_up_proj")
+                 "mla_rope_cache_write", "mla_kv_up_proj", "mla_prefill_workspace_size", "mla_prefill",
+                 "mla_prefill_status")
 NO_ALLOC_SCRATCH_BYTES = 96 << 20
 
 _lib = None
@@ -96,6 +97,13 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.mla_rope_cache_write.restype = i32
     lib.mla_rope_cache_write.argtypes = [P, i64, P, i64, P, f32, P, P, i64, i32, P, i64, P, i64, i32, i32, f32, P, i64,
                                          P, i64, i64, i32, P, i64, i64, P, P]
+    lib.mla_prefill_workspace_size.restype = sz
+    lib.mla_prefill_workspace_size.argtypes = [i32, i32, i32, i32]
+    lib.mla_prefill.restype = i32
+    lib.mla_prefill.argtypes = [P, i64, i64, P, i64, i64, P, i64, P, P, i32, i32, i32, i32, f32, i32, i32, P, P, P, sz,
+                                P]
+    lib.mla_prefill_status.restype = i32
+    lib.mla_prefill_status.argtypes = [P, ctypes.POINTER(ctypes.c_int), P]
     lib.mla_kv_up_proj.restype = i32
     lib.mla_kv_up_proj.argtypes = [P, i64, P, i64, i32, i32, P, P]
     _lib = lib
@@ -458,6 +466,48 @@ def kv_up_proj(latent, w, kv, stream=None) -> None:
     _dense(kv, "kv", torch.bfloat16, (T, N, D))
     _on_current_device(latent, w, kv)
     _check(load().mla_kv_up_proj(_ptr(latent), ls, _ptr(w), T, N, D, _ptr(kv), _stream(stream)))
+
+
+def prefill_workspace_size(batch: int, total_q: int, num_heads: int, max_splits: int = 0) -> int:
+    return int(load().mla_prefill_workspace_size(batch, total_q, num_heads, max_splits))
+
+
+def prefill(q, kv, k_pe, cu_q, cu_kv, out, workspace, *, scale: float, causal: bool = True, lse=None,
+            num_splits: int = 0, stream=None) -> None:
+    """Expanded attention of packed sequences: ``q`` [T, N, 192], ``kv``
+    [Tk, N, 256] ([k_nope | v], kv_up_proj's output) and ``k_pe`` [Tk, 64] (the
+    rotated keys all heads share; all three may be column ranges of wider
+    tensors or have permuted strides), sequence b in query rows
+    cu_q[b]..cu_q[b+1] and key rows cu_kv[b]..cu_kv[b+1] (int32 prefix sums),
+    into ``out`` [T, N, 128] and ``lse`` [T, N].  With ``causal`` the last query
+    row of a sequence sees all its keys, the one before it one less, and so
+    on; without, every row sees every key."""
+    import torch
+    qs = _rows(q, "q", (None, None, 192))
+    T, N = q.shape[0], q.shape[1]
+    ks = _rows(kv, "kv", (None, N, 256))
+    Tk = kv.shape[0]
+    (ps,) = _rows(k_pe, "k_pe", (Tk, ROPE))
+    _dense(cu_q, "cu_q", torch.int32, dims=1)
+    B = cu_q.numel() - 1
+    if B < 0:
+        raise ValueError("cu_q must hold at least one entry")
+    _dense(cu_kv, "cu_kv", torch.int32, (B + 1,))
+    _dense(out, "out", torch.bfloat16, (T, N, 128))
+    if lse is not None:
+        _dense(lse, "lse", torch.float32, (T, N))
+    _dense(workspace, "workspace", (workspace.dtype,))
+    _on_current_device(q, kv, k_pe, cu_q, cu_kv, out, workspace, lse)
+    _check(load().mla_prefill(_ptr(q), qs[0], qs[1], _ptr(kv), ks[0], ks[1], _ptr(k_pe), ps, _ptr(cu_q), _ptr(cu_kv),
+                              B, T, Tk, N, float(scale), int(bool(causal)), int(num_splits), _ptr(out), _ptr(lse),
+                              _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def prefill_status(workspace, stream=None) -> int:
+    """Device error word of the last prefill that used ``workspace`` (OR of the DEVERR_* bits)."""
+    st = ctypes.c_int(0)
+    _check(load().mla_prefill_status(_ptr(workspace), ctypes.byref(st), _stream(stream)))
+    return st.value
 
 
 def gather_cache(cache, block_table, cu_seq_lens, dst, seq_starts=None, kv_scale: float = 1.0, status=None,

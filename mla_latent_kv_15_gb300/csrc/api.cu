@@ -10,6 +10,7 @@
 
 #include "../../include/mla.h"
 #include "common.cuh"
+#include "prefill.cuh"
 #include "tmap.cuh"
 
 namespace {
@@ -603,6 +604,103 @@ int mla_kv_up_proj(const void* latent, int64_t latent_stride, const void* w, int
   cudaError_t e = mla::launch_kv_proj(tm_x, tm_w, kv, num_tokens, C, p, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "key/value projection launch");
   return ok();
+}
+
+size_t mla_prefill_workspace_size(int batch, int total_q, int num_heads, int max_splits) {
+  if (batch <= 0 || total_q <= 0 || num_heads <= 0 || max_splits < 0) return 0;
+  return mla::prefill_layout(batch, total_q, num_heads, max_splits).total;
+}
+
+int mla_prefill(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* kv, int64_t kv_token_stride,
+                int64_t kv_head_stride, const void* k_pe, int64_t k_pe_stride, const int32_t* cu_q,
+                const int32_t* cu_kv, int batch, int total_q, int total_kv, int num_heads, float scale, int causal,
+                int num_splits, void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  if (batch < 0 || total_q < 0 || total_kv < 0)
+    return fail(MLA_ERR_INVALID_ARG, "batch, total_q and total_kv must be >= 0");
+  if (num_heads < 1 || num_heads > 1024) return fail(MLA_ERR_INVALID_ARG, "num_heads must be in [1, 1024]");
+  if (!std::isfinite(scale) || scale <= 0.f) return fail(MLA_ERR_INVALID_ARG, "scale must be finite and > 0");
+  if (num_splits < 0 || num_splits > 4096) return fail(MLA_ERR_INVALID_ARG, "num_splits must be in [0, 4096]");
+  if (batch == 0 || total_q == 0) return ok();
+  if (total_kv > (1 << 30) || total_q > (1 << 30))
+    return fail(MLA_ERR_UNSUPPORTED, "total_q and total_kv must be <= 2^30");
+  if ((int64_t)total_q * num_heads >= ((int64_t)1 << 31) - 1024)
+    return fail(MLA_ERR_INVALID_ARG, "total_q * num_heads must be below 2^31");
+  if (!q || !cu_q || !cu_kv || !out || !workspace || (total_kv > 0 && (!kv || !k_pe)))
+    return fail(MLA_ERR_INVALID_ARG, "null pointer argument");
+  if (!aligned(q, 16) || !aligned(kv, 16) || !aligned(k_pe, 16) || !aligned(out, 16))
+    return fail(MLA_ERR_INVALID_ARG, "q, kv, k_pe and out must be 16-byte aligned");
+  if (!aligned(cu_q, 4) || !aligned(cu_kv, 4) || !aligned(lse, 4))
+    return fail(MLA_ERR_INVALID_ARG, "cu_q, cu_kv and lse must be 4-byte aligned");
+  if (!aligned(workspace, 256)) return fail(MLA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  if (!valid_stride(q_token_stride, 8) || !valid_stride(q_head_stride, 8) || !valid_stride(kv_token_stride, 8) ||
+      !valid_stride(kv_head_stride, 8) || !valid_stride(k_pe_stride, 8))
+    return fail(MLA_ERR_INVALID_ARG, "strides must be multiples of 8 in [8, 2^32]");
+  const int qd = mla::kNope + mla::kRope, kvd = 2 * mla::kNope;
+  const Extent eo = extent(out, 1, 0, 1, 0, (int64_t)total_q * num_heads * mla::kNope, 2);
+  if (overlap(eo, extent(q, total_q, q_token_stride, num_heads, q_head_stride, qd, 2)) ||
+      (total_kv > 0 && (overlap(eo, extent(kv, total_kv, kv_token_stride, num_heads, kv_head_stride, kvd, 2)) ||
+                        overlap(eo, extent(k_pe, total_kv, k_pe_stride, 1, 0, mla::kRope, 2)))))
+    return fail(MLA_ERR_INVALID_ARG, "out must not overlap the inputs");
+  const mla::PrefillLayout L = mla::prefill_layout(batch, total_q, num_heads, num_splits);
+  if (L.max_part_rows >= 1LL << 31) return fail(MLA_ERR_UNSUPPORTED, "total_q * num_heads * num_splits must be below 2^31");
+  if (workspace_bytes < L.total)
+    return fail(MLA_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu required", workspace_bytes, L.total);
+  const int sms = sm_count();
+  if (sms < 1) return fail(MLA_ERR_CUDA, "cannot query the current device");
+
+  CUtensorMap tm_q, tm_kv, tm_pe;
+  bool enc = mla::encode_tmap_3d(&tm_q, q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (uint64_t)qd, (uint64_t)num_heads,
+                                 (uint64_t)total_q, (uint64_t)q_head_stride * 2, (uint64_t)q_token_stride * 2, 64, 1,
+                                 mla::kPrefillTile, CU_TENSOR_MAP_SWIZZLE_128B);
+  tm_kv = tm_pe = tm_q;   // without a key no tile is loaded
+  if (total_kv > 0)
+    enc = enc &&
+          mla::encode_tmap_3d(&tm_kv, kv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (uint64_t)kvd, (uint64_t)num_heads,
+                              (uint64_t)total_kv, (uint64_t)kv_head_stride * 2, (uint64_t)kv_token_stride * 2, 64, 1,
+                              mla::kPrefillTile, CU_TENSOR_MAP_SWIZZLE_128B) &&
+          mla::encode_tmap_2d(&tm_pe, k_pe, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, mla::kRope, (uint64_t)total_kv,
+                              (uint64_t)k_pe_stride * 2, 64, mla::kPrefillTile, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (!enc) return fail(MLA_ERR_CUDA, "cuTensorMapEncodeTiled rejected a tensor layout");
+
+  mla::PrefillArgs a{};
+  a.q = q;
+  a.q_token_stride = q_token_stride;
+  a.q_head_stride = q_head_stride;
+  a.kv = kv;
+  a.kv_token_stride = kv_token_stride;
+  a.kv_head_stride = kv_head_stride;
+  a.k_pe = k_pe;
+  a.k_pe_stride = k_pe_stride;
+  a.cu_q = cu_q;
+  a.cu_kv = cu_kv;
+  a.batch = batch;
+  a.total_q = total_q;
+  a.total_kv = total_kv;
+  a.num_heads = num_heads;
+  a.causal = causal != 0;
+  a.num_splits = num_splits;
+  // as many heads side by side as keep their keys and values in 48 MB of L2
+  const int64_t head_bytes = (int64_t)total_kv * kvd * 2 + 1;
+  const int64_t fit = (48LL << 20) / head_bytes;
+  a.group_heads = (int)(fit < 1 ? 1 : fit > num_heads ? num_heads : fit);
+  a.ctas = sms < mla::kPrefillMaxCtas ? sms : mla::kPrefillMaxCtas;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.out = out;
+  a.lse = lse;
+  a.wait_limit_ns = g_wait_limit_ns;
+  a.plan = mla::prefill_plan_from(workspace, L);
+  cudaStream_t s = (cudaStream_t)stream;
+  cudaError_t e = mla::launch_prefill_plan(a, s);
+  if (e != cudaSuccess) return cuda_fail(e, "prefill plan launch");
+  e = mla::launch_prefill(tm_q, tm_kv, tm_pe, a, s);
+  if (e != cudaSuccess) return cuda_fail(e, "prefill launch");
+  e = mla::launch_prefill_combine(a, s);
+  if (e != cudaSuccess) return cuda_fail(e, "prefill combine launch");
+  return ok();
+}
+
+int mla_prefill_status(const void* workspace, int* status, void* stream) {
+  return mla_decode_status(workspace, status, stream);   // the header's first word, as a decode's
 }
 
 }  // extern "C"

@@ -1,0 +1,568 @@
+// Expanded latent attention (mla_prefill) on tcgen05: packed sequences, every
+// head with its own 128-wide key and value and one 64-wide rotated key shared
+// by all heads.
+//
+//   s_ij = scale * (q_nope_i . k_nope_j + q_pe_i . k_pe_j)
+//   out_i = sum_j exp(s_ij - m_i) v_j / sum_j exp(s_ij - m_i)
+//
+// One CTA per SM takes items (256 query rows of a head x a range of keys) and
+// holds two 128-row query tiles in shared memory.  Keys and values stream in
+// tiles of 128 as 16 KB chunks of 64 dims (three of the key, the last one from
+// the shared rotated keys, two of the value) through a ring of eight.  Tensor
+// memory: scores S0, S1 and outputs O0, O1, 128 columns each; a tile's
+// probabilities (bf16) overwrite its scores.  One thread issues, per key tile,
+//   O0 += P0 V_j,  S0 = Q0 K_{j+1},  O1 += P1 V_j,  S1 = Q1 K_{j+1}
+// so the tensor cores work on one query tile while the softmax warps of the
+// other turn its scores into probabilities.  The softmax thread of a row
+// keeps the running reference m and sum in float32 and scales O in place,
+// but only when a row's maximum has risen by more than 2^8 over the
+// reference, which leaves the result the same and is rare.  P is rounded to
+// bf16 for the product (the sum is of the unrounded values).
+#include <cuda_bf16.h>
+
+#include "prefill.cuh"
+#include "ptx.cuh"
+
+namespace mla {
+namespace {
+using namespace ptx;
+
+constexpr int kSoftmaxWarps = 8;                  // 0-3: query tile 0, 4-7: query tile 1
+constexpr int kWarpLoad = 8, kWarpMma = 9;        // warps 10, 11 only fill the warpgroup
+constexpr int kThreads = 384;
+constexpr uint32_t kRegsSoftmax = 216, kRegsOther = 72;
+static_assert(128 * (2 * kRegsSoftmax + kRegsOther) <= kThreads * 168, "register split of the launch's 168 a thread");
+
+constexpr uint32_t kChunk = 16384;                // 128 rows x 64 dims
+constexpr int kRing = 8;
+constexpr uint32_t kQTile = 3 * kChunk;
+constexpr uint32_t kColS = 0, kColO = 256;        // S0 S1 O0 O1
+constexpr float kRescale = 8.0f;                  // log2 units
+
+struct Bars {
+  uint64_t full[kRing], empty[kRing];
+  uint64_t q_full[2], q_empty[2];
+  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+};
+constexpr size_t kSmem = 1024 + 2 * kQTile + kRing * kChunk + sizeof(Bars);
+static_assert(kSmem <= 232448, "shared memory per CTA");
+
+struct Ctx {
+  Bars* bars;
+  int* status;
+  uint64_t limit_ns;
+};
+
+// Bounded waits; once one has run out, every later one returns at once.
+__device__ __forceinline__ void wait_bar(const Ctx& c, uint64_t* bar, uint32_t parity) {
+  if (mbar_try_wait(smem_u32(bar), parity)) return;
+  if (*(volatile int*)&c.bars->abort) return;
+  if (!mbar_wait(smem_u32(bar), parity, c.limit_ns)) {
+    *(volatile int*)&c.bars->abort = 1;
+    atomicOr(c.status, 1);   // MLA_DEVERR_TIMEOUT
+  }
+}
+
+struct Item {
+  int q0, nq, kv0, nkeys, lim0, prow, head;
+  int seen[2];     // keys the last row of each query tile sees (0: no such row)
+  int tiles[2];    // their key tiles
+};
+
+// Item `i` of the list: pieces longest first, interleaved over a group of heads.
+__device__ __forceinline__ Item item_at(const PrefillArgs& a, int np, int64_t i) {
+  const int64_t per = (int64_t)np * a.group_heads;
+  const int g = (int)(i / per), rem = (int)(i - g * per);
+  const int heads = min(a.group_heads, a.num_heads - g * a.group_heads);
+  const int p = rem / heads;
+  const int4* rec = reinterpret_cast<const int4*>(a.plan.pieces + p);
+  const int4 r0 = rec[0], r1 = rec[1];
+  Item it;
+  it.q0 = r0.x, it.nq = r0.y, it.kv0 = r0.z, it.nkeys = r0.w, it.lim0 = r1.x, it.prow = r1.y;
+  it.head = g * a.group_heads + rem - p * heads;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int last = min(128 * (t + 1), it.nq) - 1;
+    it.seen[t] = it.nq > 128 * t ? min(max(it.lim0 + (a.causal ? last : 0), 0), it.nkeys) : 0;
+    it.tiles[t] = (it.seen[t] + kPrefillTile - 1) / kPrefillTile;
+  }
+  return it;
+}
+
+// Items go around the CTAs, in alternating direction so that a CTA that got a
+// long one of a round gets a short one of the next.
+__device__ __forceinline__ int64_t item_index(int round) {
+  const int c = (round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
+  return (int64_t)round * gridDim.x + c;
+}
+
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// two lanes of one f32x2 instruction
+__device__ __forceinline__ void add2(float& a0, float& a1, float b0, float b1) {
+  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %3};\n add.rn.f32x2 x, x, y;\n"
+      " mov.b64 {%0, %1}, x;\n}" : "+f"(a0), "+f"(a1) : "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ void fma2(float& r0, float& r1, float a0, float a1, float b, float c) {
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %4};\n mov.b64 z, {%5, %5};\n"
+      " fma.rn.f32x2 x, x, y, z;\n mov.b64 {%0, %1}, x;\n}" : "=f"(r0), "=f"(r1) : "f"(a0), "f"(a1), "f"(b), "f"(c));
+}
+
+// ------------------------------------------------------------------ producer
+__device__ __forceinline__ void load_items(const PrefillArgs& a, const Ctx& ctx, int np, int64_t items,
+                                           const CUtensorMap* tm_q, const CUtensorMap* tm_kv,
+                                           const CUtensorMap* tm_pe, uint8_t* q_smem, uint8_t* ring) {
+  Bars* bars = ctx.bars;
+  uint32_t n = 0, q_used[2] = {0, 0};
+  volatile int* abort_flag = &bars->abort;
+  auto chunk = [&](const CUtensorMap* map, bool three, int x, int head, int row) {
+    const uint32_t slot = n % kRing;
+    wait_bar(ctx, &bars->empty[slot], ((n / kRing) & 1) ^ 1);
+    if (*abort_flag) return;
+    const uint32_t full = smem_u32(&bars->full[slot]), dst = smem_u32(ring + slot * kChunk);
+    mbar_expect_tx(full, kChunk);
+    if (three)
+      tma_load_3d(dst, map, x, head, row, full);
+    else
+      tma_load_2d(dst, map, x, row, full);
+    ++n;
+  };
+  for (int round = 0;; ++round) {
+    const int64_t i = item_index(round);
+    if ((int64_t)round * gridDim.x >= items || *abort_flag) break;
+    if (i >= items) continue;
+    const Item it = item_at(a, np, i);
+    const int tiles = max(it.tiles[0], it.tiles[1]);
+    auto query = [&](int t) {
+      if (it.tiles[t] == 0 || *abort_flag) return;
+      wait_bar(ctx, &bars->q_empty[t], (q_used[t] & 1) ^ 1);
+      if (*abort_flag) return;
+      const uint32_t full = smem_u32(&bars->q_full[t]);
+      mbar_expect_tx(full, kQTile);
+#pragma unroll
+      for (int c = 0; c < 3; ++c)
+        tma_load_3d(smem_u32(q_smem + t * kQTile + c * kChunk), tm_q, 64 * c, it.head, it.q0 + 128 * t, full);
+      ++q_used[t];
+    };
+    query(0);
+    for (int j = 0; j < tiles && !*abort_flag; ++j) {
+      const int row = it.kv0 + j * kPrefillTile;
+      chunk(tm_kv, true, 0, it.head, row);
+      chunk(tm_kv, true, 64, it.head, row);
+      chunk(tm_pe, false, 0, 0, row);
+      if (j == 0) query(1);
+      chunk(tm_kv, true, kNope, it.head, row);
+      chunk(tm_kv, true, kNope + 64, it.head, row);
+    }
+  }
+  // every issued load has landed before the CTA may exit
+  for (uint32_t k = n > kRing ? n - kRing : 0; k < n; ++k)
+    mbar_wait(smem_u32(&bars->full[k % kRing]), (k / kRing) & 1, ctx.limit_ns);
+  for (int t = 0; t < 2; ++t)
+    if (q_used[t] > 0) mbar_wait(smem_u32(&bars->q_full[t]), (q_used[t] - 1) & 1, ctx.limit_ns);
+}
+
+// -------------------------------------------------------------- MMA issuer
+// The whole warp walks the items together; lane 0 issues.
+__device__ __forceinline__ void issue_items(const PrefillArgs& a, const Ctx& ctx, int np, int64_t items,
+                                            uint32_t tbase, uint8_t* q_smem, uint8_t* ring, int lane) {
+  Bars* bars = ctx.bars;
+  constexpr uint32_t id_s = idesc_bf16_f32(128, 128, 0, 0);   // K-major queries and keys
+  constexpr uint32_t id_o = idesc_bf16_f32(128, 64, 0, 1);    // MN-major values, 64 dims at a time
+  const uint64_t q_desc = smem_desc(smem_u32(q_smem), 16, 1024, kSwizzle128B);
+  const uint64_t k_desc = smem_desc(smem_u32(ring), 16, 1024, kSwizzle128B);
+  const uint64_t v_desc = smem_desc(smem_u32(ring), kChunk, 1024, kSwizzle128B);
+  uint32_t n = 0;                          // ring chunks of the tiles before
+  uint32_t q_used[2] = {0, 0}, p_used[2] = {0, 0};
+
+  // S_t = Q_t K: chunks n0..n0+2
+  auto scores = [&](int t, uint32_t n0) {
+    if (lane == 0) {
+#pragma unroll
+      for (int c = 0; c < 3; ++c) {
+        const uint32_t slot = (n0 + c) % kRing;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mma_ss(tbase + kColS + 128 * t, q_desc + ((t * kQTile + c * kChunk + k * 32) >> 4),
+                 k_desc + ((slot * kChunk + k * 32) >> 4), id_s, (c | k) ? 1u : 0u);
+      }
+      mma_commit(smem_u32(&bars->s_full[t]));
+    }
+  };
+  auto wait_chunks = [&](uint32_t n0, int count) {
+    for (int c = 0; c < count; ++c) wait_bar(ctx, &bars->full[(n0 + c) % kRing], ((n0 + c) / kRing) & 1);
+  };
+  auto release = [&](uint32_t n0, int count) {
+    if (lane == 0)
+      for (int c = 0; c < count; ++c) mma_commit(smem_u32(&bars->empty[(n0 + c) % kRing]));
+  };
+
+  for (int round = 0;; ++round) {
+    const int64_t i = item_index(round);
+    if ((int64_t)round * gridDim.x >= items) break;
+    if (i >= items) continue;
+    const Item it = item_at(a, np, i);
+    const int tiles = max(it.tiles[0], it.tiles[1]);
+    if (tiles == 0) continue;
+    // first scores of both tiles
+    wait_chunks(n, 3);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      if (it.tiles[t] == 0) continue;
+      wait_bar(ctx, &bars->q_full[t], q_used[t] & 1);
+      tc_fence_after();
+      scores(t, n);
+      if (it.tiles[t] == 1 && lane == 0) mma_commit(smem_u32(&bars->q_empty[t]));
+      ++q_used[t];
+    }
+    release(n, 3);
+    for (int j = 0; j < tiles; ++j, n += 5) {
+      const bool more = j + 1 < tiles;
+      const int left = it.nkeys - j * kPrefillTile;     // keys of the piece from this tile on
+      wait_chunks(n + 3, 2);
+      if (left < kPrefillTile && (left & 15)) {
+        // value rows past the piece's keys meet probabilities of zero, but
+        // may hold anything: clear those inside the last 16-key step
+        const int r0 = left, rows = 16 - (left & 15);
+        for (int e = lane; e < rows * 16; e += 32) {
+          const uint32_t slot = (n + 3 + (e & 1)) % kRing;
+          *reinterpret_cast<uint4*>(ring + slot * kChunk + (r0 + (e >> 4)) * 128 + ((e >> 1) & 7) * 16) =
+              make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (j < it.tiles[t]) {
+          const int steps = min(kPrefillTile / 16, (it.seen[t] - j * kPrefillTile + 15) / 16);
+          wait_bar(ctx, &bars->p_full[t], p_used[t] & 1);
+          ++p_used[t];
+          tc_fence_after();
+          if (lane == 0) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint64_t vd = v_desc + ((((n + 3 + h) % kRing) * kChunk) >> 4);
+              for (int k = 0; k < steps; ++k)
+                mma_ts(tbase + kColO + 128 * t + 64 * h, tbase + kColS + 128 * t + 8 * k, vd + ((k * 2048) >> 4),
+                       id_o, (j | k) ? 1u : 0u);
+            }
+            if (j + 1 == it.tiles[t]) mma_commit(smem_u32(&bars->o_full[t]));
+          }
+        }
+        if (t == 1) release(n + 3, 2);
+        if (more && t == 0) wait_chunks(n + 5, 3);
+        if (j + 1 < it.tiles[t]) {
+          scores(t, n + 5);
+          if (j + 2 == it.tiles[t] && lane == 0) mma_commit(smem_u32(&bars->q_empty[t]));
+        }
+        if (more && t == 1) release(n + 5, 3);
+      }
+      __syncwarp();
+    }
+  }
+  if (lane == 0) {
+    mma_commit(smem_u32(&bars->drain));
+    mbar_wait(smem_u32(&bars->drain), 0, ctx.limit_ns);
+  }
+  __syncwarp();
+}
+
+// A row whose output came out not finite although its sum is: a key that the
+// row does not see, but rows beside it do, may hold a value that is not finite
+// (0 * inf in the matrix product).  If one of the masked keys [sees, covered)
+// does, the warp computes the row again from the keys it sees, with the
+// row's own reference and sum; otherwise the result stands.  Only inputs
+// with infinities or NaN come here.
+__device__ __noinline__ void mend_row(const PrefillArgs& a, int row, int head, int kv0, int sees, int covered,
+                                      float ref, float inv, float* part, __nv_bfloat16* out) {
+  const int lane = threadIdx.x & 31;
+  const __nv_bfloat16* kv = static_cast<const __nv_bfloat16*>(a.kv) + (int64_t)head * a.kv_head_stride;
+  bool found = false;
+  for (int j = sees; j < covered; ++j) {
+    const __nv_bfloat16* v = kv + (int64_t)(kv0 + j) * a.kv_token_stride + kNope + 4 * lane;
+    for (int e = 0; e < 4; ++e) found |= !(fabsf(__bfloat162float(v[e])) < INFINITY);
+  }
+  if (!__any_sync(0xffffffffu, found)) return;
+  const __nv_bfloat16* q =
+      static_cast<const __nv_bfloat16*>(a.q) + (int64_t)row * a.q_token_stride + (int64_t)head * a.q_head_stride;
+  const __nv_bfloat16* pe = static_cast<const __nv_bfloat16*>(a.k_pe);
+  float o[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int j0 = 0; j0 < sees; j0 += 32) {
+    float p = 0.f;
+    if (j0 + lane < sees) {
+      const __nv_bfloat16* k = kv + (int64_t)(kv0 + j0 + lane) * a.kv_token_stride;
+      const __nv_bfloat16* r = pe + (int64_t)(kv0 + j0 + lane) * a.k_pe_stride;
+      float s = 0.f;
+      for (int d = 0; d < kNope; ++d) s = fmaf(__bfloat162float(q[d]), __bfloat162float(k[d]), s);
+      for (int d = 0; d < 64; ++d) s = fmaf(__bfloat162float(q[kNope + d]), __bfloat162float(r[d]), s);
+      p = fast_exp2(fmaf(s, a.scale_log2, -ref));
+    }
+    const int n = min(32, sees - j0);
+    for (int j = 0; j < n; ++j) {
+      const float pj = __shfl_sync(0xffffffffu, p, j);
+      const __nv_bfloat16* v = kv + (int64_t)(kv0 + j0 + j) * a.kv_token_stride + kNope + 4 * lane;
+      for (int e = 0; e < 4; ++e) o[e] = fmaf(pj, __bfloat162float(v[e]), o[e]);
+    }
+  }
+  for (int e = 0; e < 4; ++e) {
+    if (part)
+      part[4 * lane + e] = o[e] * inv;
+    else
+      out[4 * lane + e] = __float2bfloat16_rn(o[e] * inv);
+  }
+}
+
+// ------------------------------------------------------------------ softmax
+__device__ __forceinline__ void softmax_items(const PrefillArgs& a, const Ctx& ctx, int np, int64_t items,
+                                              uint32_t tbase, int warp, int lane) {
+  Bars* bars = ctx.bars;
+  const int t = warp >> 2, quad = warp & 3;
+  const uint32_t lanes = (uint32_t)(32 * quad) << 16;
+  const uint32_t s_col = tbase + lanes + kColS + 128 * t, o_col = tbase + lanes + kColO + 128 * t;
+  const int row = 128 * t + 32 * quad + lane;
+  const float scale = a.scale_log2;
+  uint32_t s_used = 0, o_used = 0;
+
+  for (int round = 0;; ++round) {
+    const int64_t i = item_index(round);
+    if ((int64_t)round * gridDim.x >= items) break;
+    if (i >= items) continue;
+    const Item it = item_at(a, np, i);
+    const int tiles = it.tiles[t];
+    const int sees = min(max(it.lim0 + (a.causal ? row : 0), 0), it.nkeys);
+    const int warp_sees = min(max(it.lim0 + (a.causal ? row - lane : 0), 0), it.nkeys);   // its first row: the fewest
+    float ref = -INFINITY, sum = 0.f;
+
+    for (int j = 0; j < tiles; ++j, ++s_used) {
+      wait_bar(ctx, &bars->s_full[t], s_used & 1);
+      tc_fence_after();
+      uint32_t s[4][32];
+      float top[4];
+#pragma unroll
+      for (int g = 0; g < 4; ++g) tmem_ld32_max(s_col + 32 * g, s[g], top[g]);
+      tmem_wait_ld();
+      float m;
+      if (warp_sees >= (j + 1) * kPrefillTile) {
+        m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+      } else {
+        // a mask crosses this tile
+        const int left = sees - j * kPrefillTile;
+        m = -INFINITY;
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const float v = 32 * g + c < left ? __uint_as_float(s[g][c]) : -INFINITY;
+            s[g][c] = __float_as_uint(v);
+            m = fmaxf(m, v);
+          }
+      }
+      m *= scale;
+      const bool raise = m > ref + kRescale;
+      if (__any_sync(0xffffffffu, raise)) {
+        const float next = raise ? m : ref;
+        const float alpha = raise ? fast_exp2(ref - next) : 1.f;   // ref = -inf: 0
+        if (j > 0) {
+          // the scores' arrival implies that the products before them are
+          // done, and the next one waits for this warp
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            uint32_t o[32];
+            tmem_ld32(o_col + 32 * g, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+            tmem_st32(o_col + 32 * g, o);
+          }
+        }
+        sum *= alpha;
+        ref = next;
+      }
+      const float sub = ref == -INFINITY ? 0.f : ref;
+      float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        uint32_t p[16];
+#pragma unroll
+        for (int c = 0; c < 32; c += 4) {
+          float x0, x1, x2, x3;
+          fma2(x0, x1, __uint_as_float(s[g][c]), __uint_as_float(s[g][c + 1]), scale, -sub);
+          fma2(x2, x3, __uint_as_float(s[g][c + 2]), __uint_as_float(s[g][c + 3]), scale, -sub);
+          x0 = fast_exp2(x0), x1 = fast_exp2(x1), x2 = fast_exp2(x2), x3 = fast_exp2(x3);
+          add2(s0, s1, x0, x1);
+          add2(s2, s3, x2, x3);
+          p[c / 2] = pack_bf16x2(x0, x1);
+          p[c / 2 + 1] = pack_bf16x2(x2, x3);
+        }
+        tmem_st16(s_col + 16 * g, p);
+      }
+      sum += (s0 + s1) + (s2 + s3);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars->p_full[t]));
+    }
+
+    // the item's results
+    if (it.nq <= 128 * t) continue;
+    const bool live = row < it.nq;
+    const bool none = sum == 0.f;                   // no key seen (a NaN sum is not 0)
+    const float inv = none ? 0.f : 1.f / sum;
+    const float lse = none ? -INFINITY : (ref + log2f(sum)) * 0.69314718055994531f;
+    if (tiles > 0) {
+      wait_bar(ctx, &bars->o_full[t], o_used & 1);
+      ++o_used;
+      tc_fence_after();
+    }
+    const int64_t at = (int64_t)(it.q0 + row) * a.num_heads + it.head;
+    const int64_t part_at = it.prow + (int64_t)it.head * it.nq + row;
+    float spoilt = 0.f;                             // NaN once an output of the row is not finite
+    if (live) {
+      if (it.prow >= 0)
+        a.plan.part_lse[part_at] = lse;
+      else if (a.lse)
+        a.lse[at] = lse;
+    }
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      uint32_t o[32];
+      if (tiles > 0) {
+        tmem_ld32(o_col + 32 * g, o);
+        tmem_wait_ld();
+      }
+      if (none)
+#pragma unroll
+        for (int c = 0; c < 32; ++c) o[c] = 0;
+#pragma unroll
+      for (int c = 0; c < 32; ++c) spoilt = fmaf(__uint_as_float(o[c]), 0.f, spoilt);
+      if (live && it.prow >= 0) {
+        float4* dst = reinterpret_cast<float4*>(a.plan.part_o + part_at * kNope + 32 * g);
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          dst[c] = make_float4(__uint_as_float(o[4 * c]) * inv, __uint_as_float(o[4 * c + 1]) * inv,
+                               __uint_as_float(o[4 * c + 2]) * inv, __uint_as_float(o[4 * c + 3]) * inv);
+      } else if (live) {
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at * kNope + 32 * g);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            w[e] = pack_bf16x2(__uint_as_float(o[8 * c + 2 * e]) * inv, __uint_as_float(o[8 * c + 2 * e + 1]) * inv);
+          dst[c] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+      __syncwarp();
+    }
+    if (a.causal) {
+      // keys in the products of this tile that the row does not see
+      const int covered = min(it.nkeys, (it.seen[t] + 15) & ~15);
+      const bool odd = live && !none && spoilt != 0.f && fabsf(lse) < INFINITY && sees < covered;
+      for (unsigned rows = __ballot_sync(0xffffffffu, odd); rows; rows &= rows - 1) {
+        const int src = __ffs(rows) - 1;
+        const int64_t r_at = __shfl_sync(0xffffffffu, at, src), r_part = __shfl_sync(0xffffffffu, part_at, src);
+        mend_row(a, it.q0 + row - lane + src, it.head, it.kv0, __shfl_sync(0xffffffffu, sees, src), covered,
+                 __shfl_sync(0xffffffffu, ref, src), __shfl_sync(0xffffffffu, inv, src),
+                 it.prow >= 0 ? a.plan.part_o + r_part * kNope : nullptr,
+                 static_cast<__nv_bfloat16*>(a.out) + r_at * kNope);
+      }
+    }
+    tc_fence_before();   // the next item's products may overwrite O once this warp has handed over its P
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
+                   const __grid_constant__ CUtensorMap tm_pe, const __grid_constant__ PrefillArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* q_smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint8_t* ring = q_smem + 2 * kQTile;
+  Bars* bars = reinterpret_cast<Bars*>(ring + kRing * kChunk);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(smem_u32(&bars->full[i]), 1);
+      mbar_init(smem_u32(&bars->empty[i]), 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(smem_u32(&bars->q_full[t]), 1);
+      mbar_init(smem_u32(&bars->q_empty[t]), 1);
+      mbar_init(smem_u32(&bars->s_full[t]), 1);
+      mbar_init(smem_u32(&bars->p_full[t]), 4);
+      mbar_init(smem_u32(&bars->o_full[t]), 1);
+    }
+    mbar_init(smem_u32(&bars->drain), 1);
+    bars->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kWarpMma) {
+    tmem_alloc(smem_u32(&bars->tmem_base), 512);
+    tmem_relinquish();
+  }
+  if (warp == kWarpLoad && lane == 0) {
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_kv);
+    tma_prefetch_desc(&tm_pe);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = bars->tmem_base;
+  // everything above overlaps the plan kernel
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const Ctx ctx{bars, &a.plan.header->status, a.wait_limit_ns};
+  const int np = a.plan.header->num_pieces;
+  const int64_t items = (int64_t)np * a.num_heads;
+
+  if (warp < kSoftmaxWarps) {
+    setmaxnreg_inc<kRegsSoftmax>();
+    softmax_items(a, ctx, np, items, tbase, warp, lane);
+  } else {
+    setmaxnreg_dec<kRegsOther>();
+    if (warp == kWarpLoad) {
+      if (lane == 0) load_items(a, ctx, np, items, &tm_q, &tm_kv, &tm_pe, q_smem, ring);
+      __syncwarp();
+    } else if (warp == kWarpMma) {
+      issue_items(a, ctx, np, items, tbase, q_smem, ring, lane);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpMma) {
+    tc_fence_after();
+    tmem_dealloc(tbase, 512);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_prefill(const CUtensorMap& tm_q, const CUtensorMap& tm_kv, const CUtensorMap& tm_pe,
+                           const PrefillArgs& a, cudaStream_t s) {
+  // set on every call: the attribute belongs to the current device
+  cudaError_t e = cudaFuncSetAttribute(prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)a.ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, prefill_kernel, tm_q, tm_kv, tm_pe, a);
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
+}
+
+}  // namespace mla

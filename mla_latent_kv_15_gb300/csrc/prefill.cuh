@@ -1,0 +1,125 @@
+// Shared definitions of the expanded attention (mla_prefill): the work plan in
+// the caller's workspace and the launchers.
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+namespace mla {
+
+constexpr int kNope = 128;           // key width without the rotated part, and value width
+constexpr int kPrefillRows = 256;    // query rows per block: two 128-row tiles (tcgen05 M)
+constexpr int kPrefillTile = 128;    // keys per tile
+constexpr int kPrefillMaxCtas = 160; // upper bound of the grid (one CTA per SM)
+
+// block  = up to 256 consecutive query rows of one sequence (the same for every head)
+// piece  = a block's keys [kv0, kv0 + nkeys), cut at multiples of a tile
+// item   = a piece and a head: what a CTA processes
+struct PrefillHeader {
+  int status;        // OR of mla_device_error bits
+  int num_pieces;
+  int num_split;     // blocks cut into more than one piece
+  int pad[5];
+};
+
+struct PrefillPiece {  // 32 bytes
+  int q0;              // first query row
+  int nq;              // rows (<= 256)
+  int kv0;             // first key row
+  int nkeys;           // keys
+  int lim0;            // keys of the piece that row 0 sees (not clamped): row r sees lim0 + r (causal) or lim0
+  int prow;            // first partial row of head 0, or -1: the block's only piece
+  int pad[2];
+};
+static_assert(sizeof(PrefillPiece) == 32, "one aligned 32-byte record");
+
+struct PrefillSplit {  // a block to be joined
+  int q0, nq, pieces;
+  int prow;            // partial row of (piece p, head h, row r): prow + (p * heads + h) * nq + r
+  int before;          // rows * heads of the split blocks before it
+  int pad[3];
+};
+
+struct PrefillPlan {
+  PrefillHeader* header;
+  int* first_block;      // [batch + 1] blocks before each sequence
+  PrefillPiece* pieces;
+  PrefillSplit* splits;
+  float* part_o;         // [max_part_rows][128]
+  float* part_lse;       // [max_part_rows]
+  int max_pieces;
+  int max_part_rows;
+};
+
+struct PrefillLayout {
+  size_t first_block, pieces, splits, part_o, part_lse, total;
+  int max_blocks, max_pieces;
+  long long max_part_rows;
+};
+
+// Byte offsets for a shape.  Automatic splitting makes at most two partial
+// pieces per CTA (prefill_plan_kernel); a forced count cuts every block.
+inline PrefillLayout prefill_layout(int batch, int total_q, int num_heads, int max_splits) {
+  auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+  PrefillLayout L{};
+  const long long mb = (long long)total_q / kPrefillRows + batch;
+  const long long auto_rows = 2LL * kPrefillMaxCtas * (total_q < kPrefillRows ? total_q : kPrefillRows);
+  const long long forced_rows = max_splits > 1 ? (long long)total_q * max_splits * num_heads : 0;
+  const long long mp = mb * (max_splits > 1 ? max_splits : 1) + 2 * kPrefillMaxCtas;
+  L.max_blocks = (int)mb;
+  L.max_pieces = (int)mp;
+  L.max_part_rows = auto_rows > forced_rows ? auto_rows : forced_rows;
+  size_t off = up(sizeof(PrefillHeader));
+  L.first_block = off;  off = up(off + sizeof(int) * ((size_t)batch + 1));
+  L.pieces = off;       off = up(off + sizeof(PrefillPiece) * (size_t)mp);
+  L.splits = off;       off = up(off + sizeof(PrefillSplit) * (size_t)mb);
+  L.part_o = off;       off = up(off + sizeof(float) * kNope * (size_t)L.max_part_rows);
+  L.part_lse = off;     off = up(off + sizeof(float) * (size_t)L.max_part_rows);
+  L.total = off;
+  return L;
+}
+
+inline PrefillPlan prefill_plan_from(void* ws, const PrefillLayout& L) {
+  char* p = static_cast<char*>(ws);
+  return PrefillPlan{reinterpret_cast<PrefillHeader*>(p),
+                     reinterpret_cast<int*>(p + L.first_block),
+                     reinterpret_cast<PrefillPiece*>(p + L.pieces),
+                     reinterpret_cast<PrefillSplit*>(p + L.splits),
+                     reinterpret_cast<float*>(p + L.part_o),
+                     reinterpret_cast<float*>(p + L.part_lse),
+                     L.max_pieces,
+                     (int)L.max_part_rows};
+}
+
+struct PrefillArgs {
+  // the tensors the maps describe (elements strides), for the rows that are mended one by one
+  const void* q;
+  int64_t q_token_stride, q_head_stride;
+  const void* kv;
+  int64_t kv_token_stride, kv_head_stride;
+  const void* k_pe;
+  int64_t k_pe_stride;
+  const int32_t* cu_q;
+  const int32_t* cu_kv;
+  int batch, total_q, total_kv, num_heads;
+  int causal;
+  int num_splits;        // 0: automatic
+  int group_heads;       // heads whose items are interleaved (their keys and values stay in L2)
+  int ctas;              // grid of the attention kernel
+  float scale_log2;      // scale * log2(e), > 0
+  void* out;             // bf16 [total_q, heads, 128]
+  float* lse;            // [total_q, heads] or null
+  unsigned long long wait_limit_ns;
+  PrefillPlan plan;
+};
+
+cudaError_t launch_prefill_plan(const PrefillArgs& a, cudaStream_t s);
+// tm_q: {192, heads, total_q} boxes 64 x 1 x 128; tm_kv: {256, heads, total_kv}
+// boxes 64 x 1 x 128; tm_pe: {64, total_kv} boxes 64 x 128; all 128-byte swizzled
+cudaError_t launch_prefill(const CUtensorMap& tm_q, const CUtensorMap& tm_kv, const CUtensorMap& tm_pe,
+                           const PrefillArgs& a, cudaStream_t s);
+cudaError_t launch_prefill_combine(const PrefillArgs& a, cudaStream_t s);
+
+}  // namespace mla

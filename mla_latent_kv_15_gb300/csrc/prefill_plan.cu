@@ -1,0 +1,252 @@
+// Work plan and join of the expanded attention.
+//
+// Plan: one block of threads turns the prefix sums on the device into a list
+// of pieces, longest first, so that nothing of a call depends on the host
+// knowing the lengths (a captured graph may be replayed over other ones).
+// Every sequence's query rows are cut into blocks of 256; a block's keys are
+// those its last row sees.  The list is the same for every head.
+//
+// A block is cut over its keys only where one block would outlast the rest:
+// with T tiles of work over all heads and S CTAs, a chunk is ceil(T / S)
+// tiles, and a block of more than 1.5 chunks is cut into ceil(tiles / chunk)
+// near-equal pieces (so the cut blocks of all heads number less than S and
+// their pieces less than 2 S).  The pieces' results are float32 partials with
+// their log-sum-exp, joined by the combine kernel:
+//   lse = ln sum_p exp(lse_p),  out = sum_p exp(lse_p - lse) out_p
+// always in the order of the pieces, whichever CTA made them.
+#include <cuda_bf16.h>
+
+#include "prefill.cuh"
+
+namespace mla {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kBuckets = 1024;       // piece lengths are sorted into this many classes
+constexpr int kMinChunk = 4;         // tiles
+
+__device__ __forceinline__ int block_sum_scan(int v, int* total, int* warp_sums) {
+  // exclusive scan over the block; *total: the block's sum
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int n = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += n;
+  }
+  __syncthreads();
+  if (lane == 31) warp_sums[warp] = incl;
+  __syncthreads();
+  int before = 0, sum = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += warp_sums[w];
+    sum += warp_sums[w];
+  }
+  *total = sum;
+  return before + incl - v;
+}
+
+struct BlockOf {
+  int q0, nq, kv0, nkeys, lim0, tiles;
+};
+
+// Block i of the list: its sequence by binary search over the block counts.
+__device__ __forceinline__ BlockOf block_of(const PrefillArgs& a, int i) {
+  int lo = 0, hi = a.batch - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (a.plan.first_block[mid] <= i) lo = mid; else hi = mid - 1;
+  }
+  const int q0 = a.cu_q[lo], sq = a.cu_q[lo + 1] - q0, k0 = a.cu_kv[lo], sk = a.cu_kv[lo + 1] - k0;
+  const int r0 = (i - a.plan.first_block[lo]) * kPrefillRows;
+  BlockOf b;
+  b.q0 = q0 + r0;
+  b.nq = min(kPrefillRows, sq - r0);
+  b.kv0 = k0;
+  b.lim0 = a.causal ? sk - sq + 1 + r0 : sk;
+  b.nkeys = a.causal ? min(max(b.lim0 + b.nq - 1, 0), sk) : sk;
+  b.tiles = (b.nkeys + kPrefillTile - 1) / kPrefillTile;
+  return b;
+}
+
+__global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArgs a) {
+  __shared__ int s_hist[kBuckets];
+  __shared__ int s_warp[kThreads / 32];
+  __shared__ unsigned long long s_total;
+  __shared__ int s_longest, s_status, s_rows, s_split;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = threadIdx.x;
+  if (tid == 0) s_total = 0, s_longest = 0, s_status = 0, s_rows = 0, s_split = 0;
+  for (int i = tid; i < kBuckets; i += kThreads) s_hist[i] = 0;
+  __syncthreads();
+
+  // the sequences: checks, and the blocks before each
+  int carry = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
+    const int b = b0 + tid;
+    int n = 0;
+    if (b < a.batch) {
+      const int q0 = a.cu_q[b], q1 = a.cu_q[b + 1], k0 = a.cu_kv[b], k1 = a.cu_kv[b + 1];
+      if (q0 < 0 || q1 < q0 || q1 > a.total_q) atomicOr(&s_status, 8);
+      if (k0 < 0 || k1 < k0 || k1 > a.total_kv) atomicOr(&s_status, 2);
+      n = q0 < 0 || q1 < q0 || q1 > a.total_q ? 0 : (q1 - q0 + kPrefillRows - 1) / kPrefillRows;
+    }
+    int total;
+    const int before = block_sum_scan(n, &total, s_warp);
+    if (b < a.batch) a.plan.first_block[b] = carry + before;
+    carry += total;
+  }
+  if (tid == 0) a.plan.first_block[a.batch] = carry;
+  __syncthreads();
+  const int nblocks = carry;
+  if (s_status) {          // inconsistent prefix sums: flagged, nothing is computed
+    if (tid == 0) {
+      a.plan.header->status = s_status;
+      a.plan.header->num_pieces = 0;
+      a.plan.header->num_split = 0;
+    }
+    return;
+  }
+
+  unsigned long long mine = 0;
+  int longest = 0;
+  for (int i = tid; i < nblocks; i += kThreads) {
+    const int t = block_of(a, i).tiles;
+    mine += t;
+    longest = max(longest, t);
+  }
+  atomicAdd(&s_total, mine);
+  atomicMax(&s_longest, longest);
+  __syncthreads();
+  const unsigned long long work = s_total * a.num_heads;
+  longest = s_longest;
+  int chunk = max((int)((work + a.ctas - 1) / a.ctas), kMinChunk);
+  const bool cut = a.num_splits == 0 && 2 * longest > 3 * chunk;
+  auto pieces_of = [&](int tiles) {
+    if (a.num_splits > 0) return max(1, min(a.num_splits, tiles));
+    return cut && 2 * tiles > 3 * chunk ? (tiles + chunk - 1) / chunk : 1;
+  };
+  // length class: 0 = longest
+  const int span = longest + 1;
+  auto bucket = [&](int tiles) { return (int)((long long)(longest - tiles) * kBuckets / span); };
+
+  for (int i = tid; i < nblocks; i += kThreads) {
+    const int tiles = block_of(a, i).tiles, P = pieces_of(tiles);
+    for (int p = 0; p < P; ++p) {
+      const int t0 = (int)((long long)tiles * p / P), t1 = (int)((long long)tiles * (p + 1) / P);
+      atomicAdd(&s_hist[bucket(t1 - t0)], 1);
+    }
+  }
+  __syncthreads();
+  carry = 0;
+  for (int b0 = 0; b0 < kBuckets; b0 += kThreads) {
+    int total;
+    const int v = s_hist[b0 + tid];
+    const int before = block_sum_scan(v, &total, s_warp);
+    s_hist[b0 + tid] = carry + before;
+    carry += total;
+  }
+  __syncthreads();
+  for (int i = tid; i < nblocks; i += kThreads) {
+    const BlockOf b = block_of(a, i);
+    const int P = pieces_of(b.tiles);
+    int prow = -1;
+    if (P > 1) {
+      prow = atomicAdd(&s_rows, P * a.num_heads * b.nq);
+      PrefillSplit sp{};
+      sp.q0 = b.q0, sp.nq = b.nq, sp.pieces = P, sp.prow = prow;
+      a.plan.splits[atomicAdd(&s_split, 1)] = sp;
+    }
+    for (int p = 0; p < P; ++p) {
+      const int t0 = (int)((long long)b.tiles * p / P), t1 = (int)((long long)b.tiles * (p + 1) / P);
+      PrefillPiece r{};
+      r.q0 = b.q0;
+      r.nq = b.nq;
+      r.kv0 = b.kv0 + t0 * kPrefillTile;
+      r.nkeys = min(t1 * kPrefillTile, b.nkeys) - t0 * kPrefillTile;
+      r.lim0 = b.lim0 - t0 * kPrefillTile;
+      r.prow = prow < 0 ? -1 : prow + p * a.num_heads * b.nq;
+      const int at = atomicAdd(&s_hist[bucket(t1 - t0)], 1);
+      if (at < a.plan.max_pieces) a.plan.pieces[at] = r;
+    }
+  }
+  __syncthreads();
+  if (tid == 0) {
+    int before = 0;
+    for (int i = 0; i < s_split; ++i) {
+      a.plan.splits[i].before = before;
+      before += a.plan.splits[i].nq * a.num_heads;
+    }
+    a.plan.header->status = 0;
+    a.plan.header->num_pieces = min(carry, a.plan.max_pieces);
+    a.plan.header->num_split = s_split;
+  }
+}
+
+// One warp per (row, head) of the split blocks, four output dims a lane.
+__global__ void __launch_bounds__(256) prefill_combine_kernel(const PrefillArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int n = a.plan.header->num_split;
+  if (n == 0) return;
+  const int lane = threadIdx.x & 31;
+  const int warps = gridDim.x * 8, w = blockIdx.x * 8 + (threadIdx.x >> 5);
+  for (int i = 0; i < n; ++i) {
+    const PrefillSplit sp = a.plan.splits[i];
+    const int rows = sp.nq * a.num_heads;
+    for (int rr = (w + warps - sp.before % warps) % warps; rr < rows; rr += warps) {
+      const int h = rr / sp.nq, r = rr - h * sp.nq;
+      const int64_t step = (int64_t)a.num_heads * sp.nq;
+      const int64_t at0 = sp.prow + (int64_t)h * sp.nq + r;
+      float m = -INFINITY;
+      for (int p = 0; p < sp.pieces; ++p) m = fmaxf(m, a.plan.part_lse[at0 + p * step]);
+      const float ref = m == -INFINITY ? 0.f : m;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      float sum = 0.f;
+      for (int p = 0; p < sp.pieces; ++p) {
+        const float l = a.plan.part_lse[at0 + p * step];
+        if (l == -INFINITY) continue;
+        const float e = expf(l - ref);
+        const float4 v = *reinterpret_cast<const float4*>(a.plan.part_o + (at0 + p * step) * kNope + 4 * lane);
+        sum += e;
+        o.x += e * v.x, o.y += e * v.y, o.z += e * v.z, o.w += e * v.w;
+      }
+      const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);   // NaN stays NaN
+      const int64_t row = (int64_t)(sp.q0 + r) * a.num_heads + h;
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv),
+                           hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + row * kNope + 4 * lane) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+      if (lane == 0 && a.lse) a.lse[row] = sum == 0.f ? -INFINITY : ref + logf(sum);
+    }
+  }
+}
+
+cudaError_t launch_dependent(void (*kernel)(const PrefillArgs), int grid, int block, const PrefillArgs& a,
+                             cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)block);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_prefill_plan(const PrefillArgs& a, cudaStream_t s) {
+  return launch_dependent(prefill_plan_kernel, 1, kThreads, a, s);
+}
+
+cudaError_t launch_prefill_combine(const PrefillArgs& a, cudaStream_t s) {
+  return launch_dependent(prefill_combine_kernel, 2 * a.ctas, 256, a, s);
+}
+
+}  // namespace mla

@@ -53,3 +53,27 @@ def prefill(q, kv, k_pe, cu_q, cu_kv, scale, causal, live=None):
                 mag[q0 + i] = np.einsum("nj,jnd->nd", p / tot, np.abs(v))
                 lse[q0 + i] = (m + np.log(tot))[:, 0]
     return out, lse, mag
+
+
+def prefill_torch(q, kv, k_pe, cu_q, cu_kv, scale, causal):
+    """The same on the tensors' device in torch float64 (finite inputs)."""
+    import torch
+    T, N, _ = q.shape
+    out = torch.zeros((T, N, VDIM), dtype=torch.float64, device=q.device)
+    mag = torch.zeros_like(out)
+    lse = torch.full((T, N), -np.inf, dtype=torch.float64, device=q.device)
+    for b in range(len(cu_q) - 1):
+        q0, q1, k0, k1 = cu_q[b], cu_q[b + 1], cu_kv[b], cu_kv[b + 1]
+        sq, sk = q1 - q0, k1 - k0
+        if sq == 0 or sk == 0:
+            continue
+        for h in range(N):
+            x, y = q[q0:q1, h].double(), kv[k0:k1, h].double()
+            s = scale * (x[:, :NOPE] @ y[:, :NOPE].t() + x[:, NOPE:] @ k_pe[k0:k1].double().t())
+            if causal:
+                i = torch.arange(sq, device=q.device)[:, None] + sk - sq
+                s = s.masked_fill(torch.arange(sk, device=q.device)[None] > i, -np.inf)
+            l = torch.logsumexp(s, dim=1)
+            p = torch.exp(s - torch.where(l.isinf(), 0.0, l)[:, None])
+            out[q0:q1, h], mag[q0:q1, h], lse[q0:q1, h] = p @ y[:, NOPE:], p @ y[:, NOPE:].abs(), l
+    return out, lse, mag
