@@ -28,9 +28,11 @@ namespace {
 using namespace ptx;
 
 constexpr int kSoftmaxWarps = 8;                  // 0-3: query tile 0, 4-7: query tile 1
-constexpr int kWarpLoad = 8, kWarpMma = 9;        // warps 10, 11 only fill the warpgroup
+constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpList = 10;   // warp 11 only fills the warpgroup
+constexpr int kItemSlots = 2;                     // items known ahead
+constexpr int kItemReaders = kSoftmaxWarps + 2;   // warps that read each item
 constexpr int kThreads = 384;
-constexpr uint32_t kRegsSoftmax = 216, kRegsOther = 72;
+constexpr uint32_t kRegsSoftmax = 208, kRegsOther = 88;
 static_assert(128 * (2 * kRegsSoftmax + kRegsOther) <= kThreads * 168, "register split of the launch's 168 a thread");
 
 constexpr uint32_t kChunk = 16384;                // 128 rows x 64 dims
@@ -44,10 +46,11 @@ struct Bars {
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2], p_full[2], o_full[2];
   uint64_t drain;
+  uint64_t item_full[kItemSlots], item_empty[kItemSlots];
   uint32_t tmem_base;
   int abort;
 };
-constexpr size_t kSmem = 1024 + 2 * kQTile + kRing * kChunk + sizeof(Bars);
+constexpr size_t kSmem = 1024 + 2 * kQTile + kRing * kChunk + sizeof(Bars) + 16 + kItemSlots * 48;
 static_assert(kSmem <= 232448, "shared memory per CTA");
 
 struct Ctx {
@@ -66,16 +69,18 @@ __device__ __forceinline__ void wait_bar(const Ctx& c, uint64_t* bar, uint32_t p
   }
 }
 
-struct Item {
+struct __align__(16) Item {
   int q0, nq, kv0, nkeys, lim0, prow, head;
   int seen[2];     // keys the last row of each query tile sees (0: no such row)
   int tiles[2];    // their key tiles
+  int last;        // behind the last item: nothing to do
 };
+static_assert(sizeof(Item) == 48, "three 16-byte words");
 
 // Item `i` of the list: pieces longest first, interleaved over a group of heads.
-__device__ __forceinline__ Item item_at(const PrefillArgs& a, int np, int64_t i) {
-  const int64_t per = (int64_t)np * a.group_heads;
-  const int g = (int)(i / per), rem = (int)(i - g * per);
+__device__ __forceinline__ Item item_at(const PrefillArgs& a, int np, int i) {
+  const int per = np * a.group_heads;               // <= items, which are below 2^31
+  const int g = i / per, rem = i - g * per;
   const int heads = min(a.group_heads, a.num_heads - g * a.group_heads);
   const int p = rem / heads;
   const int4* rec = reinterpret_cast<const int4*>(a.plan.pieces + p);
@@ -89,14 +94,41 @@ __device__ __forceinline__ Item item_at(const PrefillArgs& a, int np, int64_t i)
     it.seen[t] = it.nq > 128 * t ? min(max(it.lim0 + (a.causal ? last : 0), 0), it.nkeys) : 0;
     it.tiles[t] = (it.seen[t] + kPrefillTile - 1) / kPrefillTile;
   }
+  it.last = 0;
   return it;
 }
 
-// Items go around the CTAs, in alternating direction so that a CTA that got a
-// long one of a round gets a short one of the next.
-__device__ __forceinline__ int64_t item_index(int round) {
-  const int c = (round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
-  return (int64_t)round * gridDim.x + c;
+// The list warp hands the CTA's items to the other warps: the first is the
+// CTA's own, the next come from a counter all CTAs share, so that a CTA done
+// early takes more.
+__device__ __forceinline__ void list_items(const PrefillArgs& a, const Ctx& ctx, int np, Item* slots) {
+  Bars* bars = ctx.bars;
+  const int items = np * a.num_heads;
+  int i = blockIdx.x;
+  for (uint32_t n = 0;; ++n) {
+    const uint32_t slot = n % kItemSlots;
+    Item it{};
+    it.last = 1;
+    if (i < items) it = item_at(a, np, i);
+    wait_bar(ctx, &bars->item_empty[slot], ((n / kItemSlots) & 1) ^ 1);
+    if (*(volatile int*)&bars->abort) break;
+    slots[slot] = it;
+    mbar_arrive(smem_u32(&bars->item_full[slot]));
+    if (it.last) break;
+    i = gridDim.x + atomicAdd(&a.plan.header->next, 1);
+  }
+}
+
+// The next item, read by a whole warp; one without work behind the last or after an abort.
+__device__ __forceinline__ Item next_item(const Ctx& ctx, const Item* slots, uint32_t& n, int lane) {
+  const uint32_t slot = n % kItemSlots;
+  wait_bar(ctx, &ctx.bars->item_full[slot], (n / kItemSlots) & 1);
+  Item it = slots[slot];
+  __syncwarp();
+  if (lane == 0) mbar_arrive(smem_u32(&ctx.bars->item_empty[slot]));
+  ++n;
+  if (*(volatile int*)&ctx.bars->abort) it.last = 1;
+  return it;
 }
 
 __device__ __forceinline__ float fast_exp2(float x) {
@@ -115,48 +147,54 @@ __device__ __forceinline__ void fma2(float& r0, float& r1, float a0, float a1, f
 }
 
 // ------------------------------------------------------------------ producer
-__device__ __forceinline__ void load_items(const PrefillArgs& a, const Ctx& ctx, int np, int64_t items,
-                                           const CUtensorMap* tm_q, const CUtensorMap* tm_kv,
-                                           const CUtensorMap* tm_pe, uint8_t* q_smem, uint8_t* ring) {
+// The whole warp walks the items; one elected thread loads.
+__device__ __forceinline__ void load_items(const Ctx& ctx, const Item* slots, const CUtensorMap* tm_q,
+                                           const CUtensorMap* tm_kv, const CUtensorMap* tm_pe, uint32_t q_smem,
+                                           uint32_t ring, int lane) {
   Bars* bars = ctx.bars;
-  uint32_t n = 0, q_used[2] = {0, 0};
+  uint32_t n = 0, items = 0, q_used[2] = {0, 0};
   volatile int* abort_flag = &bars->abort;
+  // one chunk into the next ring slot; a load is skipped once the CTA gives up
   auto chunk = [&](const CUtensorMap* map, bool three, int x, int head, int row) {
     const uint32_t slot = n % kRing;
     wait_bar(ctx, &bars->empty[slot], ((n / kRing) & 1) ^ 1);
     if (*abort_flag) return;
-    const uint32_t full = smem_u32(&bars->full[slot]), dst = smem_u32(ring + slot * kChunk);
-    mbar_expect_tx(full, kChunk);
-    if (three)
-      tma_load_3d(dst, map, x, head, row, full);
-    else
-      tma_load_2d(dst, map, x, row, full);
+    if (elect_one()) {
+      const uint32_t full = smem_u32(&bars->full[slot]), dst = ring + slot * kChunk;
+      mbar_expect_tx(full, kChunk);
+      if (three)
+        tma_load_3d(dst, map, x, head, row, full);
+      else
+        tma_load_2d(dst, map, x, row, full);
+    }
+    __syncwarp();
     ++n;
   };
-  for (int round = 0;; ++round) {
-    const int64_t i = item_index(round);
-    if ((int64_t)round * gridDim.x >= items || *abort_flag) break;
-    if (i >= items) continue;
-    const Item it = item_at(a, np, i);
-    const int tiles = max(it.tiles[0], it.tiles[1]);
-    auto query = [&](int t) {
-      if (it.tiles[t] == 0 || *abort_flag) return;
-      wait_bar(ctx, &bars->q_empty[t], (q_used[t] & 1) ^ 1);
-      if (*abort_flag) return;
+  auto query = [&](const Item& it, int t) {
+    if (it.tiles[t] == 0 || *abort_flag) return;
+    wait_bar(ctx, &bars->q_empty[t], (q_used[t] & 1) ^ 1);
+    if (*abort_flag) return;
+    if (elect_one()) {
       const uint32_t full = smem_u32(&bars->q_full[t]);
       mbar_expect_tx(full, kQTile);
 #pragma unroll
       for (int c = 0; c < 3; ++c)
-        tma_load_3d(smem_u32(q_smem + t * kQTile + c * kChunk), tm_q, 64 * c, it.head, it.q0 + 128 * t, full);
-      ++q_used[t];
-    };
-    query(0);
+        tma_load_3d(q_smem + t * kQTile + c * kChunk, tm_q, 64 * c, it.head, it.q0 + 128 * t, full);
+    }
+    __syncwarp();
+    ++q_used[t];
+  };
+  while (true) {
+    const Item it = next_item(ctx, slots, items, lane);
+    if (it.last) break;
+    const int tiles = max(it.tiles[0], it.tiles[1]);
+    query(it, 0);
     for (int j = 0; j < tiles && !*abort_flag; ++j) {
       const int row = it.kv0 + j * kPrefillTile;
       chunk(tm_kv, true, 0, it.head, row);
       chunk(tm_kv, true, 64, it.head, row);
       chunk(tm_pe, false, 0, 0, row);
-      if (j == 0) query(1);
+      if (j == 0) query(it, 1);
       chunk(tm_kv, true, kNope, it.head, row);
       chunk(tm_kv, true, kNope + 64, it.head, row);
     }
@@ -169,45 +207,45 @@ __device__ __forceinline__ void load_items(const PrefillArgs& a, const Ctx& ctx,
 }
 
 // -------------------------------------------------------------- MMA issuer
-// The whole warp walks the items together; lane 0 issues.
-__device__ __forceinline__ void issue_items(const PrefillArgs& a, const Ctx& ctx, int np, int64_t items,
-                                            uint32_t tbase, uint8_t* q_smem, uint8_t* ring, int lane) {
+// The whole warp walks the items together; one elected thread issues.
+__device__ __forceinline__ void issue_items(const Ctx& ctx, const Item* slots, uint32_t tbase, uint8_t* q_smem,
+                                            uint8_t* ring, int lane) {
   Bars* bars = ctx.bars;
   constexpr uint32_t id_s = idesc_bf16_f32(128, 128, 0, 0);   // K-major queries and keys
   constexpr uint32_t id_o = idesc_bf16_f32(128, 64, 0, 1);    // MN-major values, 64 dims at a time
-  const uint64_t q_desc = smem_desc(smem_u32(q_smem), 16, 1024, kSwizzle128B);
-  const uint64_t k_desc = smem_desc(smem_u32(ring), 16, 1024, kSwizzle128B);
-  const uint64_t v_desc = smem_desc(smem_u32(ring), kChunk, 1024, kSwizzle128B);
-  uint32_t n = 0;                          // ring chunks of the tiles before
+  constexpr uint32_t hi = desc_hi(1024, kSwizzle128B);
+  const uint32_t q_lo = desc_lo(smem_u32(q_smem), 16), k_lo = desc_lo(smem_u32(ring), 16),
+                 v_lo = desc_lo(smem_u32(ring), kChunk);
+  uint32_t n = 0, items = 0;               // ring chunks of the tiles before, items
   uint32_t q_used[2] = {0, 0}, p_used[2] = {0, 0};
 
   // S_t = Q_t K: chunks n0..n0+2
   auto scores = [&](int t, uint32_t n0) {
-    if (lane == 0) {
+    if (elect_one()) {
 #pragma unroll
       for (int c = 0; c < 3; ++c) {
-        const uint32_t slot = (n0 + c) % kRing;
+        const uint32_t k0 = k_lo + ((n0 + c) % kRing) * (kChunk >> 4);
+        const uint32_t q0 = q_lo + ((t * kQTile + c * kChunk) >> 4);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          mma_ss(tbase + kColS + 128 * t, q_desc + ((t * kQTile + c * kChunk + k * 32) >> 4),
-                 k_desc + ((slot * kChunk + k * 32) >> 4), id_s, (c | k) ? 1u : 0u);
+          mma_ss_lo(tbase + kColS + 128 * t, q0 + 2 * k, hi, k0 + 2 * k, hi, id_s, (c | k) ? 1u : 0u);
       }
       mma_commit(smem_u32(&bars->s_full[t]));
     }
+    __syncwarp();
   };
   auto wait_chunks = [&](uint32_t n0, int count) {
     for (int c = 0; c < count; ++c) wait_bar(ctx, &bars->full[(n0 + c) % kRing], ((n0 + c) / kRing) & 1);
   };
   auto release = [&](uint32_t n0, int count) {
-    if (lane == 0)
+    if (elect_one())
       for (int c = 0; c < count; ++c) mma_commit(smem_u32(&bars->empty[(n0 + c) % kRing]));
+    __syncwarp();
   };
 
-  for (int round = 0;; ++round) {
-    const int64_t i = item_index(round);
-    if ((int64_t)round * gridDim.x >= items) break;
-    if (i >= items) continue;
-    const Item it = item_at(a, np, i);
+  while (true) {
+    const Item it = next_item(ctx, slots, items, lane);
+    if (it.last) break;
     const int tiles = max(it.tiles[0], it.tiles[1]);
     if (tiles == 0) continue;
     // first scores of both tiles
@@ -218,7 +256,7 @@ __device__ __forceinline__ void issue_items(const PrefillArgs& a, const Ctx& ctx
       wait_bar(ctx, &bars->q_full[t], q_used[t] & 1);
       tc_fence_after();
       scores(t, n);
-      if (it.tiles[t] == 1 && lane == 0) mma_commit(smem_u32(&bars->q_empty[t]));
+      if (it.tiles[t] == 1 && elect_one()) mma_commit(smem_u32(&bars->q_empty[t]));
       ++q_used[t];
     }
     release(n, 3);
@@ -245,13 +283,13 @@ __device__ __forceinline__ void issue_items(const PrefillArgs& a, const Ctx& ctx
           wait_bar(ctx, &bars->p_full[t], p_used[t] & 1);
           ++p_used[t];
           tc_fence_after();
-          if (lane == 0) {
+          if (elect_one()) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const uint64_t vd = v_desc + ((((n + 3 + h) % kRing) * kChunk) >> 4);
+              const uint32_t v0 = v_lo + ((n + 3 + h) % kRing) * (kChunk >> 4);
               for (int k = 0; k < steps; ++k)
-                mma_ts(tbase + kColO + 128 * t + 64 * h, tbase + kColS + 128 * t + 8 * k, vd + ((k * 2048) >> 4),
-                       id_o, (j | k) ? 1u : 0u);
+                mma_ts_lo(tbase + kColO + 128 * t + 64 * h, tbase + kColS + 128 * t + 8 * k, v0 + 128 * k, hi, id_o,
+                          (j | k) ? 1u : 0u);
             }
             if (j + 1 == it.tiles[t]) mma_commit(smem_u32(&bars->o_full[t]));
           }
@@ -260,14 +298,14 @@ __device__ __forceinline__ void issue_items(const PrefillArgs& a, const Ctx& ctx
         if (more && t == 0) wait_chunks(n + 5, 3);
         if (j + 1 < it.tiles[t]) {
           scores(t, n + 5);
-          if (j + 2 == it.tiles[t] && lane == 0) mma_commit(smem_u32(&bars->q_empty[t]));
+          if (j + 2 == it.tiles[t] && elect_one()) mma_commit(smem_u32(&bars->q_empty[t]));
         }
         if (more && t == 1) release(n + 5, 3);
       }
       __syncwarp();
     }
   }
-  if (lane == 0) {
+  if (elect_one()) {
     mma_commit(smem_u32(&bars->drain));
     mbar_wait(smem_u32(&bars->drain), 0, ctx.limit_ns);
   }
@@ -320,21 +358,19 @@ __device__ __noinline__ void mend_row(const PrefillArgs& a, int row, int head, i
 }
 
 // ------------------------------------------------------------------ softmax
-__device__ __forceinline__ void softmax_items(const PrefillArgs& a, const Ctx& ctx, int np, int64_t items,
-                                              uint32_t tbase, int warp, int lane) {
+__device__ __forceinline__ void softmax_items(const PrefillArgs& a, const Ctx& ctx, const Item* slots, uint32_t tbase,
+                                              int warp, int lane) {
   Bars* bars = ctx.bars;
   const int t = warp >> 2, quad = warp & 3;
   const uint32_t lanes = (uint32_t)(32 * quad) << 16;
   const uint32_t s_col = tbase + lanes + kColS + 128 * t, o_col = tbase + lanes + kColO + 128 * t;
   const int row = 128 * t + 32 * quad + lane;
   const float scale = a.scale_log2;
-  uint32_t s_used = 0, o_used = 0;
+  uint32_t items = 0, s_used = 0, o_used = 0;
 
-  for (int round = 0;; ++round) {
-    const int64_t i = item_index(round);
-    if ((int64_t)round * gridDim.x >= items) break;
-    if (i >= items) continue;
-    const Item it = item_at(a, np, i);
+  while (true) {
+    const Item it = next_item(ctx, slots, items, lane);
+    if (it.last) break;
     const int tiles = it.tiles[t];
     const int sees = min(max(it.lim0 + (a.causal ? row : 0), 0), it.nkeys);
     const int warp_sees = min(max(it.lim0 + (a.causal ? row - lane : 0), 0), it.nkeys);   // its first row: the fewest
@@ -373,13 +409,13 @@ __device__ __forceinline__ void softmax_items(const PrefillArgs& a, const Ctx& c
           // the scores' arrival implies that the products before them are
           // done, and the next one waits for this warp
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            uint32_t o[32];
-            tmem_ld32(o_col + 32 * g, o);
+          for (int g = 0; g < 8; ++g) {
+            uint32_t o[16];
+            tmem_ld16(o_col + 16 * g, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
-            tmem_st32(o_col + 32 * g, o);
+            for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+            tmem_st16(o_col + 16 * g, o);
           }
         }
         sum *= alpha;
@@ -485,12 +521,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* q_smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t* ring = q_smem + 2 * kQTile;
   Bars* bars = reinterpret_cast<Bars*>(ring + kRing * kChunk);
+  Item* slots = reinterpret_cast<Item*>(((uintptr_t)(bars + 1) + 15) & ~(uintptr_t)15);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kRing; ++i) {
       mbar_init(smem_u32(&bars->full[i]), 1);
       mbar_init(smem_u32(&bars->empty[i]), 1);
+    }
+    for (int i = 0; i < kItemSlots; ++i) {
+      mbar_init(smem_u32(&bars->item_full[i]), 1);
+      mbar_init(smem_u32(&bars->item_empty[i]), kItemReaders);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(smem_u32(&bars->q_full[t]), 1);
@@ -520,19 +561,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const Ctx ctx{bars, &a.plan.header->status, a.wait_limit_ns};
-  const int np = a.plan.header->num_pieces;
-  const int64_t items = (int64_t)np * a.num_heads;
-
   if (warp < kSoftmaxWarps) {
     setmaxnreg_inc<kRegsSoftmax>();
-    softmax_items(a, ctx, np, items, tbase, warp, lane);
+    softmax_items(a, ctx, slots, tbase, warp, lane);
   } else {
     setmaxnreg_dec<kRegsOther>();
     if (warp == kWarpLoad) {
-      if (lane == 0) load_items(a, ctx, np, items, &tm_q, &tm_kv, &tm_pe, q_smem, ring);
-      __syncwarp();
+      load_items(ctx, slots, &tm_q, &tm_kv, &tm_pe, smem_u32(q_smem), smem_u32(ring), lane);
     } else if (warp == kWarpMma) {
-      issue_items(a, ctx, np, items, tbase, q_smem, ring, lane);
+      issue_items(ctx, slots, tbase, q_smem, ring, lane);
+    } else if (warp == kWarpList) {
+      if (lane == 0) list_items(a, ctx, a.plan.header->num_pieces, slots);
+      __syncwarp();
     }
   }
   tc_fence_before();

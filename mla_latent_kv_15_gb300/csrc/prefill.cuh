@@ -21,7 +21,8 @@ struct PrefillHeader {
   int status;        // OR of mla_device_error bits
   int num_pieces;
   int num_split;     // blocks cut into more than one piece
-  int pad[5];
+  int next;          // items handed out beyond every CTA's first
+  int pad[4];
 };
 
 struct PrefillPiece {  // 32 bytes

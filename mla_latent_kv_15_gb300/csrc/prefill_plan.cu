@@ -78,6 +78,7 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArg
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x;
+  if (tid == 0) a.plan.header->next = 0;
   if (tid == 0) s_total = 0, s_longest = 0, s_status = 0, s_rows = 0, s_split = 0;
   for (int i = tid; i < kBuckets; i += kThreads) s_hist[i] = 0;
   __syncthreads();
