@@ -648,7 +648,7 @@ int mla_prefill(const void* q, int64_t q_token_stride, int64_t q_head_stride, co
   if (workspace_bytes < L.total)
     return fail(MLA_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu required", workspace_bytes, L.total);
   const int sms = sm_count();
-  if (sms < 1) return fail(MLA_ERR_CUDA, "cannot query the current device");
+  if (sms < 2) return fail(MLA_ERR_CUDA, "cannot query the current device");
 
   CUtensorMap tm_q, tm_kv, tm_pe;
   bool enc = mla::encode_tmap_3d(&tm_q, q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (uint64_t)qd, (uint64_t)num_heads,
@@ -659,9 +659,9 @@ int mla_prefill(const void* q, int64_t q_token_stride, int64_t q_head_stride, co
     enc = enc &&
           mla::encode_tmap_3d(&tm_kv, kv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (uint64_t)kvd, (uint64_t)num_heads,
                               (uint64_t)total_kv, (uint64_t)kv_head_stride * 2, (uint64_t)kv_token_stride * 2, 64, 1,
-                              mla::kPrefillTile, CU_TENSOR_MAP_SWIZZLE_128B) &&
+                              mla::kPrefillTile / 2, CU_TENSOR_MAP_SWIZZLE_128B) &&
           mla::encode_tmap_2d(&tm_pe, k_pe, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, mla::kRope, (uint64_t)total_kv,
-                              (uint64_t)k_pe_stride * 2, 64, mla::kPrefillTile, CU_TENSOR_MAP_SWIZZLE_128B);
+                              (uint64_t)k_pe_stride * 2, 64, mla::kPrefillTile / 2, CU_TENSOR_MAP_SWIZZLE_128B);
   if (!enc) return fail(MLA_ERR_CUDA, "cuTensorMapEncodeTiled rejected a tensor layout");
 
   mla::PrefillArgs a{};
@@ -685,7 +685,7 @@ int mla_prefill(const void* q, int64_t q_token_stride, int64_t q_head_stride, co
   const int64_t head_bytes = (int64_t)total_kv * kvd * 2 + 1;
   const int64_t fit = (48LL << 20) / head_bytes;
   a.group_heads = (int)(fit < 1 ? 1 : fit > num_heads ? num_heads : fit);
-  a.ctas = sms < mla::kPrefillMaxCtas ? sms : mla::kPrefillMaxCtas;
+  a.pairs = sms / 2 < mla::kPrefillMaxPairs ? sms / 2 : mla::kPrefillMaxPairs;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.out = out;
   a.lse = lse;

@@ -5,12 +5,16 @@
 //   s_ij = scale * (q_nope_i . k_nope_j + q_pe_i . k_pe_j)
 //   out_i = sum_j exp(s_ij - m_i) v_j / sum_j exp(s_ij - m_i)
 //
-// One CTA per SM takes items (256 query rows of a head x a range of keys) and
-// holds two 128-row query tiles in shared memory.  Keys and values stream in
-// tiles of 128 as 16 KB chunks of 64 dims (three of the key, the last one from
-// the shared rotated keys, two of the value) through a ring of eight.  Tensor
-// memory: scores S0, S1 and outputs O0, O1, 128 columns each; a tile's
-// probabilities (bf16) overwrite its scores.  One thread issues, per key tile,
+// A pair of CTAs takes items (512 query rows of a head x a range of keys): a
+// product of the pair has 256 query rows, 128 in each CTA, against keys and
+// values of which each CTA holds half (64 of a tile's 128 keys for the scores,
+// 64 of the 128 value dims for the outputs), so that a key is loaded once for
+// 512 queries and shared memory has room for three tiles beside the queries
+// (a single-CTA form, with room for 1.6, waited for loads a third of the
+// time: 8192-token prompt of 128 heads, 2245 us).  Tensor memory of each CTA:
+// scores S0, S1 and outputs O0, O1, 128 columns each; a tile's
+// probabilities (bf16) overwrite its scores.  One thread of the leading CTA
+// issues, per key tile,
 //   O0 += P0 V_j,  S0 = Q0 K_{j+1},  O1 += P1 V_j,  S1 = Q1 K_{j+1}
 // so the tensor cores work on one query tile while the softmax warps of the
 // other turn its scores into probabilities.  The softmax thread of a row
@@ -28,46 +32,67 @@ namespace {
 using namespace ptx;
 
 constexpr int kSoftmaxWarps = 8;                  // 0-3: query tile 0, 4-7: query tile 1
-constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpList = 10;   // warp 11 only fills the warpgroup
+constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpList = 10, kWarpClear = 11;
 constexpr int kItemSlots = 2;                     // items known ahead
-constexpr int kItemReaders = kSoftmaxWarps + 2;   // warps that read each item
+constexpr int kItemReaders = 2 * (kSoftmaxWarps + 2) + 2;   // both CTAs' softmax, load and clearing warps, the MMA warp, the peer's list warp
 constexpr int kThreads = 384;
 constexpr uint32_t kRegsSoftmax = 208, kRegsOther = 88;
 static_assert(128 * (2 * kRegsSoftmax + kRegsOther) <= kThreads * 168, "register split of the launch's 168 a thread");
 
-constexpr uint32_t kChunk = 16384;                // 128 rows x 64 dims
-constexpr int kRing = 8;
-constexpr uint32_t kQTile = 3 * kChunk;
+constexpr uint32_t kQChunk = 16384;               // 128 rows x 64 dims
+constexpr uint32_t kQTile = 3 * kQChunk;
+constexpr uint32_t kBox = 8192;                   // 64 rows x 64 dims: one load of keys or values
+constexpr uint32_t kKeyBytes = 3 * kBox;          // the CTA's 64 keys of a tile
+constexpr uint32_t kValueBytes = 2 * kBox;        // the CTA's 64 value dims of a tile's 128 keys
+constexpr uint32_t kStage = kKeyBytes + kValueBytes;
+constexpr int kStages = 3;
 constexpr uint32_t kColS = 0, kColO = 256;        // S0 S1 O0 O1
 constexpr float kRescale = 8.0f;                  // log2 units
 
+// Barriers marked (lead) are used in the leading CTA only, by both CTAs.
 struct Bars {
-  uint64_t full[kRing], empty[kRing];
-  uint64_t q_full[2], q_empty[2];
-  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t k_full[kStages], v_full[kStages];      // (lead) both CTAs' halves have landed
+  uint64_t k_empty[kStages], v_empty[kStages];
+  uint64_t v_tail[kStages];                       // the CTA's half of a value tile with rows to clear has landed
+  uint64_t q_full[2];                             // (lead)
+  uint64_t q_empty[2];
+  uint64_t s_full[2], o_full[2];
+  uint64_t p_full[2];                             // (lead) all softmax warps of the pair
   uint64_t drain;
-  uint64_t item_full[kItemSlots], item_empty[kItemSlots];
+  uint64_t item_full[kItemSlots];
+  uint64_t item_empty[kItemSlots];                // (lead)
   uint32_t tmem_base;
   int abort;
 };
-constexpr size_t kSmem = 1024 + 2 * kQTile + kRing * kChunk + sizeof(Bars) + 16 + kItemSlots * 48;
+constexpr size_t kSmem = 1024 + 2 * kQTile + kStages * kStage + sizeof(Bars) + 16 + kItemSlots * 48;
 static_assert(kSmem <= 232448, "shared memory per CTA");
 
 struct Ctx {
   Bars* bars;
+  uint32_t rank;      // in the pair; 0 leads
   int* status;
   uint64_t limit_ns;
+  // shared::cluster address of the leading CTA's copy of one of `bars`
+  __device__ __forceinline__ uint32_t lead(uint64_t* bar) const { return mapa(smem_u32(bar), 0); }
 };
 
-// Bounded waits; once one has run out, every later one returns at once.
-__device__ __forceinline__ void wait_bar(const Ctx& c, uint64_t* bar, uint32_t parity) {
-  if (mbar_try_wait(smem_u32(bar), parity)) return;
-  if (*(volatile int*)&c.bars->abort) return;
-  if (!mbar_wait(smem_u32(bar), parity, c.limit_ns)) {
-    *(volatile int*)&c.bars->abort = 1;
-    atomicOr(c.status, 1);   // MLA_DEVERR_TIMEOUT
+// Bounded waits; once one has run out, every other one of the CTA returns, and
+// the peer's run out in turn.  Waits for an item may last as long as the item
+// before it (`times` the limit).
+__device__ __forceinline__ void wait_bar(const Ctx& c, uint64_t* bar, uint32_t parity, uint32_t times = 1) {
+  const uint32_t at = smem_u32(bar);
+  if (mbar_try_wait(at, parity)) return;
+  const uint64_t t0 = globaltimer();
+  while (!mbar_try_wait_hint(at, parity, kWaitHintNs)) {
+    if (*(volatile int*)&c.bars->abort) return;
+    if (globaltimer() - t0 > c.limit_ns * times) {
+      *(volatile int*)&c.bars->abort = 1;
+      atomicOr(c.status, 1);   // MLA_DEVERR_TIMEOUT
+      return;
+    }
   }
 }
+constexpr uint32_t kItemWait = 64;
 
 struct __align__(16) Item {
   int q0, nq, kv0, nkeys, lim0, prow, head;
@@ -90,44 +115,65 @@ __device__ __forceinline__ Item item_at(const PrefillArgs& a, int np, int i) {
   it.head = g * a.group_heads + rem - p * heads;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    const int last = min(128 * (t + 1), it.nq) - 1;
-    it.seen[t] = it.nq > 128 * t ? min(max(it.lim0 + (a.causal ? last : 0), 0), it.nkeys) : 0;
+    const int last = min(256 * (t + 1), it.nq) - 1;
+    it.seen[t] = it.nq > 256 * t ? min(max(it.lim0 + (a.causal ? last : 0), 0), it.nkeys) : 0;
     it.tiles[t] = (it.seen[t] + kPrefillTile - 1) / kPrefillTile;
   }
   it.last = 0;
   return it;
 }
 
-// The list warp hands the CTA's items to the other warps: the first is the
-// CTA's own, the next come from a counter all CTAs share, so that a CTA done
-// early takes more.
+// The leading CTA's list warp (one thread) hands the pair's items to both
+// CTAs: the first is the pair's own, the next come from a counter all pairs
+// share, so that a pair done early takes more.
 __device__ __forceinline__ void list_items(const PrefillArgs& a, const Ctx& ctx, int np, Item* slots) {
   Bars* bars = ctx.bars;
   const int items = np * a.num_heads;
-  int i = blockIdx.x;
+  const int pairs = gridDim.x / 2;
+  int i = cluster_id_x();
   for (uint32_t n = 0;; ++n) {
     const uint32_t slot = n % kItemSlots;
     Item it{};
     it.last = 1;
     if (i < items) it = item_at(a, np, i);
-    wait_bar(ctx, &bars->item_empty[slot], ((n / kItemSlots) & 1) ^ 1);
-    if (*(volatile int*)&bars->abort) break;
+    wait_bar(ctx, &bars->item_empty[slot], ((n / kItemSlots) & 1) ^ 1, kItemWait);
+    if (*(volatile int*)&bars->abort) it.last = 1;    // the peer is told
     slots[slot] = it;
     mbar_arrive(smem_u32(&bars->item_full[slot]));
+    const uint32_t far = mapa(smem_u32(&slots[slot]), 1), far_bar = mapa(smem_u32(&bars->item_full[slot]), 1);
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(&it);
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+      st_async_v4(far + 16 * k, w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3], far_bar);
     if (it.last) break;
-    i = gridDim.x + atomicAdd(&a.plan.header->next, 1);
+    i = pairs + atomicAdd(&a.plan.header->next, 1);
+  }
+}
+
+// The peer's list warp (one thread) arms its barriers for the items sent to it.
+__device__ __forceinline__ void await_items(const Ctx& ctx, const Item* slots) {
+  Bars* bars = ctx.bars;
+  for (uint32_t n = 0;; ++n) {
+    const uint32_t slot = n % kItemSlots;
+    mbar_expect_tx(smem_u32(&bars->item_full[slot]), sizeof(Item));
+    wait_bar(ctx, &bars->item_full[slot], (n / kItemSlots) & 1, kItemWait);
+    fence_cluster();
+    const bool last = *(volatile const int*)&slots[slot].last != 0;
+    mbar_arrive_remote(ctx.lead(&bars->item_empty[slot]));
+    if (last || *(volatile int*)&bars->abort) break;
   }
 }
 
 // The next item, read by a whole warp; one without work behind the last or after an abort.
 __device__ __forceinline__ Item next_item(const Ctx& ctx, const Item* slots, uint32_t& n, int lane) {
   const uint32_t slot = n % kItemSlots;
-  wait_bar(ctx, &ctx.bars->item_full[slot], (n / kItemSlots) & 1);
+  wait_bar(ctx, &ctx.bars->item_full[slot], (n / kItemSlots) & 1, kItemWait);
+  fence_cluster();   // the peer's item was written by the leading CTA
   Item it = slots[slot];
-  __syncwarp();
-  if (lane == 0) mbar_arrive(smem_u32(&ctx.bars->item_empty[slot]));
-  ++n;
   if (*(volatile int*)&ctx.bars->abort) it.last = 1;
+  __syncwarp();
+  if (lane == 0) mbar_arrive_remote(ctx.lead(&ctx.bars->item_empty[slot]));
+  ++n;
   return it;
 }
 
@@ -146,40 +192,33 @@ __device__ __forceinline__ void fma2(float& r0, float& r1, float a0, float a1, f
       " fma.rn.f32x2 x, x, y, z;\n mov.b64 {%0, %1}, x;\n}" : "=f"(r0), "=f"(r1) : "f"(a0), "f"(a1), "f"(b), "f"(c));
 }
 
+// Whether the last value tile of an item has rows past its keys inside the
+// last 16-key step of the products.  They meet probabilities of zero, but may
+// hold anything, so they are cleared.
+__device__ __forceinline__ bool has_tail(const Item& it, int tiles) {
+  const int left = it.nkeys - (tiles - 1) * kPrefillTile;
+  return left < kPrefillTile && (left & 15);
+}
+
 // ------------------------------------------------------------------ producer
-// The whole warp walks the items; one elected thread loads.
+// The whole warp walks the items; one elected thread loads the CTA's halves.
 __device__ __forceinline__ void load_items(const Ctx& ctx, const Item* slots, const CUtensorMap* tm_q,
                                            const CUtensorMap* tm_kv, const CUtensorMap* tm_pe, uint32_t q_smem,
                                            uint32_t ring, int lane) {
   Bars* bars = ctx.bars;
   uint32_t n = 0, items = 0, q_used[2] = {0, 0};
   volatile int* abort_flag = &bars->abort;
-  // one chunk into the next ring slot; a load is skipped once the CTA gives up
-  auto chunk = [&](const CUtensorMap* map, bool three, int x, int head, int row) {
-    const uint32_t slot = n % kRing;
-    wait_bar(ctx, &bars->empty[slot], ((n / kRing) & 1) ^ 1);
-    if (*abort_flag) return;
-    if (elect_one()) {
-      const uint32_t full = smem_u32(&bars->full[slot]), dst = ring + slot * kChunk;
-      mbar_expect_tx(full, kChunk);
-      if (three)
-        tma_load_3d(dst, map, x, head, row, full);
-      else
-        tma_load_2d(dst, map, x, row, full);
-    }
-    __syncwarp();
-    ++n;
-  };
   auto query = [&](const Item& it, int t) {
-    if (it.tiles[t] == 0 || *abort_flag) return;
+    if (it.tiles[t] == 0) return;
     wait_bar(ctx, &bars->q_empty[t], (q_used[t] & 1) ^ 1);
     if (*abort_flag) return;
     if (elect_one()) {
-      const uint32_t full = smem_u32(&bars->q_full[t]);
-      mbar_expect_tx(full, kQTile);
+      const uint32_t full = ctx.lead(&bars->q_full[t]);
+      mbar_expect_tx_remote(full, kQTile);
 #pragma unroll
       for (int c = 0; c < 3; ++c)
-        tma_load_3d(q_smem + t * kQTile + c * kChunk, tm_q, 64 * c, it.head, it.q0 + 128 * t, full);
+        tma_load_3d_pair(q_smem + t * kQTile + c * kQChunk, tm_q, 64 * c, it.head,
+                         it.q0 + 256 * t + 128 * (int)ctx.rank, full);
     }
     __syncwarp();
     ++q_used[t];
@@ -188,58 +227,101 @@ __device__ __forceinline__ void load_items(const Ctx& ctx, const Item* slots, co
     const Item it = next_item(ctx, slots, items, lane);
     if (it.last) break;
     const int tiles = max(it.tiles[0], it.tiles[1]);
-    query(it, 0);
-    for (int j = 0; j < tiles && !*abort_flag; ++j) {
-      const int row = it.kv0 + j * kPrefillTile;
-      chunk(tm_kv, true, 0, it.head, row);
-      chunk(tm_kv, true, 64, it.head, row);
-      chunk(tm_pe, false, 0, 0, row);
+    if (tiles > 0) query(it, 0);
+    for (int j = 0; j < tiles; ++j, ++n) {
+      const uint32_t stage = n % kStages, parity = ((n / kStages) & 1) ^ 1;
+      const uint32_t dst = ring + stage * kStage;
+      const int row = it.kv0 + j * kPrefillTile, half = row + 64 * (int)ctx.rank;
+      wait_bar(ctx, &bars->k_empty[stage], parity);
+      if (*abort_flag) break;
+      if (elect_one()) {
+        const uint32_t full = ctx.lead(&bars->k_full[stage]);
+        mbar_expect_tx_remote(full, kKeyBytes);
+        tma_load_3d_pair(dst, tm_kv, 0, it.head, half, full);
+        tma_load_3d_pair(dst + kBox, tm_kv, 64, it.head, half, full);
+        tma_load_2d_pair(dst + 2 * kBox, tm_pe, 0, half, full);
+      }
+      __syncwarp();
       if (j == 0) query(it, 1);
-      chunk(tm_kv, true, kNope, it.head, row);
-      chunk(tm_kv, true, kNope + 64, it.head, row);
+      wait_bar(ctx, &bars->v_empty[stage], parity);
+      if (*abort_flag) break;
+      const bool tail = j + 1 == tiles && has_tail(it, tiles);
+      if (elect_one()) {
+        // a tile with rows to clear lands on the CTA's own barrier; the
+        // clearing warp reports it to the leading CTA
+        const uint32_t full = tail ? mapa(smem_u32(&bars->v_tail[stage]), ctx.rank) : ctx.lead(&bars->v_full[stage]);
+        const int x = kNope + 64 * (int)ctx.rank;
+        mbar_expect_tx_remote(full, kValueBytes);
+        tma_load_3d_pair(dst + kKeyBytes, tm_kv, x, it.head, row, full);
+        tma_load_3d_pair(dst + kKeyBytes + kBox, tm_kv, x, it.head, row + 64, full);
+      }
+      __syncwarp();
     }
+    if (*abort_flag) break;
   }
-  // every issued load has landed before the CTA may exit
-  for (uint32_t k = n > kRing ? n - kRing : 0; k < n; ++k)
-    mbar_wait(smem_u32(&bars->full[k % kRing]), (k / kRing) & 1, ctx.limit_ns);
-  for (int t = 0; t < 2; ++t)
-    if (q_used[t] > 0) mbar_wait(smem_u32(&bars->q_full[t]), (q_used[t] - 1) & 1, ctx.limit_ns);
+  // Every load has landed before the pair ends: the leading CTA's barriers
+  // say so for both CTAs, and the pair ends together.
+  if (ctx.rank == 0) {
+    for (uint32_t k = n > kStages ? n - kStages : 0; k < n; ++k) {
+      wait_bar(ctx, &bars->k_full[k % kStages], (k / kStages) & 1);
+      wait_bar(ctx, &bars->v_full[k % kStages], (k / kStages) & 1);
+    }
+    for (int t = 0; t < 2; ++t)
+      if (q_used[t] > 0) wait_bar(ctx, &bars->q_full[t], (q_used[t] - 1) & 1);
+  }
+}
+
+// ------------------------------------------------------------ clearing warp
+__device__ __forceinline__ void clear_tails(const Ctx& ctx, const Item* slots, uint8_t* ring, int lane) {
+  Bars* bars = ctx.bars;
+  uint32_t n = 0, items = 0, used = 0;     // bit s of `used`: parity of stage s's tail barrier
+  while (true) {
+    const Item it = next_item(ctx, slots, items, lane);
+    if (it.last) break;
+    const int tiles = max(it.tiles[0], it.tiles[1]);
+    n += tiles;
+    if (tiles == 0 || !has_tail(it, tiles)) continue;
+    const uint32_t stage = (n - 1) % kStages;
+    wait_bar(ctx, &bars->v_tail[stage], (used >> stage) & 1);
+    used ^= 1u << stage;
+    const int left = it.nkeys - (tiles - 1) * kPrefillTile, rows = 16 - (left & 15);
+    uint8_t* v = ring + stage * kStage + kKeyBytes + left * 128;
+    for (int e = lane; e < rows * 8; e += 32) *reinterpret_cast<uint4*>(v + 16 * e) = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive_release_cluster(ctx.lead(&bars->v_full[stage]));
+  }
 }
 
 // -------------------------------------------------------------- MMA issuer
-// The whole warp walks the items together; one elected thread issues.
-__device__ __forceinline__ void issue_items(const Ctx& ctx, const Item* slots, uint32_t tbase, uint8_t* q_smem,
-                                            uint8_t* ring, int lane) {
+// One warp of the leading CTA walks the items; one elected thread issues.
+__device__ __forceinline__ void issue_items(const Ctx& ctx, const Item* slots, uint32_t tbase, uint32_t q_smem,
+                                            uint32_t ring, int lane) {
   Bars* bars = ctx.bars;
-  constexpr uint32_t id_s = idesc_bf16_f32(128, 128, 0, 0);   // K-major queries and keys
-  constexpr uint32_t id_o = idesc_bf16_f32(128, 64, 0, 1);    // MN-major values, 64 dims at a time
+  constexpr uint32_t id_s = idesc_bf16_f32(256, 128, 0, 0);   // K-major queries and keys
+  constexpr uint32_t id_o = idesc_bf16_f32(256, 128, 0, 1);   // MN-major values
   constexpr uint32_t hi = desc_hi(1024, kSwizzle128B);
-  const uint32_t q_lo = desc_lo(smem_u32(q_smem), 16), k_lo = desc_lo(smem_u32(ring), 16),
-                 v_lo = desc_lo(smem_u32(ring), kChunk);
-  uint32_t n = 0, items = 0;               // ring chunks of the tiles before, items
+  const uint32_t q_lo = desc_lo(q_smem, 16), k_lo = desc_lo(ring, 16), v_lo = desc_lo(ring + kKeyBytes, kValueBytes);
+  uint32_t n = 0, items = 0;               // tiles before, items
   uint32_t q_used[2] = {0, 0}, p_used[2] = {0, 0};
 
-  // S_t = Q_t K: chunks n0..n0+2
-  auto scores = [&](int t, uint32_t n0) {
+  // S_t = Q_t K of tile m
+  auto scores = [&](int t, uint32_t m, bool q_done) {
     if (elect_one()) {
+      const uint32_t k0 = k_lo + (m % kStages) * (kStage >> 4), q0 = q_lo + ((t * kQTile) >> 4);
 #pragma unroll
-      for (int c = 0; c < 3; ++c) {
-        const uint32_t k0 = k_lo + ((n0 + c) % kRing) * (kChunk >> 4);
-        const uint32_t q0 = q_lo + ((t * kQTile + c * kChunk) >> 4);
+      for (int c = 0; c < 3; ++c)
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          mma_ss_lo(tbase + kColS + 128 * t, q0 + 2 * k, hi, k0 + 2 * k, hi, id_s, (c | k) ? 1u : 0u);
-      }
-      mma_commit(smem_u32(&bars->s_full[t]));
+          mma_pair_ss(tbase + kColS + 128 * t, q0 + ((c * kQChunk) >> 4) + 2 * k, hi, k0 + ((c * kBox) >> 4) + 2 * k,
+                      hi, id_s, (c | k) ? 1u : 0u);
+      mma_commit_pair(smem_u32(&bars->s_full[t]));
+      if (q_done) mma_commit_pair(smem_u32(&bars->q_empty[t]));
     }
     __syncwarp();
   };
-  auto wait_chunks = [&](uint32_t n0, int count) {
-    for (int c = 0; c < count; ++c) wait_bar(ctx, &bars->full[(n0 + c) % kRing], ((n0 + c) / kRing) & 1);
-  };
-  auto release = [&](uint32_t n0, int count) {
-    if (elect_one())
-      for (int c = 0; c < count; ++c) mma_commit(smem_u32(&bars->empty[(n0 + c) % kRing]));
+  auto release = [&](uint64_t* bar) {
+    if (elect_one()) mma_commit_pair(smem_u32(bar));
     __syncwarp();
   };
 
@@ -249,33 +331,21 @@ __device__ __forceinline__ void issue_items(const Ctx& ctx, const Item* slots, u
     const int tiles = max(it.tiles[0], it.tiles[1]);
     if (tiles == 0) continue;
     // first scores of both tiles
-    wait_chunks(n, 3);
+    wait_bar(ctx, &bars->k_full[n % kStages], (n / kStages) & 1);
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       if (it.tiles[t] == 0) continue;
       wait_bar(ctx, &bars->q_full[t], q_used[t] & 1);
       tc_fence_after();
-      scores(t, n);
-      if (it.tiles[t] == 1 && elect_one()) mma_commit(smem_u32(&bars->q_empty[t]));
+      scores(t, n, it.tiles[t] == 1);
       ++q_used[t];
     }
-    release(n, 3);
-    for (int j = 0; j < tiles; ++j, n += 5) {
+    release(&bars->k_empty[n % kStages]);
+    for (int j = 0; j < tiles; ++j, ++n) {
       const bool more = j + 1 < tiles;
-      const int left = it.nkeys - j * kPrefillTile;     // keys of the piece from this tile on
-      wait_chunks(n + 3, 2);
-      if (left < kPrefillTile && (left & 15)) {
-        // value rows past the piece's keys meet probabilities of zero, but
-        // may hold anything: clear those inside the last 16-key step
-        const int r0 = left, rows = 16 - (left & 15);
-        for (int e = lane; e < rows * 16; e += 32) {
-          const uint32_t slot = (n + 3 + (e & 1)) % kRing;
-          *reinterpret_cast<uint4*>(ring + slot * kChunk + (r0 + (e >> 4)) * 128 + ((e >> 1) & 7) * 16) =
-              make_uint4(0, 0, 0, 0);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-      }
+      wait_bar(ctx, &bars->v_full[n % kStages], (n / kStages) & 1);
+      if (!more && has_tail(it, tiles)) fence_cluster();   // rows that a thread of each CTA has cleared
+      if (more) wait_bar(ctx, &bars->k_full[(n + 1) % kStages], ((n + 1) / kStages) & 1);
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         if (j < it.tiles[t]) {
@@ -284,31 +354,23 @@ __device__ __forceinline__ void issue_items(const Ctx& ctx, const Item* slots, u
           ++p_used[t];
           tc_fence_after();
           if (elect_one()) {
+            const uint32_t v0 = v_lo + (n % kStages) * (kStage >> 4);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t v0 = v_lo + ((n + 3 + h) % kRing) * (kChunk >> 4);
-              for (int k = 0; k < steps; ++k)
-                mma_ts_lo(tbase + kColO + 128 * t + 64 * h, tbase + kColS + 128 * t + 8 * k, v0 + 128 * k, hi, id_o,
-                          (j | k) ? 1u : 0u);
-            }
-            if (j + 1 == it.tiles[t]) mma_commit(smem_u32(&bars->o_full[t]));
+            for (int k = 0; k < kPrefillTile / 16; ++k)
+              if (k < steps)
+                mma_pair_ts(tbase + kColO + 128 * t, tbase + kColS + 128 * t + 8 * k, v0 + 128 * k, hi, id_o,
+                            (j | k) ? 1u : 0u);
+            if (j + 1 == it.tiles[t]) mma_commit_pair(smem_u32(&bars->o_full[t]));
           }
+          __syncwarp();
         }
-        if (t == 1) release(n + 3, 2);
-        if (more && t == 0) wait_chunks(n + 5, 3);
-        if (j + 1 < it.tiles[t]) {
-          scores(t, n + 5);
-          if (j + 2 == it.tiles[t] && elect_one()) mma_commit(smem_u32(&bars->q_empty[t]));
-        }
-        if (more && t == 1) release(n + 5, 3);
+        if (t == 1) release(&bars->v_empty[n % kStages]);
+        if (j + 1 < it.tiles[t]) scores(t, n + 1, j + 2 == it.tiles[t]);
+        if (more && t == 1) release(&bars->k_empty[(n + 1) % kStages]);
       }
-      __syncwarp();
     }
   }
-  if (elect_one()) {
-    mma_commit(smem_u32(&bars->drain));
-    mbar_wait(smem_u32(&bars->drain), 0, ctx.limit_ns);
-  }
+  if (elect_one()) mma_commit_pair(smem_u32(&bars->drain));
   __syncwarp();
 }
 
@@ -357,6 +419,72 @@ __device__ __noinline__ void mend_row(const PrefillArgs& a, int row, int head, i
   }
 }
 
+// One tile of a warp's rows: scores to probabilities, with the row's reference
+// and sum; `left` keys of the tile are seen where a mask crosses it.
+template <bool kMasked>
+__device__ __forceinline__ void softmax_tile(uint32_t s_col, uint32_t o_col, float scale, int left, bool first,
+                                             float& ref, float& sum) {
+  uint32_t s[4][32];
+  float top[4];
+#pragma unroll
+  for (int g = 0; g < 4; ++g) tmem_ld32_max(s_col + 32 * g, s[g], top[g]);
+  tmem_wait_ld();
+  float m;
+  if (!kMasked) {
+    m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+  } else {
+    m = -INFINITY;
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+#pragma unroll
+      for (int c = 0; c < 32; ++c) {
+        const float v = 32 * g + c < left ? __uint_as_float(s[g][c]) : -INFINITY;
+        s[g][c] = __float_as_uint(v);
+        m = fmaxf(m, v);
+      }
+  }
+  m *= scale;
+  const bool raise = m > ref + kRescale;
+  if (__any_sync(0xffffffffu, raise)) {
+    const float next = raise ? m : ref;
+    const float alpha = raise ? fast_exp2(ref - next) : 1.f;   // ref = -inf: 0
+    if (!first) {
+      // the scores' arrival implies that the products before them are
+      // done, and the next one waits for this warp
+#pragma unroll
+      for (int g = 0; g < 8; ++g) {
+        uint32_t o[16];
+        tmem_ld16(o_col + 16 * g, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+        tmem_st16(o_col + 16 * g, o);
+      }
+    }
+    sum *= alpha;
+    ref = next;
+  }
+  const float sub = ref == -INFINITY ? 0.f : ref;
+  float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    uint32_t p[16];
+#pragma unroll
+    for (int c = 0; c < 32; c += 4) {
+      float x0, x1, x2, x3;
+      fma2(x0, x1, __uint_as_float(s[g][c]), __uint_as_float(s[g][c + 1]), scale, -sub);
+      fma2(x2, x3, __uint_as_float(s[g][c + 2]), __uint_as_float(s[g][c + 3]), scale, -sub);
+      x0 = fast_exp2(x0), x1 = fast_exp2(x1), x2 = fast_exp2(x2), x3 = fast_exp2(x3);
+      add2(s0, s1, x0, x1);
+      add2(s2, s3, x2, x3);
+      p[c / 2] = pack_bf16x2(x0, x1);
+      p[c / 2 + 1] = pack_bf16x2(x2, x3);
+    }
+    tmem_st16(s_col + 16 * g, p);
+  }
+  sum += (s0 + s1) + (s2 + s3);
+}
+
 // ------------------------------------------------------------------ softmax
 __device__ __forceinline__ void softmax_items(const PrefillArgs& a, const Ctx& ctx, const Item* slots, uint32_t tbase,
                                               int warp, int lane) {
@@ -364,8 +492,9 @@ __device__ __forceinline__ void softmax_items(const PrefillArgs& a, const Ctx& c
   const int t = warp >> 2, quad = warp & 3;
   const uint32_t lanes = (uint32_t)(32 * quad) << 16;
   const uint32_t s_col = tbase + lanes + kColS + 128 * t, o_col = tbase + lanes + kColO + 128 * t;
-  const int row = 128 * t + 32 * quad + lane;
+  const int row = 256 * t + 128 * (int)ctx.rank + 32 * quad + lane;
   const float scale = a.scale_log2;
+  const uint32_t p_full = ctx.lead(&bars->p_full[t]);
   uint32_t items = 0, s_used = 0, o_used = 0;
 
   while (true) {
@@ -374,80 +503,40 @@ __device__ __forceinline__ void softmax_items(const PrefillArgs& a, const Ctx& c
     const int tiles = it.tiles[t];
     const int sees = min(max(it.lim0 + (a.causal ? row : 0), 0), it.nkeys);
     const int warp_sees = min(max(it.lim0 + (a.causal ? row - lane : 0), 0), it.nkeys);   // its first row: the fewest
+    const int warp_most = min(max(it.lim0 + (a.causal ? row - lane + 31 : 0), 0), it.nkeys);   // its last: the most
+    const bool idle = row - lane >= it.nq;          // a warp without rows only keeps the others company
     float ref = -INFINITY, sum = 0.f;
 
     for (int j = 0; j < tiles; ++j, ++s_used) {
       wait_bar(ctx, &bars->s_full[t], s_used & 1);
       tc_fence_after();
-      uint32_t s[4][32];
-      float top[4];
+      if (idle || warp_most <= j * kPrefillTile) {
+        if (!idle) {
+          // every key of the tile is masked
+          uint32_t zero[16];
 #pragma unroll
-      for (int g = 0; g < 4; ++g) tmem_ld32_max(s_col + 32 * g, s[g], top[g]);
-      tmem_wait_ld();
-      float m;
-      if (warp_sees >= (j + 1) * kPrefillTile) {
-        m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-      } else {
-        // a mask crosses this tile
-        const int left = sees - j * kPrefillTile;
-        m = -INFINITY;
+          for (int c = 0; c < 16; ++c) zero[c] = 0;
 #pragma unroll
-        for (int g = 0; g < 4; ++g)
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            const float v = 32 * g + c < left ? __uint_as_float(s[g][c]) : -INFINITY;
-            s[g][c] = __float_as_uint(v);
-            m = fmaxf(m, v);
-          }
-      }
-      m *= scale;
-      const bool raise = m > ref + kRescale;
-      if (__any_sync(0xffffffffu, raise)) {
-        const float next = raise ? m : ref;
-        const float alpha = raise ? fast_exp2(ref - next) : 1.f;   // ref = -inf: 0
-        if (j > 0) {
-          // the scores' arrival implies that the products before them are
-          // done, and the next one waits for this warp
-#pragma unroll
-          for (int g = 0; g < 8; ++g) {
-            uint32_t o[16];
-            tmem_ld16(o_col + 16 * g, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
-            tmem_st16(o_col + 16 * g, o);
-          }
+          for (int g = 0; g < 4; ++g) tmem_st16(s_col + 16 * g, zero);
+          tmem_wait_st();
         }
-        sum *= alpha;
-        ref = next;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(p_full);
+        continue;
       }
-      const float sub = ref == -INFINITY ? 0.f : ref;
-      float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        uint32_t p[16];
-#pragma unroll
-        for (int c = 0; c < 32; c += 4) {
-          float x0, x1, x2, x3;
-          fma2(x0, x1, __uint_as_float(s[g][c]), __uint_as_float(s[g][c + 1]), scale, -sub);
-          fma2(x2, x3, __uint_as_float(s[g][c + 2]), __uint_as_float(s[g][c + 3]), scale, -sub);
-          x0 = fast_exp2(x0), x1 = fast_exp2(x1), x2 = fast_exp2(x2), x3 = fast_exp2(x3);
-          add2(s0, s1, x0, x1);
-          add2(s2, s3, x2, x3);
-          p[c / 2] = pack_bf16x2(x0, x1);
-          p[c / 2 + 1] = pack_bf16x2(x2, x3);
-        }
-        tmem_st16(s_col + 16 * g, p);
-      }
-      sum += (s0 + s1) + (s2 + s3);
+      if (warp_sees >= (j + 1) * kPrefillTile)
+        softmax_tile<false>(s_col, o_col, scale, 0, j == 0, ref, sum);
+      else   // a mask crosses this tile
+        softmax_tile<true>(s_col, o_col, scale, sees - j * kPrefillTile, j == 0, ref, sum);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bars->p_full[t]));
+      if (lane == 0) mbar_arrive_remote(p_full);
     }
 
     // the item's results
-    if (it.nq <= 128 * t) continue;
+    if (it.nq <= 256 * t) continue;
     const bool live = row < it.nq;
     const bool none = sum == 0.f;                   // no key seen (a NaN sum is not 0)
     const float inv = none ? 0.f : 1.f / sum;
@@ -457,6 +546,7 @@ __device__ __forceinline__ void softmax_items(const PrefillArgs& a, const Ctx& c
       ++o_used;
       tc_fence_after();
     }
+    if (idle) continue;
     const int64_t at = (int64_t)(it.q0 + row) * a.num_heads + it.head;
     const int64_t part_at = it.prow + (int64_t)it.head * it.nq + row;
     float spoilt = 0.f;                             // NaN once an output of the row is not finite
@@ -514,30 +604,34 @@ __device__ __forceinline__ void softmax_items(const PrefillArgs& a, const Ctx& c
   }
 }
 
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
                    const __grid_constant__ CUtensorMap tm_pe, const __grid_constant__ PrefillArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* q_smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t* ring = q_smem + 2 * kQTile;
-  Bars* bars = reinterpret_cast<Bars*>(ring + kRing * kChunk);
+  Bars* bars = reinterpret_cast<Bars*>(ring + kStages * kStage);
   Item* slots = reinterpret_cast<Item*>(((uintptr_t)(bars + 1) + 15) & ~(uintptr_t)15);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kRing; ++i) {
-      mbar_init(smem_u32(&bars->full[i]), 1);
-      mbar_init(smem_u32(&bars->empty[i]), 1);
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(smem_u32(&bars->k_full[i]), 2);
+      mbar_init(smem_u32(&bars->v_full[i]), 2);
+      mbar_init(smem_u32(&bars->k_empty[i]), 1);
+      mbar_init(smem_u32(&bars->v_empty[i]), 1);
+      mbar_init(smem_u32(&bars->v_tail[i]), 1);
     }
     for (int i = 0; i < kItemSlots; ++i) {
       mbar_init(smem_u32(&bars->item_full[i]), 1);
       mbar_init(smem_u32(&bars->item_empty[i]), kItemReaders);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(smem_u32(&bars->q_full[t]), 1);
+      mbar_init(smem_u32(&bars->q_full[t]), 2);
       mbar_init(smem_u32(&bars->q_empty[t]), 1);
       mbar_init(smem_u32(&bars->s_full[t]), 1);
-      mbar_init(smem_u32(&bars->p_full[t]), 4);
+      mbar_init(smem_u32(&bars->p_full[t]), 8);
       mbar_init(smem_u32(&bars->o_full[t]), 1);
     }
     mbar_init(smem_u32(&bars->drain), 1);
@@ -545,8 +639,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
   if (warp == kWarpMma) {
-    tmem_alloc(smem_u32(&bars->tmem_base), 512);
-    tmem_relinquish();
+    tmem_alloc_pair(smem_u32(&bars->tmem_base), 512);
+    tmem_relinquish_pair();
   }
   if (warp == kWarpLoad && lane == 0) {
     tma_prefetch_desc(&tm_q);
@@ -554,13 +648,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tm_pe);
   }
   tc_fence_before();
-  __syncthreads();
+  cluster_sync();   // both CTAs' barriers are initialised before either uses the other's
   tc_fence_after();
   const uint32_t tbase = bars->tmem_base;
   // everything above overlaps the plan kernel
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const Ctx ctx{bars, &a.plan.header->status, a.wait_limit_ns};
+  const Ctx ctx{bars, rank, &a.plan.header->status, a.wait_limit_ns};
+
   if (warp < kSoftmaxWarps) {
     setmaxnreg_inc<kRegsSoftmax>();
     softmax_items(a, ctx, slots, tbase, warp, lane);
@@ -569,17 +664,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kWarpLoad) {
       load_items(ctx, slots, &tm_q, &tm_kv, &tm_pe, smem_u32(q_smem), smem_u32(ring), lane);
     } else if (warp == kWarpMma) {
-      issue_items(ctx, slots, tbase, q_smem, ring, lane);
+      if (rank == 0) issue_items(ctx, slots, tbase, smem_u32(q_smem), smem_u32(ring), lane);
+      wait_bar(ctx, &bars->drain, 0, kItemWait);   // every product of the pair is done
     } else if (warp == kWarpList) {
-      if (lane == 0) list_items(a, ctx, a.plan.header->num_pieces, slots);
+      if (lane == 0) {
+        if (rank == 0)
+          list_items(a, ctx, a.plan.header->num_pieces, slots);
+        else
+          await_items(ctx, slots);
+      }
       __syncwarp();
+    } else {
+      clear_tails(ctx, slots, ring, lane);
     }
   }
+  __syncwarp();
+  if (*(volatile int*)&bars->abort) {
+    // given up: loads and products in flight finish well within this time
+    const uint64_t t0 = globaltimer();
+    while (globaltimer() - t0 < 1000000ull) {
+    }
+  }
+  __syncwarp();
   tc_fence_before();
-  __syncthreads();
+  cluster_sync();   // the pair ends together: each reads and signals the other's shared memory
   if (warp == kWarpMma) {
     tc_fence_after();
-    tmem_dealloc(tbase, 512);
+    tmem_dealloc_pair(tbase, 512);
   }
 }
 
@@ -591,7 +702,7 @@ cudaError_t launch_prefill(const CUtensorMap& tm_q, const CUtensorMap& tm_kv, co
   cudaError_t e = cudaFuncSetAttribute(prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)a.ctas);
+  cfg.gridDim = dim3((unsigned)(2 * a.pairs));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = s;

@@ -10,24 +10,24 @@
 namespace mla {
 
 constexpr int kNope = 128;           // key width without the rotated part, and value width
-constexpr int kPrefillRows = 256;    // query rows per block: two 128-row tiles (tcgen05 M)
+constexpr int kPrefillRows = 512;    // query rows per block: two 256-row tiles (tcgen05 M of a CTA pair)
 constexpr int kPrefillTile = 128;    // keys per tile
-constexpr int kPrefillMaxCtas = 160; // upper bound of the grid (one CTA per SM)
+constexpr int kPrefillMaxPairs = 80; // upper bound of the grid (one CTA per SM, in pairs)
 
-// block  = up to 256 consecutive query rows of one sequence (the same for every head)
+// block  = up to 512 consecutive query rows of one sequence (the same for every head)
 // piece  = a block's keys [kv0, kv0 + nkeys), cut at multiples of a tile
-// item   = a piece and a head: what a CTA processes
+// item   = a piece and a head: what a CTA pair processes
 struct PrefillHeader {
   int status;        // OR of mla_device_error bits
   int num_pieces;
   int num_split;     // blocks cut into more than one piece
-  int next;          // items handed out beyond every CTA's first
+  int next;          // items handed out beyond every pair's first
   int pad[4];
 };
 
 struct PrefillPiece {  // 32 bytes
   int q0;              // first query row
-  int nq;              // rows (<= 256)
+  int nq;              // rows (<= 512)
   int kv0;             // first key row
   int nkeys;           // keys
   int lim0;            // keys of the piece that row 0 sees (not clamped): row r sees lim0 + r (causal) or lim0
@@ -61,14 +61,14 @@ struct PrefillLayout {
 };
 
 // Byte offsets for a shape.  Automatic splitting makes at most two partial
-// pieces per CTA (prefill_plan_kernel); a forced count cuts every block.
+// pieces per pair (prefill_plan_kernel); a forced count cuts every block.
 inline PrefillLayout prefill_layout(int batch, int total_q, int num_heads, int max_splits) {
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
   PrefillLayout L{};
   const long long mb = (long long)total_q / kPrefillRows + batch;
-  const long long auto_rows = 2LL * kPrefillMaxCtas * (total_q < kPrefillRows ? total_q : kPrefillRows);
+  const long long auto_rows = 2LL * kPrefillMaxPairs * (total_q < kPrefillRows ? total_q : kPrefillRows);
   const long long forced_rows = max_splits > 1 ? (long long)total_q * max_splits * num_heads : 0;
-  const long long mp = mb * (max_splits > 1 ? max_splits : 1) + 2 * kPrefillMaxCtas;
+  const long long mp = mb * (max_splits > 1 ? max_splits : 1) + 2 * kPrefillMaxPairs;
   L.max_blocks = (int)mb;
   L.max_pieces = (int)mp;
   L.max_part_rows = auto_rows > forced_rows ? auto_rows : forced_rows;
@@ -108,7 +108,7 @@ struct PrefillArgs {
   int causal;
   int num_splits;        // 0: automatic
   int group_heads;       // heads whose items are interleaved (their keys and values stay in L2)
-  int ctas;              // grid of the attention kernel
+  int pairs;             // grid of the attention kernel, in CTA pairs
   float scale_log2;      // scale * log2(e), > 0
   void* out;             // bf16 [total_q, heads, 128]
   float* lse;            // [total_q, heads] or null
@@ -118,7 +118,7 @@ struct PrefillArgs {
 
 cudaError_t launch_prefill_plan(const PrefillArgs& a, cudaStream_t s);
 // tm_q: {192, heads, total_q} boxes 64 x 1 x 128; tm_kv: {256, heads, total_kv}
-// boxes 64 x 1 x 128; tm_pe: {64, total_kv} boxes 64 x 128; all 128-byte swizzled
+// boxes 64 x 1 x 64; tm_pe: {64, total_kv} boxes 64 x 64; all 128-byte swizzled
 cudaError_t launch_prefill(const CUtensorMap& tm_q, const CUtensorMap& tm_kv, const CUtensorMap& tm_pe,
                            const PrefillArgs& a, cudaStream_t s);
 cudaError_t launch_prefill_combine(const PrefillArgs& a, cudaStream_t s);

@@ -3,17 +3,17 @@
 // Plan: one block of threads turns the prefix sums on the device into a list
 // of pieces, longest first, so that nothing of a call depends on the host
 // knowing the lengths (a captured graph may be replayed over other ones).
-// Every sequence's query rows are cut into blocks of 256; a block's keys are
+// Every sequence's query rows are cut into blocks of 512; a block's keys are
 // those its last row sees.  The list is the same for every head.
 //
 // A block is cut over its keys only where one block would outlast the rest:
-// with T tiles of work over all heads and S CTAs, a chunk is ceil(T / S)
+// with T tiles of work over all heads and S CTA pairs, a chunk is ceil(T / S)
 // tiles, and a block of more than 1.5 chunks is cut into ceil(tiles / chunk)
 // near-equal pieces (so the cut blocks of all heads number less than S and
 // their pieces less than 2 S).  The pieces' results are float32 partials with
 // their log-sum-exp, joined by the combine kernel:
 //   lse = ln sum_p exp(lse_p),  out = sum_p exp(lse_p - lse) out_p
-// always in the order of the pieces, whichever CTA made them.
+// always in the order of the pieces, whichever CTAs made them.
 #include <cuda_bf16.h>
 
 #include "prefill.cuh"
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArg
   __syncthreads();
   const unsigned long long work = s_total * a.num_heads;
   longest = s_longest;
-  int chunk = max((int)((work + a.ctas - 1) / a.ctas), kMinChunk);
+  int chunk = max((int)((work + a.pairs - 1) / a.pairs), kMinChunk);
   const bool cut = a.num_splits == 0 && 2 * longest > 3 * chunk;
   auto pieces_of = [&](int tiles) {
     if (a.num_splits > 0) return max(1, min(a.num_splits, tiles));
@@ -247,7 +247,7 @@ cudaError_t launch_prefill_plan(const PrefillArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_prefill_combine(const PrefillArgs& a, cudaStream_t s) {
-  return launch_dependent(prefill_combine_kernel, 2 * a.ctas, 256, a, s);
+  return launch_dependent(prefill_combine_kernel, 4 * a.pairs, 256, a, s);
 }
 
 }  // namespace mla
