@@ -146,7 +146,8 @@ def _dense(t, name: str, dtypes, shape=None, dims=None):
     """Refuse a tensor the library would misread: the C ABI takes dense
     row-major tensors of fixed element types.  ``shape`` entries of None
     match any size; ``dims`` checks only the rank."""
-    import torch
+    if t.dtype is dtypes and shape == t.shape and t.is_contiguous():
+        return                               # the usual case: exact sizes
     if not isinstance(dtypes, tuple):
         dtypes = (dtypes,)
     if t.dtype not in dtypes:
@@ -160,11 +161,12 @@ def _dense(t, name: str, dtypes, shape=None, dims=None):
             raise ValueError(f"{name} must have shape {exp}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous (dense rows), got strides {t.stride()}")
-    del torch
 
 
 def _cache_checked(cache, name="cache"):
     import torch
+    if cache.dtype is torch.bfloat16 and cache.dim() == 3 and cache.shape[2] == DQK and cache.is_contiguous():
+        return cache.shape
     _dense(cache, name, (torch.bfloat16, torch.float8_e4m3fn, torch.uint8), dims=3)
     if cache.shape[2] != DQK:
         raise ValueError(f"cache rows must be {DQK} wide, got {cache.shape[2]}")
@@ -188,39 +190,72 @@ def _rows(t, name: str, shape, writable: bool = False):
     dimensions may have any stride the library takes; returns those strides
     (a dimension of size 1 counts as packed)."""
     import torch
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise ValueError(f"{name} must be bfloat16, got {str(t.dtype).replace('torch.', '')}")
-    if t.dim() != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
+    have, strides = t.shape, t.stride()
+    if len(have) != len(shape) or any(w is not None and n != w for n, w in zip(have, shape)):
         exp = "[" + ", ".join("*" if w is None else str(w) for w in shape) + "]"
-        raise ValueError(f"{name} must have shape {exp}, got {tuple(t.shape)}")
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
-        raise ValueError(f"{name}'s last dimension must be contiguous, got strides {t.stride()}")
-    out, packed = [], t.shape[-1]
-    for d in range(t.dim() - 2, -1, -1):
-        n, st = t.shape[d], t.stride(d)
+        raise ValueError(f"{name} must have shape {exp}, got {tuple(have)}")
+    if strides[-1] != 1 and have[-1] > 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous, got strides {strides}")
+    out, packed = [], have[-1]
+    for d in range(len(have) - 2, -1, -1):
+        n, st = have[d], strides[d]
         if n <= 1:
             st = (packed + 7) // 8 * 8
         elif st % 8 or (writable and st == 0):
-            raise ValueError(f"{name}'s strides must be multiples of 8 elements, got {t.stride()}")
+            raise ValueError(f"{name}'s strides must be multiples of 8 elements, got {strides}")
         out.append(st)
         packed = max(packed, st * n)
     return out[::-1]
 
 
-def _on_current_device(*tensors) -> None:
+def _row_stride(t, name: str, rows: int, width: int, bf16, writable: bool = False) -> int:
+    """_rows of a [rows, width] tensor, the usual case first."""
+    if t.dtype is bf16 and t.shape == (rows, width):
+        s0, s1 = t.stride()
+        if s1 == 1:
+            if rows == 1:
+                return width
+            if s0 > 0 and not s0 & 7:
+                return s0
+    return _rows(t, name, (rows, width), writable)[0]
+
+
+def _head_strides(t, name: str, rows: int, heads, width: int, bf16, writable: bool = False):
+    """_rows of a [rows, heads, width] tensor, the usual case first."""
+    if t.dtype is bf16:
+        n, h, w = t.shape if t.dim() == 3 else (-1, -1, -1)
+        s0, s1, s2 = t.stride() if n >= 0 else (0, 0, 0)
+        if n == rows and (heads is None or h == heads) and w == width and s2 == 1 and h > 1 and s1 > 0 and not s1 & 7:
+            if n == 1:
+                return h * s1, s1
+            if s0 > 0 and not s0 & 7:
+                return s0, s1
+    return _rows(t, name, (rows, heads, width), writable)
+
+
+def _on_current_device(*tensors) -> int:
     """Refuse tensors of another device than the current one: the call's
-    stream, tensor maps and launch belong to the current device."""
+    stream, tensor maps and launch belong to the current device.  Returns it."""
     import torch
     dev = None
     for t in tensors:
         if t is None:
             continue
-        if not t.is_cuda:
+        at = t.get_device()
+        if at < 0:
             raise ValueError(f"expected a CUDA tensor, got one on {t.device}")
         if dev is None:
             dev = torch.cuda.current_device()
-        if t.device.index != dev:
-            raise ValueError(f"every tensor must be on the current device cuda:{dev}, got one on {t.device}")
+        if at != dev:
+            raise ValueError(f"every tensor must be on the current device cuda:{dev}, got one on cuda:{at}")
+    return dev
+
+
+def _raw_stream(stream, dev: int) -> int:
+    import torch
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def rope_cache_write(kv_c, k_pe, positions, cos_sin, slot_mapping, cache, *, q_pe=None, q_pe_out=None,
@@ -237,34 +272,39 @@ def rope_cache_write(kv_c, k_pe, positions, cos_sin, slot_mapping, cache, *, q_p
     slot is padding).  A position outside the table sets DEVERR_BAD_POSITION in
     ``status`` [1] int32 and nothing is written for its token."""
     import torch
+    bf16 = torch.bfloat16
     nb, ps, _ = _cache_checked(cache)
-    _dense(slot_mapping, "slot_mapping", torch.int64, dims=1)
     T = slot_mapping.numel()
-    (kvs,) = _rows(kv_c, "kv_c", (T, LKV))
-    (pes,) = _rows(k_pe, "k_pe", (T, ROPE))
+    _dense(slot_mapping, "slot_mapping", torch.int64, (T,))
+    kvs = _row_stride(kv_c, "kv_c", T, LKV, bf16)
+    pes = _row_stride(k_pe, "k_pe", T, ROPE, bf16)
     _dense(positions, "positions", torch.int64, (T,))
-    _dense(cos_sin, "cos_sin", torch.float32, (None, ROPE))
+    _dense(cos_sin, "cos_sin", torch.float32, (cos_sin.shape[0], ROPE))
+    weight = latent = q = q_out = flag = None
+    ls = N = qt = qh = ot = oh = 0
     if norm_weight is not None:
-        _dense(norm_weight, "norm_weight", torch.bfloat16, (LKV,))
-    ls = 0
+        _dense(norm_weight, "norm_weight", bf16, (LKV,))
+        weight = norm_weight.data_ptr()
     if latent_out is not None:
-        (ls,) = _rows(latent_out, "latent_out", (T, DQK), writable=True)
+        ls = _row_stride(latent_out, "latent_out", T, DQK, bf16, True)
+        latent = latent_out.data_ptr()
     if (q_pe is None) != (q_pe_out is None):
         raise ValueError("q_pe and q_pe_out are given together or not at all")
-    N, qs, qo = 0, (0, 0), (0, 0)
     if q_pe is not None:
-        qs = _rows(q_pe, "q_pe", (T, None, ROPE))
+        qt, qh = _head_strides(q_pe, "q_pe", T, None, ROPE, bf16)
         N = q_pe.shape[1]
-        qo = _rows(q_pe_out, "q_pe_out", (T, N, ROPE), writable=True)
+        ot, oh = _head_strides(q_pe_out, "q_pe_out", T, N, ROPE, bf16, True)
+        q, q_out = q_pe.data_ptr(), q_pe_out.data_ptr()
     if status is not None:
         _dense(status, "status", torch.int32, (1,))
-    _on_current_device(kv_c, k_pe, positions, cos_sin, slot_mapping, cache, q_pe, q_pe_out, norm_weight, latent_out,
-                       status)
-    _check(load().mla_rope_cache_write(_ptr(kv_c), kvs, _ptr(k_pe), pes, _ptr(norm_weight), float(norm_eps),
-                                       _ptr(positions), _ptr(cos_sin), cos_sin.shape[0], int(bool(interleaved)),
-                                       _ptr(slot_mapping), T, _ptr(cache), nb, ps, _dtype_code(cache),
-                                       float(kv_scale), _ptr(latent_out), ls, _ptr(q_pe), qs[0], qs[1], N,
-                                       _ptr(q_pe_out), qo[0], qo[1], _ptr(status), _stream(stream)))
+        flag = status.data_ptr()
+    dev = _on_current_device(kv_c, k_pe, positions, cos_sin, slot_mapping, cache, q_pe, q_pe_out, norm_weight,
+                             latent_out, status)
+    _check(load().mla_rope_cache_write(kv_c.data_ptr(), kvs, k_pe.data_ptr(), pes, weight, norm_eps,
+                                       positions.data_ptr(), cos_sin.data_ptr(), cos_sin.shape[0], bool(interleaved),
+                                       slot_mapping.data_ptr(), T, cache.data_ptr(), nb, ps, _dtype_code(cache),
+                                       kv_scale, latent, ls, q, qt, qh, N, q_out, ot, oh, flag,
+                                       _raw_stream(stream, dev)))
 
 
 def decode_workspace_size(batch: int, total_q: int, num_heads: int, max_splits: int = 0) -> int:
@@ -459,13 +499,15 @@ def kv_up_proj(latent, w, kv, stream=None) -> None:
     latent-to-heads projection's weight: for prefill D = 256, 128 key rows then
     128 value rows a head), ``kv`` [T, N, D]."""
     import torch
-    (ls,) = _rows(latent, "latent", (None, LKV))
+    bf16 = torch.bfloat16
+    ls = _row_stride(latent, "latent", latent.shape[0], LKV, bf16)
     T = latent.shape[0]
-    _dense(w, "w", torch.bfloat16, (None, None, LKV))
-    N, D = w.shape[0], w.shape[1]
-    _dense(kv, "kv", torch.bfloat16, (T, N, D))
-    _on_current_device(latent, w, kv)
-    _check(load().mla_kv_up_proj(_ptr(latent), ls, _ptr(w), T, N, D, _ptr(kv), _stream(stream)))
+    N, D = w.shape[:2] if w.dim() == 3 else (None, None)
+    _dense(w, "w", bf16, (N, D, LKV))
+    _dense(kv, "kv", bf16, (T, N, D))
+    dev = _on_current_device(latent, w, kv)
+    _check(load().mla_kv_up_proj(latent.data_ptr(), ls, w.data_ptr(), T, N, D, kv.data_ptr(),
+                                 _raw_stream(stream, dev)))
 
 
 def prefill_workspace_size(batch: int, total_q: int, num_heads: int, max_splits: int = 0) -> int:
@@ -483,24 +525,26 @@ def prefill(q, kv, k_pe, cu_q, cu_kv, out, workspace, *, scale: float, causal: b
     row of a sequence sees all its keys, the one before it one less, and so
     on; without, every row sees every key."""
     import torch
-    qs = _rows(q, "q", (None, None, 192))
-    T, N = q.shape[0], q.shape[1]
-    ks = _rows(kv, "kv", (None, N, 256))
-    Tk = kv.shape[0]
-    (ps,) = _rows(k_pe, "k_pe", (Tk, ROPE))
-    _dense(cu_q, "cu_q", torch.int32, dims=1)
+    bf16 = torch.bfloat16
+    T, Tk = q.shape[0], kv.shape[0]
+    qt, qh = _head_strides(q, "q", T, None, 192, bf16)
+    N = q.shape[1]
+    kt, kh = _head_strides(kv, "kv", Tk, N, 256, bf16)
+    ps = _row_stride(k_pe, "k_pe", Tk, ROPE, bf16)
     B = cu_q.numel() - 1
+    _dense(cu_q, "cu_q", torch.int32, (B + 1,))
     if B < 0:
         raise ValueError("cu_q must hold at least one entry")
     _dense(cu_kv, "cu_kv", torch.int32, (B + 1,))
-    _dense(out, "out", torch.bfloat16, (T, N, 128))
+    _dense(out, "out", bf16, (T, N, 128))
     if lse is not None:
         _dense(lse, "lse", torch.float32, (T, N))
-    _dense(workspace, "workspace", (workspace.dtype,))
-    _on_current_device(q, kv, k_pe, cu_q, cu_kv, out, workspace, lse)
-    _check(load().mla_prefill(_ptr(q), qs[0], qs[1], _ptr(kv), ks[0], ks[1], _ptr(k_pe), ps, _ptr(cu_q), _ptr(cu_kv),
-                              B, T, Tk, N, float(scale), int(bool(causal)), int(num_splits), _ptr(out), _ptr(lse),
-                              _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+    _dense(workspace, "workspace", workspace.dtype, workspace.shape)
+    dev = _on_current_device(q, kv, k_pe, cu_q, cu_kv, out, workspace, lse)
+    _check(load().mla_prefill(q.data_ptr(), qt, qh, kv.data_ptr(), kt, kh, k_pe.data_ptr(), ps, cu_q.data_ptr(),
+                              cu_kv.data_ptr(), B, T, Tk, N, scale, bool(causal), num_splits, out.data_ptr(),
+                              None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+                              _raw_stream(stream, dev)))
 
 
 def prefill_status(workspace, stream=None) -> int:

@@ -5,6 +5,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
@@ -195,6 +196,21 @@ struct RopeWriteArgs {
 struct KvProjShape {
   int bn, xrows;
 };
+
+// Let `kernel` use up to `bytes` of dynamic shared memory on the current
+// device; `done` remembers, by device, that it has been said (a process-wide
+// bit mask of the kernel's own).
+template <class K>
+inline cudaError_t allow_smem(K* kernel, size_t bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (bit && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 // ---- launchers (return cudaError_t of the launch)
 cudaError_t launch_rope_write(const RopeWriteArgs& w, int fp8, int pairs, cudaStream_t s);

@@ -186,9 +186,8 @@ cudaError_t launch_kv_proj(const CUtensorMap& tm_x, const CUtensorMap& tm_w, voi
   const uint32_t tcols = p.bn <= 64 ? 64 : p.bn <= 128 ? 128 : 256;
   const size_t floor_smem = kSmemPerSm / (512 / tcols + 1);
   if (smem < floor_smem) smem = floor_smem;
-  // set on every call: the attribute belongs to the current device
-  cudaError_t e = cudaFuncSetAttribute(kv_proj_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)(1024 + kRingBudget + kXBoxMax + sizeof(Bars) + 1024));
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(kv_proj_kernel, 1024 + kRingBudget + kXBoxMax + sizeof(Bars) + 1024, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((C + p.bn - 1) / p.bn), (unsigned)((T + kM - 1) / kM));

@@ -24,6 +24,7 @@
 // bf16 for the product (the sum is of the unrounded values).
 #include <cuda_bf16.h>
 
+#include "common.cuh"
 #include "prefill.cuh"
 #include "ptx.cuh"
 
@@ -698,8 +699,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 cudaError_t launch_prefill(const CUtensorMap& tm_q, const CUtensorMap& tm_kv, const CUtensorMap& tm_pe,
                            const PrefillArgs& a, cudaStream_t s) {
-  // set on every call: the attribute belongs to the current device
-  cudaError_t e = cudaFuncSetAttribute(prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(prefill_kernel, kSmem, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(2 * a.pairs));

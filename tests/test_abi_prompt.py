@@ -151,7 +151,10 @@ def test_binding_refuses_what_the_projection_would_misread():
 class _On:
     """Stands for a tensor of some device."""
     def __init__(self, index):
-        self.is_cuda, self.device = True, torch.device("cuda", index)
+        self.index = index
+
+    def get_device(self):
+        return self.index
 
 
 def test_binding_refuses_tensors_of_another_device(monkeypatch):
