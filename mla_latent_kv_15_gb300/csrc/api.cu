@@ -595,13 +595,15 @@ int mla_kv_up_proj(const void* latent, int64_t latent_stride, const void* w, int
   const int sms = sm_count();
   if (sms < 1) return fail(MLA_ERR_CUDA, "cannot query the current device");
   const mla::KvProjShape p = mla::kv_proj_shape(num_tokens, C, sms);
-  CUtensorMap tm_x, tm_w;
+  CUtensorMap tm_x, tm_w, tm_y;
   if (!mla::encode_tmap_2d(&tm_x, latent, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, mla::kLkv, (uint64_t)num_tokens,
                            (uint64_t)latent_stride * 2, 64, (uint32_t)p.xrows, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !mla::encode_tmap_2d(&tm_w, w, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, mla::kLkv, (uint64_t)C, mla::kLkv * 2, 64,
-                           (uint32_t)p.bn, CU_TENSOR_MAP_SWIZZLE_128B))
+                           (uint32_t)p.wrows, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !mla::encode_tmap_2d(&tm_y, kv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (uint64_t)C, (uint64_t)num_tokens,
+                           (uint64_t)C * 2, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B))
     return fail(MLA_ERR_CUDA, "cuTensorMapEncodeTiled rejected a tensor layout");
-  cudaError_t e = mla::launch_kv_proj(tm_x, tm_w, kv, num_tokens, C, p, (cudaStream_t)stream);
+  cudaError_t e = mla::launch_kv_proj(tm_x, tm_w, tm_y, kv, num_tokens, C, p, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "key/value projection launch");
   return ok();
 }

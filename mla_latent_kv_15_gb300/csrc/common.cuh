@@ -192,9 +192,11 @@ struct RopeWriteArgs {
   int* status;                // OR of mla_device_error bits, or null
 };
 
-// Tile of mla_kv_up_proj for a shape: columns and token-box rows of a CTA.
+// Tiles of mla_kv_up_proj for a shape: token and weight rows of a load box;
+// columns of a CTA's tile (bn) or of a CTA pair's (pair_bn, 0: single CTAs).
 struct KvProjShape {
-  int bn, xrows;
+  int bn, xrows, wrows;
+  int pair_bn, pairs;
 };
 
 // Let `kernel` use up to `bytes` of dynamic shared memory on the current
@@ -216,9 +218,9 @@ inline cudaError_t allow_smem(K* kernel, size_t bytes, std::atomic<uint64_t>& do
 cudaError_t launch_rope_write(const RopeWriteArgs& w, int fp8, int pairs, cudaStream_t s);
 KvProjShape kv_proj_shape(int64_t T, int64_t C, int sms);
 // y[t, c] = x[t, :] . w[c, :] (2-D tensor maps with 128-byte swizzle: x boxes
-// 64 x shape.xrows, w boxes 64 x shape.bn)
-cudaError_t launch_kv_proj(const CUtensorMap& tm_x, const CUtensorMap& tm_w, void* y, int64_t T, int64_t C,
-                           const KvProjShape& shape, cudaStream_t s);
+// 64 x shape.xrows, w boxes 64 x shape.wrows, y boxes 64 x 32)
+cudaError_t launch_kv_proj(const CUtensorMap& tm_x, const CUtensorMap& tm_w, const CUtensorMap& tm_y, void* y,
+                           int64_t T, int64_t C, const KvProjShape& shape, cudaStream_t s);
 // group_rows: query rows per group, a power of two (128; 32 for the small-rows decode variant)
 // write: the step's cache rows, quant: the step's query quantisation, both
 // done by extra blocks of the same launch (nullptr: none; quant needs an

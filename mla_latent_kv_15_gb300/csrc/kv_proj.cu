@@ -11,6 +11,12 @@
 // of a CTA is in flight at once.  With fewer than 128 tokens the token box
 // holds only round_up(T, 16) rows; the MMA rows past it read other bytes of
 // the CTA's shared memory and their results are never stored.
+//
+// Many tokens (kv_proj_pair_kernel): CTA pairs walk 256-token x kBN-column
+// tiles (cta_group::2: each CTA holds 128 tokens and half the columns of a
+// stage), two accumulators in tensor memory, so that the stores of a tile run
+// under the products of the next.  The epilogue leaves in 32-row x 64-column
+// pieces staged in shared memory and stored by TMA, which clips ragged edges.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -165,18 +171,252 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// ------------------------------------------------------------- many tokens
+
+constexpr int kPairThreads = 192;                // load warp, MMA warp, 4 epilogue warps
+constexpr uint32_t kPiece = 32 * 128;            // 32 rows x 64 bf16
+
+template <int kBN>
+struct PairShape {
+  static constexpr uint32_t kWBox = kBN / 2 * kK * 2;
+  static constexpr uint32_t kStage = kXBoxMax + kWBox;
+  static constexpr int kPieces = kBN / 64;       // of a tile and epilogue warp
+  static constexpr uint32_t kStaging = 4 * kPieces * kPiece;
+  static constexpr int kStages = (int)((232448 - 1024 - 512 - kStaging) / kStage);
+  static constexpr size_t kSmem = 1024 + kStages * kStage + kStaging + 512;
+};
+
+// Barriers marked (lead) are used in the leading CTA only, by both CTAs.
+struct PairBars {
+  uint64_t full[8];        // (lead) both CTAs' boxes have landed
+  uint64_t empty[8];
+  uint64_t acc_full[2];
+  uint64_t acc_empty[2];   // (lead) the epilogue warps of both CTAs
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+};
+static_assert(sizeof(PairBars) <= 512, "fits behind the staging");
+
+__device__ __forceinline__ void pair_wait(PairBars* bars, uint64_t* bar, uint32_t parity) {
+  const uint32_t at = smem_u32(bar);
+  if (mbar_try_wait(at, parity)) return;
+  const uint64_t t0 = globaltimer();
+  while (!mbar_try_wait_hint(at, parity, kWaitHintNs)) {
+    if (*(volatile int*)&bars->abort) return;
+    if (globaltimer() - t0 > MLA_WAIT_LIMIT_NS) {
+      *(volatile int*)&bars->abort = 1;
+      atomicOr(&g_kv_proj_error, 1u);  // MLA_DEVERR_TIMEOUT
+      return;
+    }
+  }
+}
+
+template <int kBN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    kv_proj_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
+                        const __grid_constant__ CUtensorMap tm_y, int T, int C, int tiles_m, int tiles_n) {
+  using P = PairShape<kBN>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* staging = smem + P::kStages * P::kStage;
+  PairBars* bars = reinterpret_cast<PairBars*>(staging + P::kStaging);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int first = (int)cluster_id_x(), step = gridDim.x / 2, tiles = tiles_m * tiles_n;
+  volatile int* abort_flag = &bars->abort;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < P::kStages; ++i) {
+      mbar_init(smem_u32(&bars->full[i]), 2);
+      mbar_init(smem_u32(&bars->empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&bars->acc_full[i]), 1);
+      mbar_init(smem_u32(&bars->acc_empty[i]), 8);
+    }
+    mbar_init(smem_u32(&bars->drain), 1);
+    bars->abort = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_x);
+    tma_prefetch_desc(&tm_w);
+    tma_prefetch_desc(&tm_y);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(&bars->tmem_base), 2 * kBN);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync();   // both CTAs' barriers are initialised before either uses the other's
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  // tile i: the token tiles of a column tile follow one another (its weights stay in L2, all tokens do)
+  if (warp == 0) {
+    uint32_t n = 0;
+    for (int i = first; i < tiles && !*abort_flag; i += step) {
+      const int t0 = (i % tiles_m) * 256 + 128 * (int)rank, c0 = (i / tiles_m) * kBN + kBN / 2 * (int)rank;
+      for (int c = 0; c < kChunks; ++c, ++n) {
+        const uint32_t slot = n % P::kStages;
+        pair_wait(bars, &bars->empty[slot], ((n / P::kStages) & 1) ^ 1);
+        if (*abort_flag) break;
+        if (elect_one()) {
+          const uint32_t st = smem_u32(smem + slot * P::kStage), full = mapa(smem_u32(&bars->full[slot]), 0);
+          mbar_expect_tx_remote(full, P::kStage);
+          tma_load_2d_pair(st, &tm_x, c * kK, t0, full);
+          tma_load_2d_pair(st + kXBoxMax, &tm_w, c * kK, c0, full);
+        }
+        __syncwarp();
+      }
+    }
+    // every load of the pair has landed before it ends
+    if (rank == 0)
+      for (uint32_t k = n > P::kStages ? n - P::kStages : 0; k < n; ++k)
+        pair_wait(bars, &bars->full[k % P::kStages], (k / P::kStages) & 1);
+  } else if (warp == 1) {
+    if (rank == 0) {
+      constexpr uint32_t idesc = idesc_bf16_f32(256, kBN, 0, 0);
+      constexpr uint32_t hi = desc_hi(1024, kSwizzle128B);
+      const uint32_t x_lo = desc_lo(smem_u32(smem), 16), w_lo = desc_lo(smem_u32(smem) + kXBoxMax, 16);
+      uint32_t n = 0, m = 0;
+      for (int i = first; i < tiles && !*abort_flag; i += step, ++m) {
+        const uint32_t acc = m & 1;
+        pair_wait(bars, &bars->acc_empty[acc], ((m >> 1) & 1) ^ 1);
+        tc_fence_after();
+        for (int c = 0; c < kChunks; ++c, ++n) {
+          const uint32_t slot = n % P::kStages;
+          pair_wait(bars, &bars->full[slot], (n / P::kStages) & 1);
+          if (elect_one()) {
+            const uint32_t off = slot * (P::kStage >> 4);
+#pragma unroll
+            for (int k = 0; k < kK / 16; ++k)
+              mma_pair_ss(tmem + acc * kBN, x_lo + off + 2 * k, hi, w_lo + off + 2 * k, hi, idesc, (c | k) ? 1u : 0u);
+            mma_commit_pair(smem_u32(&bars->empty[slot]));
+            if (c == kChunks - 1) mma_commit_pair(smem_u32(&bars->acc_full[acc]));
+          }
+          __syncwarp();
+        }
+      }
+      if (elect_one()) mma_commit_pair(smem_u32(&bars->drain));
+      __syncwarp();
+    }
+    pair_wait(bars, &bars->drain, 0);   // every product of the pair is done
+  } else {
+    const int q = warp & 3;
+    uint8_t* stage = staging + q * P::kPieces * kPiece;
+    uint32_t m = 0;
+    for (int i = first; i < tiles && !*abort_flag; i += step, ++m) {
+      const uint32_t acc = m & 1;
+      const int t0 = (i % tiles_m) * 256 + 128 * (int)rank + 32 * q, c0 = (i / tiles_m) * kBN;
+      pair_wait(bars, &bars->acc_full[acc], (m >> 1) & 1);
+      if (*abort_flag) break;
+      tc_fence_after();
+      const uint32_t from = tmem + acc * kBN + ((uint32_t)(32 * q) << 16);
+#pragma unroll
+      for (int p = 0; p < P::kPieces; ++p) {
+        uint32_t a[32], b[32];
+        tmem_ld32(from + 64 * p, a);
+        tmem_ld32(from + 64 * p + 32, b);
+        // this piece's store of the tile before has read it
+        if (lane == 0) bulk_wait_group_read<P::kPieces - 1>();
+        tmem_wait_ld();
+        __syncwarp();
+        const uint32_t row = smem_u32(stage + p * kPiece) + lane * 128;
+#pragma unroll
+        for (int v = 0; v < 8; ++v) {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int k = 8 * (v & 3) + 2 * e;
+            w[e] = v < 4 ? pack_bf16x2(__uint_as_float(a[k]), __uint_as_float(a[k + 1]))
+                         : pack_bf16x2(__uint_as_float(b[k]), __uint_as_float(b[k + 1]));
+          }
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + ((v ^ (lane & 7)) << 4)), "r"(w[0]),
+                       "r"(w[1]), "r"(w[2]), "r"(w[3])
+                       : "memory");
+        }
+        if (p == P::kPieces - 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote(mapa(smem_u32(&bars->acc_empty[acc]), 0));
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (t0 < T && c0 + 64 * p < C) tma_store_2d(&tm_y, c0 + 64 * p, t0, smem_u32(stage + p * kPiece));
+          bulk_commit_group();
+        }
+      }
+    }
+    if (lane == 0) bulk_wait_all();
+  }
+  __syncwarp();
+  if (*abort_flag) {
+    // given up: loads and products in flight finish well within this time
+    const uint64_t t0 = globaltimer();
+    while (globaltimer() - t0 < 1000000ull) {
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();   // the pair ends together: each reads and signals the other's shared memory
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 2 * kBN);
+  }
+}
+
+template <int kBN>
+cudaError_t launch_pair(const CUtensorMap& tm_x, const CUtensorMap& tm_w, const CUtensorMap& tm_y, int64_t T,
+                        int64_t C, int pairs, cudaStream_t s) {
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(kv_proj_pair_kernel<kBN>, PairShape<kBN>::kSmem, done);
+  if (e != cudaSuccess) return e;
+  const int64_t tm = (T + 255) / 256, tn = (C + kBN - 1) / kBN;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(2 * (tm * tn < pairs ? tm * tn : pairs)));
+  cfg.blockDim = dim3(kPairThreads);
+  cfg.dynamicSmemBytes = PairShape<kBN>::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kv_proj_pair_kernel<kBN>, tm_x, tm_w, tm_y, (int)T, (int)C, (int)tm, (int)tn);
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
+}
+
 }  // namespace
 
+// Up to 128 tokens a single CTA's tile holds them all and the weights' traffic
+// wants many CTAs (128 tokens x 32768 columns: 17.6 us, pairs 19.6).  Above,
+// pairs: 256 columns a tile where that costs no more rounds of all pairs than
+// 128, which run 15 % below the wider tile's rate (8192 tokens x 32768 columns:
+// 181 us against 216; 1021 x 5120: two rounds against three of half the size,
+// 17.5 us against 15.5).  Times include about 8 us of a graph's launch.
 KvProjShape kv_proj_shape(int64_t T, int64_t C, int sms) {
   KvProjShape p{};
-  p.bn = 128;
-  p.xrows = T >= kM ? kM : (int)((T + 15) / 16 * 16);
-  (void)C, (void)sms;
+  p.pairs = sms / 2;
+  if (T > kM && p.pairs > 0) {
+    auto rounds = [&](int bn) { return ((T + 255) / 256 * ((C + bn - 1) / bn) + p.pairs - 1) / p.pairs; };
+    p.pair_bn = 40 * rounds(256) <= 23 * rounds(128) ? 256 : 128;
+    p.wrows = p.pair_bn / 2;
+    p.xrows = kM;
+  } else {
+    p.bn = p.wrows = 128;
+    p.xrows = T >= kM ? kM : (int)((T + 15) / 16 * 16);
+  }
   return p;
 }
 
-cudaError_t launch_kv_proj(const CUtensorMap& tm_x, const CUtensorMap& tm_w, void* y, int64_t T, int64_t C,
-                           const KvProjShape& p, cudaStream_t s) {
+cudaError_t launch_kv_proj(const CUtensorMap& tm_x, const CUtensorMap& tm_w, const CUtensorMap& tm_y, void* y,
+                           int64_t T, int64_t C, const KvProjShape& p, cudaStream_t s) {
+  if (p.pair_bn == 256) return launch_pair<256>(tm_x, tm_w, tm_y, T, C, p.pairs, s);
+  if (p.pair_bn == 128) return launch_pair<128>(tm_x, tm_w, tm_y, T, C, p.pairs, s);
   const uint32_t xbox = (uint32_t)p.xrows * kK * 2, stage = xbox + (uint32_t)p.bn * kK * 2;
   int stages = (int)(kRingBudget / stage);
   if (stages > kChunks) stages = kChunks;
