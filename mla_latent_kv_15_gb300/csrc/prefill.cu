@@ -22,6 +22,10 @@
 // but only when a row's maximum has risen by more than 2^8 over the
 // reference, which leaves the result the same and is rare.  P is rounded to
 // bf16 for the product (the sum is of the unrounded values).
+//
+// An item of up to 256 rows ("narrow") has one query tile: the pair takes its
+// even key tiles as tile 0 and its odd ones as tile 1, so that the two still
+// work in turn, and the warps of tile 0 join the two results at the end.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -59,13 +63,14 @@ struct Bars {
   uint64_t q_empty[2];
   uint64_t s_full[2], o_full[2];
   uint64_t p_full[2];                             // (lead) all softmax warps of the pair
+  uint64_t x_full[4], x_done[4];                  // narrow items: rows of a quadrant of tile 1 handed over, and read
   uint64_t drain;
   uint64_t item_full[kItemSlots];
   uint64_t item_empty[kItemSlots];                // (lead)
   uint32_t tmem_base;
   int abort;
 };
-constexpr size_t kSmem = 1024 + 2 * kQTile + kStages * kStage + sizeof(Bars) + 16 + kItemSlots * 48;
+constexpr size_t kSmem = 1024 + 2 * kQTile + kStages * kStage + sizeof(Bars) + 16 + kItemSlots * 48 + 128 * 8;
 static_assert(kSmem <= 232448, "shared memory per CTA");
 
 struct Ctx {
@@ -103,40 +108,62 @@ struct __align__(16) Item {
 };
 static_assert(sizeof(Item) == 48, "three 16-byte words");
 
-// Item `i` of the list: pieces longest first, interleaved over a group of heads.
-__device__ __forceinline__ Item item_at(const PrefillArgs& a, int np, int i) {
-  const int per = np * a.group_heads;               // <= items, which are below 2^31
-  const int g = i / per, rem = i - g * per;
-  const int heads = min(a.group_heads, a.num_heads - g * a.group_heads);
-  const int p = rem / heads;
+// Whether the item has one query tile, whose key tiles alternate between the
+// two: key tile of step i of tile t.
+__device__ __forceinline__ bool narrow_item(const Item& it) { return it.nq <= kPrefillRows / 2; }
+__device__ __forceinline__ int key_tile(bool narrow, int t, int i) { return narrow ? 2 * i + t : i; }
+// Key tiles in all.
+__device__ __forceinline__ int tiles_of(const Item& it) {
+  return narrow_item(it) ? it.tiles[0] + it.tiles[1] : max(it.tiles[0], it.tiles[1]);
+}
+
+// Item `i` of the list: pieces longest first, interleaved over a group of
+// heads; in a fixed plan a piece is an item.
+__device__ __forceinline__ Item item_at(const PrefillArgs& a, int np, bool fixed, int i) {
+  int p = i, head = 0;
+  if (!fixed) {
+    const int per = np * a.group_heads;               // <= items, which are below 2^31
+    const int g = i / per, rem = i - g * per;
+    const int heads = min(a.group_heads, a.num_heads - g * a.group_heads);
+    p = rem / heads;
+    head = g * a.group_heads + rem - p * heads;
+  }
   const int4* rec = reinterpret_cast<const int4*>(a.plan.pieces + p);
   const int4 r0 = rec[0], r1 = rec[1];
   Item it;
   it.q0 = r0.x, it.nq = r0.y, it.kv0 = r0.z, it.nkeys = r0.w, it.lim0 = r1.x, it.prow = r1.y;
-  it.head = g * a.group_heads + rem - p * heads;
+  it.head = fixed ? r1.z : head;
+  if (it.prow >= 0) it.prow += head * it.nq;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int last = min(256 * (t + 1), it.nq) - 1;
     it.seen[t] = it.nq > 256 * t ? min(max(it.lim0 + (a.causal ? last : 0), 0), it.nkeys) : 0;
     it.tiles[t] = (it.seen[t] + kPrefillTile - 1) / kPrefillTile;
   }
+  if (narrow_item(it)) {
+    it.seen[1] = it.seen[0];
+    it.tiles[1] = it.tiles[0] / 2;
+    it.tiles[0] -= it.tiles[1];
+  }
   it.last = 0;
   return it;
 }
 
 // The leading CTA's list warp (one thread) hands the pair's items to both
-// CTAs: the first is the pair's own, the next come from a counter all pairs
-// share, so that a pair done early takes more.
-__device__ __forceinline__ void list_items(const PrefillArgs& a, const Ctx& ctx, int np, Item* slots) {
+// CTAs.  In a fixed plan they are the pair's range of pieces; else the first
+// is the pair's own and the next come from a counter all pairs share, so that
+// a pair done early takes more.
+__device__ __forceinline__ void list_items(const PrefillArgs& a, const Ctx& ctx, Item* slots) {
   Bars* bars = ctx.bars;
-  const int items = np * a.num_heads;
-  const int pairs = gridDim.x / 2;
-  int i = cluster_id_x();
+  const int np = a.plan.header->num_pieces, pairs = gridDim.x / 2, pair = cluster_id_x();
+  const bool fixed = a.plan.header->fixed != 0;
+  const int items = fixed ? a.plan.first_piece[pair + 1] : np * a.num_heads;
+  int i = fixed ? a.plan.first_piece[pair] : pair;
   for (uint32_t n = 0;; ++n) {
     const uint32_t slot = n % kItemSlots;
     Item it{};
     it.last = 1;
-    if (i < items) it = item_at(a, np, i);
+    if (i < items) it = item_at(a, np, fixed, i);
     wait_bar(ctx, &bars->item_empty[slot], ((n / kItemSlots) & 1) ^ 1, kItemWait);
     if (*(volatile int*)&bars->abort) it.last = 1;    // the peer is told
     slots[slot] = it;
@@ -147,7 +174,7 @@ __device__ __forceinline__ void list_items(const PrefillArgs& a, const Ctx& ctx,
     for (int k = 0; k < 3; ++k)
       st_async_v4(far + 16 * k, w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3], far_bar);
     if (it.last) break;
-    i = pairs + atomicAdd(&a.plan.header->next, 1);
+    i = fixed ? i + 1 : pairs + atomicAdd(&a.plan.header->next, 1);
   }
 }
 
@@ -210,7 +237,7 @@ __device__ __forceinline__ void load_items(const Ctx& ctx, const Item* slots, co
   uint32_t n = 0, items = 0, q_used[2] = {0, 0};
   volatile int* abort_flag = &bars->abort;
   auto query = [&](const Item& it, int t) {
-    if (it.tiles[t] == 0) return;
+    if (it.tiles[t] == 0 || (t == 1 && narrow_item(it))) return;
     wait_bar(ctx, &bars->q_empty[t], (q_used[t] & 1) ^ 1);
     if (*abort_flag) return;
     if (elect_one()) {
@@ -227,8 +254,8 @@ __device__ __forceinline__ void load_items(const Ctx& ctx, const Item* slots, co
   while (true) {
     const Item it = next_item(ctx, slots, items, lane);
     if (it.last) break;
-    const int tiles = max(it.tiles[0], it.tiles[1]);
-    if (tiles > 0) query(it, 0);
+    const int tiles = tiles_of(it);
+    query(it, 0);
     for (int j = 0; j < tiles; ++j, ++n) {
       const uint32_t stage = n % kStages, parity = ((n / kStages) & 1) ^ 1;
       const uint32_t dst = ring + stage * kStage;
@@ -279,7 +306,7 @@ __device__ __forceinline__ void clear_tails(const Ctx& ctx, const Item* slots, u
   while (true) {
     const Item it = next_item(ctx, slots, items, lane);
     if (it.last) break;
-    const int tiles = max(it.tiles[0], it.tiles[1]);
+    const int tiles = tiles_of(it);
     n += tiles;
     if (tiles == 0 || !has_tail(it, tiles)) continue;
     const uint32_t stage = (n - 1) % kStages;
@@ -306,10 +333,10 @@ __device__ __forceinline__ void issue_items(const Ctx& ctx, const Item* slots, u
   uint32_t n = 0, items = 0;               // tiles before, items
   uint32_t q_used[2] = {0, 0}, p_used[2] = {0, 0};
 
-  // S_t = Q_t K of tile m
-  auto scores = [&](int t, uint32_t m, bool q_done) {
+  // S_t = Q K of the tile in stage m (Q tile tq)
+  auto scores = [&](int t, int tq, uint32_t m, bool q_done, bool k_done) {
     if (elect_one()) {
-      const uint32_t k0 = k_lo + (m % kStages) * (kStage >> 4), q0 = q_lo + ((t * kQTile) >> 4);
+      const uint32_t k0 = k_lo + (m % kStages) * (kStage >> 4), q0 = q_lo + ((tq * kQTile) >> 4);
 #pragma unroll
       for (int c = 0; c < 3; ++c)
 #pragma unroll
@@ -317,59 +344,61 @@ __device__ __forceinline__ void issue_items(const Ctx& ctx, const Item* slots, u
           mma_pair_ss(tbase + kColS + 128 * t, q0 + ((c * kQChunk) >> 4) + 2 * k, hi, k0 + ((c * kBox) >> 4) + 2 * k,
                       hi, id_s, (c | k) ? 1u : 0u);
       mma_commit_pair(smem_u32(&bars->s_full[t]));
-      if (q_done) mma_commit_pair(smem_u32(&bars->q_empty[t]));
+      if (k_done) mma_commit_pair(smem_u32(&bars->k_empty[m % kStages]));
+      if (q_done) mma_commit_pair(smem_u32(&bars->q_empty[tq]));
     }
-    __syncwarp();
-  };
-  auto release = [&](uint64_t* bar) {
-    if (elect_one()) mma_commit_pair(smem_u32(bar));
     __syncwarp();
   };
 
   while (true) {
     const Item it = next_item(ctx, slots, items, lane);
     if (it.last) break;
-    const int tiles = max(it.tiles[0], it.tiles[1]);
-    if (tiles == 0) continue;
-    // first scores of both tiles
-    wait_bar(ctx, &bars->k_full[n % kStages], (n / kStages) & 1);
+    const bool narrow = narrow_item(it);
+    const int tiles = tiles_of(it), steps = max(it.tiles[0], it.tiles[1]);
+    // step i of tile t: its key tile has landed, then its scores.  Tile 1 is
+    // a tile's last user in a wide item (it sees no fewer keys than tile 0).
+    auto step_scores = [&](int t, int i) {
+      const uint32_t m = n + key_tile(narrow, t, i);
+      wait_bar(ctx, &bars->k_full[m % kStages], (m / kStages) & 1);
+      tc_fence_after();
+      scores(t, narrow ? 0 : t, m, narrow ? (int)(m - n) + 1 == tiles : i + 1 == it.tiles[t], narrow || t == 1);
+    };
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       if (it.tiles[t] == 0) continue;
-      wait_bar(ctx, &bars->q_full[t], q_used[t] & 1);
-      tc_fence_after();
-      scores(t, n, it.tiles[t] == 1);
-      ++q_used[t];
+      if (t == 0 || !narrow) {
+        wait_bar(ctx, &bars->q_full[t], q_used[t] & 1);
+        ++q_used[t];
+      }
+      step_scores(t, 0);
     }
-    release(&bars->k_empty[n % kStages]);
-    for (int j = 0; j < tiles; ++j, ++n) {
-      const bool more = j + 1 < tiles;
-      wait_bar(ctx, &bars->v_full[n % kStages], (n / kStages) & 1);
-      if (!more && has_tail(it, tiles)) fence_cluster();   // rows that a thread of each CTA has cleared
-      if (more) wait_bar(ctx, &bars->k_full[(n + 1) % kStages], ((n + 1) / kStages) & 1);
+    for (int i = 0; i < steps; ++i) {
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        if (j < it.tiles[t]) {
-          const int steps = min(kPrefillTile / 16, (it.seen[t] - j * kPrefillTile + 15) / 16);
-          wait_bar(ctx, &bars->p_full[t], p_used[t] & 1);
-          ++p_used[t];
-          tc_fence_after();
-          if (elect_one()) {
-            const uint32_t v0 = v_lo + (n % kStages) * (kStage >> 4);
+        if (i >= it.tiles[t]) continue;
+        const int j = key_tile(narrow, t, i);
+        const uint32_t m = n + j, stage = m % kStages;
+        const int products = min(kPrefillTile / 16, (it.seen[t] - j * kPrefillTile + 15) / 16);
+        wait_bar(ctx, &bars->v_full[stage], (m / kStages) & 1);
+        if (j + 1 == tiles && has_tail(it, tiles)) fence_cluster();   // rows that a thread of each CTA has cleared
+        wait_bar(ctx, &bars->p_full[t], p_used[t] & 1);
+        ++p_used[t];
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t v0 = v_lo + stage * (kStage >> 4);
 #pragma unroll
-            for (int k = 0; k < kPrefillTile / 16; ++k)
-              if (k < steps)
-                mma_pair_ts(tbase + kColO + 128 * t, tbase + kColS + 128 * t + 8 * k, v0 + 128 * k, hi, id_o,
-                            (j | k) ? 1u : 0u);
-            if (j + 1 == it.tiles[t]) mma_commit_pair(smem_u32(&bars->o_full[t]));
-          }
-          __syncwarp();
+          for (int k = 0; k < kPrefillTile / 16; ++k)
+            if (k < products)
+              mma_pair_ts(tbase + kColO + 128 * t, tbase + kColS + 128 * t + 8 * k, v0 + 128 * k, hi, id_o,
+                          (i | k) ? 1u : 0u);
+          if (narrow || t == 1) mma_commit_pair(smem_u32(&bars->v_empty[stage]));
+          if (i + 1 == it.tiles[t]) mma_commit_pair(smem_u32(&bars->o_full[t]));
         }
-        if (t == 1) release(&bars->v_empty[n % kStages]);
-        if (j + 1 < it.tiles[t]) scores(t, n + 1, j + 2 == it.tiles[t]);
-        if (more && t == 1) release(&bars->k_empty[(n + 1) % kStages]);
+        __syncwarp();
+        if (i + 1 < it.tiles[t]) step_scores(t, i + 1);
       }
     }
+    n += tiles;
   }
   if (elect_one()) mma_commit_pair(smem_u32(&bars->drain));
   __syncwarp();
@@ -487,28 +516,30 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_col, uint32_t o_col, flo
 }
 
 // ------------------------------------------------------------------ softmax
-__device__ __forceinline__ void softmax_items(const PrefillArgs& a, const Ctx& ctx, const Item* slots, uint32_t tbase,
-                                              int warp, int lane) {
+__device__ __forceinline__ void softmax_items(const PrefillArgs& a, const Ctx& ctx, const Item* slots, float2* handover,
+                                              uint32_t tbase, int warp, int lane) {
   Bars* bars = ctx.bars;
   const int t = warp >> 2, quad = warp & 3;
   const uint32_t lanes = (uint32_t)(32 * quad) << 16;
   const uint32_t s_col = tbase + lanes + kColS + 128 * t, o_col = tbase + lanes + kColO + 128 * t;
-  const int row = 256 * t + 128 * (int)ctx.rank + 32 * quad + lane;
   const float scale = a.scale_log2;
   const uint32_t p_full = ctx.lead(&bars->p_full[t]);
-  uint32_t items = 0, s_used = 0, o_used = 0;
+  uint32_t items = 0, s_used = 0, o_used[2] = {0, 0}, handed = 0;
 
   while (true) {
     const Item it = next_item(ctx, slots, items, lane);
     if (it.last) break;
+    const bool narrow = narrow_item(it);
     const int tiles = it.tiles[t];
+    const int row = (narrow ? 0 : 256 * t) + 128 * (int)ctx.rank + 32 * quad + lane;
     const int sees = min(max(it.lim0 + (a.causal ? row : 0), 0), it.nkeys);
     const int warp_sees = min(max(it.lim0 + (a.causal ? row - lane : 0), 0), it.nkeys);   // its first row: the fewest
     const int warp_most = min(max(it.lim0 + (a.causal ? row - lane + 31 : 0), 0), it.nkeys);   // its last: the most
     const bool idle = row - lane >= it.nq;          // a warp without rows only keeps the others company
     float ref = -INFINITY, sum = 0.f;
 
-    for (int j = 0; j < tiles; ++j, ++s_used) {
+    for (int i = 0; i < tiles; ++i, ++s_used) {
+      const int j = key_tile(narrow, t, i);
       wait_bar(ctx, &bars->s_full[t], s_used & 1);
       tc_fence_after();
       if (idle || warp_most <= j * kPrefillTile) {
@@ -527,9 +558,9 @@ __device__ __forceinline__ void softmax_items(const PrefillArgs& a, const Ctx& c
         continue;
       }
       if (warp_sees >= (j + 1) * kPrefillTile)
-        softmax_tile<false>(s_col, o_col, scale, 0, j == 0, ref, sum);
+        softmax_tile<false>(s_col, o_col, scale, 0, i == 0, ref, sum);
       else   // a mask crosses this tile
-        softmax_tile<true>(s_col, o_col, scale, sees - j * kPrefillTile, j == 0, ref, sum);
+        softmax_tile<true>(s_col, o_col, scale, sees - j * kPrefillTile, i == 0, ref, sum);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -537,19 +568,47 @@ __device__ __forceinline__ void softmax_items(const PrefillArgs& a, const Ctx& c
     }
 
     // the item's results
-    if (it.nq <= 256 * t) continue;
+    const bool both = narrow && it.tiles[1] > 0;    // tile 1 holds a part of the same rows
+    if (t == 1 && narrow) {
+      if (!both) continue;
+      ++o_used[1];
+      if (idle) continue;
+      // the warp of tile 0 with the same rows joins them
+      handover[32 * quad + lane] = make_float2(ref, sum);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars->x_full[quad]));
+      wait_bar(ctx, &bars->x_done[quad], handed & 1);
+      ++handed;
+      continue;
+    }
+    for (int u = 0; u < 2; ++u) {
+      if (it.tiles[u] == 0) continue;
+      if (u == t || both) wait_bar(ctx, &bars->o_full[u], o_used[u] & 1);
+      ++o_used[u];
+    }
+    tc_fence_after();
+    if (idle) continue;
+    float w0 = 1.f, w1 = 0.f;                       // weights of this tile's and of tile 1's part
+    bool some0 = true, some1 = false;               // whether the row sees a key of each (a NaN sum is not 0)
+    if (both) {
+      wait_bar(ctx, &bars->x_full[quad], handed & 1);
+      ++handed;
+      const float2 other = handover[32 * quad + lane];
+      const float top = fmaxf(ref, other.x), sub = top == -INFINITY ? 0.f : top;
+      w0 = fast_exp2(ref - sub);
+      w1 = fast_exp2(other.x - sub);
+      some0 = sum != 0.f;
+      some1 = other.y != 0.f;
+      sum = (some0 ? sum * w0 : 0.f) + (some1 ? other.y * w1 : 0.f);
+      ref = top;
+    }
     const bool live = row < it.nq;
-    const bool none = sum == 0.f;                   // no key seen (a NaN sum is not 0)
+    const bool none = sum == 0.f;                   // no key seen
     const float inv = none ? 0.f : 1.f / sum;
     const float lse = none ? -INFINITY : (ref + log2f(sum)) * 0.69314718055994531f;
-    if (tiles > 0) {
-      wait_bar(ctx, &bars->o_full[t], o_used & 1);
-      ++o_used;
-      tc_fence_after();
-    }
-    if (idle) continue;
+    w0 *= inv, w1 *= inv;
     const int64_t at = (int64_t)(it.q0 + row) * a.num_heads + it.head;
-    const int64_t part_at = it.prow + (int64_t)it.head * it.nq + row;
+    const int64_t part_at = (int64_t)it.prow + row;
     float spoilt = 0.f;                             // NaN once an output of the row is not finite
     if (live) {
       if (it.prow >= 0)
@@ -564,17 +623,25 @@ __device__ __forceinline__ void softmax_items(const PrefillArgs& a, const Ctx& c
         tmem_ld32(o_col + 32 * g, o);
         tmem_wait_ld();
       }
-      if (none)
 #pragma unroll
-        for (int c = 0; c < 32; ++c) o[c] = 0;
+      for (int c = 0; c < 32; ++c) o[c] = none || !some0 ? 0u : __float_as_uint(__uint_as_float(o[c]) * w0);
+      if (both) {
+        __syncwarp();
+        uint32_t e[32];
+        tmem_ld32(o_col + 128 + 32 * g, e);
+        tmem_wait_ld();
+        if (some1)
+#pragma unroll
+          for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(fmaf(__uint_as_float(e[c]), w1, __uint_as_float(o[c])));
+      }
 #pragma unroll
       for (int c = 0; c < 32; ++c) spoilt = fmaf(__uint_as_float(o[c]), 0.f, spoilt);
       if (live && it.prow >= 0) {
         float4* dst = reinterpret_cast<float4*>(a.plan.part_o + part_at * kNope + 32 * g);
 #pragma unroll
         for (int c = 0; c < 8; ++c)
-          dst[c] = make_float4(__uint_as_float(o[4 * c]) * inv, __uint_as_float(o[4 * c + 1]) * inv,
-                               __uint_as_float(o[4 * c + 2]) * inv, __uint_as_float(o[4 * c + 3]) * inv);
+          dst[c] = make_float4(__uint_as_float(o[4 * c]), __uint_as_float(o[4 * c + 1]),
+                               __uint_as_float(o[4 * c + 2]), __uint_as_float(o[4 * c + 3]));
       } else if (live) {
         uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at * kNope + 32 * g);
 #pragma unroll
@@ -582,11 +649,15 @@ __device__ __forceinline__ void softmax_items(const PrefillArgs& a, const Ctx& c
           uint32_t w[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            w[e] = pack_bf16x2(__uint_as_float(o[8 * c + 2 * e]) * inv, __uint_as_float(o[8 * c + 2 * e + 1]) * inv);
+            w[e] = pack_bf16x2(__uint_as_float(o[8 * c + 2 * e]), __uint_as_float(o[8 * c + 2 * e + 1]));
           dst[c] = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
       __syncwarp();
+    }
+    if (both) {
+      tc_fence_before();
+      if (lane == 0) mbar_arrive(smem_u32(&bars->x_done[quad]));
     }
     if (a.causal) {
       // keys in the products of this tile that the row does not see
@@ -613,6 +684,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint8_t* ring = q_smem + 2 * kQTile;
   Bars* bars = reinterpret_cast<Bars*>(ring + kStages * kStage);
   Item* slots = reinterpret_cast<Item*>(((uintptr_t)(bars + 1) + 15) & ~(uintptr_t)15);
+  float2* handover = reinterpret_cast<float2*>(slots + kItemSlots);   // (reference, sum) of a row of tile 1
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
 
@@ -634,6 +706,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&bars->s_full[t]), 1);
       mbar_init(smem_u32(&bars->p_full[t]), 8);
       mbar_init(smem_u32(&bars->o_full[t]), 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(smem_u32(&bars->x_full[i]), 1);
+      mbar_init(smem_u32(&bars->x_done[i]), 1);
     }
     mbar_init(smem_u32(&bars->drain), 1);
     bars->abort = 0;
@@ -659,7 +735,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (warp < kSoftmaxWarps) {
     setmaxnreg_inc<kRegsSoftmax>();
-    softmax_items(a, ctx, slots, tbase, warp, lane);
+    softmax_items(a, ctx, slots, handover, tbase, warp, lane);
   } else {
     setmaxnreg_dec<kRegsOther>();
     if (warp == kWarpLoad) {
@@ -670,7 +746,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else if (warp == kWarpList) {
       if (lane == 0) {
         if (rank == 0)
-          list_items(a, ctx, a.plan.header->num_pieces, slots);
+          list_items(a, ctx, slots);
         else
           await_items(ctx, slots);
       }

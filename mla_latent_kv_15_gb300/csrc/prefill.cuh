@@ -22,7 +22,8 @@ struct PrefillHeader {
   int num_pieces;
   int num_split;     // blocks cut into more than one piece
   int next;          // items handed out beyond every pair's first
-  int pad[4];
+  int fixed;         // 1: the pieces name their heads and the pairs have theirs from first_piece
+  int pad[3];
 };
 
 struct PrefillPiece {  // 32 bytes
@@ -31,21 +32,24 @@ struct PrefillPiece {  // 32 bytes
   int kv0;             // first key row
   int nkeys;           // keys
   int lim0;            // keys of the piece that row 0 sees (not clamped): row r sees lim0 + r (causal) or lim0
-  int prow;            // first partial row of head 0, or -1: the block's only piece
-  int pad[2];
+  int prow;            // first partial row (of head 0 where the piece is every head's), or -1: the only piece
+  int head;            // the piece's head (fixed plan)
+  int pad;
 };
 static_assert(sizeof(PrefillPiece) == 32, "one aligned 32-byte record");
 
 struct PrefillSplit {  // a block to be joined
   int q0, nq, pieces;
-  int prow;            // partial row of (piece p, head h, row r): prow + (p * heads + h) * nq + r
-  int before;          // rows * heads of the split blocks before it
-  int pad[3];
+  int head0, heads;    // the heads it is cut for
+  int prow;            // partial row of (piece p, head head0 + h, row r): prow + (p * heads + h) * nq + r
+  int before;          // rows * heads of the records before it
+  int pad;
 };
 
 struct PrefillPlan {
   PrefillHeader* header;
   int* first_block;      // [batch + 1] blocks before each sequence
+  int* first_piece;      // [pairs + 1] fixed plan: first piece of each pair
   PrefillPiece* pieces;
   PrefillSplit* splits;
   float* part_o;         // [max_part_rows][128]
@@ -55,10 +59,13 @@ struct PrefillPlan {
 };
 
 struct PrefillLayout {
-  size_t first_block, pieces, splits, part_o, part_lse, total;
+  size_t first_block, first_piece, pieces, splits, part_o, part_lse, total;
   int max_blocks, max_pieces;
   long long max_part_rows;
 };
+
+// A fixed plan is made for fewer items (blocks x heads) than this many a pair.
+constexpr int kPrefillFixedItems = 8;
 
 // Byte offsets for a shape.  Automatic splitting makes at most two partial
 // pieces per pair (prefill_plan_kernel); a forced count cuts every block.
@@ -68,14 +75,15 @@ inline PrefillLayout prefill_layout(int batch, int total_q, int num_heads, int m
   const long long mb = (long long)total_q / kPrefillRows + batch;
   const long long auto_rows = 2LL * kPrefillMaxPairs * (total_q < kPrefillRows ? total_q : kPrefillRows);
   const long long forced_rows = max_splits > 1 ? (long long)total_q * max_splits * num_heads : 0;
-  const long long mp = mb * (max_splits > 1 ? max_splits : 1) + 2 * kPrefillMaxPairs;
+  const long long mp = mb * (max_splits > 1 ? max_splits : 1) + (kPrefillFixedItems + 2) * kPrefillMaxPairs;
   L.max_blocks = (int)mb;
   L.max_pieces = (int)mp;
   L.max_part_rows = auto_rows > forced_rows ? auto_rows : forced_rows;
   size_t off = up(sizeof(PrefillHeader));
   L.first_block = off;  off = up(off + sizeof(int) * ((size_t)batch + 1));
+  L.first_piece = off;  off = up(off + sizeof(int) * (kPrefillMaxPairs + 1));
   L.pieces = off;       off = up(off + sizeof(PrefillPiece) * (size_t)mp);
-  L.splits = off;       off = up(off + sizeof(PrefillSplit) * (size_t)mb);
+  L.splits = off;       off = up(off + sizeof(PrefillSplit) * (size_t)(mb + kPrefillMaxPairs));
   L.part_o = off;       off = up(off + sizeof(float) * kNope * (size_t)L.max_part_rows);
   L.part_lse = off;     off = up(off + sizeof(float) * (size_t)L.max_part_rows);
   L.total = off;
@@ -86,6 +94,7 @@ inline PrefillPlan prefill_plan_from(void* ws, const PrefillLayout& L) {
   char* p = static_cast<char*>(ws);
   return PrefillPlan{reinterpret_cast<PrefillHeader*>(p),
                      reinterpret_cast<int*>(p + L.first_block),
+                     reinterpret_cast<int*>(p + L.first_piece),
                      reinterpret_cast<PrefillPiece*>(p + L.pieces),
                      reinterpret_cast<PrefillSplit*>(p + L.splits),
                      reinterpret_cast<float*>(p + L.part_o),

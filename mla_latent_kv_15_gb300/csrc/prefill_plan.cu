@@ -1,17 +1,26 @@
 // Work plan and join of the expanded attention.
 //
 // Plan: one block of threads turns the prefix sums on the device into a list
-// of pieces, longest first, so that nothing of a call depends on the host
-// knowing the lengths (a captured graph may be replayed over other ones).
-// Every sequence's query rows are cut into blocks of 512; a block's keys are
-// those its last row sees.  The list is the same for every head.
+// of pieces, so that nothing of a call depends on the host knowing the lengths
+// (a captured graph may be replayed over other ones).  Every sequence's query
+// rows are cut into blocks of 512; a block's keys are those its last row sees;
+// an item is a block and a head.  A tile of 128 keys costs two units, or one
+// for a block of up to 256 rows, which the pair takes two tiles at a time.
 //
-// A block is cut over its keys only where one block would outlast the rest:
-// with T tiles of work over all heads and S CTA pairs, a chunk is ceil(T / S)
-// tiles, and a block of more than 1.5 chunks is cut into ceil(tiles / chunk)
-// near-equal pieces (so the cut blocks of all heads number less than S and
-// their pieces less than 2 S).  The pieces' results are float32 partials with
-// their log-sum-exp, joined by the combine kernel:
+// Few items (under 8 a CTA pair): all items are laid end to end, each with a
+// fixed cost of kItemUnits in front (filling the pipeline, the epilogue: about
+// 4000 cycles against 1300 a unit), and cut into equal spans, one a pair, so
+// that every pair ends at the same time; an item on a border is cut there, in
+// at most two partial pieces a pair.
+// Many items: the list of pieces is the same for every head, longest first,
+// and the pairs take (piece, head) from it one after the other.  A block is cut
+// over its keys only where it would outlast the rest: with T units over all
+// heads and S pairs, a chunk is ceil(T / S), and a block of more than 1.5
+// chunks is cut into ceil(cost / chunk) near-equal pieces (so the cut blocks
+// of all heads number less than S and their pieces less than 2 S).
+//
+// The pieces' results are float32 partials with their log-sum-exp, joined by
+// the combine kernel:
 //   lse = ln sum_p exp(lse_p),  out = sum_p exp(lse_p - lse) out_p
 // always in the order of the pieces, whichever CTAs made them.
 #include <cuda_bf16.h>
@@ -23,7 +32,9 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kBuckets = 1024;       // piece lengths are sorted into this many classes
-constexpr int kMinChunk = 4;         // tiles
+constexpr int kMinChunk = 8;         // units
+constexpr int kItemUnits = 3;
+constexpr int kMaxFixed = kPrefillFixedItems * kPrefillMaxPairs;   // blocks of a fixed plan, at most
 
 __device__ __forceinline__ int block_sum_scan(int v, int* total, int* warp_sums) {
   // exclusive scan over the block; *total: the block's sum
@@ -49,6 +60,8 @@ __device__ __forceinline__ int block_sum_scan(int v, int* total, int* warp_sums)
 
 struct BlockOf {
   int q0, nq, kv0, nkeys, lim0, tiles;
+  int unit;    // cost of a tile
+  __device__ int cost() const { return tiles * unit; }
 };
 
 // Block i of the list: its sequence by binary search over the block counts.
@@ -67,12 +80,28 @@ __device__ __forceinline__ BlockOf block_of(const PrefillArgs& a, int i) {
   b.lim0 = a.causal ? sk - sq + 1 + r0 : sk;
   b.nkeys = a.causal ? min(max(b.lim0 + b.nq - 1, 0), sk) : sk;
   b.tiles = (b.nkeys + kPrefillTile - 1) / kPrefillTile;
+  b.unit = b.nq > kPrefillRows / 2 ? 2 : 1;
   return b;
+}
+
+// Key tiles [t0, t1) of a block.
+__device__ __forceinline__ PrefillPiece piece_of(const BlockOf& b, int t0, int t1, int prow, int head) {
+  PrefillPiece r{};
+  r.q0 = b.q0;
+  r.nq = b.nq;
+  r.kv0 = b.kv0 + t0 * kPrefillTile;
+  r.nkeys = max(min(t1 * kPrefillTile, b.nkeys) - t0 * kPrefillTile, 0);
+  r.lim0 = b.lim0 - t0 * kPrefillTile;
+  r.prow = prow;
+  r.head = head;
+  return r;
 }
 
 __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArgs a) {
   __shared__ int s_hist[kBuckets];
   __shared__ int s_warp[kThreads / 32];
+  __shared__ int s_before[kMaxFixed];              // units of the blocks before each, fixed plan
+  __shared__ int s_pair[kPrefillMaxPairs + 1];
   __shared__ unsigned long long s_total;
   __shared__ int s_longest, s_status, s_rows, s_split;
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -107,6 +136,7 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArg
       a.plan.header->status = s_status;
       a.plan.header->num_pieces = 0;
       a.plan.header->num_split = 0;
+      a.plan.header->fixed = 0;
     }
     return;
   }
@@ -114,7 +144,7 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArg
   unsigned long long mine = 0;
   int longest = 0;
   for (int i = tid; i < nblocks; i += kThreads) {
-    const int t = block_of(a, i).tiles;
+    const int t = block_of(a, i).cost();
     mine += t;
     longest = max(longest, t);
   }
@@ -123,54 +153,120 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArg
   __syncthreads();
   const unsigned long long work = s_total * a.num_heads;
   longest = s_longest;
-  int chunk = max((int)((work + a.pairs - 1) / a.pairs), kMinChunk);
-  const bool cut = a.num_splits == 0 && 2 * longest > 3 * chunk;
-  auto pieces_of = [&](int tiles) {
-    if (a.num_splits > 0) return max(1, min(a.num_splits, tiles));
-    return cut && 2 * tiles > 3 * chunk ? (tiles + chunk - 1) / chunk : 1;
-  };
-  // length class: 0 = longest
-  const int span = longest + 1;
-  auto bucket = [&](int tiles) { return (int)((long long)(longest - tiles) * kBuckets / span); };
 
-  for (int i = tid; i < nblocks; i += kThreads) {
-    const int tiles = block_of(a, i).tiles, P = pieces_of(tiles);
-    for (int p = 0; p < P; ++p) {
-      const int t0 = (int)((long long)tiles * p / P), t1 = (int)((long long)tiles * (p + 1) / P);
-      atomicAdd(&s_hist[bucket(t1 - t0)], 1);
+  if (a.num_splits == 0 && (long long)nblocks * a.num_heads < (long long)kPrefillFixedItems * a.pairs) {
+    // fixed plan: head h's block b lies at h * all + s_before[b]
+    const int items = nblocks * a.num_heads;
+    int all = 0;
+    for (int b0 = 0; b0 < nblocks; b0 += kThreads) {
+      const int b = b0 + tid;
+      int total;
+      const int before = block_sum_scan(b < nblocks ? block_of(a, b).cost() + kItemUnits : 0, &total, s_warp);
+      if (b < nblocks) s_before[b] = all + before;
+      all += total;
     }
-  }
-  __syncthreads();
-  carry = 0;
-  for (int b0 = 0; b0 < kBuckets; b0 += kThreads) {
+    for (int p = tid; p <= kPrefillMaxPairs; p += kThreads) s_pair[p] = 0;
+    __syncthreads();
+    const long long length = (long long)all * a.num_heads;
+    // pairs in use: no more pieces than leave each about kMinChunk units
+    const int used = (int)min((long long)a.pairs, max((long long)items, length / (kItemUnits + kMinChunk)));
+    auto border = [&](int p) { return length * p / used; };
+    int listed = 0;
+    for (int i0 = 0; i0 < items; i0 += kThreads) {
+      const int i = i0 + tid, h = i / nblocks;
+      const bool mine_is = i < items;
+      BlockOf b{};
+      long long s = 0;
+      int p0 = 0, n = 0;
+      if (mine_is) {
+        b = block_of(a, i - h * nblocks);
+        s = (long long)h * all + s_before[i - h * nblocks];
+        p0 = (int)(s * used / length);
+        while (p0 + 1 < used && border(p0 + 1) <= s) ++p0;
+        while (border(p0) > s) --p0;
+      }
+      const long long end = s + kItemUnits + b.cost();
+      // calls f(pair, t0, t1) for every piece of the item
+      auto cut = [&](auto f) {
+        int t0 = 0;
+        for (int p = p0;; ++p) {
+          const bool fin = p + 1 >= used || border(p + 1) >= end;
+          const int t1 = fin ? b.tiles : (int)min(max((border(p + 1) - s - kItemUnits) / b.unit, 0LL), (long long)b.tiles);
+          if (t1 > t0 || (fin && b.tiles == 0)) f(p, t0, t1);
+          t0 = t1;
+          if (fin) break;
+        }
+      };
+      if (mine_is) cut([&](int, int, int) { ++n; });
+      int total;
+      int at = listed + block_sum_scan(n, &total, s_warp);
+      listed += total;
+      if (mine_is) {
+        int prow = -1, k = 0;
+        if (n > 1) {
+          prow = atomicAdd(&s_rows, n * b.nq);
+          PrefillSplit sp{};
+          sp.q0 = b.q0, sp.nq = b.nq, sp.pieces = n, sp.head0 = h, sp.heads = 1, sp.prow = prow;
+          a.plan.splits[atomicAdd(&s_split, 1)] = sp;
+        }
+        cut([&](int p, int t0, int t1) {
+          a.plan.pieces[at + k] = piece_of(b, t0, t1, n > 1 ? prow + k * b.nq : -1, h);
+          atomicAdd(&s_pair[p], 1);
+          ++k;
+        });
+      }
+    }
+    __syncthreads();
     int total;
-    const int v = s_hist[b0 + tid];
-    const int before = block_sum_scan(v, &total, s_warp);
-    s_hist[b0 + tid] = carry + before;
-    carry += total;
-  }
-  __syncthreads();
-  for (int i = tid; i < nblocks; i += kThreads) {
-    const BlockOf b = block_of(a, i);
-    const int P = pieces_of(b.tiles);
-    int prow = -1;
-    if (P > 1) {
-      prow = atomicAdd(&s_rows, P * a.num_heads * b.nq);
-      PrefillSplit sp{};
-      sp.q0 = b.q0, sp.nq = b.nq, sp.pieces = P, sp.prow = prow;
-      a.plan.splits[atomicAdd(&s_split, 1)] = sp;
+    const int count = tid < kPrefillMaxPairs ? s_pair[tid] : 0;
+    const int before = block_sum_scan(count, &total, s_warp);
+    if (tid <= kPrefillMaxPairs) a.plan.first_piece[tid] = before;
+    carry = listed;
+  } else {
+    const int chunk = max((int)min((work + a.pairs - 1) / a.pairs, 1ull << 30), kMinChunk);
+    const bool cut = a.num_splits == 0 && 2 * longest > 3 * chunk;
+    auto pieces_of = [&](const BlockOf& b) {
+      if (a.num_splits > 0) return max(1, min(a.num_splits, b.tiles));
+      return cut && 2 * b.cost() > 3 * chunk ? min((b.cost() + chunk - 1) / chunk, b.tiles) : 1;
+    };
+    // length class: 0 = longest
+    const int span = longest + 1;
+    auto bucket = [&](int cost) { return (int)((long long)(longest - cost) * kBuckets / span); };
+
+    for (int i = tid; i < nblocks; i += kThreads) {
+      const BlockOf b = block_of(a, i);
+      const int P = pieces_of(b);
+      for (int p = 0; p < P; ++p) {
+        const int t0 = (int)((long long)b.tiles * p / P), t1 = (int)((long long)b.tiles * (p + 1) / P);
+        atomicAdd(&s_hist[bucket((t1 - t0) * b.unit)], 1);
+      }
     }
-    for (int p = 0; p < P; ++p) {
-      const int t0 = (int)((long long)b.tiles * p / P), t1 = (int)((long long)b.tiles * (p + 1) / P);
-      PrefillPiece r{};
-      r.q0 = b.q0;
-      r.nq = b.nq;
-      r.kv0 = b.kv0 + t0 * kPrefillTile;
-      r.nkeys = min(t1 * kPrefillTile, b.nkeys) - t0 * kPrefillTile;
-      r.lim0 = b.lim0 - t0 * kPrefillTile;
-      r.prow = prow < 0 ? -1 : prow + p * a.num_heads * b.nq;
-      const int at = atomicAdd(&s_hist[bucket(t1 - t0)], 1);
-      if (at < a.plan.max_pieces) a.plan.pieces[at] = r;
+    __syncthreads();
+    carry = 0;
+    for (int b0 = 0; b0 < kBuckets; b0 += kThreads) {
+      int total;
+      const int v = s_hist[b0 + tid];
+      const int before = block_sum_scan(v, &total, s_warp);
+      s_hist[b0 + tid] = carry + before;
+      carry += total;
+    }
+    __syncthreads();
+    for (int i = tid; i < nblocks; i += kThreads) {
+      const BlockOf b = block_of(a, i);
+      const int P = pieces_of(b);
+      int prow = -1;
+      if (P > 1) {
+        prow = atomicAdd(&s_rows, P * a.num_heads * b.nq);
+        PrefillSplit sp{};
+        sp.q0 = b.q0, sp.nq = b.nq, sp.pieces = P, sp.head0 = 0, sp.heads = a.num_heads, sp.prow = prow;
+        a.plan.splits[atomicAdd(&s_split, 1)] = sp;
+      }
+      for (int p = 0; p < P; ++p) {
+        const int t0 = (int)((long long)b.tiles * p / P), t1 = (int)((long long)b.tiles * (p + 1) / P);
+        const int at = atomicAdd(&s_hist[bucket((t1 - t0) * b.unit)], 1);
+        if (at < a.plan.max_pieces)
+          a.plan.pieces[at] = piece_of(b, t0, t1, prow < 0 ? -1 : prow + p * a.num_heads * b.nq, 0);
+      }
     }
   }
   __syncthreads();
@@ -178,11 +274,12 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArg
     int before = 0;
     for (int i = 0; i < s_split; ++i) {
       a.plan.splits[i].before = before;
-      before += a.plan.splits[i].nq * a.num_heads;
+      before += a.plan.splits[i].nq * a.plan.splits[i].heads;
     }
     a.plan.header->status = 0;
     a.plan.header->num_pieces = min(carry, a.plan.max_pieces);
     a.plan.header->num_split = s_split;
+    a.plan.header->fixed = a.num_splits == 0 && (long long)nblocks * a.num_heads < (long long)kPrefillFixedItems * a.pairs;
   }
 }
 
@@ -195,10 +292,10 @@ __global__ void __launch_bounds__(256) prefill_combine_kernel(const PrefillArgs 
   const int warps = gridDim.x * 8, w = blockIdx.x * 8 + (threadIdx.x >> 5);
   for (int i = 0; i < n; ++i) {
     const PrefillSplit sp = a.plan.splits[i];
-    const int rows = sp.nq * a.num_heads;
+    const int rows = sp.nq * sp.heads;
     for (int rr = (w + warps - sp.before % warps) % warps; rr < rows; rr += warps) {
       const int h = rr / sp.nq, r = rr - h * sp.nq;
-      const int64_t step = (int64_t)a.num_heads * sp.nq;
+      const int64_t step = (int64_t)sp.heads * sp.nq;
       const int64_t at0 = sp.prow + (int64_t)h * sp.nq + r;
       float m = -INFINITY;
       for (int p = 0; p < sp.pieces; ++p) m = fmaxf(m, a.plan.part_lse[at0 + p * step]);
@@ -214,7 +311,7 @@ __global__ void __launch_bounds__(256) prefill_combine_kernel(const PrefillArgs 
         o.x += e * v.x, o.y += e * v.y, o.z += e * v.z, o.w += e * v.w;
       }
       const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);   // NaN stays NaN
-      const int64_t row = (int64_t)(sp.q0 + r) * a.num_heads + h;
+      const int64_t row = (int64_t)(sp.q0 + r) * a.num_heads + sp.head0 + h;
       const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv),
                            hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
       *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + row * kNope + 4 * lane) =

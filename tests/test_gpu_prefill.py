@@ -187,6 +187,35 @@ def test_prefill_non_finite_keys_reach_only_the_rows_that_see_them(splits):
     assert ((c.lse.double() - lse).abs() <= 3.3e-4 + 2.0 ** -20 * lse.abs())[fine].all()
 
 
+@pytest.mark.parametrize("rows", [100, 200])
+def test_prefill_non_finite_keys_of_short_sequences(rows):
+    """The same for sequences of one query tile, whose key tiles alternate."""
+    c = Case([rows], [500], 2, seed=18)
+    clean = c.kv.clone()
+    c.kv[470, 0, 130] = float("inf")
+    c.kv[390 + 3, 1, 200] = float("nan")       # seen by every row when rows is 100
+    c.run()
+    torch.cuda.synchronize()
+    want = torch.zeros_like(c.out, dtype=torch.bool)
+    i = torch.arange(rows, device="cuda")
+    want[:, 0, 2] = i >= 470 - (500 - rows)
+    want[:, 1, 72] = i >= 393 - (500 - rows)
+    assert torch.equal(~torch.isfinite(c.out), want) and torch.isfinite(c.lse).all()
+    ref, lse, mag = prompt_ref.prefill_torch(c.q, clean, c.k_pe, c.at_q, c.at_kv, SCALE, True)
+    err = (c.out.double() - ref).abs()
+    assert (err <= 2.0 ** -8 * ref.abs() + (2.0 ** -8 + 6.6e-4 + 2.0 ** -18) * mag)[~want].all()
+
+
+@pytest.mark.parametrize("q_lens,kv_lens,heads", [([1] * 8, [8191, 4097, 1, 777, 6000, 129, 8000, 0], 16),
+                                                  ([512], [9000], 20), ([600, 1, 256, 257], [600, 9001, 3000, 2570], 8),
+                                                  ([1], [20000], 1), ([3000], [3000], 9), ([256] * 9, [256] * 9, 70)])
+def test_prefill_balanced_over_the_pairs(q_lens, kv_lens, heads):
+    """Few items: each is cut where the pairs' spans end, in pieces of any
+    number of tiles."""
+    Case(q_lens, kv_lens, heads, seed=19).run(True).check(True)
+    Case(q_lens, kv_lens, heads, seed=20).run(False).check(False)
+
+
 def test_prefill_is_deterministic():
     c = Case([300, 1, 40], [900, 4000, 2000], 16, seed=11).run()
     torch.cuda.synchronize()
