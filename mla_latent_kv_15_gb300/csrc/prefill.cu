@@ -83,13 +83,18 @@ struct Ctx {
 };
 
 // Bounded waits; once one has run out, every other one of the CTA returns, and
-// the peer's run out in turn.  Waits for an item may last as long as the item
-// before it (`times` the limit).
+// the peer's run out in turn.  kCluster: the acquire covers what the other CTA
+// has written to shared memory.  Waits for an item may last as long as the
+// item before it (`times` the limit).
+template <bool kCluster = false>
 __device__ __forceinline__ void wait_bar(const Ctx& c, uint64_t* bar, uint32_t parity, uint32_t times = 1) {
   const uint32_t at = smem_u32(bar);
-  if (mbar_try_wait(at, parity)) return;
+  auto done = [&] {
+    return kCluster ? mbar_try_wait_cluster_hint(at, parity, kWaitHintNs) : mbar_try_wait_hint(at, parity, kWaitHintNs);
+  };
+  if (kCluster ? mbar_try_wait_cluster(at, parity) : mbar_try_wait(at, parity)) return;
   const uint64_t t0 = globaltimer();
-  while (!mbar_try_wait_hint(at, parity, kWaitHintNs)) {
+  while (!done()) {
     if (*(volatile int*)&c.bars->abort) return;
     if (globaltimer() - t0 > c.limit_ns * times) {
       *(volatile int*)&c.bars->abort = 1;
@@ -184,8 +189,7 @@ __device__ __forceinline__ void await_items(const Ctx& ctx, const Item* slots) {
   for (uint32_t n = 0;; ++n) {
     const uint32_t slot = n % kItemSlots;
     mbar_expect_tx(smem_u32(&bars->item_full[slot]), sizeof(Item));
-    wait_bar(ctx, &bars->item_full[slot], (n / kItemSlots) & 1, kItemWait);
-    fence_cluster();
+    wait_bar<true>(ctx, &bars->item_full[slot], (n / kItemSlots) & 1, kItemWait);
     const bool last = *(volatile const int*)&slots[slot].last != 0;
     mbar_arrive_remote(ctx.lead(&bars->item_empty[slot]));
     if (last || *(volatile int*)&bars->abort) break;
@@ -195,8 +199,7 @@ __device__ __forceinline__ void await_items(const Ctx& ctx, const Item* slots) {
 // The next item, read by a whole warp; one without work behind the last or after an abort.
 __device__ __forceinline__ Item next_item(const Ctx& ctx, const Item* slots, uint32_t& n, int lane) {
   const uint32_t slot = n % kItemSlots;
-  wait_bar(ctx, &ctx.bars->item_full[slot], (n / kItemSlots) & 1, kItemWait);
-  fence_cluster();   // the peer's item was written by the leading CTA
+  wait_bar<true>(ctx, &ctx.bars->item_full[slot], (n / kItemSlots) & 1, kItemWait);
   Item it = slots[slot];
   if (*(volatile int*)&ctx.bars->abort) it.last = 1;
   __syncwarp();
@@ -218,6 +221,12 @@ __device__ __forceinline__ void add2(float& a0, float& a1, float b0, float b1) {
 __device__ __forceinline__ void fma2(float& r0, float& r1, float a0, float a1, float b, float c) {
   asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %4};\n mov.b64 z, {%5, %5};\n"
       " fma.rn.f32x2 x, x, y, z;\n mov.b64 {%0, %1}, x;\n}" : "=f"(r0), "=f"(r1) : "f"(a0), "f"(a1), "f"(b), "f"(c));
+}
+
+__device__ __forceinline__ void st_global_32b(void* p, const uint32_t* r) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 
 // Whether the last value tile of an item has rows past its keys inside the
@@ -524,6 +533,7 @@ __device__ __forceinline__ void softmax_items(const PrefillArgs& a, const Ctx& c
   const uint32_t s_col = tbase + lanes + kColS + 128 * t, o_col = tbase + lanes + kColO + 128 * t;
   const float scale = a.scale_log2;
   const uint32_t p_full = ctx.lead(&bars->p_full[t]);
+  const bool wide_out = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;   // 32-byte stores
   uint32_t items = 0, s_used = 0, o_used[2] = {0, 0}, handed = 0;
 
   while (true) {
@@ -637,20 +647,21 @@ __device__ __forceinline__ void softmax_items(const PrefillArgs& a, const Ctx& c
 #pragma unroll
       for (int c = 0; c < 32; ++c) spoilt = fmaf(__uint_as_float(o[c]), 0.f, spoilt);
       if (live && it.prow >= 0) {
-        float4* dst = reinterpret_cast<float4*>(a.plan.part_o + part_at * kNope + 32 * g);
+        float* dst = a.plan.part_o + part_at * kNope + 32 * g;
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-          dst[c] = make_float4(__uint_as_float(o[4 * c]), __uint_as_float(o[4 * c + 1]),
-                               __uint_as_float(o[4 * c + 2]), __uint_as_float(o[4 * c + 3]));
+        for (int c = 0; c < 4; ++c) st_global_32b(dst + 8 * c, &o[8 * c]);
       } else if (live) {
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at * kNope + 32 * g);
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + at * kNope + 32 * g;
+        uint32_t w[16];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t w[4];
+        for (int c = 0; c < 16; ++c) w[c] = pack_bf16x2(__uint_as_float(o[2 * c]), __uint_as_float(o[2 * c + 1]));
+        if (wide_out) {
+          st_global_32b(dst, w);
+          st_global_32b(dst + 16, w + 8);
+        } else {
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            w[e] = pack_bf16x2(__uint_as_float(o[8 * c + 2 * e]), __uint_as_float(o[8 * c + 2 * e + 1]));
-          dst[c] = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int c = 0; c < 4; ++c)
+            reinterpret_cast<uint4*>(dst)[c] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
         }
       }
       __syncwarp();

@@ -23,7 +23,8 @@ struct PrefillHeader {
   int num_split;     // blocks cut into more than one piece
   int next;          // items handed out beyond every pair's first
   int fixed;         // 1: the pieces name their heads and the pairs have theirs from first_piece
-  int pad[3];
+  int split_rows;    // rows x heads of the split blocks
+  int pad[2];
 };
 
 struct PrefillPiece {  // 32 bytes

@@ -64,15 +64,23 @@ struct BlockOf {
   __device__ int cost() const { return tiles * unit; }
 };
 
+// The prefix sums and the blocks before each sequence, in shared memory for
+// up to kSeqs sequences (every step of a search is then a few cycles), else
+// where the caller and the workspace have them.
+constexpr int kSeqs = 512;
+struct Sequences {
+  const int *cu_q, *cu_kv, *first;
+};
+
 // Block i of the list: its sequence by binary search over the block counts.
-__device__ __forceinline__ BlockOf block_of(const PrefillArgs& a, int i) {
+__device__ __forceinline__ BlockOf block_of(const PrefillArgs& a, const Sequences& sq_, int i) {
   int lo = 0, hi = a.batch - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (a.plan.first_block[mid] <= i) lo = mid; else hi = mid - 1;
+    if (sq_.first[mid] <= i) lo = mid; else hi = mid - 1;
   }
-  const int q0 = a.cu_q[lo], sq = a.cu_q[lo + 1] - q0, k0 = a.cu_kv[lo], sk = a.cu_kv[lo + 1] - k0;
-  const int r0 = (i - a.plan.first_block[lo]) * kPrefillRows;
+  const int q0 = sq_.cu_q[lo], sq = sq_.cu_q[lo + 1] - q0, k0 = sq_.cu_kv[lo], sk = sq_.cu_kv[lo + 1] - k0;
+  const int r0 = (i - sq_.first[lo]) * kPrefillRows;
   BlockOf b;
   b.q0 = q0 + r0;
   b.nq = min(kPrefillRows, sq - r0);
@@ -102,6 +110,7 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArg
   __shared__ int s_warp[kThreads / 32];
   __shared__ int s_before[kMaxFixed];              // units of the blocks before each, fixed plan
   __shared__ int s_pair[kPrefillMaxPairs + 1];
+  __shared__ int s_seq[3][kSeqs + 1];
   __shared__ unsigned long long s_total;
   __shared__ int s_longest, s_status, s_rows, s_split;
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -113,22 +122,34 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArg
   __syncthreads();
 
   // the sequences: checks, and the blocks before each
+  const bool local = a.batch <= kSeqs;
+  Sequences seqs{a.cu_q, a.cu_kv, a.plan.first_block};
+  int* first = a.plan.first_block;
+  if (local) {
+    for (int b = tid; b <= a.batch; b += kThreads) {
+      s_seq[0][b] = a.cu_q[b];
+      s_seq[1][b] = a.cu_kv[b];
+    }
+    seqs = Sequences{s_seq[0], s_seq[1], s_seq[2]};
+    first = s_seq[2];
+    __syncthreads();
+  }
   int carry = 0;
   for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
     const int b = b0 + tid;
     int n = 0;
     if (b < a.batch) {
-      const int q0 = a.cu_q[b], q1 = a.cu_q[b + 1], k0 = a.cu_kv[b], k1 = a.cu_kv[b + 1];
-      if (q0 < 0 || q1 < q0 || q1 > a.total_q) atomicOr(&s_status, 8);
+      const int q0 = seqs.cu_q[b], q1 = seqs.cu_q[b + 1], k0 = seqs.cu_kv[b], k1 = seqs.cu_kv[b + 1];
+      const bool bad = q0 < 0 || q1 < q0 || q1 > a.total_q;
+      if (bad) atomicOr(&s_status, 8);
       if (k0 < 0 || k1 < k0 || k1 > a.total_kv) atomicOr(&s_status, 2);
-      n = q0 < 0 || q1 < q0 || q1 > a.total_q ? 0 : (q1 - q0 + kPrefillRows - 1) / kPrefillRows;
+      n = bad ? 0 : (q1 - q0 + kPrefillRows - 1) / kPrefillRows;
     }
     int total;
     const int before = block_sum_scan(n, &total, s_warp);
-    if (b < a.batch) a.plan.first_block[b] = carry + before;
+    if (b < a.batch) first[b] = carry + before;
     carry += total;
   }
-  if (tid == 0) a.plan.first_block[a.batch] = carry;
   __syncthreads();
   const int nblocks = carry;
   if (s_status) {          // inconsistent prefix sums: flagged, nothing is computed
@@ -144,7 +165,7 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArg
   unsigned long long mine = 0;
   int longest = 0;
   for (int i = tid; i < nblocks; i += kThreads) {
-    const int t = block_of(a, i).cost();
+    const int t = block_of(a, seqs, i).cost();
     mine += t;
     longest = max(longest, t);
   }
@@ -161,7 +182,7 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArg
     for (int b0 = 0; b0 < nblocks; b0 += kThreads) {
       const int b = b0 + tid;
       int total;
-      const int before = block_sum_scan(b < nblocks ? block_of(a, b).cost() + kItemUnits : 0, &total, s_warp);
+      const int before = block_sum_scan(b < nblocks ? block_of(a, seqs, b).cost() + kItemUnits : 0, &total, s_warp);
       if (b < nblocks) s_before[b] = all + before;
       all += total;
     }
@@ -179,7 +200,7 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArg
       long long s = 0;
       int p0 = 0, n = 0;
       if (mine_is) {
-        b = block_of(a, i - h * nblocks);
+        b = block_of(a, seqs, i - h * nblocks);
         s = (long long)h * all + s_before[i - h * nblocks];
         p0 = (int)(s * used / length);
         while (p0 + 1 < used && border(p0 + 1) <= s) ++p0;
@@ -234,7 +255,7 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArg
     auto bucket = [&](int cost) { return (int)((long long)(longest - cost) * kBuckets / span); };
 
     for (int i = tid; i < nblocks; i += kThreads) {
-      const BlockOf b = block_of(a, i);
+      const BlockOf b = block_of(a, seqs, i);
       const int P = pieces_of(b);
       for (int p = 0; p < P; ++p) {
         const int t0 = (int)((long long)b.tiles * p / P), t1 = (int)((long long)b.tiles * (p + 1) / P);
@@ -252,7 +273,7 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArg
     }
     __syncthreads();
     for (int i = tid; i < nblocks; i += kThreads) {
-      const BlockOf b = block_of(a, i);
+      const BlockOf b = block_of(a, seqs, i);
       const int P = pieces_of(b);
       int prow = -1;
       if (P > 1) {
@@ -270,12 +291,17 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArg
     }
   }
   __syncthreads();
+  // rows of the split blocks before each
+  int rows = 0;
+  for (int i0 = 0; i0 < s_split; i0 += kThreads) {
+    const int i = i0 + tid;
+    int total;
+    const int before = block_sum_scan(i < s_split ? a.plan.splits[i].nq * a.plan.splits[i].heads : 0, &total, s_warp);
+    if (i < s_split) a.plan.splits[i].before = rows + before;
+    rows += total;
+  }
   if (tid == 0) {
-    int before = 0;
-    for (int i = 0; i < s_split; ++i) {
-      a.plan.splits[i].before = before;
-      before += a.plan.splits[i].nq * a.plan.splits[i].heads;
-    }
+    a.plan.header->split_rows = rows;
     a.plan.header->status = 0;
     a.plan.header->num_pieces = min(carry, a.plan.max_pieces);
     a.plan.header->num_split = s_split;
@@ -283,41 +309,56 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArg
   }
 }
 
-// One warp per (row, head) of the split blocks, four output dims a lane.
+// One warp per (row, head) of the split blocks, four output dims a lane; the
+// records' row counts are searched in shared memory where they fit.
+constexpr int kSearch = 1024;
+
 __global__ void __launch_bounds__(256) prefill_combine_kernel(const PrefillArgs a) {
+  __shared__ int s_before[kSearch];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int n = a.plan.header->num_split;
+  const int n = a.plan.header->num_split, total = a.plan.header->split_rows;
   if (n == 0) return;
+  for (int i = threadIdx.x; i < n && i < kSearch; i += blockDim.x) s_before[i] = a.plan.splits[i].before;
+  __syncthreads();
   const int lane = threadIdx.x & 31;
-  const int warps = gridDim.x * 8, w = blockIdx.x * 8 + (threadIdx.x >> 5);
-  for (int i = 0; i < n; ++i) {
-    const PrefillSplit sp = a.plan.splits[i];
-    const int rows = sp.nq * sp.heads;
-    for (int rr = (w + warps - sp.before % warps) % warps; rr < rows; rr += warps) {
-      const int h = rr / sp.nq, r = rr - h * sp.nq;
-      const int64_t step = (int64_t)sp.heads * sp.nq;
-      const int64_t at0 = sp.prow + (int64_t)h * sp.nq + r;
-      float m = -INFINITY;
-      for (int p = 0; p < sp.pieces; ++p) m = fmaxf(m, a.plan.part_lse[at0 + p * step]);
-      const float ref = m == -INFINITY ? 0.f : m;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      float sum = 0.f;
-      for (int p = 0; p < sp.pieces; ++p) {
-        const float l = a.plan.part_lse[at0 + p * step];
-        if (l == -INFINITY) continue;
-        const float e = expf(l - ref);
-        const float4 v = *reinterpret_cast<const float4*>(a.plan.part_o + (at0 + p * step) * kNope + 4 * lane);
-        sum += e;
-        o.x += e * v.x, o.y += e * v.y, o.z += e * v.z, o.w += e * v.w;
-      }
-      const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);   // NaN stays NaN
-      const int64_t row = (int64_t)(sp.q0 + r) * a.num_heads + sp.head0 + h;
-      const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv),
-                           hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + row * kNope + 4 * lane) =
-          make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-      if (lane == 0 && a.lse) a.lse[row] = sum == 0.f ? -INFINITY : ref + logf(sum);
+  const int warps = gridDim.x * 8;
+  for (int rr = blockIdx.x * 8 + (threadIdx.x >> 5); rr < total; rr += warps) {
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      const int before = mid < kSearch ? s_before[mid] : a.plan.splits[mid].before;
+      if (before <= rr) lo = mid; else hi = mid - 1;
     }
+    const PrefillSplit sp = a.plan.splits[lo];
+    const int own = rr - sp.before;
+    const int h = own / sp.nq, r = own - h * sp.nq;
+    const int64_t step = (int64_t)sp.heads * sp.nq;
+    const int64_t at0 = sp.prow + (int64_t)h * sp.nq + r;
+    float m = -INFINITY;
+    for (int p = lane; p < sp.pieces; p += 32) m = fmaxf(m, a.plan.part_lse[at0 + p * step]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float ref = m == -INFINITY ? 0.f : m;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+    for (int p0 = 0; p0 < sp.pieces; p0 += 32) {
+      const float l = p0 + lane < sp.pieces ? a.plan.part_lse[at0 + (p0 + lane) * step] : -INFINITY;
+      const float e = l == -INFINITY ? 0.f : expf(l - ref);
+      const int m32 = min(32, sp.pieces - p0);
+#pragma unroll 4
+      for (int p = 0; p < m32; ++p) {
+        const float w = __shfl_sync(0xffffffffu, e, p);
+        const float4 v = *reinterpret_cast<const float4*>(a.plan.part_o + (at0 + (p0 + p) * step) * kNope + 4 * lane);
+        sum += w;
+        if (w != 0.f) o.x += w * v.x, o.y += w * v.y, o.z += w * v.z, o.w += w * v.w;
+      }
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int64_t row = (int64_t)(sp.q0 + r) * a.num_heads + sp.head0 + h;
+    const __nv_bfloat162 x = __floats2bfloat162_rn(o.x * inv, o.y * inv), y = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + row * kNope + 4 * lane) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+    if (lane == 0 && a.lse) a.lse[row] = sum == 0.f ? -INFINITY : ref + logf(sum);
   }
 }
 
