@@ -89,12 +89,9 @@ struct Ctx {
 template <bool kCluster = false>
 __device__ __forceinline__ void wait_bar(const Ctx& c, uint64_t* bar, uint32_t parity, uint32_t times = 1) {
   const uint32_t at = smem_u32(bar);
-  auto done = [&] {
-    return kCluster ? mbar_try_wait_cluster_hint(at, parity, kWaitHintNs) : mbar_try_wait_hint(at, parity, kWaitHintNs);
-  };
   if (kCluster ? mbar_try_wait_cluster(at, parity) : mbar_try_wait(at, parity)) return;
   const uint64_t t0 = globaltimer();
-  while (!done()) {
+  while (!(kCluster ? mbar_try_wait_cluster_hint(at, parity, kWaitHintNs) : mbar_try_wait_hint(at, parity, kWaitHintNs))) {
     if (*(volatile int*)&c.bars->abort) return;
     if (globaltimer() - t0 > c.limit_ns * times) {
       *(volatile int*)&c.bars->abort = 1;
@@ -424,6 +421,7 @@ __device__ __noinline__ void mend_row(const PrefillArgs& a, int row, int head, i
   const int lane = threadIdx.x & 31;
   const __nv_bfloat16* kv = static_cast<const __nv_bfloat16*>(a.kv) + (int64_t)head * a.kv_head_stride;
   bool found = false;
+#pragma unroll 1
   for (int j = sees; j < covered; ++j) {
     const __nv_bfloat16* v = kv + (int64_t)(kv0 + j) * a.kv_token_stride + kNope + 4 * lane;
     for (int e = 0; e < 4; ++e) found |= !(fabsf(__bfloat162float(v[e])) < INFINITY);
@@ -433,17 +431,21 @@ __device__ __noinline__ void mend_row(const PrefillArgs& a, int row, int head, i
       static_cast<const __nv_bfloat16*>(a.q) + (int64_t)row * a.q_token_stride + (int64_t)head * a.q_head_stride;
   const __nv_bfloat16* pe = static_cast<const __nv_bfloat16*>(a.k_pe);
   float o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
   for (int j0 = 0; j0 < sees; j0 += 32) {
     float p = 0.f;
     if (j0 + lane < sees) {
       const __nv_bfloat16* k = kv + (int64_t)(kv0 + j0 + lane) * a.kv_token_stride;
       const __nv_bfloat16* r = pe + (int64_t)(kv0 + j0 + lane) * a.k_pe_stride;
       float s = 0.f;
+#pragma unroll 4
       for (int d = 0; d < kNope; ++d) s = fmaf(__bfloat162float(q[d]), __bfloat162float(k[d]), s);
+#pragma unroll 4
       for (int d = 0; d < 64; ++d) s = fmaf(__bfloat162float(q[kNope + d]), __bfloat162float(r[d]), s);
       p = fast_exp2(fmaf(s, a.scale_log2, -ref));
     }
     const int n = min(32, sees - j0);
+#pragma unroll 1
     for (int j = 0; j < n; ++j) {
       const float pj = __shfl_sync(0xffffffffu, p, j);
       const __nv_bfloat16* v = kv + (int64_t)(kv0 + j0 + j) * a.kv_token_stride + kNope + 4 * lane;
@@ -458,30 +460,33 @@ __device__ __noinline__ void mend_row(const PrefillArgs& a, int row, int head, i
   }
 }
 
-// One tile of a warp's rows: scores to probabilities, with the row's reference
-// and sum; `left` keys of the tile are seen where a mask crosses it.
-template <bool kMasked>
-__device__ __forceinline__ void softmax_tile(uint32_t s_col, uint32_t o_col, float scale, int left, bool first,
-                                             float& ref, float& sum) {
+// The pieces below that a tile or an item runs once are kept as small loops:
+// fetching straight-line code for them cost several thousand cycles each time
+// (the tile's own code is the only part that is hot).
+
+// Scores of keys that a row does not see, the tile's from `left` on, become -inf.
+__device__ __forceinline__ void mask_tile(uint32_t s_col, int left) {
+#pragma unroll 1
+  for (int g = 0; g < 4; ++g, left -= 32) {
+    uint32_t s[32];
+    tmem_ld32(s_col + 32 * g, s);
+    tmem_wait_ld();
+#pragma unroll
+    for (int c = 0; c < 32; ++c) s[c] = c < left ? s[c] : 0xff800000u;
+    tmem_st32(s_col + 32 * g, s);
+  }
+  tmem_wait_st();
+}
+
+// One tile of a warp's rows: scores to probabilities, with the row's reference and sum.
+__device__ __forceinline__ void softmax_tile(uint32_t s_col, uint32_t o_col, float scale, bool first, float& ref,
+                                             float& sum) {
   uint32_t s[4][32];
   float top[4];
 #pragma unroll
   for (int g = 0; g < 4; ++g) tmem_ld32_max(s_col + 32 * g, s[g], top[g]);
   tmem_wait_ld();
-  float m;
-  if (!kMasked) {
-    m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-  } else {
-    m = -INFINITY;
-#pragma unroll
-    for (int g = 0; g < 4; ++g)
-#pragma unroll
-      for (int c = 0; c < 32; ++c) {
-        const float v = 32 * g + c < left ? __uint_as_float(s[g][c]) : -INFINITY;
-        s[g][c] = __float_as_uint(v);
-        m = fmaxf(m, v);
-      }
-  }
+  float m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
   m *= scale;
   const bool raise = m > ref + kRescale;
   if (__any_sync(0xffffffffu, raise)) {
@@ -490,7 +495,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_col, uint32_t o_col, flo
     if (!first) {
       // the scores' arrival implies that the products before them are
       // done, and the next one waits for this warp
-#pragma unroll
+#pragma unroll 1
       for (int g = 0; g < 8; ++g) {
         uint32_t o[16];
         tmem_ld16(o_col + 16 * g, o);
@@ -558,7 +563,7 @@ __device__ __forceinline__ void softmax_items(const PrefillArgs& a, const Ctx& c
           uint32_t zero[16];
 #pragma unroll
           for (int c = 0; c < 16; ++c) zero[c] = 0;
-#pragma unroll
+#pragma unroll 1
           for (int g = 0; g < 4; ++g) tmem_st16(s_col + 16 * g, zero);
           tmem_wait_st();
         }
@@ -567,10 +572,8 @@ __device__ __forceinline__ void softmax_items(const PrefillArgs& a, const Ctx& c
         if (lane == 0) mbar_arrive_remote(p_full);
         continue;
       }
-      if (warp_sees >= (j + 1) * kPrefillTile)
-        softmax_tile<false>(s_col, o_col, scale, 0, i == 0, ref, sum);
-      else   // a mask crosses this tile
-        softmax_tile<true>(s_col, o_col, scale, sees - j * kPrefillTile, i == 0, ref, sum);
+      if (warp_sees < (j + 1) * kPrefillTile) mask_tile(s_col, sees - j * kPrefillTile);
+      softmax_tile(s_col, o_col, scale, i == 0, ref, sum);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -626,7 +629,7 @@ __device__ __forceinline__ void softmax_items(const PrefillArgs& a, const Ctx& c
       else if (a.lse)
         a.lse[at] = lse;
     }
-#pragma unroll
+#pragma unroll 1
     for (int g = 0; g < 4; ++g) {
       uint32_t o[32];
       if (tiles > 0) {
