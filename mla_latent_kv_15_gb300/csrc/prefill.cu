@@ -337,71 +337,66 @@ __device__ __forceinline__ void issue_items(const Ctx& ctx, const Item* slots, u
   constexpr uint32_t hi = desc_hi(1024, kSwizzle128B);
   const uint32_t q_lo = desc_lo(q_smem, 16), k_lo = desc_lo(ring, 16), v_lo = desc_lo(ring + kKeyBytes, kValueBytes);
   uint32_t n = 0, items = 0;               // tiles before, items
-  uint32_t q_used[2] = {0, 0}, p_used[2] = {0, 0};
-
-  // S_t = Q K of the tile in stage m (Q tile tq)
-  auto scores = [&](int t, int tq, uint32_t m, bool q_done, bool k_done) {
-    if (elect_one()) {
-      const uint32_t k0 = k_lo + (m % kStages) * (kStage >> 4), q0 = q_lo + ((tq * kQTile) >> 4);
-#pragma unroll
-      for (int c = 0; c < 3; ++c)
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mma_pair_ss(tbase + kColS + 128 * t, q0 + ((c * kQChunk) >> 4) + 2 * k, hi, k0 + ((c * kBox) >> 4) + 2 * k,
-                      hi, id_s, (c | k) ? 1u : 0u);
-      mma_commit_pair(smem_u32(&bars->s_full[t]));
-      if (k_done) mma_commit_pair(smem_u32(&bars->k_empty[m % kStages]));
-      if (q_done) mma_commit_pair(smem_u32(&bars->q_empty[tq]));
-    }
-    __syncwarp();
-  };
+  uint32_t q_parity = 0, p_parity = 0;     // bit t: of query tile t's next load, of tile t's next probabilities
 
   while (true) {
     const Item it = next_item(ctx, slots, items, lane);
     if (it.last) break;
     const bool narrow = narrow_item(it);
     const int tiles = tiles_of(it), steps = max(it.tiles[0], it.tiles[1]);
-    // step i of tile t: its key tile has landed, then its scores.  Tile 1 is
-    // a tile's last user in a wide item (it sees no fewer keys than tile 0).
-    auto step_scores = [&](int t, int i) {
-      const uint32_t m = n + key_tile(narrow, t, i);
-      wait_bar(ctx, &bars->k_full[m % kStages], (m / kStages) & 1);
-      tc_fence_after();
-      scores(t, narrow ? 0 : t, m, narrow ? (int)(m - n) + 1 == tiles : i + 1 == it.tiles[t], narrow || t == 1);
-    };
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      if (it.tiles[t] == 0) continue;
-      if (t == 0 || !narrow) {
-        wait_bar(ctx, &bars->q_full[t], q_used[t] & 1);
-        ++q_used[t];
-      }
-      step_scores(t, 0);
-    }
-    for (int i = 0; i < steps; ++i) {
-#pragma unroll
+    const bool tail = tiles > 0 && has_tail(it, tiles);
+    // Step i of the two tiles in turn: outputs of key tile i, scores of the
+    // next; step -1 has the first scores alone.  One copy of the code (see
+    // above): both tiles and all steps run through it.
+    for (int i = steps > 0 ? -1 : 0; i < steps; ++i) {
+#pragma unroll 1
       for (int t = 0; t < 2; ++t) {
-        if (i >= it.tiles[t]) continue;
-        const int j = key_tile(narrow, t, i);
+        const int count = t ? it.tiles[1] : it.tiles[0];
+        if (i >= count || count == 0) continue;
+        const int tq = narrow ? 0 : t;
+        const bool sole = narrow || t == 1;   // a key tile's last user: tile 1 sees no fewer keys than tile 0
+        const uint32_t s_col = tbase + kColS + 128 * t;
+        if (i >= 0) {
+          const int j = key_tile(narrow, t, i);
+          const uint32_t m = n + j, stage = m % kStages;
+          const int products = min(kPrefillTile / 16, ((t ? it.seen[1] : it.seen[0]) - j * kPrefillTile + 15) / 16);
+          wait_bar(ctx, &bars->v_full[stage], (m / kStages) & 1);
+          if (tail && j + 1 == tiles) fence_cluster();   // rows that a thread of each CTA has cleared
+          wait_bar(ctx, &bars->p_full[t], (p_parity >> t) & 1);
+          p_parity ^= 1u << t;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t v0 = v_lo + stage * (kStage >> 4);
+#pragma unroll
+            for (int k = 0; k < kPrefillTile / 16; ++k)
+              if (k < products)
+                mma_pair_ts(tbase + kColO + 128 * t, s_col + 8 * k, v0 + 128 * k, hi, id_o, (i | k) ? 1u : 0u);
+            if (sole) mma_commit_pair(smem_u32(&bars->v_empty[stage]));
+            if (i + 1 == count) mma_commit_pair(smem_u32(&bars->o_full[t]));
+          }
+          __syncwarp();
+          if (i + 1 == count) continue;
+        } else if (t == 0 || !narrow) {
+          wait_bar(ctx, &bars->q_full[t], (q_parity >> t) & 1);
+          q_parity ^= 1u << t;
+        }
+        const int j = key_tile(narrow, t, i + 1);
         const uint32_t m = n + j, stage = m % kStages;
-        const int products = min(kPrefillTile / 16, (it.seen[t] - j * kPrefillTile + 15) / 16);
-        wait_bar(ctx, &bars->v_full[stage], (m / kStages) & 1);
-        if (j + 1 == tiles && has_tail(it, tiles)) fence_cluster();   // rows that a thread of each CTA has cleared
-        wait_bar(ctx, &bars->p_full[t], p_used[t] & 1);
-        ++p_used[t];
+        wait_bar(ctx, &bars->k_full[stage], (m / kStages) & 1);
         tc_fence_after();
         if (elect_one()) {
-          const uint32_t v0 = v_lo + stage * (kStage >> 4);
+          const uint32_t k0 = k_lo + stage * (kStage >> 4), q0 = q_lo + tq * (kQTile >> 4);
 #pragma unroll
-          for (int k = 0; k < kPrefillTile / 16; ++k)
-            if (k < products)
-              mma_pair_ts(tbase + kColO + 128 * t, tbase + kColS + 128 * t + 8 * k, v0 + 128 * k, hi, id_o,
-                          (i | k) ? 1u : 0u);
-          if (narrow || t == 1) mma_commit_pair(smem_u32(&bars->v_empty[stage]));
-          if (i + 1 == it.tiles[t]) mma_commit_pair(smem_u32(&bars->o_full[t]));
+          for (int c = 0; c < 3; ++c)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_pair_ss(s_col, q0 + ((c * kQChunk) >> 4) + 2 * k, hi, k0 + ((c * kBox) >> 4) + 2 * k, hi, id_s,
+                          (c | k) ? 1u : 0u);
+          mma_commit_pair(smem_u32(&bars->s_full[t]));
+          if (sole) mma_commit_pair(smem_u32(&bars->k_empty[stage]));
+          if (narrow ? j + 1 == tiles : i + 2 == count) mma_commit_pair(smem_u32(&bars->q_empty[tq]));
         }
         __syncwarp();
-        if (i + 1 < it.tiles[t]) step_scores(t, i + 1);
       }
     }
     n += tiles;
