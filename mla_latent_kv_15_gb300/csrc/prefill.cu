@@ -121,14 +121,14 @@ __device__ __forceinline__ int tiles_of(const Item& it) {
 
 // Item `i` of the list: pieces longest first, interleaved over a group of
 // heads; in a fixed plan a piece is an item.
-__device__ __forceinline__ Item item_at(const PrefillArgs& a, int np, bool fixed, int i) {
+__device__ __forceinline__ Item item_at(const PrefillArgs& a, int np, int group, bool fixed, int i) {
   int p = i, head = 0;
   if (!fixed) {
-    const int per = np * a.group_heads;               // <= items, which are below 2^31
+    const int per = np * group;               // <= items, which are below 2^31
     const int g = i / per, rem = i - g * per;
-    const int heads = min(a.group_heads, a.num_heads - g * a.group_heads);
+    const int heads = min(group, a.num_heads - g * group);
     p = rem / heads;
-    head = g * a.group_heads + rem - p * heads;
+    head = g * group + rem - p * heads;
   }
   const int4* rec = reinterpret_cast<const int4*>(a.plan.pieces + p);
   const int4 r0 = rec[0], r1 = rec[1];
@@ -159,13 +159,14 @@ __device__ __forceinline__ void list_items(const PrefillArgs& a, const Ctx& ctx,
   Bars* bars = ctx.bars;
   const int np = a.plan.header->num_pieces, pairs = gridDim.x / 2, pair = cluster_id_x();
   const bool fixed = a.plan.header->fixed != 0;
+  const int group = a.plan.header->group_heads;
   const int items = fixed ? a.plan.first_piece[pair + 1] : np * a.num_heads;
   int i = fixed ? a.plan.first_piece[pair] : pair;
   for (uint32_t n = 0;; ++n) {
     const uint32_t slot = n % kItemSlots;
     Item it{};
     it.last = 1;
-    if (i < items) it = item_at(a, np, fixed, i);
+    if (i < items) it = item_at(a, np, group, fixed, i);
     wait_bar(ctx, &bars->item_empty[slot], ((n / kItemSlots) & 1) ^ 1, kItemWait);
     if (*(volatile int*)&bars->abort) it.last = 1;    // the peer is told
     slots[slot] = it;

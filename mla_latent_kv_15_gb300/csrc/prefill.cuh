@@ -24,7 +24,8 @@ struct PrefillHeader {
   int next;          // items handed out beyond every pair's first
   int fixed;         // 1: the pieces name their heads and the pairs have theirs from first_piece
   int split_rows;    // rows x heads of the split blocks
-  int pad[2];
+  int group_heads;   // heads whose items are interleaved
+  int pad;
 };
 
 struct PrefillPiece {  // 32 bytes
@@ -117,7 +118,7 @@ struct PrefillArgs {
   int batch, total_q, total_kv, num_heads;
   int causal;
   int num_splits;        // 0: automatic
-  int group_heads;       // heads whose items are interleaved (their keys and values stay in L2)
+  int group_heads;       // heads whose keys and values stay in L2 together
   int pairs;             // grid of the attention kernel, in CTA pairs
   float scale_log2;      // scale * log2(e), > 0
   void* out;             // bf16 [total_q, heads, 128]

@@ -23,6 +23,11 @@
 // the combine kernel:
 //   lse = ln sum_p exp(lse_p),  out = sum_p exp(lse_p - lse) out_p
 // always in the order of the pieces, whichever CTAs made them.
+//
+// Both kernels run every instruction about once, from cold instruction
+// caches, so their time is the code they fetch: loops stay loops, and what
+// occurs twice is a function (the plan unrolled and inlined was 56 KB of code
+// and took 8-10 us).
 #include <cuda_bf16.h>
 
 #include "prefill.cuh"
@@ -36,11 +41,11 @@ constexpr int kMinChunk = 8;         // units
 constexpr int kItemUnits = 3;
 constexpr int kMaxFixed = kPrefillFixedItems * kPrefillMaxPairs;   // blocks of a fixed plan, at most
 
-__device__ __forceinline__ int block_sum_scan(int v, int* total, int* warp_sums) {
+__device__ __noinline__ int block_sum_scan(int v, int* total, int* warp_sums) {
   // exclusive scan over the block; *total: the block's sum
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int incl = v;
-#pragma unroll
+#pragma unroll 1
   for (int o = 1; o < 32; o <<= 1) {
     const int n = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += n;
@@ -49,7 +54,7 @@ __device__ __forceinline__ int block_sum_scan(int v, int* total, int* warp_sums)
   if (lane == 31) warp_sums[warp] = incl;
   __syncthreads();
   int before = 0, sum = 0;
-#pragma unroll
+#pragma unroll 1
   for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) before += warp_sums[w];
     sum += warp_sums[w];
@@ -73,8 +78,9 @@ struct Sequences {
 };
 
 // Block i of the list: its sequence by binary search over the block counts.
-__device__ __forceinline__ BlockOf block_of(const PrefillArgs& a, const Sequences& sq_, int i) {
+__device__ __noinline__ BlockOf block_of(const PrefillArgs& a, const Sequences& sq_, int i) {
   int lo = 0, hi = a.batch - 1;
+#pragma unroll 1
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (sq_.first[mid] <= i) lo = mid; else hi = mid - 1;
@@ -92,8 +98,12 @@ __device__ __forceinline__ BlockOf block_of(const PrefillArgs& a, const Sequence
   return b;
 }
 
-// Key tiles [t0, t1) of a block.
-__device__ __forceinline__ PrefillPiece piece_of(const BlockOf& b, int t0, int t1, int prow, int head) {
+// a * b / c without overflow of the product
+__device__ __noinline__ long long mul_div(long long a, int b, long long c) { return a * b / c; }
+
+// Piece `at` of the list: key tiles [t0, t1) of a block.
+__device__ __noinline__ void put_piece(const PrefillArgs& a, int at, const BlockOf& b, int t0, int t1, int prow,
+                                       int head) {
   PrefillPiece r{};
   r.q0 = b.q0;
   r.nq = b.nq;
@@ -102,7 +112,17 @@ __device__ __forceinline__ PrefillPiece piece_of(const BlockOf& b, int t0, int t
   r.lim0 = b.lim0 - t0 * kPrefillTile;
   r.prow = prow;
   r.head = head;
-  return r;
+  if (at < a.plan.max_pieces) a.plan.pieces[at] = r;
+}
+
+// A cut block's record; returns its first partial row.
+__device__ __noinline__ int put_split(const PrefillArgs& a, const BlockOf& b, int pieces, int head0, int heads,
+                                      int* rows, int* splits) {
+  PrefillSplit sp{};
+  sp.q0 = b.q0, sp.nq = b.nq, sp.pieces = pieces, sp.head0 = head0, sp.heads = heads;
+  sp.prow = atomicAdd(rows, pieces * heads * b.nq);
+  a.plan.splits[atomicAdd(splits, 1)] = sp;
+  return sp.prow;
 }
 
 __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArgs a) {
@@ -118,6 +138,7 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArg
   const int tid = threadIdx.x;
   if (tid == 0) a.plan.header->next = 0;
   if (tid == 0) s_total = 0, s_longest = 0, s_status = 0, s_rows = 0, s_split = 0;
+#pragma unroll 1
   for (int i = tid; i < kBuckets; i += kThreads) s_hist[i] = 0;
   __syncthreads();
 
@@ -126,6 +147,7 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArg
   Sequences seqs{a.cu_q, a.cu_kv, a.plan.first_block};
   int* first = a.plan.first_block;
   if (local) {
+#pragma unroll 1
     for (int b = tid; b <= a.batch; b += kThreads) {
       s_seq[0][b] = a.cu_q[b];
       s_seq[1][b] = a.cu_kv[b];
@@ -135,6 +157,7 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArg
     __syncthreads();
   }
   int carry = 0;
+#pragma unroll 1
   for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
     const int b = b0 + tid;
     int n = 0;
@@ -158,12 +181,14 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArg
       a.plan.header->num_pieces = 0;
       a.plan.header->num_split = 0;
       a.plan.header->fixed = 0;
+      a.plan.header->group_heads = 1;
     }
     return;
   }
 
   unsigned long long mine = 0;
   int longest = 0;
+#pragma unroll 1
   for (int i = tid; i < nblocks; i += kThreads) {
     const int t = block_of(a, seqs, i).cost();
     mine += t;
@@ -175,10 +200,13 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArg
   const unsigned long long work = s_total * a.num_heads;
   longest = s_longest;
 
-  if (a.num_splits == 0 && (long long)nblocks * a.num_heads < (long long)kPrefillFixedItems * a.pairs) {
+  const bool fixed = a.num_splits == 0 && longest > kMinChunk &&
+                     (long long)nblocks * a.num_heads < (long long)kPrefillFixedItems * a.pairs;
+  if (fixed) {
     // fixed plan: head h's block b lies at h * all + s_before[b]
     const int items = nblocks * a.num_heads;
     int all = 0;
+#pragma unroll 1
     for (int b0 = 0; b0 < nblocks; b0 += kThreads) {
       const int b = b0 + tid;
       int total;
@@ -186,13 +214,15 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArg
       if (b < nblocks) s_before[b] = all + before;
       all += total;
     }
+#pragma unroll 1
     for (int p = tid; p <= kPrefillMaxPairs; p += kThreads) s_pair[p] = 0;
     __syncthreads();
     const long long length = (long long)all * a.num_heads;
     // pairs in use: no more pieces than leave each about kMinChunk units
     const int used = (int)min((long long)a.pairs, max((long long)items, length / (kItemUnits + kMinChunk)));
-    auto border = [&](int p) { return length * p / used; };
+    auto border = [&](int p) { return mul_div(length, p, used); };
     int listed = 0;
+#pragma unroll 1
     for (int i0 = 0; i0 < items; i0 += kThreads) {
       const int i = i0 + tid, h = i / nblocks;
       const bool mine_is = i < items;
@@ -202,39 +232,39 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArg
       if (mine_is) {
         b = block_of(a, seqs, i - h * nblocks);
         s = (long long)h * all + s_before[i - h * nblocks];
-        p0 = (int)(s * used / length);
+        p0 = (int)mul_div(s, used, length);
         while (p0 + 1 < used && border(p0 + 1) <= s) ++p0;
         while (border(p0) > s) --p0;
       }
       const long long end = s + kItemUnits + b.cost();
-      // calls f(pair, t0, t1) for every piece of the item
-      auto cut = [&](auto f) {
-        int t0 = 0;
-        for (int p = p0;; ++p) {
-          const bool fin = p + 1 >= used || border(p + 1) >= end;
-          const int t1 = fin ? b.tiles : (int)min(max((border(p + 1) - s - kItemUnits) / b.unit, 0LL), (long long)b.tiles);
-          if (t1 > t0 || (fin && b.tiles == 0)) f(p, t0, t1);
-          t0 = t1;
-          if (fin) break;
+      // two walks over the item's pieces: they are counted, then listed
+      int at = 0, prow = -1;
+#pragma unroll 1
+      for (int walk = 0; walk < 2; ++walk) {
+        if (mine_is) {
+          int t0 = 0, k = 0;
+#pragma unroll 1
+          for (int p = p0;; ++p) {
+            const long long stop = p + 1 >= used ? end : border(p + 1);
+            const bool fin = stop >= end;
+            const int t1 = fin ? b.tiles : (int)min(max(stop - s - kItemUnits, 0LL) >> (b.unit - 1), (long long)b.tiles);
+            if (t1 > t0 || (fin && b.tiles == 0)) {
+              if (walk) {
+                put_piece(a, at + k, b, t0, t1, n > 1 ? prow + k * b.nq : -1, h);
+                atomicAdd(&s_pair[p], 1);
+              }
+              ++k;
+            }
+            t0 = t1;
+            if (fin) break;
+          }
+          n = k;
         }
-      };
-      if (mine_is) cut([&](int, int, int) { ++n; });
-      int total;
-      int at = listed + block_sum_scan(n, &total, s_warp);
-      listed += total;
-      if (mine_is) {
-        int prow = -1, k = 0;
-        if (n > 1) {
-          prow = atomicAdd(&s_rows, n * b.nq);
-          PrefillSplit sp{};
-          sp.q0 = b.q0, sp.nq = b.nq, sp.pieces = n, sp.head0 = h, sp.heads = 1, sp.prow = prow;
-          a.plan.splits[atomicAdd(&s_split, 1)] = sp;
-        }
-        cut([&](int p, int t0, int t1) {
-          a.plan.pieces[at + k] = piece_of(b, t0, t1, n > 1 ? prow + k * b.nq : -1, h);
-          atomicAdd(&s_pair[p], 1);
-          ++k;
-        });
+        if (walk) break;
+        int total;
+        at = listed + block_sum_scan(n, &total, s_warp);
+        listed += total;
+        if (mine_is && n > 1) prow = put_split(a, b, n, h, 1, &s_rows, &s_split);
       }
     }
     __syncthreads();
@@ -252,18 +282,21 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArg
     };
     // length class: 0 = longest
     const int span = longest + 1;
-    auto bucket = [&](int cost) { return (int)((long long)(longest - cost) * kBuckets / span); };
+    auto bucket = [&](int cost) { return (int)mul_div(longest - cost, kBuckets, span); };
 
+#pragma unroll 1
     for (int i = tid; i < nblocks; i += kThreads) {
       const BlockOf b = block_of(a, seqs, i);
       const int P = pieces_of(b);
+#pragma unroll 1
       for (int p = 0; p < P; ++p) {
-        const int t0 = (int)((long long)b.tiles * p / P), t1 = (int)((long long)b.tiles * (p + 1) / P);
+        const int t0 = (int)mul_div(b.tiles, p, P), t1 = (int)mul_div(b.tiles, p + 1, P);
         atomicAdd(&s_hist[bucket((t1 - t0) * b.unit)], 1);
       }
     }
     __syncthreads();
     carry = 0;
+#pragma unroll 1
     for (int b0 = 0; b0 < kBuckets; b0 += kThreads) {
       int total;
       const int v = s_hist[b0 + tid];
@@ -272,27 +305,26 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArg
       carry += total;
     }
     __syncthreads();
+#pragma unroll 1
     for (int i = tid; i < nblocks; i += kThreads) {
       const BlockOf b = block_of(a, seqs, i);
       const int P = pieces_of(b);
       int prow = -1;
       if (P > 1) {
-        prow = atomicAdd(&s_rows, P * a.num_heads * b.nq);
-        PrefillSplit sp{};
-        sp.q0 = b.q0, sp.nq = b.nq, sp.pieces = P, sp.head0 = 0, sp.heads = a.num_heads, sp.prow = prow;
-        a.plan.splits[atomicAdd(&s_split, 1)] = sp;
+        prow = put_split(a, b, P, 0, a.num_heads, &s_rows, &s_split);
       }
+#pragma unroll 1
       for (int p = 0; p < P; ++p) {
-        const int t0 = (int)((long long)b.tiles * p / P), t1 = (int)((long long)b.tiles * (p + 1) / P);
+        const int t0 = (int)mul_div(b.tiles, p, P), t1 = (int)mul_div(b.tiles, p + 1, P);
         const int at = atomicAdd(&s_hist[bucket((t1 - t0) * b.unit)], 1);
-        if (at < a.plan.max_pieces)
-          a.plan.pieces[at] = piece_of(b, t0, t1, prow < 0 ? -1 : prow + p * a.num_heads * b.nq, 0);
+        put_piece(a, at, b, t0, t1, prow < 0 ? -1 : prow + p * a.num_heads * b.nq, 0);
       }
     }
   }
   __syncthreads();
   // rows of the split blocks before each
   int rows = 0;
+#pragma unroll 1
   for (int i0 = 0; i0 < s_split; i0 += kThreads) {
     const int i = i0 + tid;
     int total;
@@ -305,7 +337,10 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArg
     a.plan.header->status = 0;
     a.plan.header->num_pieces = min(carry, a.plan.max_pieces);
     a.plan.header->num_split = s_split;
-    a.plan.header->fixed = a.num_splits == 0 && (long long)nblocks * a.num_heads < (long long)kPrefillFixedItems * a.pairs;
+    a.plan.header->fixed = fixed;
+    // Heads are taken in groups whose keys and values stay in L2, unless a long
+    // item of the last group would outlast the other pairs by much.
+    a.plan.header->group_heads = work < 16ull * longest * a.pairs ? a.num_heads : a.group_heads;
   }
 }
 
@@ -318,39 +353,56 @@ __global__ void __launch_bounds__(256) prefill_combine_kernel(const PrefillArgs 
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int n = a.plan.header->num_split, total = a.plan.header->split_rows;
   if (n == 0) return;
+#pragma unroll 1
   for (int i = threadIdx.x; i < n && i < kSearch; i += blockDim.x) s_before[i] = a.plan.splits[i].before;
   __syncthreads();
   const int lane = threadIdx.x & 31;
-  const int warps = gridDim.x * 8;
-  for (int rr = blockIdx.x * 8 + (threadIdx.x >> 5); rr < total; rr += warps) {
-    int lo = 0, hi = n - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      const int before = mid < kSearch ? s_before[mid] : a.plan.splits[mid].before;
-      if (before <= rr) lo = mid; else hi = mid - 1;
+  // consecutive rows to a warp, mostly of one record
+  const int warps = gridDim.x * 8, per = (total + warps - 1) / warps;
+  const int from = (blockIdx.x * 8 + (threadIdx.x >> 5)) * per, to = min(from + per, total);
+  PrefillSplit sp{};
+  int ends = 0;              // first row behind the record
+#pragma unroll 1
+  for (int rr = from; rr < to; ++rr) {
+    if (rr == from || rr >= ends) {
+      int lo = 0, hi = n - 1;
+#pragma unroll 1
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        const int before = mid < kSearch ? s_before[mid] : a.plan.splits[mid].before;
+        if (before <= rr) lo = mid; else hi = mid - 1;
+      }
+      sp = a.plan.splits[lo];
+      ends = sp.before + sp.nq * sp.heads;
     }
-    const PrefillSplit sp = a.plan.splits[lo];
     const int own = rr - sp.before;
     const int h = own / sp.nq, r = own - h * sp.nq;
-    const int64_t step = (int64_t)sp.heads * sp.nq;
-    const int64_t at0 = sp.prow + (int64_t)h * sp.nq + r;
-    float m = -INFINITY;
-    for (int p = lane; p < sp.pieces; p += 32) m = fmaxf(m, a.plan.part_lse[at0 + p * step]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float ref = m == -INFINITY ? 0.f : m;
+    const int step = sp.heads * sp.nq;                        // all partial rows are below 2^31
+    const float* lse = a.plan.part_lse + sp.prow + own;
+    const float4* part = reinterpret_cast<const float4*>(a.plan.part_o + (int64_t)(sp.prow + own) * kNope) + lane;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float sum = 0.f;
-    for (int p0 = 0; p0 < sp.pieces; p0 += 32) {
-      const float l = p0 + lane < sp.pieces ? a.plan.part_lse[at0 + (p0 + lane) * step] : -INFINITY;
-      const float e = l == -INFINITY ? 0.f : expf(l - ref);
-      const int m32 = min(32, sp.pieces - p0);
-#pragma unroll 4
-      for (int p = 0; p < m32; ++p) {
-        const float w = __shfl_sync(0xffffffffu, e, p);
-        const float4 v = *reinterpret_cast<const float4*>(a.plan.part_o + (at0 + (p0 + p) * step) * kNope + 4 * lane);
+    float ref = -INFINITY, sum = 0.f;
+    // four pieces at a time; the reference follows the largest
+#pragma unroll 1
+    for (int p0 = 0; p0 < sp.pieces; p0 += 4) {
+      float l[4];
+      float4 v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const bool is = p0 + e < sp.pieces;
+        l[e] = is ? lse[(int64_t)(p0 + e) * step] : -INFINITY;
+        v[e] = is ? part[(int64_t)(p0 + e) * step * (kNope / 4)] : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      const float top = fmaxf(fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])), ref);
+      const float sub = top == -INFINITY ? 0.f : top;
+      const float old = expf(ref - sub);                      // ref = -inf: 0
+      sum *= old, o.x *= old, o.y *= old, o.z *= old, o.w *= old;
+      ref = top;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float w = l[e] == -INFINITY ? 0.f : expf(l[e] - sub);
         sum += w;
-        if (w != 0.f) o.x += w * v.x, o.y += w * v.y, o.z += w * v.z, o.w += w * v.w;
+        if (w != 0.f) o.x += w * v[e].x, o.y += w * v[e].y, o.z += w * v[e].z, o.w += w * v[e].w;
       }
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -385,7 +437,7 @@ cudaError_t launch_prefill_plan(const PrefillArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_prefill_combine(const PrefillArgs& a, cudaStream_t s) {
-  return launch_dependent(prefill_combine_kernel, 4 * a.pairs, 256, a, s);
+  return launch_dependent(prefill_combine_kernel, 12 * a.pairs, 256, a, s);   // six blocks an SM
 }
 
 }  // namespace mla
