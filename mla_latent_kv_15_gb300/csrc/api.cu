@@ -694,11 +694,12 @@ int mla_prefill(const void* q, int64_t q_token_stride, int64_t q_head_stride, co
   a.wait_limit_ns = g_wait_limit_ns;
   a.plan = mla::prefill_plan_from(workspace, L);
   cudaStream_t s = (cudaStream_t)stream;
-  cudaError_t e = mla::launch_prefill_plan(a, s);
+  a.direct = num_splits <= 1 && batch <= mla::kPrefillDirectBatch && total_kv <= mla::kPrefillDirectKeys;
+  cudaError_t e = a.direct ? cudaSuccess : mla::launch_prefill_plan(a, s);
   if (e != cudaSuccess) return cuda_fail(e, "prefill plan launch");
   e = mla::launch_prefill(tm_q, tm_kv, tm_pe, a, s);
   if (e != cudaSuccess) return cuda_fail(e, "prefill launch");
-  e = mla::launch_prefill_combine(a, s);
+  if (!a.direct) e = mla::launch_prefill_combine(a, s);
   if (e != cudaSuccess) return cuda_fail(e, "prefill combine launch");
   return ok();
 }

@@ -119,6 +119,22 @@ __device__ __forceinline__ int tiles_of(const Item& it) {
   return narrow_item(it) ? it.tiles[0] + it.tiles[1] : max(it.tiles[0], it.tiles[1]);
 }
 
+// What follows from an item's rows and keys.
+__device__ __forceinline__ void finish_item(const PrefillArgs& a, Item& it) {
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int last = min(256 * (t + 1), it.nq) - 1;
+    it.seen[t] = it.nq > 256 * t ? min(max(it.lim0 + (a.causal ? last : 0), 0), it.nkeys) : 0;
+    it.tiles[t] = (it.seen[t] + kPrefillTile - 1) / kPrefillTile;
+  }
+  if (narrow_item(it)) {
+    it.seen[1] = it.seen[0];
+    it.tiles[1] = it.tiles[0] / 2;
+    it.tiles[0] -= it.tiles[1];
+  }
+  it.last = 0;
+}
+
 // Item `i` of the list: pieces longest first, interleaved over a group of
 // heads; in a fixed plan a piece is an item.
 __device__ __forceinline__ Item item_at(const PrefillArgs& a, int np, int group, bool fixed, int i) {
@@ -136,48 +152,84 @@ __device__ __forceinline__ Item item_at(const PrefillArgs& a, int np, int group,
   it.q0 = r0.x, it.nq = r0.y, it.kv0 = r0.z, it.nkeys = r0.w, it.lim0 = r1.x, it.prow = r1.y;
   it.head = fixed ? r1.z : head;
   if (it.prow >= 0) it.prow += head * it.nq;
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const int last = min(256 * (t + 1), it.nq) - 1;
-    it.seen[t] = it.nq > 256 * t ? min(max(it.lim0 + (a.causal ? last : 0), 0), it.nkeys) : 0;
-    it.tiles[t] = (it.seen[t] + kPrefillTile - 1) / kPrefillTile;
-  }
-  if (narrow_item(it)) {
-    it.seen[1] = it.seen[0];
-    it.tiles[1] = it.tiles[0] / 2;
-    it.tiles[0] -= it.tiles[1];
-  }
-  it.last = 0;
+  finish_item(a, it);
   return it;
 }
 
-// The leading CTA's list warp (one thread) hands the pair's items to both
-// CTAs.  In a fixed plan they are the pair's range of pieces; else the first
-// is the pair's own and the next come from a counter all pairs share, so that
-// a pair done early takes more.
-__device__ __forceinline__ void list_items(const PrefillArgs& a, const Ctx& ctx, Item* slots) {
+// Item `i` without a plan, by the whole warp: lane b holds sequence b (`seq`:
+// its first rows and lengths) and the blocks before it.
+__device__ __forceinline__ Item item_direct(const PrefillArgs& a, const int4 seq, int before, int blocks, int i) {
+  const int blk = i / a.num_heads;
+  const unsigned owner = __ballot_sync(0xffffffffu, blk >= before && blk < before + blocks);
+  const int src = __ffs(owner) - 1;
+  const int r0 = (blk - __shfl_sync(0xffffffffu, before, src)) * kPrefillRows;
+  const PrefillBlock b = prefill_block(__shfl_sync(0xffffffffu, seq.x, src), __shfl_sync(0xffffffffu, seq.y, src),
+                                       __shfl_sync(0xffffffffu, seq.z, src), __shfl_sync(0xffffffffu, seq.w, src), r0,
+                                       a.causal);
+  Item it;
+  it.q0 = b.q0, it.nq = b.nq, it.kv0 = b.kv0, it.nkeys = b.nkeys, it.lim0 = b.lim0, it.prow = -1;
+  it.head = i - blk * a.num_heads;
+  finish_item(a, it);
+  return it;
+}
+
+// The leading CTA's list warp hands the pair's items to both CTAs.  In a
+// fixed plan they are the pair's range of pieces, without a plan every
+// pairs-th item; else the first is the pair's own and the next come from a
+// counter all pairs share, so that a pair done early takes more.
+__device__ __forceinline__ void list_items(const PrefillArgs& a, const Ctx& ctx, Item* slots, int lane) {
   Bars* bars = ctx.bars;
-  const int np = a.plan.header->num_pieces, pairs = gridDim.x / 2, pair = cluster_id_x();
-  const bool fixed = a.plan.header->fixed != 0;
-  const int group = a.plan.header->group_heads;
-  const int items = fixed ? a.plan.first_piece[pair + 1] : np * a.num_heads;
-  int i = fixed ? a.plan.first_piece[pair] : pair;
+  PrefillHeader* head = a.plan.header;
+  const int pairs = gridDim.x / 2, pair = cluster_id_x();
+  int np = 0, group = 1, items, i = pair;
+  bool fixed = false;
+  int4 seq = make_int4(0, 0, 0, 0);
+  int before = 0, blocks = 0;
+  if (a.direct) {
+    int bad = 0;
+    if (lane < a.batch) {
+      const int q0 = a.cu_q[lane], q1 = a.cu_q[lane + 1], k0 = a.cu_kv[lane], k1 = a.cu_kv[lane + 1];
+      if (q0 < 0 || q1 < q0 || q1 > a.total_q) bad |= 8;     // MLA_DEVERR_BAD_QSL
+      if (k0 < 0 || k1 < k0 || k1 > a.total_kv) bad |= 2;    // MLA_DEVERR_BAD_SEQ_LEN
+      seq = make_int4(q0, q1 - q0, k0, k1 - k0);
+      blocks = bad & 8 ? 0 : (q1 - q0 + kPrefillRows - 1) / kPrefillRows;
+    }
+    int incl = blocks;
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+      const int n = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += n;
+      bad |= __shfl_xor_sync(0xffffffffu, bad, o);
+    }
+    before = incl - blocks;
+    items = bad ? 0 : __shfl_sync(0xffffffffu, incl, 31) * a.num_heads;
+    if (pair == 0 && lane == 0) head->status = bad;
+  } else {
+    np = head->num_pieces;
+    group = head->group_heads;
+    fixed = head->fixed != 0;
+    items = fixed ? a.plan.first_piece[pair + 1] : np * a.num_heads;
+    if (fixed) i = a.plan.first_piece[pair];
+  }
   for (uint32_t n = 0;; ++n) {
     const uint32_t slot = n % kItemSlots;
     Item it{};
     it.last = 1;
-    if (i < items) it = item_at(a, np, group, fixed, i);
+    if (i < items) it = a.direct ? item_direct(a, seq, before, blocks, i) : item_at(a, np, group, fixed, i);
     wait_bar(ctx, &bars->item_empty[slot], ((n / kItemSlots) & 1) ^ 1, kItemWait);
-    if (*(volatile int*)&bars->abort) it.last = 1;    // the peer is told
-    slots[slot] = it;
-    mbar_arrive(smem_u32(&bars->item_full[slot]));
-    const uint32_t far = mapa(smem_u32(&slots[slot]), 1), far_bar = mapa(smem_u32(&bars->item_full[slot]), 1);
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(&it);
-#pragma unroll
-    for (int k = 0; k < 3; ++k)
-      st_async_v4(far + 16 * k, w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3], far_bar);
-    if (it.last) break;
-    i = fixed ? i + 1 : pairs + atomicAdd(&a.plan.header->next, 1);
+    int next = 0;
+    if (lane == 0) {
+      if (*(volatile int*)&bars->abort) it.last = 1;    // the peer is told
+      slots[slot] = it;
+      mbar_arrive(smem_u32(&bars->item_full[slot]));
+      const uint32_t far = mapa(smem_u32(&slots[slot]), 1), far_bar = mapa(smem_u32(&bars->item_full[slot]), 1);
+      st_async_v4(far, it.q0, it.nq, it.kv0, it.nkeys, far_bar);
+      st_async_v4(far + 16, it.lim0, it.prow, it.head, it.seen[0], far_bar);
+      st_async_v4(far + 32, it.seen[1], it.tiles[0], it.tiles[1], it.last, far_bar);
+      if (!it.last && !fixed && !a.direct) next = atomicAdd(&head->next, 1);
+    }
+    if (__shfl_sync(0xffffffffu, it.last, 0)) break;
+    i = fixed ? i + 1 : pairs + (a.direct ? i : __shfl_sync(0xffffffffu, next, 0));
   }
 }
 
@@ -738,7 +790,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync();   // both CTAs' barriers are initialised before either uses the other's
   tc_fence_after();
   const uint32_t tbase = bars->tmem_base;
-  // everything above overlaps the plan kernel
+  // everything above overlaps the kernel before (the plan)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const Ctx ctx{bars, rank, &a.plan.header->status, a.wait_limit_ns};
@@ -754,12 +806,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (rank == 0) issue_items(ctx, slots, tbase, smem_u32(q_smem), smem_u32(ring), lane);
       wait_bar(ctx, &bars->drain, 0, kItemWait);   // every product of the pair is done
     } else if (warp == kWarpList) {
-      if (lane == 0) {
-        if (rank == 0)
-          list_items(a, ctx, slots);
-        else
-          await_items(ctx, slots);
-      }
+      if (rank == 0)
+        list_items(a, ctx, slots, lane);
+      else if (lane == 0)
+        await_items(ctx, slots);
       __syncwarp();
     } else {
       clear_tails(ctx, slots, ring, lane);

@@ -118,6 +118,7 @@ struct PrefillArgs {
   int batch, total_q, total_kv, num_heads;
   int causal;
   int num_splits;        // 0: automatic
+  int direct;            // no plan (kPrefillDirectKeys)
   int group_heads;       // heads whose keys and values stay in L2 together
   int pairs;             // grid of the attention kernel, in CTA pairs
   float scale_log2;      // scale * log2(e), > 0
@@ -126,6 +127,28 @@ struct PrefillArgs {
   unsigned long long wait_limit_ns;
   PrefillPlan plan;
 };
+
+// Calls of at most this many sequences and key rows need no plan: no item is
+// long enough to be cut or to be taken early, and every pair's list warp finds
+// its items from the prefix sums (one launch instead of three).
+constexpr int kPrefillDirectBatch = 32;
+constexpr int kPrefillDirectKeys = 512;
+
+#ifdef __CUDACC__
+// Query rows r0.. of a sequence of sq rows from q0 over sk keys from k0, as a block.
+struct PrefillBlock {
+  int q0, nq, kv0, nkeys, lim0;
+};
+__device__ __forceinline__ PrefillBlock prefill_block(int q0, int sq, int k0, int sk, int r0, int causal) {
+  PrefillBlock b;
+  b.q0 = q0 + r0;
+  b.nq = min(kPrefillRows, sq - r0);
+  b.kv0 = k0;
+  b.lim0 = causal ? sk - sq + 1 + r0 : sk;
+  b.nkeys = causal ? min(max(b.lim0 + b.nq - 1, 0), sk) : sk;
+  return b;
+}
+#endif
 
 cudaError_t launch_prefill_plan(const PrefillArgs& a, cudaStream_t s);
 // tm_q: {192, heads, total_q} boxes 64 x 1 x 128; tm_kv: {256, heads, total_kv}

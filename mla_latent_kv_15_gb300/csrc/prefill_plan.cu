@@ -63,8 +63,8 @@ __device__ __noinline__ int block_sum_scan(int v, int* total, int* warp_sums) {
   return before + incl - v;
 }
 
-struct BlockOf {
-  int q0, nq, kv0, nkeys, lim0, tiles;
+struct BlockOf : PrefillBlock {
+  int tiles;
   int unit;    // cost of a tile
   __device__ int cost() const { return tiles * unit; }
 };
@@ -86,13 +86,8 @@ __device__ __noinline__ BlockOf block_of(const PrefillArgs& a, const Sequences& 
     if (sq_.first[mid] <= i) lo = mid; else hi = mid - 1;
   }
   const int q0 = sq_.cu_q[lo], sq = sq_.cu_q[lo + 1] - q0, k0 = sq_.cu_kv[lo], sk = sq_.cu_kv[lo + 1] - k0;
-  const int r0 = (i - sq_.first[lo]) * kPrefillRows;
   BlockOf b;
-  b.q0 = q0 + r0;
-  b.nq = min(kPrefillRows, sq - r0);
-  b.kv0 = k0;
-  b.lim0 = a.causal ? sk - sq + 1 + r0 : sk;
-  b.nkeys = a.causal ? min(max(b.lim0 + b.nq - 1, 0), sk) : sk;
+  static_cast<PrefillBlock&>(b) = prefill_block(q0, sq, k0, sk, (i - sq_.first[lo]) * kPrefillRows, a.causal);
   b.tiles = (b.nkeys + kPrefillTile - 1) / kPrefillTile;
   b.unit = b.nq > kPrefillRows / 2 ? 2 : 1;
   return b;
@@ -131,6 +126,7 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArg
   __shared__ int s_before[kMaxFixed];              // units of the blocks before each, fixed plan
   __shared__ int s_pair[kPrefillMaxPairs + 1];
   __shared__ int s_seq[3][kSeqs + 1];
+  __shared__ BlockOf s_block[kThreads];            // few blocks: all of them
   __shared__ unsigned long long s_total;
   __shared__ int s_longest, s_status, s_rows, s_split;
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -138,8 +134,6 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArg
   const int tid = threadIdx.x;
   if (tid == 0) a.plan.header->next = 0;
   if (tid == 0) s_total = 0, s_longest = 0, s_status = 0, s_rows = 0, s_split = 0;
-#pragma unroll 1
-  for (int i = tid; i < kBuckets; i += kThreads) s_hist[i] = 0;
   __syncthreads();
 
   // the sequences: checks, and the blocks before each
@@ -186,16 +180,22 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArg
     return;
   }
 
+  // a block a thread, looked up once, where there are no more
+  const bool few = nblocks <= kThreads;
+  auto block = [&](int i) { return few ? s_block[i] : block_of(a, seqs, i); };
   unsigned long long mine = 0;
   int longest = 0;
 #pragma unroll 1
   for (int i = tid; i < nblocks; i += kThreads) {
-    const int t = block_of(a, seqs, i).cost();
-    mine += t;
-    longest = max(longest, t);
+    const BlockOf b = block_of(a, seqs, i);
+    if (few) s_block[i] = b;
+    mine += b.cost();
+    longest = max(longest, b.cost());
   }
-  atomicAdd(&s_total, mine);
-  atomicMax(&s_longest, longest);
+  if (mine) {
+    atomicAdd(&s_total, mine);
+    atomicMax(&s_longest, longest);
+  }
   __syncthreads();
   const unsigned long long work = s_total * a.num_heads;
   longest = s_longest;
@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArg
     for (int b0 = 0; b0 < nblocks; b0 += kThreads) {
       const int b = b0 + tid;
       int total;
-      const int before = block_sum_scan(b < nblocks ? block_of(a, seqs, b).cost() + kItemUnits : 0, &total, s_warp);
+      const int before = block_sum_scan(b < nblocks ? block(b).cost() + kItemUnits : 0, &total, s_warp);
       if (b < nblocks) s_before[b] = all + before;
       all += total;
     }
@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArg
       long long s = 0;
       int p0 = 0, n = 0;
       if (mine_is) {
-        b = block_of(a, seqs, i - h * nblocks);
+        b = block(i - h * nblocks);
         s = (long long)h * all + s_before[i - h * nblocks];
         p0 = (int)mul_div(s, used, length);
         while (p0 + 1 < used && border(p0 + 1) <= s) ++p0;
@@ -280,44 +280,62 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArg
       if (a.num_splits > 0) return max(1, min(a.num_splits, b.tiles));
       return cut && 2 * b.cost() > 3 * chunk ? min((b.cost() + chunk - 1) / chunk, b.tiles) : 1;
     };
-    // length class: 0 = longest
-    const int span = longest + 1;
-    auto bucket = [&](int cost) { return (int)mul_div(longest - cost, kBuckets, span); };
+    if (few && !cut && a.num_splits == 0) {
+      // every block is a piece: its place is the number of longer ones before it
+      if (tid < nblocks) {
+        const BlockOf b = s_block[tid];
+        int at = 0;
+#pragma unroll 1
+        for (int i = 0; i < nblocks; ++i) {
+          const int c = s_block[i].cost();
+          at += c > b.cost() || (c == b.cost() && i < tid);
+        }
+        put_piece(a, at, b, 0, b.tiles, -1, 0);
+      }
+      carry = nblocks;
+    } else {
+      // length class: 0 = longest
+      const int span = longest + 1;
+      auto bucket = [&](int cost) { return (int)mul_div(longest - cost, kBuckets, span); };
 
 #pragma unroll 1
-    for (int i = tid; i < nblocks; i += kThreads) {
-      const BlockOf b = block_of(a, seqs, i);
-      const int P = pieces_of(b);
+      for (int i = tid; i < kBuckets; i += kThreads) s_hist[i] = 0;
+      __syncthreads();
 #pragma unroll 1
-      for (int p = 0; p < P; ++p) {
-        const int t0 = (int)mul_div(b.tiles, p, P), t1 = (int)mul_div(b.tiles, p + 1, P);
-        atomicAdd(&s_hist[bucket((t1 - t0) * b.unit)], 1);
+      for (int i = tid; i < nblocks; i += kThreads) {
+        const BlockOf b = block(i);
+        const int P = pieces_of(b);
+#pragma unroll 1
+        for (int p = 0; p < P; ++p) {
+          const int t0 = (int)mul_div(b.tiles, p, P), t1 = (int)mul_div(b.tiles, p + 1, P);
+          atomicAdd(&s_hist[bucket((t1 - t0) * b.unit)], 1);
+        }
       }
-    }
-    __syncthreads();
-    carry = 0;
+      __syncthreads();
+      carry = 0;
 #pragma unroll 1
-    for (int b0 = 0; b0 < kBuckets; b0 += kThreads) {
-      int total;
-      const int v = s_hist[b0 + tid];
-      const int before = block_sum_scan(v, &total, s_warp);
-      s_hist[b0 + tid] = carry + before;
-      carry += total;
-    }
-    __syncthreads();
-#pragma unroll 1
-    for (int i = tid; i < nblocks; i += kThreads) {
-      const BlockOf b = block_of(a, seqs, i);
-      const int P = pieces_of(b);
-      int prow = -1;
-      if (P > 1) {
-        prow = put_split(a, b, P, 0, a.num_heads, &s_rows, &s_split);
+      for (int b0 = 0; b0 < kBuckets; b0 += kThreads) {
+        int total;
+        const int v = s_hist[b0 + tid];
+        const int before = block_sum_scan(v, &total, s_warp);
+        s_hist[b0 + tid] = carry + before;
+        carry += total;
       }
+      __syncthreads();
 #pragma unroll 1
-      for (int p = 0; p < P; ++p) {
-        const int t0 = (int)mul_div(b.tiles, p, P), t1 = (int)mul_div(b.tiles, p + 1, P);
-        const int at = atomicAdd(&s_hist[bucket((t1 - t0) * b.unit)], 1);
-        put_piece(a, at, b, t0, t1, prow < 0 ? -1 : prow + p * a.num_heads * b.nq, 0);
+      for (int i = tid; i < nblocks; i += kThreads) {
+        const BlockOf b = block(i);
+        const int P = pieces_of(b);
+        int prow = -1;
+        if (P > 1) {
+          prow = put_split(a, b, P, 0, a.num_heads, &s_rows, &s_split);
+        }
+#pragma unroll 1
+        for (int p = 0; p < P; ++p) {
+          const int t0 = (int)mul_div(b.tiles, p, P), t1 = (int)mul_div(b.tiles, p + 1, P);
+          const int at = atomicAdd(&s_hist[bucket((t1 - t0) * b.unit)], 1);
+          put_piece(a, at, b, t0, t1, prow < 0 ? -1 : prow + p * a.num_heads * b.nq, 0);
+        }
       }
     }
   }

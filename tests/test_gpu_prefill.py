@@ -288,6 +288,19 @@ def test_prefill_inconsistent_sums_are_flagged_and_write_nothing():
     Case([50, 50], [50, 40], 2, seed=15).run().check()
 
 
+@pytest.mark.parametrize("q_lens,kv_lens,heads", [([1] * 32, [16] * 32, 5), ([1] * 33, [15] * 33, 5), ([600, 0, 40], [512, 0, 0], 7),
+                                                  ([3, 500, 1], [100, 412, 0], 100), ([3, 500, 1], [100, 412, 1], 100)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prefill_around_the_sizes_without_a_plan(q_lens, kv_lens, heads, causal):
+    """Up to 32 sequences over up to 512 key rows take one launch."""
+    c = Case(q_lens, kv_lens, heads, seed=21, pad_q=2).run(causal).check(causal)
+    c.cu_q[-1] = c.q.shape[0] + 1
+    c.out.fill_(7.0)
+    c.run(causal)
+    torch.cuda.synchronize()
+    assert mla.prefill_status(c.ws) == mla.DEVERR_BAD_QSL and (c.out == 7.0).all()
+
+
 def test_prefill_without_rows_or_keys():
     Case([0, 0], [3, 4], 2).run()                       # no query row: nothing to do
     c = Case([5, 300], [0, 0], 2).run()                 # no key at all
