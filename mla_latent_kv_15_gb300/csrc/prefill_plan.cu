@@ -125,6 +125,7 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArg
   __shared__ int s_warp[kThreads / 32];
   __shared__ int s_before[kMaxFixed];              // units of the blocks before each, fixed plan
   __shared__ int s_pair[kPrefillMaxPairs + 1];
+  __shared__ long long s_border[kPrefillMaxPairs + 1];
   __shared__ int s_seq[3][kSeqs + 1];
   __shared__ BlockOf s_block[kThreads];            // few blocks: all of them
   __shared__ unsigned long long s_total;
@@ -215,12 +216,14 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArg
       all += total;
     }
 #pragma unroll 1
-    for (int p = tid; p <= kPrefillMaxPairs; p += kThreads) s_pair[p] = 0;
-    __syncthreads();
     const long long length = (long long)all * a.num_heads;
     // pairs in use: no more pieces than leave each about kMinChunk units
     const int used = (int)min((long long)a.pairs, max((long long)items, length / (kItemUnits + kMinChunk)));
-    auto border = [&](int p) { return mul_div(length, p, used); };
+    if (tid <= kPrefillMaxPairs) {
+      s_pair[tid] = 0;
+      s_border[tid] = used > 0 ? mul_div(length, min(tid, used), used) : 0;   // where pair `tid`'s span begins
+    }
+    __syncthreads();
     int listed = 0;
 #pragma unroll 1
     for (int i0 = 0; i0 < items; i0 += kThreads) {
@@ -232,9 +235,12 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArg
       if (mine_is) {
         b = block(i - h * nblocks);
         s = (long long)h * all + s_before[i - h * nblocks];
-        p0 = (int)mul_div(s, used, length);
-        while (p0 + 1 < used && border(p0 + 1) <= s) ++p0;
-        while (border(p0) > s) --p0;
+        int hi = used - 1;
+#pragma unroll 1
+        while (p0 < hi) {
+          const int mid = (p0 + hi + 1) >> 1;
+          if (s_border[mid] <= s) p0 = mid; else hi = mid - 1;
+        }
       }
       const long long end = s + kItemUnits + b.cost();
       // two walks over the item's pieces: they are counted, then listed
@@ -245,7 +251,7 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArg
           int t0 = 0, k = 0;
 #pragma unroll 1
           for (int p = p0;; ++p) {
-            const long long stop = p + 1 >= used ? end : border(p + 1);
+            const long long stop = p + 1 >= used ? end : s_border[p + 1];
             const bool fin = stop >= end;
             const int t1 = fin ? b.tiles : (int)min(max(stop - s - kItemUnits, 0LL) >> (b.unit - 1), (long long)b.tiles);
             if (t1 > t0 || (fin && b.tiles == 0)) {
