@@ -126,16 +126,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!mbar_wait(smem_u32(&bars->full[c % stages]), (c / stages) & 1)) give_up(bars);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t idesc = idesc_bf16_f32(kM, bn, 0, 0);
-      for (int c = 0; c < kChunks; ++c) {
-        const int slot = c % stages;
-        if (!mbar_wait(smem_u32(&bars->full[slot]), (c / stages) & 1)) {
-          give_up(bars);
-          break;
-        }
-        if (*abort_flag) break;
-        tc_fence_after();
+    const uint32_t idesc = idesc_bf16_f32(kM, bn, 0, 0);
+    for (int c = 0; c < kChunks; ++c) {
+      const int slot = c % stages;
+      if (!mbar_wait(smem_u32(&bars->full[slot]), (c / stages) & 1)) {
+        give_up(bars);
+        break;
+      }
+      if (*abort_flag) break;
+      tc_fence_after();
+      if (elect_one()) {
         const uint32_t st = smem_u32(smem + slot * stage_bytes);
         const uint64_t xd = smem_desc(st, 16, 1024, kSwizzle128B);
         const uint64_t wd = smem_desc(st + xbox, 16, 1024, kSwizzle128B);
@@ -143,10 +143,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; k < kK / 16; ++k)
           mma_ss(tmem, xd + ((k * 32) >> 4), wd + ((k * 32) >> 4), idesc, (c > 0 || k > 0) ? 1u : 0u);
         mma_commit(smem_u32(&bars->empty[slot]));
+        if (c == kChunks - 1) mma_commit(smem_u32(&bars->d_full));
       }
-      mma_commit(smem_u32(&bars->d_full));
-      if (!mbar_wait(smem_u32(&bars->d_full), 0)) give_up(bars);
+      __syncwarp();
     }
+    if (!*abort_flag && !mbar_wait(smem_u32(&bars->d_full), 0)) give_up(bars);
+    __syncwarp();
   } else {
     const int q = warp & 3;
     const int64_t t = t0 + 32 * q + lane;
