@@ -17,6 +17,11 @@
 // stage), two accumulators in tensor memory, so that the stores of a tile run
 // under the products of the next.  The epilogue leaves in 32-row x 64-column
 // pieces staged in shared memory and stored by TMA, which clips ragged edges.
+// What bounds it is the loads' latency beside the stores (8192 tokens x 32768
+// columns: 136 us without the stores): shared memory goes to load stages, and
+// two staged pieces a warp are enough (pieces 2, 4, 6, 8, leaving 6, 5, 4, 3
+// stages: 174, 181, 186, 200 us; the tokens kept in shared memory and only
+// weights streamed, four stages: 212; 32-byte stores from registers: 202).
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -178,13 +183,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 constexpr int kPairThreads = 192;                // load warp, MMA warp, 4 epilogue warps
 constexpr uint32_t kPiece = 32 * 128;            // 32 rows x 64 bf16
 
+constexpr int kPieces = 2;                       // staged pieces of an epilogue warp
+
 template <int kBN>
 struct PairShape {
   static constexpr uint32_t kWBox = kBN / 2 * kK * 2;
   static constexpr uint32_t kStage = kXBoxMax + kWBox;
-  static constexpr int kPieces = kBN / 64;       // of a tile and epilogue warp
   static constexpr uint32_t kStaging = 4 * kPieces * kPiece;
-  static constexpr int kStages = (int)((232448 - 1024 - 512 - kStaging) / kStage);
+  static constexpr int kStages = (int)((232448 - 1024 - 512 - kStaging) / kStage) < 8
+                                     ? (int)((232448 - 1024 - 512 - kStaging) / kStage)
+                                     : 8;
   static constexpr size_t kSmem = 1024 + kStages * kStage + kStaging + 512;
 };
 
@@ -307,7 +315,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     pair_wait(bars, &bars->drain, 0);   // every product of the pair is done
   } else {
     const int q = warp & 3;
-    uint8_t* stage = staging + q * P::kPieces * kPiece;
+    uint8_t* stage = staging + q * kPieces * kPiece;
     uint32_t m = 0;
     for (int i = first; i < tiles && !*abort_flag; i += step, ++m) {
       const uint32_t acc = m & 1;
@@ -316,16 +324,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       if (*abort_flag) break;
       tc_fence_after();
       const uint32_t from = tmem + acc * kBN + ((uint32_t)(32 * q) << 16);
-#pragma unroll
-      for (int p = 0; p < P::kPieces; ++p) {
+#pragma unroll 1
+      for (int p = 0; p < kBN / 64; ++p) {
+        uint8_t* piece = stage + (p % kPieces) * kPiece;
         uint32_t a[32], b[32];
         tmem_ld32(from + 64 * p, a);
         tmem_ld32(from + 64 * p + 32, b);
-        // this piece's store of the tile before has read it
-        if (lane == 0) bulk_wait_group_read<P::kPieces - 1>();
+        // the piece's last store has read it
+        if (lane == 0) bulk_wait_group_read<kPieces - 1>();
         tmem_wait_ld();
         __syncwarp();
-        const uint32_t row = smem_u32(stage + p * kPiece) + lane * 128;
+        const uint32_t row = smem_u32(piece) + lane * 128;
 #pragma unroll
         for (int v = 0; v < 8; ++v) {
           uint32_t w[4];
@@ -339,7 +348,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                        "r"(w[1]), "r"(w[2]), "r"(w[3])
                        : "memory");
         }
-        if (p == P::kPieces - 1) {
+        if (p == kBN / 64 - 1) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_remote(mapa(smem_u32(&bars->acc_empty[acc]), 0));
@@ -347,7 +356,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          if (t0 < T && c0 + 64 * p < C) tma_store_2d(&tm_y, c0 + 64 * p, t0, smem_u32(stage + p * kPiece));
+          if (t0 < T && c0 + 64 * p < C) tma_store_2d(&tm_y, c0 + 64 * p, t0, smem_u32(piece));
           bulk_commit_group();
         }
       }
