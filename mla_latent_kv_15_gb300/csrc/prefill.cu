@@ -513,9 +513,12 @@ __device__ __noinline__ void mend_row(const PrefillArgs& a, int row, int head, i
 // (the tile's own code is the only part that is hot).
 
 // Scores of keys that a row does not see, the tile's from `left` on, become -inf.
-__device__ __forceinline__ void mask_tile(uint32_t s_col, int left) {
+// The warp's rows see `fewest` of its keys or more.
+__device__ __forceinline__ void mask_tile(uint32_t s_col, int left, int fewest) {
+  const int g0 = max(fewest, 0) >> 5;
+  left -= 32 * g0;
 #pragma unroll 1
-  for (int g = 0; g < 4; ++g, left -= 32) {
+  for (int g = g0; g < 4; ++g, left -= 32) {
     uint32_t s[32];
     tmem_ld32(s_col + 32 * g, s);
     tmem_wait_ld();
@@ -620,7 +623,7 @@ __device__ __forceinline__ void softmax_items(const PrefillArgs& a, const Ctx& c
         if (lane == 0) mbar_arrive_remote(p_full);
         continue;
       }
-      if (warp_sees < (j + 1) * kPrefillTile) mask_tile(s_col, sees - j * kPrefillTile);
+      if (warp_sees < (j + 1) * kPrefillTile) mask_tile(s_col, sees - j * kPrefillTile, warp_sees - j * kPrefillTile);
       softmax_tile(s_col, o_col, scale, i == 0, ref, sum);
       tmem_wait_st();
       tc_fence_before();
