@@ -550,7 +550,9 @@ MLA_API int mla_prefill_status(const void* workspace, int* status, void* stream)
  * default 1 s; otherwise 1e5..1e9), and with skip_first_tile != 0 the first
  * CTA of the grid never loads its first cache tile, so the wait for that tile
  * runs out.  The decode still returns; its outputs are then undefined and the
- * error word reports the timeout.  Call with (0, 0) to restore the defaults.
+ * error word reports the timeout.  mla_prefill takes both settings in the same
+ * way (the skipped tile is the first keys of its first CTA).  Call with (0, 0)
+ * to restore the defaults.
  */
 MLA_API int mla_set_decode_wait_test(int skip_first_tile, unsigned long long wait_limit_ns);
 

@@ -443,7 +443,8 @@ def set_decode_wait_test(skip_first_tile: bool = False, wait_limit_ns: int = 0) 
     """Test aid for the bounded on-chip waits: later decodes of this thread
     run with every wait bounded by ``wait_limit_ns`` (0: the default 1 s) and,
     with ``skip_first_tile``, one CTA never loads its first cache tile, so a
-    wait for it runs out and the device error word gets DEVERR_TIMEOUT."""
+    wait for it runs out and the device error word gets DEVERR_TIMEOUT.
+    Later prefills of the thread do the same."""
     _check(load().mla_set_decode_wait_test(int(bool(skip_first_tile)), int(wait_limit_ns)))
 
 

@@ -692,6 +692,7 @@ int mla_prefill(const void* q, int64_t q_token_stride, int64_t q_head_stride, co
   a.out = out;
   a.lse = lse;
   a.wait_limit_ns = g_wait_limit_ns;
+  a.debug_skip_tile = g_test_skip_tile;
   a.plan = mla::prefill_plan_from(workspace, L);
   cudaStream_t s = (cudaStream_t)stream;
   a.direct = num_splits <= 1 && batch <= mla::kPrefillDirectBatch && total_kv <= mla::kPrefillDirectKeys;

@@ -289,7 +289,7 @@ __device__ __forceinline__ bool has_tail(const Item& it, int tiles) {
 
 // ------------------------------------------------------------------ producer
 // The whole warp walks the items; one elected thread loads the CTA's halves.
-__device__ __forceinline__ void load_items(const Ctx& ctx, const Item* slots, const CUtensorMap* tm_q,
+__device__ __forceinline__ void load_items(const PrefillArgs& a, const Ctx& ctx, const Item* slots, const CUtensorMap* tm_q,
                                            const CUtensorMap* tm_kv, const CUtensorMap* tm_pe, uint32_t q_smem,
                                            uint32_t ring, int lane) {
   Bars* bars = ctx.bars;
@@ -321,7 +321,9 @@ __device__ __forceinline__ void load_items(const Ctx& ctx, const Item* slots, co
       const int row = it.kv0 + j * kPrefillTile, half = row + 64 * (int)ctx.rank;
       wait_bar(ctx, &bars->k_empty[stage], parity);
       if (*abort_flag) break;
-      if (elect_one()) {
+      // test aid: without these keys the waits of the pair run out
+      const bool skip = a.debug_skip_tile && blockIdx.x == 0 && n == 0;
+      if (!skip && elect_one()) {
         const uint32_t full = ctx.lead(&bars->k_full[stage]);
         mbar_expect_tx_remote(full, kKeyBytes);
         tma_load_3d_pair(dst, tm_kv, 0, it.head, half, full);
@@ -804,7 +806,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else {
     setmaxnreg_dec<kRegsOther>();
     if (warp == kWarpLoad) {
-      load_items(ctx, slots, &tm_q, &tm_kv, &tm_pe, smem_u32(q_smem), smem_u32(ring), lane);
+      load_items(a, ctx, slots, &tm_q, &tm_kv, &tm_pe, smem_u32(q_smem), smem_u32(ring), lane);
     } else if (warp == kWarpMma) {
       if (rank == 0) issue_items(ctx, slots, tbase, smem_u32(q_smem), smem_u32(ring), lane);
       wait_bar(ctx, &bars->drain, 0, kItemWait);   // every product of the pair is done

@@ -125,6 +125,7 @@ struct PrefillArgs {
   void* out;             // bf16 [total_q, heads, 128]
   float* lse;            // [total_q, heads] or null
   unsigned long long wait_limit_ns;
+  int debug_skip_tile;   // test aid: the first pair's leading CTA never loads its first keys
   PrefillPlan plan;
 };
 

@@ -100,6 +100,58 @@ def test_kv_up_proj_refusals(lib):
     assert lib.mla_last_error() == b""
 
 
+def test_prefill_refusals(lib):
+    names = "q qts qhs kv kts khs pe pes cu_q cu_kv B T Tk N scale causal splits out lse ws wsb stream".split()
+    need = lib.mla_prefill_workspace_size(2, 100, 4, 0)
+    good = dict(q=at(1), qts=768, qhs=192, kv=at(100), kts=1024, khs=256, pe=at(200), pes=576, cu_q=at(300), cu_kv=at(301),
+                B=2, T=100, Tk=500, N=4, scale=0.07, causal=1, splits=0, out=at(400), lse=at(500), ws=at(600), wsb=need,
+                stream=None)
+
+    def refused(code, text, **over):
+        rc = lib.mla_prefill(*[dict(good, **over)[n] for n in names])
+        assert rc == code, (rc, lib.mla_last_error())
+        assert text.encode() in lib.mla_last_error(), lib.mla_last_error()
+
+    for name in ("B", "T", "Tk"):
+        refused(-1, ">= 0", **{name: -1})
+    refused(-1, "num_heads", N=0)
+    refused(-1, "num_heads", N=1025)
+    for bad in (0.0, -0.1, float("nan"), float("inf")):
+        refused(-1, "scale", scale=bad)
+    refused(-1, "num_splits", splits=-1)
+    refused(-1, "num_splits", splits=4097)
+    refused(-2, "2^30", Tk=(1 << 30) + 1)
+    refused(-1, "2^31", T=1 << 30)
+    for name in ("q", "kv", "pe", "cu_q", "cu_kv", "out", "ws"):
+        refused(-1, "null", **{name: None})
+    for name in ("q", "kv", "pe", "out"):
+        refused(-1, "aligned", **{name: P(good[name].value + 8)})
+    for name in ("cu_q", "cu_kv", "lse"):
+        refused(-1, "aligned", **{name: P(good[name].value + 2)})
+    refused(-1, "256-byte", ws=P(good["ws"].value + 128))
+    for name in ("qts", "qhs", "kts", "khs", "pes"):
+        for bad in (0, -8, 12, (1 << 32) + 8):
+            refused(-1, "strides", **{name: bad})
+    refused(-1, "overlap", out=P((1 << 20) + 1024))
+    refused(-1, "overlap", out=P((100 << 20) + 1024))
+    refused(-1, "overlap", out=P((200 << 20) + 1024))
+    refused(-4, "workspace", wsb=need - 1)
+    refused(-4, "workspace", splits=8)
+    refused(-2, "num_splits", T=1 << 20, N=1024, splits=4096, out=at(1 << 20))
+    # nothing to do
+    assert lib.mla_prefill(*[dict(good, B=0, q=None, out=None, ws=None)[n] for n in names]) == 0
+    assert lib.mla_prefill(*[dict(good, T=0, q=None, out=None, ws=None)[n] for n in names]) == 0
+    assert lib.mla_last_error() == b""
+    assert lib.mla_prefill_status(None, None, None) == -1
+
+
+def test_prefill_workspace_size(lib):
+    f = lib.mla_prefill_workspace_size
+    assert f(0, 10, 4, 0) == 0 and f(1, 0, 4, 0) == 0 and f(1, 10, 0, 0) == 0 and f(1, 10, 4, -1) == 0
+    assert 0 < f(1, 1, 1, 0) < f(1, 512, 128, 0) <= f(8, 100000, 128, 0) < 200 << 20
+    assert f(1, 512, 128, 8) > f(1, 512, 128, 0)
+
+
 def bf16(*shape):
     return torch.empty(shape, dtype=torch.bfloat16)
 
@@ -165,3 +217,25 @@ def test_binding_refuses_tensors_of_another_device(monkeypatch):
         mla._on_current_device(_On(0), _On(1))
     with pytest.raises(ValueError, match="current device"):
         mla._on_current_device(_On(1), _On(1))
+
+
+def test_binding_refuses_what_the_prefill_would_misread():
+    import mla_latent_kv_15_gb300 as mla
+    q, kv, pe = bf16(6, 4, 192), bf16(9, 4, 256), bf16(9, 64)
+    cu = torch.tensor([0, 6], dtype=torch.int32)
+    ws = torch.empty(1024, dtype=torch.uint8)
+    good = dict(q=q, kv=kv, k_pe=pe, cu_q=cu, cu_kv=cu.clone(), out=bf16(6, 4, 128), workspace=ws, scale=0.07)
+
+    def call(**over):
+        mla.prefill(**dict(good, **over))
+
+    for text, over in (("q must have shape", dict(q=bf16(6, 4, 128))), ("q must be bfloat16", dict(q=torch.empty(6, 4, 192))),
+                       ("kv must have shape", dict(kv=bf16(9, 3, 256))), ("k_pe must have shape", dict(k_pe=bf16(8, 64))),
+                       ("multiples of 8", dict(q=bf16(6, 4, 196)[..., :192])),
+                       ("last dimension", dict(kv=bf16(9, 256, 4).transpose(1, 2))),
+                       ("cu_q must be int32", dict(cu_q=cu.long())), ("cu_kv must have shape", dict(cu_kv=torch.zeros(3, dtype=torch.int32))),
+                       ("cu_q must hold", dict(cu_q=torch.zeros(0, dtype=torch.int32))),
+                       ("out must have shape", dict(out=bf16(6, 4, 192))), ("out must be contiguous", dict(out=bf16(4, 6, 128).transpose(0, 1))),
+                       ("lse must be float32", dict(lse=bf16(6, 4))), ("CUDA tensor", dict())):
+        with pytest.raises(ValueError, match=text):
+            call(**over)

@@ -309,3 +309,18 @@ def test_prefill_without_rows_or_keys():
     mla.prefill(c.q, c.kv, c.k_pe, c.cu_q, c.cu_kv, c.out, c.ws, scale=SCALE)    # no LSE wanted
     torch.cuda.synchronize()
     assert (c.lse == 7.0).all() and not (c.out == 7.0).all()
+
+
+@pytest.mark.parametrize("q_lens,kv_lens,heads", [([300], [300], 2), ([700, 1], [900, 5000], 16), ([4000], [4000], 40)])
+def test_prefill_waits_are_bounded(q_lens, kv_lens, heads):
+    """Keys that never arrive: the waits for them run out, the call returns and
+    says so, and the next one is clean."""
+    c = Case(q_lens, kv_lens, heads, seed=22)
+    try:
+        mla.set_decode_wait_test(skip_first_tile=True, wait_limit_ns=2_000_000)
+        c.run()
+        torch.cuda.synchronize()
+        assert mla.prefill_status(c.ws) & mla.DEVERR_TIMEOUT
+    finally:
+        mla.set_decode_wait_test()
+    c.run().check()
