@@ -362,9 +362,13 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArg
     a.plan.header->num_pieces = min(carry, a.plan.max_pieces);
     a.plan.header->num_split = s_split;
     a.plan.header->fixed = fixed;
-    // Heads are taken in groups whose keys and values stay in L2, unless a long
-    // item of the last group would outlast the other pairs by much.
-    a.plan.header->group_heads = work < 16ull * longest * a.pairs ? a.num_heads : a.group_heads;
+    // Heads are taken in even groups whose keys and values stay in L2, but of at
+    // least twice the longest item's work for every pair, which the last group's
+    // long items would otherwise outlast.
+    const unsigned long long least = s_total ? (2ull * longest * a.pairs + s_total - 1) / s_total : 1;
+    const int group = (int)min((unsigned long long)a.num_heads, max(least, (unsigned long long)a.group_heads));
+    const int groups = a.num_heads / group;
+    a.plan.header->group_heads = (a.num_heads + groups - 1) / groups;
   }
 }
 
