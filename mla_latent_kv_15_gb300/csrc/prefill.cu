@@ -675,7 +675,7 @@ __device__ __forceinline__ void softmax_items(const PrefillArgs& a, const Ctx& c
     w0 *= inv, w1 *= inv;
     const int64_t at = (int64_t)(it.q0 + row) * a.num_heads + it.head;
     const int64_t part_at = (int64_t)it.prow + row;
-    float spoilt = 0.f;                             // NaN once an output of the row is not finite
+    float spoilt[4] = {0.f, 0.f, 0.f, 0.f};         // NaN once an output of the row is not finite
     if (live) {
       if (it.prow >= 0)
         a.plan.part_lse[part_at] = lse;
@@ -701,7 +701,7 @@ __device__ __forceinline__ void softmax_items(const PrefillArgs& a, const Ctx& c
           for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(fmaf(__uint_as_float(e[c]), w1, __uint_as_float(o[c])));
       }
 #pragma unroll
-      for (int c = 0; c < 32; ++c) spoilt = fmaf(__uint_as_float(o[c]), 0.f, spoilt);
+      for (int c = 0; c < 32; ++c) spoilt[c & 3] = fmaf(__uint_as_float(o[c]), 0.f, spoilt[c & 3]);
       if (live && it.prow >= 0) {
         float* dst = a.plan.part_o + part_at * kNope + 32 * g;
 #pragma unroll
@@ -729,7 +729,7 @@ __device__ __forceinline__ void softmax_items(const PrefillArgs& a, const Ctx& c
     if (a.causal) {
       // keys in the products of this tile that the row does not see
       const int covered = min(it.nkeys, (it.seen[t] + 15) & ~15);
-      const bool odd = live && !none && spoilt != 0.f && fabsf(lse) < INFINITY && sees < covered;
+      const bool odd = live && !none && (spoilt[0] + spoilt[1]) + (spoilt[2] + spoilt[3]) != 0.f && fabsf(lse) < INFINITY && sees < covered;
       for (unsigned rows = __ballot_sync(0xffffffffu, odd); rows; rows &= rows - 1) {
         const int src = __ffs(rows) - 1;
         const int64_t r_at = __shfl_sync(0xffffffffu, at, src), r_part = __shfl_sync(0xffffffffu, part_at, src);
