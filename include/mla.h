@@ -440,7 +440,8 @@ MLA_API int mla_gather_cache(const void* cache, int64_t num_blocks, int page_siz
  *   q_pe            bf16, 64 values of (t, h) at q_pe + t * q_token_stride +
  *                   h * q_head_stride, or NULL (then q_pe_out is NULL too)
  *   q_pe_out        the same with its own strides; may be q_pe itself (equal
- *                   strides: in place), else it overlaps no other argument
+ *                   strides: in place), else it overlaps no other argument (column
+ *                   ranges of the same rows do not overlap)
  *   status          one int32 on the device, or NULL: OR-ed into, never cleared
  * All strides are multiples of 8 elements, all tensors 16-byte aligned.
  * num_tokens in [0, 8388480]; 0 is a no-op.  One launch.
@@ -512,7 +513,7 @@ MLA_API size_t mla_prefill_workspace_size(int batch, int total_q, int num_heads,
  *               or MLA_DEVERR_BAD_SEQ_LEN (cu_kv) is set and nothing is written
  *   total_q, total_kv  rows of q and out, of kv and k_pe;  <= 2^30,
  *               total_q * num_heads < 2^31
- *   scale       finite and > 0
+ *   scale       > 0, finite (and so scale * log2 e)
  *   num_splits  0: long key ranges are split where that balances the SMs;
  *               k > 0: every block of query rows is cut into min(k, tiles) pieces
  *   out         [total_q, num_heads, 128] bf16, dense; overlaps no input

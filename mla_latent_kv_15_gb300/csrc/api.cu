@@ -484,16 +484,27 @@ int mla_proj_status(int* status, int clear, void* stream) {
 
 namespace {
 
-// [first byte, last byte + 1) of a strided tensor of `n0` x `n1` rows of
-// `width` elements (strides in elements).
+// Bytes [lo, hi) of a strided tensor of `n0` x `n1` rows of `width` elements
+// (strides in elements).  Where the outer stride holds all the inner rows,
+// the tensor is columns [0, row) of a pitched one.
 struct Extent {
   uintptr_t lo, hi;
+  uintptr_t row, pitch;
 };
 Extent extent(const void* p, int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t width, int64_t elem_bytes) {
   const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-  return Extent{lo, lo + (uintptr_t)(((n0 - 1) * s0 + (n1 - 1) * s1 + width) * elem_bytes)};
+  const uintptr_t row = (uintptr_t)(((n1 - 1) * s1 + width) * elem_bytes);
+  const uintptr_t pitch = (uintptr_t)(s0 * elem_bytes);
+  return Extent{lo, lo + (uintptr_t)((n0 - 1) * s0 * elem_bytes) + row, row, n0 > 1 && row <= pitch ? pitch : 0};
 }
-bool overlap(const Extent& a, const Extent& b) { return a.lo < b.hi && b.lo < a.hi; }
+// Whether two tensors may share bytes (column ranges of the same pitched
+// rows are told apart, other strided layouts by their first and last bytes).
+bool overlap(const Extent& a, const Extent& b) {
+  if (!(a.lo < b.hi && b.lo < a.hi)) return false;
+  if (a.pitch == 0 || a.pitch != b.pitch) return true;
+  const uintptr_t d = b.lo >= a.lo ? (b.lo - a.lo) % a.pitch : (a.pitch - (a.lo - b.lo) % a.pitch) % a.pitch;
+  return !(d >= a.row && d + b.row <= a.pitch);
+}
 
 constexpr int64_t kMaxStride = 1LL << 32;   // elements
 bool valid_stride(int64_t s, int64_t least) { return s >= least && s % 8 == 0 && s <= kMaxStride; }
@@ -620,7 +631,8 @@ int mla_prefill(const void* q, int64_t q_token_stride, int64_t q_head_stride, co
   if (batch < 0 || total_q < 0 || total_kv < 0)
     return fail(MLA_ERR_INVALID_ARG, "batch, total_q and total_kv must be >= 0");
   if (num_heads < 1 || num_heads > 1024) return fail(MLA_ERR_INVALID_ARG, "num_heads must be in [1, 1024]");
-  if (!std::isfinite(scale) || scale <= 0.f) return fail(MLA_ERR_INVALID_ARG, "scale must be finite and > 0");
+  if (!std::isfinite(scale * 1.4426950408889634f) || scale <= 0.f)
+    return fail(MLA_ERR_INVALID_ARG, "scale must be > 0 and scale * log2(e) finite");
   if (num_splits < 0 || num_splits > 4096) return fail(MLA_ERR_INVALID_ARG, "num_splits must be in [0, 4096]");
   if (batch == 0 || total_q == 0) return ok();
   if (total_kv > (1 << 30) || total_q > (1 << 30))

@@ -26,7 +26,7 @@ def test_rope_cache_write_refusals(lib):
              "ls q qts qhs N qo qots qohs status stream").split()
     good = dict(kv_c=at(1), kvs=576, k_pe=at(100), pes=64, weight=at(200), eps=1e-6, positions=at(201), table=at(300),
                 max_pos=100, pairs=1, slots=at(202), T=8, cache=at(400), nb=10, page=64, dtype=0, kv_scale=1.0,
-                latent=at(500), ls=576, q=at(600), qts=16 * 192, qhs=192, N=16, qo=at(700), qots=16 * 64, qohs=64,
+                latent=at(500), ls=576, q=at(600), qts=20 * 192, qhs=192, N=20, qo=at(700), qots=20 * 64, qohs=64,
                 status=at(203), stream=None)
 
     def refused(code, text, **over):
@@ -69,8 +69,16 @@ def test_rope_cache_write_refusals(lib):
     refused(-1, "latent must not overlap", latent=at(1), ls=576)          # k_pe is elsewhere: not the input rows
     refused(-1, "latent must not overlap", latent=at(1), k_pe=P((1 << 20) + 1024), pes=640, kvs=640, ls=576)
     refused(-1, "q_pe_out must be q_pe", qo=P((600 << 20) + 128))
-    refused(-1, "q_pe_out must be q_pe", qo=at(600), qots=16 * 64, qohs=64)  # other strides than q_pe's
+    refused(-1, "q_pe_out must be q_pe", qo=at(600), qots=20 * 64, qohs=64)  # other strides than q_pe's
     refused(-1, "q_pe_out must be q_pe", qo=at(400))
+    # column ranges of one fused projection's rows are apart: [q of 20 heads | kv_c | k_pe], rotated in place
+    base, pitch = 1 << 30, 20 * 192 + 576
+    fused = dict(kv_c=P(base + 2 * 20 * 192), kvs=pitch, k_pe=P(base + 2 * (20 * 192 + 512)), pes=pitch,
+                 q=P(base + 256), qts=pitch, qhs=192, qo=P(base + 256), qots=pitch, qohs=192, latent=None)
+    refused(-1, "q_pe_out must be q_pe", **dict(fused, k_pe=P(base + 2 * 20 * 192 - 16)))
+    refused(-2, "num_tokens", **dict(fused, T=8388481))      # (its own layout is accepted: only the size is refused)
+    from mla_latent_kv_15_gb300 import MLA_OK
+    assert lib.mla_rope_cache_write(*[dict(good, **dict(fused, T=0))[n] for n in names]) == MLA_OK
     # nothing to do
     assert lib.mla_rope_cache_write(*[dict(good, T=0, kv_c=None, cache=None, q=None, qo=None)[n] for n in names]) == 0
     assert lib.mla_last_error() == b""
@@ -116,7 +124,7 @@ def test_prefill_refusals(lib):
         refused(-1, ">= 0", **{name: -1})
     refused(-1, "num_heads", N=0)
     refused(-1, "num_heads", N=1025)
-    for bad in (0.0, -0.1, float("nan"), float("inf")):
+    for bad in (0.0, -0.1, float("nan"), float("inf"), 3e38):
         refused(-1, "scale", scale=bad)
     refused(-1, "num_splits", splits=-1)
     refused(-1, "num_splits", splits=4097)

@@ -219,3 +219,24 @@ def test_append_zero_tokens_and_captured_replay():
     assert torch.equal(c.cache.view(-1, DQK)[c.slots], cache.view(-1, DQK)[c.slots])
     ref = c.rows(True)
     near(f64(c.cache).reshape(-1, DQK)[c.slots.cpu().numpy()], ref, c.magnitude(ref), 2.0 ** -8)
+
+
+def test_append_from_one_fused_projection():
+    """Queries and latent rows as column ranges of the same rows, the query
+    rotated where it lies; nothing else of the rows changes."""
+    T, N = 37, 4
+    c = Case(T, N, 64, False, True, seed=12, wide=False)
+    fused = torch.empty(T, N * 192 + DQK, dtype=torch.bfloat16, device="cuda")
+    q = fused.as_strided((T, N, 192), (fused.stride(0), 192, 1))
+    q.copy_(c.q)
+    fused[:, N * 192:] = c.down
+    before = fused.clone()
+    want_q = torch.empty(T, N, ROPE, dtype=torch.bfloat16, device="cuda")
+    other = c.cache.clone()
+    mla.rope_cache_write(c.kv_c, c.k_pe, c.positions, c.table, c.slots, other, q_pe=c.q[..., 128:], q_pe_out=want_q,
+                         norm_weight=c.weight)
+    mla.rope_cache_write(fused[:, N * 192:N * 192 + LKV], fused[:, N * 192 + LKV:], c.positions, c.table, c.slots, c.cache,
+                         q_pe=q[..., 128:], q_pe_out=q[..., 128:], norm_weight=c.weight)
+    torch.cuda.synchronize()
+    assert torch.equal(c.cache, other) and torch.equal(q[..., 128:], want_q)
+    assert torch.equal(q[..., :128], c.q[..., :128]) and torch.equal(fused[:, N * 192:], before[:, N * 192:])
