@@ -516,7 +516,8 @@ MLA_API size_t mla_prefill_workspace_size(int batch, int total_q, int num_heads,
  *   scale       > 0, finite (and so scale * log2 e)
  *   num_splits  0: long key ranges are split where that balances the SMs;
  *               k > 0: every block of query rows is cut into min(k, tiles) pieces
- *   out         [total_q, num_heads, 128] bf16, dense; overlaps no input
+ *   out         [total_q, num_heads, 128] bf16, dense, 32-byte aligned; overlaps
+ *               no input
  *   lse         [total_q, num_heads] float32, or NULL
  *   workspace   >= mla_prefill_workspace_size(batch, total_q, num_heads,
  *               num_splits) bytes, 256-byte aligned; scratch only.  Calls that

@@ -641,8 +641,8 @@ int mla_prefill(const void* q, int64_t q_token_stride, int64_t q_head_stride, co
     return fail(MLA_ERR_INVALID_ARG, "total_q * num_heads must be below 2^31");
   if (!q || !cu_q || !cu_kv || !out || !workspace || (total_kv > 0 && (!kv || !k_pe)))
     return fail(MLA_ERR_INVALID_ARG, "null pointer argument");
-  if (!aligned(q, 16) || !aligned(kv, 16) || !aligned(k_pe, 16) || !aligned(out, 16))
-    return fail(MLA_ERR_INVALID_ARG, "q, kv, k_pe and out must be 16-byte aligned");
+  if (!aligned(q, 16) || !aligned(kv, 16) || !aligned(k_pe, 16) || !aligned(out, 32))
+    return fail(MLA_ERR_INVALID_ARG, "q, kv and k_pe must be 16-byte aligned, out 32-byte aligned");
   if (!aligned(cu_q, 4) || !aligned(cu_kv, 4) || !aligned(lse, 4))
     return fail(MLA_ERR_INVALID_ARG, "cu_q, cu_kv and lse must be 4-byte aligned");
   if (!aligned(workspace, 256)) return fail(MLA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");

@@ -41,7 +41,7 @@ constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpList = 10, kWarpClear = 11;
 constexpr int kItemSlots = 2;                     // items known ahead
 constexpr int kItemReaders = 2 * (kSoftmaxWarps + 2) + 2;   // both CTAs' softmax, load and clearing warps, the MMA warp, the peer's list warp
 constexpr int kThreads = 384;
-constexpr uint32_t kRegsSoftmax = 208, kRegsOther = 88;
+constexpr uint32_t kRegsSoftmax = 216, kRegsOther = 72;
 static_assert(128 * (2 * kRegsSoftmax + kRegsOther) <= kThreads * 168, "register split of the launch's 168 a thread");
 
 constexpr uint32_t kQChunk = 16384;               // 128 rows x 64 dims
@@ -591,7 +591,6 @@ __device__ __forceinline__ void softmax_items(const PrefillArgs& a, const Ctx& c
   const uint32_t s_col = tbase + lanes + kColS + 128 * t, o_col = tbase + lanes + kColO + 128 * t;
   const float scale = a.scale_log2;
   const uint32_t p_full = ctx.lead(&bars->p_full[t]);
-  const bool wide_out = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;   // 32-byte stores
   uint32_t items = 0, s_used = 0, o_used[2] = {0, 0}, handed = 0;
 
   while (true) {
@@ -711,14 +710,8 @@ __device__ __forceinline__ void softmax_items(const PrefillArgs& a, const Ctx& c
         uint32_t w[16];
 #pragma unroll
         for (int c = 0; c < 16; ++c) w[c] = pack_bf16x2(__uint_as_float(o[2 * c]), __uint_as_float(o[2 * c + 1]));
-        if (wide_out) {
-          st_global_32b(dst, w);
-          st_global_32b(dst + 16, w + 8);
-        } else {
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            reinterpret_cast<uint4*>(dst)[c] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
-        }
+        st_global_32b(dst, w);
+        st_global_32b(dst + 16, w + 8);
       }
       __syncwarp();
     }

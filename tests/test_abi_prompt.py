@@ -132,8 +132,8 @@ def test_prefill_refusals(lib):
     refused(-1, "2^31", T=1 << 30)
     for name in ("q", "kv", "pe", "cu_q", "cu_kv", "out", "ws"):
         refused(-1, "null", **{name: None})
-    for name in ("q", "kv", "pe", "out"):
-        refused(-1, "aligned", **{name: P(good[name].value + 8)})
+    for name, off in (("q", 8), ("kv", 8), ("pe", 8), ("out", 16)):
+        refused(-1, "aligned", **{name: P(good[name].value + off)})
     for name in ("cu_q", "cu_kv", "lse"):
         refused(-1, "aligned", **{name: P(good[name].value + 2)})
     refused(-1, "256-byte", ws=P(good["ws"].value + 128))
