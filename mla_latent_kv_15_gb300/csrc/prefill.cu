@@ -69,6 +69,7 @@ struct Bars {
   uint64_t item_empty[kItemSlots];                // (lead)
   uint32_t tmem_base;
   int abort;
+  int mending;                                    // warps of the pair that compute rows again (mend_row)
 };
 constexpr size_t kSmem = 1024 + 2 * kQTile + kStages * kStage + sizeof(Bars) + 16 + kItemSlots * 48 + 128 * 8;
 static_assert(kSmem <= 232448, "shared memory per CTA");
@@ -83,16 +84,18 @@ struct Ctx {
 };
 
 // Bounded waits; once one has run out, every other one of the CTA returns, and
-// the peer's run out in turn.  kCluster: the acquire covers what the other CTA
+// the peer's run out in turn.  The time in which rows are mended, which ends by
+// itself but may be long, does not count.  kCluster: the acquire covers what the other CTA
 // has written to shared memory.  Waits for an item may last as long as the
 // item before it (`times` the limit).
 template <bool kCluster = false>
 __device__ __forceinline__ void wait_bar(const Ctx& c, uint64_t* bar, uint32_t parity, uint32_t times = 1) {
   const uint32_t at = smem_u32(bar);
   if (kCluster ? mbar_try_wait_cluster(at, parity) : mbar_try_wait(at, parity)) return;
-  const uint64_t t0 = globaltimer();
+  uint64_t t0 = globaltimer();
   while (!(kCluster ? mbar_try_wait_cluster_hint(at, parity, kWaitHintNs) : mbar_try_wait_hint(at, parity, kWaitHintNs))) {
     if (*(volatile int*)&c.bars->abort) return;
+    if (*(volatile int*)&c.bars->mending) t0 = globaltimer();
     if (globaltimer() - t0 > c.limit_ns * times) {
       *(volatile int*)&c.bars->abort = 1;
       atomicOr(c.status, 1);   // MLA_DEVERR_TIMEOUT
@@ -101,6 +104,16 @@ __device__ __forceinline__ void wait_bar(const Ctx& c, uint64_t* bar, uint32_t p
   }
 }
 constexpr uint32_t kItemWait = 64;
+
+// The pair's count of warps that mend rows, kept in both CTAs.
+__device__ __noinline__ void count_mending(const Ctx& c, int lane, int step) {
+  __syncwarp();
+  if (lane < 2)
+    asm volatile("red.relaxed.cluster.shared::cluster.add.s32 [%0], %1;" ::"r"(mapa(smem_u32(&c.bars->mending), lane)),
+                 "r"(step)
+                 : "memory");
+  __syncwarp();
+}
 
 struct __align__(16) Item {
   int q0, nq, kv0, nkeys, lim0, prow, head;
@@ -460,6 +473,22 @@ __device__ __forceinline__ void issue_items(const Ctx& ctx, const Item* slots, u
   __syncwarp();
 }
 
+__device__ __forceinline__ void values4(const __nv_bfloat16* at, float (&x)[4]) {
+  const uint2 v = *reinterpret_cast<const uint2*>(at);
+  x[0] = __uint_as_float(v.x << 16), x[1] = __uint_as_float(v.x & 0xffff0000u);
+  x[2] = __uint_as_float(v.y << 16), x[3] = __uint_as_float(v.y & 0xffff0000u);
+}
+__device__ __forceinline__ float dot8(const __nv_bfloat16* a, const __nv_bfloat16* b, float s) {
+  const uint4 x = *reinterpret_cast<const uint4*>(a), y = *reinterpret_cast<const uint4*>(b);
+  const uint32_t u[4] = {x.x, x.y, x.z, x.w}, v[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    s = fmaf(__uint_as_float(u[i] << 16), __uint_as_float(v[i] << 16), s);
+    s = fmaf(__uint_as_float(u[i] & 0xffff0000u), __uint_as_float(v[i] & 0xffff0000u), s);
+  }
+  return s;
+}
+
 // A row whose output came out not finite although its sum is: a key that the
 // row does not see, but rows beside it do, may hold a value that is not finite
 // (0 * inf in the matrix product).  If one of the masked keys [sees, covered)
@@ -471,10 +500,11 @@ __device__ __noinline__ void mend_row(const PrefillArgs& a, int row, int head, i
   const int lane = threadIdx.x & 31;
   const __nv_bfloat16* kv = static_cast<const __nv_bfloat16*>(a.kv) + (int64_t)head * a.kv_head_stride;
   bool found = false;
-#pragma unroll 1
+#pragma unroll 4
   for (int j = sees; j < covered; ++j) {
-    const __nv_bfloat16* v = kv + (int64_t)(kv0 + j) * a.kv_token_stride + kNope + 4 * lane;
-    for (int e = 0; e < 4; ++e) found |= !(fabsf(__bfloat162float(v[e])) < INFINITY);
+    float v[4];
+    values4(kv + (int64_t)(kv0 + j) * a.kv_token_stride + kNope + 4 * lane, v);
+    for (int e = 0; e < 4; ++e) found |= !(fabsf(v[e]) < INFINITY);
   }
   if (!__any_sync(0xffffffffu, found)) return;
   const __nv_bfloat16* q =
@@ -488,18 +518,19 @@ __device__ __noinline__ void mend_row(const PrefillArgs& a, int row, int head, i
       const __nv_bfloat16* k = kv + (int64_t)(kv0 + j0 + lane) * a.kv_token_stride;
       const __nv_bfloat16* r = pe + (int64_t)(kv0 + j0 + lane) * a.k_pe_stride;
       float s = 0.f;
-#pragma unroll 4
-      for (int d = 0; d < kNope; ++d) s = fmaf(__bfloat162float(q[d]), __bfloat162float(k[d]), s);
-#pragma unroll 4
-      for (int d = 0; d < 64; ++d) s = fmaf(__bfloat162float(q[kNope + d]), __bfloat162float(r[d]), s);
+#pragma unroll 8
+      for (int d = 0; d < kNope; d += 8) s = dot8(q + d, k + d, s);
+#pragma unroll
+      for (int d = 0; d < 64; d += 8) s = dot8(q + kNope + d, r + d, s);
       p = fast_exp2(fmaf(s, a.scale_log2, -ref));
     }
     const int n = min(32, sees - j0);
-#pragma unroll 1
+#pragma unroll 8
     for (int j = 0; j < n; ++j) {
       const float pj = __shfl_sync(0xffffffffu, p, j);
-      const __nv_bfloat16* v = kv + (int64_t)(kv0 + j0 + j) * a.kv_token_stride + kNope + 4 * lane;
-      for (int e = 0; e < 4; ++e) o[e] = fmaf(pj, __bfloat162float(v[e]), o[e]);
+      float v[4];
+      values4(kv + (int64_t)(kv0 + j0 + j) * a.kv_token_stride + kNope + 4 * lane, v);
+      for (int e = 0; e < 4; ++e) o[e] = fmaf(pj, v[e], o[e]);
     }
   }
   for (int e = 0; e < 4; ++e) {
@@ -723,7 +754,9 @@ __device__ __forceinline__ void softmax_items(const PrefillArgs& a, const Ctx& c
       // keys in the products of this tile that the row does not see
       const int covered = min(it.nkeys, (it.seen[t] + 15) & ~15);
       const bool odd = live && !none && (spoilt[0] + spoilt[1]) + (spoilt[2] + spoilt[3]) != 0.f && fabsf(lse) < INFINITY && sees < covered;
-      for (unsigned rows = __ballot_sync(0xffffffffu, odd); rows; rows &= rows - 1) {
+      const unsigned odd_rows = __ballot_sync(0xffffffffu, odd);
+      if (odd_rows) count_mending(ctx, lane, 1);
+      for (unsigned rows = odd_rows; rows; rows &= rows - 1) {
         const int src = __ffs(rows) - 1;
         const int64_t r_at = __shfl_sync(0xffffffffu, at, src), r_part = __shfl_sync(0xffffffffu, part_at, src);
         mend_row(a, it.q0 + row - lane + src, it.head, it.kv0, __shfl_sync(0xffffffffu, sees, src), covered,
@@ -731,6 +764,7 @@ __device__ __forceinline__ void softmax_items(const PrefillArgs& a, const Ctx& c
                  it.prow >= 0 ? a.plan.part_o + r_part * kNope : nullptr,
                  static_cast<__nv_bfloat16*>(a.out) + r_at * kNope);
       }
+      if (odd_rows) count_mending(ctx, lane, -1);
     }
     tc_fence_before();   // the next item's products may overwrite O once this warp has handed over its P
   }
@@ -773,6 +807,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     mbar_init(smem_u32(&bars->drain), 1);
     bars->abort = 0;
+    bars->mending = 0;
     fence_mbar_init();
   }
   if (warp == kWarpMma) {

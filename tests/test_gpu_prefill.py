@@ -324,3 +324,27 @@ def test_prefill_waits_are_bounded(q_lens, kv_lens, heads):
     finally:
         mla.set_decode_wait_test()
     c.run().check()
+
+
+def test_prefill_mending_rows_outlasts_the_wait_limit():
+    """An infinity that only the last row sees: the rows beside it are computed
+    again over 16000 keys, which takes longer than the waits' limit set here;
+    the time does not count as a wait that ran out."""
+    heads, keys = 170, 16000
+    c = Case([300], [keys], heads, seed=31, splits=1)
+    clean = c.kv.clone()
+    c.kv[keys - 1, :, 128] = float("inf")
+    try:
+        mla.set_decode_wait_test(wait_limit_ns=2_000_000)
+        c.run()
+        torch.cuda.synchronize()
+        assert mla.prefill_status(c.ws) == 0
+    finally:
+        mla.set_decode_wait_test()
+    assert (c.out[299, :, 0] == float("inf")).all()
+    c.out[299, :, 0] = 0
+    assert torch.isfinite(c.out).all()
+    for h in (0, 80, 169):
+        ref, lse, mag = prompt_ref.prefill_torch(c.q[:, h:h + 1], clean[:, h:h + 1], c.k_pe, c.at_q, c.at_kv, SCALE, True)
+        err = (c.out[:299, h:h + 1].double() - ref[:299]).abs()
+        assert (err <= 2.0 ** -8 * ref[:299].abs() + (2.0 ** -8 + 6.6e-4 + 2.0 ** -18) * mag[:299]).all()
