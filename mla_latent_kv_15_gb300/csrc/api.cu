@@ -657,7 +657,7 @@ int mla_prefill(const void* q, int64_t q_token_stride, int64_t q_head_stride, co
     return fail(MLA_ERR_INVALID_ARG, "out must not overlap the inputs");
   const mla::PrefillLayout L = mla::prefill_layout(batch, total_q, num_heads, num_splits);
   if (L.max_part_rows >= 1LL << 31) return fail(MLA_ERR_UNSUPPORTED, "total_q * num_heads * num_splits must be below 2^31");
-  if ((int64_t)L.max_pieces * num_heads >= (1LL << 31) - 4096)
+  if (L.max_pieces * num_heads >= (1LL << 31) - 4096)
     return fail(MLA_ERR_UNSUPPORTED, "batch * num_heads is too large");
   if (workspace_bytes < L.total)
     return fail(MLA_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu required", workspace_bytes, L.total);

@@ -62,8 +62,7 @@ struct PrefillPlan {
 
 struct PrefillLayout {
   size_t first_block, first_piece, pieces, splits, part_o, part_lse, total;
-  int max_blocks, max_pieces;
-  long long max_part_rows;
+  long long max_pieces, max_part_rows;
 };
 
 // A fixed plan is made for fewer items (blocks x heads) than this many a pair.
@@ -78,8 +77,7 @@ inline PrefillLayout prefill_layout(int batch, int total_q, int num_heads, int m
   const long long auto_rows = 2LL * kPrefillMaxPairs * (total_q < kPrefillRows ? total_q : kPrefillRows);
   const long long forced_rows = max_splits > 1 ? (long long)total_q * max_splits * num_heads : 0;
   const long long mp = mb * (max_splits > 1 ? max_splits : 1) + (kPrefillFixedItems + 2) * kPrefillMaxPairs;
-  L.max_blocks = (int)mb;
-  L.max_pieces = (int)mp;
+  L.max_pieces = mp;
   L.max_part_rows = auto_rows > forced_rows ? auto_rows : forced_rows;
   size_t off = up(sizeof(PrefillHeader));
   L.first_block = off;  off = up(off + sizeof(int) * ((size_t)batch + 1));
@@ -101,7 +99,7 @@ inline PrefillPlan prefill_plan_from(void* ws, const PrefillLayout& L) {
                      reinterpret_cast<PrefillSplit*>(p + L.splits),
                      reinterpret_cast<float*>(p + L.part_o),
                      reinterpret_cast<float*>(p + L.part_lse),
-                     L.max_pieces,
+                     (int)L.max_pieces,
                      (int)L.max_part_rows};
 }
 

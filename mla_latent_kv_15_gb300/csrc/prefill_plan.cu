@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArg
   const unsigned long long work = s_total * a.num_heads;
   longest = s_longest;
 
-  const bool fixed = a.num_splits == 0 && longest > kMinChunk &&
+  const bool fixed = a.num_splits == 0 && longest > kMinChunk && s_total < (1ull << 30) &&
                      (long long)nblocks * a.num_heads < (long long)kPrefillFixedItems * a.pairs;
   if (fixed) {
     // fixed plan: head h's block b lies at h * all + s_before[b]
@@ -215,7 +215,6 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArg
       if (b < nblocks) s_before[b] = all + before;
       all += total;
     }
-#pragma unroll 1
     const long long length = (long long)all * a.num_heads;
     // pairs in use: no more pieces than leave each about kMinChunk units
     const int used = (int)min((long long)a.pairs, max((long long)items, length / (kItemUnits + kMinChunk)));
@@ -280,7 +279,7 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArg
     if (tid <= kPrefillMaxPairs) a.plan.first_piece[tid] = before;
     carry = listed;
   } else {
-    const int chunk = max((int)min((work + a.pairs - 1) / a.pairs, 1ull << 30), kMinChunk);
+    const int chunk = max((int)min((work + a.pairs - 1) / a.pairs, 1ull << 28), kMinChunk);
     const bool cut = a.num_splits == 0 && 2 * longest > 3 * chunk;
     auto pieces_of = [&](const BlockOf& b) {
       if (a.num_splits > 0) return max(1, min(a.num_splits, b.tiles));
