@@ -193,9 +193,9 @@ struct RopeWriteArgs {
 };
 
 // Tiles of mla_kv_up_proj for a shape: token and weight rows of a load box;
-// columns of a CTA's tile (bn) or of a CTA pair's (pair_bn, 0: single CTAs).
+// columns of a CTA pair's tile (pair_bn, 0: single CTAs, 128 columns each).
 struct KvProjShape {
-  int bn, xrows, wrows;
+  int xrows, wrows;
   int pair_bn, pairs;
 };
 

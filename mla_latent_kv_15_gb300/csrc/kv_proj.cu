@@ -6,7 +6,7 @@
 // accumulation in tensor memory, one rounding to bf16.
 //
 // Few tokens (kv_proj_kernel): the weights are the traffic.  One CTA computes
-// a 128-token x bn-column tile; its ring holds as much of the 512-deep
+// a 128-token x 128-column tile; its ring holds as much of the 512-deep
 // contraction as the shared memory of half an SM does, so nearly every load
 // of a CTA is in flight at once.  With fewer than 128 tokens the token box
 // holds only round_up(T, 16) rows; the MMA rows past it read other bytes of
@@ -32,6 +32,7 @@ namespace {
 using namespace ptx;
 
 constexpr int kM = 128;                          // tokens per CTA (MMA M)
+constexpr int kFewCols = 128;                    // columns of a tile of kv_proj_kernel
 constexpr int kK = 64;                           // contraction dims per stage: one 128-byte swizzled row
 constexpr int kChunks = kLkv / kK;               // 8
 constexpr int kThreads = 192;                    // TMA warp, MMA warp, 4 epilogue warps
@@ -68,15 +69,15 @@ __device__ __forceinline__ void store_cols32(__nv_bfloat16* dst, const uint32_t 
 
 __global__ void __launch_bounds__(kThreads, 1)
     kv_proj_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
-                   __nv_bfloat16* __restrict__ y, int64_t T, int64_t C, int bn, int stages, int xrows) {
+                   __nv_bfloat16* __restrict__ y, int64_t T, int64_t C, int stages, int xrows) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const uint32_t xbox = (uint32_t)xrows * kK * 2, wbox = (uint32_t)bn * kK * 2;
+  constexpr uint32_t wbox = kFewCols * kK * 2;
+  const uint32_t xbox = (uint32_t)xrows * kK * 2;
   const uint32_t stage_bytes = xbox + wbox;
   Bars* bars = reinterpret_cast<Bars*>(smem + stages * stage_bytes + (kXBoxMax - xbox));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int c0 = blockIdx.x * bn, t0 = blockIdx.y * kM;
-  const uint32_t tcols = bn <= 64 ? 64 : bn <= 128 ? 128 : 256;
+  const int c0 = blockIdx.x * kFewCols, t0 = blockIdx.y * kM;
   const int npre = stages < kChunks ? stages : kChunks;
 
   if (threadIdx.x == 0) {
@@ -100,7 +101,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(&bars->tmem_base), tcols);
+    tmem_alloc(smem_u32(&bars->tmem_base), kFewCols);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -131,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!mbar_wait(smem_u32(&bars->full[c % stages]), (c / stages) & 1)) give_up(bars);
     }
   } else if (warp == 1) {
-    const uint32_t idesc = idesc_bf16_f32(kM, bn, 0, 0);
+    const uint32_t idesc = idesc_bf16_f32(kM, kFewCols, 0, 0);
     for (int c = 0; c < kChunks; ++c) {
       const int slot = c % stages;
       if (!mbar_wait(smem_u32(&bars->full[slot]), (c / stages) & 1)) {
@@ -162,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     if (done && !*abort_flag) {
       __nv_bfloat16* dst = y + t * C + c0;
-      for (int j = 0; j < bn; j += 32) {
+      for (int j = 0; j < kFewCols; j += 32) {
         uint32_t r[32];
         tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + j, r);
         tmem_wait_ld();
@@ -174,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, tcols);
+    tmem_dealloc(tmem, kFewCols);
   }
 }
 
@@ -404,10 +405,11 @@ cudaError_t launch_pair(const CUtensorMap& tm_x, const CUtensorMap& tm_w, const 
 }  // namespace
 
 // Up to 128 tokens a single CTA's tile holds them all and the weights' traffic
-// wants many CTAs (128 tokens x 32768 columns: 17.6 us, pairs 19.6).  Above,
+// wants many CTAs (128 tokens x 32768 columns: 17.6 us, pairs 19.6; tiles of
+// 32, 64 or 256 columns gain nothing).  Above,
 // pairs: 256 columns a tile where that costs no more rounds of all pairs than
 // 128, which run 15 % below the wider tile's rate (8192 tokens x 32768 columns:
-// 181 us against 216; 1021 x 5120: two rounds against three of half the size,
+// 173 us against 216; 1021 x 5120: two rounds against three of half the size,
 // 17.5 us against 15.5).  Times include about 8 us of a graph's launch.
 KvProjShape kv_proj_shape(int64_t T, int64_t C, int sms) {
   KvProjShape p{};
@@ -418,7 +420,7 @@ KvProjShape kv_proj_shape(int64_t T, int64_t C, int sms) {
     p.wrows = p.pair_bn / 2;
     p.xrows = kM;
   } else {
-    p.bn = p.wrows = 128;
+    p.wrows = kFewCols;
     p.xrows = T >= kM ? kM : (int)((T + 15) / 16 * 16);
   }
   return p;
@@ -428,20 +430,19 @@ cudaError_t launch_kv_proj(const CUtensorMap& tm_x, const CUtensorMap& tm_w, con
                            int64_t T, int64_t C, const KvProjShape& p, cudaStream_t s) {
   if (p.pair_bn == 256) return launch_pair<256>(tm_x, tm_w, tm_y, T, C, p.pairs, s);
   if (p.pair_bn == 128) return launch_pair<128>(tm_x, tm_w, tm_y, T, C, p.pairs, s);
-  const uint32_t xbox = (uint32_t)p.xrows * kK * 2, stage = xbox + (uint32_t)p.bn * kK * 2;
+  const uint32_t xbox = (uint32_t)p.xrows * kK * 2, stage = xbox + kFewCols * kK * 2;
   int stages = (int)(kRingBudget / stage);
   if (stages > kChunks) stages = kChunks;
   size_t smem = 1024 + (size_t)stages * stage + (kXBoxMax - xbox) + sizeof(Bars);
   // never more CTAs on an SM than its 512 tensor-memory columns hold (an
   // allocation beyond them would wait for another CTA to finish)
-  const uint32_t tcols = p.bn <= 64 ? 64 : p.bn <= 128 ? 128 : 256;
-  const size_t floor_smem = kSmemPerSm / (512 / tcols + 1);
+  constexpr size_t floor_smem = kSmemPerSm / (512 / kFewCols + 1);
   if (smem < floor_smem) smem = floor_smem;
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_smem(kv_proj_kernel, 1024 + kRingBudget + kXBoxMax + sizeof(Bars) + 1024, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((C + p.bn - 1) / p.bn), (unsigned)((T + kM - 1) / kM));
+  cfg.gridDim = dim3((unsigned)((C + kFewCols - 1) / kFewCols), (unsigned)((T + kM - 1) / kM));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -450,7 +451,7 @@ cudaError_t launch_kv_proj(const CUtensorMap& tm_x, const CUtensorMap& tm_w, con
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kv_proj_kernel, tm_x, tm_w, static_cast<__nv_bfloat16*>(y), T, C, p.bn, stages,
+  e = cudaLaunchKernelEx(&cfg, kv_proj_kernel, tm_x, tm_w, static_cast<__nv_bfloat16*>(y), T, C, stages,
                          p.xrows);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
