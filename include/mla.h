@@ -525,9 +525,10 @@ MLA_API size_t mla_prefill_workspace_size(int batch, int total_q, int num_heads,
  * A value that is not finite makes the rows that see its key not finite; in
  * keys a row does not see it has no effect on the row.
  * batch == 0 or total_q == 0 is a no-op.  Three launches (plan, attention,
- * join), or the attention alone for up to 32 sequences over up to 512 key rows;
- * nothing of them depends on device data, so a captured call may be replayed
- * over other lengths.
+ * join); for up to 32 sequences the attention alone over up to 512 key rows,
+ * and no plan where total_q / 512 + batch blocks times heads are few.  Nothing of
+ * this depends on device data, so a captured call may be replayed over other
+ * lengths.
  */
 MLA_API int mla_prefill(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* kv,
                         int64_t kv_token_stride, int64_t kv_head_stride, const void* k_pe, int64_t k_pe_stride,

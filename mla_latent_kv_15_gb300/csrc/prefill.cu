@@ -186,63 +186,166 @@ __device__ __forceinline__ Item item_direct(const PrefillArgs& a, const int4 seq
   return it;
 }
 
-// The leading CTA's list warp hands the pair's items to both CTAs.  In a
-// fixed plan they are the pair's range of pieces, without a plan every
-// pairs-th item; else the first is the pair's own and the next come from a
-// counter all pairs share, so that a pair done early takes more.
-__device__ __forceinline__ void list_items(const PrefillArgs& a, const Ctx& ctx, Item* slots, int lane) {
+// A pair's span of all items laid end to end (head after head, `all` units
+// each; lane b: sequence b's units and those before it).
+struct Span {
+  long long from, to;     // [from, to)
+  long long at;           // where item (head, sequence src, row r0) begins
+  int head, src, r0;
+};
+
+__device__ __forceinline__ PrefillBlock span_block(const PrefillArgs& a, const int4 seq, const Span& p) {
+  return prefill_block(__shfl_sync(0xffffffffu, seq.x, p.src), __shfl_sync(0xffffffffu, seq.y, p.src),
+                       __shfl_sync(0xffffffffu, seq.z, p.src), __shfl_sync(0xffffffffu, seq.w, p.src), p.r0, a.causal);
+}
+// Behind the item of `cost` units at p.at.
+__device__ __forceinline__ void span_advance(Span& p, int cost, int rows, unsigned filled) {
+  p.at += kPrefillItemUnits + cost;
+  p.r0 += kPrefillRows;
+  if (p.r0 < rows) return;
+  p.r0 = 0;
+  const unsigned later = p.src == 31 ? 0 : filled & ~((2u << p.src) - 1);
+  p.head += later == 0;
+  p.src = __ffs(later ? later : filled) - 1;
+}
+// The span's next piece, by the whole warp; behind its end, it.last.  The
+// first piece of an item that ends in another span is noted for the join.
+__device__ __forceinline__ void span_next(const PrefillArgs& a, const int4 seq, Span& p, unsigned filled, long long length,
+                                       int used, int pair, Item& it) {
+  it.last = 1;
+  while (p.at < p.to && it.last) {
+    const PrefillBlock b = span_block(a, seq, p);
+    const int tiles = b.tiles(), unit = b.unit(), rows = __shfl_sync(0xffffffffu, seq.y, p.src);
+    const long long end = p.at + kPrefillItemUnits + b.cost();
+    const int t0 = prefill_tiles_before(p.from, p.at, unit, tiles);
+    const int t1 = end <= p.to ? tiles : prefill_tiles_before(p.to, p.at, unit, tiles);
+    if (t1 > t0 || (end <= p.to && tiles == 0)) {
+      it.q0 = b.q0, it.nq = b.nq, it.kv0 = b.kv0 + t0 * kPrefillTile, it.lim0 = b.lim0 - t0 * kPrefillTile;
+      it.nkeys = min(t1 * kPrefillTile, b.nkeys) - t0 * kPrefillTile;
+      it.head = p.head;
+      const int own = 2 * pair + (t0 == 0), first = prefill_span_rows(a.total_q) * own;
+      it.prow = t0 == 0 && t1 == tiles ? -1 : first;
+      if (t0 == 0 && t1 < tiles && (threadIdx.x & 31) == 0) {
+        PrefillSplit sp{};
+        sp.q0 = b.q0, sp.nq = b.nq, sp.head0 = p.head, sp.heads = 1, sp.prow = first;
+        sp.stride = 2 * prefill_span_rows(a.total_q);
+        // up to the first span that ends at `end` or behind it; no span between is without a tile
+        // (a span is at least as long as an empty item, 3 units, a tile 2)
+        sp.pieces = (int)((end * used + length - 1) / length) - pair;
+        a.plan.splits[pair] = sp;
+      }
+      finish_item(a, it);
+    }
+    span_advance(p, b.cost(), rows, filled);
+  }
+}
+
+// The leading CTA's list warp hands the pair's item number n to both CTAs.
+// Returns whether it was the last (a last one tells the peer of an abort, too).
+__device__ __forceinline__ bool hand_item(const Ctx& ctx, Item* slots, int lane, uint32_t n, Item& it) {
   Bars* bars = ctx.bars;
+  const uint32_t slot = n % kItemSlots;
+  wait_bar(ctx, &bars->item_empty[slot], ((n / kItemSlots) & 1) ^ 1, kItemWait);
+  if (lane == 0) {
+    if (*(volatile int*)&bars->abort) it.last = 1;
+    slots[slot] = it;
+    mbar_arrive(smem_u32(&bars->item_full[slot]));
+    const uint32_t far = mapa(smem_u32(&slots[slot]), 1), far_bar = mapa(smem_u32(&bars->item_full[slot]), 1);
+    st_async_v4(far, it.q0, it.nq, it.kv0, it.nkeys, far_bar);
+    st_async_v4(far + 16, it.lim0, it.prow, it.head, it.seen[0], far_bar);
+    st_async_v4(far + 32, it.seen[1], it.tiles[0], it.tiles[1], it.last, far_bar);
+  }
+  return __shfl_sync(0xffffffffu, it.last, 0) != 0;
+}
+
+// The items of a plan: in a fixed one they are the pair's range of pieces, else
+// the first is the pair's own and the next come from a counter all pairs
+// share, so that a pair done early takes more.
+__device__ __forceinline__ void list_plan(const PrefillArgs& a, const Ctx& ctx, Item* slots, int lane) {
   PrefillHeader* head = a.plan.header;
   const int pairs = gridDim.x / 2, pair = cluster_id_x();
-  int np = 0, group = 1, items, i = pair;
-  bool fixed = false;
-  int4 seq = make_int4(0, 0, 0, 0);
-  int before = 0, blocks = 0;
-  if (a.direct) {
-    int bad = 0;
-    if (lane < a.batch) {
-      const int q0 = a.cu_q[lane], q1 = a.cu_q[lane + 1], k0 = a.cu_kv[lane], k1 = a.cu_kv[lane + 1];
-      if (q0 < 0 || q1 < q0 || q1 > a.total_q) bad |= 8;     // MLA_DEVERR_BAD_QSL
-      if (k0 < 0 || k1 < k0 || k1 > a.total_kv) bad |= 2;    // MLA_DEVERR_BAD_SEQ_LEN
-      seq = make_int4(q0, q1 - q0, k0, k1 - k0);
-      blocks = bad & 8 ? 0 : (q1 - q0 + kPrefillRows - 1) / kPrefillRows;
-    }
-    int incl = blocks;
-#pragma unroll 1
-    for (int o = 1; o < 32; o <<= 1) {
-      const int n = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += n;
-      bad |= __shfl_xor_sync(0xffffffffu, bad, o);
-    }
-    before = incl - blocks;
-    items = bad ? 0 : __shfl_sync(0xffffffffu, incl, 31) * a.num_heads;
-    if (pair == 0 && lane == 0) head->status = bad;
-  } else {
-    np = head->num_pieces;
-    group = head->group_heads;
-    fixed = head->fixed != 0;
-    items = fixed ? a.plan.first_piece[pair + 1] : np * a.num_heads;
-    if (fixed) i = a.plan.first_piece[pair];
-  }
+  const int np = head->num_pieces, group = head->group_heads;
+  const bool fixed = head->fixed != 0;
+  const int items = fixed ? a.plan.first_piece[pair + 1] : np * a.num_heads;
+  int i = fixed ? a.plan.first_piece[pair] : pair;
   for (uint32_t n = 0;; ++n) {
-    const uint32_t slot = n % kItemSlots;
     Item it{};
     it.last = 1;
-    if (i < items) it = a.direct ? item_direct(a, seq, before, blocks, i) : item_at(a, np, group, fixed, i);
-    wait_bar(ctx, &bars->item_empty[slot], ((n / kItemSlots) & 1) ^ 1, kItemWait);
+    if (i < items) it = item_at(a, np, group, fixed, i);
+    if (hand_item(ctx, slots, lane, n, it)) break;
     int next = 0;
-    if (lane == 0) {
-      if (*(volatile int*)&bars->abort) it.last = 1;    // the peer is told
-      slots[slot] = it;
-      mbar_arrive(smem_u32(&bars->item_full[slot]));
-      const uint32_t far = mapa(smem_u32(&slots[slot]), 1), far_bar = mapa(smem_u32(&bars->item_full[slot]), 1);
-      st_async_v4(far, it.q0, it.nq, it.kv0, it.nkeys, far_bar);
-      st_async_v4(far + 16, it.lim0, it.prow, it.head, it.seen[0], far_bar);
-      st_async_v4(far + 32, it.seen[1], it.tiles[0], it.tiles[1], it.last, far_bar);
-      if (!it.last && !fixed && !a.direct) next = atomicAdd(&head->next, 1);
+    if (lane == 0 && !fixed) next = atomicAdd(&head->next, 1);
+    i = fixed ? i + 1 : pairs + __shfl_sync(0xffffffffu, next, 0);
+  }
+}
+
+// The items without a plan: the pair's span of all items, or, where none is
+// long, every pairs-th.
+__device__ __noinline__ void list_direct(const PrefillArgs& a, const Ctx& ctx, Item* slots, int lane) {
+  const int pairs = gridDim.x / 2, pair = cluster_id_x();
+  int4 seq = make_int4(0, 0, 0, 0);
+  int blocks = 0, bad = 0;
+  if (lane < a.batch) {
+    const int q0 = a.cu_q[lane], q1 = a.cu_q[lane + 1], k0 = a.cu_kv[lane], k1 = a.cu_kv[lane + 1];
+    if (q0 < 0 || q1 < q0 || q1 > a.total_q) bad |= 8;     // MLA_DEVERR_BAD_QSL
+    if (k0 < 0 || k1 < k0 || k1 > a.total_kv) bad |= 2;    // MLA_DEVERR_BAD_SEQ_LEN
+    seq = make_int4(q0, q1 - q0, k0, k1 - k0);
+    blocks = bad ? 0 : (q1 - q0 + kPrefillRows - 1) / kPrefillRows;
+  }
+  int units = 0, longest = 0;
+  if (a.spans) {
+#pragma unroll 1
+    for (int b = 0; b < blocks; ++b) {
+      const int c = prefill_block(seq.x, seq.y, seq.z, seq.w, b * kPrefillRows, a.causal).cost();
+      units += c + kPrefillItemUnits;
+      longest = max(longest, c);
     }
-    if (__shfl_sync(0xffffffffu, it.last, 0)) break;
-    i = fixed ? i + 1 : pairs + (a.direct ? i : __shfl_sync(0xffffffffu, next, 0));
+    if (lane == 0) a.plan.splits[pair].pieces = 0;
+  }
+  int incl = blocks, uincl = units;
+#pragma unroll 1
+  for (int o = 1; o < 32; o <<= 1) {
+    const int n = __shfl_up_sync(0xffffffffu, incl, o), u = __shfl_up_sync(0xffffffffu, uincl, o);
+    if (lane >= o) incl += n, uincl += u;
+    bad |= __shfl_xor_sync(0xffffffffu, bad, o);
+    longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
+  }
+  const int before = incl - blocks, items = bad ? 0 : __shfl_sync(0xffffffffu, incl, 31) * a.num_heads;
+  if (pair == 0 && lane == 0) a.plan.header->status = bad;
+
+  const bool spans = longest > kPrefillMinChunk && items > 0;
+  const unsigned filled = __ballot_sync(0xffffffffu, blocks > 0);
+  Span span{};
+  long long length = 0;
+  int used = 1;
+  if (spans) {
+    const int all = __shfl_sync(0xffffffffu, uincl, 31);
+    length = (long long)all * a.num_heads;
+    used = prefill_spans(length, items, pairs);
+    span.from = length * min(pair, used) / used;
+    span.to = length * min(pair + 1, used) / used;
+    span.at = length;
+    if (span.from < length) {
+      span.head = (int)(span.from / all);
+      const int rem = (int)(span.from - (long long)span.head * all);
+      span.src = __ffs(__ballot_sync(0xffffffffu, rem >= uincl - units && rem < uincl)) - 1;
+      span.at = (long long)span.head * all + __shfl_sync(0xffffffffu, uincl - units, span.src);
+      while (true) {
+        const int cost = span_block(a, seq, span).cost(), rows = __shfl_sync(0xffffffffu, seq.y, span.src);
+        if (span.at + kPrefillItemUnits + cost > span.from) break;
+        span_advance(span, cost, rows, filled);
+      }
+    }
+  }
+  int i = pair;
+  for (uint32_t n = 0;; ++n, i += pairs) {
+    Item it{};
+    it.last = 1;
+    if (spans)
+      span_next(a, seq, span, filled, length, used, pair, it);
+    else if (i < items)
+      it = item_direct(a, seq, before, blocks, i);
+    if (hand_item(ctx, slots, lane, n, it)) break;
   }
 }
 
@@ -839,8 +942,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (rank == 0) issue_items(ctx, slots, tbase, smem_u32(q_smem), smem_u32(ring), lane);
       wait_bar(ctx, &bars->drain, 0, kItemWait);   // every product of the pair is done
     } else if (warp == kWarpList) {
-      if (rank == 0)
-        list_items(a, ctx, slots, lane);
+      if (rank == 0 && a.direct)
+        list_direct(a, ctx, slots, lane);
+      else if (rank == 0)
+        list_plan(a, ctx, slots, lane);
       else if (lane == 0)
         await_items(ctx, slots);
       __syncwarp();

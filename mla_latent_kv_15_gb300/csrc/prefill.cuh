@@ -43,9 +43,9 @@ static_assert(sizeof(PrefillPiece) == 32, "one aligned 32-byte record");
 struct PrefillSplit {  // a block to be joined
   int q0, nq, pieces;
   int head0, heads;    // the heads it is cut for
-  int prow;            // partial row of (piece p, head head0 + h, row r): prow + (p * heads + h) * nq + r
-  int before;          // rows * heads of the records before it
-  int pad;
+  int prow;            // partial row of (piece p, head head0 + h, row r): prow + p * stride + h * nq + r
+  int before;          // rows * heads of the records before it (with a plan)
+  int stride;          // partial rows from a piece to the next
 };
 
 struct PrefillPlan {
@@ -68,13 +68,18 @@ struct PrefillLayout {
 // A fixed plan is made for fewer items (blocks x heads) than this many a pair.
 constexpr int kPrefillFixedItems = 8;
 
+// Partial rows of a piece where the pairs cut items by themselves: pair p's
+// first piece, of an item that began before it, has those from 2 p times this,
+// its last, of an item that ends behind it, the next.
+__host__ __device__ inline int prefill_span_rows(int total_q) { return total_q < kPrefillRows ? total_q : kPrefillRows; }
+
 // Byte offsets for a shape.  Automatic splitting makes at most two partial
 // pieces per pair (prefill_plan_kernel); a forced count cuts every block.
 inline PrefillLayout prefill_layout(int batch, int total_q, int num_heads, int max_splits) {
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
   PrefillLayout L{};
   const long long mb = (long long)total_q / kPrefillRows + batch;
-  const long long auto_rows = 2LL * kPrefillMaxPairs * (total_q < kPrefillRows ? total_q : kPrefillRows);
+  const long long auto_rows = 2LL * kPrefillMaxPairs * prefill_span_rows(total_q);
   const long long forced_rows = max_splits > 1 ? (long long)total_q * max_splits * num_heads : 0;
   const long long mp = mb * (max_splits > 1 ? max_splits : 1) + (kPrefillFixedItems + 2) * kPrefillMaxPairs;
   L.max_pieces = mp;
@@ -116,7 +121,8 @@ struct PrefillArgs {
   int batch, total_q, total_kv, num_heads;
   int causal;
   int num_splits;        // 0: automatic
-  int direct;            // no plan (kPrefillDirectKeys)
+  int direct;            // no plan: the pairs find their items by themselves
+  int spans;             // ... which may be cut (then the join is launched)
   int group_heads;       // heads whose keys and values stay in L2 together
   int pairs;             // grid of the attention kernel, in CTA pairs
   float scale_log2;      // scale * log2(e), > 0
@@ -127,17 +133,40 @@ struct PrefillArgs {
   PrefillPlan plan;
 };
 
-// Calls of at most this many sequences and key rows need no plan: no item is
-// long enough to be cut or to be taken early, and every pair's list warp finds
-// its items from the prefix sums (one launch instead of three).
+// Calls of at most this many sequences need no plan where they have few items
+// (below) or no more than this many key rows: every pair's list warp finds its
+// items from the prefix sums, a lane a sequence (8 single tokens over up to 8191
+// keys: 16 heads 60.2 us a call with the plan, 55.1 without, 1 head 26.5 and
+// 22.0).  Over few key rows no item is long enough to be cut or to be taken
+// early, and the attention is the only launch (37-token prompt of 16 heads:
+// 14 us a call with all three, 11 alone).
 constexpr int kPrefillDirectBatch = 32;
 constexpr int kPrefillDirectKeys = 512;
+
+// Costs of items, in units (see the plan): a tile of 128 keys is two, or one
+// for a block of up to 256 rows; an item's start and end as much as 3.
+constexpr int kPrefillMinChunk = 8;
+constexpr int kPrefillItemUnits = 3;
 
 #ifdef __CUDACC__
 // Query rows r0.. of a sequence of sq rows from q0 over sk keys from k0, as a block.
 struct PrefillBlock {
   int q0, nq, kv0, nkeys, lim0;
+  __device__ int tiles() const { return (nkeys + kPrefillTile - 1) / kPrefillTile; }
+  __device__ int unit() const { return nq > kPrefillRows / 2 ? 2 : 1; }
+  __device__ int cost() const { return tiles() * unit(); }
 };
+// Items laid end to end, each with its fixed cost in front, are cut into
+// `used` equal spans: how many (no more than leave each about kPrefillMinChunk
+// units), and where span p begins.
+__device__ __forceinline__ int prefill_spans(long long length, int items, int pairs) {
+  const long long by_length = length / (kPrefillItemUnits + kPrefillMinChunk);
+  return (int)min((long long)pairs, max((long long)items, by_length));
+}
+// Tiles of an item at `s` that lie before `border`.
+__device__ __forceinline__ int prefill_tiles_before(long long border, long long s, int unit, int tiles) {
+  return (int)min(max(border - s - kPrefillItemUnits, 0LL) >> (unit - 1), (long long)tiles);
+}
 __device__ __forceinline__ PrefillBlock prefill_block(int q0, int sq, int k0, int sk, int r0, int causal) {
   PrefillBlock b;
   b.q0 = q0 + r0;

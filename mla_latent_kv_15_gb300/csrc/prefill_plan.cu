@@ -11,7 +11,8 @@
 // fixed cost of kItemUnits in front (filling the pipeline, the epilogue: about
 // 4000 cycles against 1300 a unit), and cut into equal spans, one a pair, so
 // that every pair ends at the same time; an item on a border is cut there, in
-// at most two partial pieces a pair.
+// at most two partial pieces a pair.  (Up to 32 sequences the pairs do this by
+// themselves, without this kernel.)
 // Many items: the list of pieces is the same for every head, longest first,
 // and the pairs take (piece, head) from it one after the other.  A block is cut
 // over its keys only where it would outlast the rest: with T units over all
@@ -37,8 +38,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kBuckets = 1024;       // piece lengths are sorted into this many classes
-constexpr int kMinChunk = 8;         // units
-constexpr int kItemUnits = 3;
+constexpr int kMinChunk = kPrefillMinChunk, kItemUnits = kPrefillItemUnits;
 constexpr int kMaxFixed = kPrefillFixedItems * kPrefillMaxPairs;   // blocks of a fixed plan, at most
 
 __device__ __noinline__ int block_sum_scan(int v, int* total, int* warp_sums) {
@@ -63,11 +63,7 @@ __device__ __noinline__ int block_sum_scan(int v, int* total, int* warp_sums) {
   return before + incl - v;
 }
 
-struct BlockOf : PrefillBlock {
-  int tiles;
-  int unit;    // cost of a tile
-  __device__ int cost() const { return tiles * unit; }
-};
+using BlockOf = PrefillBlock;
 
 // The prefix sums and the blocks before each sequence, in shared memory for
 // up to kSeqs sequences (every step of a search is then a few cycles), else
@@ -86,11 +82,7 @@ __device__ __noinline__ BlockOf block_of(const PrefillArgs& a, const Sequences& 
     if (sq_.first[mid] <= i) lo = mid; else hi = mid - 1;
   }
   const int q0 = sq_.cu_q[lo], sq = sq_.cu_q[lo + 1] - q0, k0 = sq_.cu_kv[lo], sk = sq_.cu_kv[lo + 1] - k0;
-  BlockOf b;
-  static_cast<PrefillBlock&>(b) = prefill_block(q0, sq, k0, sk, (i - sq_.first[lo]) * kPrefillRows, a.causal);
-  b.tiles = (b.nkeys + kPrefillTile - 1) / kPrefillTile;
-  b.unit = b.nq > kPrefillRows / 2 ? 2 : 1;
-  return b;
+  return prefill_block(q0, sq, k0, sk, (i - sq_.first[lo]) * kPrefillRows, a.causal);
 }
 
 // a * b / c without overflow of the product
@@ -114,7 +106,7 @@ __device__ __noinline__ void put_piece(const PrefillArgs& a, int at, const Block
 __device__ __noinline__ int put_split(const PrefillArgs& a, const BlockOf& b, int pieces, int head0, int heads,
                                       int* rows, int* splits) {
   PrefillSplit sp{};
-  sp.q0 = b.q0, sp.nq = b.nq, sp.pieces = pieces, sp.head0 = head0, sp.heads = heads;
+  sp.q0 = b.q0, sp.nq = b.nq, sp.pieces = pieces, sp.head0 = head0, sp.heads = heads, sp.stride = heads * b.nq;
   sp.prow = atomicAdd(rows, pieces * heads * b.nq);
   a.plan.splits[atomicAdd(splits, 1)] = sp;
   return sp.prow;
@@ -216,8 +208,7 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArg
       all += total;
     }
     const long long length = (long long)all * a.num_heads;
-    // pairs in use: no more pieces than leave each about kMinChunk units
-    const int used = (int)min((long long)a.pairs, max((long long)items, length / (kItemUnits + kMinChunk)));
+    const int used = prefill_spans(length, items, a.pairs);
     if (tid <= kPrefillMaxPairs) {
       s_pair[tid] = 0;
       s_border[tid] = used > 0 ? mul_div(length, min(tid, used), used) : 0;   // where pair `tid`'s span begins
@@ -252,8 +243,8 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArg
           for (int p = p0;; ++p) {
             const long long stop = p + 1 >= used ? end : s_border[p + 1];
             const bool fin = stop >= end;
-            const int t1 = fin ? b.tiles : (int)min(max(stop - s - kItemUnits, 0LL) >> (b.unit - 1), (long long)b.tiles);
-            if (t1 > t0 || (fin && b.tiles == 0)) {
+            const int t1 = fin ? b.tiles() : prefill_tiles_before(stop, s, b.unit(), b.tiles());
+            if (t1 > t0 || (fin && b.tiles() == 0)) {
               if (walk) {
                 put_piece(a, at + k, b, t0, t1, n > 1 ? prow + k * b.nq : -1, h);
                 atomicAdd(&s_pair[p], 1);
@@ -282,8 +273,8 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArg
     const int chunk = max((int)min((work + a.pairs - 1) / a.pairs, 1ull << 28), kMinChunk);
     const bool cut = a.num_splits == 0 && 2 * longest > 3 * chunk;
     auto pieces_of = [&](const BlockOf& b) {
-      if (a.num_splits > 0) return max(1, min(a.num_splits, b.tiles));
-      return cut && 2 * b.cost() > 3 * chunk ? min((b.cost() + chunk - 1) / chunk, b.tiles) : 1;
+      if (a.num_splits > 0) return max(1, min(a.num_splits, b.tiles()));
+      return cut && 2 * b.cost() > 3 * chunk ? min((b.cost() + chunk - 1) / chunk, b.tiles()) : 1;
     };
     if (few && !cut && a.num_splits == 0) {
       // every block is a piece: its place is the number of longer ones before it
@@ -295,7 +286,7 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArg
           const int c = s_block[i].cost();
           at += c > b.cost() || (c == b.cost() && i < tid);
         }
-        put_piece(a, at, b, 0, b.tiles, -1, 0);
+        put_piece(a, at, b, 0, b.tiles(), -1, 0);
       }
       carry = nblocks;
     } else {
@@ -312,8 +303,8 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArg
         const int P = pieces_of(b);
 #pragma unroll 1
         for (int p = 0; p < P; ++p) {
-          const int t0 = (int)mul_div(b.tiles, p, P), t1 = (int)mul_div(b.tiles, p + 1, P);
-          atomicAdd(&s_hist[bucket((t1 - t0) * b.unit)], 1);
+          const int t0 = (int)mul_div(b.tiles(), p, P), t1 = (int)mul_div(b.tiles(), p + 1, P);
+          atomicAdd(&s_hist[bucket((t1 - t0) * b.unit())], 1);
         }
       }
       __syncthreads();
@@ -337,8 +328,8 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArg
         }
 #pragma unroll 1
         for (int p = 0; p < P; ++p) {
-          const int t0 = (int)mul_div(b.tiles, p, P), t1 = (int)mul_div(b.tiles, p + 1, P);
-          const int at = atomicAdd(&s_hist[bucket((t1 - t0) * b.unit)], 1);
+          const int t0 = (int)mul_div(b.tiles(), p, P), t1 = (int)mul_div(b.tiles(), p + 1, P);
+          const int at = atomicAdd(&s_hist[bucket((t1 - t0) * b.unit())], 1);
           put_piece(a, at, b, t0, t1, prow < 0 ? -1 : prow + p * a.num_heads * b.nq, 0);
         }
       }
@@ -374,16 +365,40 @@ __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const PrefillArg
 // One warp per (row, head) of the split blocks, four output dims a lane; the
 // records' row counts are searched in shared memory where they fit.
 constexpr int kSearch = 1024;
+static_assert(kPrefillMaxPairs <= 96, "three records a lane");
 
 __global__ void __launch_bounds__(256) prefill_combine_kernel(const PrefillArgs a) {
   __shared__ int s_before[kSearch];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int n = a.plan.header->num_split, total = a.plan.header->split_rows;
-  if (n == 0) return;
-#pragma unroll 1
-  for (int i = threadIdx.x; i < n && i < kSearch; i += blockDim.x) s_before[i] = a.plan.splits[i].before;
-  __syncthreads();
   const int lane = threadIdx.x & 31;
+  int n = a.pairs, total;
+  if (a.direct) {
+    // a record a pair, most of them empty; three to a lane
+    int rows[3], sum = 0;
+    for (int e = 0; e < 3; ++e) {
+      const int i = 3 * lane + e;
+      rows[e] = i < n && a.plan.splits[i].pieces > 0 ? a.plan.splits[i].nq : 0;
+      sum += rows[e];
+    }
+    int incl = sum;
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+      const int before = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += before;
+    }
+    total = __shfl_sync(0xffffffffu, incl, 31);
+    if (total == 0) return;
+    if (threadIdx.x < 32)
+      for (int e = 0, before = incl - sum; e < 3; before += rows[e], ++e) s_before[3 * lane + e] = before;
+  } else {
+    n = a.plan.header->num_split, total = a.plan.header->split_rows;
+    if (n == 0) return;
+#pragma unroll 1
+    for (int i = threadIdx.x; i < n && i < kSearch; i += blockDim.x) s_before[i] = a.plan.splits[i].before;
+  }
+  __syncthreads();
+  // the pieces behind a pair's first lie where the pairs have their first partial rows
+  const int skew = a.direct ? prefill_span_rows(a.total_q) : 0;
   // consecutive rows to a warp, mostly of one record
   const int warps = gridDim.x * 8, per = (total + warps - 1) / warps;
   const int from = (blockIdx.x * 8 + (threadIdx.x >> 5)) * per, to = min(from + per, total);
@@ -400,11 +415,11 @@ __global__ void __launch_bounds__(256) prefill_combine_kernel(const PrefillArgs 
         if (before <= rr) lo = mid; else hi = mid - 1;
       }
       sp = a.plan.splits[lo];
+      if (a.direct) sp.before = s_before[lo];
       ends = sp.before + sp.nq * sp.heads;
     }
     const int own = rr - sp.before;
     const int h = own / sp.nq, r = own - h * sp.nq;
-    const int step = sp.heads * sp.nq;                        // all partial rows are below 2^31
     const float* lse = a.plan.part_lse + sp.prow + own;
     const float4* part = reinterpret_cast<const float4*>(a.plan.part_o + (int64_t)(sp.prow + own) * kNope) + lane;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -417,8 +432,9 @@ __global__ void __launch_bounds__(256) prefill_combine_kernel(const PrefillArgs 
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const bool is = p0 + e < sp.pieces;
-        l[e] = is ? lse[(int64_t)(p0 + e) * step] : -INFINITY;
-        v[e] = is ? part[(int64_t)(p0 + e) * step * (kNope / 4)] : make_float4(0.f, 0.f, 0.f, 0.f);
+        const int64_t at = (int64_t)(p0 + e) * sp.stride - (p0 + e > 0 ? skew : 0);
+        l[e] = is ? lse[at] : -INFINITY;
+        v[e] = is ? part[at * (kNope / 4)] : make_float4(0.f, 0.f, 0.f, 0.f);
       }
       const float top = fmaxf(fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])), ref);
       const float sub = top == -INFINITY ? 0.f : top;

@@ -348,3 +348,21 @@ def test_prefill_mending_rows_outlasts_the_wait_limit():
         ref, lse, mag = prompt_ref.prefill_torch(c.q[:, h:h + 1], clean[:, h:h + 1], c.k_pe, c.at_q, c.at_kv, SCALE, True)
         err = (c.out[:299, h:h + 1].double() - ref[:299]).abs()
         assert (err <= 2.0 ** -8 * ref[:299].abs() + (2.0 ** -8 + 6.6e-4 + 2.0 ** -18) * mag[:299]).all()
+
+
+@pytest.mark.parametrize("q_lens,kv_lens,heads", [
+    ([1] * 8, [8191, 4097, 1, 777, 6000, 129, 8000, 0], 16), ([512], [9000], 20), ([600, 1, 256, 257], [600, 9001, 3000, 2570], 8),
+    ([1], [70000], 1), ([1] * 31 + [300], [0] * 31 + [5000], 3), ([0, 3, 0, 700, 2], [900, 3, 5, 2900, 1], 5),
+    ([5000], [5000], 7), ([16] * 32, [130, 2000] * 16, 2), ([1, 513], [1300, 1024], 37), ([2, 3], [600, 513], 150),
+    ([260] * 3, [1025, 1030, 1100], 60), ([1] * 20, [1024 + 130 * i for i in range(20)], 30)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prefill_with_and_without_a_plan(q_lens, kv_lens, heads, causal):
+    """Up to 32 sequences the pairs find and cut their items by themselves; with
+    more (empty ones here) a plan does.  The pieces are the same, and so are
+    the results to the bit."""
+    a = Case(q_lens, kv_lens, heads, seed=32).run(causal).check(causal)
+    none = [0] * 33
+    b = Case(q_lens + none, kv_lens + none, heads, seed=32).run(causal)
+    torch.cuda.synchronize()
+    assert mla.prefill_status(b.ws) == 0
+    assert torch.equal(a.out, b.out) and torch.equal(a.lse, b.lse)
