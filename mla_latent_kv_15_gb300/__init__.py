@@ -165,8 +165,10 @@ def _dense(t, name: str, dtypes, shape=None, dims=None):
 
 def _cache_checked(cache, name="cache"):
     import torch
-    if cache.dtype is torch.bfloat16 and cache.dim() == 3 and cache.shape[2] == DQK and cache.is_contiguous():
-        return cache.shape
+    dtype, shape = cache.dtype, cache.shape
+    if ((dtype is torch.bfloat16 or dtype is torch.float8_e4m3fn) and len(shape) == 3 and shape[2] == DQK and
+            cache.is_contiguous()):
+        return shape
     _dense(cache, name, (torch.bfloat16, torch.float8_e4m3fn, torch.uint8), dims=3)
     if cache.shape[2] != DQK:
         raise ValueError(f"cache rows must be {DQK} wide, got {cache.shape[2]}")
@@ -239,6 +241,11 @@ def _on_current_device(*tensors) -> int:
     """Refuse tensors of another device than the current one: the call's
     stream, tensor maps and launch belong to the current device.  Returns it."""
     import torch
+    found = {t.get_device() for t in tensors if t is not None}
+    if len(found) == 1:                      # the usual case
+        dev = found.pop()
+        if dev >= 0 and dev == torch.cuda.current_device():
+            return dev
     dev = None
     for t in tensors:
         if t is None:
