@@ -649,12 +649,12 @@ __device__ __noinline__ void mend_row(const PrefillArgs& a, int row, int head, i
 // (the tile's own code is the only part that is hot).
 
 // Scores of keys that a row does not see, the tile's from `left` on, become -inf.
-// The warp's rows see `fewest` of its keys or more.
-__device__ __forceinline__ void mask_tile(uint32_t s_col, int left, int fewest) {
+// The warp's rows see `fewest` of its keys or more and none behind `most`.
+__device__ __forceinline__ void mask_tile(uint32_t s_col, int left, int fewest, int most) {
   const int g0 = max(fewest, 0) >> 5;
   left -= 32 * g0;
 #pragma unroll 1
-  for (int g = g0; g < 4; ++g, left -= 32) {
+  for (int g = g0; g < 4 && 32 * g < most; ++g, left -= 32) {
     uint32_t s[32];
     tmem_ld32(s_col + 32 * g, s);
     tmem_wait_ld();
@@ -662,6 +662,11 @@ __device__ __forceinline__ void mask_tile(uint32_t s_col, int left, int fewest) 
     for (int c = 0; c < 32; ++c) s[c] = c < left ? s[c] : 0xff800000u;
     tmem_st32(s_col + 32 * g, s);
   }
+  uint32_t none[16];
+#pragma unroll
+  for (int c = 0; c < 16; ++c) none[c] = 0xff800000u;
+#pragma unroll 1
+  for (int g = 2 * ((most + 31) >> 5); g < 8; ++g) tmem_st16(s_col + 16 * g, none);
   tmem_wait_st();
 }
 
@@ -758,7 +763,7 @@ __device__ __forceinline__ void softmax_items(const PrefillArgs& a, const Ctx& c
         if (lane == 0) mbar_arrive_remote(p_full);
         continue;
       }
-      if (warp_sees < (j + 1) * kPrefillTile) mask_tile(s_col, sees - j * kPrefillTile, warp_sees - j * kPrefillTile);
+      if (warp_sees < (j + 1) * kPrefillTile) mask_tile(s_col, sees - j * kPrefillTile, warp_sees - j * kPrefillTile, warp_most - j * kPrefillTile);
       softmax_tile(s_col, o_col, scale, i == 0, ref, sum);
       tmem_wait_st();
       tc_fence_before();
