@@ -114,3 +114,50 @@ def test_prefill_of_one_launch_replayed_over_other_lengths():
         seen = inside[:, None] & ~l.isinf()
         assert ((lse.double() - l).abs() <= 3.3e-4 + 2.0 ** -20 * l.abs())[seen].all()
         assert (lse[inside[:, None] & l.isinf()] == -math.inf).all()
+
+
+@pytest.mark.parametrize("extra,heads", [(0, 5), (40, 5), (0, 200)])
+def test_prefill_replayed_over_other_lengths_with_cut_items(extra, heads):
+    """The same where items are cut and joined: spans found by the pairs, by a
+    plan (more than 32 sequences), and a list of many items."""
+    Tq, Tk = 700, 4000
+    q, kv, pe = rnd(Tq, heads, 192, seed=9), rnd(Tk, heads, 256, seed=10), rnd(Tk, 64, seed=11)
+    n = 3 + extra
+    cu_q, cu_kv = torch.zeros(n + 1, dtype=torch.int32, device="cuda"), torch.zeros(n + 1, dtype=torch.int32, device="cuda")
+    out = torch.empty(Tq, heads, 128, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(Tq, heads, device="cuda")
+    ws = torch.full((mla.prefill_workspace_size(n, Tq, heads),), 0xEE, dtype=torch.uint8, device="cuda")
+
+    def call():
+        mla.prefill(q, kv, pe, cu_q, cu_kv, out, ws, scale=SCALE, lse=lse)
+
+    call()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for at_q, at_kv in (([0, 1, 2, 3], [0, 3999, 4000, 4000]), ([0, 0, 0, 0], [0, 1000, 2000, 4000]),
+                        ([0, 600, 601, 700], [0, 700, 3000, 4000]), ([5, 6, 6, 6], [9, 3990, 3990, 3990]),
+                        ([0, 300, 500, 700], [0, 5000, 5000, 5000]), ([0, 300, 200, 700], [0, 1000, 2000, 3000]),
+                        ([0, 256, 512, 700], [0, 100, 200, 300]), ([0, 700, 700, 700], [0, 4000, 4000, 4000])):
+        cu_q.copy_(torch.tensor(at_q + [at_q[-1]] * extra, dtype=torch.int32))
+        cu_kv.copy_(torch.tensor(at_kv + [at_kv[-1]] * extra, dtype=torch.int32))
+        out.fill_(7.0)
+        lse.fill_(7.0)
+        g.replay()
+        torch.cuda.synchronize()
+        want_bits = (0 if at_q == sorted(at_q) else mla.DEVERR_BAD_QSL) | (0 if at_kv[-1] <= Tk else mla.DEVERR_BAD_SEQ_LEN)
+        assert mla.prefill_status(ws) == want_bits
+        inside = torch.zeros(Tq, dtype=torch.bool, device="cuda")
+        if want_bits == 0:
+            inside[at_q[0]:at_q[-1]] = True
+        assert (out[~inside] == 7.0).all() and (lse[~inside] == 7.0).all()
+        if want_bits:
+            continue
+        for h in (0, heads - 1):
+            want, l, m = prompt_ref.prefill_torch(q[:, h:h + 1], kv[:, h:h + 1], pe, at_q, at_kv, SCALE, True)
+            err = (out[:, h:h + 1].double() - want).abs()
+            assert (err <= 2.0 ** -8 * want.abs() + (2.0 ** -8 + 6.6e-4 + 2.0 ** -18) * m)[inside].all()
+            seen = inside[:, None] & ~l.isinf()
+            assert ((lse[:, h:h + 1].double() - l).abs() <= 3.3e-4 + 2.0 ** -20 * l.abs())[seen].all()
+            assert (lse[:, h:h + 1][inside[:, None] & l.isinf()] == -math.inf).all()
