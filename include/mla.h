@@ -524,6 +524,8 @@ MLA_API size_t mla_prefill_workspace_size(int batch, int total_q, int num_heads,
  *               may overlap on the GPU need a workspace each
  * A value that is not finite makes the rows that see its key not finite; in
  * keys a row does not see it has no effect on the row.
+ * Outputs are summed in float32 before they are divided by the sum of the
+ * probabilities, which are at most 2^8: values beyond 2^120 / keys may overflow.
  * batch == 0 or total_q == 0 is a no-op.  Three launches (plan, attention,
  * join); for up to 32 sequences the attention alone over up to 512 key rows,
  * and no plan where total_q / 512 + batch blocks times heads are few.  Nothing of
