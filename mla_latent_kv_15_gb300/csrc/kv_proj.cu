@@ -22,6 +22,8 @@
 // two staged pieces a warp are enough (pieces 2, 4, 6, 8, leaving 6, 5, 4, 3
 // stages: 174, 181, 186, 200 us; the tokens kept in shared memory and only
 // weights streamed, four stages: 212; 32-byte stores from registers: 202).
+// Without the graph's launch 173 us back to back: 1590 TFLOP/s, 83 % of the
+// library's burst rate and 94 % of its sustained one.
 #include <cuda_bf16.h>
 
 #include "common.cuh"

@@ -26,6 +26,15 @@
 // An item of up to 256 rows ("narrow") has one query tile: the pair takes its
 // even key tiles as tile 0 and its odd ones as tile 1, so that the two still
 // work in turn, and the warps of tile 0 join the two results at the end.
+//
+// Measured (128 heads): causal prompt of 8192 tokens 1650 us back to back, 1666
+// TFLOP/s, 98 % of the library's matrix rate under the same power cap; 512 rows
+// over 16384 keys without a mask 428 us, 1605 TFLOP/s; eight single tokens over
+// up to 8191 keys of 16 heads 55 us, 4.1 TB/s.  A step of a query tile takes
+// ~1430 cycles, its products at least 1280; short prompts lose ~4000 cycles an
+// item and ~2000 on each key tile that tile 1 has alone (16 prompts of 1024, 32
+// heads: 182 us, half of it products).  Two threads a row (16 softmax warps of
+// 96 registers) were slower: 8192 tokens 1840 us, 16 prompts of 1024 199.
 #include <cuda_bf16.h>
 
 #include "common.cuh"

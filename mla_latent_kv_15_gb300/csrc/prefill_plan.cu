@@ -28,7 +28,8 @@
 // Both kernels run every instruction about once, from cold instruction
 // caches, so their time is the code they fetch: loops stay loops, and what
 // occurs twice is a function (the plan unrolled and inlined was 56 KB of code
-// and took 8-10 us).
+// and took 8-10 us).  In a call among others the plan takes about 5 us, the join
+// 4 (112 rows) to 12 (38000 rows); bound by latency both.
 #include <cuda_bf16.h>
 
 #include "prefill.cuh"

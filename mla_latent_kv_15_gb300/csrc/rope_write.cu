@@ -19,7 +19,8 @@
 // (8192 tokens of 128 heads with latent rows, about 8 us of graph launch
 // included: 8 heads a warp 68.7 us, 16: 60.5, 32: 52.4, 64: 56.5; 299 MB at the
 // copy rate are 44).  The data is loaded before the position is known, so the
-// two latencies overlap.
+// two latencies overlap.  (A call among others: 44.7 us, 99 % of the copy rate;
+// 64 tokens 3.3 us in a graph.)
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
