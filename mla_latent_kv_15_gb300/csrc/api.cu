@@ -707,12 +707,12 @@ int mla_prefill(const void* q, int64_t q_token_stride, int64_t q_head_stride, co
   a.debug_skip_tile = g_test_skip_tile;
   a.plan = mla::prefill_plan_from(workspace, L);
   cudaStream_t s = (cudaStream_t)stream;
-  // without a plan: few key rows, or few items whose units count in 32 bits
+  // without a plan: few key rows, or few items of not too many units
   const int64_t blocks = (int64_t)total_q / mla::kPrefillRows + batch;
   const bool small = num_splits <= 1 && total_kv <= mla::kPrefillDirectKeys;
   a.spans = !small && num_splits == 0 && batch <= mla::kPrefillDirectBatch &&
             blocks * num_heads < mla::kPrefillFixedItems * a.pairs &&
-            blocks * (2 * (int64_t)total_kv / mla::kPrefillTile + 8) < (1LL << 30);
+            blocks * num_heads * (2 * (int64_t)total_kv / mla::kPrefillTile + 8) < mla::kPrefillDirectUnits;
   a.direct = batch <= mla::kPrefillDirectBatch && (small || a.spans);
   cudaError_t e = a.direct ? cudaSuccess : mla::launch_prefill_plan(a, s);
   if (e != cudaSuccess) return cuda_fail(e, "prefill plan launch");

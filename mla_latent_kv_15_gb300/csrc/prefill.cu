@@ -198,8 +198,8 @@ __device__ __forceinline__ Item item_direct(const PrefillArgs& a, const int4 seq
 // A pair's span of all items laid end to end (head after head, `all` units
 // each; lane b: sequence b's units and those before it).
 struct Span {
-  long long from, to;     // [from, to)
-  long long at;           // where item (head, sequence src, row r0) begins
+  int from, to;           // [from, to)
+  int at;                 // where item (head, sequence src, row r0) begins
   int head, src, r0;
 };
 
@@ -219,13 +219,13 @@ __device__ __forceinline__ void span_advance(Span& p, int cost, int rows, unsign
 }
 // The span's next piece, by the whole warp; behind its end, it.last.  The
 // first piece of an item that ends in another span is noted for the join.
-__device__ __forceinline__ void span_next(const PrefillArgs& a, const int4 seq, Span& p, unsigned filled, long long length,
+__device__ __forceinline__ void span_next(const PrefillArgs& a, const int4 seq, Span& p, unsigned filled, int length,
                                        int used, int pair, Item& it) {
   it.last = 1;
   while (p.at < p.to && it.last) {
     const PrefillBlock b = span_block(a, seq, p);
     const int tiles = b.tiles(), unit = b.unit(), rows = __shfl_sync(0xffffffffu, seq.y, p.src);
-    const long long end = p.at + kPrefillItemUnits + b.cost();
+    const int end = p.at + kPrefillItemUnits + b.cost();
     const int t0 = prefill_tiles_before(p.from, p.at, unit, tiles);
     const int t1 = end <= p.to ? tiles : prefill_tiles_before(p.to, p.at, unit, tiles);
     if (t1 > t0 || (end <= p.to && tiles == 0)) {
@@ -240,7 +240,7 @@ __device__ __forceinline__ void span_next(const PrefillArgs& a, const int4 seq, 
         sp.stride = 2 * prefill_span_rows(a.total_q);
         // up to the first span that ends at `end` or behind it; no span between is without a tile
         // (a span is at least as long as an empty item, 3 units, a tile 2)
-        sp.pieces = (int)((end * used + length - 1) / length) - pair;
+        sp.pieces = (int)(((unsigned)end * used + length - 1) / (unsigned)length) - pair;
         a.plan.splits[pair] = sp;
       }
       finish_item(a, it);
@@ -325,20 +325,19 @@ __device__ __noinline__ void list_direct(const PrefillArgs& a, const Ctx& ctx, I
   const bool spans = longest > kPrefillMinChunk && items > 0;
   const unsigned filled = __ballot_sync(0xffffffffu, blocks > 0);
   Span span{};
-  long long length = 0;
-  int used = 1;
+  int length = 0, used = 1;
   if (spans) {
     const int all = __shfl_sync(0xffffffffu, uincl, 31);
-    length = (long long)all * a.num_heads;
+    length = all * a.num_heads;               // below kPrefillDirectUnits
     used = prefill_spans(length, items, pairs);
-    span.from = length * min(pair, used) / used;
-    span.to = length * min(pair + 1, used) / used;
+    span.from = (int)((unsigned)length * min(pair, used) / (unsigned)used);
+    span.to = (int)((unsigned)length * min(pair + 1, used) / (unsigned)used);
     span.at = length;
     if (span.from < length) {
-      span.head = (int)(span.from / all);
-      const int rem = (int)(span.from - (long long)span.head * all);
+      span.head = span.from / all;
+      const int rem = span.from - span.head * all;
       span.src = __ffs(__ballot_sync(0xffffffffu, rem >= uincl - units && rem < uincl)) - 1;
-      span.at = (long long)span.head * all + __shfl_sync(0xffffffffu, uincl - units, span.src);
+      span.at = span.head * all + __shfl_sync(0xffffffffu, uincl - units, span.src);
       while (true) {
         const int cost = span_block(a, seq, span).cost(), rows = __shfl_sync(0xffffffffu, seq.y, span.src);
         if (span.at + kPrefillItemUnits + cost > span.from) break;

@@ -371,6 +371,7 @@ static_assert(kPrefillMaxPairs <= 96, "three records a lane");
 __global__ void __launch_bounds__(256) prefill_combine_kernel(const PrefillArgs a) {
   __shared__ int s_before[kSearch];
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31;
   int n = a.pairs, total;
   if (a.direct) {
@@ -481,7 +482,7 @@ cudaError_t launch_prefill_plan(const PrefillArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_prefill_combine(const PrefillArgs& a, cudaStream_t s) {
-  return launch_dependent(prefill_combine_kernel, 12 * a.pairs, 256, a, s);   // six blocks an SM
+  return launch_dependent(prefill_combine_kernel, 6 * a.pairs, 256, a, s);   // three blocks an SM: all run at once
 }
 
 }  // namespace mla
