@@ -137,7 +137,7 @@ struct PrefillArgs {
 // (below) or no more than this many key rows: every pair's list warp finds its
 // items from the prefix sums, a lane a sequence (8 single tokens over up to 8191
 // keys: 16 heads 60.2 us a call with the plan, 55.1 without, 1 head 26.5 and
-// 22.0).  Over few key rows no item is long enough to be cut or to be taken
+// 22.0, before its spans were shortened).  Over few key rows no item is long enough to be cut or to be taken
 // early, and the attention is the only launch (37-token prompt of 16 heads:
 // 14 us a call with all three, 11 alone).
 constexpr int kPrefillDirectBatch = 32;
