@@ -193,9 +193,9 @@ struct RopeWriteArgs {
 };
 
 // Tiles of mla_kv_up_proj for a shape: token and weight rows of a load box;
-// columns of a CTA pair's tile (pair_bn, 0: single CTAs, 128 columns each).
+// columns of a CTA's tile (bn) or of a CTA pair's (pair_bn, 0: single CTAs).
 struct KvProjShape {
-  int xrows, wrows;
+  int bn, xrows, wrows;
   int pair_bn, pairs;
 };
 

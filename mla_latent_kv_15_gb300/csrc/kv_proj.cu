@@ -6,7 +6,7 @@
 // accumulation in tensor memory, one rounding to bf16.
 //
 // Few tokens (kv_proj_kernel): the weights are the traffic.  One CTA computes
-// a 128-token x 128-column tile; its ring holds as much of the 512-deep
+// a 128-token x kBN-column tile; its ring holds as much of the 512-deep
 // contraction as the shared memory of half an SM does, so nearly every load
 // of a CTA is in flight at once.  With fewer than 128 tokens the token box
 // holds only round_up(T, 16) rows; the MMA rows past it read other bytes of
@@ -34,7 +34,6 @@ namespace {
 using namespace ptx;
 
 constexpr int kM = 128;                          // tokens per CTA (MMA M)
-constexpr int kFewCols = 128;                    // columns of a tile of kv_proj_kernel
 constexpr int kK = 64;                           // contraction dims per stage: one 128-byte swizzled row
 constexpr int kChunks = kLkv / kK;               // 8
 constexpr int kThreads = 192;                    // TMA warp, MMA warp, 4 epilogue warps
@@ -69,17 +68,18 @@ __device__ __forceinline__ void store_cols32(__nv_bfloat16* dst, const uint32_t 
                      pack_bf16x2(__uint_as_float(r[8 * v + 6]), __uint_as_float(r[8 * v + 7])));
 }
 
+template <int kBN>
 __global__ void __launch_bounds__(kThreads, 1)
     kv_proj_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                    __nv_bfloat16* __restrict__ y, int64_t T, int64_t C, int stages, int xrows) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  constexpr uint32_t wbox = kFewCols * kK * 2;
+  constexpr uint32_t wbox = kBN * kK * 2;
   const uint32_t xbox = (uint32_t)xrows * kK * 2;
   const uint32_t stage_bytes = xbox + wbox;
   Bars* bars = reinterpret_cast<Bars*>(smem + stages * stage_bytes + (kXBoxMax - xbox));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int c0 = blockIdx.x * kFewCols, t0 = blockIdx.y * kM;
+  const int c0 = blockIdx.x * kBN, t0 = blockIdx.y * kM;
   const int npre = stages < kChunks ? stages : kChunks;
 
   if (threadIdx.x == 0) {
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(&bars->tmem_base), kFewCols);
+    tmem_alloc(smem_u32(&bars->tmem_base), kBN);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!mbar_wait(smem_u32(&bars->full[c % stages]), (c / stages) & 1)) give_up(bars);
     }
   } else if (warp == 1) {
-    const uint32_t idesc = idesc_bf16_f32(kM, kFewCols, 0, 0);
+    const uint32_t idesc = idesc_bf16_f32(kM, kBN, 0, 0);
     for (int c = 0; c < kChunks; ++c) {
       const int slot = c % stages;
       if (!mbar_wait(smem_u32(&bars->full[slot]), (c / stages) & 1)) {
@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     if (done && !*abort_flag) {
       __nv_bfloat16* dst = y + t * C + c0;
-      for (int j = 0; j < kFewCols; j += 32) {
+      for (int j = 0; j < kBN; j += 32) {
         uint32_t r[32];
         tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + j, r);
         tmem_wait_ld();
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, kFewCols);
+    tmem_dealloc(tmem, kBN);
   }
 }
 
@@ -404,25 +404,58 @@ cudaError_t launch_pair(const CUtensorMap& tm_x, const CUtensorMap& tm_w, const 
   return cudaGetLastError();
 }
 
+template <int kBN>
+cudaError_t launch_few(const CUtensorMap& tm_x, const CUtensorMap& tm_w, void* y, int64_t T, int64_t C, int xrows,
+                       cudaStream_t s) {
+  const uint32_t xbox = (uint32_t)xrows * kK * 2, stage = xbox + kBN * kK * 2;
+  int stages = (int)(kRingBudget / stage);
+  if (stages > kChunks) stages = kChunks;
+  size_t smem = 1024 + (size_t)stages * stage + (kXBoxMax - xbox) + sizeof(Bars);
+  // never more CTAs on an SM than its 512 tensor-memory columns hold (an
+  // allocation beyond them would wait for another CTA to finish)
+  constexpr size_t floor_smem = kSmemPerSm / (512 / kBN + 1);
+  if (smem < floor_smem) smem = floor_smem;
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(kv_proj_kernel<kBN>, 1024 + kRingBudget + kXBoxMax + sizeof(Bars) + 1024, done);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((C + kBN - 1) / kBN), (unsigned)((T + kM - 1) / kM));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kv_proj_kernel<kBN>, tm_x, tm_w, static_cast<__nv_bfloat16*>(y), T, C, stages,
+                         xrows);
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
+}
+
 }  // namespace
 
 // Up to 128 tokens a single CTA's tile holds them all and the weights' traffic
-// wants many CTAs (128 tokens x 32768 columns: 17.6 us, pairs 19.6; tiles of
-// 32, 64 or 256 columns gain nothing).  Above,
-// pairs: 256 columns a tile where that costs no more rounds of all pairs than
-// 128, which run 15 % below the wider tile's rate (8192 tokens x 32768 columns:
-// 173 us against 216; 1021 x 5120: two rounds against three of half the size,
-// 17.5 us against 15.5).  Times include about 8 us of a graph's launch.
+// wants many CTAs: 32 columns each while that makes no more CTAs than SMs, for
+// the shorter products and stores (37 or 128 tokens x 4096 columns: 4.2 us a
+// launch among others, with 128 columns 4.6 and 5.2), else 128 (64 tokens x
+// 32768: 8.7 us, with 32 columns 17.7, with 64 11.7, pairs 12.3).  Above, pairs:
+// 256 or 128 columns a tile, whichever takes less by the rounds of all pairs, at
+// a rate 15 % lower for 128, and a sixth of a round for the wider last tile's
+// stores (8192 tokens x 32768 columns: 54 rounds 173 us, 108 of half the size
+// 216; 4096 x 5120: 5 rounds 21.4, 9 23.0; 512 x 16384: 2 rounds 10.0, 4 10.6; 256
+// x 16384: one round 8.1, two 7.4; 1021 x 5120: two rounds 9.5, three 7.5).
 KvProjShape kv_proj_shape(int64_t T, int64_t C, int sms) {
   KvProjShape p{};
   p.pairs = sms / 2;
   if (T > kM && p.pairs > 0) {
     auto rounds = [&](int bn) { return ((T + 255) / 256 * ((C + bn - 1) / bn) + p.pairs - 1) / p.pairs; };
-    p.pair_bn = 40 * rounds(256) <= 23 * rounds(128) ? 256 : 128;
+    p.pair_bn = 200 * rounds(256) + 33 <= 115 * rounds(128) ? 256 : 128;
     p.wrows = p.pair_bn / 2;
     p.xrows = kM;
   } else {
-    p.wrows = kFewCols;
+    p.bn = p.wrows = (C + 31) / 32 <= sms ? 32 : 128;
     p.xrows = T >= kM ? kM : (int)((T + 15) / 16 * 16);
   }
   return p;
@@ -432,31 +465,8 @@ cudaError_t launch_kv_proj(const CUtensorMap& tm_x, const CUtensorMap& tm_w, con
                            int64_t T, int64_t C, const KvProjShape& p, cudaStream_t s) {
   if (p.pair_bn == 256) return launch_pair<256>(tm_x, tm_w, tm_y, T, C, p.pairs, s);
   if (p.pair_bn == 128) return launch_pair<128>(tm_x, tm_w, tm_y, T, C, p.pairs, s);
-  const uint32_t xbox = (uint32_t)p.xrows * kK * 2, stage = xbox + kFewCols * kK * 2;
-  int stages = (int)(kRingBudget / stage);
-  if (stages > kChunks) stages = kChunks;
-  size_t smem = 1024 + (size_t)stages * stage + (kXBoxMax - xbox) + sizeof(Bars);
-  // never more CTAs on an SM than its 512 tensor-memory columns hold (an
-  // allocation beyond them would wait for another CTA to finish)
-  constexpr size_t floor_smem = kSmemPerSm / (512 / kFewCols + 1);
-  if (smem < floor_smem) smem = floor_smem;
-  static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(kv_proj_kernel, 1024 + kRingBudget + kXBoxMax + sizeof(Bars) + 1024, done);
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((C + kFewCols - 1) / kFewCols), (unsigned)((T + kM - 1) / kM));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kv_proj_kernel, tm_x, tm_w, static_cast<__nv_bfloat16*>(y), T, C, stages,
-                         p.xrows);
-  if (e != cudaSuccess) return e;
-  return cudaGetLastError();
+  if (p.bn == 32) return launch_few<32>(tm_x, tm_w, y, T, C, p.xrows, s);
+  return launch_few<128>(tm_x, tm_w, y, T, C, p.xrows, s);
 }
 
 cudaError_t kv_proj_status(int* status, int clear, cudaStream_t s) {
