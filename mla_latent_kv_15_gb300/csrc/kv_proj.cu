@@ -190,6 +190,7 @@ constexpr int kPieces = 2;                       // staged pieces of an epilogue
 
 template <int kBN>
 struct PairShape {
+  static constexpr uint32_t kTmem = kBN <= 128 ? 256 : 512;   // columns: two accumulators, a power of two
   static constexpr uint32_t kWBox = kBN / 2 * kK * 2;
   static constexpr uint32_t kStage = kXBoxMax + kWBox;
   static constexpr uint32_t kStaging = 4 * kPieces * kPiece;
@@ -256,7 +257,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     tma_prefetch_desc(&tm_y);
   }
   if (warp == 1) {
-    tmem_alloc_pair(smem_u32(&bars->tmem_base), 2 * kBN);
+    tmem_alloc_pair(smem_u32(&bars->tmem_base), P::kTmem);
     tmem_relinquish_pair();
   }
   tc_fence_before();
@@ -329,7 +330,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       const uint32_t from = tmem + acc * kBN + ((uint32_t)(32 * q) << 16);
 #pragma unroll 1
       for (int p = 0; p < kBN / 64; ++p) {
-        uint8_t* piece = stage + (p % kPieces) * kPiece;
+        uint8_t* piece = stage + (m * (kBN / 64) + p) % kPieces * kPiece;   // the pieces in turn, across tiles
         uint32_t a[32], b[32];
         tmem_ld32(from + 64 * p, a);
         tmem_ld32(from + 64 * p + 32, b);
@@ -378,7 +379,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   cluster_sync();   // the pair ends together: each reads and signals the other's shared memory
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc_pair(tmem, 2 * kBN);
+    tmem_dealloc_pair(tmem, P::kTmem);
   }
 }
 
@@ -441,17 +442,22 @@ cudaError_t launch_few(const CUtensorMap& tm_x, const CUtensorMap& tm_w, void* y
 // the shorter products and stores (37 or 128 tokens x 4096 columns: 4.2 us a
 // launch among others, with 128 columns 4.6 and 5.2), else 128 (64 tokens x
 // 32768: 8.7 us, with 32 columns 17.7, with 64 11.7, pairs 12.3).  Above, pairs:
-// 256 or 128 columns a tile, whichever takes less by the rounds of all pairs, at
-// a rate 15 % lower for 128, and a sixth of a round for the wider last tile's
-// stores (8192 tokens x 32768 columns: 54 rounds 173 us, 108 of half the size
-// 216; 4096 x 5120: 5 rounds 21.4, 9 23.0; 512 x 16384: 2 rounds 10.0, 4 10.6; 256
-// x 16384: one round 8.1, two 7.4; 1021 x 5120: two rounds 9.5, three 7.5).
+// 128, 192 or 256 columns a tile, whichever costs least: the rounds of all pairs
+// at 129 : 161 : 200 (the wider tile reads less for a product), and 62 for the
+// last stores of the wider ones.  Measured, us a launch among others, rounds in
+// brackets:     128         192         256
+//   200 x 16384   6.5 (2)     7.9 (2)     7.2 (1)
+//  1021 x  5120   7.9 (3)     7.1 (2)     8.2 (2)
+//  2048 x 10240  21.4 (9)    18.5 (6)    19.3 (5)
+//  4096 x  4096  18.7 (7)    17.4 (5)    15.6 (4)
+//  8192 x 32768   213 (108)   191 (72)    182 (54)
 KvProjShape kv_proj_shape(int64_t T, int64_t C, int sms) {
   KvProjShape p{};
   p.pairs = sms / 2;
   if (T > kM && p.pairs > 0) {
     auto rounds = [&](int bn) { return ((T + 255) / 256 * ((C + bn - 1) / bn) + p.pairs - 1) / p.pairs; };
-    p.pair_bn = 200 * rounds(256) + 33 <= 115 * rounds(128) ? 256 : 128;
+    const int64_t c128 = 129 * rounds(128), c192 = 161 * rounds(192) + 62, c256 = 200 * rounds(256) + 62;
+    p.pair_bn = c128 <= c192 && c128 <= c256 ? 128 : c192 < c256 ? 192 : 256;
     p.wrows = p.pair_bn / 2;
     p.xrows = kM;
   } else {
@@ -464,6 +470,7 @@ KvProjShape kv_proj_shape(int64_t T, int64_t C, int sms) {
 cudaError_t launch_kv_proj(const CUtensorMap& tm_x, const CUtensorMap& tm_w, const CUtensorMap& tm_y, void* y,
                            int64_t T, int64_t C, const KvProjShape& p, cudaStream_t s) {
   if (p.pair_bn == 256) return launch_pair<256>(tm_x, tm_w, tm_y, T, C, p.pairs, s);
+  if (p.pair_bn == 192) return launch_pair<192>(tm_x, tm_w, tm_y, T, C, p.pairs, s);
   if (p.pair_bn == 128) return launch_pair<128>(tm_x, tm_w, tm_y, T, C, p.pairs, s);
   if (p.bn == 32) return launch_few<32>(tm_x, tm_w, y, T, C, p.xrows, s);
   return launch_few<128>(tm_x, tm_w, y, T, C, p.xrows, s);

@@ -99,3 +99,16 @@ def test_kv_up_proj_splits_into_key_and_value_weights():
     ref = torch.einsum("tl,ndl->tnd", x, w[:, 128:].double())
     assert ((kv[..., 128:].double() - v.double()).abs() <= 2 * (2.0 ** -8 * ref.abs() + 2.0 ** -14 * mag)).all()
     check(kv, lat, w)
+
+
+@pytest.mark.parametrize("T,N,D", [(1021, 20, 256), (1021, 40, 256), (300, 40, 256), (2048, 20, 256), (2050, 39, 264),
+                                   (37, 19, 256), (128, 5, 40), (128, 20, 256), (200, 64, 256), (1021, 64, 256)])
+def test_kv_up_proj_tile_widths(T, N, D):
+    """Sizes that take each of the tile widths, more than one tile a pair, three
+    times with other operands: no tile's stores meet the next one's."""
+    for seed in range(3):
+        lat, w = data(T, N, D, 7 * T + N + seed, True)
+        kv = torch.full((T, N, D), float("nan"), dtype=torch.bfloat16, device="cuda")
+        mla.kv_up_proj(lat[:, :512], w, kv)
+        torch.cuda.synchronize()
+        check(kv, lat, w)
