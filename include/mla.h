@@ -522,8 +522,11 @@ MLA_API size_t mla_prefill_workspace_size(int batch, int total_q, int num_heads,
  *   workspace   >= mla_prefill_workspace_size(batch, total_q, num_heads,
  *               num_splits) bytes, 256-byte aligned; scratch only.  Calls that
  *               may overlap on the GPU need a workspace each
- * A value that is not finite makes the rows that see its key not finite; in
- * keys a row does not see it has no effect on the row.
+ * An infinity or NaN has no effect on rows that do not see its key.  In a
+ * value it makes the rows that see the key not finite, however small the key's
+ * weight and wherever the keys are cut.  A score of NaN or +infinity makes its
+ * row NaN; one of -infinity leaves its key no weight, and a row of which all
+ * scores are -infinity is as one without keys.
  * Outputs are summed in float32 before they are divided by the sum of the
  * probabilities, which are at most 2^8: values beyond 2^120 / keys may overflow.
  * batch == 0 or total_q == 0 is a no-op.  Three launches (plan, attention,

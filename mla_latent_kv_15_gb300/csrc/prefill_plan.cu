@@ -445,9 +445,11 @@ __global__ void __launch_bounds__(256) prefill_combine_kernel(const PrefillArgs 
       ref = top;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
+        // a piece without a key has zeros; one whose weight is too small for a
+        // float still counts, so that 0 * inf is NaN as in an item that is not cut
         const float w = l[e] == -INFINITY ? 0.f : expf(l[e] - sub);
         sum += w;
-        if (w != 0.f) o.x += w * v[e].x, o.y += w * v[e].y, o.z += w * v[e].z, o.w += w * v[e].w;
+        o.x += w * v[e].x, o.y += w * v[e].y, o.z += w * v[e].z, o.w += w * v[e].w;
       }
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;

@@ -1,4 +1,5 @@
-"""GPU tests of the prefill whose values say which key they belong to.
+"""GPU tests of the prefill whose values say which key they belong to, and of
+values that are not finite across the cuts.
 
 A value row is zero but for one dim, the key's tile (or its place in the tile)
 modulo 128, so an output is a sum of probabilities of a few tiles' keys, all
@@ -64,3 +65,26 @@ def test_prefill_takes_every_key_of_a_tile_once(q_lens, kv_lens, heads, causal):
     c = Case(q_lens, kv_lens, heads, seed=52)
     mark(c, kv_lens, lambda j: j % 128, lambda j: 1.0 + j // 128)
     check(c.run(causal), causal)
+
+
+@pytest.mark.parametrize("low", [0, 1, 3])
+@pytest.mark.parametrize("splits", [0, 1, 4])
+def test_prefill_value_that_is_not_finite_counts_wherever_the_keys_are_cut(low, splits):
+    """A quarter of the keys scores 150 below the others, so that all its
+    probabilities are zeros in float32.  An infinity among their values makes
+    the output not finite all the same (0 * inf), in one piece or cut."""
+    keys = 4096
+    c = Case([1, 2], [keys, keys], 1, seed=53, splits=splits)
+    level = torch.zeros(keys, device="cuda")
+    level[1024 * low:1024 * (low + 1)] = -150.0
+    c.q[..., 128:] = 0
+    c.q[..., 128] = 1.0
+    c.k_pe[:, 0] = (level.repeat(2) / SCALE).to(torch.bfloat16)
+    c.kv[1024 * low + 100, 0, 128 + 5] = float("inf")          # of the first sequence
+    c.kv[1024 * low + 300, 0, 128 + 77] = float("nan")
+    c.run()
+    torch.cuda.synchronize()
+    want = torch.zeros_like(c.out, dtype=torch.bool)
+    want[0, 0, 5] = want[0, 0, 77] = True
+    assert torch.equal(~torch.isfinite(c.out), want)
+    assert torch.isfinite(c.lse).all()
