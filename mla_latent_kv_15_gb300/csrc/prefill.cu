@@ -952,8 +952,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == kWarpLoad) {
       load_items(a, ctx, slots, &tm_q, &tm_kv, &tm_pe, smem_u32(q_smem), smem_u32(ring), lane);
     } else if (warp == kWarpMma) {
-      if (rank == 0) issue_items(ctx, slots, tbase, smem_u32(q_smem), smem_u32(ring), lane);
-      wait_bar(ctx, &bars->drain, 0, kItemWait);   // every product of the pair is done
+      if (rank == 0) {
+        issue_items(ctx, slots, tbase, smem_u32(q_smem), smem_u32(ring), lane);
+        wait_bar(ctx, &bars->drain, 0);   // every product of the pair is done
+      }
     } else if (warp == kWarpList) {
       if (rank == 0 && a.direct)
         list_direct(a, ctx, slots, lane);
@@ -977,6 +979,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc_fence_before();
   cluster_sync();   // the pair ends together: each reads and signals the other's shared memory
   if (warp == kWarpMma) {
+    // The last signal to the peer's own barriers is on its way by now.  Awaited
+    // earlier, from the kernel's start, the wait would bound the whole call.
+    if (rank == 1) wait_bar(ctx, &bars->drain, 0);
+    __syncwarp();
     tc_fence_after();
     tmem_dealloc_pair(tbase, 512);
   }

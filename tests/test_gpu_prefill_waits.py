@@ -1,0 +1,39 @@
+"""GPU tests of the prefill's bounded waits where nothing is wrong: a limit on
+one wait does not limit the call or an item, whose lengths are the work's."""
+import pytest
+import torch
+
+from test_gpu_prefill import Case
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    import mla_latent_kv_15_gb300 as mla
+
+
+def same_under_a_short_limit(c, limit_ns, causal):
+    c.run(causal)
+    torch.cuda.synchronize()
+    assert mla.prefill_status(c.ws) == 0
+    out, lse = c.out.clone(), c.lse.clone()
+    c.out.fill_(7.0)
+    begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    try:
+        mla.set_decode_wait_test(wait_limit_ns=limit_ns)
+        begin.record()
+        c.run(causal)
+        end.record()
+        torch.cuda.synchronize()
+        assert mla.prefill_status(c.ws) == 0
+    finally:
+        mla.set_decode_wait_test()
+    assert torch.equal(c.out, out) and torch.equal(c.lse, lse)
+    return begin.elapsed_time(end) * 1e6
+
+
+def test_prefill_outlasts_the_limit_of_its_waits_for_an_item():
+    """Thousands of items, each far below the limit of a wait for an item (64
+    times that of the others), the call above it."""
+    c = Case([24576], [24576], 128, seed=61)
+    took = same_under_a_short_limit(c, 150_000, True)
+    assert took > 64 * 150_000, f"the call took {took / 1e6:.2f} ms: too short to tell"
