@@ -95,8 +95,8 @@ struct Ctx {
 // Bounded waits; once one has run out, every other one of the CTA returns, and
 // the peer's run out in turn.  The time in which rows are mended, which ends by
 // itself but may be long, does not count.  kCluster: the acquire covers what the other CTA
-// has written to shared memory.  Waits for an item may last as long as the
-// item before it (`times` the limit).
+// has written to shared memory.  Waits for an item, or for its last keys, may
+// last as long as an item (`times` the limit).
 template <bool kCluster = false>
 __device__ __forceinline__ void wait_bar(const Ctx& c, uint64_t* bar, uint32_t parity, uint32_t times = 1) {
   const uint32_t at = smem_u32(bar);
@@ -495,7 +495,7 @@ __device__ __forceinline__ void clear_tails(const Ctx& ctx, const Item* slots, u
     n += tiles;
     if (tiles == 0 || !has_tail(it, tiles)) continue;
     const uint32_t stage = (n - 1) % kStages;
-    wait_bar(ctx, &bars->v_tail[stage], (used >> stage) & 1);
+    wait_bar(ctx, &bars->v_tail[stage], (used >> stage) & 1, kItemWait);   // from the item's start to its last keys
     used ^= 1u << stage;
     const int left = it.nkeys - (tiles - 1) * kPrefillTile, rows = 16 - (left & 15);
     uint8_t* v = ring + stage * kStage + kKeyBytes + left * 128;

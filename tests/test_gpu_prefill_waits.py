@@ -37,3 +37,11 @@ def test_prefill_outlasts_the_limit_of_its_waits_for_an_item():
     c = Case([24576], [24576], 128, seed=61)
     took = same_under_a_short_limit(c, 150_000, True)
     assert took > 64 * 150_000, f"the call took {took / 1e6:.2f} ms: too short to tell"
+
+
+def test_prefill_item_with_a_ragged_end_outlasts_the_limit_of_a_wait():
+    """The last value rows of an item, which are cleared past the sequence's
+    end, are awaited from the item's start."""
+    c = Case([512], [60005], 8, seed=62, splits=1)
+    took = same_under_a_short_limit(c, 100_000, False)
+    assert took > 2 * 100_000, f"the call took {took / 1e6:.2f} ms: too short to tell"
