@@ -315,8 +315,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       }
       if (elect_one()) mma_commit_pair(smem_u32(&bars->drain));
       __syncwarp();
+      pair_wait(bars, &bars->drain, 0);   // every product of the pair is done
     }
-    pair_wait(bars, &bars->drain, 0);   // every product of the pair is done
   } else {
     const int q = warp & 3;
     uint8_t* stage = staging + q * kPieces * kPiece;
@@ -378,6 +378,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   tc_fence_before();
   cluster_sync();   // the pair ends together: each reads and signals the other's shared memory
   if (warp == 1) {
+    // the last signal to the peer's own barriers is on its way by now (awaited
+    // from the kernel's start, the wait would bound the whole call)
+    if (rank == 1) pair_wait(bars, &bars->drain, 0);
+    __syncwarp();
     tc_fence_after();
     tmem_dealloc_pair(tmem, P::kTmem);
   }
