@@ -724,7 +724,16 @@ int mla_prefill(const void* q, int64_t q_token_stride, int64_t q_head_stride, co
 }
 
 int mla_prefill_status(const void* workspace, int* status, void* stream) {
-  return mla_decode_status(workspace, status, stream);   // the header's first word, as a decode's
+  if (!workspace || !status) return fail(MLA_ERR_INVALID_ARG, "null pointer argument");
+  mla::PrefillHeader h;
+  cudaError_t e = cudaMemcpyAsync(&h, workspace, sizeof h, cudaMemcpyDeviceToHost, (cudaStream_t)stream);
+  if (e == cudaSuccess) e = cudaStreamSynchronize((cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "status read");
+  int bits = h.status;
+  for (int i = 0; i < h.ctas && i < 2 * mla::kPrefillMaxPairs; ++i)
+    if (h.gave_up[i]) bits |= MLA_DEVERR_TIMEOUT;
+  *status = bits;
+  return ok();
 }
 
 }  // extern "C"

@@ -86,14 +86,13 @@ static_assert(kSmem <= 232448, "shared memory per CTA");
 struct Ctx {
   Bars* bars;
   uint32_t rank;      // in the pair; 0 leads
-  int* status;
   uint64_t limit_ns;
   // shared::cluster address of the leading CTA's copy of one of `bars`
   __device__ __forceinline__ uint32_t lead(uint64_t* bar) const { return mapa(smem_u32(bar), 0); }
 };
 
 // Bounded waits; once one has run out, every other one of the CTA returns, and
-// the peer's run out in turn.  The time in which rows are mended, which ends by
+// the peer's run out in turn; the CTA reports it when it ends.  The time in which rows are mended, which ends by
 // itself but may be long, does not count.  kCluster: the acquire covers what the other CTA
 // has written to shared memory.  Waits for an item, or for its last keys, may
 // last as long as an item (`times` the limit).
@@ -107,7 +106,6 @@ __device__ __forceinline__ void wait_bar(const Ctx& c, uint64_t* bar, uint32_t p
     if (*(volatile int*)&c.bars->mending) t0 = globaltimer();
     if (globaltimer() - t0 > c.limit_ns * times) {
       *(volatile int*)&c.bars->abort = 1;
-      atomicOr(c.status, 1);   // MLA_DEVERR_TIMEOUT
       return;
     }
   }
@@ -942,7 +940,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // everything above overlaps the kernel before (the plan)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const Ctx ctx{bars, rank, &a.plan.header->status, a.wait_limit_ns};
+  const Ctx ctx{bars, rank, a.wait_limit_ns};
 
   if (warp < kSoftmaxWarps) {
     setmaxnreg_inc<kRegsSoftmax>();
@@ -983,6 +981,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // earlier, from the kernel's start, the wait would bound the whole call.
     if (rank == 1) wait_bar(ctx, &bars->drain, 0);
     __syncwarp();
+    if (lane == 0) {
+      a.plan.header->gave_up[blockIdx.x] = *(volatile int*)&bars->abort;
+      if (blockIdx.x == 0) a.plan.header->ctas = gridDim.x;
+    }
     tc_fence_after();
     tmem_dealloc_pair(tbase, 512);
   }

@@ -17,15 +17,18 @@ constexpr int kPrefillMaxPairs = 80; // upper bound of the grid (one CTA per SM,
 // block  = up to 512 consecutive query rows of one sequence (the same for every head)
 // piece  = a block's keys [kv0, kv0 + nkeys), cut at multiples of a tile
 // item   = a piece and a head: what a CTA pair processes
+// A call's errors have a word for each writer, all of them stored by every call
+// and joined by the host's read: nothing orders the CTAs' stores.
 struct PrefillHeader {
-  int status;        // OR of mla_device_error bits
+  int status;        // OR of mla_device_error bits of the prefix sums
   int num_pieces;
   int num_split;     // blocks cut into more than one piece
   int next;          // items handed out beyond every pair's first
   int fixed;         // 1: the pieces name their heads and the pairs have theirs from first_piece
   int split_rows;    // rows x heads of the split blocks
   int group_heads;   // heads whose items are interleaved
-  int pad;
+  int ctas;          // grid of the attention kernel
+  int gave_up[2 * kPrefillMaxPairs];   // by CTA: 1 if a bounded wait ran out
 };
 
 struct PrefillPiece {  // 32 bytes

@@ -45,3 +45,30 @@ def test_prefill_item_with_a_ragged_end_outlasts_the_limit_of_a_wait():
     c = Case([512], [60005], 8, seed=62, splits=1)
     took = same_under_a_short_limit(c, 100_000, False)
     assert took > 2 * 100_000, f"the call took {took / 1e6:.2f} ms: too short to tell"
+
+
+@pytest.mark.parametrize("q_lens,kv_lens,heads", [([300], [300], 2), ([1] * 8, [3000] * 8, 16), ([1] * 40, [3000] * 40, 1),
+                                                  ([600] * 3, [700] * 3, 128)])
+def test_prefill_status_is_of_the_last_call(q_lens, kv_lens, heads):
+    """One launch, two and three: whatever the workspace held, a clean call
+    reads clean, one whose keys never arrive and one of inconsistent sums say
+    so, and the next is clean again."""
+    c = Case(q_lens, kv_lens, heads, seed=63)
+    cu_q = c.cu_q.clone()
+    for junk in (0xFF, 0x01, 0xEE):
+        c.ws.fill_(junk)
+        c.run()
+        assert mla.prefill_status(c.ws) == 0
+        try:
+            mla.set_decode_wait_test(skip_first_tile=True, wait_limit_ns=2_000_000)
+            c.run()
+            assert mla.prefill_status(c.ws) == mla.DEVERR_TIMEOUT
+        finally:
+            mla.set_decode_wait_test()
+        c.ws.fill_(junk)
+        c.cu_q[-1] = c.q.shape[0] + 1
+        c.run()
+        assert mla.prefill_status(c.ws) == mla.DEVERR_BAD_QSL
+        c.cu_q.copy_(cu_q)
+        c.out.fill_(7.0)
+        c.run().check()
