@@ -443,6 +443,7 @@ MLA_API int mla_gather_cache(const void* cache, int64_t num_blocks, int page_siz
  *                   strides: in place), else it overlaps no other argument (column
  *                   ranges of the same rows do not overlap)
  *   status          one int32 on the device, or NULL: OR-ed into, never cleared
+ * The cache and latent overlap no other argument, but for latent's rows in place.
  * All strides are multiples of 8 elements, all tensors 16-byte aligned.
  * num_tokens in [0, 8388480]; 0 is a no-op.  One launch.
  */

@@ -497,6 +497,7 @@ Extent extent(const void* p, int64_t n0, int64_t s0, int64_t n1, int64_t s1, int
   const uintptr_t pitch = (uintptr_t)(s0 * elem_bytes);
   return Extent{lo, lo + (uintptr_t)((n0 - 1) * s0 * elem_bytes) + row, row, n0 > 1 && row <= pitch ? pitch : 0};
 }
+Extent dense(const void* p, int64_t bytes) { return extent(p, 1, 0, 1, 0, bytes, 1); }
 // Whether two tensors may share bytes (column ranges of the same pitched
 // rows are told apart, other strided layouts by their first and last bytes).
 bool overlap(const Extent& a, const Extent& b) {
@@ -545,17 +546,29 @@ int mla_rope_cache_write(const void* kv_c, int64_t kv_c_stride, const void* k_pe
     return fail(MLA_ERR_INVALID_ARG, "kv_c_stride and k_pe_stride must be multiples of 8 in [0, 2^32]");
   if (latent && !valid_stride(latent_stride, mla::kDqk))
     return fail(MLA_ERR_INVALID_ARG, "latent_stride must be a multiple of 8 in [576, 2^32]");
-  const Extent ec = extent(cache, 1, 0, 1, 0, num_blocks * page_size * mla::kDqk, cache_dtype == MLA_BF16 ? 2 : 1);
+  const Extent ec = dense(cache, num_blocks * page_size * mla::kDqk * (cache_dtype == MLA_BF16 ? 2 : 1));
   const Extent ek = extent(kv_c, num_tokens, kv_c_stride, 1, 0, mla::kLkv, 2);
   const Extent ep = extent(k_pe, num_tokens, k_pe_stride, 1, 0, mla::kRope, 2);
-  if (overlap(ec, ek) || overlap(ec, ep)) return fail(MLA_ERR_INVALID_ARG, "the cache must not overlap the inputs");
+  // what every token's rows depend on, and the status word (a table larger
+  // than any memory is one of unknown size)
+  const int64_t table_rows = max_positions < (1LL << 31) ? max_positions : 1;
+  const Extent shared[] = {dense(positions, num_tokens * 8), dense(slot_mapping, num_tokens * 8),
+                           dense(cos_sin, table_rows * mla::kRope * 4), dense(norm_weight, mla::kLkv * 2),
+                           dense(status, 4)};
+  auto overlaps_shared = [&](const Extent& x) {
+    for (const Extent& s : shared)
+      if (s.lo && overlap(x, s)) return true;
+    return false;
+  };
+  if (overlap(ec, ek) || overlap(ec, ep) || overlaps_shared(ec))
+    return fail(MLA_ERR_INVALID_ARG, "the cache must not overlap the inputs");
   Extent el{0, 0};
   if (latent) {
     el = extent(latent, num_tokens, latent_stride, 1, 0, mla::kDqk, 2);
     // in place: the latent rows are the input rows themselves
     const bool same = latent == kv_c && static_cast<const char*>(k_pe) == static_cast<char*>(latent) + 2 * mla::kLkv &&
                       (num_tokens == 1 || (latent_stride == kv_c_stride && latent_stride == k_pe_stride));
-    if (overlap(el, ec) || (!same && (overlap(el, ek) || overlap(el, ep))))
+    if (overlap(el, ec) || overlaps_shared(el) || (!same && (overlap(el, ek) || overlap(el, ep))))
       return fail(MLA_ERR_INVALID_ARG, "latent must not overlap the cache, nor the inputs unless it is their rows");
   }
   mla::RopeWriteArgs w{kv_c,          kv_c_stride,   k_pe,       k_pe_stride,
@@ -577,7 +590,7 @@ int mla_rope_cache_write(const void* kv_c, int64_t kv_c_stride, const void* k_pe
     const bool same = q_pe == q_pe_out && (num_tokens == 1 || q_token_stride == q_out_token_stride) &&
                       (num_heads == 1 || q_head_stride == q_out_head_stride);
     if ((!same && overlap(eq, eo)) || overlap(eo, ec) || overlap(eo, ek) || overlap(eo, ep) || overlap(eq, ec) ||
-        (latent && (overlap(el, eo) || overlap(el, eq))))
+        overlaps_shared(eo) || (latent && (overlap(el, eo) || overlap(el, eq))))
       return fail(MLA_ERR_INVALID_ARG, "q_pe_out must be q_pe itself or overlap no other argument");
   }
   cudaError_t e = mla::launch_rope_write(w, cache_dtype == MLA_FP8_E4M3, interleaved != 0, (cudaStream_t)stream);

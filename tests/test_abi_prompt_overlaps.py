@@ -1,0 +1,45 @@
+"""CPU checks that the prompt-side entry points refuse outputs over arguments
+they read or write.  The addresses are never dereferenced: every call here is
+refused on the host."""
+import ctypes
+
+import pytest
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from mla_latent_kv_15_gb300 import _build
+    import mla_latent_kv_15_gb300 as mla
+    _build.build()
+    return mla.load()
+
+
+P = ctypes.c_void_p
+
+
+def at(mib, more=0):
+    return P((mib << 20) + more)
+
+
+ROPE_NAMES = ("kv_c kvs k_pe pes weight eps positions table max_pos pairs slots T cache nb page dtype kv_scale latent "
+              "ls q qts qhs N qo qots qohs status stream").split()
+ROPE = dict(kv_c=at(1), kvs=576, k_pe=at(100), pes=64, weight=at(200), eps=1e-6, positions=at(201), table=at(300),
+            max_pos=100, pairs=1, slots=at(202), T=8, cache=at(400), nb=10, page=64, dtype=0, kv_scale=1.0,
+            latent=at(500), ls=576, q=at(600), qts=20 * 192, qhs=192, N=20, qo=at(700), qots=20 * 64, qohs=64,
+            status=at(203), stream=None)
+
+
+@pytest.mark.parametrize("name,offset", [("weight", 512), ("positions", 32), ("slots", 32), ("table", 25600 - 16),
+                                         ("status", 0)])
+def test_append_outputs_over_what_all_tokens_read(lib, name, offset):
+    def refuse(text, **over):
+        rc = lib.mla_rope_cache_write(*[dict(ROPE, **over)[n] for n in ROPE_NAMES])
+        assert rc == -1 and text.encode() in lib.mla_last_error(), (rc, lib.mla_last_error())
+
+    there = P(ROPE[name].value + offset)
+    refuse("cache must not overlap", cache=there)
+    refuse("latent must not overlap", latent=there)
+    refuse("q_pe_out must be q_pe", qo=there)
+    # one row before it, and a table of unknown size (only its first row is known)
+    refuse("q_pe strides", latent=P(ROPE[name].value - 8 * 1152), qts=20)
+    refuse("q_pe strides", max_pos=1 << 62, qts=20)
