@@ -519,9 +519,10 @@ MLA_API size_t mla_prefill_workspace_size(int batch, int total_q, int num_heads,
  *               k > 0: every block of query rows is cut into min(k, tiles) pieces
  *   out         [total_q, num_heads, 128] bf16, dense, 32-byte aligned; overlaps
  *               no input
- *   lse         [total_q, num_heads] float32, or NULL
+ *   lse         [total_q, num_heads] float32, or NULL; overlaps no other argument
  *   workspace   >= mla_prefill_workspace_size(batch, total_q, num_heads,
- *               num_splits) bytes, 256-byte aligned; scratch only.  Calls that
+ *               num_splits) bytes, 256-byte aligned; scratch only, and those bytes
+ *               overlap no other argument.  Calls that
  *               may overlap on the GPU need a workspace each
  * An infinity or NaN has no effect on rows that do not see its key.  In a
  * value it makes the rows that see the key not finite, however small the key's

@@ -663,17 +663,30 @@ int mla_prefill(const void* q, int64_t q_token_stride, int64_t q_head_stride, co
       !valid_stride(kv_head_stride, 8) || !valid_stride(k_pe_stride, 8))
     return fail(MLA_ERR_INVALID_ARG, "strides must be multiples of 8 in [8, 2^32]");
   const int qd = mla::kNope + mla::kRope, kvd = 2 * mla::kNope;
-  const Extent eo = extent(out, 1, 0, 1, 0, (int64_t)total_q * num_heads * mla::kNope, 2);
-  if (overlap(eo, extent(q, total_q, q_token_stride, num_heads, q_head_stride, qd, 2)) ||
-      (total_kv > 0 && (overlap(eo, extent(kv, total_kv, kv_token_stride, num_heads, kv_head_stride, kvd, 2)) ||
-                        overlap(eo, extent(k_pe, total_kv, k_pe_stride, 1, 0, mla::kRope, 2)))))
-    return fail(MLA_ERR_INVALID_ARG, "out must not overlap the inputs");
+  const int64_t rows = (int64_t)total_q * num_heads;
+  const Extent eo = dense(out, rows * mla::kNope * 2), es = dense(lse, rows * 4);
+  const Extent inputs[] = {extent(q, total_q, q_token_stride, num_heads, q_head_stride, qd, 2),
+                           dense(cu_q, (batch + 1LL) * 4), dense(cu_kv, (batch + 1LL) * 4),
+                           extent(kv, total_kv, kv_token_stride, num_heads, kv_head_stride, kvd, 2),
+                           extent(k_pe, total_kv, k_pe_stride, 1, 0, mla::kRope, 2)};
+  const int num_inputs = total_kv > 0 ? 5 : 3;
+  auto overlaps_inputs = [&](const Extent& x) {
+    for (int i = 0; i < num_inputs; ++i)
+      if (overlap(x, inputs[i])) return true;
+    return false;
+  };
+  if (overlaps_inputs(eo)) return fail(MLA_ERR_INVALID_ARG, "out must not overlap the inputs");
   const mla::PrefillLayout L = mla::prefill_layout(batch, total_q, num_heads, num_splits);
   if (L.max_part_rows >= 1LL << 31) return fail(MLA_ERR_UNSUPPORTED, "total_q * num_heads * num_splits must be below 2^31");
   if (L.max_pieces * num_heads >= (1LL << 31) - 4096)
     return fail(MLA_ERR_UNSUPPORTED, "batch * num_heads is too large");
+  if (lse && (overlap(es, eo) || overlaps_inputs(es)))
+    return fail(MLA_ERR_INVALID_ARG, "lse must not overlap out or the inputs");
   if (workspace_bytes < L.total)
     return fail(MLA_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu required", workspace_bytes, L.total);
+  const Extent ew = dense(workspace, (int64_t)L.total);
+  if (overlap(ew, eo) || (lse && overlap(ew, es)) || overlaps_inputs(ew))
+    return fail(MLA_ERR_INVALID_ARG, "the workspace must not overlap the other arguments");
   const int sms = sm_count();
   if (sms < 2) return fail(MLA_ERR_CUDA, "cannot query the current device");
 

@@ -43,3 +43,30 @@ def test_append_outputs_over_what_all_tokens_read(lib, name, offset):
     # one row before it, and a table of unknown size (only its first row is known)
     refuse("q_pe strides", latent=P(ROPE[name].value - 8 * 1152), qts=20)
     refuse("q_pe strides", max_pos=1 << 62, qts=20)
+
+
+PREFILL_NAMES = "q qts qhs kv kts khs pe pes cu_q cu_kv B T Tk N scale causal splits out lse ws wsb stream".split()
+
+
+@pytest.mark.parametrize("name,offset", [("q", 100 * 4 * 192 * 2 - 256), ("kv", 256), ("pe", 256), ("cu_q", 0), ("cu_kv", 0),
+                                         ("out", 256), ("lse", 1024)])
+def test_prefill_outputs_over_other_arguments(lib, name, offset):
+    need = lib.mla_prefill_workspace_size(2, 100, 4, 0)
+    good = dict(q=at(1), qts=768, qhs=192, kv=at(100), kts=1024, khs=256, pe=at(200), pes=576, cu_q=at(300),
+                cu_kv=at(301), B=2, T=100, Tk=500, N=4, scale=0.07, causal=1, splits=0, out=at(400), lse=at(500),
+                ws=at(600), wsb=need + (1 << 20), stream=None)
+
+    def refuse(text, **over):
+        rc = lib.mla_prefill(*[dict(good, **over)[n] for n in PREFILL_NAMES])
+        assert rc in (-1, -4) and text.encode() in lib.mla_last_error(), (rc, lib.mla_last_error())
+
+    there = P(good[name].value + offset)
+    if name not in ("out", "lse"):
+        refuse("out must not overlap", out=there)
+    if name != "lse":
+        refuse("lse must not overlap", lse=there)
+    refuse("workspace must not overlap", ws=there)
+    # right behind the bytes a call needs there may be anything
+    refuse("smaller than", lse=P(there.value - 100 * 4 * 4) if name in ("cu_q", "cu_kv") else at(900), wsb=need - 1)
+    # without a key, the key tensors are not read
+    refuse("smaller than", Tk=0, out=at(100), lse=at(200), wsb=need - 1)
