@@ -6,6 +6,7 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <numeric>
 #include <string>
 
 #include "../../include/mla.h"
@@ -485,26 +486,35 @@ int mla_proj_status(int* status, int clear, void* stream) {
 namespace {
 
 // Bytes [lo, hi) of a strided tensor of `n0` x `n1` rows of `width` elements
-// (strides in elements).  Where the outer stride holds all the inner rows,
-// the tensor is columns [0, row) of a pitched one.
+// (strides in elements).  Every row of `width` bytes begins a multiple of
+// `step` bytes behind lo (0: there is one row).  Where the outer stride holds
+// all the inner rows, the tensor is columns [0, row) of a pitched one.
 struct Extent {
   uintptr_t lo, hi;
+  uintptr_t width, step;
   uintptr_t row, pitch;
 };
 Extent extent(const void* p, int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t width, int64_t elem_bytes) {
   const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
   const uintptr_t row = (uintptr_t)(((n1 - 1) * s1 + width) * elem_bytes);
-  const uintptr_t pitch = (uintptr_t)(s0 * elem_bytes);
-  return Extent{lo, lo + (uintptr_t)((n0 - 1) * s0 * elem_bytes) + row, row, n0 > 1 && row <= pitch ? pitch : 0};
+  const uintptr_t outer = (uintptr_t)(s0 * elem_bytes), inner = (uintptr_t)(s1 * elem_bytes);
+  return Extent{lo, lo + (uintptr_t)(n0 - 1) * outer + row, (uintptr_t)(width * elem_bytes),
+                std::gcd(n0 > 1 ? outer : 0, n1 > 1 ? inner : 0), row, n0 > 1 && row <= outer ? outer : 0};
 }
 Extent dense(const void* p, int64_t bytes) { return extent(p, 1, 0, 1, 0, bytes, 1); }
-// Whether two tensors may share bytes (column ranges of the same pitched
-// rows are told apart, other strided layouts by their first and last bytes).
+// Whether `a` bytes and `b` bytes from two addresses, repeated every `step`, share some.
+bool columns_meet(uintptr_t a_lo, uintptr_t a, uintptr_t b_lo, uintptr_t b, uintptr_t step) {
+  const uintptr_t d = b_lo >= a_lo ? (b_lo - a_lo) % step : (step - (a_lo - b_lo) % step) % step;
+  return !(d >= a && d + b <= step);
+}
+// Whether two tensors may share bytes (column ranges of the same pitched rows,
+// of tokens or of heads, are told apart, other strided layouts by their first
+// and last bytes).
 bool overlap(const Extent& a, const Extent& b) {
   if (!(a.lo < b.hi && b.lo < a.hi)) return false;
-  if (a.pitch == 0 || a.pitch != b.pitch) return true;
-  const uintptr_t d = b.lo >= a.lo ? (b.lo - a.lo) % a.pitch : (a.pitch - (a.lo - b.lo) % a.pitch) % a.pitch;
-  return !(d >= a.row && d + b.row <= a.pitch);
+  if (a.pitch && a.pitch == b.pitch && !columns_meet(a.lo, a.row, b.lo, b.row, a.pitch)) return false;
+  const uintptr_t step = std::gcd(a.step, b.step);
+  return step == 0 || columns_meet(a.lo, a.width, b.lo, b.width, step);
 }
 
 constexpr int64_t kMaxStride = 1LL << 32;   // elements

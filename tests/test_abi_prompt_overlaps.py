@@ -70,3 +70,17 @@ def test_prefill_outputs_over_other_arguments(lib, name, offset):
     refuse("smaller than", lse=P(there.value - 100 * 4 * 4) if name in ("cu_q", "cu_kv") else at(900), wsb=need - 1)
     # without a key, the key tensors are not read
     refuse("smaller than", Tk=0, out=at(100), lse=at(200), wsb=need - 1)
+
+
+@pytest.mark.parametrize("T,N", [(8, 20), (1, 20), (8, 1)])
+@pytest.mark.parametrize("head_major", [False, True])
+@pytest.mark.parametrize("first", [16, 56, -16, -56, 256 - 56])
+def test_append_rotated_queries_that_meet_their_source_in_some_columns(lib, T, N, head_major, first):
+    """Queries and rotated queries in the same 256-wide rows of heads, `first`
+    columns apart: fewer than 64 forwards, backwards or round the row's end."""
+    ts, hs = (256, T * 256) if head_major else (N * 256, 256)
+    names = dict(qts=ts, qhs=hs, qots=ts, qohs=hs, T=T, N=N, q=at(600, 256), qo=at(600, 256 + 2 * first), latent=None)
+    if first > 64 and T * N == 1:
+        return                           # one row: behind it lies nothing
+    rc = lib.mla_rope_cache_write(*[dict(ROPE, **names)[n] for n in ROPE_NAMES])
+    assert rc == -1 and b"q_pe_out must be q_pe" in lib.mla_last_error(), (rc, lib.mla_last_error())
