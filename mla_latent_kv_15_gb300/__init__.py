@@ -231,7 +231,7 @@ def _head_strides(t, name: str, rows: int, heads, width: int, bf16, writable: bo
         s0, s1, s2 = t.stride() if n >= 0 else (0, 0, 0)
         if n == rows and (heads is None or h == heads) and w == width and s2 == 1 and h > 1 and s1 > 0 and not s1 & 7:
             if n == 1:
-                return h * s1, s1
+                return w, s1                 # there is no next row
             if s0 > 0 and not s0 & 7:
                 return s0, s1
     return _rows(t, name, (rows, heads, width), writable)
