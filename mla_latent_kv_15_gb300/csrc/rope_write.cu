@@ -51,6 +51,10 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
   return v;
 }
 
+// Plain loads throughout: the kernel may start beside the one before it (a
+// programmatic dependent), which may still be writing what this one reads, and
+// the read-only path is for memory that nobody writes while the kernel runs.
+
 // The table entries a thread's two vectors (dims 8v.. and 8v+32.., v < 4) need.
 // Pairs (2k, 2k+1): entries 4v..4v+3 for the first vector, 4v+16.. for the
 // second; pairs (k, k+32): entries 8v..8v+7 for both.
@@ -59,13 +63,13 @@ struct Turn {
 };
 
 template <bool kPairs>
-__device__ __forceinline__ Turn load_turn(const float* __restrict__ row, int v) {
+__device__ __forceinline__ Turn load_turn(const float* row, int v) {
   Turn t;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int at = kPairs ? 4 * v + 16 * h : 8 * v + 4 * h;
-    const float4 c = __ldg(reinterpret_cast<const float4*>(row + at));
-    const float4 s = __ldg(reinterpret_cast<const float4*>(row + 32 + at));
+    const float4 c = *reinterpret_cast<const float4*>(row + at);
+    const float4 s = *reinterpret_cast<const float4*>(row + 32 + at);
     t.cos[4 * h] = c.x, t.cos[4 * h + 1] = c.y, t.cos[4 * h + 2] = c.z, t.cos[4 * h + 3] = c.w;
     t.sin[4 * h] = s.x, t.sin[4 * h + 1] = s.y, t.sin[4 * h + 2] = s.z, t.sin[4 * h + 3] = s.w;
   }
@@ -145,8 +149,8 @@ __device__ __forceinline__ void latent_row(const RopeWriteArgs& w, int64_t tok, 
     const float r = 1.0f / sqrtf(ss * (1.0f / kLkv) + w.norm_eps);
     const uint4* g = static_cast<const uint4*>(w.norm_weight);
     float g0[8], g1[8];
-    unpack8(__ldg(g + lane), g0);
-    unpack8(__ldg(g + lane + 32), g1);
+    unpack8(g[lane], g0);
+    unpack8(g[lane + 32], g1);
 #pragma unroll
     for (int k = 0; k < 8; ++k) x0[k] = x0[k] * r * g0[k], x1[k] = x1[k] * r * g1[k];
   }
