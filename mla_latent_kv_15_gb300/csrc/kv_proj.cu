@@ -443,24 +443,33 @@ cudaError_t launch_few(const CUtensorMap& tm_x, const CUtensorMap& tm_w, void* y
 
 // Up to 128 tokens a single CTA's tile holds them all and the weights' traffic
 // wants many CTAs: 32 columns each while that makes no more CTAs than SMs, for
-// the shorter products and stores (37 or 128 tokens x 4096 columns: 4.2 us a
-// launch among others, with 128 columns 4.6 and 5.2), else 128 (64 tokens x
-// 32768: 8.7 us, with 32 columns 17.7, with 64 11.7, pairs 12.3).  Above, pairs:
-// 128, 192 or 256 columns a tile, whichever costs least: the rounds of all pairs
-// at 129 : 161 : 200 (the wider tile reads less for a product), and 62 for the
-// last stores of the wider ones.  Measured, us a launch among others, rounds in
-// brackets:     128         192         256
-//   200 x 16384   6.5 (2)     7.9 (2)     7.2 (1)
-//  1021 x  5120   7.9 (3)     7.1 (2)     8.2 (2)
-//  2048 x 10240  21.4 (9)    18.5 (6)    19.3 (5)
-//  4096 x  4096  18.7 (7)    17.4 (5)    15.6 (4)
-//  8192 x 32768   213 (108)   191 (72)    182 (54)
+// the shorter products and stores, else 128.  Measured, us a launch among others
+// in a graph, weights in L2:  32 columns   128
+//    37 tokens x 4096                4.2   4.6
+//   128        x 4096                4.2   5.2
+//    37        x 5120 (160 CTAs)     4.9   4.7
+//    64        x 32768              17.7   8.7
+// Above, pairs: 128, 192 or 256 columns a tile, whichever costs least: the
+// rounds of all pairs at 100 : 120 : 140 (the wider tile reads less for a
+// product), and 45 and 70 for the last stores of the wider ones.  Constants from
+// 85 drawn shapes (129 to 8192 tokens, 256 to 32768 columns, weights from L2 and
+// from HBM), where the choice takes 0.1 % longer than the best width on average
+// and 3.8 % at most; on 60 others 0.04 % and 1.8 %.  One width for all would take
+// 7 % (128), 8 % (192) or 11 % (256) longer on average.  Some shapes, us a launch
+// as above in short bursts, rounds in brackets:
+//                   128         192         256
+//   200 x 16384    6.6 (2)     7.9 (2)     7.3 (1)
+//  1021 x  5120    8.1 (3)     7.2 (2)     8.4 (2)
+//  2048 x 10240   21.4 (9)    18.7 (6)    19.5 (5)
+//  4096 x  4096   17.5 (7)    16.4 (5)    15.9 (4)
+//  5386 x  7168   33.1 (17)   30.9 (11)   28.8 (9)
+//  8192 x 32768    206 (108)   183 (72)    168 (54)
 KvProjShape kv_proj_shape(int64_t T, int64_t C, int sms) {
   KvProjShape p{};
   p.pairs = sms / 2;
   if (T > kM && p.pairs > 0) {
     auto rounds = [&](int bn) { return ((T + 255) / 256 * ((C + bn - 1) / bn) + p.pairs - 1) / p.pairs; };
-    const int64_t c128 = 129 * rounds(128), c192 = 161 * rounds(192) + 62, c256 = 200 * rounds(256) + 62;
+    const int64_t c128 = 100 * rounds(128), c192 = 120 * rounds(192) + 45, c256 = 140 * rounds(256) + 70;
     p.pair_bn = c128 <= c192 && c128 <= c256 ? 128 : c192 < c256 ? 192 : 256;
     p.wrows = p.pair_bn / 2;
     p.xrows = kM;
