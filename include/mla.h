@@ -544,10 +544,11 @@ MLA_API int mla_prefill(const void* q, int64_t q_token_stride, int64_t q_head_st
                         void* workspace, size_t workspace_bytes, void* stream);
 
 /*
- * mla_prefill_status -- copy the device error word of the last mla_prefill
- * that used `workspace` (OR of mla_device_error bits; 0 = clean) to *status.
- * Synchronises `stream`.  The word is written anew by every mla_prefill that
- * launches (a no-op call leaves it as it was).
+ * mla_prefill_status -- the device error word of the last mla_prefill that
+ * used `workspace` (OR of mla_device_error bits; 0 = clean) to *status: joined
+ * here from a word of every CTA.  Synchronises `stream`.  The words are written
+ * anew by every mla_prefill that launches (a no-op call leaves them as they
+ * were).
  */
 MLA_API int mla_prefill_status(const void* workspace, int* status, void* stream);
 
