@@ -486,12 +486,12 @@ int mla_proj_status(int* status, int clear, void* stream) {
 namespace {
 
 // Bytes [lo, hi) of a strided tensor of `n0` x `n1` rows of `width` elements
-// (strides in elements).  Every row of `width` bytes begins a multiple of
-// `step` bytes behind lo (0: there is one row).  Where the outer stride holds
-// all the inner rows, the tensor is columns [0, row) of a pitched one.
+// (strides in elements); `outer` and `inner` are the strides that lead to more
+// than one row.  Where the outer one holds all the inner rows, the tensor is
+// columns [0, row) of a pitched one.
 struct Extent {
   uintptr_t lo, hi;
-  uintptr_t width, step;
+  uintptr_t width, outer, inner;
   uintptr_t row, pitch;
 };
 Extent extent(const void* p, int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t width, int64_t elem_bytes) {
@@ -499,7 +499,7 @@ Extent extent(const void* p, int64_t n0, int64_t s0, int64_t n1, int64_t s1, int
   const uintptr_t row = (uintptr_t)(((n1 - 1) * s1 + width) * elem_bytes);
   const uintptr_t outer = (uintptr_t)(s0 * elem_bytes), inner = (uintptr_t)(s1 * elem_bytes);
   return Extent{lo, lo + (uintptr_t)(n0 - 1) * outer + row, (uintptr_t)(width * elem_bytes),
-                std::gcd(n0 > 1 ? outer : 0, n1 > 1 ? inner : 0), row, n0 > 1 && row <= outer ? outer : 0};
+                n0 > 1 ? outer : 0, n1 > 1 ? inner : 0, row, n0 > 1 && row <= outer ? outer : 0};
 }
 Extent dense(const void* p, int64_t bytes) { return extent(p, 1, 0, 1, 0, bytes, 1); }
 // Whether `a` bytes and `b` bytes from two addresses, repeated every `step`, share some.
@@ -513,7 +513,8 @@ bool columns_meet(uintptr_t a_lo, uintptr_t a, uintptr_t b_lo, uintptr_t b, uint
 bool overlap(const Extent& a, const Extent& b) {
   if (!(a.lo < b.hi && b.lo < a.hi)) return false;
   if (a.pitch && a.pitch == b.pitch && !columns_meet(a.lo, a.row, b.lo, b.row, a.pitch)) return false;
-  const uintptr_t step = std::gcd(a.step, b.step);
+  // every row of both begins a multiple of `step` behind its tensor's first
+  const uintptr_t step = std::gcd(std::gcd(a.outer, a.inner), std::gcd(b.outer, b.inner));
   return step == 0 || columns_meet(a.lo, a.width, b.lo, b.width, step);
 }
 
