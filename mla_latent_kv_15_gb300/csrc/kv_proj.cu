@@ -22,7 +22,7 @@
 // two staged pieces a warp are enough (pieces 2, 4, 6, 8, leaving 6, 5, 4, 3
 // stages: 174, 181, 186, 200 us; the tokens kept in shared memory and only
 // weights streamed, four stages: 212; 32-byte stores from registers: 202).
-// Without the graph's launch 173 us back to back: 1590 TFLOP/s, 83 % of the
+// Without the graph's launch 173 us back to back in a long run: 1590 TFLOP/s, 83 % of the
 // library's burst rate and 94 % of its sustained one.
 #include <cuda_bf16.h>
 
@@ -463,7 +463,7 @@ cudaError_t launch_few(const CUtensorMap& tm_x, const CUtensorMap& tm_w, void* y
 //  2048 x 10240   21.4 (9)    18.7 (6)    19.5 (5)
 //  4096 x  4096   17.5 (7)    16.4 (5)    15.9 (4)
 //  5386 x  7168   33.1 (17)   30.9 (11)   28.8 (9)
-//  8192 x 32768    206 (108)   183 (72)    168 (54)
+//  8192 x 32768    206 (108)   183 (72)    168 (54)    (long runs, under the power cap: 173 to 187)
 KvProjShape kv_proj_shape(int64_t T, int64_t C, int sms) {
   KvProjShape p{};
   p.pairs = sms / 2;
