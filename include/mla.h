@@ -58,7 +58,7 @@ enum mla_device_error {
   MLA_DEVERR_BAD_SEQ_LEN = 2,   /* seq_len > max_pages_per_seq*page_size   */
   MLA_DEVERR_BAD_BLOCK = 4,     /* block-table entry outside [0,num_blocks) */
   MLA_DEVERR_BAD_QSL = 8,       /* query_start_loc inconsistent with total_q */
-  MLA_DEVERR_BAD_POSITION = 16  /* position outside the rotation table      */
+  MLA_DEVERR_BAD_POSITION = 16  /* position outside the rotation table, or a kept index out of place */
 };
 
 /*
@@ -553,6 +553,145 @@ MLA_API int mla_prefill(const void* q, int64_t q_token_stride, int64_t q_head_st
 MLA_API int mla_prefill_status(const void* workspace, int* status, void* stream);
 
 /*
+ * mla_decode_shared_workspace_size -- bytes of device workspace
+ * mla_decode_shared needs: mla_decode_workspace_size's arguments and the number
+ * of prefixes.  Depends on sizes only.
+ */
+MLA_API size_t mla_decode_shared_workspace_size(int batch, int prefixes, int total_q, int num_heads, int max_splits);
+
+/*
+ * mla_decode_shared -- mla_decode for requests that stand behind shared
+ * prefixes: requests prefix_requests[g] .. prefix_requests[g+1] - 1 share the
+ * prefix_lens[g] keys of row g of prefix_table, whose rows are read and scored
+ * once for all their query rows together, and each has its own keys behind
+ * them.  Query token t of request b (of its Sq_b) attends over
+ *
+ *   every key of its prefix, and its own keys j < seq_lens[b] - Sq_b + 1 + t
+ *
+ * in one softmax: out and lse are those of mla_decode over the concatenated
+ * keys (while seq_lens[b] >= Sq_b - 1; a request without own keys, a padded
+ * one too, gets the attention over its prefix).  A row that sees no key gets
+ * out = 0 and lse = -inf.
+ *   prefix_table     [prefixes, max_prefix_pages] int32: pages of each prefix
+ *   prefix_lens      [prefixes] int32 keys of each prefix; 0 is none
+ *   prefix_requests  [prefixes + 1] int32, non-decreasing, first 0, last batch
+ *                    (requests behind the same prefix follow one another)
+ *   block_table, seq_lens: each request's own pages and tokens (its query
+ *                    tokens included), from the first behind the prefix; a
+ *                    prefix need not end with a page
+ *   q_abs, q_pe, cache (bf16 or e4m3), page_size, query_start_loc, num_heads,
+ *   scale, num_splits, out, lse: as for mla_decode.  total_q * num_heads < 2^30,
+ *                    and a table's pages * page_size + total_q <= 2^30
+ *   workspace        >= mla_decode_shared_workspace_size(...) bytes, 256-byte
+ *                    aligned.  Calls that may overlap on the GPU need a
+ *                    workspace each
+ * Outputs and workspace overlap no other argument.  Rows of a page behind the
+ * last key are not looked at, whatever they hold.  Keys that are seen, and
+ * queries, are finite; one that is not leaves the outputs of the requests that
+ * read it unspecified, and no others.
+ * Device data: mla_decode_status(workspace) gives MLA_DEVERR_BAD_SEQ_LEN (a
+ * length beyond its table: cut to it), MLA_DEVERR_BAD_BLOCK (the page reads as
+ * zeros), MLA_DEVERR_BAD_QSL (prefix_requests or query_start_loc inconsistent:
+ * nothing is written).  Three launches, none of which depends on device data,
+ * so a captured call may be replayed over other lengths and groups.
+ */
+MLA_API int mla_decode_shared(const void* q_abs, const void* q_pe, const void* cache, int64_t num_blocks,
+                              int page_size, int cache_dtype, float kv_scale, const int32_t* prefix_table,
+                              int max_prefix_pages, const int32_t* prefix_lens, const int32_t* prefix_requests,
+                              int prefixes, const int32_t* block_table, int max_pages_per_seq,
+                              const int32_t* seq_lens, int batch, const int32_t* query_start_loc, int total_q,
+                              int num_heads, float scale, int num_splits, void* out, float* lse, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/*
+ * mla_key_weights -- how much attention each cached key of a request gets from
+ * all its query rows, accumulated over steps (what a cache that is to be kept
+ * small goes by):
+ *
+ *   weights[b, j] = decay * weights[b, j] + sum over (t, h) that see key j of
+ *                   exp(scale * (q_abs[t,h] . kv_c_j + q_pe[t,h] . k_pe_j) - lse[t, h])
+ *
+ * for j < seq_lens[b], with the window of mla_decode (token t of Sq sees keys
+ * j < seq_lens[b] - Sq + 1 + t).  Weights behind seq_lens[b] are left as they
+ * were.
+ *   lse          [total_q, num_heads] float32: the rows' natural-log
+ *                log-sum-exp, as mla_decode returns it (the weights of a row
+ *                then add up to 1) or mla_decode_shared (block_table and
+ *                seq_lens the requests' own: the weights of their own keys).
+ *                A row with lse = -inf gives no weight
+ *   decay        finite, >= 0; 0: the old weights are not read
+ *   weights      float32, weight_len a request at weights + b * weight_stride
+ *                elements (weight_stride in [weight_len, 2^32])
+ *   q_abs, q_pe, cache (bf16 or e4m3), page_size, block_table, seq_lens,
+ *   query_start_loc, num_heads, scale: as for mla_decode.
+ *                total_q * num_heads < 2^30, max_pages_per_seq * page_size <= 2^30
+ *   status       one int32 on the device, or NULL: OR-ed into, never cleared:
+ *                MLA_DEVERR_BAD_SEQ_LEN (a length beyond the table or
+ *                weight_len: cut to both), MLA_DEVERR_BAD_BLOCK (the page reads
+ *                as zeros), MLA_DEVERR_BAD_QSL (a request's tokens are not
+ *                within total_q: it counts as without query rows),
+ *                MLA_DEVERR_TIMEOUT (weights are then incomplete)
+ * weights and status overlap no other argument.  Scores and sums are float32,
+ * a key's rows summed in one order: the same bits every time.  A key that is
+ * not finite has an effect on its own weight alone.  batch == 0 is a no-op.
+ * One launch.
+ */
+MLA_API int mla_key_weights(const void* q_abs, const void* q_pe, const void* cache, int64_t num_blocks, int page_size,
+                            int cache_dtype, float kv_scale, const int32_t* block_table, int max_pages_per_seq,
+                            const int32_t* seq_lens, int batch, const int32_t* query_start_loc, int total_q,
+                            int num_heads, float scale, const float* lse, float decay, float* weights,
+                            int64_t weight_stride, int weight_len, int* status, void* stream);
+
+/*
+ * mla_evict_select -- which keys a request keeps when it may have `budget`:
+ * with n = seq_lens[b] <= budget all of them, else its first `sinks`, its last
+ * `recent`, and of the keys between those the budget - sinks - recent of the
+ * largest weight (equal weights: the lowest index first; -0 equals +0; NaN
+ * counts below every number).
+ *   weights      float32 rows of weight_len at weight_stride (mla_key_weights')
+ *   seq_lens     [batch] int32; above weight_len: MLA_DEVERR_BAD_SEQ_LEN in
+ *                *status, cut to it
+ *   keep         [batch, budget] int32: the kept indices in ascending order, -1
+ *                behind the last
+ *   keep_lens    [batch] int32: min(n, budget); may be seq_lens itself
+ *   sinks, recent  >= 0, sinks + recent <= budget
+ *   status       one int32 on the device, or NULL: OR-ed into, never cleared
+ * Outputs overlap no other argument (but keep_lens as said).  One launch.
+ */
+MLA_API int mla_evict_select(const float* weights, int64_t weight_stride, int weight_len, const int32_t* seq_lens,
+                             int batch, int budget, int sinks, int recent, int32_t* keep, int32_t* keep_lens,
+                             int* status, void* stream);
+
+/*
+ * mla_cache_compact -- move the kept rows of every request to the front of its
+ * pages, in place: for i < keep_lens[b]
+ *
+ *   row i of request b = its row keep[b, i]    (weights[b, i] = weights[b, keep[b, i]])
+ *
+ * where row p is cache[block_table[b, p / page_size], p % page_size].  All rows
+ * are read as they were before the call.  Afterwards keep_lens are the
+ * requests' lengths and the pages behind them are free; rows (and weights) from
+ * keep_lens[b] on are left as they were.  Keys keep the rotation of the position
+ * they were written at.
+ *   keep         [batch, max_keep] int32, keep[b, i] >= i (mla_evict_select's).
+ *                An entry below i, or beyond the table or weight_len, sets
+ *                MLA_DEVERR_BAD_POSITION in *status and its row is not written
+ *   keep_lens    [batch] int32; above max_keep: MLA_DEVERR_BAD_SEQ_LEN, cut to it
+ *   block_table  [batch, max_pages_per_seq] int32.  Pages of rows that move
+ *                belong to one request alone (a shared prefix is not compacted:
+ *                give the requests' own pages); a page outside [0, num_blocks)
+ *                sets MLA_DEVERR_BAD_BLOCK and its rows are not moved
+ *   cache        bf16 or e4m3 rows of 576, any page_size >= 1
+ *   weights      as for mla_key_weights, or NULL
+ *   status       one int32 on the device, or NULL: OR-ed into, never cleared
+ * cache, weights and status overlap no other argument.  One launch.
+ */
+MLA_API int mla_cache_compact(void* cache, int64_t num_blocks, int page_size, int cache_dtype,
+                              const int32_t* block_table, int max_pages_per_seq, const int32_t* keep, int max_keep,
+                              const int32_t* keep_lens, int batch, float* weights, int64_t weight_stride,
+                              int weight_len, int* status, void* stream);
+
+/*
  * mla_set_decode_wait_test -- test aid for the failure detection of the
  * decode kernels (the pages have no counterpart).  Every mbarrier wait inside
  * a decode is bounded in wall time; when one runs out, the CTA records
@@ -563,8 +702,9 @@ MLA_API int mla_prefill_status(const void* workspace, int* status, void* stream)
  * CTA of the grid never loads its first cache tile, so the wait for that tile
  * runs out.  The decode still returns; its outputs are then undefined and the
  * error word reports the timeout.  mla_prefill takes both settings in the same
- * way (the skipped tile is the first keys of its first CTA).  Call with (0, 0)
- * to restore the defaults.
+ * way (the skipped tile is the first keys of its first CTA), and so do
+ * mla_decode_shared and mla_key_weights.  Call with (0, 0) to restore the
+ * defaults.
  */
 MLA_API int mla_set_decode_wait_test(int skip_first_tile, unsigned long long wait_limit_ns);
 

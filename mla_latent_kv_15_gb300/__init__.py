@@ -33,7 +33,8 @@ C_ABI_SYMBOLS = ("mla_cache_write", "mla_decode_workspace_size", "mla_decode", "
                  "mla_gather_cache", "mla_quantize_fp8", "mla_decode_fp8q", "mla_set_decode_wait_test",
                  "mla_decode_no_alloc_status", "mla_decode_step", "mla_decode_fp8q_step",
                  "mla_rope_cache_write", "mla_kv_up_proj", "mla_prefill_workspace_size", "mla_prefill",
-                 "mla_prefill_status")
+                 "mla_prefill_status", "mla_decode_shared_workspace_size", "mla_decode_shared", "mla_key_weights",
+                 "mla_evict_select", "mla_cache_compact")
 NO_ALLOC_SCRATCH_BYTES = 96 << 20
 
 _lib = None
@@ -104,6 +105,18 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                                 P]
     lib.mla_prefill_status.restype = i32
     lib.mla_prefill_status.argtypes = [P, ctypes.POINTER(ctypes.c_int), P]
+    lib.mla_decode_shared_workspace_size.restype = sz
+    lib.mla_decode_shared_workspace_size.argtypes = [i32, i32, i32, i32, i32]
+    lib.mla_decode_shared.restype = i32
+    lib.mla_decode_shared.argtypes = [P, P, P, i64, i32, i32, f32, P, i32, P, P, i32, P, i32, P, i32, P, i32, i32, f32,
+                                      i32, P, P, P, sz, P]
+    lib.mla_key_weights.restype = i32
+    lib.mla_key_weights.argtypes = [P, P, P, i64, i32, i32, f32, P, i32, P, i32, P, i32, i32, f32, P, f32, P, i64, i32,
+                                    P, P]
+    lib.mla_evict_select.restype = i32
+    lib.mla_evict_select.argtypes = [P, i64, i32, P, i32, i32, i32, i32, P, P, P, P]
+    lib.mla_cache_compact.restype = i32
+    lib.mla_cache_compact.argtypes = [P, i64, i32, i32, P, i32, P, i32, P, i32, P, i64, i32, P, P]
     lib.mla_kv_up_proj.restype = i32
     lib.mla_kv_up_proj.argtypes = [P, i64, P, i64, i32, i32, P, P]
     _lib = lib
@@ -451,7 +464,7 @@ def set_decode_wait_test(skip_first_tile: bool = False, wait_limit_ns: int = 0) 
     run with every wait bounded by ``wait_limit_ns`` (0: the default 1 s) and,
     with ``skip_first_tile``, one CTA never loads its first cache tile, so a
     wait for it runs out and the device error word gets DEVERR_TIMEOUT.
-    Later prefills of the thread do the same."""
+    Later prefills, shared decodes and key weights of the thread do the same."""
     _check(load().mla_set_decode_wait_test(int(bool(skip_first_tile)), int(wait_limit_ns)))
 
 
@@ -560,6 +573,134 @@ def prefill_status(workspace, stream=None) -> int:
     st = ctypes.c_int(0)
     _check(load().mla_prefill_status(_ptr(workspace), ctypes.byref(st), _stream(stream)))
     return st.value
+
+
+def decode_shared_workspace_size(batch: int, prefixes: int, total_q: int, num_heads: int, max_splits: int = 0) -> int:
+    return int(load().mla_decode_shared_workspace_size(batch, prefixes, total_q, num_heads, max_splits))
+
+
+def decode_shared(q_abs, q_pe, cache, prefix_table, prefix_lens, prefix_requests, block_table, seq_lens, out,
+                  workspace, *, scale: float, query_start_loc=None, lse=None, num_splits: int = 0,
+                  kv_scale: float = 1.0, stream=None) -> None:
+    """decode() for requests behind shared prefixes, each prefix read once for
+    all of them: requests ``prefix_requests[g]`` .. ``prefix_requests[g+1] - 1``
+    ([G+1] int32) see the ``prefix_lens[g]`` ([G] int32) keys of row g of
+    ``prefix_table`` [G, pages] int32, and behind them their own keys
+    (``block_table``, ``seq_lens``: without the prefix).  ``workspace`` from
+    decode_shared_workspace_size; errors by decode_status(workspace)."""
+    import torch
+    nb, ps, _ = _decode_checked(q_abs, q_pe, cache, block_table, seq_lens, out, query_start_loc, lse)
+    T, N = q_abs.shape[:2]
+    i32 = torch.int32
+    _dense(prefix_table, "prefix_table", i32, dims=2)
+    G = prefix_table.shape[0]
+    _dense(prefix_lens, "prefix_lens", i32, (G,))
+    _dense(prefix_requests, "prefix_requests", i32, (G + 1,))
+    _dense(workspace, "workspace", workspace.dtype, workspace.shape)
+    dev = _on_current_device(q_abs, q_pe, cache, prefix_table, prefix_lens, prefix_requests, block_table, seq_lens,
+                             out, workspace, query_start_loc, lse)
+    _check(load().mla_decode_shared(q_abs.data_ptr(), q_pe.data_ptr(), cache.data_ptr(), nb, ps, _dtype_code(cache),
+                                    kv_scale, prefix_table.data_ptr(), prefix_table.shape[1], prefix_lens.data_ptr(),
+                                    prefix_requests.data_ptr(), G, block_table.data_ptr(), block_table.shape[1],
+                                    seq_lens.data_ptr(), seq_lens.shape[0],
+                                    None if query_start_loc is None else query_start_loc.data_ptr(), T, N, scale,
+                                    num_splits, out.data_ptr(), None if lse is None else lse.data_ptr(),
+                                    workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, dev)))
+
+
+def _weight_rows(weights, batch: int):
+    """(stride, width) of a [batch, W] float32 tensor with contiguous rows."""
+    import torch
+    if weights.dtype is not torch.float32:
+        raise ValueError(f"weights must be float32, got {str(weights.dtype).replace('torch.', '')}")
+    if weights.dim() != 2 or weights.shape[0] != batch:
+        raise ValueError(f"weights must have shape [{batch}, *], got {tuple(weights.shape)}")
+    width = weights.shape[1]
+    stride, inner = weights.stride()
+    if width > 1 and inner != 1:
+        raise ValueError(f"weights' last dimension must be contiguous, got strides {weights.stride()}")
+    return (width if batch <= 1 else stride), width
+
+
+def _status(status):
+    import torch
+    if status is None:
+        return None
+    _dense(status, "status", torch.int32, (1,))
+    return status.data_ptr()
+
+
+def key_weights(q_abs, q_pe, cache, block_table, seq_lens, lse, weights, *, scale: float, query_start_loc=None,
+                decay: float = 1.0, kv_scale: float = 1.0, status=None, stream=None) -> None:
+    """weights[b, j] = decay * weights[b, j] + the attention weight that key j
+    of request b gets from all the query rows that see it, for j < seq_lens[b]
+    (``weights`` [B, W] float32, rows may be further apart).  ``lse`` [T, N] is
+    the rows' log-sum-exp: decode()'s, or decode_shared()'s with the requests'
+    own block table and lengths.  decay 0 does not read the old weights.  Errors
+    are OR-ed into ``status`` [1] int32."""
+    import torch
+    i32 = torch.int32
+    _dense(q_abs, "q_abs", torch.bfloat16, (None, None, LKV))
+    T, N, _ = q_abs.shape
+    _dense(q_pe, "q_pe", torch.bfloat16, (T, N, ROPE))
+    nb, ps, _ = _cache_checked(cache)
+    _dense(seq_lens, "seq_lens", i32, dims=1)
+    B = seq_lens.shape[0]
+    _dense(block_table, "block_table", i32, (B, None))
+    if query_start_loc is not None:
+        _dense(query_start_loc, "query_start_loc", i32, (B + 1,))
+    _dense(lse, "lse", torch.float32, (T, N))
+    stride, width = _weight_rows(weights, B)
+    flag = _status(status)
+    dev = _on_current_device(q_abs, q_pe, cache, block_table, seq_lens, lse, weights, query_start_loc, status)
+    _check(load().mla_key_weights(q_abs.data_ptr(), q_pe.data_ptr(), cache.data_ptr(), nb, ps, _dtype_code(cache),
+                                  kv_scale, block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(), B,
+                                  None if query_start_loc is None else query_start_loc.data_ptr(), T, N, scale,
+                                  lse.data_ptr(), decay, weights.data_ptr(), stride, width, flag,
+                                  _raw_stream(stream, dev)))
+
+
+def evict_select(weights, seq_lens, keep, keep_lens, *, sinks: int = 0, recent: int = 0, status=None,
+                 stream=None) -> None:
+    """The keys each request keeps of its seq_lens[b]: all, if ``keep`` [B,
+    budget] int32 holds them, else the first ``sinks``, the last ``recent`` and,
+    between them, those of the largest ``weights`` [B, W] (ties: the lowest
+    index).  ``keep`` gets their indices, ascending, -1 behind the last, and
+    ``keep_lens`` [B] int32 (which may be ``seq_lens`` itself) their number."""
+    import torch
+    i32 = torch.int32
+    _dense(seq_lens, "seq_lens", i32, dims=1)
+    B = seq_lens.shape[0]
+    _dense(keep, "keep", i32, (B, None))
+    _dense(keep_lens, "keep_lens", i32, (B,))
+    stride, width = _weight_rows(weights, B)
+    flag = _status(status)
+    dev = _on_current_device(weights, seq_lens, keep, keep_lens, status)
+    _check(load().mla_evict_select(weights.data_ptr(), stride, width, seq_lens.data_ptr(), B, keep.shape[1], sinks,
+                                   recent, keep.data_ptr(), keep_lens.data_ptr(), flag, _raw_stream(stream, dev)))
+
+
+def cache_compact(cache, block_table, keep, keep_lens, *, weights=None, status=None, stream=None) -> None:
+    """Row i of request b becomes its row keep[b, i], i < keep_lens[b], in place
+    (and weights[b, i] weights[b, keep[b, i]]): evict_select's choice moved to
+    the front of the request's pages.  keep[b, i] >= i; the pages belong to one
+    request alone."""
+    import torch
+    i32 = torch.int32
+    nb, ps, _ = _cache_checked(cache)
+    _dense(keep_lens, "keep_lens", i32, dims=1)
+    B = keep_lens.shape[0]
+    _dense(keep, "keep", i32, (B, None))
+    _dense(block_table, "block_table", i32, (B, None))
+    stride, width, at = 0, 0, None
+    if weights is not None:
+        stride, width = _weight_rows(weights, B)
+        at = weights.data_ptr()
+    flag = _status(status)
+    dev = _on_current_device(cache, block_table, keep, keep_lens, weights, status)
+    _check(load().mla_cache_compact(cache.data_ptr(), nb, ps, _dtype_code(cache), block_table.data_ptr(),
+                                    block_table.shape[1], keep.data_ptr(), keep.shape[1], keep_lens.data_ptr(), B, at,
+                                    stride, width, flag, _raw_stream(stream, dev)))
 
 
 def gather_cache(cache, block_table, cu_seq_lens, dst, seq_starts=None, kv_scale: float = 1.0, status=None,

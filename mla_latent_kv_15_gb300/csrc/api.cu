@@ -130,14 +130,16 @@ size_t mla_decode_workspace_size(int batch, int total_q, int num_heads, int max_
 
 namespace {
 
-// The decode of mla_decode (q8 == nullptr: bf16 q_abs and q_pe) and of
-// mla_decode_fp8q (q8: e4m3 [q_abs | q_pe] rows with q_scale, e4m3 cache).
+// The decode of mla_decode (q8 == nullptr: bf16 q_abs and q_pe), of
+// mla_decode_fp8q (q8: e4m3 [q_abs | q_pe] rows with q_scale, e4m3 cache) and
+// of mla_decode_shared (shared: the prefixes, with their block table).
 int decode_impl(const void* q_abs, const void* q_pe, const void* q8, float q_scale, const void* cache,
                 int64_t num_blocks, int page_size, int cache_dtype, float kv_scale, const int32_t* block_table,
                 int max_pages_per_seq, const int32_t* seq_lens, int batch, const int32_t* query_start_loc,
                 int total_q, int num_heads, float scale, int num_splits, void* out, float* lse, void* workspace,
                 size_t workspace_bytes, void* stream, const mla::CacheWriteArgs* write = nullptr,
-                const mla::QuantArgs* quant = nullptr) {
+                const mla::QuantArgs* quant = nullptr, const mla::SharedArgs* shared = nullptr,
+                const int32_t* prefix_table = nullptr) {
   if (batch < 0 || total_q < 0) return fail(MLA_ERR_INVALID_ARG, "batch and total_q must be >= 0");
   if (num_heads < 1 || num_heads > 1024) return fail(MLA_ERR_INVALID_ARG, "num_heads must be in [1, 1024]");
   if (batch == 0 || total_q == 0) return ok();
@@ -172,7 +174,8 @@ int decode_impl(const void* q_abs, const void* q_pe, const void* q8, float q_sca
   if (!std::isfinite(scale) || scale == 0.f) return fail(MLA_ERR_INVALID_ARG, "scale must be finite and nonzero");
   if (num_splits < 0 || num_splits > 4096) return fail(MLA_ERR_INVALID_ARG, "num_splits must be in [0, 4096]");
 
-  const mla::WorkspaceLayout L = mla::workspace_layout(batch, total_q, num_heads, num_splits);
+  const mla::WorkspaceLayout L =
+      mla::workspace_layout(batch, total_q, num_heads, num_splits, shared ? shared->prefixes : -1);
   if (workspace_bytes < L.total)
     return fail(MLA_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu required", workspace_bytes, L.total);
   const int sms = sm_count();
@@ -255,24 +258,29 @@ int decode_impl(const void* q_abs, const void* q_pe, const void* q8, float q_sca
   a.wait_limit_ns = g_wait_limit_ns;
   a.debug_skip_tile = g_test_skip_tile;
   a.plan = plan;
+  a.prefix_table = prefix_table;
+  a.max_prefix_pages = shared ? shared->max_pages : 0;
 
   cudaStream_t s = (cudaStream_t)stream;
   // small head counts with one query token per request (total_q == batch):
   // 32-row groups and the decode variant with small receive buffers and a
   // deeper cache ring.  Groups never outnumber the batch then: a request with
   // Sq tokens gives ceil(Sq * N / 32) <= Sq groups.
-  const int small_rows = !q8 && cache_dtype == MLA_BF16 && num_heads <= 32 && total_q == batch;
+  const int small_rows = !shared && !q8 && cache_dtype == MLA_BF16 && num_heads <= 32 && total_q == batch;
   const int variant = q8 ? 3 : (cache_dtype == MLA_FP8_E4M3 ? 1 : (small_rows ? 2 : 0));
-  cudaError_t e = mla::launch_plan(seq_lens, query_start_loc, batch, num_heads, max_pages_per_seq, page_size,
-                                   num_splits, clusters, small_rows ? 32 : mla::kRows, a.plan, write, quant, sms,
-                                   s);
+  cudaError_t e = shared ? mla::launch_shared_plan(seq_lens, query_start_loc, batch, num_heads, max_pages_per_seq,
+                                                   page_size, num_splits, clusters, a.plan, *shared, s)
+                         : mla::launch_plan(seq_lens, query_start_loc, batch, num_heads, max_pages_per_seq, page_size,
+                                            num_splits, clusters, small_rows ? 32 : mla::kRows, a.plan, write, quant,
+                                            sms, s);
   if (e != cudaSuccess) return cuda_fail(e, "plan launch");
   const bool timed = g_timing_start && g_timing_stop;
   if (timed && (e = cudaEventRecord(g_timing_start, s)) != cudaSuccess) return cuda_fail(e, "timing event");
-  e = mla::launch_decode(tm_q, tm_qr, tm_kv, tm_kvr, tm_out, tm_part, variant, a, clusters, s);
+  e = shared ? mla::launch_decode_shared(tm_q, tm_qr, tm_kv, tm_kvr, tm_out, tm_part, variant, a, clusters, s)
+             : mla::launch_decode(tm_q, tm_qr, tm_kv, tm_kvr, tm_out, tm_part, variant, a, clusters, s);
   if (e != cudaSuccess) return cuda_fail(e, "decode launch");
   if (timed && (e = cudaEventRecord(g_timing_stop, s)) != cudaSuccess) return cuda_fail(e, "timing event");
-  e = mla::launch_combine(a, L.max_groups, sms, s);
+  e = shared ? mla::launch_combine_shared(a, L.max_groups, sms, s) : mla::launch_combine(a, L.max_groups, sms, s);
   if (e != cudaSuccess) return cuda_fail(e, "combine launch");
   return ok();
 }
@@ -518,6 +526,24 @@ bool overlap(const Extent& a, const Extent& b) {
   return step == 0 || columns_meet(a.lo, a.width, b.lo, b.width, step);
 }
 
+// Whether an output (a null one is none) shares bytes with another or an input.
+bool any_overlap(const Extent* outputs, int n_out, const Extent* inputs, int n_in) {
+  for (int i = 0; i < n_out; ++i) {
+    if (!outputs[i].lo) continue;
+    for (int j = 0; j < i; ++j)
+      if (outputs[j].lo && overlap(outputs[i], outputs[j])) return true;
+    for (int j = 0; j < n_in; ++j)
+      if (inputs[j].lo && overlap(outputs[i], inputs[j])) return true;
+  }
+  return false;
+}
+// `batch` rows of `len` float32 weights, `stride` elements apart.
+Extent weight_extent(const void* p, int64_t batch, int64_t stride, int64_t len) {
+  return len > 0 ? extent(p, batch, stride, 1, 0, len, 4) : Extent{};
+}
+
+constexpr int kMaxBatch = 1 << 20;
+constexpr int64_t kMaxKeys = 1LL << 30;     // keys of a request, as far as a table or a row of weights reaches
 constexpr int64_t kMaxStride = 1LL << 32;   // elements
 bool valid_stride(int64_t s, int64_t least) { return s >= least && s % 8 == 0 && s <= kMaxStride; }
 
@@ -770,6 +796,226 @@ int mla_prefill_status(const void* workspace, int* status, void* stream) {
   for (int i = 0; i < h.ctas && i < 2 * mla::kPrefillMaxPairs; ++i)
     if (h.gave_up[i]) bits |= MLA_DEVERR_TIMEOUT;
   *status = bits;
+  return ok();
+}
+
+size_t mla_decode_shared_workspace_size(int batch, int prefixes, int total_q, int num_heads, int max_splits) {
+  if (batch <= 0 || prefixes <= 0 || total_q <= 0 || num_heads <= 0 || max_splits < 0) return 0;
+  return mla::workspace_layout(batch, total_q, num_heads, max_splits, prefixes).total;
+}
+
+int mla_decode_shared(const void* q_abs, const void* q_pe, const void* cache, int64_t num_blocks, int page_size,
+                      int cache_dtype, float kv_scale, const int32_t* prefix_table, int max_prefix_pages,
+                      const int32_t* prefix_lens, const int32_t* prefix_requests, int prefixes,
+                      const int32_t* block_table, int max_pages_per_seq, const int32_t* seq_lens, int batch,
+                      const int32_t* query_start_loc, int total_q, int num_heads, float scale, int num_splits,
+                      void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  if (batch < 0 || total_q < 0 || prefixes < 0)
+    return fail(MLA_ERR_INVALID_ARG, "batch, prefixes and total_q must be >= 0");
+  if (num_heads < 1 || num_heads > 1024) return fail(MLA_ERR_INVALID_ARG, "num_heads must be in [1, 1024]");
+  if (batch == 0 || total_q == 0) return ok();
+  if (prefixes < 1) return fail(MLA_ERR_INVALID_ARG, "a batch needs at least one prefix (its length may be 0)");
+  if (batch > kMaxBatch || prefixes > kMaxBatch)
+    return fail(MLA_ERR_UNSUPPORTED, "batch and prefixes must be <= %d", kMaxBatch);
+  if (!prefix_table || !prefix_lens || !prefix_requests) return fail(MLA_ERR_INVALID_ARG, "null pointer argument");
+  if (!aligned(prefix_table, 4) || !aligned(prefix_lens, 4) || !aligned(prefix_requests, 4))
+    return fail(MLA_ERR_INVALID_ARG, "prefix_table, prefix_lens and prefix_requests must be 4-byte aligned");
+  if (!valid_page_size(page_size))
+    return fail(MLA_ERR_UNSUPPORTED, "page_size must be 16, 32, 64, 128 or 256 (got %d)", page_size);
+  if (max_prefix_pages <= 0) return fail(MLA_ERR_INVALID_ARG, "max_prefix_pages must be positive");
+  if (max_pages_per_seq <= 0) return fail(MLA_ERR_INVALID_ARG, "max_pages_per_seq must be positive");
+  if ((int64_t)max_prefix_pages * page_size + total_q > kMaxKeys ||
+      (int64_t)max_pages_per_seq * page_size + total_q > kMaxKeys)
+    return fail(MLA_ERR_UNSUPPORTED, "pages of a table * page_size + total_q must be <= 2^30");
+  if (!std::isfinite(scale * 1.4426950408889634f) || scale == 0.f)
+    return fail(MLA_ERR_INVALID_ARG, "scale must be nonzero and scale * log2(e) finite");
+  if (cache_dtype == MLA_FP8_E4M3 && !std::isnormal(scale * 1.4426950408889634f * kv_scale))
+    return fail(MLA_ERR_INVALID_ARG, "scale * kv_scale must be a normal float (the scores' factor)");
+  if (num_splits < 0 || num_splits > 4096) return fail(MLA_ERR_INVALID_ARG, "num_splits must be in [0, 4096]");
+  const int64_t rows = (int64_t)total_q * num_heads;
+  if (rows >= ((int64_t)1 << 30))
+    return fail(MLA_ERR_UNSUPPORTED, "total_q * num_heads must be below 2^30");
+  if (2 * (rows / mla::kRows + batch + 2) * (num_splits > 1 ? num_splits : 1) * mla::kRows >= (int64_t)1 << 31)
+    return fail(MLA_ERR_UNSUPPORTED, "total_q * num_heads * num_splits is too large");
+  const mla::WorkspaceLayout L = mla::workspace_layout(batch, total_q, num_heads, num_splits, prefixes);
+  const int esize = cache_dtype == MLA_FP8_E4M3 ? 1 : 2;
+  const Extent outputs[] = {dense(out, rows * mla::kLkv * 2), dense(lse, rows * 4), dense(workspace, (int64_t)L.total)};
+  const Extent inputs[] = {dense(q_abs, rows * mla::kLkv * 2),
+                           dense(q_pe, rows * mla::kRope * 2),
+                           dense(cache, num_blocks * page_size * mla::kDqk * esize),
+                           dense(prefix_table, (int64_t)prefixes * max_prefix_pages * 4),
+                           dense(prefix_lens, prefixes * 4LL),
+                           dense(prefix_requests, (prefixes + 1LL) * 4),
+                           dense(block_table, (int64_t)batch * max_pages_per_seq * 4),
+                           dense(seq_lens, batch * 4LL),
+                           dense(query_start_loc, (batch + 1LL) * 4)};
+  if (num_blocks > 0 && num_blocks < (1LL << 31) && any_overlap(outputs, 3, inputs, 9))
+    return fail(MLA_ERR_INVALID_ARG, "out, lse and the workspace must not overlap each other or the inputs");
+  const mla::SharedArgs sh{prefix_lens, prefix_requests, prefixes, max_prefix_pages, total_q};
+  return decode_impl(q_abs, q_pe, nullptr, 0.f, cache, num_blocks, page_size, cache_dtype, kv_scale, block_table,
+                     max_pages_per_seq, seq_lens, batch, query_start_loc, total_q, num_heads, scale, num_splits, out,
+                     lse, workspace, workspace_bytes, stream, nullptr, nullptr, &sh, prefix_table);
+}
+
+int mla_key_weights(const void* q_abs, const void* q_pe, const void* cache, int64_t num_blocks, int page_size,
+                    int cache_dtype, float kv_scale, const int32_t* block_table, int max_pages_per_seq,
+                    const int32_t* seq_lens, int batch, const int32_t* query_start_loc, int total_q, int num_heads,
+                    float scale, const float* lse, float decay, float* weights, int64_t weight_stride, int weight_len,
+                    int* status, void* stream) {
+  if (batch < 0 || total_q < 0 || weight_len < 0)
+    return fail(MLA_ERR_INVALID_ARG, "batch, total_q and weight_len must be >= 0");
+  if (num_heads < 1 || num_heads > 1024) return fail(MLA_ERR_INVALID_ARG, "num_heads must be in [1, 1024]");
+  if (cache_dtype != MLA_BF16 && cache_dtype != MLA_FP8_E4M3)
+    return fail(MLA_ERR_INVALID_ARG, "cache_dtype must be MLA_BF16 or MLA_FP8_E4M3 (got %d)", cache_dtype);
+  const bool fp8 = cache_dtype == MLA_FP8_E4M3;
+  if (fp8 && !(std::isfinite(kv_scale) && kv_scale > 0.f))
+    return fail(MLA_ERR_INVALID_ARG, "kv_scale must be finite and > 0 for an fp8 cache");
+  const float factor = scale * 1.4426950408889634f * (fp8 ? kv_scale : 1.f);
+  if (!std::isnormal(factor))
+    return fail(MLA_ERR_INVALID_ARG, "scale must be nonzero and scale * log2(e) (* kv_scale) a normal float");
+  if (!(std::isfinite(decay) && decay >= 0.f)) return fail(MLA_ERR_INVALID_ARG, "decay must be finite and >= 0");
+  if (batch == 0 || weight_len == 0) return ok();
+  if (!query_start_loc && total_q != batch)
+    return fail(MLA_ERR_INVALID_ARG, "without query_start_loc every request has one query token (total_q == batch)");
+  if (batch > kMaxBatch) return fail(MLA_ERR_UNSUPPORTED, "batch must be <= %d", kMaxBatch);
+  if (!valid_page_size(page_size))
+    return fail(MLA_ERR_UNSUPPORTED, "page_size must be 16, 32, 64, 128 or 256 (got %d)", page_size);
+  if (num_blocks <= 0 || num_blocks * (int64_t)page_size >= (int64_t)1 << 31)
+    return fail(MLA_ERR_INVALID_ARG, "num_blocks * page_size must be in [1, 2^31)");
+  if (max_pages_per_seq <= 0) return fail(MLA_ERR_INVALID_ARG, "max_pages_per_seq must be positive");
+  if ((int64_t)max_pages_per_seq * page_size > kMaxKeys || weight_len > kMaxKeys)
+    return fail(MLA_ERR_UNSUPPORTED, "max_pages_per_seq * page_size and weight_len must be <= 2^30");
+  const int64_t rows = (int64_t)total_q * num_heads;
+  if (rows >= (int64_t)1 << 30) return fail(MLA_ERR_UNSUPPORTED, "total_q * num_heads must be below 2^30");
+  if (!cache || !block_table || !seq_lens || !weights || (total_q > 0 && (!q_abs || !q_pe || !lse)))
+    return fail(MLA_ERR_INVALID_ARG, "null pointer argument");
+  if (!aligned(q_abs, 16) || !aligned(q_pe, 16) || !aligned(cache, 16))
+    return fail(MLA_ERR_INVALID_ARG, "q_abs, q_pe and cache must be 16-byte aligned");
+  if (!aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(query_start_loc, 4) || !aligned(lse, 4) ||
+      !aligned(weights, 4) || !aligned(status, 4))
+    return fail(MLA_ERR_INVALID_ARG, "block_table, seq_lens, query_start_loc, lse, weights and status must be 4-byte aligned");
+  if (weight_stride < weight_len || weight_stride > kMaxStride)
+    return fail(MLA_ERR_INVALID_ARG, "weight_stride must be in [weight_len, 2^32]");
+  const Extent outputs[] = {weight_extent(weights, batch, weight_stride, weight_len), dense(status, 4)};
+  const Extent inputs[] = {dense(total_q ? q_abs : nullptr, rows * mla::kLkv * 2),
+                           dense(total_q ? q_pe : nullptr, rows * mla::kRope * 2),
+                           dense(cache, num_blocks * page_size * mla::kDqk * (fp8 ? 1 : 2)),
+                           dense(block_table, (int64_t)batch * max_pages_per_seq * 4),
+                           dense(seq_lens, batch * 4LL),
+                           dense(query_start_loc, (batch + 1LL) * 4),
+                           dense(total_q ? lse : nullptr, rows * 4)};
+  if (any_overlap(outputs, 2, inputs, 7))
+    return fail(MLA_ERR_INVALID_ARG, "weights and status must not overlap each other or the inputs");
+  const int sms = sm_count();
+  if (sms < 1) return fail(MLA_ERR_CUDA, "cannot query the current device");
+  // a request's rows come in boxes of a token's heads (rounded up to 16 rows,
+  // at most 128), as many to a product as its 128 columns hold
+  const int q_box = num_heads >= 128 ? 128 : (num_heads + 15) / 16 * 16;
+  const int row_tile = 128 / q_box * q_box;
+  CUtensorMap tm_q, tm_qr, tm_kv;
+  bool enc = mla::encode_tmap_2d(&tm_kv, cache, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                                 mla::kDqk, (uint64_t)num_blocks * page_size, mla::kDqk * (fp8 ? 1 : 2), 64,
+                                 page_size < 128 ? page_size : 128,
+                                 fp8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B);
+  tm_q = tm_qr = tm_kv;   // without a query row none is loaded
+  if (total_q > 0)
+    enc = enc &&
+          mla::encode_tmap_2d(&tm_q, q_abs, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, mla::kLkv, rows, mla::kLkv * 2, 64, q_box,
+                              CU_TENSOR_MAP_SWIZZLE_128B) &&
+          mla::encode_tmap_2d(&tm_qr, q_pe, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, mla::kRope, rows, mla::kRope * 2, 64,
+                              q_box, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (!enc) return fail(MLA_ERR_CUDA, "cuTensorMapEncodeTiled rejected a tensor layout");
+  mla::KeyWeightArgs a{};
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.qsl = query_start_loc;
+  a.lse = lse;
+  a.weights = weights;
+  a.weight_stride = weight_stride;
+  a.weight_len = weight_len;
+  a.batch = batch;
+  a.total_q = total_q;
+  a.num_heads = num_heads;
+  a.max_pages = max_pages_per_seq;
+  a.page_size = page_size;
+  a.num_blocks = num_blocks;
+  a.scale_log2 = factor;
+  a.decay = decay;
+  a.q_box = q_box;
+  a.row_tile = row_tile;
+  a.status = status;
+  a.wait_limit_ns = g_wait_limit_ns;
+  a.debug_skip_tile = g_test_skip_tile;
+  cudaError_t e = mla::launch_key_weights(tm_q, tm_qr, tm_kv, fp8, a, sms, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "key weights launch");
+  return ok();
+}
+
+int mla_evict_select(const float* weights, int64_t weight_stride, int weight_len, const int32_t* seq_lens, int batch,
+                     int budget, int sinks, int recent, int32_t* keep, int32_t* keep_lens, int* status, void* stream) {
+  if (batch < 0 || weight_len < 0) return fail(MLA_ERR_INVALID_ARG, "batch and weight_len must be >= 0");
+  if (budget < 1) return fail(MLA_ERR_INVALID_ARG, "budget must be positive (got %d)", budget);
+  if (sinks < 0 || recent < 0 || sinks > budget || recent > budget - sinks)
+    return fail(MLA_ERR_INVALID_ARG, "sinks and recent must be >= 0 and sinks + recent <= budget");
+  if (batch == 0) return ok();
+  if (batch > kMaxBatch) return fail(MLA_ERR_UNSUPPORTED, "batch must be <= %d", kMaxBatch);
+  if (weight_len > kMaxKeys || budget > kMaxKeys)
+    return fail(MLA_ERR_UNSUPPORTED, "weight_len and budget must be <= 2^30");
+  if ((weight_len > 0 && !weights) || !seq_lens || !keep || !keep_lens)
+    return fail(MLA_ERR_INVALID_ARG, "null pointer argument");
+  if (!aligned(weights, 4) || !aligned(seq_lens, 4) || !aligned(keep, 4) || !aligned(keep_lens, 4) ||
+      !aligned(status, 4))
+    return fail(MLA_ERR_INVALID_ARG, "tensors must be 4-byte aligned");
+  if (weight_stride < weight_len || weight_stride > kMaxStride)
+    return fail(MLA_ERR_INVALID_ARG, "weight_stride must be in [weight_len, 2^32]");
+  const bool in_place = keep_lens == seq_lens;
+  const Extent outputs[] = {dense(keep, (int64_t)batch * budget * 4), dense(keep_lens, batch * 4LL), dense(status, 4)};
+  const Extent inputs[] = {weight_extent(weights, batch, weight_stride, weight_len),
+                           dense(in_place ? nullptr : seq_lens, batch * 4LL)};
+  if (any_overlap(outputs, 3, inputs, 2))
+    return fail(MLA_ERR_INVALID_ARG,
+                "keep, keep_lens and status must not overlap each other or the inputs (keep_lens may be seq_lens itself)");
+  const int sms = sm_count();
+  if (sms < 1) return fail(MLA_ERR_CUDA, "cannot query the current device");
+  const mla::SelectArgs a{weights, weight_stride, weight_len, seq_lens, batch, budget,
+                          sinks,   recent,        keep,       keep_lens, status};
+  cudaError_t e = mla::launch_select(a, sms, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "selection launch");
+  return ok();
+}
+
+int mla_cache_compact(void* cache, int64_t num_blocks, int page_size, int cache_dtype, const int32_t* block_table,
+                      int max_pages_per_seq, const int32_t* keep, int max_keep, const int32_t* keep_lens, int batch,
+                      float* weights, int64_t weight_stride, int weight_len, int* status, void* stream) {
+  if (batch < 0 || max_keep < 0) return fail(MLA_ERR_INVALID_ARG, "batch and max_keep must be >= 0");
+  if (cache_dtype != MLA_BF16 && cache_dtype != MLA_FP8_E4M3)
+    return fail(MLA_ERR_INVALID_ARG, "cache_dtype must be MLA_BF16 or MLA_FP8_E4M3 (got %d)", cache_dtype);
+  if (page_size <= 0 || num_blocks <= 0 || max_pages_per_seq <= 0 || num_blocks > (1LL << 40) / page_size)
+    return fail(MLA_ERR_INVALID_ARG,
+                "page_size, num_blocks and max_pages_per_seq must be positive and num_blocks * page_size <= 2^40");
+  if (batch == 0 || max_keep == 0) return ok();
+  if (batch > kMaxBatch) return fail(MLA_ERR_UNSUPPORTED, "batch must be <= %d", kMaxBatch);
+  if (max_keep > kMaxKeys) return fail(MLA_ERR_UNSUPPORTED, "max_keep must be <= 2^30");
+  if (!cache || !block_table || !keep || !keep_lens) return fail(MLA_ERR_INVALID_ARG, "null pointer argument");
+  if (!aligned(cache, 16)) return fail(MLA_ERR_INVALID_ARG, "cache must be 16-byte aligned");
+  if (!aligned(block_table, 4) || !aligned(keep, 4) || !aligned(keep_lens, 4) || !aligned(weights, 4) ||
+      !aligned(status, 4))
+    return fail(MLA_ERR_INVALID_ARG, "block_table, keep, keep_lens, weights and status must be 4-byte aligned");
+  if (weights && (weight_len < 1 || weight_len > kMaxKeys || weight_stride < weight_len || weight_stride > kMaxStride))
+    return fail(MLA_ERR_INVALID_ARG, "weight_len must be in [1, 2^30] and weight_stride in [weight_len, 2^32]");
+  const int row_bytes = mla::kDqk * (cache_dtype == MLA_FP8_E4M3 ? 1 : 2);
+  const Extent outputs[] = {dense(cache, num_blocks * page_size * row_bytes),
+                            weight_extent(weights, batch, weight_stride, weight_len), dense(status, 4)};
+  const Extent inputs[] = {dense(block_table, (int64_t)batch * max_pages_per_seq * 4),
+                           dense(keep, (int64_t)batch * max_keep * 4), dense(keep_lens, batch * 4LL)};
+  if (any_overlap(outputs, 3, inputs, 3))
+    return fail(MLA_ERR_INVALID_ARG, "cache, weights and status must not overlap each other or the inputs");
+  const int sms = sm_count();
+  if (sms < 1) return fail(MLA_ERR_CUDA, "cannot query the current device");
+  const mla::CompactArgs a{static_cast<uint8_t*>(cache), num_blocks, page_size, block_table, max_pages_per_seq, keep,
+                           keep_lens, batch, max_keep, weights, weight_stride, weight_len, status};
+  cudaError_t e = mla::launch_compact(a, row_bytes, sms, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "compaction launch");
   return ok();
 }
 

@@ -28,7 +28,8 @@ struct PlanHeader {
   int num_clusters;
   int total_tiles;
   int tiles_per_cluster;
-  int pad[2];
+  int own_groups;    // mla_decode_shared: groups before this one are prefixes' (else 0)
+  int pad;
 };
 
 struct GroupRec {    // 32 bytes
@@ -68,21 +69,27 @@ struct Plan {
   uint16_t* part_o;      // [max_units][128][512] fp16 codes
   float* part_scale;     // [max_units][128][16] 2^e of each 32-dim chunk
   float* part_lse;       // [max_units][128]
+  // mla_decode_shared: of each group of a request's own keys, the first group
+  // of its prefix and that group's first query row
+  int2* behind;          // [max_groups]
   int max_groups;
   int max_units;
 };
 
 struct WorkspaceLayout {
-  size_t header, groups, units, unit_cluster, cluster_begin, part_o, part_scale, part_lse, total;
+  size_t header, groups, units, unit_cluster, cluster_begin, part_o, part_scale, part_lse, behind, total;
   int max_groups, max_units;
 };
 
-// Byte offsets of each plan array for a batch shape (host and device agree).
-inline WorkspaceLayout workspace_layout(int batch, int total_q, int num_heads, int max_splits) {
+// Byte offsets of each plan array for a batch shape (host and device agree);
+// prefixes: of mla_decode_shared, whose groups cover every row a second time
+// (-1: a plain decode).
+inline WorkspaceLayout workspace_layout(int batch, int total_q, int num_heads, int max_splits, int prefixes = -1) {
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
   WorkspaceLayout L{};
   long long rows = (long long)total_q * num_heads;
   long long mg = (rows + 127LL * batch) / kRows + 1;
+  if (prefixes >= 0) mg += (rows + 127LL * prefixes) / kRows + 1;
   long long mu = mg * (max_splits > 1 ? max_splits : 1) + kMaxClusters;
   L.max_groups = (int)mg;
   L.max_units = (int)mu;
@@ -95,6 +102,7 @@ inline WorkspaceLayout workspace_layout(int batch, int total_q, int num_heads, i
   L.part_o = off;        off = up(off + sizeof(uint16_t) * (size_t)mu * kRows * kLkv);
   L.part_scale = off;    off = up(off + sizeof(float) * (size_t)mu * kRows * (kLkv / 32));
   L.part_lse = off;      off = up(off + sizeof(float) * (size_t)mu * kRows);
+  L.behind = off;        if (prefixes >= 0) off = up(off + sizeof(int2) * (size_t)mg);
   L.total = off;
   return L;
 }
@@ -110,6 +118,7 @@ inline Plan plan_from_workspace(void* ws, const WorkspaceLayout& L) {
   P.part_o = reinterpret_cast<uint16_t*>(p + L.part_o);
   P.part_scale = reinterpret_cast<float*>(p + L.part_scale);
   P.part_lse = reinterpret_cast<float*>(p + L.part_lse);
+  P.behind = reinterpret_cast<int2*>(p + L.behind);
   P.max_groups = L.max_groups;
   P.max_units = L.max_units;
   return P;
@@ -135,6 +144,69 @@ struct DecodeArgs {
   unsigned long long wait_limit_ns;   // bound of every on-chip wait (1 s)
   int debug_skip_tile;      // test aid: CTA 0 of cluster 0 never loads its first cache tile
   Plan plan;
+  const int32_t* prefix_table;   // mla_decode_shared: block table of the prefixes
+  int max_prefix_pages;
+};
+
+// The shared prefixes of mla_decode_shared: requests begin[g] .. begin[g+1] - 1
+// stand behind the first lens[g] keys of row g of the prefix block table.
+struct SharedArgs {
+  const int32_t* lens;
+  const int32_t* begin;     // [prefixes + 1]
+  int prefixes;
+  int max_pages;
+  int total_q;
+};
+
+// mla_key_weights: the sum over a request's query rows of exp(score - lse),
+// for each of its keys.
+struct KeyWeightArgs {
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* qsl;         // may be null: one query token per request
+  const float* lse;           // [total_q * heads]
+  float* weights;             // rows of weight_len at weight_stride
+  int64_t weight_stride;
+  int weight_len;
+  int batch, total_q, num_heads;
+  int max_pages, page_size;
+  int64_t num_blocks;
+  float scale_log2;           // scale * log2(e) (* kv_scale for e4m3)
+  float decay;
+  int q_box, row_tile;        // query rows of a load box (a multiple of 16) and of a product
+  int* status;                // OR of mla_device_error bits, or null
+  unsigned long long wait_limit_ns;
+  int debug_skip_tile;        // test aid: the first tile's first chunk never comes
+};
+
+// mla_cache_compact: row keep[b][i] of request b to its row i, i < keep_lens[b].
+struct CompactArgs {
+  uint8_t* cache;
+  int64_t num_blocks;
+  int page_size;
+  const int32_t* block_table;
+  int max_pages;
+  const int32_t* keep;        // [batch][max_keep]
+  const int32_t* keep_lens;
+  int batch;
+  int max_keep;
+  float* weights;             // rows of weight_len at weight_stride, or null
+  int64_t weight_stride;
+  int weight_len;
+  int* status;                // OR of mla_device_error bits, or null
+};
+
+// mla_evict_select: the indices of the keys each request keeps.
+struct SelectArgs {
+  const float* weights;       // rows of weight_len at weight_stride
+  int64_t weight_stride;
+  int weight_len;
+  const int32_t* seq_lens;
+  int batch;
+  int budget, sinks, recent;
+  int32_t* keep;              // [batch][budget]
+  int32_t* keep_lens;
+  int* status;
 };
 
 // The new rows of a step for concat_and_cache_mla: token t's kv_c (512 bf16)
@@ -228,6 +300,11 @@ cudaError_t launch_kv_proj(const CUtensorMap& tm_x, const CUtensorMap& tm_w, con
 cudaError_t launch_plan(const int32_t* seq_lens, const int32_t* qsl, int batch, int num_heads, int max_pages,
                         int page_size, int num_splits, int num_clusters, int group_rows, Plan plan,
                         const CacheWriteArgs* write, const QuantArgs* quant, int sm_count, cudaStream_t s);
+// the plan of mla_decode_shared: groups of kRows rows, first those of the
+// prefixes (all requests behind one together), then those of the requests
+cudaError_t launch_shared_plan(const int32_t* seq_lens, const int32_t* qsl, int batch, int num_heads, int max_pages,
+                               int page_size, int num_splits, int num_clusters, Plan plan, const SharedArgs& shared,
+                               cudaStream_t s);
 // variant: 0 bf16 cache, 1 e4m3 cache, 2 bf16 cache with <= 32-row groups
 // (plan built with group_rows = 32), 3 e4m3 query and e4m3 cache.  Tensor
 // maps: the query's latent columns (64-dim boxes; 128-dim e4m3 boxes for
@@ -238,6 +315,17 @@ cudaError_t launch_plan(const int32_t* seq_lens, const int32_t* qsl, int batch, 
 cudaError_t launch_decode(const CUtensorMap& tm_q, const CUtensorMap& tm_qr, const CUtensorMap& tm_kv,
                           const CUtensorMap& tm_kvr, const CUtensorMap& tm_out, const CUtensorMap& tm_part,
                           int variant, const DecodeArgs& a, int num_clusters, cudaStream_t s);
+// the same for a plan of launch_shared_plan (variants 0 and 1)
+cudaError_t launch_decode_shared(const CUtensorMap& tm_q, const CUtensorMap& tm_qr, const CUtensorMap& tm_kv,
+                                 const CUtensorMap& tm_kvr, const CUtensorMap& tm_out, const CUtensorMap& tm_part,
+                                 int variant, const DecodeArgs& a, int num_clusters, cudaStream_t s);
+cudaError_t launch_combine_shared(const DecodeArgs& a, int max_groups, int sm_count, cudaStream_t s);
+// Tensor maps, 64-column boxes: query rows (q_abs, q_pe; a.q_box rows, 128-B
+// swizzle), cache rows (min(page, 128) rows; bf16 128-B swizzle, e4m3 none)
+cudaError_t launch_key_weights(const CUtensorMap& tm_q, const CUtensorMap& tm_qr, const CUtensorMap& tm_kv, int fp8,
+                               const KeyWeightArgs& a, int sm_count, cudaStream_t s);
+cudaError_t launch_compact(const CompactArgs& a, int row_bytes, int sm_count, cudaStream_t s);
+cudaError_t launch_select(const SelectArgs& a, int sm_count, cudaStream_t s);
 // sm_count: of the current device (the combine runs one wave of blocks)
 cudaError_t launch_combine(const DecodeArgs& a, int max_groups, int sm_count, cudaStream_t s);
 cudaError_t launch_merge_states(const void* o_a, const float* lse_a, const void* o_b, const float* lse_b,

@@ -337,7 +337,9 @@ __device__ __forceinline__ void e4m3x16_to_bf16(const uint4 v, uint32_t (&o)[8])
 // reads its share of the whole tile, then all write.  e4m3 -> f16 -> f32 ->
 // bf16 is exact: every e4m3 value is a bf16 value.  Runs on the 128 threads of
 // the expansion warps; 9 chunks of 16 codes each.
-__device__ __forceinline__ void expand_e4m3_tile(uint32_t stage, int t) {
+// Keys from `live` on become zeros (kClean: the tile reaches past the last key).
+template <bool kClean>
+__device__ __forceinline__ void expand_e4m3_tile(uint32_t stage, int t, int live) {
   constexpr int kPer = kFp8TileBytes / 16 / 128;
   static_assert(kPer == 9, "8 latent chunks and 1 rope chunk per thread");
   uint4 v[kPer];
@@ -349,6 +351,11 @@ __device__ __forceinline__ void expand_e4m3_tile(uint32_t stage, int t) {
   }
   // rope: row t >> 1, chunk t & 1
   v[8] = lds128(stage + kFp8InPlace + kVBoxes * kFp8Box + (t >> 1) * 32 + (t & 1) * 16);
+  if constexpr (kClean) {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k)
+      if ((k < 8 ? ((t + 128 * k) >> 2) & 63 : t >> 1) >= live) v[k] = make_uint4(0, 0, 0, 0);
+  }
   named_bar_expand();
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
@@ -371,7 +378,8 @@ __device__ __forceinline__ void expand_e4m3_tile(uint32_t stage, int t) {
   }
 }
 
-template <int kVariant>
+// kShared: a plan of launch_shared_plan, in whose units b < 0 is prefix ~b.
+template <int kVariant, bool kShared = false>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kThreads, 1)
     decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_qr,
                   const __grid_constant__ CUtensorMap tm_kv, const __grid_constant__ CUtensorMap tm_kvr,
@@ -383,6 +391,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kTh
   // measured 1 % faster there; the e4m3 variants' softmax warps spill more
   // with it and the e4m3-query one ran 10 % slower)
   constexpr bool kTmaStore = kVariant == 0;
+  // the P.V issuer's warp zeroes the value rows behind a unit's last key: their
+  // probabilities are zero, but what a page holds there may be infinite or NaN
+  // (an e4m3 tile's are zeroed as it is expanded)
+  constexpr bool kCleans = kShared && !kCacheFp8;
   constexpr int kStages = Layout<kVariant>::kStages;
   constexpr int kXBytes = Layout<kVariant>::kXBytes;
   constexpr int kXRows = Layout<kVariant>::kXRows;
@@ -461,11 +473,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kTh
       const int xl = 256 * (int)rank, xr = kLkv + 32 * (int)rank;   // first latent / rope column of the CTA
       // cache lines are read once per pair: evict them first, so that the
       // split-KV partials, queries and block tables stay in L2
-      const uint64_t pol = l2_policy_evict_first();
+      const uint64_t pol_once = l2_policy_evict_first();
+      // (a prefix's are read by every group of rows behind it)
+      const uint64_t pol_again = kShared ? l2_policy_evict_last() : 0;
       for (int u = ubeg; u < uend; ++u) {
         const UnitRec ur = P.units[u];
         const UnitRec& gr = ur;
-        const int32_t* bt = a.block_table + (size_t)gr.b * a.max_pages;
+        const bool prefix = kShared && gr.b < 0;
+        const int32_t* bt =
+            prefix ? a.prefix_table + (size_t)~gr.b * a.max_prefix_pages : a.block_table + (size_t)gr.b * a.max_pages;
+        const int max_pages = prefix ? a.max_prefix_pages : a.max_pages;
+        const uint64_t pol = prefix ? pol_again : pol_once;
         // loads the CTA's columns of tile j (all sub-pages) into dst, counting on `full`:
         //   bf16:           4 latent boxes of 64 x 128 B, then the 64 x 64-B rope box
         //   e4m3 (v1):      4 latent boxes of 64 x 64 B, then the 64 x 32-B rope box
@@ -475,7 +493,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kTh
           const int key = j * kTile + sb * sub_rows;
           const int lp = key / a.page_size;
           int y = oob_row;                   // sub-pages past the group's last key are not read
-          if (key < gr.lmax && lp < a.max_pages) {
+          if (key < gr.lmax && lp < max_pages) {
             const int blk = bt[lp];
             if (blk >= 0 && blk < a.num_blocks)
               y = blk * a.page_size + key % a.page_size;
@@ -514,8 +532,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kTh
         }
         for (int jj = 0; jj < ntiles; ++jj, ++item) {
           // test aid: CTA 0 of cluster 0 never loads its first cache tile, so
-          // a consumer's bounded wait for it runs out
-          if (a.debug_skip_tile && cluster == 0 && rank == 0 && u == ubeg && jj == 0) continue;
+          // a consumer's bounded wait for it runs out (kShared: the plan's
+          // first unit, whichever cluster has it)
+          if (a.debug_skip_tile && (kShared ? u == 0 : cluster == 0 && u == ubeg) && rank == 0 && jj == 0) continue;
           const uint32_t slot = item % kStages, round = item / kStages;
           {
             // The block-table lookups precede the slot wait, so their
@@ -646,7 +665,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kTh
   };
   auto pv_issuer = [&]() {
     // ------------------------------------------------------ P.V-MMA issuer
-    if (lane == 0) {
+    if (kCleans || lane == 0) {
       constexpr uint32_t id_pv = idesc_bf16_f32(128, 256, 0, 1);    // MN-major values, N = 256
       // values = the CTA's output dims = boxes 0-3 of its stage; 16-key steps are 2048 B apart
       const uint64_t v_desc0 = smem_desc(smem_u32(stages), kBox, 1024, kSwizzle128B);
@@ -659,19 +678,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kTh
         for (int jj = 0; jj < ntiles; ++jj, ++item, ++it) {
           const uint32_t slot = item % kStages, round = item / kStages;
           wait_bar(ctx, &bars->kv_full[slot], round & 1);
+          if constexpr (kCleans) {
+            const int live = ur.lmax - (ur.tile_begin + jj) * kTile;   // keys from here on are behind the last
+            if (live < kTile) {
+              __syncwarp();
+              const uint32_t st = smem_u32(stages + slot * kStageBytes);
+              for (int p = 0; p < kVBoxes; ++p)
+                for (int at = live * 128 + lane * 16; at < kTile * 128; at += 32 * 16)
+                  sts128(st + p * kBox + at, 0, 0, 0, 0);
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
+          }
           wait_bar(ctx, &bars->p_full, it & 1);
           tc_fence_after();
           const uint64_t vd = v_desc0 + slot * kStageDesc;
           const uint32_t pa = tbase + kTmemP;
-          mma_ts(tbase + kTmemO, pa, vd, id_pv, jj > 0 ? 1u : 0u);
+          if (!kCleans || lane == 0) {
+            mma_ts(tbase + kTmemO, pa, vd, id_pv, jj > 0 ? 1u : 0u);
 #pragma unroll
-          for (int k = 1; k < kTile / 16; ++k) mma_ts(tbase + kTmemO, pa + 8 * k, vd + ((k * 2048) >> 4), id_pv, 1);
-          mma_commit(smem_u32(&bars->p_free));
-          mma_commit(smem_u32(&bars->kv_empty[slot]));
+            for (int k = 1; k < kTile / 16; ++k) mma_ts(tbase + kTmemO, pa + 8 * k, vd + ((k * 2048) >> 4), id_pv, 1);
+            mma_commit(smem_u32(&bars->p_free));
+            mma_commit(smem_u32(&bars->kv_empty[slot]));
+          }
         }
-        mma_commit(smem_u32(&bars->o_full));
+        if (!kCleans || lane == 0) mma_commit(smem_u32(&bars->o_full));
       }
-      mma_commit(smem_u32(&bars->p_drain));
+      if (!kCleans || lane == 0) mma_commit(smem_u32(&bars->p_drain));
       mbar_wait(smem_u32(&bars->p_drain), 0, a.wait_limit_ns);
     }
     __syncwarp();
@@ -715,7 +748,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kTh
             sts128(rowa + (((c0 + 1) ^ (r & 7)) << 4), o[4], o[5], o[6], o[7]);
           }
         } else {
-          expand_e4m3_tile(smem_u32(stages + slot * kStageBytes), te);
+          expand_e4m3_tile<kShared>(smem_u32(stages + slot * kStageBytes), te,
+                                    ur.lmax - (ur.tile_begin + jj) * kTile);
         }
         fence_proxy_async_smem();    // bf16 writes visible to the MMAs
         named_bar_expand();
@@ -1310,12 +1344,13 @@ size_t decode_smem_bytes(int variant) {
                       : (variant == 2 ? smem_bytes<2>() : (variant == 3 ? smem_bytes<3>() : smem_bytes<0>()));
 }
 
-cudaError_t launch_decode(const CUtensorMap& tm_q, const CUtensorMap& tm_qr, const CUtensorMap& tm_kv,
-                          const CUtensorMap& tm_kvr, const CUtensorMap& tm_out, const CUtensorMap& tm_part,
-                          int variant, const DecodeArgs& a, int num_clusters, cudaStream_t s) {
+namespace {
+
+template <class K>
+cudaError_t launch(K* kern, const CUtensorMap& tm_q, const CUtensorMap& tm_qr, const CUtensorMap& tm_kv,
+                   const CUtensorMap& tm_kvr, const CUtensorMap& tm_out, const CUtensorMap& tm_part, int variant,
+                   const DecodeArgs& a, int num_clusters, cudaStream_t s) {
   const size_t smem = decode_smem_bytes(variant);
-  auto kern = variant == 1 ? decode_kernel<1>
-                           : (variant == 2 ? decode_kernel<2> : (variant == 3 ? decode_kernel<3> : decode_kernel<0>));
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   // programmatic dependent launch: the prologue (barriers, TMEM, cluster
@@ -1334,6 +1369,23 @@ cudaError_t launch_decode(const CUtensorMap& tm_q, const CUtensorMap& tm_qr, con
   e = cudaLaunchKernelEx(&cfg, kern, tm_q, tm_qr, tm_kv, tm_kvr, tm_out, tm_part, a);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_decode(const CUtensorMap& tm_q, const CUtensorMap& tm_qr, const CUtensorMap& tm_kv,
+                          const CUtensorMap& tm_kvr, const CUtensorMap& tm_out, const CUtensorMap& tm_part,
+                          int variant, const DecodeArgs& a, int num_clusters, cudaStream_t s) {
+  auto kern = variant == 1 ? decode_kernel<1>
+                           : (variant == 2 ? decode_kernel<2> : (variant == 3 ? decode_kernel<3> : decode_kernel<0>));
+  return launch(kern, tm_q, tm_qr, tm_kv, tm_kvr, tm_out, tm_part, variant, a, num_clusters, s);
+}
+
+cudaError_t launch_decode_shared(const CUtensorMap& tm_q, const CUtensorMap& tm_qr, const CUtensorMap& tm_kv,
+                                 const CUtensorMap& tm_kvr, const CUtensorMap& tm_out, const CUtensorMap& tm_part,
+                                 int variant, const DecodeArgs& a, int num_clusters, cudaStream_t s) {
+  return launch(variant == 1 ? decode_kernel<1, true> : decode_kernel<0, true>, tm_q, tm_qr, tm_kv, tm_kvr, tm_out,
+                tm_part, variant, a, num_clusters, s);
 }
 
 }  // namespace mla

@@ -143,6 +143,103 @@ __global__ void __launch_bounds__(256, 2) combine_kernel(const DecodeArgs a) {
   }
 }
 
+// The merge of mla_decode_shared: a row's partials are those of its own group
+// and those of the row among its prefix's groups.  Items, threads and loads as
+// in combine_kernel; rows that the decode wrote itself (one piece, and no
+// prefix keys) are left.
+__global__ void __launch_bounds__(256, 2) combine_shared_kernel(const DecodeArgs a) {
+  const Plan& P = a.plan;
+  constexpr int kQuads = kRows / 4;
+  constexpr int kFew = 4;             // partials whose loads are all in flight at once
+  constexpr int kChunks = kLkv / 32;
+  const int VG = (int)gridDim.x * 4;
+  const int first = P.header->own_groups * kQuads, items = P.header->num_groups * kQuads;
+  const int own_groups = P.header->own_groups;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out);
+  const int sub = threadIdx.x & 15;
+  const int d0 = sub * 8;
+  const int quad_row = (threadIdx.x >> 4) & 3;
+  for (int item = first + (int)blockIdx.x * 4 + (int)(threadIdx.x >> 6); item < items; item += VG) {
+    const GroupRec gr = P.groups[item / kQuads];
+    const int2 behind = P.behind[item / kQuads];
+    const int r = (item % kQuads) * 4 + quad_row;
+    if (r >= gr.nrows || gr.row0 + r >= a.total_rows) continue;
+    const int R = gr.row0 + r;
+    // the row among its prefix's rows
+    const int pr = R - behind.y, pg = behind.x + pr / kRows;
+    int pre = 0;
+    size_t pre_at = 0;
+    if (pg < own_groups) {
+      pre = P.groups[pg].pieces;
+      pre_at = (size_t)P.groups[pg].ubase * kRows + pr % kRows;
+    }
+    const int n = gr.pieces + pre;
+    if (pre == 0 && gr.pieces == 1) continue;   // written by the decode kernel
+    const size_t own_at = (size_t)gr.ubase * kRows + r;
+    auto at = [&](int i) { return i < pre ? pre_at + (size_t)i * kRows : own_at + (size_t)(i - pre) * kRows; };
+    float acc[32];
+#pragma unroll
+    for (int k = 0; k < 32; ++k) acc[k] = 0.f;
+    // in batches of kFew partials, each merged into what the batches before left
+    float mx = -INFINITY, wsum = 0.f;
+    for (int i0 = 0; i0 < n; i0 += kFew) {
+      float l[kFew], sc[kFew][4];
+      uint4 x[kFew][4];
+#pragma unroll
+      for (int i = 0; i < kFew; ++i) {
+        l[i] = -INFINITY;
+        if (i0 + i < n) {
+          const size_t p = at(i0 + i);
+          l[i] = P.part_lse[p];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            sc[i][c] = P.part_scale[p * kChunks + 4 * c + (sub >> 2)];
+            x[i][c] = *reinterpret_cast<const uint4*>(P.part_o + p * kLkv + 128 * c + d0);
+          }
+        }
+      }
+      float top = mx;
+#pragma unroll
+      for (int i = 0; i < kFew; ++i) top = fmaxf(top, l[i]);
+      if (top == -INFINITY) continue;
+      const float keep = __expf(mx - top);
+      wsum *= keep;
+#pragma unroll
+      for (int k = 0; k < 32; ++k) acc[k] *= keep;
+#pragma unroll
+      for (int i = 0; i < kFew; ++i) {
+        if (i0 + i < n) {
+          const float w = __expf(l[i] - top);
+          wsum += w;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) accumulate(acc + 8 * c, w * sc[i][c], x[i][c]);
+        }
+      }
+      mx = top;
+    }
+    float lse = -INFINITY;
+    if (mx != -INFINITY) {
+      const float inv = 1.f / wsum;
+#pragma unroll
+      for (int k = 0; k < 32; ++k) acc[k] *= inv;
+      lse = mx + __logf(wsum);
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      uint4 v;
+      __nv_bfloat162 h;
+      h = __floats2bfloat162_rn(acc[8 * c + 0], acc[8 * c + 1]); v.x = *reinterpret_cast<uint32_t*>(&h);
+      h = __floats2bfloat162_rn(acc[8 * c + 2], acc[8 * c + 3]); v.y = *reinterpret_cast<uint32_t*>(&h);
+      h = __floats2bfloat162_rn(acc[8 * c + 4], acc[8 * c + 5]); v.z = *reinterpret_cast<uint32_t*>(&h);
+      h = __floats2bfloat162_rn(acc[8 * c + 6], acc[8 * c + 7]); v.w = *reinterpret_cast<uint32_t*>(&h);
+      *reinterpret_cast<uint4*>(out + (size_t)R * kLkv + 128 * c + d0) = v;
+    }
+    if (a.lse && sub == 0) a.lse[R] = lse;
+  }
+}
+
 template <bool kBf16>
 __device__ __forceinline__ void load8(const void* base, size_t idx, float (&x)[8]) {
   if (kBf16) {
@@ -238,6 +335,24 @@ cudaError_t launch_combine(const DecodeArgs& a, int max_groups, int sm_count, cu
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cudaError_t e = cudaLaunchKernelEx(&cfg, combine_kernel, a);
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
+}
+
+cudaError_t launch_combine_shared(const DecodeArgs& a, int max_groups, int sm_count, cudaStream_t s) {
+  const long long max_items = (long long)max_groups * (kRows / 4);
+  long long blocks = (long long)(sm_count > 0 ? sm_count : 1) * 2;
+  if (blocks * 4 > max_items) blocks = (max_items + 3) / 4;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(blocks < 1 ? 1 : blocks));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, combine_shared_kernel, a);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }

@@ -16,6 +16,10 @@
 //     pieces and pieces go to the pair whose span holds their midpoint.
 // Pieces of a split group write partials that the combine kernel merges
 // with the LSE rule of merge_attn_states.
+//
+// For mla_decode_shared (kShared) the prefixes come before the requests, as
+// sources of groups of their own: the rows of all requests behind a prefix,
+// together, over the prefix's keys, every one of which every row sees.
 #include "cache_rows.cuh"
 #include "common.cuh"
 
@@ -97,12 +101,12 @@ __device__ __forceinline__ int muldiv(int a, int b, int c) {
 // cache rows (blocks 1 .. write_blocks, 8 tokens a block; 1 bf16 cache,
 // 2 e4m3 cache) and, in mode 3 (e4m3 cache), the query's quantisation (the
 // remaining blocks, grid-stride over its 8-value vectors).
-template <bool kStaged, int kMode>
+template <bool kStaged, int kMode, bool kShared = false>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* __restrict__ seq_lens,
                                                     const int32_t* __restrict__ qsl, int batch, int N,
                                                     int max_pages, int page_size, int num_splits, int C,
                                                     int GR, Plan P, const CacheWriteArgs w, const QuantArgs qa,
-                                                    int write_blocks) {
+                                                    int write_blocks, const SharedArgs sh) {
   if constexpr (kMode != 0) {
     if (blockIdx.x > 0) {
       // as the cache-write kernel: wait for the kernel before, then let the
@@ -148,8 +152,53 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* __res
   const long long kv_cap = (long long)max_pages * page_size;
   const int gshift = __ffs(GR) - 1;   // GR is a power of two
 
-  // 1. groups of every request
+  // 1. groups of every request (kShared: of every prefix, then of every
+  //    request; b < 0 marks prefix ~b)
   int carry = 0;
+  const int np = kShared ? sh.prefixes : 0;
+  for (int base = 0; base < np; base += kPlanThreads) {
+    const int p = base + tid;
+    int ng = 0, q0 = 0, rows = 0;
+    if (p < np) {
+      const int r0 = sh.begin[p], r1 = sh.begin[p + 1];
+      const bool fits = r0 >= 0 && r0 <= r1 && r1 <= batch && (p > 0 || r0 == 0) && (p < np - 1 || r1 == batch);
+      int q1 = 0;
+      if (fits) {
+        q0 = qsl ? qsl[r0] : r0;
+        q1 = qsl ? qsl[r1] : r1;
+      }
+      if (!fits || q0 < 0 || q0 > q1 || q1 > sh.total_q) {
+        atomicOr(&s_flags, 8);   // MLA_DEVERR_BAD_QSL
+        q0 = q1 = 0;
+      }
+      rows = (q1 - q0) * N;
+      ng = (rows + GR - 1) >> gshift;
+    }
+    int total;
+    const int gb = block_excl_scan(ng, &total, s_sums, sums_row) + carry;
+    if (p < np && ng > 0) {
+      const long long cap = (long long)sh.max_pages * page_size;
+      long long keys = sh.lens[p];
+      if (keys > cap) {
+        atomicOr(&s_flags, 2);   // MLA_DEVERR_BAD_SEQ_LEN
+        keys = cap;
+      }
+      if (keys < 0) keys = 0;
+      for (int g = 0; g < ng && gb + g < P.max_groups; ++g) {
+        if (kStaged) s_kbase[gb + g] = (int)keys;   // every row sees them all
+        GroupRec r;
+        r.b = ~p;
+        r.row0 = q0 * N + g * GR;
+        r.nrows = min(GR, rows - g * GR);
+        r.lmax = (int)keys;
+        r.tiles = (int)((keys + kTile - 1) / kTile);
+        r.pieces = r.ubase = r.tpos = 0;
+        grp[gb + g] = r;
+      }
+    }
+    carry += total;
+  }
+  const int own_groups = carry;   // kShared: the first group of a request
   for (int base = 0; base < batch; base += kPlanThreads) {
     const int b = base + tid;
     int sq = 0, ng = 0, q0 = 0;
@@ -159,6 +208,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* __res
       q0 = qsl ? qsl[b] : b;
       sq = qsl ? qsl[b + 1] - q0 : 1;
       seq = seq_lens[b];
+      if (kShared && (sq < 0 || q0 < 0 || q0 > sh.total_q - sq)) {
+        atomicOr(&s_flags, 8);
+        sq = 0;
+      }
       if (sq < 0) sq = 0;
       ng = (int)(((long long)sq * N + GR - 1) >> gshift);
     }
@@ -192,6 +245,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* __res
     carry += total;
   }
   int G = carry;
+  if (kShared) {
+    __syncthreads();
+    if (s_flags & 8) G = 0;   // the rows of prefixes and requests do not fit together: plan nothing
+    __syncthreads();
+  }
   if (G > P.max_groups) {  // query_start_loc disagrees with total_q: plan nothing
     if (tid == 0) atomicOr(&s_flags, 8);  // MLA_DEVERR_BAD_QSL
     G = 0;
@@ -268,8 +326,34 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* __res
     const GroupRec r = grp[g];
     const int s0 = r.tpos + kUnitCostTiles;       // first real tile on the axis
     int kbase = 0;
+    bool partial = r.pieces > 1;
+    if (kShared) {
+      if (g < own_groups) {
+        partial = true;           // joined with its rows' own keys
+      } else {
+        // the prefix of request r.b: the last one that begins at or before it
+        // (one without requests begins where the next one does)
+        int lo = 0, hi = sh.prefixes - 1;
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) >> 1;
+          if (sh.begin[mid] <= r.b) lo = mid; else hi = mid - 1;
+        }
+        const int first = qsl ? qsl[sh.begin[lo]] : sh.begin[lo];
+        // its first group: the last one of a prefix that begins at or before
+        // its first row, and has rows
+        int a = 0, z = own_groups - 1;
+        while (a < z) {
+          const int mid = (a + z + 1) >> 1;
+          if (grp[mid].row0 <= first * N) a = mid; else z = mid - 1;
+        }
+        P.behind[g] = make_int2(a, first * N);
+        partial = partial || grp[a].tiles > 0;
+      }
+    }
     if (kStaged) {
       kbase = s_kbase[g];
+    } else if (kShared && r.b < 0) {
+      kbase = r.lmax;
     } else if (r.pieces > 0) {
       const int sq = qsl ? qsl[r.b + 1] - qsl[r.b] : 1;
       const int q0 = qsl ? qsl[r.b] : r.b;
@@ -294,7 +378,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* __res
         u.tile_begin = max(s0, span_start(cl)) - s0;
         u.tile_end = min(s0 + r.tiles, span_start(cl + 1)) - s0;
       }
-      u.slot = r.pieces > 1 ? r.ubase + i : -1;
+      u.slot = partial ? r.ubase + i : -1;
       P.units[r.ubase + i] = u;
       ucl[r.ubase + i] = cl;
     }
@@ -320,7 +404,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* __res
     h.num_clusters = C;
     h.total_tiles = T;
     h.tiles_per_cluster = W;
-    h.pad[0] = h.pad[1] = 0;
+    h.own_groups = own_groups;
+    h.pad = 0;
     *P.header = h;
   }
 }
@@ -356,12 +441,33 @@ cudaError_t launch_plan(const int32_t* seq_lens, const int32_t* qsl, int batch, 
   const CacheWriteArgs w = writes ? *write : CacheWriteArgs{};
   const QuantArgs qa = quant ? *quant : QuantArgs{};
   using Kernel = void (*)(const int32_t*, const int32_t*, int, int, int, int, int, int, int, Plan,
-                          const CacheWriteArgs, const QuantArgs, int);
+                          const CacheWriteArgs, const QuantArgs, int, const SharedArgs);
   static const Kernel kernels[2][4] = {
       {plan_kernel<false, 0>, plan_kernel<false, 1>, plan_kernel<false, 2>, plan_kernel<false, 3>},
       {plan_kernel<true, 0>, plan_kernel<true, 1>, plan_kernel<true, 2>, plan_kernel<true, 3>}};
   cudaError_t e = cudaLaunchKernelEx(&cfg, kernels[staged][mode], seq_lens, qsl, batch, num_heads, max_pages,
-                                     page_size, num_splits, num_clusters, group_rows, plan, w, qa, write_blocks);
+                                     page_size, num_splits, num_clusters, group_rows, plan, w, qa, write_blocks,
+                                     SharedArgs{});
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
+}
+
+cudaError_t launch_shared_plan(const int32_t* seq_lens, const int32_t* qsl, int batch, int num_heads, int max_pages,
+                               int page_size, int num_splits, int num_clusters, Plan plan, const SharedArgs& shared,
+                               cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(1);
+  cfg.blockDim = dim3(kPlanThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const bool staged = plan.max_groups <= kPlanSmemGroups && plan.max_units <= kPlanSmemUnits;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, staged ? plan_kernel<true, 0, true> : plan_kernel<false, 0, true>, seq_lens,
+                                     qsl, batch, num_heads, max_pages, page_size, num_splits, num_clusters, kRows, plan,
+                                     CacheWriteArgs{}, QuantArgs{}, 0, shared);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
