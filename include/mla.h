@@ -681,7 +681,8 @@ MLA_API int mla_evict_select(const float* weights, int64_t weight_stride, int we
  *                belong to one request alone (a shared prefix is not compacted:
  *                give the requests' own pages); a page outside [0, num_blocks)
  *                sets MLA_DEVERR_BAD_BLOCK and its rows are not moved
- *   cache        bf16 or e4m3 rows of 576, any page_size >= 1
+ *   cache        bf16 or e4m3 rows of 576, any page_size >= 1, num_blocks *
+ *                page_size < 2^31
  *   weights      as for mla_key_weights, or NULL
  *   status       one int32 on the device, or NULL: OR-ed into, never cleared
  * cache, weights and status overlap no other argument.  One launch.

@@ -990,9 +990,9 @@ int mla_cache_compact(void* cache, int64_t num_blocks, int page_size, int cache_
   if (batch < 0 || max_keep < 0) return fail(MLA_ERR_INVALID_ARG, "batch and max_keep must be >= 0");
   if (cache_dtype != MLA_BF16 && cache_dtype != MLA_FP8_E4M3)
     return fail(MLA_ERR_INVALID_ARG, "cache_dtype must be MLA_BF16 or MLA_FP8_E4M3 (got %d)", cache_dtype);
-  if (page_size <= 0 || num_blocks <= 0 || max_pages_per_seq <= 0 || num_blocks > (1LL << 40) / page_size)
+  if (page_size <= 0 || num_blocks <= 0 || max_pages_per_seq <= 0 || num_blocks > ((1LL << 31) - 1) / page_size)
     return fail(MLA_ERR_INVALID_ARG,
-                "page_size, num_blocks and max_pages_per_seq must be positive and num_blocks * page_size <= 2^40");
+                "page_size, num_blocks and max_pages_per_seq must be positive and num_blocks * page_size < 2^31");
   if (batch == 0 || max_keep == 0) return ok();
   if (batch > kMaxBatch) return fail(MLA_ERR_UNSUPPORTED, "batch must be <= %d", kMaxBatch);
   if (max_keep > kMaxKeys) return fail(MLA_ERR_UNSUPPORTED, "max_keep must be <= 2^30");

@@ -286,6 +286,19 @@ inline cudaError_t allow_smem(K* kernel, size_t bytes, std::atomic<uint64_t>& do
   return e;
 }
 
+// Let `kernel` be launched in clusters of up to 16 CTAs; `done` as above.
+template <class K>
+inline cudaError_t allow_wide_clusters(K* kernel, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (bit && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
 // ---- launchers (return cudaError_t of the launch)
 cudaError_t launch_rope_write(const RopeWriteArgs& w, int fp8, int pairs, cudaStream_t s);
 KvProjShape kv_proj_shape(int64_t T, int64_t C, int sms);

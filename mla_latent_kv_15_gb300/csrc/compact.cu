@@ -8,10 +8,11 @@
 // earlier wave writes.  So nothing is read after it was overwritten, whatever
 // the order of keep, with no scratch rows and no waiting between clusters.
 //
-// A copy, bound by HBM or, for one request, by how many rows its cluster has in
-// flight: every thread moves one row of a wave by two bulk copies (global ->
-// shared -> global), kStages waves deep, and looks its pages up two waves ahead
-// (the chain keep -> block table -> row would cost a wave its time).
+// A copy, bound by HBM or, for one request, by its chain of latencies (index,
+// page, row, store).  A CTA has a warp that loads a wave's rows into shared
+// memory and one that stores them, by a bulk copy a row, and two that look the
+// rows up ahead of them; two CTAs share an SM, so that one issues copies while
+// the other's lanes do (a warp issues its lanes' copies one after the other).
 #include "common.cuh"
 #include "ptx.cuh"
 
@@ -20,13 +21,30 @@ namespace {
 
 using namespace ptx;
 
+constexpr int kRowsPerWave = 32;     // of a CTA: a lane each
+constexpr int kThreads = 128;        // warp 0 loads, 1 stores, 2 and 3 look up even and odd waves
+constexpr int kLook = 8;             // waves looked up ahead
+constexpr int kMaxCtas = 16;         // of a request's cluster
+
 template <int kRowBytes>
 struct CompactShape {
-  static constexpr int kRowsPerCta = kRowBytes > 1024 ? 32 : 64;   // threads too
-  static constexpr int kStages = 6;
-  static constexpr int kStageBytes = kRowsPerCta * kRowBytes;
-  static constexpr size_t kSmem = (size_t)kStages * (kStageBytes + kRowsPerCta * 12) + 8 * kStages;
+  static constexpr int kStages = kRowBytes > 1024 ? 3 : 6;
+  static constexpr int kStageBytes = kRowsPerWave * kRowBytes;
 };
+
+struct Bars {
+  uint64_t full[6], empty[6], look_full[kLook], look_empty[kLook];
+  uint64_t go[2];                    // every CTA of the cluster has its rows of the wave
+  int src[kLook][kRowsPerWave], dst[kLook][kRowsPerWave];   // cache rows; dst < 0: nothing moves
+  float weight[kLook][kRowsPerWave];
+  int abort;
+};
+
+template <int kRowBytes>
+constexpr size_t smem_bytes() {
+  return CompactShape<kRowBytes>::kStages * CompactShape<kRowBytes>::kStageBytes + sizeof(Bars);
+}
+static_assert(2 * (smem_bytes<1152>() + 1024) <= 233472 && 2 * (smem_bytes<576>() + 1024) <= 233472, "two CTAs an SM");
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
@@ -38,130 +56,161 @@ __device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t byt
                : "memory");
 }
 
+// A bounded wait; false once some wait of the CTA has run out.
+__device__ __forceinline__ bool wait(Bars* bars, int* status, uint64_t* bar, uint32_t parity) {
+  const uint32_t at = smem_u32(bar);
+  if (mbar_try_wait(at, parity)) return true;
+  const uint64_t t0 = globaltimer();
+  while (!mbar_try_wait_hint(at, parity, kWaitHintNs)) {
+    if (*(volatile int*)&bars->abort) return false;
+    if (globaltimer() - t0 > MLA_WAIT_LIMIT_NS) {
+      *(volatile int*)&bars->abort = 1;
+      if (status) atomicOr(status, 1);        // MLA_DEVERR_TIMEOUT
+      return false;
+    }
+  }
+  return true;
+}
+
 template <int kRowBytes>
-__global__ void __launch_bounds__(CompactShape<kRowBytes>::kRowsPerCta) compact_kernel(const CompactArgs a, int ctas) {
+__global__ void __launch_bounds__(kThreads) compact_kernel(const CompactArgs a, int ctas) {
   using S = CompactShape<kRowBytes>;
-  constexpr int R = S::kRowsPerCta, kStages = S::kStages;
-  constexpr int kLead = kStages - 2;          // waves whose loads are out
+  constexpr int R = kRowsPerWave, kStages = S::kStages;
   extern __shared__ __align__(128) uint8_t smem[];
-  int64_t* to = reinterpret_cast<int64_t*>(smem + kStages * S::kStageBytes);   // [kStages][R] slot, -1: stays
-  float* wbuf = reinterpret_cast<float*>(to + kStages * R);                    // [kStages][R]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(wbuf + kStages * R);
-  const int t = threadIdx.x;
+  Bars* bars = reinterpret_cast<Bars*>(smem + kStages * S::kStageBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int b = blockIdx.x / ctas, rank = blockIdx.x % ctas;
-  if (t == 0) {
-    for (int i = 0; i < kStages; ++i) mbar_init(smem_u32(&bars[i]), R);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(smem_u32(&bars->full[i]), R);
+      mbar_init(smem_u32(&bars->empty[i]), 1);
+    }
+    for (int i = 0; i < kLook; ++i) {
+      mbar_init(smem_u32(&bars->look_full[i]), 1);
+      mbar_init(smem_u32(&bars->look_empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&bars->go[i]), ctas);
+    bars->abort = 0;
     fence_mbar_init();
   }
-  __syncthreads();
+  cluster_sync();
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   int len = a.keep_lens[b];
   if (len > a.max_keep) {
-    if (t == 0 && rank == 0 && a.status) atomicOr(a.status, 2);   // MLA_DEVERR_BAD_SEQ_LEN
+    if (threadIdx.x == 0 && rank == 0 && a.status) atomicOr(a.status, 2);   // MLA_DEVERR_BAD_SEQ_LEN
     len = a.max_keep;
   }
   if (len < 0) len = 0;
   const int per_wave = ctas * R;
   const int waves = (len + per_wave - 1) / per_wave;
-  const int32_t* keep = a.keep + (int64_t)b * a.max_keep;
-  const int32_t* table = a.block_table + (int64_t)b * a.max_pages;
+  const int first = rank * R + lane;          // the lane's row of wave w is first + w * per_wave
   float* weights = a.weights ? a.weights + (int64_t)b * a.weight_stride : nullptr;
-  const int first = rank * R + t;
 
-  // Two steps ahead of a wave's loads: the source index, then the two pages.
-  struct Look {
-    int src, pg_src, pg_dst;    // src < 0: nothing to move
-    float weight;
-  };
-  auto index_of = [&](int w) {
-    const int64_t i = (int64_t)w * per_wave + first;
-    return w < waves && i < len ? keep[i] : -2;
-  };
-  auto pages_of = [&](int w, int src) {
-    Look k{-1, 0, 0, 0.f};
-    if (src == -2) return k;
-    const int i = w * per_wave + first;
+  if (warp >= 2) {
+    // ------------------------------------------------------------- look-ups
+    const int32_t* keep = a.keep + (int64_t)b * a.max_keep;
+    const int32_t* table = a.block_table + (int64_t)b * a.max_pages;
     const int64_t cap = (int64_t)a.max_pages * a.page_size;
-    if (src < i || src >= cap || (weights && src >= a.weight_len)) {
-      if (a.status) atomicOr(a.status, 16);   // MLA_DEVERR_BAD_POSITION
-      return k;
-    }
-    if (src == i) return k;                   // in its place already
-    k.src = src;
-    k.pg_src = table[src / a.page_size];
-    k.pg_dst = table[i / a.page_size];
-    if (weights) k.weight = weights[src];
-    return k;
-  };
-  auto issue = [&](int w, const Look& k) {
-    const int st = w % kStages;
-    const uint32_t bar = smem_u32(&bars[st]);
-    int64_t dst = -1;
-    if (k.src >= 0) {
-      if (k.pg_src < 0 || k.pg_src >= a.num_blocks || k.pg_dst < 0 || k.pg_dst >= a.num_blocks) {
-        if (a.status) atomicOr(a.status, 4);  // MLA_DEVERR_BAD_BLOCK
-      } else {
-        const int i = w * per_wave + first;
-        dst = (int64_t)k.pg_dst * a.page_size + i % a.page_size;
-        const int64_t src = (int64_t)k.pg_src * a.page_size + k.src % a.page_size;
-        mbar_expect_tx(bar, kRowBytes);
-        bulk_load(smem_u32(smem + st * S::kStageBytes + t * kRowBytes), a.cache + src * kRowBytes, kRowBytes, bar);
+    auto index_of = [&](int w) {
+      const int64_t i = first + (int64_t)w * per_wave;
+      return i < len ? keep[i] : -1;
+    };
+    int next = index_of(warp - 2);
+    for (int w = warp - 2; w < waves; w += 2) {
+      const int i = first + w * per_wave, from = next;
+      next = index_of(w + 2);
+      const int at = w % kLook;
+      int src = -1, dst = -1;
+      float weight = 0.f;
+      if (i < len) {
+        if (from < i || from >= cap || (weights && from >= a.weight_len)) {
+          if (a.status) atomicOr(a.status, 16);   // MLA_DEVERR_BAD_POSITION
+        } else if (from != i) {               // else in its place already
+          const int p0 = table[from / a.page_size], p1 = table[i / a.page_size];
+          if (weights) weight = weights[from];
+          if (p0 < 0 || p0 >= a.num_blocks || p1 < 0 || p1 >= a.num_blocks) {
+            if (a.status) atomicOr(a.status, 4);  // MLA_DEVERR_BAD_BLOCK
+          } else {
+            src = p0 * a.page_size + from % a.page_size;
+            dst = p1 * a.page_size + i % a.page_size;
+          }
+        }
       }
+      if (!wait(bars, a.status, &bars->look_empty[at], ((w / kLook) & 1) ^ 1)) break;
+      bars->src[at][lane] = src;
+      bars->dst[at][lane] = dst;
+      bars->weight[at][lane] = weight;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars->look_full[at]));
     }
-    if (dst < 0) mbar_arrive(bar);
-    to[st * R + t] = dst;
-    wbuf[st * R + t] = k.weight;              // (read before the wave's barrier, as the row)
-  };
-
-  int src_next = index_of(0);
-  Look look = pages_of(0, src_next);
-  src_next = index_of(1);
-  for (int w = 0; w < kLead && w < waves; ++w) {
-    const Look next = pages_of(w + 1, src_next);
-    src_next = index_of(w + 2);
-    issue(w, look);
-    look = next;
+  } else if (warp == 0) {
+    // ---------------------------------------------------------------- loads
+    for (int w = 0; w < waves; ++w) {
+      const int at = w % kLook, st = w % kStages;
+      if (!wait(bars, a.status, &bars->look_full[at], (w / kLook) & 1)) break;
+      if (!wait(bars, a.status, &bars->empty[st], ((w / kStages) & 1) ^ 1)) break;
+      __syncwarp();
+      const uint32_t bar = smem_u32(&bars->full[st]);
+      if (bars->dst[at][lane] >= 0) {
+        mbar_expect_tx(bar, kRowBytes);
+        bulk_load(smem_u32(smem + st * S::kStageBytes + lane * kRowBytes),
+                  a.cache + (int64_t)bars->src[at][lane] * kRowBytes, kRowBytes, bar);
+      } else {
+        mbar_arrive(bar);
+      }
+      __syncwarp();
+    }
+  } else {
+    // --------------------------------------------------------------- stores
+    for (int w = 0; w < waves; ++w) {
+      const int at = w % kLook, st = w % kStages;
+      if (!wait(bars, a.status, &bars->look_full[at], (w / kLook) & 1)) break;
+      const int dst = bars->dst[at][lane];
+      const float weight = bars->weight[at][lane];
+      if (!wait(bars, a.status, &bars->full[st], (w / kStages) & 1)) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars->look_empty[at]));
+      // every row of the wave is in some CTA's shared memory before one is
+      // written (the arrivals order nothing but this: those rows have been read)
+      if (ctas > 1) {
+        if (lane < ctas) mbar_arrive_remote(mapa(smem_u32(&bars->go[w & 1]), lane));
+        if (!wait(bars, a.status, &bars->go[w & 1], (w >> 1) & 1)) break;
+        __syncwarp();
+      }
+      if (dst >= 0) {
+        bulk_store(a.cache + (int64_t)dst * kRowBytes, smem_u32(smem + st * S::kStageBytes + lane * kRowBytes), kRowBytes);
+        if (weights) weights[first + w * per_wave] = weight;
+      }
+      bulk_commit_group();                    // one a wave, empty or not
+      bulk_wait_group_read<1>();              // the wave before has left its stage
+      __syncwarp();
+      if (w > 0 && lane == 0) mbar_arrive(smem_u32(&bars->empty[(w - 1) % kStages]));
+    }
+    bulk_wait_all();
   }
-  bool dead = false;
-  for (int w = 0; w < waves; ++w) {
-    const int st = w % kStages, ahead = w + kLead;
-    if (ahead < waves) {
-      // the stage's last row has left it (this thread's own, two waves ago)
-      bulk_wait_group_read<1>();
-      const Look next = pages_of(ahead + 1, src_next);
-      src_next = index_of(ahead + 2);
-      issue(ahead, look);
-      look = next;
+  __syncwarp();
+  if (*(volatile int*)&bars->abort) {
+    // given up: copies in flight finish well within this time
+    const uint64_t t0 = globaltimer();
+    while (globaltimer() - t0 < 1000000ull) {
     }
-    if (!dead && !mbar_wait(smem_u32(&bars[st]), (w / kStages) & 1)) {
-      dead = true;                            // nothing more is written by this thread
-      if (a.status) atomicOr(a.status, 1);    // MLA_DEVERR_TIMEOUT
-    }
-    // every row of the wave is in some CTA's shared memory before one is written
-    __syncwarp();
-    cluster_sync();
-    const int64_t dst = to[st * R + t];
-    if (!dead && dst >= 0) {
-      bulk_store(a.cache + dst * kRowBytes, smem_u32(smem + st * S::kStageBytes + t * kRowBytes), kRowBytes);
-      if (weights) weights[w * per_wave + first] = wbuf[st * R + t];
-    }
-    bulk_commit_group();                      // one a wave, empty or not
   }
-  bulk_wait_all();
+  __syncwarp();
+  cluster_sync();                             // no CTA leaves while another may signal it
 }
 
 template <int kRowBytes>
 cudaError_t launch(const CompactArgs& a, int ctas, cudaStream_t s) {
-  using S = CompactShape<kRowBytes>;
-  static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(compact_kernel<kRowBytes>, S::kSmem, done);
+  static std::atomic<uint64_t> done{0}, wide{0};
+  cudaError_t e = allow_smem(compact_kernel<kRowBytes>, smem_bytes<kRowBytes>(), done);
   if (e != cudaSuccess) return e;
+  if (ctas > 8 && (e = allow_wide_clusters(compact_kernel<kRowBytes>, wide)) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.batch * (unsigned)ctas);
-  cfg.blockDim = dim3(S::kRowsPerCta);
-  cfg.dynamicSmemBytes = S::kSmem;
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem_bytes<kRowBytes>();
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -179,10 +228,9 @@ cudaError_t launch(const CompactArgs& a, int ctas, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_compact(const CompactArgs& a, int row_bytes, int sm_count, cudaStream_t s) {
-  // as many CTAs a request as give every SM one, no more than its rows fill
-  const int rows = row_bytes > 1024 ? CompactShape<1152>::kRowsPerCta : CompactShape<576>::kRowsPerCta;
+  // as many CTAs a request as are on the card at once, no more than its rows fill
   int ctas = 1;
-  while (ctas < 8 && a.batch * ctas * 2 <= sm_count && ctas * rows < a.max_keep) ctas *= 2;
+  while (ctas < kMaxCtas && (int64_t)a.batch * ctas <= sm_count && ctas * kRowsPerWave < a.max_keep) ctas *= 2;
   return row_bytes > 1024 ? launch<1152>(a, ctas, s) : launch<576>(a, ctas, s);
 }
 

@@ -3,14 +3,16 @@
 // accumulated weight, ties to the lowest index, in ascending order.
 //
 // A request belongs to one cluster of CTAs, each with a contiguous slice of its
-// weights in shared memory.  The smallest weight kept is found by its digits:
-// 32-bit codes that order as the weights do, four passes of 8 bits, a histogram
-// of the digits behind the digits found so far, summed over the cluster.  Then
-// every warp counts the codes above and at the threshold in its part of the
-// slice, and writes its kept indices behind those of the warps before it.
+// weights in shared memory, as 32-bit codes that order as the weights do.  The
+// smallest code kept is found by its digits, 11, 11 and 10 bits from the top: a
+// histogram of the digit behind the digits found so far, summed over the
+// cluster, gives the digit that holds the last place.  (Weights are positive,
+// so the first digit is the exponent and two bits of the mantissa: few codes
+// are left for the second.)  Then every warp counts the codes above and at the
+// threshold in its part of the slice, and writes its kept indices behind those
+// of the warps before it.
 //
-// Bound by the passes' latency (a weight is read from memory once): barriers of
-// a cluster, and the histogram's atomics, which lanes of equal digits share.
+// A weight is read from memory once: bound by the chain of passes and barriers.
 #include "common.cuh"
 #include "ptx.cuh"
 
@@ -21,6 +23,7 @@ using namespace ptx;
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
+constexpr int kBins = 2048;
 constexpr int kSliceMax = 40960;     // codes of a slice held in shared memory
 
 // Codes order as weights do: -0 as +0, NaN below everything.
@@ -35,20 +38,48 @@ __device__ __forceinline__ int ld_cluster(const int* local, int rank) {
   asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(mapa(smem_u32(local), (uint32_t)rank)) : "memory");
   return v;
 }
+__device__ __forceinline__ int4 ld_cluster4(const int* local, int rank) {
+  int4 v;
+  asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(mapa(smem_u32(local), (uint32_t)rank))
+               : "memory");
+  return v;
+}
+
+__device__ __forceinline__ int warp_incl_scan(int v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+
+struct Shared {
+  alignas(16) int hist[2][kBins];    // of two digits in turn: one is read by the cluster while the other is counted
+  int warp_sum[kWarps];
+  int digit, above;
+  int count[2];                      // codes of the slice above and at the threshold, for the cluster
+  int w_above[kWarps], w_equal[kWarps];
+};
 
 // kHeld: slices fit in shared memory; else codes are made from the weights in
 // every pass.
 template <bool kHeld>
 __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a, int ctas) {
-  extern __shared__ uint32_t codes[];
-  __shared__ int hist[2][256];       // of two passes in turn: a CTA may read the last pass's beside this one's counting
-  __shared__ int total[256];
-  __shared__ int s_digit, s_above;
-  __shared__ int s_count[2];         // codes of the slice above and at the threshold, for the cluster
-  __shared__ int w_above[kWarps], w_equal[kWarps];
+  extern __shared__ __align__(16) uint32_t codes[];
+  __shared__ Shared sm;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = blockIdx.x / ctas, rank = blockIdx.x % ctas;
-  for (int i = tid; i < 512; i += kThreads) (&hist[0][0])[i] = 0;
+  auto cluster_wide = [&]() {
+    if (ctas > 1)
+      cluster_sync();
+    else
+      __syncthreads();
+  };
+  for (int i = tid; i < kBins; i += kThreads) sm.hist[0][i] = 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
@@ -64,7 +95,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a, in
   for (int i = len + me; i < a.budget; i += all) keep[i] = -1;
   if (n <= a.budget) {               // every key stays
     for (int i = me; i < n; i += all) keep[i] = i;
-    cluster_sync();                  // (seq_lens may be keep_lens)
+    cluster_wide();                  // (seq_lens may be keep_lens)
     if (me == 0) a.keep_lens[b] = len;
     return;
   }
@@ -72,123 +103,163 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a, in
   const int lo = a.sinks, hi = n - a.recent;
   const int need = a.budget - a.sinks - a.recent;
   const float* weights = a.weights + (int64_t)b * a.weight_stride;
-  // every warp of the cluster has `part` keys (a multiple of 32), in order
-  const int part = ((n + ctas * kWarps - 1) / (ctas * kWarps) + 31) & ~31;
+  // every warp of the cluster has `part` keys (a multiple of 128), in order
+  const int part = ((n + ctas * kWarps - 1) / (ctas * kWarps) + 127) & ~127;
   const int slice = part * kWarps;
-  const int k0 = rank * slice;                          // first key of the slice
-  const int beg = max(lo, k0), end = min(hi, k0 + slice);   // its competing keys
-  for (int i = me; i < lo; i += all) keep[i] = i;
-  for (int i = me; i < a.recent; i += all) keep[a.budget - a.recent + i] = hi + i;
-
-  auto code_at = [&](int i) { return kHeld ? codes[i - k0] : code_of(weights[i]); };
-  if (kHeld) {
-    for (int i = beg + tid; i < end; i += kThreads) codes[i - k0] = code_of(weights[i]);
-  }
+  const int k0 = rank * slice;                              // first key of the slice
+  const int beg = max(lo - k0, 0), end = min(hi - k0, slice);   // its competing keys, counted from k0
+  const float* own = weights + k0;
+  const int held = (end + 3) & ~3;                          // codes looked at, four a thread and step
   __syncthreads();
+
+  if (need > 0) {
+    // the codes, and the first digit's histogram; keys that do not compete get
+    // no bin and are left out below by their index
+    for (int i0 = 4 * tid; i0 < held; i0 += 4 * kThreads) {
+      uint32_t c[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int i = i0 + k;
+        c[k] = i >= beg && i < end ? code_of(own[i]) : 0;
+      }
+      if (kHeld) *reinterpret_cast<uint4*>(codes + i0) = make_uint4(c[0], c[1], c[2], c[3]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (i0 + k >= beg && i0 + k < end) atomicAdd(&sm.hist[0][c[k] >> 21], 1);
+    }
+  }
+  auto codes_at = [&](int i0, uint32_t (&c)[4]) {
+    if (kHeld) {
+      const uint4 v = *reinterpret_cast<const uint4*>(codes + i0);
+      c[0] = v.x, c[1] = v.y, c[2] = v.z, c[3] = v.w;
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) c[k] = i0 + k >= beg && i0 + k < end ? code_of(own[i0 + k]) : 0;
+    }
+  };
 
   // the threshold: the need-th largest code, digit by digit
   uint32_t found = 0;
   int left = need;                   // places among the codes that share the digits found
-  for (int pass = 0; pass < 4 && need > 0; ++pass) {
-    const int shift = 24 - 8 * pass;
-    int* h = hist[pass & 1];
-    for (int i0 = beg; i0 < end; i0 += kThreads) {
-      const int i = i0 + tid;
-      const uint32_t c = i < end ? code_at(i) : 0;
-      const bool in = i < end && (pass == 0 || (c >> (shift + 8)) == found);
-      // lanes of equal digits add once
-      const unsigned live = __ballot_sync(0xffffffffu, in);
-      if (in) {
-        const int d = (c >> shift) & 255;
-        const unsigned same = __match_any_sync(live, d);
-        if (lane == __ffs(same) - 1) atomicAdd(&h[d], __popc(same));
+  for (int pass = 0; pass < 3 && need > 0; ++pass) {
+    int* h = sm.hist[pass & 1];
+    if (pass > 0) {
+      const int shift = pass == 1 ? 10 : 0, above = pass == 1 ? 21 : 10;
+      const uint32_t mask = pass == 1 ? 2047 : 1023;
+      for (int i0 = 4 * tid; i0 < held; i0 += 4 * kThreads) {
+        uint32_t c[4];
+        codes_at(i0, c);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if ((c[k] >> above) == found && i0 + k >= beg && i0 + k < end) atomicAdd(&h[c[k] >> shift & mask], 1);
       }
-      __syncwarp();
     }
-    cluster_sync();
-    if (tid < 256) {
-      int sum = 0;
-      for (int r = 0; r < ctas; ++r) sum += ld_cluster(&h[tid], r);
-      total[tid] = sum;
-      hist[(pass & 1) ^ 1][tid] = 0;   // (every CTA has read it: before the barrier above)
+    cluster_wide();
+    // thread t has bins kBins - 4 (t + 1) .. kBins - 4 t - 1: from the top down
+    const int top = kBins - 4 * (tid + 1);
+    int4 v = make_int4(0, 0, 0, 0);
+    for (int r = 0; r < ctas; ++r) {
+      const int4 u = ctas > 1 ? ld_cluster4(h + top, r) : *reinterpret_cast<const int4*>(h + top);
+      v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
     }
+    // (the other histogram was read by every CTA before the barrier above)
+    *reinterpret_cast<int4*>(sm.hist[(pass & 1) ^ 1] + top) = make_int4(0, 0, 0, 0);
+    const int sum = v.x + v.y + v.z + v.w;
+    const int incl = warp_incl_scan(sum);
+    if (lane == 31) sm.warp_sum[warp] = incl;
     __syncthreads();
-    if (warp == 0) {
-      // lane l has digits 255 - 8 l down to 248 - 8 l
-      int own[8], sum = 0;
+    int before = incl - sum;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) sum += own[k] = total[255 - 8 * lane - k];
-      int before = sum;
+    for (int w = 0; w < kWarps; ++w) before += w < warp ? sm.warp_sum[w] : 0;
+    if (before < left && before + sum >= left) {
+      const int bin[4] = {v.w, v.z, v.y, v.x};
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, before, o);
-        if (lane >= o) before += v;
-      }
-      before -= sum;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        if (before < left && before + own[k] >= left) {
-          s_digit = 255 - 8 * lane - k;
-          s_above = before;
+      for (int k = 0; k < 4; ++k) {
+        if (before < left && before + bin[k] >= left) {
+          sm.digit = top + 3 - k;
+          sm.above = before;
         }
-        before += own[k];
+        before += bin[k];
       }
     }
     __syncthreads();
-    found = (found << 8) | (uint32_t)s_digit;
-    left -= s_above;
+    found = pass == 2 ? (found << 10) | (uint32_t)sm.digit : (found << 11) | (uint32_t)sm.digit;
+    left -= sm.above;
   }
   // `left` of the codes equal to `found` stay, and all above it
   int above = 0, equal = 0;
-  const int w0 = max(beg, k0 + warp * part), w1 = min(end, k0 + (warp + 1) * part);
+  const int w0 = warp * part, w1 = min(end, w0 + part);     // the warp's keys, counted from k0
   if (need > 0) {
-    for (int i0 = w0; i0 < w1; i0 += 32) {
-      const int i = i0 + lane;
-      const uint32_t c = i < w1 ? code_at(i) : 0;
-      above += __popc(__ballot_sync(0xffffffffu, i < w1 && c > found));
-      equal += __popc(__ballot_sync(0xffffffffu, i < w1 && c == found));
+    for (int i0 = w0 + 4 * lane; i0 < w1; i0 += 128) {
+      uint32_t c[4];
+      codes_at(i0, c);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const bool in = i0 + k >= beg && i0 + k < end;
+        above += in && c[k] > found;
+        equal += in && c[k] == found;
+      }
     }
+    above = __reduce_add_sync(0xffffffffu, above);
+    equal = __reduce_add_sync(0xffffffffu, equal);
   }
   if (lane == 0) {
-    w_above[warp] = above;
-    w_equal[warp] = equal;
+    sm.w_above[warp] = above;
+    sm.w_equal[warp] = equal;
   }
   __syncthreads();
+  int sum_above = 0, sum_equal = 0;
+  above = equal = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const int u = sm.w_above[w], v = sm.w_equal[w];
+    above += w < warp ? u : 0;
+    equal += w < warp ? v : 0;
+    sum_above += u;
+    sum_equal += v;
+  }
   if (tid == 0) {
-    int x = 0, y = 0;
-    for (int w = 0; w < kWarps; ++w) {
-      const int u = w_above[w], v = w_equal[w];
-      w_above[w] = x;
-      w_equal[w] = y;
-      x += u;
-      y += v;
-    }
-    s_count[0] = x;
-    s_count[1] = y;
+    sm.count[0] = sum_above;
+    sm.count[1] = sum_equal;
   }
-  cluster_sync();
+  cluster_wide();
   if (me == 0) a.keep_lens[b] = len;
+  for (int i = me; i < lo; i += all) keep[i] = i;
+  for (int i = me; i < a.recent; i += all) keep[a.budget - a.recent + i] = hi + i;
   if (need > 0 && w0 < w1) {
-    above = w_above[warp];
-    equal = w_equal[warp];
     for (int r = 0; r < rank; ++r) {
-      above += ld_cluster(&s_count[0], r);
-      equal += ld_cluster(&s_count[1], r);
+      above += ld_cluster(&sm.count[0], r);
+      equal += ld_cluster(&sm.count[1], r);
     }
-    const unsigned below = (1u << lane) - 1;
-    for (int i0 = w0; i0 < w1; i0 += 32) {
-      const int i = i0 + lane;
-      const uint32_t c = i < w1 ? code_at(i) : 0;
-      const unsigned up = __ballot_sync(0xffffffffu, i < w1 && c > found);
-      const unsigned eq = __ballot_sync(0xffffffffu, i < w1 && c == found);
-      const int rank_eq = equal + __popc(eq & below);
-      const bool stays = (up >> lane & 1) || ((eq >> lane & 1) && rank_eq < left);
-      if (stays) keep[lo + above + __popc(up & below) + min(rank_eq, left)] = i;
-      above += __popc(up);
-      equal += __popc(eq);
+    for (int j0 = w0; j0 < w1; j0 += 128) {
+      const int i0 = j0 + 4 * lane;
+      uint32_t c[4];
+      int up = 0, eq = 0;            // bit k: key i0 + k is above, at the threshold
+      if (i0 < held) {
+        codes_at(i0, c);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const bool in = i0 + k >= beg && i0 + k < end;
+          up |= (in && c[k] > found) << k;
+          eq |= (in && c[k] == found) << k;
+        }
+      }
+      const int mine = __popc(up) | __popc(eq) << 16;
+      const int incl = warp_incl_scan(mine);
+      const int total = __shfl_sync(0xffffffffu, incl, 31);
+      int ahead = above + ((incl - mine) & 0xffff), same = equal + ((incl - mine) >> 16);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const bool is_up = up >> k & 1, is_eq = eq >> k & 1;
+        if (is_up || (is_eq && same < left)) keep[lo + ahead + min(same, left)] = k0 + i0 + k;
+        ahead += is_up;
+        same += is_eq;
+      }
+      above += total & 0xffff;
+      equal += total >> 16;
     }
   }
-  cluster_sync();                    // no CTA leaves while its counts are read
+  if (ctas > 1) cluster_sync();      // no CTA leaves while its counts are read
 }
 
 }  // namespace
@@ -196,8 +267,8 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a, in
 cudaError_t launch_select(const SelectArgs& a, int sm_count, cudaStream_t s) {
   // CTAs a request: a few keys a thread, all requests' on the card at once
   int ctas = 1;
-  while (ctas < 8 && a.batch * ctas * 2 <= 2 * sm_count && ctas * kThreads * 4 < a.weight_len) ctas *= 2;
-  const int64_t part = (((int64_t)a.weight_len + ctas * kWarps - 1) / (ctas * kWarps) + 31) / 32 * 32;
+  while (ctas < 8 && (int64_t)a.batch * ctas <= sm_count && ctas * kThreads * 16 < a.weight_len) ctas *= 2;
+  const int64_t part = (((int64_t)a.weight_len + ctas * kWarps - 1) / (ctas * kWarps) + 127) / 128 * 128;
   const bool held = part * kWarps <= kSliceMax;
   const size_t smem = held ? (size_t)part * kWarps * 4 : 0;
   static std::atomic<uint64_t> done{0};

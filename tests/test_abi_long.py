@@ -157,7 +157,7 @@ def test_cache_compact_refusals(lib):
     refused(-1, "cache_dtype", dtype=7)
     for name in ("nb", "page", "mp"):
         refused(-1, "positive", **{name: 0})
-    refused(-1, "2^40", nb=1 << 40)
+    refused(-1, "2^31", nb=1 << 25)
     refused(-2, "batch", B=(1 << 20) + 1)
     refused(-2, "2^30", mk=(1 << 30) + 1)
     for name in ("cache", "bt", "keep", "lens"):
