@@ -21,16 +21,17 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kSliceMax = 40960;     // codes of a slice held in shared memory
 
-// Codes order as weights do: -0 as +0, NaN below everything.
+// Codes order as weights do: -0 as +0, NaN below everything.  0 is no weight's
+// code: that of the keys which do not compete.
 __device__ __forceinline__ uint32_t code_of(float w) {
   const uint32_t u = __float_as_uint(w + 0.f);     // -0 + 0 = +0
-  if ((u & 0x7fffffffu) > 0x7f800000u) return 0;   // NaN
-  return u & 0x80000000u ? ~u : u | 0x80000000u;
+  const uint32_t c = u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
+  return w == w ? c : 1;                           // (-infinity's is 0x007fffff)
 }
 
 __device__ __forceinline__ int ld_cluster(const int* local, int rank) {
@@ -38,10 +39,10 @@ __device__ __forceinline__ int ld_cluster(const int* local, int rank) {
   asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(mapa(smem_u32(local), (uint32_t)rank)) : "memory");
   return v;
 }
-__device__ __forceinline__ int4 ld_cluster4(const int* local, int rank) {
-  int4 v;
-  asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+__device__ __forceinline__ int2 ld_cluster2(const int* local, int rank) {
+  int2 v;
+  asm volatile("ld.shared::cluster.v2.s32 {%0, %1}, [%2];"
+               : "=r"(v.x), "=r"(v.y)
                : "r"(mapa(smem_u32(local), (uint32_t)rank))
                : "memory");
   return v;
@@ -68,7 +69,7 @@ struct Shared {
 // kHeld: slices fit in shared memory; else codes are made from the weights in
 // every pass.
 template <bool kHeld>
-__global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a, int ctas) {
+__global__ void __launch_bounds__(kThreads, 1) select_kernel(const SelectArgs a, int ctas) {
   extern __shared__ __align__(16) uint32_t codes[];
   __shared__ Shared sm;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -113,20 +114,27 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a, in
   __syncthreads();
 
   if (need > 0) {
-    // the codes, and the first digit's histogram; keys that do not compete get
-    // no bin and are left out below by their index
-    for (int i0 = 4 * tid; i0 < held; i0 += 4 * kThreads) {
-      uint32_t c[4];
+    // the codes, and the first digit's histogram: kAtOnce loads of a thread in
+    // flight.  (Code 0 is counted too: it is below every place.)
+    constexpr int kAtOnce = 8;
+    for (int base = tid; base < held; base += kAtOnce * kThreads) {
+      float w[kAtOnce];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int i = i0 + k;
-        c[k] = i >= beg && i < end ? code_of(own[i]) : 0;
+      for (int k = 0; k < kAtOnce; ++k) {
+        const int i = base + k * kThreads;
+        w[k] = i >= beg && i < end ? own[i] : 0.f;
       }
-      if (kHeld) *reinterpret_cast<uint4*>(codes + i0) = make_uint4(c[0], c[1], c[2], c[3]);
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (i0 + k >= beg && i0 + k < end) atomicAdd(&sm.hist[0][c[k] >> 21], 1);
+      for (int k = 0; k < kAtOnce; ++k) {
+        const int i = base + k * kThreads;
+        if (i < held) {
+          const uint32_t c = i >= beg && i < end ? code_of(w[k]) : 0;
+          if (kHeld) codes[i] = c;
+          atomicAdd(&sm.hist[0][c >> 21], 1);
+        }
+      }
     }
+    __syncthreads();
   }
   auto codes_at = [&](int i0, uint32_t (&c)[4]) {
     if (kHeld) {
@@ -151,36 +159,29 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a, in
         codes_at(i0, c);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          if ((c[k] >> above) == found && i0 + k >= beg && i0 + k < end) atomicAdd(&h[c[k] >> shift & mask], 1);
+          if ((c[k] >> above) == found) atomicAdd(&h[c[k] >> shift & mask], 1);
       }
     }
     cluster_wide();
-    // thread t has bins kBins - 4 (t + 1) .. kBins - 4 t - 1: from the top down
-    const int top = kBins - 4 * (tid + 1);
-    int4 v = make_int4(0, 0, 0, 0);
+    // thread t has bins kBins - 2 t - 2 and kBins - 2 t - 1: from the top down
+    const int top = kBins - 2 * (tid + 1);
+    int2 v = make_int2(0, 0);
     for (int r = 0; r < ctas; ++r) {
-      const int4 u = ctas > 1 ? ld_cluster4(h + top, r) : *reinterpret_cast<const int4*>(h + top);
-      v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+      const int2 u = ctas > 1 ? ld_cluster2(h + top, r) : *reinterpret_cast<const int2*>(h + top);
+      v.x += u.x, v.y += u.y;
     }
     // (the other histogram was read by every CTA before the barrier above)
-    *reinterpret_cast<int4*>(sm.hist[(pass & 1) ^ 1] + top) = make_int4(0, 0, 0, 0);
-    const int sum = v.x + v.y + v.z + v.w;
+    *reinterpret_cast<int2*>(sm.hist[(pass & 1) ^ 1] + top) = make_int2(0, 0);
+    const int sum = v.x + v.y;
     const int incl = warp_incl_scan(sum);
     if (lane == 31) sm.warp_sum[warp] = incl;
     __syncthreads();
-    int before = incl - sum;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) before += w < warp ? sm.warp_sum[w] : 0;
+    const int sums = sm.warp_sum[lane];      // of warp `lane`
+    const int before = incl - sum + __reduce_add_sync(0xffffffffu, lane < warp ? sums : 0);
     if (before < left && before + sum >= left) {
-      const int bin[4] = {v.w, v.z, v.y, v.x};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (before < left && before + bin[k] >= left) {
-          sm.digit = top + 3 - k;
-          sm.above = before;
-        }
-        before += bin[k];
-      }
+      const bool upper = before + v.y >= left;
+      sm.digit = upper ? top + 1 : top;
+      sm.above = upper ? before : before + v.y;
     }
     __syncthreads();
     found = pass == 2 ? (found << 10) | (uint32_t)sm.digit : (found << 11) | (uint32_t)sm.digit;
@@ -188,16 +189,15 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a, in
   }
   // `left` of the codes equal to `found` stay, and all above it
   int above = 0, equal = 0;
-  const int w0 = warp * part, w1 = min(end, w0 + part);     // the warp's keys, counted from k0
+  const int w0 = warp * part, w1 = min(held, w0 + part);     // the warp's keys, counted from k0
   if (need > 0) {
     for (int i0 = w0 + 4 * lane; i0 < w1; i0 += 128) {
       uint32_t c[4];
       codes_at(i0, c);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const bool in = i0 + k >= beg && i0 + k < end;
-        above += in && c[k] > found;
-        equal += in && c[k] == found;
+        above += c[k] > found;
+        equal += c[k] == found;
       }
     }
     above = __reduce_add_sync(0xffffffffu, above);
@@ -208,16 +208,11 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a, in
     sm.w_equal[warp] = equal;
   }
   __syncthreads();
-  int sum_above = 0, sum_equal = 0;
-  above = equal = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    const int u = sm.w_above[w], v = sm.w_equal[w];
-    above += w < warp ? u : 0;
-    equal += w < warp ? v : 0;
-    sum_above += u;
-    sum_equal += v;
-  }
+  const int of_above = sm.w_above[lane], of_equal = sm.w_equal[lane];   // of warp `lane`
+  const int sum_above = __reduce_add_sync(0xffffffffu, of_above);
+  const int sum_equal = __reduce_add_sync(0xffffffffu, of_equal);
+  above = __reduce_add_sync(0xffffffffu, lane < warp ? of_above : 0);
+  equal = __reduce_add_sync(0xffffffffu, lane < warp ? of_equal : 0);
   if (tid == 0) {
     sm.count[0] = sum_above;
     sm.count[1] = sum_equal;
@@ -234,26 +229,23 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a, in
     for (int j0 = w0; j0 < w1; j0 += 128) {
       const int i0 = j0 + 4 * lane;
       uint32_t c[4];
-      int up = 0, eq = 0;            // bit k: key i0 + k is above, at the threshold
-      if (i0 < held) {
+      int mine = 0;                  // codes above, and at the threshold from bit 16 on
+      if (i0 < w1) {
         codes_at(i0, c);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const bool in = i0 + k >= beg && i0 + k < end;
-          up |= (in && c[k] > found) << k;
-          eq |= (in && c[k] == found) << k;
-        }
+        for (int k = 0; k < 4; ++k) mine += (c[k] > found) + ((c[k] == found) << 16);
       }
-      const int mine = __popc(up) | __popc(eq) << 16;
       const int incl = warp_incl_scan(mine);
       const int total = __shfl_sync(0xffffffffu, incl, 31);
-      int ahead = above + ((incl - mine) & 0xffff), same = equal + ((incl - mine) >> 16);
+      if (mine) {
+        int ahead = above + ((incl - mine) & 0xffff), same = equal + ((incl - mine) >> 16);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const bool is_up = up >> k & 1, is_eq = eq >> k & 1;
-        if (is_up || (is_eq && same < left)) keep[lo + ahead + min(same, left)] = k0 + i0 + k;
-        ahead += is_up;
-        same += is_eq;
+        for (int k = 0; k < 4; ++k) {
+          const bool is_up = c[k] > found, is_eq = c[k] == found;
+          if (is_up || (is_eq && same < left)) keep[lo + ahead + min(same, left)] = k0 + i0 + k;
+          ahead += is_up;
+          same += is_eq;
+        }
       }
       above += total & 0xffff;
       equal += total >> 16;
@@ -267,7 +259,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a, in
 cudaError_t launch_select(const SelectArgs& a, int sm_count, cudaStream_t s) {
   // CTAs a request: a few keys a thread, all requests' on the card at once
   int ctas = 1;
-  while (ctas < 8 && (int64_t)a.batch * ctas <= sm_count && ctas * kThreads * 16 < a.weight_len) ctas *= 2;
+  while (ctas < 8 && (int64_t)a.batch * ctas * 2 <= sm_count && ctas * kThreads * 8 < a.weight_len) ctas *= 2;
   const int64_t part = (((int64_t)a.weight_len + ctas * kWarps - 1) / (ctas * kWarps) + 127) / 128 * 128;
   const bool held = part * kWarps <= kSliceMax;
   const size_t smem = held ? (size_t)part * kWarps * 4 : 0;
