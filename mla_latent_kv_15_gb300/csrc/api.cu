@@ -907,11 +907,14 @@ int mla_key_weights(const void* q_abs, const void* q_pe, const void* cache, int6
   if (any_overlap(outputs, 2, inputs, 7))
     return fail(MLA_ERR_INVALID_ARG, "weights and status must not overlap each other or the inputs");
   const int sms = sm_count();
-  if (sms < 1) return fail(MLA_ERR_CUDA, "cannot query the current device");
-  // a request's rows come in boxes of a token's heads (rounded up to 16 rows,
-  // at most 128), as many to a product as its 128 columns hold
-  const int q_box = num_heads >= 128 ? 128 : (num_heads + 15) / 16 * 16;
-  const int row_tile = 128 / q_box * q_box;
+  if (sms < 2) return fail(MLA_ERR_CUDA, "cannot query the current device");
+  // Columns of a product: a request's query rows (of an average one, where
+  // query_start_loc says) in as few tiles of at most 128 as hold them, a
+  // multiple of 32; each CTA of a pair loads half of them
+  const int64_t per_request = (total_q + (int64_t)batch - 1) / batch * num_heads;
+  const int64_t row_tiles = per_request > 128 ? (per_request + 127) / 128 : 1;
+  int row_tile = (int)((per_request + row_tiles - 1) / row_tiles + 31) / 32 * 32;
+  if (row_tile < 32) row_tile = 32;
   CUtensorMap tm_q, tm_qr, tm_kv;
   bool enc = mla::encode_tmap_2d(&tm_kv, cache, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                                  mla::kDqk, (uint64_t)num_blocks * page_size, mla::kDqk * (fp8 ? 1 : 2), 64,
@@ -920,10 +923,10 @@ int mla_key_weights(const void* q_abs, const void* q_pe, const void* cache, int6
   tm_q = tm_qr = tm_kv;   // without a query row none is loaded
   if (total_q > 0)
     enc = enc &&
-          mla::encode_tmap_2d(&tm_q, q_abs, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, mla::kLkv, rows, mla::kLkv * 2, 64, q_box,
-                              CU_TENSOR_MAP_SWIZZLE_128B) &&
+          mla::encode_tmap_2d(&tm_q, q_abs, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, mla::kLkv, rows, mla::kLkv * 2, 64,
+                              row_tile / 2, CU_TENSOR_MAP_SWIZZLE_128B) &&
           mla::encode_tmap_2d(&tm_qr, q_pe, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, mla::kRope, rows, mla::kRope * 2, 64,
-                              q_box, CU_TENSOR_MAP_SWIZZLE_128B);
+                              row_tile / 2, CU_TENSOR_MAP_SWIZZLE_128B);
   if (!enc) return fail(MLA_ERR_CUDA, "cuTensorMapEncodeTiled rejected a tensor layout");
   mla::KeyWeightArgs a{};
   a.block_table = block_table;
@@ -941,7 +944,6 @@ int mla_key_weights(const void* q_abs, const void* q_pe, const void* cache, int6
   a.num_blocks = num_blocks;
   a.scale_log2 = factor;
   a.decay = decay;
-  a.q_box = q_box;
   a.row_tile = row_tile;
   a.status = status;
   a.wait_limit_ns = g_wait_limit_ns;

@@ -3,17 +3,22 @@
 //   w[j] = decay * w[j] + sum over rows (t, h) that see key j of
 //          exp(scale * q[t, h] . k_j - lse[t, h])
 //
-// The product is taken with the keys as its rows, S = K . Q^T: 128 keys by up
-// to 128 query rows, so that a thread of the epilogue holds one key's scores
-// and sums its exponentials along its own columns, with no exchange between
-// lanes and no atomics: a key's rows are all summed by one CTA, in one order.
+// The product is taken with the keys as its rows, S = K . Q^T, so that a thread
+// of the epilogue holds one key's scores and sums its exponentials along its
+// own columns, with no exchange between lanes and no atomics: a key's rows are
+// all summed by one CTA, in one order.
 //
-// A CTA takes a contiguous share of all requests' 128-key tiles, and for each
-// the request's row tiles in turn; both operands stream through a ring in
-// 64-column chunks (one 128-byte swizzled row a key or query row).  An e4m3
-// cache lands as codes beside the chunk and is expanded to bf16 by four warps.
-// Two accumulators in tensor memory: a tile's exponentials run under the next
-// one's products.
+// CTA pairs (cta_group::2) take contiguous shares of all requests' 256-key
+// tiles, 128 keys a CTA.  A tile's nine 64-column chunks stay in shared memory
+// while the request's row tiles of up to 128 query rows (half of them in each
+// CTA) stream past them; with one row tile a request the nine slots are a ring
+// like any other.  So the cache is read once whatever the number of rows, and a
+// pair's query rows once a 256-key tile.  Four accumulators in tensor memory: a
+// tile's exponentials run under the next products.
+//
+// An e4m3 cache lands as codes in a ring of its own and is expanded to bf16 by
+// four warps, each a whole chunk, so that the wait of one for its writes to be
+// seen by the pair's leader runs beside the others' work.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -26,35 +31,51 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kKeys = 128;                     // keys of a tile (MMA M)
+constexpr int kKeys = 128;                     // keys of a CTA's half of a tile (MMA rows)
+constexpr int kPairKeys = 2 * kKeys;
 constexpr int kChunks = kDqk / 64;             // 9
-constexpr uint32_t kKBytes = kKeys * 128;      // a chunk of a key tile, bf16
+constexpr uint32_t kKBytes = kKeys * 128;      // a chunk of a CTA's keys, bf16: one 128-byte swizzled row a key
 constexpr uint32_t kRawBytes = kKeys * 64;     // the same as e4m3 codes
-constexpr uint32_t kQBytes = 128 * 128;        // a chunk of up to 128 query rows
-constexpr int kThreads = 512;                  // warp 0 loads, 1 issues, 4-11 epilogue, 12-15 expand e4m3
-constexpr int kWarpEpilogue = 4, kWarpExpand = 12;
+constexpr int kRowTile = 128;                  // query rows of a product at most (its columns)
+constexpr uint32_t kQBytes = kRowTile / 2 * 128;   // a chunk of a CTA's half of them
+constexpr int kAcc = 4;                        // accumulators of kRowTile columns
+constexpr int kWarpK = 0, kWarpQ = 1, kWarpMma = 2, kWarpEpilogue = 4, kWarpExpand = 12;
+constexpr int kExpandWarps = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <bool kFp8>
 struct Shape {
-  static constexpr uint32_t kStage = kKBytes + kQBytes + (kFp8 ? kRawBytes : 0);
-  static constexpr int kStages = kFp8 ? 5 : 6;
-  static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + 4096;
+  static constexpr int kThreads = kFp8 ? 512 : 384;
+  static constexpr int kKSlots = kFp8 ? 9 : 10;    // at least a tile's chunks
+  static constexpr int kQStages = kFp8 ? 4 : 7;
+  static constexpr int kRawStages = kFp8 ? 5 : 0;
+  static constexpr uint32_t kQAt = kKSlots * kKBytes;
+  static constexpr uint32_t kRawAt = kQAt + kQStages * kQBytes;
+  static constexpr uint32_t kBarsAt = kRawAt + kRawStages * kRawBytes;
 };
 
+// Barriers marked (lead) are used in the leading CTA only, by both CTAs.
 struct Bars {
-  uint64_t full[6], empty[6], raw_full[6];
-  uint64_t d_full[2], d_empty[2];
+  uint64_t k_full[10], q_full[7];  // (lead) both CTAs' halves are there
+  uint64_t k_empty[10], q_empty[7];
+  uint64_t raw_full[5], raw_empty[5];
+  uint64_t d_full[kAcc];
+  uint64_t d_empty[kAcc];          // (lead) the epilogue warps of both CTAs
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
-  int tile0, tiles, b0;           // this CTA's share: first tile of request b0, tiles in all
-  int leads;                      // the share begins with the first tile of all
-  long long sums[kThreads / 32];
-  float lse2[2][128];             // lse * log2 e of the row tile's rows, two tiles in turn
-  float half[2][kKeys];           // sums of the second column half
+  int tile0, tiles, b0;            // the pair's share: first tile of request b0, tiles in all
+  int leads;                       // the share begins with the first tile of all
+  long long sums[16];
+  float lse2[2][kRowTile];         // lse * log2 e of the row tile's rows, two tiles in turn
+  float half[2][kKeys];            // sums of the second half of the columns
 };
-static_assert(sizeof(Bars) <= 4096, "fits behind the stages");
+
+template <bool kFp8>
+constexpr size_t smem_bytes() {
+  return 1024 + Shape<kFp8>::kBarsAt + sizeof(Bars);
+}
+static_assert(smem_bytes<false>() <= 232448 && smem_bytes<true>() <= 232448, "shared memory per CTA");
 
 struct Ctx {
   Bars* bars;
@@ -111,27 +132,35 @@ struct Request {
 };
 
 template <bool kFp8>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kFp8>::kThreads, 1)
     key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_qr,
                        const __grid_constant__ CUtensorMap tm_kv, const KeyWeightArgs a) {
   using S = Shape<kFp8>;
-  constexpr int kStages = S::kStages;
+  constexpr int kThreads = S::kThreads;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  Bars* bars = reinterpret_cast<Bars*>(smem + kStages * S::kStage);
+  Bars* bars = reinterpret_cast<Bars*>(smem + S::kBarsAt);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_ctarank();
   const Ctx ctx{bars, a.status, a.wait_limit_ns};
   volatile int* abort_flag = &bars->abort;
 
   if (tid == 0) {
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(smem_u32(&bars->full[i]), kFp8 ? 5 : 1);   // the loads, and the four expanding warps
-      mbar_init(smem_u32(&bars->empty[i]), 1);
-      mbar_init(smem_u32(&bars->raw_full[i]), 1);
+    for (int i = 0; i < S::kKSlots; ++i) {
+      mbar_init(smem_u32(&bars->k_full[i]), 2);      // each CTA's load, or expanding warp
+      mbar_init(smem_u32(&bars->k_empty[i]), 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < S::kQStages; ++i) {
+      mbar_init(smem_u32(&bars->q_full[i]), 2);
+      mbar_init(smem_u32(&bars->q_empty[i]), 1);
+    }
+    for (int i = 0; i < S::kRawStages; ++i) {
+      mbar_init(smem_u32(&bars->raw_full[i]), 1);
+      mbar_init(smem_u32(&bars->raw_empty[i]), 1);
+    }
+    for (int i = 0; i < kAcc; ++i) {
       mbar_init(smem_u32(&bars->d_full[i]), 1);
-      mbar_init(smem_u32(&bars->d_empty[i]), 8);
+      mbar_init(smem_u32(&bars->d_empty[i]), 16);
     }
     mbar_init(smem_u32(&bars->drain), 1);
     bars->abort = 0;
@@ -140,9 +169,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tm_qr);
     tma_prefetch_desc(&tm_kv);
   }
-  if (warp == 1) {
-    tmem_alloc(smem_u32(&bars->tmem_base), 256);
-    tmem_relinquish();
+  if (warp == kWarpMma) {
+    tmem_alloc_pair(smem_u32(&bars->tmem_base), kAcc * kRowTile);
+    tmem_relinquish_pair();
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -152,8 +181,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int n = a.seq_lens[b];
     return n < 0 ? 0 : (n > cap ? cap : n);
   };
-  // this CTA's share of all tiles: a sum over the batch, then the request
-  // that holds the share's first tile
+  auto tiles_of = [&](int b) { return b < a.batch ? (keys_of(b) + kPairKeys - 1) / kPairKeys : 0; };
+  // the pair's share of all tiles: a sum over the batch, then the request that
+  // holds the share's first tile
   {
     auto block_sum = [&](long long v, long long& before) {   // the block's sum, and that of the threads before this one
       long long incl = v;
@@ -174,18 +204,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return all;
     };
-    long long total = 0, before;
+    const int pair = (int)cluster_id_x(), pairs = gridDim.x / 2;
+    long long total = 0, before = 0;
+    long long before0 = 0;                       // of the first kThreads requests, kept for the search
     for (int base = 0; base < a.batch; base += kThreads) {
       const int b = base + tid;
-      if (b < a.batch && blockIdx.x == 0 && a.seq_lens[b] > cap) raise(ctx, 2);   // MLA_DEVERR_BAD_SEQ_LEN
-      total += block_sum(b < a.batch ? (keys_of(b) + kKeys - 1) / kKeys : 0, before);
+      if (blockIdx.x == 0 && b < a.batch && a.seq_lens[b] > cap) raise(ctx, 2);   // MLA_DEVERR_BAD_SEQ_LEN
+      total += block_sum(tiles_of(b), before);
+      if (base == 0) before0 = before;
     }
-    const long long lo = total * blockIdx.x / gridDim.x, hi = total * (blockIdx.x + 1) / gridDim.x;
+    const long long lo = total * pair / pairs, hi = total * (pair + 1) / pairs;
     long long at = 0;
     for (int base = 0; base < a.batch && at <= lo; base += kThreads) {
       const int b = base + tid;
-      const int tiles = b < a.batch ? (keys_of(b) + kKeys - 1) / kKeys : 0;
-      const long long all = block_sum(tiles, before);
+      const int tiles = tiles_of(b);
+      long long all = total;
+      if (a.batch <= kThreads)
+        before = before0;
+      else
+        all = block_sum(tiles, before);
       if (at + before <= lo && lo < at + before + tiles) {
         bars->b0 = b;
         bars->tile0 = (int)(lo - at - before);
@@ -198,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   tc_fence_before();
-  __syncthreads();
+  cluster_sync();   // both CTAs' barriers are initialised before either uses the other's
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
   const int tiles = bars->tiles;
@@ -217,13 +254,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     r.row_tiles = (r.rows + width - 1) / width;
     return r;
   };
-  // calls body(request number, request, key tile, whether the request is new) for every tile of the share
+  // calls body(request number, request, key tile) for every tile of the share
   auto for_tiles = [&](auto&& body) {
     int b = bars->b0, t = bars->tile0;
     bool fresh = true;
     Request r{};
     for (int i = 0; i < tiles; ++i, ++t) {
-      while (fresh || t * kKeys >= r.n) {
+      while (fresh || t * kPairKeys >= r.n) {
         if (!fresh) {
           ++b;
           t = 0;
@@ -235,17 +272,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   };
 
-  if (warp == 0) {
-    // ------------------------------------------------------------------ loads
+  if (warp == kWarpK) {
+    // ------------------------------------------------------------------- keys
     uint32_t n = 0;
     const int sub_rows = a.page_size < kKeys ? a.page_size : kKeys;
     const int nsub = kKeys / sub_rows;
     const uint64_t pol = l2_policy_evict_first();
-    bool skip = a.debug_skip_tile && bars->leads;
+    bool skip = a.debug_skip_tile && bars->leads && rank == 0;
     for_tiles([&](int b, const Request& r, int t) {
+      if (r.row_tiles == 0) return;
       // lane l < nsub: the cache row of sub-page l
       int y = (int)(a.num_blocks * a.page_size);   // past the cache: reads zeros
-      const int key = t * kKeys + lane * sub_rows;
+      const int key = t * kPairKeys + kKeys * (int)rank + lane * sub_rows;
       if (lane < nsub && key < r.n) {
         const int blk = a.block_table[(int64_t)b * a.max_pages + key / a.page_size];
         if (blk >= 0 && blk < a.num_blocks)
@@ -253,94 +291,126 @@ __global__ void __launch_bounds__(kThreads, 1)
         else
           raise(ctx, 4);   // MLA_DEVERR_BAD_BLOCK
       }
-      for (int rt = 0; rt < r.row_tiles; ++rt) {
-        const int row0 = r.q0 * a.num_heads + rt * width;
-        const int boxes = (min(width, r.rows - rt * width) + a.q_box - 1) / a.q_box;
-        for (int c = 0; c < kChunks; ++c, ++n) {
-          if (*abort_flag) return;
-          const uint32_t slot = n % kStages;
-          wait(ctx, &bars->empty[slot], ((n / kStages) & 1) ^ 1);
+      for (int c = 0; c < kChunks; ++c, ++n) {
+        if (*abort_flag) return;
+        if constexpr (kFp8) {
+          const uint32_t slot = n % S::kRawStages;
+          wait(ctx, &bars->raw_empty[slot], ((n / S::kRawStages) & 1) ^ 1);
           __syncwarp();
           if (skip) {      // test aid: the first chunk never comes
             skip = false;
             continue;
           }
-          const uint32_t st = smem_u32(smem + slot * S::kStage), full = smem_u32(&bars->full[slot]);
-          const uint32_t raw = smem_u32(&bars->raw_full[slot]);
-          if (lane == 0) {
-            mbar_expect_tx(full, boxes * a.q_box * 128u + (kFp8 ? 0u : kKBytes));
-            if (kFp8) mbar_expect_tx(raw, kRawBytes);
-            for (int i = 0; i < boxes; ++i)
-              tma_load_2d(st + kKBytes + i * a.q_box * 128u, c < 8 ? &tm_q : &tm_qr, c < 8 ? 64 * c : 0,
-                          row0 + i * a.q_box, full);
-          }
+          const uint32_t full = smem_u32(&bars->raw_full[slot]);
+          if (lane == 0) mbar_expect_tx(full, kRawBytes);
           __syncwarp();
-          if (lane < nsub) {
-            if (kFp8)
-              tma_load_2d_hint(st + kKBytes + kQBytes + lane * sub_rows * 64u, &tm_kv, 64 * c, y, raw, pol);
-            else
-              tma_load_2d_hint(st + lane * sub_rows * 128u, &tm_kv, 64 * c, y, full, pol);
-          }
+          if (lane < nsub)
+            tma_load_2d_hint(smem_u32(smem + S::kRawAt + slot * kRawBytes) + lane * sub_rows * 64u, &tm_kv, 64 * c, y,
+                             full, pol);
+        } else {
+          const uint32_t slot = n % S::kKSlots;
+          wait(ctx, &bars->k_empty[slot], ((n / S::kKSlots) & 1) ^ 1);
           __syncwarp();
+          if (skip) {
+            skip = false;
+            continue;
+          }
+          const uint32_t full = mapa(smem_u32(&bars->k_full[slot]), 0);
+          if (lane == 0) mbar_expect_tx_remote(full, kKBytes);
+          __syncwarp();
+          if (lane < nsub)
+            tma_load_2d_pair_hint(smem_u32(smem + slot * kKBytes) + lane * sub_rows * 128u, &tm_kv, 64 * c, y, full, pol);
         }
+        __syncwarp();
       }
     });
-    // every load has landed before the CTA ends
-    for (uint32_t k = n > kStages ? n - kStages : 0; k < n && !*abort_flag; ++k) {
-      if (kFp8) wait(ctx, &bars->raw_full[k % kStages], (k / kStages) & 1);
-      wait(ctx, &bars->full[k % kStages], (k / kStages) & 1);
+    // every load has landed before the CTA ends (the leader's barriers count both CTAs')
+    if constexpr (kFp8) {
+      for (uint32_t k = n > S::kRawStages ? n - S::kRawStages : 0; k < n && !*abort_flag; ++k)
+        wait(ctx, &bars->raw_full[k % S::kRawStages], (k / S::kRawStages) & 1);
+    } else if (rank == 0) {
+      for (uint32_t k = n > S::kKSlots ? n - S::kKSlots : 0; k < n && !*abort_flag; ++k)
+        wait(ctx, &bars->k_full[k % S::kKSlots], (k / S::kKSlots) & 1);
     }
-  } else if (warp == 1) {
-    // --------------------------------------------------------------- products
-    const uint32_t hi = desc_hi(1024, kSwizzle128B);
-    const uint32_t k_lo = desc_lo(smem_u32(smem), 16), q_lo = desc_lo(smem_u32(smem) + kKBytes, 16);
-    uint32_t n = 0, m = 0;
+  } else if (warp == kWarpQ) {
+    // ------------------------------------------------------------- query rows
+    uint32_t n = 0;
+    const uint32_t bytes = width / 2 * 128u;
     for_tiles([&](int, const Request& r, int) {
-      for (int rt = 0; rt < r.row_tiles; ++rt, ++m) {
-        if (*abort_flag) return;
-        const uint32_t acc = m & 1;
-        const uint32_t cols = (uint32_t)(min(width, r.rows - rt * width) + 15) & ~15u;
-        const uint32_t idesc = idesc_bf16_f32(128, cols, 0, 0);
-        wait(ctx, &bars->d_empty[acc], ((m >> 1) & 1) ^ 1);
+      for (int rt = 0; rt < r.row_tiles; ++rt) {
+        const int row0 = r.q0 * a.num_heads + rt * width + width / 2 * (int)rank;
         for (int c = 0; c < kChunks; ++c, ++n) {
-          const uint32_t slot = n % kStages;
-          wait(ctx, &bars->full[slot], (n / kStages) & 1);
+          if (*abort_flag) return;
+          const uint32_t stage = n % S::kQStages;
+          wait(ctx, &bars->q_empty[stage], ((n / S::kQStages) & 1) ^ 1);
           __syncwarp();
-          tc_fence_after();
           if (elect_one()) {
-            const uint32_t off = slot * (S::kStage >> 4);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_ss(tmem + acc * 128, ((uint64_t)hi << 32) | (k_lo + off + 2 * k),
-                     ((uint64_t)hi << 32) | (q_lo + off + 2 * k), idesc, (c | k) ? 1u : 0u);
-            mma_commit(smem_u32(&bars->empty[slot]));
-            if (c == kChunks - 1) mma_commit(smem_u32(&bars->d_full[acc]));
+            const uint32_t full = mapa(smem_u32(&bars->q_full[stage]), 0);
+            mbar_expect_tx_remote(full, bytes);
+            tma_load_2d_pair(smem_u32(smem + S::kQAt + stage * kQBytes), c < 8 ? &tm_q : &tm_qr, c < 8 ? 64 * c : 0,
+                             row0, full);
           }
           __syncwarp();
         }
       }
     });
-    if (elect_one()) mma_commit(smem_u32(&bars->drain));
-    __syncwarp();
-    wait(ctx, &bars->drain, 0);
+    if (rank == 0)
+      for (uint32_t k = n > S::kQStages ? n - S::kQStages : 0; k < n && !*abort_flag; ++k)
+        wait(ctx, &bars->q_full[k % S::kQStages], (k / S::kQStages) & 1);
+  } else if (warp == kWarpMma) {
+    // --------------------------------------------------------------- products
+    if (rank == 0) {
+      const uint32_t idesc = idesc_bf16_f32(256, width, 0, 0);
+      constexpr uint32_t hi = desc_hi(1024, kSwizzle128B);
+      const uint32_t k_lo = desc_lo(smem_u32(smem), 16), q_lo = desc_lo(smem_u32(smem + S::kQAt), 16);
+      uint32_t kn = 0, qn = 0, m = 0;
+      for_tiles([&](int, const Request& r, int) {
+        for (int rt = 0; rt < r.row_tiles; ++rt, ++m) {
+          if (*abort_flag) return;
+          const uint32_t acc = m % kAcc;
+          wait(ctx, &bars->d_empty[acc], ((m / kAcc) & 1) ^ 1);
+          for (int c = 0; c < kChunks; ++c, ++qn) {
+            const uint32_t kc = kn + c, slot = kc % S::kKSlots, stage = qn % S::kQStages;
+            if (rt == 0) wait(ctx, &bars->k_full[slot], (kc / S::kKSlots) & 1);
+            wait(ctx, &bars->q_full[stage], (qn / S::kQStages) & 1);
+            __syncwarp();
+            tc_fence_after();
+            if (elect_one()) {
+              const uint32_t ka = k_lo + slot * (kKBytes >> 4), qa = q_lo + stage * (kQBytes >> 4);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma_pair_ss(tmem + acc * kRowTile, ka + 2 * k, hi, qa + 2 * k, hi, idesc, (c | k) ? 1u : 0u);
+              mma_commit_pair(smem_u32(&bars->q_empty[stage]));
+              if (rt == r.row_tiles - 1) mma_commit_pair(smem_u32(&bars->k_empty[slot]));
+              if (c == kChunks - 1) mma_commit_pair(smem_u32(&bars->d_full[acc]));
+            }
+            __syncwarp();
+          }
+        }
+        if (r.row_tiles > 0) kn += kChunks;
+      });
+      if (elect_one()) mma_commit_pair(smem_u32(&bars->drain));
+      __syncwarp();
+      wait(ctx, &bars->drain, 0);
+    }
   } else if (warp >= kWarpEpilogue && warp < kWarpExpand) {
     // --------------------------------------------------------------- epilogue
     const int e = tid - 32 * kWarpEpilogue;      // 0..255
-    const int q4 = warp & 3, hh = e >> 7;        // tensor-memory lanes 32 q4.., columns of half hh
+    const int q4 = warp & 3, hh = e >> 7;        // tensor-memory lanes 32 q4.., 32-column groups of parity hh
     const int key = q4 * 32 + lane;
     const uint32_t from = tmem + ((uint32_t)(q4 * 32) << 16);
     uint32_t m = 0, tile_no = 0;
     int at_b = -1;
     uint32_t set = 0;                            // the buffer of lse2 in use
     for_tiles([&](int b, const Request& r, int t) {
-      const int j = t * kKeys + key;
+      const int j = t * kPairKeys + kKeys * (int)rank + key;
       // the first of the request's rows that sees key j (the rest follow)
       const int late = j - (r.n - r.sq);
       const int first_row = late > 0 ? late * a.num_heads : 0;
       const int first_max = __reduce_max_sync(0xffffffffu, first_row);
       float sum[4] = {0.f, 0.f, 0.f, 0.f};
       for (int rt = 0; rt < r.row_tiles; ++rt, ++m) {
-        const uint32_t acc = m & 1;
+        const uint32_t acc = m % kAcc;
         const int base = rt * width, cols = min(width, r.rows - base);
         if (r.row_tiles > 1 || at_b != b) {
           set ^= 1;
@@ -352,13 +422,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           at_b = b;
         }
         const float* lse2 = bars->lse2[set];
-        wait(ctx, &bars->d_full[acc], (m >> 1) & 1);
+        wait(ctx, &bars->d_full[acc], (m / kAcc) & 1);
         __syncwarp();
         tc_fence_after();
-        // 32 columns at a time, the halves in turn
         for (int c0 = 32 * hh; c0 < cols; c0 += 64) {
           uint32_t s[32];
-          tmem_ld32(from + acc * 128 + c0, s);
+          tmem_ld32(from + acc * kRowTile + c0, s);
           tmem_wait_ld();
           if (c0 + 32 <= cols && first_max <= base + c0) {
 #pragma unroll
@@ -380,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bars->d_empty[acc]));
+        if (lane == 0) mbar_arrive_remote(mapa(smem_u32(&bars->d_empty[acc]), 0));
       }
       const float mine = (sum[0] + sum[1]) + (sum[2] + sum[3]);
       float* half = bars->half[tile_no++ & 1];
@@ -394,29 +463,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     });
   } else if (kFp8 && warp >= kWarpExpand) {
     // -------------------------------------------------------- e4m3 expansion
-    const int te = tid - 32 * kWarpExpand;       // 0..127
+    const uint32_t turn = (uint32_t)(warp - kWarpExpand);
     uint32_t n = 0;
     for_tiles([&](int, const Request& r, int) {
-      for (int i = 0; i < r.row_tiles * kChunks; ++i, ++n) {
-        const uint32_t slot = n % kStages;
-        wait(ctx, &bars->raw_full[slot], (n / kStages) & 1);
+      if (r.row_tiles == 0) return;
+      for (int c = 0; c < kChunks; ++c, ++n) {
+        if (n % kExpandWarps != turn) continue;
+        const uint32_t from = n % S::kRawStages, slot = n % S::kKSlots;
+        wait(ctx, &bars->raw_full[from], (n / S::kRawStages) & 1);
+        wait(ctx, &bars->k_empty[slot], ((n / S::kKSlots) & 1) ^ 1);
         __syncwarp();
-        const uint8_t* st = smem + slot * S::kStage;
-        uint4 v[4];
+        const uint4* src = reinterpret_cast<const uint4*>(smem + S::kRawAt + from * kRawBytes);
+        uint8_t* dst = smem + slot * kKBytes;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = reinterpret_cast<const uint4*>(st + kKBytes + kQBytes)[te + 128 * k];
+        for (int g = 0; g < 4; ++g) {
+          uint4 v[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int at = te + 128 * k, q = at & 3, row = at >> 2;
-          uint32_t o[8];
-          widen16(v[k], o);
-          uint4* dst = reinterpret_cast<uint4*>(smem + slot * S::kStage + row * 128);
-          dst[(2 * q) ^ (row & 7)] = make_uint4(o[0], o[1], o[2], o[3]);
-          dst[(2 * q + 1) ^ (row & 7)] = make_uint4(o[4], o[5], o[6], o[7]);
+          for (int k = 0; k < 4; ++k) v[k] = src[lane + 32 * (4 * g + k)];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int at = lane + 32 * (4 * g + k), q = at & 3, row = at >> 2;
+            uint32_t o[8];
+            widen16(v[k], o);
+            uint4* to = reinterpret_cast<uint4*>(dst + row * 128);
+            to[(2 * q) ^ (row & 7)] = make_uint4(o[0], o[1], o[2], o[3]);
+            to[(2 * q + 1) ^ (row & 7)] = make_uint4(o[4], o[5], o[6], o[7]);
+          }
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bars->full[slot]));
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&bars->raw_empty[from]));
+          mbar_arrive_release_cluster(mapa(smem_u32(&bars->k_full[slot]), 0));
+        }
       }
     });
   }
@@ -427,11 +506,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (globaltimer() - t0 < 1000000ull) {
     }
   }
+  __syncwarp();
   tc_fence_before();
-  __syncthreads();
-  if (warp == 1) {
+  cluster_sync();   // the pair ends together: each reads and signals the other's shared memory
+  if (warp == kWarpMma) {
+    // the last signal to the peer's own barriers is on its way by now
+    if (rank == 1) wait(ctx, &bars->drain, 0);
+    __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem, 256);
+    tmem_dealloc_pair(tmem, kAcc * kRowTile);
   }
 }
 
@@ -439,16 +522,17 @@ template <bool kFp8>
 cudaError_t launch(const CUtensorMap& tm_q, const CUtensorMap& tm_qr, const CUtensorMap& tm_kv, const KeyWeightArgs& a,
                    int sm_count, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(key_weights_kernel<kFp8>, Shape<kFp8>::kSmem, done);
+  cudaError_t e = allow_smem(key_weights_kernel<kFp8>, smem_bytes<kFp8>(), done);
   if (e != cudaSuccess) return e;
-  // no more CTAs than tiles there can be
+  // no more pairs than tiles there can be
   const int64_t reach = (int64_t)a.max_pages * a.page_size < a.weight_len ? (int64_t)a.max_pages * a.page_size
                                                                           : (int64_t)a.weight_len;
-  const int64_t most = a.batch * ((reach + kKeys - 1) / kKeys);
+  const int64_t most = a.batch * ((reach + kPairKeys - 1) / kPairKeys);
+  const int pairs = sm_count / 2;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(most < sm_count ? (most > 0 ? most : 1) : sm_count));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Shape<kFp8>::kSmem;
+  cfg.gridDim = dim3(2u * (unsigned)(most < pairs ? (most > 0 ? most : 1) : pairs));
+  cfg.blockDim = dim3(Shape<kFp8>::kThreads);
+  cfg.dynamicSmemBytes = smem_bytes<kFp8>();
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
