@@ -918,7 +918,7 @@ int mla_key_weights(const void* q_abs, const void* q_pe, const void* cache, int6
   CUtensorMap tm_q, tm_qr, tm_kv;
   bool enc = mla::encode_tmap_2d(&tm_kv, cache, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                                  mla::kDqk, (uint64_t)num_blocks * page_size, mla::kDqk * (fp8 ? 1 : 2), 64,
-                                 page_size < 128 ? page_size : 128,
+                                 page_size < (fp8 ? 64 : 128) ? page_size : (fp8 ? 64 : 128),
                                  fp8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B);
   tm_q = tm_qr = tm_kv;   // without a query row none is loaded
   if (total_q > 0)

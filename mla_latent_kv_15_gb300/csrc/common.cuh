@@ -334,7 +334,8 @@ cudaError_t launch_decode_shared(const CUtensorMap& tm_q, const CUtensorMap& tm_
                                  int variant, const DecodeArgs& a, int num_clusters, cudaStream_t s);
 cudaError_t launch_combine_shared(const DecodeArgs& a, int max_groups, int sm_count, cudaStream_t s);
 // Tensor maps, 64-column boxes: query rows (q_abs, q_pe; a.row_tile / 2 rows,
-// 128-B swizzle), cache rows (min(page, 128) rows; bf16 128-B swizzle, e4m3 none)
+// 128-B swizzle), cache rows (bf16: min(page, 128) rows, 128-B swizzle;
+// e4m3: min(page, 64), none)
 cudaError_t launch_key_weights(const CUtensorMap& tm_q, const CUtensorMap& tm_qr, const CUtensorMap& tm_kv, int fp8,
                                const KeyWeightArgs& a, int sm_count, cudaStream_t s);
 cudaError_t launch_compact(const CompactArgs& a, int row_bytes, int sm_count, cudaStream_t s);

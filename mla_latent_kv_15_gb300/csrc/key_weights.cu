@@ -17,8 +17,10 @@
 // tile's exponentials run under the next products.
 //
 // An e4m3 cache lands as codes in a ring of its own and is expanded to bf16 by
-// four warps, each a whole chunk, so that the wait of one for its writes to be
-// seen by the pair's leader runs beside the others' work.
+// eight warps, each half a chunk, so that the wait of one for its writes to be
+// seen by the pair's leader runs beside the others' work.  A stage of that ring
+// is always the same warp's (loads may land out of order, and a wait two phases
+// ahead would not wait).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -35,20 +37,26 @@ constexpr int kKeys = 128;                     // keys of a CTA's half of a tile
 constexpr int kPairKeys = 2 * kKeys;
 constexpr int kChunks = kDqk / 64;             // 9
 constexpr uint32_t kKBytes = kKeys * 128;      // a chunk of a CTA's keys, bf16: one 128-byte swizzled row a key
-constexpr uint32_t kRawBytes = kKeys * 64;     // the same as e4m3 codes
+constexpr int kRawKeys = 64;                   // keys of a load of e4m3 codes: half of a chunk
+constexpr uint32_t kRawBytes = kRawKeys * 64;
 constexpr int kRowTile = 128;                  // query rows of a product at most (its columns)
 constexpr uint32_t kQBytes = kRowTile / 2 * 128;   // a chunk of a CTA's half of them
 constexpr int kAcc = 4;                        // accumulators of kRowTile columns
 constexpr int kWarpK = 0, kWarpQ = 1, kWarpMma = 2, kWarpEpilogue = 4, kWarpExpand = 12;
-constexpr int kExpandWarps = 4;
+constexpr int kExpandWarps = 8;                // each has one stage of the ring of codes to itself
+constexpr int kLseTiles = 8;                   // row tiles of a request whose lse is kept on chip
+// e4m3: registers a thread of the issuing warps, the epilogue's and the
+// expanding ones, of the launch's 96 for each of its five warpgroups
+constexpr uint32_t kRegsIssue = 56, kRegsEpilogue = 136, kRegsExpand = 72;
+static_assert(kRegsIssue + 2 * kRegsEpilogue + 2 * kRegsExpand <= 5 * 96, "register split");
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <bool kFp8>
 struct Shape {
-  static constexpr int kThreads = kFp8 ? 512 : 384;
+  static constexpr int kThreads = kFp8 ? 640 : 384;
   static constexpr int kKSlots = kFp8 ? 9 : 10;    // at least a tile's chunks
-  static constexpr int kQStages = kFp8 ? 4 : 7;
-  static constexpr int kRawStages = kFp8 ? 5 : 0;
+  static constexpr int kQStages = kFp8 ? 5 : 7;
+  static constexpr int kRawStages = kFp8 ? kExpandWarps : 0;
   static constexpr uint32_t kQAt = kKSlots * kKBytes;
   static constexpr uint32_t kRawAt = kQAt + kQStages * kQBytes;
   static constexpr uint32_t kBarsAt = kRawAt + kRawStages * kRawBytes;
@@ -58,7 +66,7 @@ struct Shape {
 struct Bars {
   uint64_t k_full[10], q_full[7];  // (lead) both CTAs' halves are there
   uint64_t k_empty[10], q_empty[7];
-  uint64_t raw_full[5], raw_empty[5];
+  uint64_t raw_full[kExpandWarps], raw_empty[kExpandWarps];
   uint64_t d_full[kAcc];
   uint64_t d_empty[kAcc];          // (lead) the epilogue warps of both CTAs
   uint64_t drain;
@@ -66,8 +74,10 @@ struct Bars {
   int abort;
   int tile0, tiles, b0;            // the pair's share: first tile of request b0, tiles in all
   int leads;                       // the share begins with the first tile of all
-  long long sums[16];
-  float lse2[2][kRowTile];         // lse * log2 e of the row tile's rows, two tiles in turn
+  long long sums[20];
+  // lse * log2 e of the request's rows; where it has more than kLseTiles row
+  // tiles, of two row tiles in turn
+  alignas(16) float lse2[kLseTiles][kRowTile];
   float half[2][kKeys];            // sums of the second half of the columns
 };
 
@@ -147,7 +157,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kFp8>::kThread
 
   if (tid == 0) {
     for (int i = 0; i < S::kKSlots; ++i) {
-      mbar_init(smem_u32(&bars->k_full[i]), 2);      // each CTA's load, or expanding warp
+      mbar_init(smem_u32(&bars->k_full[i]), kFp8 ? 4 : 2);   // each CTA's load, or two expanding warps
       mbar_init(smem_u32(&bars->k_empty[i]), 1);
     }
     for (int i = 0; i < S::kQStages; ++i) {
@@ -272,56 +282,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kFp8>::kThread
     }
   };
 
-  if (warp == kWarpK) {
+  auto load_keys = [&]() {
     // ------------------------------------------------------------------- keys
     uint32_t n = 0;
-    const int sub_rows = a.page_size < kKeys ? a.page_size : kKeys;
-    const int nsub = kKeys / sub_rows;
+    constexpr int kLoadKeys = kFp8 ? kRawKeys : kKeys;
+    const int sub_rows = a.page_size < kLoadKeys ? a.page_size : kLoadKeys;
+    const int nsub = kLoadKeys / sub_rows;         // boxes of a load
     const uint64_t pol = l2_policy_evict_first();
     bool skip = a.debug_skip_tile && bars->leads && rank == 0;
     for_tiles([&](int b, const Request& r, int t) {
       if (r.row_tiles == 0) return;
-      // lane l < nsub: the cache row of sub-page l
+      // lane l < kKeys / sub_rows: the cache row of sub-page l of the CTA's keys
       int y = (int)(a.num_blocks * a.page_size);   // past the cache: reads zeros
       const int key = t * kPairKeys + kKeys * (int)rank + lane * sub_rows;
-      if (lane < nsub && key < r.n) {
+      if (lane * sub_rows < kKeys && key < r.n) {
         const int blk = a.block_table[(int64_t)b * a.max_pages + key / a.page_size];
         if (blk >= 0 && blk < a.num_blocks)
           y = blk * a.page_size + key % a.page_size;
         else
           raise(ctx, 4);   // MLA_DEVERR_BAD_BLOCK
       }
-      for (int c = 0; c < kChunks; ++c, ++n) {
-        if (*abort_flag) return;
-        if constexpr (kFp8) {
-          const uint32_t slot = n % S::kRawStages;
-          wait(ctx, &bars->raw_empty[slot], ((n / S::kRawStages) & 1) ^ 1);
+      for (int c = 0; c < kChunks; ++c) {
+        for (int h = 0; h < kKeys / kLoadKeys; ++h, ++n) {
+          if (*abort_flag) return;
+          const uint32_t slot = n % (kFp8 ? S::kRawStages : S::kKSlots), round = n / (kFp8 ? S::kRawStages : S::kKSlots);
+          wait(ctx, kFp8 ? &bars->raw_empty[slot] : &bars->k_empty[slot], (round & 1) ^ 1);
           __syncwarp();
-          if (skip) {      // test aid: the first chunk never comes
+          if (skip) {      // test aid: the first load never comes
             skip = false;
             continue;
           }
-          const uint32_t full = smem_u32(&bars->raw_full[slot]);
-          if (lane == 0) mbar_expect_tx(full, kRawBytes);
-          __syncwarp();
-          if (lane < nsub)
-            tma_load_2d_hint(smem_u32(smem + S::kRawAt + slot * kRawBytes) + lane * sub_rows * 64u, &tm_kv, 64 * c, y,
-                             full, pol);
-        } else {
-          const uint32_t slot = n % S::kKSlots;
-          wait(ctx, &bars->k_empty[slot], ((n / S::kKSlots) & 1) ^ 1);
-          __syncwarp();
-          if (skip) {
-            skip = false;
-            continue;
+          const int box = lane - h * nsub;         // the lane's box of this load
+          if constexpr (kFp8) {
+            const uint32_t full = smem_u32(&bars->raw_full[slot]);
+            if (lane == 0) mbar_expect_tx(full, kRawBytes);
+            __syncwarp();
+            if (box >= 0 && box < nsub)
+              tma_load_2d_hint(smem_u32(smem + S::kRawAt + slot * kRawBytes) + box * sub_rows * 64u, &tm_kv, 64 * c, y,
+                               full, pol);
+          } else {
+            const uint32_t full = mapa(smem_u32(&bars->k_full[slot]), 0);
+            if (lane == 0) mbar_expect_tx_remote(full, kKBytes);
+            __syncwarp();
+            if (box >= 0 && box < nsub)
+              tma_load_2d_pair_hint(smem_u32(smem + slot * kKBytes) + box * sub_rows * 128u, &tm_kv, 64 * c, y, full,
+                                    pol);
           }
-          const uint32_t full = mapa(smem_u32(&bars->k_full[slot]), 0);
-          if (lane == 0) mbar_expect_tx_remote(full, kKBytes);
           __syncwarp();
-          if (lane < nsub)
-            tma_load_2d_pair_hint(smem_u32(smem + slot * kKBytes) + lane * sub_rows * 128u, &tm_kv, 64 * c, y, full, pol);
         }
-        __syncwarp();
       }
     });
     // every load has landed before the CTA ends (the leader's barriers count both CTAs')
@@ -332,7 +340,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kFp8>::kThread
       for (uint32_t k = n > S::kKSlots ? n - S::kKSlots : 0; k < n && !*abort_flag; ++k)
         wait(ctx, &bars->k_full[k % S::kKSlots], (k / S::kKSlots) & 1);
     }
-  } else if (warp == kWarpQ) {
+  };
+  auto load_queries = [&]() {
     // ------------------------------------------------------------- query rows
     uint32_t n = 0;
     const uint32_t bytes = width / 2 * 128u;
@@ -357,7 +366,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kFp8>::kThread
     if (rank == 0)
       for (uint32_t k = n > S::kQStages ? n - S::kQStages : 0; k < n && !*abort_flag; ++k)
         wait(ctx, &bars->q_full[k % S::kQStages], (k / S::kQStages) & 1);
-  } else if (warp == kWarpMma) {
+  };
+  auto multiply = [&]() {
     // --------------------------------------------------------------- products
     if (rank == 0) {
       const uint32_t idesc = idesc_bf16_f32(256, width, 0, 0);
@@ -393,35 +403,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kFp8>::kThread
       __syncwarp();
       wait(ctx, &bars->drain, 0);
     }
-  } else if (warp >= kWarpEpilogue && warp < kWarpExpand) {
+  };
+  auto epilogue = [&]() {
     // --------------------------------------------------------------- epilogue
     const int e = tid - 32 * kWarpEpilogue;      // 0..255
     const int q4 = warp & 3, hh = e >> 7;        // tensor-memory lanes 32 q4.., 32-column groups of parity hh
     const int key = q4 * 32 + lane;
     const uint32_t from = tmem + ((uint32_t)(q4 * 32) << 16);
-    uint32_t m = 0, tile_no = 0;
+    uint32_t m = 0, tile_no = 0, turn = 0;
     int at_b = -1;
-    uint32_t set = 0;                            // the buffer of lse2 in use
+    // lse * log2 e of one of the request's rows
+    auto lse2_of = [&](const Request& r, int row) {
+      const float l = a.lse[(int64_t)r.q0 * a.num_heads + row] * kLog2e;
+      return l == -INFINITY ? INFINITY : l;      // a row without keys gives no weight
+    };
     for_tiles([&](int b, const Request& r, int t) {
       const int j = t * kPairKeys + kKeys * (int)rank + key;
       // the first of the request's rows that sees key j (the rest follow)
       const int late = j - (r.n - r.sq);
       const int first_row = late > 0 ? late * a.num_heads : 0;
       const int first_max = __reduce_max_sync(0xffffffffu, first_row);
+      const bool kept = r.row_tiles <= kLseTiles;
+      if (kept && at_b != b) {
+        epilogue_sync();                         // the last request's are read
+        for (int row = e; row < r.rows; row += 256) bars->lse2[row / width][row % width] = lse2_of(r, row);
+        epilogue_sync();
+      }
+      at_b = b;
       float sum[4] = {0.f, 0.f, 0.f, 0.f};
       for (int rt = 0; rt < r.row_tiles; ++rt, ++m) {
         const uint32_t acc = m % kAcc;
         const int base = rt * width, cols = min(width, r.rows - base);
-        if (r.row_tiles > 1 || at_b != b) {
-          set ^= 1;
-          if (e < cols) {
-            const float l = a.lse[(int64_t)r.q0 * a.num_heads + base + e] * kLog2e;
-            bars->lse2[set][e] = l == -INFINITY ? INFINITY : l;   // a row without keys gives no weight
-          }
+        const float* lse2 = bars->lse2[rt % kLseTiles];
+        if (!kept) {
+          lse2 = bars->lse2[++turn & 1];
+          if (e < cols) bars->lse2[turn & 1][e] = lse2_of(r, base + e);
           epilogue_sync();
-          at_b = b;
         }
-        const float* lse2 = bars->lse2[set];
         wait(ctx, &bars->d_full[acc], (m / kAcc) & 1);
         __syncwarp();
         tc_fence_after();
@@ -461,22 +479,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kFp8>::kThread
         *w = a.decay != 0.f ? fmaf(a.decay, *w, got) : got;
       }
     });
-  } else if (kFp8 && warp >= kWarpExpand) {
+  };
+  auto expand = [&]() {
     // -------------------------------------------------------- e4m3 expansion
-    const uint32_t turn = (uint32_t)(warp - kWarpExpand);
-    uint32_t n = 0;
+    const uint32_t mine = (uint32_t)(warp - kWarpExpand);   // the warp's stage
+    uint32_t n = 0;                                           // chunks so far
+    uint32_t uses = 0;
     for_tiles([&](int, const Request& r, int) {
       if (r.row_tiles == 0) return;
       for (int c = 0; c < kChunks; ++c, ++n) {
-        if (n % kExpandWarps != turn) continue;
-        const uint32_t from = n % S::kRawStages, slot = n % S::kKSlots;
-        wait(ctx, &bars->raw_full[from], (n / S::kRawStages) & 1);
+        // loads 2 n and 2 n + 1 hold the chunk's halves
+        if (n % (kExpandWarps / 2) != mine / 2) continue;
+        const uint32_t slot = n % S::kKSlots;
+        wait(ctx, &bars->raw_full[mine], uses++ & 1);
         wait(ctx, &bars->k_empty[slot], ((n / S::kKSlots) & 1) ^ 1);
         __syncwarp();
-        const uint4* src = reinterpret_cast<const uint4*>(smem + S::kRawAt + from * kRawBytes);
-        uint8_t* dst = smem + slot * kKBytes;
+        const uint4* src = reinterpret_cast<const uint4*>(smem + S::kRawAt + mine * kRawBytes);
+        uint8_t* dst = smem + slot * kKBytes + (mine & 1) * kRawKeys * 128;
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
+        for (int g = 0; g < 2; ++g) {
           uint4 v[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) v[k] = src[lane + 32 * (4 * g + k)];
@@ -493,11 +514,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kFp8>::kThread
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(smem_u32(&bars->raw_empty[from]));
+          mbar_arrive(smem_u32(&bars->raw_empty[mine]));
           mbar_arrive_release_cluster(mapa(smem_u32(&bars->k_full[slot]), 0));
         }
       }
     });
+  };
+
+  if constexpr (kFp8) {
+    // each warpgroup sets its register budget
+    if (warp < kWarpEpilogue) {
+      setmaxnreg_dec<kRegsIssue>();
+      if (warp == kWarpK)
+        load_keys();
+      else if (warp == kWarpQ)
+        load_queries();
+      else if (warp == kWarpMma)
+        multiply();
+    } else if (warp < kWarpExpand) {
+      setmaxnreg_inc<kRegsEpilogue>();
+      epilogue();
+    } else {
+      setmaxnreg_dec<kRegsExpand>();
+      expand();
+    }
+  } else {
+    if (warp == kWarpK)
+      load_keys();
+    else if (warp == kWarpQ)
+      load_queries();
+    else if (warp == kWarpMma)
+      multiply();
+    else if (warp >= kWarpEpilogue)
+      epilogue();
   }
   __syncwarp();
   if (*abort_flag) {
