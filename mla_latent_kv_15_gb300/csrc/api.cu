@@ -909,16 +909,16 @@ int mla_key_weights(const void* q_abs, const void* q_pe, const void* cache, int6
   const int sms = sm_count();
   if (sms < 2) return fail(MLA_ERR_CUDA, "cannot query the current device");
   // Columns of a product: a request's query rows (of an average one, where
-  // query_start_loc says) in as few tiles of at most 128 as hold them, a
+  // query_start_loc says) in as few tiles of at most 256 as hold them, a
   // multiple of 32; each CTA of a pair loads half of them
   const int64_t per_request = (total_q + (int64_t)batch - 1) / batch * num_heads;
-  const int64_t row_tiles = per_request > 128 ? (per_request + 127) / 128 : 1;
+  const int64_t row_tiles = per_request > 256 ? (per_request + 255) / 256 : 1;
   int row_tile = (int)((per_request + row_tiles - 1) / row_tiles + 31) / 32 * 32;
   if (row_tile < 32) row_tile = 32;
   CUtensorMap tm_q, tm_qr, tm_kv;
   bool enc = mla::encode_tmap_2d(&tm_kv, cache, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                                 mla::kDqk, (uint64_t)num_blocks * page_size, mla::kDqk * (fp8 ? 1 : 2), 64,
-                                 page_size < (fp8 ? 64 : 128) ? page_size : (fp8 ? 64 : 128),
+                                 mla::kDqk, (uint64_t)num_blocks * page_size, mla::kDqk * (fp8 ? 1 : 2), fp8 ? 192 : 64,
+                                 page_size < (fp8 ? 32 : 128) ? page_size : (fp8 ? 32 : 128),
                                  fp8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B);
   tm_q = tm_qr = tm_kv;   // without a query row none is loaded
   if (total_q > 0)

@@ -173,7 +173,7 @@ struct KeyWeightArgs {
   int64_t num_blocks;
   float scale_log2;           // scale * log2(e) (* kv_scale for e4m3)
   float decay;
-  int row_tile;               // query rows of a product: a multiple of 32, at most 128
+  int row_tile;               // query rows of a product: a multiple of 32, at most 256
   int* status;                // OR of mla_device_error bits, or null
   unsigned long long wait_limit_ns;
   int debug_skip_tile;        // test aid: the first tile's first chunk never comes
@@ -333,9 +333,9 @@ cudaError_t launch_decode_shared(const CUtensorMap& tm_q, const CUtensorMap& tm_
                                  const CUtensorMap& tm_kvr, const CUtensorMap& tm_out, const CUtensorMap& tm_part,
                                  int variant, const DecodeArgs& a, int num_clusters, cudaStream_t s);
 cudaError_t launch_combine_shared(const DecodeArgs& a, int max_groups, int sm_count, cudaStream_t s);
-// Tensor maps, 64-column boxes: query rows (q_abs, q_pe; a.row_tile / 2 rows,
-// 128-B swizzle), cache rows (bf16: min(page, 128) rows, 128-B swizzle;
-// e4m3: min(page, 64), none)
+// Tensor maps: query rows (q_abs, q_pe; boxes of 64 columns x a.row_tile / 2
+// rows, 128-B swizzle), cache rows (bf16: 64 x min(page, 128), 128-B swizzle;
+// e4m3: 192 x min(page, 32), none)
 cudaError_t launch_key_weights(const CUtensorMap& tm_q, const CUtensorMap& tm_qr, const CUtensorMap& tm_kv, int fp8,
                                const KeyWeightArgs& a, int sm_count, cudaStream_t s);
 cudaError_t launch_compact(const CompactArgs& a, int row_bytes, int sm_count, cudaStream_t s);

@@ -10,17 +10,16 @@
 //
 // CTA pairs (cta_group::2) take contiguous shares of all requests' 256-key
 // tiles, 128 keys a CTA.  A tile's nine 64-column chunks stay in shared memory
-// while the request's row tiles of up to 128 query rows (half of them in each
+// while the request's row tiles of up to 256 query rows (half of them in each
 // CTA) stream past them; with one row tile a request the nine slots are a ring
 // like any other.  So the cache is read once whatever the number of rows, and a
-// pair's query rows once a 256-key tile.  Four accumulators in tensor memory: a
-// tile's exponentials run under the next products.
+// pair's query rows once a 256-key tile.  Two accumulators of up to 256 columns
+// in tensor memory (four of up to 128): a tile's exponentials run under the next
+// products.
 //
 // An e4m3 cache lands as codes in a ring of its own and is expanded to bf16 by
-// eight warps, each half a chunk, so that the wait of one for its writes to be
-// seen by the pair's leader runs beside the others' work.  A stage of that ring
-// is always the same warp's (loads may land out of order, and a wait two phases
-// ahead would not wait).
+// seven warps.  A stage of that ring is always the same warp's (loads may land
+// out of order, and a wait two phases ahead would not wait).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -37,47 +36,48 @@ constexpr int kKeys = 128;                     // keys of a CTA's half of a tile
 constexpr int kPairKeys = 2 * kKeys;
 constexpr int kChunks = kDqk / 64;             // 9
 constexpr uint32_t kKBytes = kKeys * 128;      // a chunk of a CTA's keys, bf16: one 128-byte swizzled row a key
-constexpr int kRawKeys = 64;                   // keys of a load of e4m3 codes: half of a chunk
-constexpr uint32_t kRawBytes = kRawKeys * 64;
-constexpr int kRowTile = 128;                  // query rows of a product at most (its columns)
-constexpr uint32_t kQBytes = kRowTile / 2 * 128;   // a chunk of a CTA's half of them
-constexpr int kAcc = 4;                        // accumulators of kRowTile columns
+// a load of e4m3 codes: 32 keys x 192 columns, three chunks (rows of 64 bytes
+// load at half the rate of rows of 128 and more)
+constexpr int kRawKeys = 32, kRawChunks = 3;
+constexpr uint32_t kRawRow = kRawChunks * 64, kRawBytes = kRawKeys * kRawRow;
+constexpr int kRowTile = 256;                  // query rows of a product at most (its columns)
+constexpr int kMaxQStages = 8;
 constexpr int kWarpK = 0, kWarpQ = 1, kWarpMma = 2, kWarpEpilogue = 4, kWarpExpand = 12;
-constexpr int kExpandWarps = 8;                // each has one stage of the ring of codes to itself
-constexpr int kLseTiles = 8;                   // row tiles of a request whose lse is kept on chip
+constexpr int kExpandWarps = 7;                // each has one stage of the ring of codes to itself
+constexpr int kLseRows = 1024;                 // rows of a request whose lse is kept on chip
 // e4m3: registers a thread of the issuing warps, the epilogue's and the
 // expanding ones, of the launch's 96 for each of its five warpgroups
-constexpr uint32_t kRegsIssue = 56, kRegsEpilogue = 136, kRegsExpand = 72;
+constexpr uint32_t kRegsIssue = 56, kRegsEpilogue = 112, kRegsExpand = 96;
 static_assert(kRegsIssue + 2 * kRegsEpilogue + 2 * kRegsExpand <= 5 * 96, "register split");
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <bool kFp8>
 struct Shape {
   static constexpr int kThreads = kFp8 ? 640 : 384;
-  static constexpr int kKSlots = kFp8 ? 9 : 10;    // at least a tile's chunks
-  static constexpr int kQStages = kFp8 ? 5 : 7;
+  static constexpr int kKSlots = kChunks;
+  static constexpr uint32_t kQRegion = kFp8 ? 32768 : 65536;   // as many stages of a CTA's half of a row tile as fit
   static constexpr int kRawStages = kFp8 ? kExpandWarps : 0;
   static constexpr uint32_t kQAt = kKSlots * kKBytes;
-  static constexpr uint32_t kRawAt = kQAt + kQStages * kQBytes;
+  static constexpr uint32_t kRawAt = kQAt + kQRegion;
   static constexpr uint32_t kBarsAt = kRawAt + kRawStages * kRawBytes;
 };
 
 // Barriers marked (lead) are used in the leading CTA only, by both CTAs.
 struct Bars {
-  uint64_t k_full[10], q_full[7];  // (lead) both CTAs' halves are there
-  uint64_t k_empty[10], q_empty[7];
+  uint64_t k_full[kChunks], q_full[kMaxQStages];  // (lead) both CTAs' halves are there
+  uint64_t k_empty[kChunks], q_empty[kMaxQStages];
   uint64_t raw_full[kExpandWarps], raw_empty[kExpandWarps];
-  uint64_t d_full[kAcc];
-  uint64_t d_empty[kAcc];          // (lead) the epilogue warps of both CTAs
+  uint64_t d_full[4];
+  uint64_t d_empty[4];             // (lead) the epilogue warps of both CTAs
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
   int tile0, tiles, b0;            // the pair's share: first tile of request b0, tiles in all
   int leads;                       // the share begins with the first tile of all
   long long sums[20];
-  // lse * log2 e of the request's rows; where it has more than kLseTiles row
-  // tiles, of two row tiles in turn
-  alignas(16) float lse2[kLseTiles][kRowTile];
+  // lse * log2 e of the request's rows; where it has more than these, of two row
+  // tiles in turn
+  alignas(16) float lse2[kLseRows];
   float half[2][kKeys];            // sums of the second half of the columns
 };
 
@@ -157,10 +157,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kFp8>::kThread
 
   if (tid == 0) {
     for (int i = 0; i < S::kKSlots; ++i) {
-      mbar_init(smem_u32(&bars->k_full[i]), kFp8 ? 4 : 2);   // each CTA's load, or two expanding warps
+      mbar_init(smem_u32(&bars->k_full[i]), kFp8 ? 2 * kKeys / kRawKeys : 2);   // each CTA's load, or expanded loads
       mbar_init(smem_u32(&bars->k_empty[i]), 1);
     }
-    for (int i = 0; i < S::kQStages; ++i) {
+    for (int i = 0; i < kMaxQStages; ++i) {
       mbar_init(smem_u32(&bars->q_full[i]), 2);
       mbar_init(smem_u32(&bars->q_empty[i]), 1);
     }
@@ -168,7 +168,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kFp8>::kThread
       mbar_init(smem_u32(&bars->raw_full[i]), 1);
       mbar_init(smem_u32(&bars->raw_empty[i]), 1);
     }
-    for (int i = 0; i < kAcc; ++i) {
+    for (int i = 0; i < 4; ++i) {
       mbar_init(smem_u32(&bars->d_full[i]), 1);
       mbar_init(smem_u32(&bars->d_empty[i]), 16);
     }
@@ -180,7 +180,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kFp8>::kThread
     tma_prefetch_desc(&tm_kv);
   }
   if (warp == kWarpMma) {
-    tmem_alloc_pair(smem_u32(&bars->tmem_base), kAcc * kRowTile);
+    tmem_alloc_pair(smem_u32(&bars->tmem_base), 512);
     tmem_relinquish_pair();
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -250,6 +250,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kFp8>::kThread
   const uint32_t tmem = bars->tmem_base;
   const int tiles = bars->tiles;
   const int width = a.row_tile;
+  const uint32_t q_bytes = width / 2 * 128u;                   // a chunk of a CTA's half of a row tile
+  const uint32_t q_stages = min(S::kQRegion / q_bytes, (uint32_t)kMaxQStages);
+  const uint32_t acc_cols = width > 128 ? 256 : 128, accs = 512 / acc_cols;
+  // a position in a ring, and how often it has gone round
+  struct Turn {
+    uint32_t at, round;
+    __device__ void next(uint32_t n) {
+      if (++at == n) {
+        at = 0;
+        ++round;
+      }
+    }
+  };
 
   auto request = [&](int b) {
     Request r;
@@ -284,8 +297,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kFp8>::kThread
 
   auto load_keys = [&]() {
     // ------------------------------------------------------------------- keys
-    uint32_t n = 0;
+    uint32_t n = 0;                                // loads so far
     constexpr int kLoadKeys = kFp8 ? kRawKeys : kKeys;
+    constexpr uint32_t kSlots = kFp8 ? S::kRawStages : S::kKSlots;
     const int sub_rows = a.page_size < kLoadKeys ? a.page_size : kLoadKeys;
     const int nsub = kLoadKeys / sub_rows;         // boxes of a load
     const uint64_t pol = l2_policy_evict_first();
@@ -302,10 +316,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kFp8>::kThread
         else
           raise(ctx, 4);   // MLA_DEVERR_BAD_BLOCK
       }
-      for (int c = 0; c < kChunks; ++c) {
+      // e4m3: 32 keys after 32 keys of three chunks, then of the next three
+      for (int c = 0; c < kChunks; c += kFp8 ? kRawChunks : 1) {
         for (int h = 0; h < kKeys / kLoadKeys; ++h, ++n) {
           if (*abort_flag) return;
-          const uint32_t slot = n % (kFp8 ? S::kRawStages : S::kKSlots), round = n / (kFp8 ? S::kRawStages : S::kKSlots);
+          const uint32_t slot = n % kSlots, round = n / kSlots;
           wait(ctx, kFp8 ? &bars->raw_empty[slot] : &bars->k_empty[slot], (round & 1) ^ 1);
           __syncwarp();
           if (skip) {      // test aid: the first load never comes
@@ -313,18 +328,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kFp8>::kThread
             continue;
           }
           const int box = lane - h * nsub;         // the lane's box of this load
+          const bool mine = box >= 0 && box < nsub;
           if constexpr (kFp8) {
             const uint32_t full = smem_u32(&bars->raw_full[slot]);
             if (lane == 0) mbar_expect_tx(full, kRawBytes);
             __syncwarp();
-            if (box >= 0 && box < nsub)
-              tma_load_2d_hint(smem_u32(smem + S::kRawAt + slot * kRawBytes) + box * sub_rows * 64u, &tm_kv, 64 * c, y,
-                               full, pol);
+            if (mine)
+              tma_load_2d_hint(smem_u32(smem + S::kRawAt + slot * kRawBytes) + box * sub_rows * kRawRow, &tm_kv, 64 * c,
+                               y, full, pol);
           } else {
             const uint32_t full = mapa(smem_u32(&bars->k_full[slot]), 0);
             if (lane == 0) mbar_expect_tx_remote(full, kKBytes);
             __syncwarp();
-            if (box >= 0 && box < nsub)
+            if (mine)
               tma_load_2d_pair_hint(smem_u32(smem + slot * kKBytes) + box * sub_rows * 128u, &tm_kv, 64 * c, y, full,
                                     pol);
           }
@@ -343,29 +359,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kFp8>::kThread
   };
   auto load_queries = [&]() {
     // ------------------------------------------------------------- query rows
-    uint32_t n = 0;
-    const uint32_t bytes = width / 2 * 128u;
+    Turn q{0, 0};
     for_tiles([&](int, const Request& r, int) {
       for (int rt = 0; rt < r.row_tiles; ++rt) {
         const int row0 = r.q0 * a.num_heads + rt * width + width / 2 * (int)rank;
-        for (int c = 0; c < kChunks; ++c, ++n) {
+        for (int c = 0; c < kChunks; ++c, q.next(q_stages)) {
           if (*abort_flag) return;
-          const uint32_t stage = n % S::kQStages;
-          wait(ctx, &bars->q_empty[stage], ((n / S::kQStages) & 1) ^ 1);
+          wait(ctx, &bars->q_empty[q.at], (q.round & 1) ^ 1);
           __syncwarp();
           if (elect_one()) {
-            const uint32_t full = mapa(smem_u32(&bars->q_full[stage]), 0);
-            mbar_expect_tx_remote(full, bytes);
-            tma_load_2d_pair(smem_u32(smem + S::kQAt + stage * kQBytes), c < 8 ? &tm_q : &tm_qr, c < 8 ? 64 * c : 0,
-                             row0, full);
+            const uint32_t full = mapa(smem_u32(&bars->q_full[q.at]), 0);
+            mbar_expect_tx_remote(full, q_bytes);
+            tma_load_2d_pair(smem_u32(smem + S::kQAt + q.at * q_bytes), c < 8 ? &tm_q : &tm_qr, c < 8 ? 64 * c : 0, row0,
+                             full);
           }
           __syncwarp();
         }
       }
     });
     if (rank == 0)
-      for (uint32_t k = n > S::kQStages ? n - S::kQStages : 0; k < n && !*abort_flag; ++k)
-        wait(ctx, &bars->q_full[k % S::kQStages], (k / S::kQStages) & 1);
+      for (uint32_t k = 0; k < q_stages && !*abort_flag; ++k, q.next(q_stages))
+        if (q.round > 0) wait(ctx, &bars->q_full[q.at], (q.round - 1) & 1);   // its last load
   };
   auto multiply = [&]() {
     // --------------------------------------------------------------- products
@@ -373,31 +387,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kFp8>::kThread
       const uint32_t idesc = idesc_bf16_f32(256, width, 0, 0);
       constexpr uint32_t hi = desc_hi(1024, kSwizzle128B);
       const uint32_t k_lo = desc_lo(smem_u32(smem), 16), q_lo = desc_lo(smem_u32(smem + S::kQAt), 16);
-      uint32_t kn = 0, qn = 0, m = 0;
+      uint32_t tile = 0;                         // tiles with rows so far: each takes every key slot once
+      Turn q{0, 0}, d{0, 0};
       for_tiles([&](int, const Request& r, int) {
-        for (int rt = 0; rt < r.row_tiles; ++rt, ++m) {
+        for (int rt = 0; rt < r.row_tiles; ++rt, d.next(accs)) {
           if (*abort_flag) return;
-          const uint32_t acc = m % kAcc;
-          wait(ctx, &bars->d_empty[acc], ((m / kAcc) & 1) ^ 1);
-          for (int c = 0; c < kChunks; ++c, ++qn) {
-            const uint32_t kc = kn + c, slot = kc % S::kKSlots, stage = qn % S::kQStages;
-            if (rt == 0) wait(ctx, &bars->k_full[slot], (kc / S::kKSlots) & 1);
-            wait(ctx, &bars->q_full[stage], (qn / S::kQStages) & 1);
+          wait(ctx, &bars->d_empty[d.at], (d.round & 1) ^ 1);
+          for (int c = 0; c < kChunks; ++c, q.next(q_stages)) {
+            if (rt == 0) wait(ctx, &bars->k_full[c], tile & 1);
+            wait(ctx, &bars->q_full[q.at], q.round & 1);
             __syncwarp();
             tc_fence_after();
             if (elect_one()) {
-              const uint32_t ka = k_lo + slot * (kKBytes >> 4), qa = q_lo + stage * (kQBytes >> 4);
+              const uint32_t ka = k_lo + c * (kKBytes >> 4), qa = q_lo + q.at * (q_bytes >> 4);
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                mma_pair_ss(tmem + acc * kRowTile, ka + 2 * k, hi, qa + 2 * k, hi, idesc, (c | k) ? 1u : 0u);
-              mma_commit_pair(smem_u32(&bars->q_empty[stage]));
-              if (rt == r.row_tiles - 1) mma_commit_pair(smem_u32(&bars->k_empty[slot]));
-              if (c == kChunks - 1) mma_commit_pair(smem_u32(&bars->d_full[acc]));
+                mma_pair_ss(tmem + d.at * acc_cols, ka + 2 * k, hi, qa + 2 * k, hi, idesc, (c | k) ? 1u : 0u);
+              mma_commit_pair(smem_u32(&bars->q_empty[q.at]));
+              if (rt == r.row_tiles - 1) mma_commit_pair(smem_u32(&bars->k_empty[c]));
+              if (c == kChunks - 1) mma_commit_pair(smem_u32(&bars->d_full[d.at]));
             }
             __syncwarp();
           }
         }
-        if (r.row_tiles > 0) kn += kChunks;
+        if (r.row_tiles > 0) ++tile;
       });
       if (elect_one()) mma_commit_pair(smem_u32(&bars->drain));
       __syncwarp();
@@ -410,7 +423,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kFp8>::kThread
     const int q4 = warp & 3, hh = e >> 7;        // tensor-memory lanes 32 q4.., 32-column groups of parity hh
     const int key = q4 * 32 + lane;
     const uint32_t from = tmem + ((uint32_t)(q4 * 32) << 16);
-    uint32_t m = 0, tile_no = 0, turn = 0;
+    Turn d{0, 0};
+    uint32_t tile_no = 0, turn = 0;
     int at_b = -1;
     // lse * log2 e of one of the request's rows
     auto lse2_of = [&](const Request& r, int row) {
@@ -423,29 +437,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kFp8>::kThread
       const int late = j - (r.n - r.sq);
       const int first_row = late > 0 ? late * a.num_heads : 0;
       const int first_max = __reduce_max_sync(0xffffffffu, first_row);
-      const bool kept = r.row_tiles <= kLseTiles;
+      const bool kept = r.rows <= kLseRows;
       if (kept && at_b != b) {
         epilogue_sync();                         // the last request's are read
-        for (int row = e; row < r.rows; row += 256) bars->lse2[row / width][row % width] = lse2_of(r, row);
+        for (int row = e; row < r.rows; row += 256) bars->lse2[row] = lse2_of(r, row);
         epilogue_sync();
       }
       at_b = b;
       float sum[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int rt = 0; rt < r.row_tiles; ++rt, ++m) {
-        const uint32_t acc = m % kAcc;
+      for (int rt = 0; rt < r.row_tiles; ++rt, d.next(accs)) {
         const int base = rt * width, cols = min(width, r.rows - base);
-        const float* lse2 = bars->lse2[rt % kLseTiles];
+        const float* lse2 = bars->lse2 + base;
         if (!kept) {
-          lse2 = bars->lse2[++turn & 1];
-          if (e < cols) bars->lse2[turn & 1][e] = lse2_of(r, base + e);
+          float* to = bars->lse2 + (++turn & 1) * kRowTile;
+          if (e < cols) to[e] = lse2_of(r, base + e);
+          lse2 = to;
           epilogue_sync();
         }
-        wait(ctx, &bars->d_full[acc], (m / kAcc) & 1);
+        wait(ctx, &bars->d_full[d.at], d.round & 1);
         __syncwarp();
         tc_fence_after();
         for (int c0 = 32 * hh; c0 < cols; c0 += 64) {
           uint32_t s[32];
-          tmem_ld32(from + acc * kRowTile + c0, s);
+          tmem_ld32(from + d.at * acc_cols + c0, s);
           tmem_wait_ld();
           if (c0 + 32 <= cols && first_max <= base + c0) {
 #pragma unroll
@@ -467,7 +481,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kFp8>::kThread
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_remote(mapa(smem_u32(&bars->d_empty[acc]), 0));
+        if (lane == 0) mbar_arrive_remote(mapa(smem_u32(&bars->d_empty[d.at]), 0));
       }
       const float mine = (sum[0] + sum[1]) + (sum[2] + sum[3]);
       float* half = bars->half[tile_no++ & 1];
@@ -483,41 +497,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kFp8>::kThread
   auto expand = [&]() {
     // -------------------------------------------------------- e4m3 expansion
     const uint32_t mine = (uint32_t)(warp - kWarpExpand);   // the warp's stage
-    uint32_t n = 0;                                           // chunks so far
-    uint32_t uses = 0;
+    uint32_t load = 0, tile = 0, uses = 0;                    // loads, tiles so far
+    if (mine >= kExpandWarps) return;
     for_tiles([&](int, const Request& r, int) {
       if (r.row_tiles == 0) return;
-      for (int c = 0; c < kChunks; ++c, ++n) {
-        // loads 2 n and 2 n + 1 hold the chunk's halves
-        if (n % (kExpandWarps / 2) != mine / 2) continue;
-        const uint32_t slot = n % S::kKSlots;
-        wait(ctx, &bars->raw_full[mine], uses++ & 1);
-        wait(ctx, &bars->k_empty[slot], ((n / S::kKSlots) & 1) ^ 1);
-        __syncwarp();
-        const uint4* src = reinterpret_cast<const uint4*>(smem + S::kRawAt + mine * kRawBytes);
-        uint8_t* dst = smem + slot * kKBytes + (mine & 1) * kRawKeys * 128;
+      for (int c = 0; c < kChunks; c += kRawChunks) {
+        for (int h = 0; h < kKeys / kRawKeys; ++h, ++load) {
+          if (load % kExpandWarps != mine) continue;
+          wait(ctx, &bars->raw_full[mine], uses++ & 1);
+          __syncwarp();
+          // the codes leave their stage at once, for its next load
+          constexpr int kPieces = kRawBytes / 16 / 32;
+          const uint4* src = reinterpret_cast<const uint4*>(smem + S::kRawAt + mine * kRawBytes);
+          uint4 v[kPieces];
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          uint4 v[4];
+          for (int k = 0; k < kPieces; ++k) v[k] = src[lane + 32 * k];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&bars->raw_empty[mine]));
 #pragma unroll
-          for (int k = 0; k < 4; ++k) v[k] = src[lane + 32 * (4 * g + k)];
+          for (int k = 0; k < kRawChunks; ++k) wait(ctx, &bars->k_empty[c + k], (tile & 1) ^ 1);
+          __syncwarp();
+          uint8_t* dst = smem + c * kKBytes + h * kRawKeys * 128;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int at = lane + 32 * (4 * g + k), q = at & 3, row = at >> 2;
+          for (int k = 0; k < kPieces; ++k) {
+            // 16 codes: piece q of row `row`, columns 16 (q % 4) of chunk q / 4
+            const int at = lane + 32 * k, row = at / 12, q = at % 12, p = 2 * (q & 3);
             uint32_t o[8];
             widen16(v[k], o);
-            uint4* to = reinterpret_cast<uint4*>(dst + row * 128);
-            to[(2 * q) ^ (row & 7)] = make_uint4(o[0], o[1], o[2], o[3]);
-            to[(2 * q + 1) ^ (row & 7)] = make_uint4(o[4], o[5], o[6], o[7]);
+            uint4* to = reinterpret_cast<uint4*>(dst + (q >> 2) * kKBytes + row * 128);
+            to[p ^ (row & 7)] = make_uint4(o[0], o[1], o[2], o[3]);
+            to[(p + 1) ^ (row & 7)] = make_uint4(o[4], o[5], o[6], o[7]);
           }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(smem_u32(&bars->raw_empty[mine]));
-          mbar_arrive_release_cluster(mapa(smem_u32(&bars->k_full[slot]), 0));
+          // the writes are in this CTA's shared memory, for the tensor cores to
+          // read, before the leader hears of them
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane < kRawChunks) mbar_arrive_remote(mapa(smem_u32(&bars->k_full[c + lane]), 0));
         }
       }
+      ++tile;
     });
   };
 
@@ -563,7 +581,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kFp8>::kThread
     if (rank == 1) wait(ctx, &bars->drain, 0);
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc_pair(tmem, kAcc * kRowTile);
+    tmem_dealloc_pair(tmem, 512);
   }
 }
 
