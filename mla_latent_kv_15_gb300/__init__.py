@@ -579,6 +579,49 @@ def decode_shared_workspace_size(batch: int, prefixes: int, total_q: int, num_he
     return int(load().mla_decode_shared_workspace_size(batch, prefixes, total_q, num_heads, max_splits))
 
 
+# Checks of the calls for long contexts: the usual case in one expression (a
+# tensor's attributes are most of a small call's time), _dense to say what is wrong.
+
+def _vector(t, name: str, dtype, n=None):
+    """The length of a dense 1-D tensor."""
+    shape = t.shape
+    if not (t.dtype is dtype and len(shape) == 1 and (n is None or shape[0] == n) and t.is_contiguous()):
+        _dense(t, name, dtype, (n,))
+    return shape[0]
+
+
+def _table(t, name: str, dtype, rows=None):
+    """The shape of a dense 2-D tensor."""
+    shape = t.shape
+    if not (t.dtype is dtype and len(shape) == 2 and (rows is None or shape[0] == rows) and t.is_contiguous()):
+        _dense(t, name, dtype, (rows, None))
+    return shape
+
+
+def _query(q_abs, q_pe, bf16):
+    """(tokens, heads) of an absorbed query and its rope part."""
+    shape = q_abs.shape
+    if not (q_abs.dtype is bf16 and len(shape) == 3 and shape[2] == LKV and q_abs.is_contiguous()):
+        _dense(q_abs, "q_abs", bf16, (None, None, LKV))
+    T, N, _ = shape
+    _dense(q_pe, "q_pe", bf16, (T, N, ROPE))
+    return T, N
+
+
+def _weight_rows(weights, batch: int, f32):
+    """(stride, width) of a [batch, W] float32 tensor with contiguous rows."""
+    shape = weights.shape
+    if weights.dtype is not f32:
+        raise ValueError(f"weights must be float32, got {str(weights.dtype).replace('torch.', '')}")
+    if len(shape) != 2 or shape[0] != batch:
+        raise ValueError(f"weights must have shape [{batch}, *], got {tuple(shape)}")
+    width = shape[1]
+    stride, inner = weights.stride()
+    if inner != 1 and width > 1:
+        raise ValueError(f"weights' last dimension must be contiguous, got strides {(stride, inner)}")
+    return (width if batch <= 1 else stride), width
+
+
 def decode_shared(q_abs, q_pe, cache, prefix_table, prefix_lens, prefix_requests, block_table, seq_lens, out,
                   workspace, *, scale: float, query_start_loc=None, lse=None, num_splits: int = 0,
                   kv_scale: float = 1.0, stream=None) -> None:
@@ -589,45 +632,30 @@ def decode_shared(q_abs, q_pe, cache, prefix_table, prefix_lens, prefix_requests
     (``block_table``, ``seq_lens``: without the prefix).  ``workspace`` from
     decode_shared_workspace_size; errors by decode_status(workspace)."""
     import torch
-    nb, ps, _ = _decode_checked(q_abs, q_pe, cache, block_table, seq_lens, out, query_start_loc, lse)
-    T, N = q_abs.shape[:2]
-    i32 = torch.int32
-    _dense(prefix_table, "prefix_table", i32, dims=2)
-    G = prefix_table.shape[0]
-    _dense(prefix_lens, "prefix_lens", i32, (G,))
-    _dense(prefix_requests, "prefix_requests", i32, (G + 1,))
+    bf16, i32 = torch.bfloat16, torch.int32
+    T, N = _query(q_abs, q_pe, bf16)
+    nb, ps, _ = _cache_checked(cache)
+    G, prefix_pages = _table(prefix_table, "prefix_table", i32)
+    _vector(prefix_lens, "prefix_lens", i32, G)
+    _vector(prefix_requests, "prefix_requests", i32, G + 1)
+    B = _vector(seq_lens, "seq_lens", i32)
+    pages = _table(block_table, "block_table", i32, B)[1]
+    _dense(out, "out", bf16, (T, N, LKV))
     _dense(workspace, "workspace", workspace.dtype, workspace.shape)
+    qsl = at_lse = None
+    if query_start_loc is not None:
+        _vector(query_start_loc, "query_start_loc", i32, B + 1)
+        qsl = query_start_loc.data_ptr()
+    if lse is not None:
+        _dense(lse, "lse", torch.float32, (T, N))
+        at_lse = lse.data_ptr()
     dev = _on_current_device(q_abs, q_pe, cache, prefix_table, prefix_lens, prefix_requests, block_table, seq_lens,
                              out, workspace, query_start_loc, lse)
     _check(load().mla_decode_shared(q_abs.data_ptr(), q_pe.data_ptr(), cache.data_ptr(), nb, ps, _dtype_code(cache),
-                                    kv_scale, prefix_table.data_ptr(), prefix_table.shape[1], prefix_lens.data_ptr(),
-                                    prefix_requests.data_ptr(), G, block_table.data_ptr(), block_table.shape[1],
-                                    seq_lens.data_ptr(), seq_lens.shape[0],
-                                    None if query_start_loc is None else query_start_loc.data_ptr(), T, N, scale,
-                                    num_splits, out.data_ptr(), None if lse is None else lse.data_ptr(),
+                                    kv_scale, prefix_table.data_ptr(), prefix_pages, prefix_lens.data_ptr(),
+                                    prefix_requests.data_ptr(), G, block_table.data_ptr(), pages,
+                                    seq_lens.data_ptr(), B, qsl, T, N, scale, num_splits, out.data_ptr(), at_lse,
                                     workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, dev)))
-
-
-def _weight_rows(weights, batch: int):
-    """(stride, width) of a [batch, W] float32 tensor with contiguous rows."""
-    import torch
-    if weights.dtype is not torch.float32:
-        raise ValueError(f"weights must be float32, got {str(weights.dtype).replace('torch.', '')}")
-    if weights.dim() != 2 or weights.shape[0] != batch:
-        raise ValueError(f"weights must have shape [{batch}, *], got {tuple(weights.shape)}")
-    width = weights.shape[1]
-    stride, inner = weights.stride()
-    if width > 1 and inner != 1:
-        raise ValueError(f"weights' last dimension must be contiguous, got strides {weights.stride()}")
-    return (width if batch <= 1 else stride), width
-
-
-def _status(status):
-    import torch
-    if status is None:
-        return None
-    _dense(status, "status", torch.int32, (1,))
-    return status.data_ptr()
 
 
 def key_weights(q_abs, q_pe, cache, block_table, seq_lens, lse, weights, *, scale: float, query_start_loc=None,
@@ -639,23 +667,23 @@ def key_weights(q_abs, q_pe, cache, block_table, seq_lens, lse, weights, *, scal
     own block table and lengths.  decay 0 does not read the old weights.  Errors
     are OR-ed into ``status`` [1] int32."""
     import torch
-    i32 = torch.int32
-    _dense(q_abs, "q_abs", torch.bfloat16, (None, None, LKV))
-    T, N, _ = q_abs.shape
-    _dense(q_pe, "q_pe", torch.bfloat16, (T, N, ROPE))
+    i32, f32 = torch.int32, torch.float32
+    T, N = _query(q_abs, q_pe, torch.bfloat16)
     nb, ps, _ = _cache_checked(cache)
-    _dense(seq_lens, "seq_lens", i32, dims=1)
-    B = seq_lens.shape[0]
-    _dense(block_table, "block_table", i32, (B, None))
+    B = _vector(seq_lens, "seq_lens", i32)
+    pages = _table(block_table, "block_table", i32, B)[1]
+    _dense(lse, "lse", f32, (T, N))
+    stride, width = _weight_rows(weights, B, f32)
+    qsl = flag = None
     if query_start_loc is not None:
-        _dense(query_start_loc, "query_start_loc", i32, (B + 1,))
-    _dense(lse, "lse", torch.float32, (T, N))
-    stride, width = _weight_rows(weights, B)
-    flag = _status(status)
+        _vector(query_start_loc, "query_start_loc", i32, B + 1)
+        qsl = query_start_loc.data_ptr()
+    if status is not None:
+        _vector(status, "status", i32, 1)
+        flag = status.data_ptr()
     dev = _on_current_device(q_abs, q_pe, cache, block_table, seq_lens, lse, weights, query_start_loc, status)
     _check(load().mla_key_weights(q_abs.data_ptr(), q_pe.data_ptr(), cache.data_ptr(), nb, ps, _dtype_code(cache),
-                                  kv_scale, block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(), B,
-                                  None if query_start_loc is None else query_start_loc.data_ptr(), T, N, scale,
+                                  kv_scale, block_table.data_ptr(), pages, seq_lens.data_ptr(), B, qsl, T, N, scale,
                                   lse.data_ptr(), decay, weights.data_ptr(), stride, width, flag,
                                   _raw_stream(stream, dev)))
 
@@ -669,15 +697,17 @@ def evict_select(weights, seq_lens, keep, keep_lens, *, sinks: int = 0, recent: 
     ``keep_lens`` [B] int32 (which may be ``seq_lens`` itself) their number."""
     import torch
     i32 = torch.int32
-    _dense(seq_lens, "seq_lens", i32, dims=1)
-    B = seq_lens.shape[0]
-    _dense(keep, "keep", i32, (B, None))
-    _dense(keep_lens, "keep_lens", i32, (B,))
-    stride, width = _weight_rows(weights, B)
-    flag = _status(status)
+    B = _vector(seq_lens, "seq_lens", i32)
+    budget = _table(keep, "keep", i32, B)[1]
+    _vector(keep_lens, "keep_lens", i32, B)
+    stride, width = _weight_rows(weights, B, torch.float32)
+    flag = None
+    if status is not None:
+        _vector(status, "status", i32, 1)
+        flag = status.data_ptr()
     dev = _on_current_device(weights, seq_lens, keep, keep_lens, status)
-    _check(load().mla_evict_select(weights.data_ptr(), stride, width, seq_lens.data_ptr(), B, keep.shape[1], sinks,
-                                   recent, keep.data_ptr(), keep_lens.data_ptr(), flag, _raw_stream(stream, dev)))
+    _check(load().mla_evict_select(weights.data_ptr(), stride, width, seq_lens.data_ptr(), B, budget, sinks, recent,
+                                   keep.data_ptr(), keep_lens.data_ptr(), flag, _raw_stream(stream, dev)))
 
 
 def cache_compact(cache, block_table, keep, keep_lens, *, weights=None, status=None, stream=None) -> None:
@@ -688,19 +718,20 @@ def cache_compact(cache, block_table, keep, keep_lens, *, weights=None, status=N
     import torch
     i32 = torch.int32
     nb, ps, _ = _cache_checked(cache)
-    _dense(keep_lens, "keep_lens", i32, dims=1)
-    B = keep_lens.shape[0]
-    _dense(keep, "keep", i32, (B, None))
-    _dense(block_table, "block_table", i32, (B, None))
-    stride, width, at = 0, 0, None
+    B = _vector(keep_lens, "keep_lens", i32)
+    most = _table(keep, "keep", i32, B)[1]
+    pages = _table(block_table, "block_table", i32, B)[1]
+    stride, width, at, flag = 0, 0, None, None
     if weights is not None:
-        stride, width = _weight_rows(weights, B)
+        stride, width = _weight_rows(weights, B, torch.float32)
         at = weights.data_ptr()
-    flag = _status(status)
+    if status is not None:
+        _vector(status, "status", i32, 1)
+        flag = status.data_ptr()
     dev = _on_current_device(cache, block_table, keep, keep_lens, weights, status)
-    _check(load().mla_cache_compact(cache.data_ptr(), nb, ps, _dtype_code(cache), block_table.data_ptr(),
-                                    block_table.shape[1], keep.data_ptr(), keep.shape[1], keep_lens.data_ptr(), B, at,
-                                    stride, width, flag, _raw_stream(stream, dev)))
+    _check(load().mla_cache_compact(cache.data_ptr(), nb, ps, _dtype_code(cache), block_table.data_ptr(), pages,
+                                    keep.data_ptr(), most, keep_lens.data_ptr(), B, at, stride, width, flag,
+                                    _raw_stream(stream, dev)))
 
 
 def gather_cache(cache, block_table, cu_seq_lens, dst, seq_starts=None, kv_scale: float = 1.0, status=None,

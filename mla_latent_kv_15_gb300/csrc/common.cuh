@@ -29,7 +29,7 @@ struct PlanHeader {
   int total_tiles;
   int tiles_per_cluster;
   int own_groups;    // mla_decode_shared: groups before this one are prefixes' (else 0)
-  int pad;
+  int own_rows;      // and the most rows that a group from there on has
 };
 
 struct GroupRec {    // 32 bytes

@@ -149,12 +149,13 @@ __global__ void __launch_bounds__(256, 2) combine_kernel(const DecodeArgs a) {
 // prefix keys) are left.
 __global__ void __launch_bounds__(256, 2) combine_shared_kernel(const DecodeArgs a) {
   const Plan& P = a.plan;
-  constexpr int kQuads = kRows / 4;
   constexpr int kFew = 4;             // partials whose loads are all in flight at once
   constexpr int kChunks = kLkv / 32;
   const int VG = (int)gridDim.x * 4;
-  const int first = P.header->own_groups * kQuads, items = P.header->num_groups * kQuads;
-  const int own_groups = P.header->own_groups;
+  const PlanHeader head = *P.header;
+  const int own_groups = head.own_groups;
+  const int quads = (head.own_rows + 3) / 4;   // of a group: as many as the largest has
+  const int first = own_groups * quads, items = head.num_groups * quads;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out);
@@ -162,9 +163,9 @@ __global__ void __launch_bounds__(256, 2) combine_shared_kernel(const DecodeArgs
   const int d0 = sub * 8;
   const int quad_row = (threadIdx.x >> 4) & 3;
   for (int item = first + (int)blockIdx.x * 4 + (int)(threadIdx.x >> 6); item < items; item += VG) {
-    const GroupRec gr = P.groups[item / kQuads];
-    const int2 behind = P.behind[item / kQuads];
-    const int r = (item % kQuads) * 4 + quad_row;
+    const GroupRec gr = P.groups[item / quads];
+    const int2 behind = P.behind[item / quads];
+    const int r = (item % quads) * 4 + quad_row;
     if (r >= gr.nrows || gr.row0 + r >= a.total_rows) continue;
     const int R = gr.row0 + r;
     // the row among its prefix's rows

@@ -129,6 +129,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* __res
     }
   }
   __shared__ int s_flags;
+  __shared__ int s_own_rows;
   __shared__ int s_span[kMaxClusters + 1];   // first axis position of every span
   __shared__ GroupRec s_groups[kStaged ? kPlanSmemGroups : 1];
   __shared__ int s_ucl[kStaged ? kPlanSmemUnits : 1];
@@ -147,7 +148,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* __res
   // the decode kernel may launch now: its prologue (barriers, TMEM, cluster
   // sync) overlaps the plan; it waits for this grid before reading the plan
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (tid == 0) s_flags = 0;
+  if (tid == 0) s_flags = s_own_rows = 0;
   __syncthreads();
   const long long kv_cap = (long long)max_pages * page_size;
   const int gshift = __ffs(GR) - 1;   // GR is a power of two
@@ -218,6 +219,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* __res
     int total;
     const int gb = block_excl_scan(ng, &total, s_sums, sums_row) + carry;
     if (b < batch && ng > 0) {
+      if (kShared) atomicMax(&s_own_rows, min(GR, sq * N));
       if (seq > kv_cap) {
         atomicOr(&s_flags, 2);  // MLA_DEVERR_BAD_SEQ_LEN
         seq = kv_cap;
@@ -405,7 +407,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* __res
     h.total_tiles = T;
     h.tiles_per_cluster = W;
     h.own_groups = own_groups;
-    h.pad = 0;
+    h.own_rows = kShared ? s_own_rows : 0;
     *P.header = h;
   }
 }
