@@ -130,12 +130,6 @@ size_t mla_decode_workspace_size(int batch, int total_q, int num_heads, int max_
 
 namespace {
 
-// Whether the prefixes of a mla_decode_shared get the kernel that scores many
-// rows at once, or go with the requests through the decode kernel.
-bool split_prefixes(const mla::SharedArgs& shared, int cache_dtype, int page_size, int64_t rows) {
-  return cache_dtype == MLA_BF16 && rows >= 512 && (int64_t)shared.max_pages * page_size >= 2048;
-}
-
 // The decode of mla_decode (q8 == nullptr: bf16 q_abs and q_pe), of
 // mla_decode_fp8q (q8: e4m3 [q_abs | q_pe] rows with q_scale, e4m3 cache) and
 // of mla_decode_shared (shared: the prefixes, with their block table).
@@ -180,19 +174,10 @@ int decode_impl(const void* q_abs, const void* q_pe, const void* q8, float q_sca
   if (!std::isfinite(scale) || scale == 0.f) return fail(MLA_ERR_INVALID_ARG, "scale must be finite and nonzero");
   if (num_splits < 0 || num_splits > 4096) return fail(MLA_ERR_INVALID_ARG, "num_splits must be in [0, 4096]");
 
-  mla::WorkspaceLayout L{};
-  mla::SharedLayout SL{};
-  // prefixes have a kernel of their own where their rows and keys are many
-  const bool split = shared && split_prefixes(*shared, cache_dtype, page_size, (int64_t)total_q * num_heads);
-  if (shared) {
-    SL = mla::shared_layout(batch, total_q, num_heads, num_splits, shared->prefixes);
-    L = split ? SL.own : SL.joint;
-  } else {
-    L = mla::workspace_layout(batch, total_q, num_heads, num_splits);
-  }
-  const size_t need = shared ? SL.total : L.total;
-  if (workspace_bytes < need)
-    return fail(MLA_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu required", workspace_bytes, need);
+  const mla::WorkspaceLayout L =
+      mla::workspace_layout(batch, total_q, num_heads, num_splits, shared ? shared->prefixes : -1);
+  if (workspace_bytes < L.total)
+    return fail(MLA_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu required", workspace_bytes, L.total);
   const int sms = sm_count();
   if (sms < 2) return fail(MLA_ERR_CUDA, "cannot query the current device");
   const int clusters = sms / 2 < mla::kMaxClusters ? sms / 2 : mla::kMaxClusters;
@@ -243,17 +228,7 @@ int decode_impl(const void* q_abs, const void* q_pe, const void* q8, float q_sca
         mla::encode_tmap_2d(&tm_out, out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, mla::kLkv, rows, mla::kLkv * 2, 64, 32,
                             CU_TENSOR_MAP_SWIZZLE_128B) &&
         mla::encode_tmap_2d(&tm_part, plan.part_o, CU_TENSOR_MAP_DATA_TYPE_UINT16, mla::kLkv,
-                            (uint64_t)(L.max_units + (split ? SL.prefix.max_units : 0)) * mla::kRows, mla::kLkv * 2, 64, 32,
-                            CU_TENSOR_MAP_SWIZZLE_128B);
-  CUtensorMap tm_pq{}, tm_pk{}, tm_pv{};
-  if (split)
-    enc = enc &&
-          mla::encode_tmap_2d(&tm_pq, q_pe, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, mla::kRope, rows, mla::kRope * 2, 64, 64,
-                              CU_TENSOR_MAP_SWIZZLE_128B) &&
-          mla::encode_tmap_2d(&tm_pk, cache, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, mla::kDqk, kv_rows, mla::kDqk * 2, 64,
-                              page_size < 128 ? page_size : 128, CU_TENSOR_MAP_SWIZZLE_128B) &&
-          mla::encode_tmap_2d(&tm_pv, cache, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, mla::kDqk, kv_rows, mla::kDqk * 2, 64,
-                              kv_box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
+                            (uint64_t)L.max_units * mla::kRows, mla::kLkv * 2, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B);
   if (!enc) return fail(MLA_ERR_CUDA, "cuTensorMapEncodeTiled rejected a tensor layout");
 
   mla::DecodeArgs a{};
@@ -285,12 +260,6 @@ int decode_impl(const void* q_abs, const void* q_pe, const void* q8, float q_sca
   a.plan = plan;
   a.prefix_table = prefix_table;
   a.max_prefix_pages = shared ? shared->max_pages : 0;
-  a.prefix = split ? mla::plan_from_workspace(workspace, SL.prefix, SL.own.max_units) : plan;
-  mla::SharedArgs sh{};
-  if (shared) {
-    sh = *shared;
-    sh.first = reinterpret_cast<int2*>(static_cast<char*>(workspace) + L.first);
-  }
 
   cudaStream_t s = (cudaStream_t)stream;
   // small head counts with one query token per request (total_q == batch):
@@ -299,18 +268,15 @@ int decode_impl(const void* q_abs, const void* q_pe, const void* q8, float q_sca
   // Sq tokens gives ceil(Sq * N / 32) <= Sq groups.
   const int small_rows = !shared && !q8 && cache_dtype == MLA_BF16 && num_heads <= 32 && total_q == batch;
   const int variant = q8 ? 3 : (cache_dtype == MLA_FP8_E4M3 ? 1 : (small_rows ? 2 : 0));
-  cudaError_t e =
-      split    ? mla::launch_split_plan(seq_lens, query_start_loc, batch, num_heads, max_pages_per_seq, page_size,
-                                        num_splits, clusters, a.plan, a.prefix, sh, s)
-      : shared ? mla::launch_shared_plan(seq_lens, query_start_loc, batch, num_heads, max_pages_per_seq, page_size,
-                                         num_splits, clusters, a.plan, sh, s)
-               : mla::launch_plan(seq_lens, query_start_loc, batch, num_heads, max_pages_per_seq, page_size,
-                                  num_splits, clusters, small_rows ? 32 : mla::kRows, a.plan, write, quant, sms, s);
-  if (e == cudaSuccess && split) e = mla::launch_prefix(tm_q, tm_pq, tm_pk, tm_pv, a, clusters, s);
+  cudaError_t e = shared ? mla::launch_shared_plan(seq_lens, query_start_loc, batch, num_heads, max_pages_per_seq,
+                                                   page_size, num_splits, clusters, a.plan, *shared, s)
+                         : mla::launch_plan(seq_lens, query_start_loc, batch, num_heads, max_pages_per_seq, page_size,
+                                            num_splits, clusters, small_rows ? 32 : mla::kRows, a.plan, write, quant,
+                                            sms, s);
   if (e != cudaSuccess) return cuda_fail(e, "plan launch");
   const bool timed = g_timing_start && g_timing_stop;
   if (timed && (e = cudaEventRecord(g_timing_start, s)) != cudaSuccess) return cuda_fail(e, "timing event");
-  e = shared ? mla::launch_decode_shared(tm_q, tm_qr, tm_kv, tm_kvr, tm_out, tm_part, variant, split, a, clusters, s)
+  e = shared ? mla::launch_decode_shared(tm_q, tm_qr, tm_kv, tm_kvr, tm_out, tm_part, variant, a, clusters, s)
              : mla::launch_decode(tm_q, tm_qr, tm_kv, tm_kvr, tm_out, tm_part, variant, a, clusters, s);
   if (e != cudaSuccess) return cuda_fail(e, "decode launch");
   if (timed && (e = cudaEventRecord(g_timing_stop, s)) != cudaSuccess) return cuda_fail(e, "timing event");
@@ -835,7 +801,7 @@ int mla_prefill_status(const void* workspace, int* status, void* stream) {
 
 size_t mla_decode_shared_workspace_size(int batch, int prefixes, int total_q, int num_heads, int max_splits) {
   if (batch <= 0 || prefixes <= 0 || total_q <= 0 || num_heads <= 0 || max_splits < 0) return 0;
-  return mla::shared_layout(batch, total_q, num_heads, max_splits, prefixes).total;
+  return mla::workspace_layout(batch, total_q, num_heads, max_splits, prefixes).total;
 }
 
 int mla_decode_shared(const void* q_abs, const void* q_pe, const void* cache, int64_t num_blocks, int page_size,
@@ -871,7 +837,7 @@ int mla_decode_shared(const void* q_abs, const void* q_pe, const void* cache, in
     return fail(MLA_ERR_UNSUPPORTED, "total_q * num_heads must be below 2^30");
   if (2 * (rows / mla::kRows + batch + 2) * (num_splits > 1 ? num_splits : 1) * mla::kRows >= (int64_t)1 << 31)
     return fail(MLA_ERR_UNSUPPORTED, "total_q * num_heads * num_splits is too large");
-  const mla::SharedLayout L = mla::shared_layout(batch, total_q, num_heads, num_splits, prefixes);
+  const mla::WorkspaceLayout L = mla::workspace_layout(batch, total_q, num_heads, num_splits, prefixes);
   const int esize = cache_dtype == MLA_FP8_E4M3 ? 1 : 2;
   const Extent outputs[] = {dense(out, rows * mla::kLkv * 2), dense(lse, rows * 4), dense(workspace, (int64_t)L.total)};
   const Extent inputs[] = {dense(q_abs, rows * mla::kLkv * 2),
@@ -885,7 +851,7 @@ int mla_decode_shared(const void* q_abs, const void* q_pe, const void* cache, in
                            dense(query_start_loc, (batch + 1LL) * 4)};
   if (num_blocks > 0 && num_blocks < (1LL << 31) && any_overlap(outputs, 3, inputs, 9))
     return fail(MLA_ERR_INVALID_ARG, "out, lse and the workspace must not overlap each other or the inputs");
-  const mla::SharedArgs sh{prefix_lens, prefix_requests, prefixes, max_prefix_pages, total_q, nullptr};
+  const mla::SharedArgs sh{prefix_lens, prefix_requests, prefixes, max_prefix_pages, total_q};
   return decode_impl(q_abs, q_pe, nullptr, 0.f, cache, num_blocks, page_size, cache_dtype, kv_scale, block_table,
                      max_pages_per_seq, seq_lens, batch, query_start_loc, total_q, num_heads, scale, num_splits, out,
                      lse, workspace, workspace_bytes, stream, nullptr, nullptr, &sh, prefix_table);

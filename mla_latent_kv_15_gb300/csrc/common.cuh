@@ -16,7 +16,6 @@ constexpr int kRope = 64;          // decoupled rope width (k_pe, q_pe)
 constexpr int kDqk = kLkv + kRope; // cache row width
 constexpr int kRows = 128;         // query rows per work unit (tcgen05 M)
 constexpr int kTile = 64;          // keys per tile (S MMA N, P.V MMA K)
-constexpr int kPrefixTile = 256;   // keys per tile of the prefixes' kernel
 constexpr int kMaxClusters = 128;  // upper bound of CTA pairs in the decode grid
 
 // Work-unit plan written by the scheduler kernel into the workspace.
@@ -73,81 +72,42 @@ struct Plan {
   // mla_decode_shared: of each group of a request's own keys, the first group
   // of its prefix and that group's first query row
   int2* behind;          // [max_groups]
-  int* redo;             // prefixes' kernel: [max_units] whether the decode kernel does the unit again
-  int slot0;             // partial-result slot of unit 0
   int max_groups;
   int max_units;
 };
 
 struct WorkspaceLayout {
-  size_t header, groups, units, unit_cluster, cluster_begin, part_o, part_scale, part_lse, behind, first, redo, total;
+  size_t header, groups, units, unit_cluster, cluster_begin, part_o, part_scale, part_lse, behind, total;
   int max_groups, max_units;
 };
 
-inline size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
-
-// The most groups of 128 rows that `sources` (requests or prefixes) cut all rows into.
-inline long long most_groups(long long rows, long long sources) { return (rows + 127LL * sources) / kRows + 1; }
-
-// Places of a plan of at most `mg` groups and `mu` units from `off` on, without the partials.
-inline size_t place_plan(WorkspaceLayout& L, size_t off, long long mg, long long mu) {
+// Byte offsets of each plan array for a batch shape (host and device agree);
+// prefixes: of mla_decode_shared, whose groups cover every row a second time
+// (-1: a plain decode).
+inline WorkspaceLayout workspace_layout(int batch, int total_q, int num_heads, int max_splits, int prefixes = -1) {
+  auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+  WorkspaceLayout L{};
+  long long rows = (long long)total_q * num_heads;
+  long long mg = (rows + 127LL * batch) / kRows + 1;
+  if (prefixes >= 0) mg += (rows + 127LL * prefixes) / kRows + 1;
+  long long mu = mg * (max_splits > 1 ? max_splits : 1) + kMaxClusters;
   L.max_groups = (int)mg;
   L.max_units = (int)mu;
-  L.header = off;        off = up256(off + sizeof(PlanHeader));
-  L.groups = off;        off = up256(off + sizeof(GroupRec) * (size_t)mg);
-  L.units = off;         off = up256(off + sizeof(UnitRec) * (size_t)mu);
-  L.unit_cluster = off;  off = up256(off + sizeof(int) * (size_t)mu);
-  L.cluster_begin = off; off = up256(off + sizeof(int) * (kMaxClusters + 1));
-  return off;
-}
-inline size_t place_partials(WorkspaceLayout& L, size_t off, size_t slots) {
-  L.part_o = off;        off = up256(off + sizeof(uint16_t) * slots * kRows * kLkv);
-  L.part_scale = off;    off = up256(off + sizeof(float) * slots * kRows * (kLkv / 32));
-  L.part_lse = off;      off = up256(off + sizeof(float) * slots * kRows);
-  return off;
-}
-
-// Byte offsets of each plan array for a batch shape (host and device agree).
-inline WorkspaceLayout workspace_layout(int batch, int total_q, int num_heads, int max_splits) {
-  WorkspaceLayout L{};
-  const long long mg = most_groups((long long)total_q * num_heads, batch);
-  const long long mu = mg * (max_splits > 1 ? max_splits : 1) + kMaxClusters;
-  L.total = place_partials(L, place_plan(L, 0, mg, mu), (size_t)mu);
+  size_t off = 0;
+  L.header = off;        off = up(off + sizeof(PlanHeader));
+  L.groups = off;        off = up(off + sizeof(GroupRec) * (size_t)mg);
+  L.units = off;         off = up(off + sizeof(UnitRec) * (size_t)mu);
+  L.unit_cluster = off;  off = up(off + sizeof(int) * (size_t)mu);
+  L.cluster_begin = off; off = up(off + sizeof(int) * (kMaxClusters + 1));
+  L.part_o = off;        off = up(off + sizeof(uint16_t) * (size_t)mu * kRows * kLkv);
+  L.part_scale = off;    off = up(off + sizeof(float) * (size_t)mu * kRows * (kLkv / 32));
+  L.part_lse = off;      off = up(off + sizeof(float) * (size_t)mu * kRows);
+  L.behind = off;        if (prefixes >= 0) off = up(off + sizeof(int2) * (size_t)mg);
+  L.total = off;
   return L;
 }
 
-// The same for mla_decode_shared, where the prefixes' groups cover every row a
-// second time: on one axis with the requests' (joint), or in a plan of their
-// own (prefix) beside that of the requests (own, whose status word is the
-// call's), with the partials of both in one array.  Whichever it is has the
-// whole workspace.
-struct SharedLayout {
-  WorkspaceLayout joint, own, prefix;
-  size_t total;
-};
-inline SharedLayout shared_layout(int batch, int total_q, int num_heads, int max_splits, int prefixes) {
-  SharedLayout S{};
-  const long long rows = (long long)total_q * num_heads, k = max_splits > 1 ? max_splits : 1;
-  const long long go = most_groups(rows, batch), gp = most_groups(rows, prefixes);
-  const long long uo = go * k + kMaxClusters, up = gp * k + kMaxClusters;
-  WorkspaceLayout& J = S.joint;
-  size_t off = place_partials(J, place_plan(J, 0, go + gp, (go + gp) * k + kMaxClusters), (size_t)((go + gp) * k + kMaxClusters));
-  J.behind = off;        off = up256(off + sizeof(int2) * (size_t)(go + gp));
-  J.first = off;         off = up256(off + sizeof(int2) * (size_t)prefixes);
-  J.total = off;
-  WorkspaceLayout &O = S.own, &X = S.prefix;
-  off = place_plan(X, place_plan(O, 0, go, uo), gp, up);
-  off = place_partials(O, off, (size_t)(uo + up));
-  X.part_o = O.part_o, X.part_scale = O.part_scale, X.part_lse = O.part_lse;
-  O.behind = off;        off = up256(off + sizeof(int2) * (size_t)go);
-  O.first = off;         off = up256(off + sizeof(int2) * (size_t)prefixes);
-  X.redo = off;          off = up256(off + sizeof(int) * (size_t)up);
-  O.total = X.total = off;
-  S.total = J.total > off ? J.total : off;
-  return S;
-}
-
-inline Plan plan_from_workspace(void* ws, const WorkspaceLayout& L, int slot0 = 0) {
+inline Plan plan_from_workspace(void* ws, const WorkspaceLayout& L) {
   char* p = static_cast<char*>(ws);
   Plan P;
   P.header = reinterpret_cast<PlanHeader*>(p + L.header);
@@ -159,8 +119,6 @@ inline Plan plan_from_workspace(void* ws, const WorkspaceLayout& L, int slot0 = 
   P.part_scale = reinterpret_cast<float*>(p + L.part_scale);
   P.part_lse = reinterpret_cast<float*>(p + L.part_lse);
   P.behind = reinterpret_cast<int2*>(p + L.behind);
-  P.redo = reinterpret_cast<int*>(p + L.redo);
-  P.slot0 = slot0;
   P.max_groups = L.max_groups;
   P.max_units = L.max_units;
   return P;
@@ -186,11 +144,8 @@ struct DecodeArgs {
   unsigned long long wait_limit_ns;   // bound of every on-chip wait (1 s)
   int debug_skip_tile;      // test aid: CTA 0 of cluster 0 never loads its first cache tile
   Plan plan;
-  // mla_decode_shared: the prefixes' block table, and the plan that holds their
-  // groups (their own, or `plan` where they are on its axis)
-  const int32_t* prefix_table;
+  const int32_t* prefix_table;   // mla_decode_shared: block table of the prefixes
   int max_prefix_pages;
-  Plan prefix;
 };
 
 // The shared prefixes of mla_decode_shared: requests begin[g] .. begin[g+1] - 1
@@ -201,7 +156,6 @@ struct SharedArgs {
   int prefixes;
   int max_pages;
   int total_q;
-  int2* first;              // [prefixes], written by the plan: first group and first query row of each
 };
 
 // mla_key_weights: the sum over a request's query rows of exp(score - lse),
@@ -364,10 +318,6 @@ cudaError_t launch_plan(const int32_t* seq_lens, const int32_t* qsl, int batch, 
 cudaError_t launch_shared_plan(const int32_t* seq_lens, const int32_t* qsl, int batch, int num_heads, int max_pages,
                                int page_size, int num_splits, int num_clusters, Plan plan, const SharedArgs& shared,
                                cudaStream_t s);
-// two plans: the requests' own, and the prefixes' (in tiles of kPrefixTile keys)
-cudaError_t launch_split_plan(const int32_t* seq_lens, const int32_t* qsl, int batch, int num_heads, int max_pages,
-                              int page_size, int num_splits, int num_clusters, const Plan& own, const Plan& prefix,
-                              const SharedArgs& shared, cudaStream_t s);
 // variant: 0 bf16 cache, 1 e4m3 cache, 2 bf16 cache with <= 32-row groups
 // (plan built with group_rows = 32), 3 e4m3 query and e4m3 cache.  Tensor
 // maps: the query's latent columns (64-dim boxes; 128-dim e4m3 boxes for
@@ -378,18 +328,10 @@ cudaError_t launch_split_plan(const int32_t* seq_lens, const int32_t* qsl, int b
 cudaError_t launch_decode(const CUtensorMap& tm_q, const CUtensorMap& tm_qr, const CUtensorMap& tm_kv,
                           const CUtensorMap& tm_kvr, const CUtensorMap& tm_out, const CUtensorMap& tm_part,
                           int variant, const DecodeArgs& a, int num_clusters, cudaStream_t s);
-// the same for a plan of launch_shared_plan (variants 0 and 1); `split`: for
-// those of launch_split_plan, with the prefixes' units that their kernel left
-// to be done again (bf16 cache)
+// the same for a plan of launch_shared_plan (variants 0 and 1)
 cudaError_t launch_decode_shared(const CUtensorMap& tm_q, const CUtensorMap& tm_qr, const CUtensorMap& tm_kv,
                                  const CUtensorMap& tm_kvr, const CUtensorMap& tm_out, const CUtensorMap& tm_part,
-                                 int variant, int split, const DecodeArgs& a, int num_clusters, cudaStream_t s);
-// The units of a.prefix (a plan of launch_split_plan) on a bf16 cache.  Tensor
-// maps: the query's latent and rope rows (boxes of 64 columns x 64 rows), the
-// cache's rows (64 columns x min(page, 128) rows for the keys, x min(page, 64)
-// for the values), all 128-B swizzled.
-cudaError_t launch_prefix(const CUtensorMap& tm_q, const CUtensorMap& tm_qr, const CUtensorMap& tm_k,
-                          const CUtensorMap& tm_v, const DecodeArgs& a, int num_clusters, cudaStream_t s);
+                                 int variant, const DecodeArgs& a, int num_clusters, cudaStream_t s);
 cudaError_t launch_combine_shared(const DecodeArgs& a, int max_groups, int sm_count, cudaStream_t s);
 // Tensor maps: query rows (q_abs, q_pe; boxes of 64 columns x a.row_tile / 2
 // rows, 128-B swizzle), cache rows (bf16: 64 x min(page, 128), 128-B swizzle;

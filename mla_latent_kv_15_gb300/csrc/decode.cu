@@ -378,10 +378,8 @@ __device__ __forceinline__ void expand_e4m3_tile(uint32_t stage, int t, int live
   }
 }
 
-// kShared: 1 a plan of launch_shared_plan, in whose units b < 0 is prefix ~b; 2
-// those of launch_split_plan: before a pair's own units, the units that the
-// prefixes' kernel left to be done again.
-template <int kVariant, int kShared = 0>
+// kShared: a plan of launch_shared_plan, in whose units b < 0 is prefix ~b.
+template <int kVariant, bool kShared = false>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kThreads, 1)
     decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_qr,
                   const __grid_constant__ CUtensorMap tm_kv, const __grid_constant__ CUtensorMap tm_kvr,
@@ -396,7 +394,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kTh
   // the P.V issuer's warp zeroes the value rows behind a unit's last key: their
   // probabilities are zero, but what a page holds there may be infinite or NaN
   // (an e4m3 tile's are zeroed as it is expanded)
-  constexpr bool kCleans = kShared != 0 && !kCacheFp8;
+  constexpr bool kCleans = kShared && !kCacheFp8;
   constexpr int kStages = Layout<kVariant>::kStages;
   constexpr int kXBytes = Layout<kVariant>::kXBytes;
   constexpr int kXRows = Layout<kVariant>::kXRows;
@@ -453,24 +451,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kTh
   // the combine kernel may launch now (its blocks take SMs as CTAs of this
   // grid finish; it waits for the whole grid before reading the partials)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  // units ubeg..uend - 1, of which those before `own_beg` are prefixes' (kShared 2)
-  const int own_beg = P.cluster_begin[cluster], uend = P.cluster_begin[cluster + 1];
-  const int pre_end = kShared == 2 ? a.prefix.cluster_begin[cluster + 1] : 0;
-  const int ubeg = kShared == 2 ? own_beg - (pre_end - a.prefix.cluster_begin[cluster]) : own_beg;
-  // unit u, or whether there is nothing to do for it
-  auto get_unit = [&](int u, UnitRec& ur) {
-    if (kShared == 2 && u < own_beg) {
-      const int at = pre_end - (own_beg - u);
-      if (!a.prefix.redo[at]) return false;
-      ur = a.prefix.units[at];
-      // (in tiles of the prefixes' kernel)
-      ur.tile_begin *= kPrefixTile / kTile;
-      ur.tile_end = min(ur.tile_end * (kPrefixTile / kTile), (ur.lmax + kTile - 1) / kTile);
-      return true;
-    }
-    ur = P.units[u];
-    return true;
-  };
+  const int ubeg = P.cluster_begin[cluster];
+  const int uend = P.cluster_begin[cluster + 1];
 
   // Role bodies; the dispatch below differs per cache type: with an e4m3
   // cache each warpgroup first sets its register budget, so the compiler
@@ -493,12 +475,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kTh
       // split-KV partials, queries and block tables stay in L2
       const uint64_t pol_once = l2_policy_evict_first();
       // (a prefix's are read by every group of rows behind it)
-      const uint64_t pol_again = kShared != 0 ? l2_policy_evict_last() : 0;
+      const uint64_t pol_again = kShared ? l2_policy_evict_last() : 0;
       for (int u = ubeg; u < uend; ++u) {
-        UnitRec ur;
-        if (!get_unit(u, ur)) continue;
+        const UnitRec ur = P.units[u];
         const UnitRec& gr = ur;
-        const bool prefix = kShared != 0 && gr.b < 0;
+        const bool prefix = kShared && gr.b < 0;
         const int32_t* bt =
             prefix ? a.prefix_table + (size_t)~gr.b * a.max_prefix_pages : a.block_table + (size_t)gr.b * a.max_pages;
         const int max_pages = prefix ? a.max_prefix_pages : a.max_pages;
@@ -553,7 +534,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kTh
           // test aid: CTA 0 of cluster 0 never loads its first cache tile, so
           // a consumer's bounded wait for it runs out (kShared: the plan's
           // first unit, whichever cluster has it)
-          if (a.debug_skip_tile && (kShared ? u == 0 && u >= own_beg : cluster == 0 && u == ubeg) && rank == 0 && jj == 0) continue;
+          if (a.debug_skip_tile && (kShared ? u == 0 : cluster == 0 && u == ubeg) && rank == 0 && jj == 0) continue;
           const uint32_t slot = item % kStages, round = item / kStages;
           {
             // The block-table lookups precede the slot wait, so their
@@ -627,12 +608,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kTh
       const uint32_t d = tbase + kTmemS;
       const uint32_t qa = tbase + kTmemQ;      // latent box p, 16-dim step k: column p*32 + k*8; rope: 128 + k*8
       uint32_t item = 0, it = 0, units_done = 0;
-      for (int u = ubeg; u < uend; ++u) {
-        UnitRec ur;
-        if (!get_unit(u, ur)) continue;
+      for (int u = ubeg; u < uend; ++u, ++units_done) {
+        const UnitRec ur = P.units[u];
         const int ntiles = ur.tile_end - ur.tile_begin;
         item += 2;  // query items are consumed by the softmax warps
-        wait_bar(ctx, &bars->q_ready, units_done++ & 1);
+        wait_bar(ctx, &bars->q_ready, units_done & 1);
         if constexpr (kQ8) {
           // the query items' slots get their kx_free phase too (after every
           // earlier MMA, like the tile items' commits)
@@ -692,8 +672,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kTh
       constexpr uint64_t kStageDesc = kStageBytes >> 4;
       uint32_t item = 0, it = 0;
       for (int u = ubeg; u < uend; ++u) {
-        UnitRec ur;
-        if (!get_unit(u, ur)) continue;
+        const UnitRec ur = P.units[u];
         const int ntiles = ur.tile_end - ur.tile_begin;
         item += 2;
         for (int jj = 0; jj < ntiles; ++jj, ++item, ++it) {
@@ -735,8 +714,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kTh
     const int te = threadIdx.x - 32 * kWarpExpand0;   // 0..127
     uint32_t item = 0;
     for (int u = ubeg; u < uend; ++u) {
-      UnitRec ur;
-      if (!get_unit(u, ur)) continue;
+      const UnitRec ur = P.units[u];
       const int ntiles = ur.tile_end - ur.tile_begin;
       item += 2;  // the query items are loaded by the producer
       for (int jj = 0; jj < ntiles; ++jj, ++item) {
@@ -770,7 +748,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kTh
             sts128(rowa + (((c0 + 1) ^ (r & 7)) << 4), o[4], o[5], o[6], o[7]);
           }
         } else {
-          expand_e4m3_tile<kShared != 0>(smem_u32(stages + slot * kStageBytes), te,
+          expand_e4m3_tile<kShared>(smem_u32(stages + slot * kStageBytes), te,
                                     ur.lmax - (ur.tile_begin + jj) * kTile);
         }
         fence_proxy_async_smem();    // bf16 writes visible to the MMAs
@@ -929,14 +907,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kTh
     // A unit's record is one 32-byte line; the epilogue of the unit before
     // prefetches it into L1, so the load at the unit's start is short.
     auto prefetch_unit = [&](int u) {
-      if (kShared != 2 || u >= own_beg) asm volatile("prefetch.global.L1 [%0];" ::"l"(P.units + u));
+      asm volatile("prefetch.global.L1 [%0];" ::"l"(P.units + u));
     };
     if (ubeg < uend) prefetch_unit(ubeg);
 
     uint32_t item = 0, it = 0, units_done = 0;
-    for (int u = ubeg; u < uend; ++u) {
-      UnitRec ur;
-      if (!get_unit(u, ur)) continue;
+    for (int u = ubeg; u < uend; ++u, ++units_done) {
+      const UnitRec ur = P.units[u];
       const UnitRec& gr = ur;
       nrows_cur = gr.nrows;
       const int R = gr.row0 + row;
@@ -1168,7 +1145,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kTh
       psum[hh * kRows + row] = l;
       named_bar_pair(q4);
       const float lt = l + psum[(1 - hh) * kRows + row];
-      wait_bar(ctx, &bars->o_full, units_done++ & 1);
+      wait_bar(ctx, &bars->o_full, units_done & 1);
       __syncwarp();
       tc_fence_after();
       const float inv = lt > 0.f ? a.out_scale / lt : 0.f;
@@ -1406,9 +1383,9 @@ cudaError_t launch_decode(const CUtensorMap& tm_q, const CUtensorMap& tm_qr, con
 
 cudaError_t launch_decode_shared(const CUtensorMap& tm_q, const CUtensorMap& tm_qr, const CUtensorMap& tm_kv,
                                  const CUtensorMap& tm_kvr, const CUtensorMap& tm_out, const CUtensorMap& tm_part,
-                                 int variant, int split, const DecodeArgs& a, int num_clusters, cudaStream_t s) {
-  return launch(split ? decode_kernel<0, 2> : (variant == 1 ? decode_kernel<1, 1> : decode_kernel<0, 1>), tm_q, tm_qr,
-                tm_kv, tm_kvr, tm_out, tm_part, split ? 0 : variant, a, num_clusters, s);
+                                 int variant, const DecodeArgs& a, int num_clusters, cudaStream_t s) {
+  return launch(variant == 1 ? decode_kernel<1, true> : decode_kernel<0, true>, tm_q, tm_qr, tm_kv, tm_kvr, tm_out,
+                tm_part, variant, a, num_clusters, s);
 }
 
 }  // namespace mla

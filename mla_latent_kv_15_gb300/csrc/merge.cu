@@ -152,16 +152,12 @@ __global__ void __launch_bounds__(256, 2) combine_shared_kernel(const DecodeArgs
   constexpr int kFew = 4;             // partials whose loads are all in flight at once
   constexpr int kChunks = kLkv / 32;
   const int VG = (int)gridDim.x * 4;
-  const Plan& X = a.prefix;           // holds the prefixes' groups
   const PlanHeader head = *P.header;
-  const int pre_groups = X.header->num_groups;
+  const int own_groups = head.own_groups;
   const int quads = (head.own_rows + 3) / 4;   // of a group: as many as the largest has
-  const int first = head.own_groups * quads, items = head.num_groups * quads;
+  const int first = own_groups * quads, items = head.num_groups * quads;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  // the call's error word is that of the requests' plan
-  if (X.header != P.header && blockIdx.x == 0 && threadIdx.x == 0 && X.header->status)
-    atomicOr(&P.header->status, X.header->status);
   __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out);
   const int sub = threadIdx.x & 15;
   const int d0 = sub * 8;
@@ -176,9 +172,9 @@ __global__ void __launch_bounds__(256, 2) combine_shared_kernel(const DecodeArgs
     const int pr = R - behind.y, pg = behind.x + pr / kRows;
     int pre = 0;
     size_t pre_at = 0;
-    if (pg < pre_groups) {
-      pre = X.groups[pg].pieces;
-      pre_at = (size_t)(X.slot0 + X.groups[pg].ubase) * kRows + pr % kRows;
+    if (pg < own_groups) {
+      pre = P.groups[pg].pieces;
+      pre_at = (size_t)P.groups[pg].ubase * kRows + pr % kRows;
     }
     const int n = gr.pieces + pre;
     if (pre == 0 && gr.pieces == 1) continue;   // written by the decode kernel

@@ -17,10 +17,9 @@
 // Pieces of a split group write partials that the combine kernel merges
 // with the LSE rule of merge_attn_states.
 //
-// For mla_decode_shared the prefixes are sources of groups of their own: the
-// rows of all requests behind a prefix, together, over the prefix's keys, every
-// one of which every row sees.  Either on one axis with the requests, before
-// them, or in a plan of their own for the prefixes' kernel.
+// For mla_decode_shared (kShared) the prefixes come before the requests, as
+// sources of groups of their own: the rows of all requests behind a prefix,
+// together, over the prefix's keys, every one of which every row sees.
 #include "cache_rows.cuh"
 #include "common.cuh"
 
@@ -50,8 +49,6 @@ constexpr int kPlanSmemGroups = 1024;   // staged plans: at most this many group
 // pairs starting more groups get fewer real tiles.
 constexpr int kUnitCostTiles = 3;
 constexpr int kPlanSmemUnits = 2048;    // and units
-// The same cost of a unit of the prefixes' kernel in its tiles of 256 keys.
-constexpr int kPrefixCostTiles = 2;
 
 // Exclusive scan over the block (blockDim.x == kPlanThreads) with one
 // barrier: every warp scans its values and publishes its total; after the
@@ -96,40 +93,49 @@ __device__ __forceinline__ int muldiv(int a, int b, int c) {
   return (int)(p / (unsigned long long)c);
 }
 
-// What a plan's groups are made of: the requests of a plain decode; prefixes and
-// the requests behind them on one axis; prefixes alone, in the tiles of the
-// kernel that is theirs; the requests behind them alone.
-enum Source { kRequests, kJoint, kPrefixes, kOwn };
-
-template <bool kStaged>
-struct PlanShared {
-  int flags;
-  int own_rows;
-  int span[kMaxClusters + 1];   // first axis position of every span
-  GroupRec groups[kStaged ? kPlanSmemGroups : 1];
-  int ucl[kStaged ? kPlanSmemUnits : 1];
-  int kbase[kStaged ? kPlanSmemGroups : 1];   // seq_len - Sq + 1 - q0 of each group's request
-  int sums[2][kPlanThreads / 32];
-};
-
 // kStaged: the group records and unit clusters live in shared memory while
 // the plan is built (each phase reads what other threads wrote in the
 // previous one) and are copied out at the end; for plans that fit.
-template <bool kStaged, int kSource>
-__device__ __forceinline__ void build_plan(PlanShared<kStaged>& sm, const int32_t* __restrict__ seq_lens,
-                                           const int32_t* __restrict__ qsl, int batch, int N, int max_pages,
-                                           int page_size, int num_splits, int C, int GR, Plan P, const SharedArgs& sh) {
-  int& s_flags = sm.flags;
-  int& s_own_rows = sm.own_rows;
-  auto& s_span = sm.span;
-  auto& s_groups = sm.groups;
-  auto& s_ucl = sm.ucl;
-  auto& s_kbase = sm.kbase;
-  auto& s_sums = sm.sums;
+// kMode: blocks 1.. of the launch do the step's other small jobs while block
+// 0 builds the plan, so they cost the step no launch of their own: the new
+// cache rows (blocks 1 .. write_blocks, 8 tokens a block; 1 bf16 cache,
+// 2 e4m3 cache) and, in mode 3 (e4m3 cache), the query's quantisation (the
+// remaining blocks, grid-stride over its 8-value vectors).
+template <bool kStaged, int kMode, bool kShared = false>
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* __restrict__ seq_lens,
+                                                    const int32_t* __restrict__ qsl, int batch, int N,
+                                                    int max_pages, int page_size, int num_splits, int C,
+                                                    int GR, Plan P, const CacheWriteArgs w, const QuantArgs qa,
+                                                    int write_blocks, const SharedArgs sh) {
+  if constexpr (kMode != 0) {
+    if (blockIdx.x > 0) {
+      // as the cache-write kernel: wait for the kernel before, then let the
+      // next one launch (the decode waits for this whole grid)
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+      const int b = (int)blockIdx.x - 1;
+      if (b < write_blocks) {
+        const int64_t tok = b * 8LL + (threadIdx.x >> 5);
+        if (tok < w.num_tokens) write_cache_row<kMode >= 2>(w, tok, threadIdx.x & 31);
+        return;
+      }
+      if constexpr (kMode == 3) {
+        const int64_t nvec = qa.rows * (kDqk / 8);
+        const int64_t stride = (int64_t)(gridDim.x - 1 - write_blocks) * kPlanThreads;
+        for (int64_t v = (int64_t)(b - write_blocks) * kPlanThreads + threadIdx.x; v < nvec; v += stride)
+          quantize_query_vec(qa, v);
+      }
+      return;
+    }
+  }
+  __shared__ int s_flags;
+  __shared__ int s_own_rows;
+  __shared__ int s_span[kMaxClusters + 1];   // first axis position of every span
+  __shared__ GroupRec s_groups[kStaged ? kPlanSmemGroups : 1];
+  __shared__ int s_ucl[kStaged ? kPlanSmemUnits : 1];
+  __shared__ int s_kbase[kStaged ? kPlanSmemGroups : 1];   // seq_len - Sq + 1 - q0 of each group's request
+  __shared__ int s_sums[2][kPlanThreads / 32];
   int sums_row = 0;
-  constexpr int kTileKeys = kSource == kPrefixes ? kPrefixTile : kTile;
-  constexpr int kCost = kSource == kPrefixes ? kPrefixCostTiles : kUnitCostTiles;
-  constexpr bool kBehind = kSource == kJoint || kSource == kOwn;   // requests behind prefixes
   GroupRec* grp = kStaged ? s_groups : P.groups;
   int* ucl = kStaged ? s_ucl : P.unit_cluster;
   const int tid = threadIdx.x;
@@ -147,18 +153,15 @@ __device__ __forceinline__ void build_plan(PlanShared<kStaged>& sm, const int32_
   const long long kv_cap = (long long)max_pages * page_size;
   const int gshift = __ffs(GR) - 1;   // GR is a power of two
 
-  // 1. groups of every source: of the prefixes (b < 0 marks prefix ~b), then of
-  //    the requests
+  // 1. groups of every request (kShared: of every prefix, then of every
+  //    request; b < 0 marks prefix ~b)
   int carry = 0;
-  const int np = kSource == kRequests ? 0 : sh.prefixes;
-  int at_prefix = 0;                 // groups of prefixes so far (of kRows rows)
+  const int np = kShared ? sh.prefixes : 0;
   for (int base = 0; base < np; base += kPlanThreads) {
     const int p = base + tid;
     int ng = 0, q0 = 0, rows = 0;
-    long long keys = 0;
     if (p < np) {
       const int r0 = sh.begin[p], r1 = sh.begin[p + 1];
-      keys = sh.lens[p];
       const bool fits = r0 >= 0 && r0 <= r1 && r1 <= batch && (p > 0 || r0 == 0) && (p < np - 1 || r1 == batch);
       int q1 = 0;
       if (fits) {
@@ -170,13 +173,13 @@ __device__ __forceinline__ void build_plan(PlanShared<kStaged>& sm, const int32_
         q0 = q1 = 0;
       }
       rows = (q1 - q0) * N;
-      ng = (rows + kRows - 1) / kRows;
+      ng = (rows + GR - 1) >> gshift;
     }
     int total;
-    const int gb = block_excl_scan(ng, &total, s_sums, sums_row) + at_prefix;
-    if (kBehind && p < np) sh.first[p] = make_int2(gb, q0 * N);
-    if (kSource != kOwn && p < np && ng > 0) {
+    const int gb = block_excl_scan(ng, &total, s_sums, sums_row) + carry;
+    if (p < np && ng > 0) {
       const long long cap = (long long)sh.max_pages * page_size;
+      long long keys = sh.lens[p];
       if (keys > cap) {
         atomicOr(&s_flags, 2);   // MLA_DEVERR_BAD_SEQ_LEN
         keys = cap;
@@ -186,18 +189,17 @@ __device__ __forceinline__ void build_plan(PlanShared<kStaged>& sm, const int32_
         if (kStaged) s_kbase[gb + g] = (int)keys;   // every row sees them all
         GroupRec r;
         r.b = ~p;
-        r.row0 = q0 * N + g * kRows;
-        r.nrows = min(kRows, rows - g * kRows);
+        r.row0 = q0 * N + g * GR;
+        r.nrows = min(GR, rows - g * GR);
         r.lmax = (int)keys;
-        r.tiles = (int)((keys + kTileKeys - 1) / kTileKeys);
+        r.tiles = (int)((keys + kTile - 1) / kTile);
         r.pieces = r.ubase = r.tpos = 0;
         grp[gb + g] = r;
       }
     }
-    at_prefix += total;
+    carry += total;
   }
-  if (kSource == kJoint || kSource == kPrefixes) carry = at_prefix;
-  const int own_groups = carry;      // the first group of a request
+  const int own_groups = carry;   // kShared: the first group of a request
   for (int base = 0; base < batch; base += kPlanThreads) {
     const int b = base + tid;
     int sq = 0, ng = 0, q0 = 0;
@@ -206,19 +208,18 @@ __device__ __forceinline__ void build_plan(PlanShared<kStaged>& sm, const int32_
       // all of the request's loads at once
       q0 = qsl ? qsl[b] : b;
       sq = qsl ? qsl[b + 1] - q0 : 1;
-      seq = kSource == kPrefixes ? 0 : seq_lens[b];
-      if (kSource != kRequests && (sq < 0 || q0 < 0 || q0 > sh.total_q - sq)) {
+      seq = seq_lens[b];
+      if (kShared && (sq < 0 || q0 < 0 || q0 > sh.total_q - sq)) {
         atomicOr(&s_flags, 8);
         sq = 0;
       }
       if (sq < 0) sq = 0;
       ng = (int)(((long long)sq * N + GR - 1) >> gshift);
     }
-    if (kSource == kPrefixes) continue;   // (their query rows are checked, no more)
     int total;
     const int gb = block_excl_scan(ng, &total, s_sums, sums_row) + carry;
     if (b < batch && ng > 0) {
-      if (kBehind) atomicMax(&s_own_rows, min(GR, sq * N));
+      if (kShared) atomicMax(&s_own_rows, min(GR, sq * N));
       if (seq > kv_cap) {
         atomicOr(&s_flags, 2);  // MLA_DEVERR_BAD_SEQ_LEN
         seq = kv_cap;
@@ -246,7 +247,7 @@ __device__ __forceinline__ void build_plan(PlanShared<kStaged>& sm, const int32_
     carry += total;
   }
   int G = carry;
-  if (kSource != kRequests) {
+  if (kShared) {
     __syncthreads();
     if (s_flags & 8) G = 0;   // the rows of prefixes and requests do not fit together: plan nothing
     __syncthreads();
@@ -263,7 +264,7 @@ __device__ __forceinline__ void build_plan(PlanShared<kStaged>& sm, const int32_
   for (int base = 0; base < G; base += kPlanThreads) {
     const int g = base + tid;
     const int tl = g < G ? grp[g].tiles : 0;
-    const int t = tl > 0 ? tl + kCost : 0;
+    const int t = tl > 0 ? tl + kUnitCostTiles : 0;
     int total;
     const int pos = block_excl_scan(t, &total, s_sums, sums_row) + carry;
     if (g < G) grp[g].tpos = pos;
@@ -298,7 +299,7 @@ __device__ __forceinline__ void build_plan(PlanShared<kStaged>& sm, const int32_
     if (g < G) {
       const GroupRec r = grp[g];
       if (r.tiles > 0) {
-        const int s0 = r.tpos + kCost;   // first real tile on the axis
+        const int s0 = r.tpos + kUnitCostTiles;   // first real tile on the axis
         if (num_splits > 0)
           pieces = min(num_splits, r.tiles);
         else
@@ -325,24 +326,35 @@ __device__ __forceinline__ void build_plan(PlanShared<kStaged>& sm, const int32_
   // 4. units
   for (int g = tid; g < G; g += kPlanThreads) {
     const GroupRec r = grp[g];
-    const int s0 = r.tpos + kCost;       // first real tile on the axis
+    const int s0 = r.tpos + kUnitCostTiles;       // first real tile on the axis
     int kbase = 0;
     bool partial = r.pieces > 1;
-    if (kSource != kRequests && g < own_groups) partial = true;   // joined with its rows' own keys
-    if (kBehind && g >= own_groups) {
-      // the prefix of request r.b: the last one that begins at or before it
-      // (one without requests begins where the next one does)
-      int lo = 0, hi = sh.prefixes - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (sh.begin[mid] <= r.b) lo = mid; else hi = mid - 1;
+    if (kShared) {
+      if (g < own_groups) {
+        partial = true;           // joined with its rows' own keys
+      } else {
+        // the prefix of request r.b: the last one that begins at or before it
+        // (one without requests begins where the next one does)
+        int lo = 0, hi = sh.prefixes - 1;
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) >> 1;
+          if (sh.begin[mid] <= r.b) lo = mid; else hi = mid - 1;
+        }
+        const int first = qsl ? qsl[sh.begin[lo]] : sh.begin[lo];
+        // its first group: the last one of a prefix that begins at or before
+        // its first row, and has rows
+        int a = 0, z = own_groups - 1;
+        while (a < z) {
+          const int mid = (a + z + 1) >> 1;
+          if (grp[mid].row0 <= first * N) a = mid; else z = mid - 1;
+        }
+        P.behind[g] = make_int2(a, first * N);
+        partial = partial || grp[a].tiles > 0;
       }
-      P.behind[g] = sh.first[lo];
-      partial = partial || sh.lens[lo] > 0;
     }
     if (kStaged) {
       kbase = s_kbase[g];
-    } else if (kSource != kRequests && r.b < 0) {
+    } else if (kShared && r.b < 0) {
       kbase = r.lmax;
     } else if (r.pieces > 0) {
       const int sq = qsl ? qsl[r.b + 1] - qsl[r.b] : 1;
@@ -368,8 +380,7 @@ __device__ __forceinline__ void build_plan(PlanShared<kStaged>& sm, const int32_
         u.tile_begin = max(s0, span_start(cl)) - s0;
         u.tile_end = min(s0 + r.tiles, span_start(cl + 1)) - s0;
       }
-      u.slot = partial ? P.slot0 + r.ubase + i : -1;
-      if (kSource == kPrefixes) P.redo[r.ubase + i] = 0;
+      u.slot = partial ? r.ubase + i : -1;
       P.units[r.ubase + i] = u;
       ucl[r.ubase + i] = cl;
     }
@@ -396,58 +407,9 @@ __device__ __forceinline__ void build_plan(PlanShared<kStaged>& sm, const int32_
     h.total_tiles = T;
     h.tiles_per_cluster = W;
     h.own_groups = own_groups;
-    h.own_rows = kBehind ? s_own_rows : 0;
+    h.own_rows = kShared ? s_own_rows : 0;
     *P.header = h;
   }
-}
-
-// kMode: blocks 1.. of the launch do the step's other small jobs while block
-// 0 builds the plan, so they cost the step no launch of their own: the new
-// cache rows (blocks 1 .. write_blocks, 8 tokens a block; 1 bf16 cache,
-// 2 e4m3 cache) and, in mode 3 (e4m3 cache), the query's quantisation (the
-// remaining blocks, grid-stride over its 8-value vectors).
-template <bool kStaged, int kMode, int kSource = kRequests>
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* __restrict__ seq_lens,
-                                                    const int32_t* __restrict__ qsl, int batch, int N,
-                                                    int max_pages, int page_size, int num_splits, int C,
-                                                    int GR, Plan P, const CacheWriteArgs w, const QuantArgs qa,
-                                                    int write_blocks, const SharedArgs sh) {
-  if constexpr (kMode != 0) {
-    if (blockIdx.x > 0) {
-      // as the cache-write kernel: wait for the kernel before, then let the
-      // next one launch (the decode waits for this whole grid)
-      asm volatile("griddepcontrol.wait;" ::: "memory");
-      asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-      const int b = (int)blockIdx.x - 1;
-      if (b < write_blocks) {
-        const int64_t tok = b * 8LL + (threadIdx.x >> 5);
-        if (tok < w.num_tokens) write_cache_row<kMode >= 2>(w, tok, threadIdx.x & 31);
-        return;
-      }
-      if constexpr (kMode == 3) {
-        const int64_t nvec = qa.rows * (kDqk / 8);
-        const int64_t stride = (int64_t)(gridDim.x - 1 - write_blocks) * kPlanThreads;
-        for (int64_t v = (int64_t)(b - write_blocks) * kPlanThreads + threadIdx.x; v < nvec; v += stride)
-          quantize_query_vec(qa, v);
-      }
-      return;
-    }
-  }
-  __shared__ PlanShared<kStaged> sm;
-  build_plan<kStaged, kSource>(sm, seq_lens, qsl, batch, N, max_pages, page_size, num_splits, C, GR, P, sh);
-}
-
-// The two plans of a mla_decode_shared whose prefixes have a kernel of their
-// own, by a block each.
-template <bool kStaged>
-__global__ void __launch_bounds__(kPlanThreads)
-    split_plan_kernel(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ qsl, int batch, int N,
-                      int max_pages, int page_size, int num_splits, int C, Plan own, Plan prefix, const SharedArgs sh) {
-  __shared__ PlanShared<kStaged> sm;
-  if (blockIdx.x == 0)
-    build_plan<kStaged, kOwn>(sm, seq_lens, qsl, batch, N, max_pages, page_size, num_splits, C, kRows, own, sh);
-  else
-    build_plan<kStaged, kPrefixes>(sm, seq_lens, qsl, batch, N, max_pages, page_size, num_splits, C, kRows, prefix, sh);
 }
 
 }  // namespace
@@ -505,29 +467,9 @@ cudaError_t launch_shared_plan(const int32_t* seq_lens, const int32_t* qsl, int 
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   const bool staged = plan.max_groups <= kPlanSmemGroups && plan.max_units <= kPlanSmemUnits;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, staged ? plan_kernel<true, 0, kJoint> : plan_kernel<false, 0, kJoint>, seq_lens,
+  cudaError_t e = cudaLaunchKernelEx(&cfg, staged ? plan_kernel<true, 0, true> : plan_kernel<false, 0, true>, seq_lens,
                                      qsl, batch, num_heads, max_pages, page_size, num_splits, num_clusters, kRows, plan,
                                      CacheWriteArgs{}, QuantArgs{}, 0, shared);
-  if (e != cudaSuccess) return e;
-  return cudaGetLastError();
-}
-
-cudaError_t launch_split_plan(const int32_t* seq_lens, const int32_t* qsl, int batch, int num_heads, int max_pages,
-                              int page_size, int num_splits, int num_clusters, const Plan& own, const Plan& prefix,
-                              const SharedArgs& shared, cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2);
-  cfg.blockDim = dim3(kPlanThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  auto fits = [](const Plan& p) { return p.max_groups <= kPlanSmemGroups && p.max_units <= kPlanSmemUnits; };
-  cudaError_t e =
-      cudaLaunchKernelEx(&cfg, fits(own) && fits(prefix) ? split_plan_kernel<true> : split_plan_kernel<false>, seq_lens,
-                         qsl, batch, num_heads, max_pages, page_size, num_splits, num_clusters, own, prefix, shared);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
