@@ -57,6 +57,18 @@ struct UnitRec {     // 32 bytes
 };
 static_assert(sizeof(UnitRec) == 32, "unit record: one aligned 32-byte piece");
 
+// Where the partials of a group's rows are: of its own keys, and of the rows
+// among their prefix's (two groups of 128 rows at most, the second from row
+// `split` on).  Piece i of row r is partial row at + 128 i + r.
+struct JoinRec {     // 48 bytes
+  int row0, nrows;
+  int own_at, own_pieces;
+  int pre_at, pre_pieces;
+  int split;
+  int pre2_at, pre2_pieces;
+  int pad[3];
+};
+
 struct Plan {
   PlanHeader* header;
   GroupRec* groups;
@@ -69,15 +81,13 @@ struct Plan {
   uint16_t* part_o;      // [max_units][128][512] fp16 codes
   float* part_scale;     // [max_units][128][16] 2^e of each 32-dim chunk
   float* part_lse;       // [max_units][128]
-  // mla_decode_shared: of each group of a request's own keys, the first group
-  // of its prefix and that group's first query row
-  int2* behind;          // [max_groups]
+  JoinRec* joins;        // mla_decode_shared: of each group of a request's own keys
   int max_groups;
   int max_units;
 };
 
 struct WorkspaceLayout {
-  size_t header, groups, units, unit_cluster, cluster_begin, part_o, part_scale, part_lse, behind, total;
+  size_t header, groups, units, unit_cluster, cluster_begin, part_o, part_scale, part_lse, joins, total;
   int max_groups, max_units;
 };
 
@@ -102,7 +112,7 @@ inline WorkspaceLayout workspace_layout(int batch, int total_q, int num_heads, i
   L.part_o = off;        off = up(off + sizeof(uint16_t) * (size_t)mu * kRows * kLkv);
   L.part_scale = off;    off = up(off + sizeof(float) * (size_t)mu * kRows * (kLkv / 32));
   L.part_lse = off;      off = up(off + sizeof(float) * (size_t)mu * kRows);
-  L.behind = off;        if (prefixes >= 0) off = up(off + sizeof(int2) * (size_t)mg);
+  L.joins = off;         if (prefixes >= 0) off = up(off + sizeof(JoinRec) * (size_t)mg);
   L.total = off;
   return L;
 }
@@ -118,7 +128,7 @@ inline Plan plan_from_workspace(void* ws, const WorkspaceLayout& L) {
   P.part_o = reinterpret_cast<uint16_t*>(p + L.part_o);
   P.part_scale = reinterpret_cast<float*>(p + L.part_scale);
   P.part_lse = reinterpret_cast<float*>(p + L.part_lse);
-  P.behind = reinterpret_cast<int2*>(p + L.behind);
+  P.joins = reinterpret_cast<JoinRec*>(p + L.joins);
   P.max_groups = L.max_groups;
   P.max_units = L.max_units;
   return P;

@@ -473,9 +473,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kTh
       const int xl = 256 * (int)rank, xr = kLkv + 32 * (int)rank;   // first latent / rope column of the CTA
       // cache lines are read once per pair: evict them first, so that the
       // split-KV partials, queries and block tables stay in L2
-      const uint64_t pol_once = l2_policy_evict_first();
-      // (a prefix's are read by every group of rows behind it)
-      const uint64_t pol_again = kShared ? l2_policy_evict_last() : 0;
+      const uint64_t pol = l2_policy_evict_first();
       for (int u = ubeg; u < uend; ++u) {
         const UnitRec ur = P.units[u];
         const UnitRec& gr = ur;
@@ -483,7 +481,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kTh
         const int32_t* bt =
             prefix ? a.prefix_table + (size_t)~gr.b * a.max_prefix_pages : a.block_table + (size_t)gr.b * a.max_pages;
         const int max_pages = prefix ? a.max_prefix_pages : a.max_pages;
-        const uint64_t pol = prefix ? pol_again : pol_once;
         // loads the CTA's columns of tile j (all sub-pages) into dst, counting on `full`:
         //   bf16:           4 latent boxes of 64 x 128 B, then the 64 x 64-B rope box
         //   e4m3 (v1):      4 latent boxes of 64 x 64 B, then the 64 x 32-B rope box
@@ -1347,11 +1344,11 @@ size_t decode_smem_bytes(int variant) {
 namespace {
 
 template <class K>
-cudaError_t launch(K* kern, const CUtensorMap& tm_q, const CUtensorMap& tm_qr, const CUtensorMap& tm_kv,
+cudaError_t launch(K* kern, std::atomic<uint64_t>& done, const CUtensorMap& tm_q, const CUtensorMap& tm_qr, const CUtensorMap& tm_kv,
                    const CUtensorMap& tm_kvr, const CUtensorMap& tm_out, const CUtensorMap& tm_part, int variant,
                    const DecodeArgs& a, int num_clusters, cudaStream_t s) {
   const size_t smem = decode_smem_bytes(variant);
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = allow_smem(kern, smem, done);
   if (e != cudaSuccess) return e;
   // programmatic dependent launch: the prologue (barriers, TMEM, cluster
   // sync) overlaps the plan kernel; the kernel waits for it before reading the plan
@@ -1378,13 +1375,15 @@ cudaError_t launch_decode(const CUtensorMap& tm_q, const CUtensorMap& tm_qr, con
                           int variant, const DecodeArgs& a, int num_clusters, cudaStream_t s) {
   auto kern = variant == 1 ? decode_kernel<1>
                            : (variant == 2 ? decode_kernel<2> : (variant == 3 ? decode_kernel<3> : decode_kernel<0>));
-  return launch(kern, tm_q, tm_qr, tm_kv, tm_kvr, tm_out, tm_part, variant, a, num_clusters, s);
+  static std::atomic<uint64_t> done[4];
+  return launch(kern, done[variant], tm_q, tm_qr, tm_kv, tm_kvr, tm_out, tm_part, variant, a, num_clusters, s);
 }
 
 cudaError_t launch_decode_shared(const CUtensorMap& tm_q, const CUtensorMap& tm_qr, const CUtensorMap& tm_kv,
                                  const CUtensorMap& tm_kvr, const CUtensorMap& tm_out, const CUtensorMap& tm_part,
                                  int variant, const DecodeArgs& a, int num_clusters, cudaStream_t s) {
-  return launch(variant == 1 ? decode_kernel<1, true> : decode_kernel<0, true>, tm_q, tm_qr, tm_kv, tm_kvr, tm_out,
+  static std::atomic<uint64_t> done[2];
+  return launch(variant == 1 ? decode_kernel<1, true> : decode_kernel<0, true>, done[variant == 1], tm_q, tm_qr, tm_kv, tm_kvr, tm_out,
                 tm_part, variant, a, num_clusters, s);
 }
 

@@ -143,8 +143,8 @@ __global__ void __launch_bounds__(256, 2) combine_kernel(const DecodeArgs a) {
   }
 }
 
-// The merge of mla_decode_shared: a row's partials are those of its own group
-// and those of the row among its prefix's groups.  Items, threads and loads as
+// The merge of mla_decode_shared: a row's partials are those of its own keys and
+// those of the row among its prefix's, as the plan's records say.  Items, threads and loads as
 // in combine_kernel; rows that the decode wrote itself (one piece, and no
 // prefix keys) are left.
 __global__ void __launch_bounds__(256, 2) combine_shared_kernel(const DecodeArgs a) {
@@ -155,30 +155,29 @@ __global__ void __launch_bounds__(256, 2) combine_shared_kernel(const DecodeArgs
   const PlanHeader head = *P.header;
   const int own_groups = head.own_groups;
   const int quads = (head.own_rows + 3) / 4;   // of a group: as many as the largest has
-  const int first = own_groups * quads, items = head.num_groups * quads;
+  const int items = head.num_groups * quads;
+  int item = own_groups * quads + (int)blockIdx.x * 4 + (int)(threadIdx.x >> 6);
+  // (the plan is complete before this grid starts: the first record is read
+  // before the wait for the partials)
+  JoinRec next{};
+  if (item < items) next = P.joins[item / quads];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out);
   const int sub = threadIdx.x & 15;
   const int d0 = sub * 8;
   const int quad_row = (threadIdx.x >> 4) & 3;
-  for (int item = first + (int)blockIdx.x * 4 + (int)(threadIdx.x >> 6); item < items; item += VG) {
-    const GroupRec gr = P.groups[item / quads];
-    const int2 behind = P.behind[item / quads];
+  for (; item < items; item += VG) {
+    const JoinRec gr = next;
+    if (item + VG < items) next = P.joins[(item + VG) / quads];
     const int r = (item % quads) * 4 + quad_row;
     if (r >= gr.nrows || gr.row0 + r >= a.total_rows) continue;
     const int R = gr.row0 + r;
-    // the row among its prefix's rows
-    const int pr = R - behind.y, pg = behind.x + pr / kRows;
-    int pre = 0;
-    size_t pre_at = 0;
-    if (pg < own_groups) {
-      pre = P.groups[pg].pieces;
-      pre_at = (size_t)P.groups[pg].ubase * kRows + pr % kRows;
-    }
-    const int n = gr.pieces + pre;
-    if (pre == 0 && gr.pieces == 1) continue;   // written by the decode kernel
-    const size_t own_at = (size_t)gr.ubase * kRows + r;
+    const bool second = r >= gr.split;
+    const int pre = second ? gr.pre2_pieces : gr.pre_pieces;
+    const int n = gr.own_pieces + pre;
+    if (pre == 0 && gr.own_pieces == 1) continue;   // written by the decode kernel
+    const size_t pre_at = second ? gr.pre2_at + (r - gr.split) : gr.pre_at + r, own_at = gr.own_at + r;
     auto at = [&](int i) { return i < pre ? pre_at + (size_t)i * kRows : own_at + (size_t)(i - pre) * kRows; };
     float acc[32];
 #pragma unroll

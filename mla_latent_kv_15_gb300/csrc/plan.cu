@@ -135,6 +135,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* __res
   __shared__ int s_ucl[kStaged ? kPlanSmemUnits : 1];
   __shared__ int s_kbase[kStaged ? kPlanSmemGroups : 1];   // seq_len - Sq + 1 - q0 of each group's request
   __shared__ int s_sums[2][kPlanThreads / 32];
+  // of the first kPlanThreads prefixes: first request, first group, first query row
+  __shared__ int s_pbegin[kShared ? kPlanThreads : 1], s_pgroup[kShared ? kPlanThreads : 1], s_prow[kShared ? kPlanThreads : 1];
   int sums_row = 0;
   GroupRec* grp = kStaged ? s_groups : P.groups;
   int* ucl = kStaged ? s_ucl : P.unit_cluster;
@@ -157,11 +159,21 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* __res
   //    request; b < 0 marks prefix ~b)
   int carry = 0;
   const int np = kShared ? sh.prefixes : 0;
+  // the first requests' loads, beside the prefixes'
+  int q0_ahead = 0, q1_ahead = 0, seq_ahead = 0;
+  if (kShared && tid < batch) {
+    q0_ahead = qsl ? qsl[tid] : tid;
+    q1_ahead = qsl ? qsl[tid + 1] : tid + 1;
+    seq_ahead = seq_lens[tid];
+  }
   for (int base = 0; base < np; base += kPlanThreads) {
     const int p = base + tid;
     int ng = 0, q0 = 0, rows = 0;
+    long long keys = 0;
     if (p < np) {
       const int r0 = sh.begin[p], r1 = sh.begin[p + 1];
+      keys = sh.lens[p];
+      if (base == 0) s_pbegin[p] = r0;
       const bool fits = r0 >= 0 && r0 <= r1 && r1 <= batch && (p > 0 || r0 == 0) && (p < np - 1 || r1 == batch);
       int q1 = 0;
       if (fits) {
@@ -177,9 +189,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* __res
     }
     int total;
     const int gb = block_excl_scan(ng, &total, s_sums, sums_row) + carry;
+    if (p < np && base == 0) {
+      s_pgroup[p] = gb;
+      s_prow[p] = q0 * N;
+    }
     if (p < np && ng > 0) {
       const long long cap = (long long)sh.max_pages * page_size;
-      long long keys = sh.lens[p];
       if (keys > cap) {
         atomicOr(&s_flags, 2);   // MLA_DEVERR_BAD_SEQ_LEN
         keys = cap;
@@ -206,9 +221,15 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* __res
     long long seq = 0;
     if (b < batch) {
       // all of the request's loads at once
-      q0 = qsl ? qsl[b] : b;
-      sq = qsl ? qsl[b + 1] - q0 : 1;
-      seq = seq_lens[b];
+      if (kShared && base == 0) {
+        q0 = q0_ahead;
+        sq = q1_ahead - q0;
+        seq = seq_ahead;
+      } else {
+        q0 = qsl ? qsl[b] : b;
+        sq = qsl ? qsl[b + 1] - q0 : 1;
+        seq = seq_lens[b];
+      }
       if (kShared && (sq < 0 || q0 < 0 || q0 > sh.total_q - sq)) {
         atomicOr(&s_flags, 8);
         sq = 0;
@@ -335,20 +356,42 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* __res
       } else {
         // the prefix of request r.b: the last one that begins at or before it
         // (one without requests begins where the next one does)
-        int lo = 0, hi = sh.prefixes - 1;
+        const bool few = np <= kPlanThreads;
+        int lo = 0, hi = np - 1;
         while (lo < hi) {
           const int mid = (lo + hi + 1) >> 1;
-          if (sh.begin[mid] <= r.b) lo = mid; else hi = mid - 1;
+          if ((few ? s_pbegin[mid] : sh.begin[mid]) <= r.b) lo = mid; else hi = mid - 1;
         }
-        const int first = qsl ? qsl[sh.begin[lo]] : sh.begin[lo];
-        // its first group: the last one of a prefix that begins at or before
-        // its first row, and has rows
-        int a = 0, z = own_groups - 1;
-        while (a < z) {
-          const int mid = (a + z + 1) >> 1;
-          if (grp[mid].row0 <= first * N) a = mid; else z = mid - 1;
+        int a, first;                // its first group, and that group's first row
+        if (few) {
+          a = s_pgroup[lo];
+          first = s_prow[lo];
+        } else {
+          first = (qsl ? qsl[sh.begin[lo]] : sh.begin[lo]) * N;
+          // the last group of a prefix that begins at or before that row, and has rows
+          int z = own_groups - 1;
+          a = 0;
+          while (a < z) {
+            const int mid = (a + z + 1) >> 1;
+            if (grp[mid].row0 <= first) a = mid; else z = mid - 1;
+          }
         }
-        P.behind[g] = make_int2(a, first * N);
+        const int off = r.row0 - first, pg = a + off / kRows;
+        const GroupRec x = grp[pg];
+        JoinRec j{};
+        j.row0 = r.row0;
+        j.nrows = r.nrows;
+        j.own_at = r.ubase * kRows;
+        j.own_pieces = r.pieces;
+        j.pre_at = x.ubase * kRows + off % kRows;
+        j.pre_pieces = x.pieces;
+        j.split = kRows - off % kRows;
+        if (j.split < r.nrows) {
+          const GroupRec y = grp[pg + 1];
+          j.pre2_at = y.ubase * kRows;
+          j.pre2_pieces = y.pieces;
+        }
+        P.joins[g] = j;
         partial = partial || grp[a].tiles > 0;
       }
     }
