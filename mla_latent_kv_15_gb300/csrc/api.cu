@@ -280,7 +280,7 @@ int decode_impl(const void* q_abs, const void* q_pe, const void* q8, float q_sca
              : mla::launch_decode(tm_q, tm_qr, tm_kv, tm_kvr, tm_out, tm_part, variant, a, clusters, s);
   if (e != cudaSuccess) return cuda_fail(e, "decode launch");
   if (timed && (e = cudaEventRecord(g_timing_stop, s)) != cudaSuccess) return cuda_fail(e, "timing event");
-  e = shared ? mla::launch_combine_shared(a, L.max_groups, sms, s) : mla::launch_combine(a, L.max_groups, sms, s);
+  e = shared ? mla::launch_combine_shared(a, sms, s) : mla::launch_combine(a, L.max_groups, sms, s);
   if (e != cudaSuccess) return cuda_fail(e, "combine launch");
   return ok();
 }
@@ -851,7 +851,10 @@ int mla_decode_shared(const void* q_abs, const void* q_pe, const void* cache, in
                            dense(query_start_loc, (batch + 1LL) * 4)};
   if (num_blocks > 0 && num_blocks < (1LL << 31) && any_overlap(outputs, 3, inputs, 9))
     return fail(MLA_ERR_INVALID_ARG, "out, lse and the workspace must not overlap each other or the inputs");
-  const mla::SharedArgs sh{prefix_lens, prefix_requests, prefixes, max_prefix_pages, total_q};
+  // A unit's fixed cost in tiles.  A fit of the CTAs' times gives 4.1 us a unit
+  // and 1.0 a tile (e4m3 rows 3.6 and 1.3 to 2.0); 24 drawn batches take 1.7 %
+  // over their best with 5 (3: 3.0 %, 4: 2.2, 6: 1.4; e4m3 3: 3.6, 4: 2.1, 6: 0.7)
+  const mla::SharedArgs sh{prefix_lens, prefix_requests, prefixes, max_prefix_pages, total_q, 5};
   return decode_impl(q_abs, q_pe, nullptr, 0.f, cache, num_blocks, page_size, cache_dtype, kv_scale, block_table,
                      max_pages_per_seq, seq_lens, batch, query_start_loc, total_q, num_heads, scale, num_splits, out,
                      lse, workspace, workspace_bytes, stream, nullptr, nullptr, &sh, prefix_table);

@@ -166,6 +166,7 @@ struct SharedArgs {
   int prefixes;
   int max_pages;
   int total_q;
+  int unit_cost;            // of a work unit, in tiles
 };
 
 // mla_key_weights: the sum over a request's query rows of exp(score - lse),
@@ -342,7 +343,7 @@ cudaError_t launch_decode(const CUtensorMap& tm_q, const CUtensorMap& tm_qr, con
 cudaError_t launch_decode_shared(const CUtensorMap& tm_q, const CUtensorMap& tm_qr, const CUtensorMap& tm_kv,
                                  const CUtensorMap& tm_kvr, const CUtensorMap& tm_out, const CUtensorMap& tm_part,
                                  int variant, const DecodeArgs& a, int num_clusters, cudaStream_t s);
-cudaError_t launch_combine_shared(const DecodeArgs& a, int max_groups, int sm_count, cudaStream_t s);
+cudaError_t launch_combine_shared(const DecodeArgs& a, int sm_count, cudaStream_t s);
 // Tensor maps: query rows (q_abs, q_pe; boxes of 64 columns x a.row_tile / 2
 // rows, 128-B swizzle), cache rows (bf16: 64 x min(page, 128), 128-B swizzle;
 // e4m3: 192 x min(page, 32), none)

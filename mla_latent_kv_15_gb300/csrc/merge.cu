@@ -144,98 +144,120 @@ __global__ void __launch_bounds__(256, 2) combine_kernel(const DecodeArgs a) {
 }
 
 // The merge of mla_decode_shared: a row's partials are those of its own keys and
-// those of the row among its prefix's, as the plan's records say.  Items, threads and loads as
-// in combine_kernel; rows that the decode wrote itself (one piece, and no
-// prefix keys) are left.
+// those of the row among its prefix's, as the plan's records say; a prefix cut
+// over many pairs leaves up to one a pair.  64 threads a row, eight dims each,
+// and so few registers a partial that the loads of kMany are in flight at once.
+// A block joins four rows at a time or, where no more rows than blocks are, one
+// row whose partials its four parts share.  (With 16 threads a row and four
+// partials at once the join of 64 rows over ten partials took 7.7 us.)  Rows
+// that the decode wrote itself (one piece, and no prefix keys) are left.
+struct Joined {
+  float mx, wsum, acc[8];
+};
+
 __global__ void __launch_bounds__(256, 2) combine_shared_kernel(const DecodeArgs a) {
   const Plan& P = a.plan;
-  constexpr int kFew = 4;             // partials whose loads are all in flight at once
-  constexpr int kChunks = kLkv / 32;
-  const int VG = (int)gridDim.x * 4;
+  constexpr int kMany = 8;
+  __shared__ Joined s_part[3][64];
   const PlanHeader head = *P.header;
-  const int own_groups = head.own_groups;
-  const int quads = (head.own_rows + 3) / 4;   // of a group: as many as the largest has
-  const int items = head.num_groups * quads;
-  int item = own_groups * quads + (int)blockIdx.x * 4 + (int)(threadIdx.x >> 6);
+  const bool single = (long long)(head.num_groups - head.own_groups) * head.own_rows <= gridDim.x;
+  const int per = single ? 1 : 4;              // rows of an item
+  const int row_items = (head.own_rows + per - 1) / per;   // of a group: as many as the largest has
+  const int items = head.num_groups * row_items;
+  int item = head.own_groups * row_items + (int)blockIdx.x;
   // (the plan is complete before this grid starts: the first record is read
   // before the wait for the partials)
   JoinRec next{};
-  if (item < items) next = P.joins[item / quads];
+  if (item < items) next = P.joins[item / row_items];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out);
-  const int sub = threadIdx.x & 15;
-  const int d0 = sub * 8;
-  const int quad_row = (threadIdx.x >> 4) & 3;
-  for (; item < items; item += VG) {
+  const int sub = threadIdx.x & 63, part = threadIdx.x >> 6;
+  const int first = single ? part : 0, step = single ? 4 : 1;   // the thread's partials of its row
+  for (; item < items; item += (int)gridDim.x) {
     const JoinRec gr = next;
-    if (item + VG < items) next = P.joins[(item + VG) / quads];
-    const int r = (item % quads) * 4 + quad_row;
-    if (r >= gr.nrows || gr.row0 + r >= a.total_rows) continue;
-    const int R = gr.row0 + r;
+    if (item + (int)gridDim.x < items) next = P.joins[(item + (int)gridDim.x) / row_items];
+    const int r = (item % row_items) * per + (single ? 0 : part);
+    if (r >= gr.nrows || gr.row0 + r >= a.total_rows) continue;   // (the whole block where it shares a row)
     const bool second = r >= gr.split;
     const int pre = second ? gr.pre2_pieces : gr.pre_pieces;
     const int n = gr.own_pieces + pre;
     if (pre == 0 && gr.own_pieces == 1) continue;   // written by the decode kernel
     const size_t pre_at = second ? gr.pre2_at + (r - gr.split) : gr.pre_at + r, own_at = gr.own_at + r;
-    auto at = [&](int i) { return i < pre ? pre_at + (size_t)i * kRows : own_at + (size_t)(i - pre) * kRows; };
-    float acc[32];
+    Joined j{-INFINITY, 0.f, {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}};
+    // kMany partials at a time, each merged into what those before left
+    for (int i0 = first; i0 < n; i0 += kMany * step) {
+      float l[kMany], sc[kMany];
+      uint4 x[kMany];
 #pragma unroll
-    for (int k = 0; k < 32; ++k) acc[k] = 0.f;
-    // in batches of kFew partials, each merged into what the batches before left
-    float mx = -INFINITY, wsum = 0.f;
-    for (int i0 = 0; i0 < n; i0 += kFew) {
-      float l[kFew], sc[kFew][4];
-      uint4 x[kFew][4];
-#pragma unroll
-      for (int i = 0; i < kFew; ++i) {
+      for (int i = 0; i < kMany; ++i) {
+        const int k = i0 + i * step;
         l[i] = -INFINITY;
-        if (i0 + i < n) {
-          const size_t p = at(i0 + i);
+        if (k < n) {
+          const size_t p = k < pre ? pre_at + (size_t)k * kRows : own_at + (size_t)(k - pre) * kRows;
           l[i] = P.part_lse[p];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            sc[i][c] = P.part_scale[p * kChunks + 4 * c + (sub >> 2)];
-            x[i][c] = *reinterpret_cast<const uint4*>(P.part_o + p * kLkv + 128 * c + d0);
-          }
+          sc[i] = P.part_scale[p * (kLkv / 32) + (sub >> 2)];
+          x[i] = *reinterpret_cast<const uint4*>(P.part_o + p * kLkv + 8 * sub);
         }
       }
-      float top = mx;
+      float top = j.mx;
 #pragma unroll
-      for (int i = 0; i < kFew; ++i) top = fmaxf(top, l[i]);
+      for (int i = 0; i < kMany; ++i) top = fmaxf(top, l[i]);
       if (top == -INFINITY) continue;
-      const float keep = __expf(mx - top);
-      wsum *= keep;
+      const float keep = __expf(j.mx - top);
+      j.wsum *= keep;
 #pragma unroll
-      for (int k = 0; k < 32; ++k) acc[k] *= keep;
+      for (int k = 0; k < 8; ++k) j.acc[k] *= keep;
 #pragma unroll
-      for (int i = 0; i < kFew; ++i) {
-        if (i0 + i < n) {
+      for (int i = 0; i < kMany; ++i) {
+        if (i0 + i * step < n) {
           const float w = __expf(l[i] - top);
-          wsum += w;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) accumulate(acc + 8 * c, w * sc[i][c], x[i][c]);
+          j.wsum += w;
+          accumulate(j.acc, w * sc[i], x[i]);
         }
       }
-      mx = top;
+      j.mx = top;
+    }
+    if (single) {
+      // the four parts, in their order
+      __syncthreads();
+      if (part > 0) s_part[part - 1][sub] = j;
+      __syncthreads();
+      if (part > 0) continue;
+      float top = j.mx;
+#pragma unroll
+      for (int i = 0; i < 3; ++i) top = fmaxf(top, s_part[i][sub].mx);
+      if (top != -INFINITY) {
+        const float keep = __expf(j.mx - top);
+        j.wsum *= keep;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) j.acc[k] *= keep;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          const Joined& o = s_part[i][sub];
+          const float w = __expf(o.mx - top);
+          j.wsum += w * o.wsum;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) j.acc[k] = fmaf(w, o.acc[k], j.acc[k]);
+        }
+        j.mx = top;
+      }
     }
     float lse = -INFINITY;
-    if (mx != -INFINITY) {
-      const float inv = 1.f / wsum;
+    if (j.mx != -INFINITY) {
+      const float inv = 1.f / j.wsum;
 #pragma unroll
-      for (int k = 0; k < 32; ++k) acc[k] *= inv;
-      lse = mx + __logf(wsum);
+      for (int k = 0; k < 8; ++k) j.acc[k] *= inv;
+      lse = j.mx + __logf(j.wsum);
     }
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      uint4 v;
-      __nv_bfloat162 h;
-      h = __floats2bfloat162_rn(acc[8 * c + 0], acc[8 * c + 1]); v.x = *reinterpret_cast<uint32_t*>(&h);
-      h = __floats2bfloat162_rn(acc[8 * c + 2], acc[8 * c + 3]); v.y = *reinterpret_cast<uint32_t*>(&h);
-      h = __floats2bfloat162_rn(acc[8 * c + 4], acc[8 * c + 5]); v.z = *reinterpret_cast<uint32_t*>(&h);
-      h = __floats2bfloat162_rn(acc[8 * c + 6], acc[8 * c + 7]); v.w = *reinterpret_cast<uint32_t*>(&h);
-      *reinterpret_cast<uint4*>(out + (size_t)R * kLkv + 128 * c + d0) = v;
-    }
+    uint4 v;
+    __nv_bfloat162 h;
+    h = __floats2bfloat162_rn(j.acc[0], j.acc[1]); v.x = *reinterpret_cast<uint32_t*>(&h);
+    h = __floats2bfloat162_rn(j.acc[2], j.acc[3]); v.y = *reinterpret_cast<uint32_t*>(&h);
+    h = __floats2bfloat162_rn(j.acc[4], j.acc[5]); v.z = *reinterpret_cast<uint32_t*>(&h);
+    h = __floats2bfloat162_rn(j.acc[6], j.acc[7]); v.w = *reinterpret_cast<uint32_t*>(&h);
+    const size_t R = (size_t)(gr.row0 + r);
+    *reinterpret_cast<uint4*>(out + R * kLkv + 8 * sub) = v;
     if (a.lse && sub == 0) a.lse[R] = lse;
   }
 }
@@ -339,10 +361,10 @@ cudaError_t launch_combine(const DecodeArgs& a, int max_groups, int sm_count, cu
   return cudaGetLastError();
 }
 
-cudaError_t launch_combine_shared(const DecodeArgs& a, int max_groups, int sm_count, cudaStream_t s) {
-  const long long max_items = (long long)max_groups * (kRows / 4);
+cudaError_t launch_combine_shared(const DecodeArgs& a, int sm_count, cudaStream_t s) {
+  const long long max_rows = a.total_rows;
   long long blocks = (long long)(sm_count > 0 ? sm_count : 1) * 2;
-  if (blocks * 4 > max_items) blocks = (max_items + 3) / 4;
+  if (blocks > max_rows) blocks = max_rows;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(blocks < 1 ? 1 : blocks));
   cfg.blockDim = dim3(256);

@@ -154,6 +154,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* __res
   __syncthreads();
   const long long kv_cap = (long long)max_pages * page_size;
   const int gshift = __ffs(GR) - 1;   // GR is a power of two
+  const int unit_cost = kShared ? sh.unit_cost : kUnitCostTiles;
 
   // 1. groups of every request (kShared: of every prefix, then of every
   //    request; b < 0 marks prefix ~b)
@@ -285,7 +286,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* __res
   for (int base = 0; base < G; base += kPlanThreads) {
     const int g = base + tid;
     const int tl = g < G ? grp[g].tiles : 0;
-    const int t = tl > 0 ? tl + kUnitCostTiles : 0;
+    const int t = tl > 0 ? tl + unit_cost : 0;
     int total;
     const int pos = block_excl_scan(t, &total, s_sums, sums_row) + carry;
     if (g < G) grp[g].tpos = pos;
@@ -320,7 +321,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* __res
     if (g < G) {
       const GroupRec r = grp[g];
       if (r.tiles > 0) {
-        const int s0 = r.tpos + kUnitCostTiles;   // first real tile on the axis
+        const int s0 = r.tpos + unit_cost;   // first real tile on the axis
         if (num_splits > 0)
           pieces = min(num_splits, r.tiles);
         else
@@ -345,87 +346,124 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* __res
   __syncthreads();
 
   // 4. units
-  for (int g = tid; g < G; g += kPlanThreads) {
-    const GroupRec r = grp[g];
-    const int s0 = r.tpos + kUnitCostTiles;       // first real tile on the axis
-    int kbase = 0;
-    bool partial = r.pieces > 1;
-    if (kShared) {
-      if (g < own_groups) {
-        partial = true;           // joined with its rows' own keys
-      } else {
-        // the prefix of request r.b: the last one that begins at or before it
-        // (one without requests begins where the next one does)
-        const bool few = np <= kPlanThreads;
-        int lo = 0, hi = np - 1;
-        while (lo < hi) {
-          const int mid = (lo + hi + 1) >> 1;
-          if ((few ? s_pbegin[mid] : sh.begin[mid]) <= r.b) lo = mid; else hi = mid - 1;
-        }
-        int a, first;                // its first group, and that group's first row
-        if (few) {
-          a = s_pgroup[lo];
-          first = s_prow[lo];
-        } else {
-          first = (qsl ? qsl[sh.begin[lo]] : sh.begin[lo]) * N;
-          // the last group of a prefix that begins at or before that row, and has rows
-          int z = own_groups - 1;
-          a = 0;
-          while (a < z) {
-            const int mid = (a + z + 1) >> 1;
-            if (grp[mid].row0 <= first) a = mid; else z = mid - 1;
-          }
-        }
-        const int off = r.row0 - first, pg = a + off / kRows;
-        const GroupRec x = grp[pg];
-        JoinRec j{};
-        j.row0 = r.row0;
-        j.nrows = r.nrows;
-        j.own_at = r.ubase * kRows;
-        j.own_pieces = r.pieces;
-        j.pre_at = x.ubase * kRows + off % kRows;
-        j.pre_pieces = x.pieces;
-        j.split = kRows - off % kRows;
-        if (j.split < r.nrows) {
-          const GroupRec y = grp[pg + 1];
-          j.pre2_at = y.ubase * kRows;
-          j.pre2_pieces = y.pieces;
-        }
-        P.joins[g] = j;
-        partial = partial || grp[a].tiles > 0;
+  if constexpr (kShared) {
+    // where each group's partials are
+    for (int g = own_groups + tid; g < G; g += kPlanThreads) {
+      const GroupRec r = grp[g];
+      // the prefix of request r.b: the last one that begins at or before it
+      // (one without requests begins where the next one does)
+      const bool few = np <= kPlanThreads;
+      int lo = 0, hi = np - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if ((few ? s_pbegin[mid] : sh.begin[mid]) <= r.b) lo = mid; else hi = mid - 1;
       }
+      int a, first;                // its first group, and that group's first row
+      if (few) {
+        a = s_pgroup[lo];
+        first = s_prow[lo];
+      } else {
+        first = (qsl ? qsl[sh.begin[lo]] : sh.begin[lo]) * N;
+        // the last group of a prefix that begins at or before that row, and has rows
+        int z = own_groups - 1;
+        a = 0;
+        while (a < z) {
+          const int mid = (a + z + 1) >> 1;
+          if (grp[mid].row0 <= first) a = mid; else z = mid - 1;
+        }
+      }
+      const int off = r.row0 - first, pg = a + off / kRows;
+      const GroupRec x = grp[pg];
+      JoinRec j{};
+      j.row0 = r.row0;
+      j.nrows = r.nrows;
+      j.own_at = r.ubase * kRows;
+      j.own_pieces = r.pieces;
+      j.pre_at = x.ubase * kRows + off % kRows;
+      j.pre_pieces = x.pieces;
+      j.split = kRows - off % kRows;
+      if (j.split < r.nrows) {
+        const GroupRec y = grp[pg + 1];
+        j.pre2_at = y.ubase * kRows;
+        j.pre2_pieces = y.pieces;
+      }
+      P.joins[g] = j;
     }
-    if (kStaged) {
-      kbase = s_kbase[g];
-    } else if (kShared && r.b < 0) {
-      kbase = r.lmax;
-    } else if (r.pieces > 0) {
-      const int sq = qsl ? qsl[r.b + 1] - qsl[r.b] : 1;
-      const int q0 = qsl ? qsl[r.b] : r.b;
-      const long long seq = min((long long)seq_lens[r.b], kv_cap);
-      kbase = (int)(seq - sq + 1 - q0);
-    }
-    const int c0 = num_splits > 0 || r.pieces == 0 ? 0 : span_of(s0);   // the span of the group's first piece
-    for (int i = 0; i < r.pieces; ++i) {
+    __syncthreads();
+    // a unit a thread: a long prefix of few rows is one group of many pieces
+    for (int at = tid; at < U; at += kPlanThreads) {
+      int lo = 0, hi = G - 1;       // the last group that begins at or before unit `at`
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (grp[mid].ubase <= at) lo = mid; else hi = mid - 1;
+      }
+      const GroupRec r = grp[lo];
+      const int i = at - r.ubase, s0 = r.tpos + unit_cost;
+      // a prefix's rows are joined with their own keys, and the other way round
+      const bool partial = r.pieces > 1 || lo < own_groups || P.joins[lo].pre_pieces > 0;
       UnitRec u;
       int cl;
       u.b = r.b;
       u.row0 = r.row0;
       u.nrows = r.nrows;
       u.lmax = r.lmax;
-      u.kbase = kbase;
+      if (kStaged) {
+        u.kbase = s_kbase[lo];
+      } else if (r.b < 0) {
+        u.kbase = r.lmax;
+      } else {
+        const int q0 = qsl ? qsl[r.b] : r.b, sq = qsl ? qsl[r.b + 1] - q0 : 1;
+        u.kbase = (int)(min((long long)seq_lens[r.b], kv_cap) - sq + 1 - q0);
+      }
       if (num_splits > 0) {
         u.tile_begin = muldiv(i, r.tiles, r.pieces);
         u.tile_end = muldiv(i + 1, r.tiles, r.pieces);
         cl = min(C - 1, span_of(s0 + (u.tile_begin + u.tile_end) / 2));
       } else {
-        cl = c0 + i;
+        cl = span_of(s0) + i;
         u.tile_begin = max(s0, span_start(cl)) - s0;
         u.tile_end = min(s0 + r.tiles, span_start(cl + 1)) - s0;
       }
-      u.slot = partial ? r.ubase + i : -1;
-      P.units[r.ubase + i] = u;
-      ucl[r.ubase + i] = cl;
+      u.slot = partial ? at : -1;
+      P.units[at] = u;
+      ucl[at] = cl;
+    }
+  } else {
+    for (int g = tid; g < G; g += kPlanThreads) {
+      const GroupRec r = grp[g];
+      const int s0 = r.tpos + unit_cost;           // first real tile on the axis
+      int kbase = 0;
+      const bool partial = r.pieces > 1;
+      if (kStaged) {
+        kbase = s_kbase[g];
+      } else if (r.pieces > 0) {
+        const int sq = qsl ? qsl[r.b + 1] - qsl[r.b] : 1;
+        const int q0 = qsl ? qsl[r.b] : r.b;
+        const long long seq = min((long long)seq_lens[r.b], kv_cap);
+        kbase = (int)(seq - sq + 1 - q0);
+      }
+      const int c0 = num_splits > 0 || r.pieces == 0 ? 0 : span_of(s0);   // the span of the group's first piece
+      for (int i = 0; i < r.pieces; ++i) {
+        UnitRec u;
+        int cl;
+        u.b = r.b;
+        u.row0 = r.row0;
+        u.nrows = r.nrows;
+        u.lmax = r.lmax;
+        u.kbase = kbase;
+        if (num_splits > 0) {
+          u.tile_begin = muldiv(i, r.tiles, r.pieces);
+          u.tile_end = muldiv(i + 1, r.tiles, r.pieces);
+          cl = min(C - 1, span_of(s0 + (u.tile_begin + u.tile_end) / 2));
+        } else {
+          cl = c0 + i;
+          u.tile_begin = max(s0, span_start(cl)) - s0;
+          u.tile_end = min(s0 + r.tiles, span_start(cl + 1)) - s0;
+        }
+        u.slot = partial ? r.ubase + i : -1;
+        P.units[r.ubase + i] = u;
+        ucl[r.ubase + i] = cl;
+      }
     }
   }
   __syncthreads();
