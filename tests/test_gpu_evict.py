@@ -152,6 +152,34 @@ def test_key_weights_not_finite():
     assert w.weights[0, 299].isnan() and w.weights[0, :299].isfinite().all()
 
 
+def test_key_weights_every_e4m3_code():
+    # key j holds code j in one column and a code of another sign behind it; one query reads the column
+    p = long_ref.Pages([256], 64, fp8=True, seed=11)
+    flat = p.cache.view(torch.uint8).view(-1, 576)
+    codes = torch.arange(256, dtype=torch.uint8, device="cuda")
+    for column in (0, 65, 511, 513, 575):
+        flat.zero_()
+        flat[p.slots(0, 256), column] = codes
+        if column + 1 < 576:
+            flat[p.slots(0, 256), column + 1] = codes ^ 0x80
+        q = torch.zeros(1, 1, 576, dtype=torch.bfloat16, device="cuda")
+        q[0, 0, column] = 1.0
+        w = torch.full((1, 256), 7.0, device="cuda")
+        mla.key_weights(q[..., :512].contiguous(), q[..., 512:].contiguous(), p.cache, p.table, i32([256]),
+                        torch.zeros(1, 1, device="cuda"), w, scale=1.0, decay=0.0, kv_scale=0.25)
+        torch.cuda.synchronize()
+        value = codes.view(torch.float8_e4m3fn).double()
+        finite = value.isfinite()
+        ref = torch.exp(0.25 * value)
+        # one product; the exponent's rounding (2^-24 of up to 162 in binary units) and its power's 2^-21;
+        # a power past float32's largest (exp 112 is 4e48) is infinite there
+        over = ref > torch.finfo(torch.float32).max
+        assert (w[0] == float("inf"))[finite & over].all()
+        assert ((w[0].double() - ref).abs() <= (162 * 2.0 ** -23 + 2.0 ** -21) * ref + 1e-37)[finite & ~over].all()
+        if column + 1 < 576:                   # NaN times zero beside it
+            assert w[0][~finite].isnan().all()
+
+
 def test_key_weights_device_errors():
     w = Weights([300, 200], 16, 1, 64, False, seed=7)
     w.pages.table[0, 1] = -7
