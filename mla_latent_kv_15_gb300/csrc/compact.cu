@@ -9,10 +9,9 @@
 // the order of keep, with no scratch rows and no waiting between clusters.
 //
 // A copy, bound by HBM or, for one request, by its chain of latencies (index,
-// page, row, store).  A CTA has a warp that loads a wave's rows into shared
-// memory and one that stores them, by a bulk copy a row, and two that look the
-// rows up ahead of them; two CTAs share an SM, so that one issues copies while
-// the other's lanes do (a warp issues its lanes' copies one after the other).
+// page, row, store).  A CTA has warps that load a wave's rows into shared memory
+// and warps that store them, by a bulk copy a row, and warps that look the rows
+// up ahead of them; two CTAs share an SM.
 #include "common.cuh"
 #include "ptx.cuh"
 
@@ -21,20 +20,29 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kRowsPerWave = 32;     // of a CTA: a lane each
-constexpr int kThreads = 128;        // warp 0 loads, 1 stores, 2 and 3 look up even and odd waves
+constexpr int kRowsPerWave = 32;     // of a CTA
+// Warps that load and that store, each an equal part of a wave's rows, and that
+// look up, in turn.  A warp issues its lanes' bulk copies one after the other,
+// some 70 cycles each.
+constexpr int kCopyWarps = 4, kLookWarps = 4;
+constexpr int kRowsPerWarp = kRowsPerWave / kCopyWarps;
+constexpr int kWarpStore = kCopyWarps, kWarpLook = 2 * kCopyWarps;
+constexpr int kThreads = 32 * (2 * kCopyWarps + kLookWarps);
 constexpr int kLook = 8;             // waves looked up ahead
 constexpr int kMaxCtas = 16;         // of a request's cluster
 
 template <int kRowBytes>
 struct CompactShape {
   static constexpr int kStages = kRowBytes > 1024 ? 3 : 6;
+  static_assert(kStages < kLook, "a wave's barrier is not used again while a warp waits for it");
   static constexpr int kStageBytes = kRowsPerWave * kRowBytes;
 };
 
 struct Bars {
   uint64_t full[6], empty[6], look_full[kLook], look_empty[kLook];
-  uint64_t go[2];                    // every CTA of the cluster has its rows of the wave
+  // every CTA of the cluster has its rows of the wave (of kLook waves: a storing
+  // warp may be as many ahead of another as there are stages)
+  uint64_t go[kLook];
   int src[kLook][kRowsPerWave], dst[kLook][kRowsPerWave];   // cache rows; dst < 0: nothing moves
   float weight[kLook][kRowsPerWave];
   int abort;
@@ -44,6 +52,7 @@ template <int kRowBytes>
 constexpr size_t smem_bytes() {
   return CompactShape<kRowBytes>::kStages * CompactShape<kRowBytes>::kStageBytes + sizeof(Bars);
 }
+static_assert(kLook % kLookWarps == 0 && kRowsPerWave == 32, "a slot of looked-up rows is always the same warp's");
 static_assert(2 * (smem_bytes<1152>() + 1024) <= 233472 && 2 * (smem_bytes<576>() + 1024) <= 233472, "two CTAs an SM");
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
@@ -83,13 +92,13 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactArgs a, 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(smem_u32(&bars->full[i]), R);
-      mbar_init(smem_u32(&bars->empty[i]), 1);
+      mbar_init(smem_u32(&bars->empty[i]), kCopyWarps);
     }
     for (int i = 0; i < kLook; ++i) {
       mbar_init(smem_u32(&bars->look_full[i]), 1);
-      mbar_init(smem_u32(&bars->look_empty[i]), 1);
+      mbar_init(smem_u32(&bars->look_empty[i]), kCopyWarps);
+      mbar_init(smem_u32(&bars->go[i]), ctas);
     }
-    for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&bars->go[i]), ctas);
     bars->abort = 0;
     fence_mbar_init();
   }
@@ -105,10 +114,12 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactArgs a, 
   if (len < 0) len = 0;
   const int per_wave = ctas * R;
   const int waves = (len + per_wave - 1) / per_wave;
-  const int first = rank * R + lane;          // the lane's row of wave w is first + w * per_wave
+  // the thread's row of a wave, of the CTA's R, and its row of wave w: first + w * per_wave
+  const int row = warp >= kWarpLook ? lane : (warp % kCopyWarps) * kRowsPerWarp + lane;
+  const int first = rank * R + row;
   float* weights = a.weights ? a.weights + (int64_t)b * a.weight_stride : nullptr;
 
-  if (warp >= 2) {
+  if (warp >= kWarpLook) {
     // ------------------------------------------------------------- look-ups
     const int32_t* keep = a.keep + (int64_t)b * a.max_keep;
     const int32_t* table = a.block_table + (int64_t)b * a.max_pages;
@@ -117,10 +128,10 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactArgs a, 
       const int64_t i = first + (int64_t)w * per_wave;
       return i < len ? keep[i] : -1;
     };
-    int next = index_of(warp - 2);
-    for (int w = warp - 2; w < waves; w += 2) {
+    int next = index_of(warp - kWarpLook);
+    for (int w = warp - kWarpLook; w < waves; w += kLookWarps) {
       const int i = first + w * per_wave, from = next;
-      next = index_of(w + 2);
+      next = index_of(w + kLookWarps);
       const int at = w % kLook;
       int src = -1, dst = -1;
       float weight = 0.f;
@@ -145,7 +156,7 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactArgs a, 
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars->look_full[at]));
     }
-  } else if (warp == 0) {
+  } else if (warp < kWarpStore) {
     // ---------------------------------------------------------------- loads
     for (int w = 0; w < waves; ++w) {
       const int at = w % kLook, st = w % kStages;
@@ -153,12 +164,14 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactArgs a, 
       if (!wait(bars, a.status, &bars->empty[st], ((w / kStages) & 1) ^ 1)) break;
       __syncwarp();
       const uint32_t bar = smem_u32(&bars->full[st]);
-      if (bars->dst[at][lane] >= 0) {
-        mbar_expect_tx(bar, kRowBytes);
-        bulk_load(smem_u32(smem + st * S::kStageBytes + lane * kRowBytes),
-                  a.cache + (int64_t)bars->src[at][lane] * kRowBytes, kRowBytes, bar);
-      } else {
-        mbar_arrive(bar);
+      if (lane < kRowsPerWarp) {
+        if (bars->dst[at][row] >= 0) {
+          mbar_expect_tx(bar, kRowBytes);
+          bulk_load(smem_u32(smem + st * S::kStageBytes + row * kRowBytes),
+                    a.cache + (int64_t)bars->src[at][row] * kRowBytes, kRowBytes, bar);
+        } else {
+          mbar_arrive(bar);
+        }
       }
       __syncwarp();
     }
@@ -167,20 +180,20 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactArgs a, 
     for (int w = 0; w < waves; ++w) {
       const int at = w % kLook, st = w % kStages;
       if (!wait(bars, a.status, &bars->look_full[at], (w / kLook) & 1)) break;
-      const int dst = bars->dst[at][lane];
-      const float weight = bars->weight[at][lane];
+      const int dst = lane < kRowsPerWarp ? bars->dst[at][row] : -1;
+      const float weight = lane < kRowsPerWarp ? bars->weight[at][row] : 0.f;
       if (!wait(bars, a.status, &bars->full[st], (w / kStages) & 1)) break;
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars->look_empty[at]));
       // every row of the wave is in some CTA's shared memory before one is
       // written (the arrivals order nothing but this: those rows have been read)
       if (ctas > 1) {
-        if (lane < ctas) mbar_arrive_remote(mapa(smem_u32(&bars->go[w & 1]), lane));
-        if (!wait(bars, a.status, &bars->go[w & 1], (w >> 1) & 1)) break;
+        if (warp == kWarpStore && lane < ctas) mbar_arrive_remote(mapa(smem_u32(&bars->go[at]), lane));
+        if (!wait(bars, a.status, &bars->go[at], (w / kLook) & 1)) break;
         __syncwarp();
       }
       if (dst >= 0) {
-        bulk_store(a.cache + (int64_t)dst * kRowBytes, smem_u32(smem + st * S::kStageBytes + lane * kRowBytes), kRowBytes);
+        bulk_store(a.cache + (int64_t)dst * kRowBytes, smem_u32(smem + st * S::kStageBytes + row * kRowBytes), kRowBytes);
         if (weights) weights[first + w * per_wave] = weight;
       }
       bulk_commit_group();                    // one a wave, empty or not
@@ -228,9 +241,13 @@ cudaError_t launch(const CompactArgs& a, int ctas, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_compact(const CompactArgs& a, int row_bytes, int sm_count, cudaStream_t s) {
-  // as many CTAs a request as are on the card at once, no more than its rows fill
+  // CTAs a request: as many as its rows fill, and as are on the card at once, two
+  // an SM; clusters of 16 only where they leave half of those places free (they
+  // do not all find a place beside one another: 16 requests of 4096 rows 33 us
+  // with 8, 35 with 16; 8 requests 22 and 19)
   int ctas = 1;
-  while (ctas < kMaxCtas && (int64_t)a.batch * ctas <= sm_count && ctas * kRowsPerWave < a.max_keep) ctas *= 2;
+  while (ctas < kMaxCtas && (int64_t)a.batch * ctas * (ctas == 8 ? 2 : 1) <= sm_count && ctas * kRowsPerWave < a.max_keep)
+    ctas *= 2;
   return row_bytes > 1024 ? launch<1152>(a, ctas, s) : launch<576>(a, ctas, s);
 }
 
