@@ -100,38 +100,50 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const SelectArgs a,
     if (me == 0) a.keep_lens[b] = len;
     return;
   }
+  // Keys are counted from the 16-byte boundary before the row's weights, `shift`
+  // weights ahead of the first, so that four at a time can be loaded.
+  const float* weights = a.weights + (int64_t)b * a.weight_stride;
+  const int shift = (int)(reinterpret_cast<uintptr_t>(weights) / 4 % 4);
   // keys [lo, hi) compete for `need` places
   const int lo = a.sinks, hi = n - a.recent;
   const int need = a.budget - a.sinks - a.recent;
-  const float* weights = a.weights + (int64_t)b * a.weight_stride;
-  // every warp of the cluster has `part` keys (a multiple of 128), in order
-  const int part = ((n + ctas * kWarps - 1) / (ctas * kWarps) + 127) & ~127;
+  // every warp of the cluster has `part` of them (a multiple of 128), in order
+  const int part = ((n + 3 + ctas * kWarps - 1) / (ctas * kWarps) + 127) & ~127;
   const int slice = part * kWarps;
-  const int k0 = rank * slice;                              // first key of the slice
-  const int beg = max(lo - k0, 0), end = min(hi - k0, slice);   // its competing keys, counted from k0
-  const float* own = weights + k0;
+  const int k0 = rank * slice;                              // first of the slice
+  const int beg = max(lo + shift - k0, 0), end = min(hi + shift - k0, slice);   // its competing keys, from k0
+  const float* own = weights - shift + k0;
   const int held = (end + 3) & ~3;                          // codes looked at, four a thread and step
   __syncthreads();
 
   if (need > 0) {
-    // the codes, and the first digit's histogram: kAtOnce loads of a thread in
+    // the codes, and the first digit's histogram: kAtOnce quads of a thread in
     // flight.  (Code 0 is counted too: it is below every place.)
     constexpr int kAtOnce = 8;
-    for (int base = tid; base < held; base += kAtOnce * kThreads) {
-      float w[kAtOnce];
+    for (int base = 4 * tid; base < held; base += 4 * kAtOnce * kThreads) {
+      float4 w[kAtOnce];
 #pragma unroll
       for (int k = 0; k < kAtOnce; ++k) {
-        const int i = base + k * kThreads;
-        w[k] = i >= beg && i < end ? own[i] : 0.f;
+        const int i = base + 4 * k * kThreads;
+        if (i >= beg && i + 4 <= end)
+          w[k] = *reinterpret_cast<const float4*>(own + i);
+        else
+          w[k] = make_float4(i >= beg && i < end ? own[i] : 0.f, i + 1 >= beg && i + 1 < end ? own[i + 1] : 0.f,
+                             i + 2 >= beg && i + 2 < end ? own[i + 2] : 0.f, i + 3 >= beg && i + 3 < end ? own[i + 3] : 0.f);
       }
 #pragma unroll
       for (int k = 0; k < kAtOnce; ++k) {
-        const int i = base + k * kThreads;
-        if (i < held) {
-          const uint32_t c = i >= beg && i < end ? code_of(w[k]) : 0;
-          if (kHeld) codes[i] = c;
-          atomicAdd(&sm.hist[0][c >> 21], 1);
+        const int i = base + 4 * k * kThreads;
+        if (i >= held) break;
+        uint32_t c[4] = {code_of(w[k].x), code_of(w[k].y), code_of(w[k].z), code_of(w[k].w)};
+        if (i < beg || i + 4 > end) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (i + e < beg || i + e >= end) c[e] = 0;
         }
+        if (kHeld) *reinterpret_cast<uint4*>(codes + i) = make_uint4(c[0], c[1], c[2], c[3]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) atomicAdd(&sm.hist[0][c[e] >> 21], 1);
       }
     }
     __syncthreads();
@@ -157,9 +169,14 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const SelectArgs a,
       for (int i0 = 4 * tid; i0 < held; i0 += 4 * kThreads) {
         uint32_t c[4];
         codes_at(i0, c);
+        bool any = false;            // (few codes share the digits found)
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if ((c[k] >> above) == found) atomicAdd(&h[c[k] >> shift & mask], 1);
+        for (int k = 0; k < 4; ++k) any |= (c[k] >> above) == found;
+        if (any) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if ((c[k] >> above) == found) atomicAdd(&h[c[k] >> shift & mask], 1);
+        }
       }
     }
     cluster_wide();
@@ -187,18 +204,30 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const SelectArgs a,
     found = pass == 2 ? (found << 10) | (uint32_t)sm.digit : (found << 11) | (uint32_t)sm.digit;
     left -= sm.above;
   }
-  // `left` of the codes equal to `found` stay, and all above it
-  int above = 0, equal = 0;
+  // `left` of the codes equal to `found` stay, and all above it.  Of 1024 keys of
+  // a warp, a lane holds the votes on 32: which are above, which at the threshold.
   const int w0 = warp * part, w1 = min(held, w0 + part);     // the warp's keys, counted from k0
+  uint2* words = reinterpret_cast<uint2*>(codes + slice);    // kHeld: [slice / 32]
+  auto vote = [&](int g0) {
+    uint2 mine = make_uint2(0, 0);
+    const int rows = min((w1 - g0 + 31) / 32, 32);
+#pragma unroll 4
+    for (int k = 0; k < rows; ++k) {
+      const int i = g0 + 32 * k + lane;
+      uint32_t c = 0;
+      if (i < w1) c = kHeld ? codes[i] : (i >= beg && i < end ? code_of(own[i]) : 0);
+      const unsigned up = __ballot_sync(0xffffffffu, c > found), eq = __ballot_sync(0xffffffffu, c == found);
+      if (lane == k) mine = make_uint2(up, eq);
+    }
+    return mine;
+  };
+  int above = 0, equal = 0;
   if (need > 0) {
-    for (int i0 = w0 + 4 * lane; i0 < w1; i0 += 128) {
-      uint32_t c[4];
-      codes_at(i0, c);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        above += c[k] > found;
-        equal += c[k] == found;
-      }
+    for (int g0 = w0; g0 < w1; g0 += 1024) {
+      const uint2 v = vote(g0);
+      if (kHeld && g0 + 32 * lane < w0 + part) words[g0 / 32 + lane] = v;
+      above += __popc(v.x);
+      equal += __popc(v.y);
     }
     above = __reduce_add_sync(0xffffffffu, above);
     equal = __reduce_add_sync(0xffffffffu, equal);
@@ -226,29 +255,23 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const SelectArgs a,
       above += ld_cluster(&sm.count[0], r);
       equal += ld_cluster(&sm.count[1], r);
     }
-    for (int j0 = w0; j0 < w1; j0 += 128) {
-      const int i0 = j0 + 4 * lane;
-      uint32_t c[4];
-      int mine = 0;                  // codes above, and at the threshold from bit 16 on
-      if (i0 < w1) {
-        codes_at(i0, c);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) mine += (c[k] > found) + ((c[k] == found) << 16);
-      }
-      const int incl = warp_incl_scan(mine);
-      const int total = __shfl_sync(0xffffffffu, incl, 31);
-      if (mine) {
-        int ahead = above + ((incl - mine) & 0xffff), same = equal + ((incl - mine) >> 16);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const bool is_up = c[k] > found, is_eq = c[k] == found;
-          if (is_up || (is_eq && same < left)) keep[lo + ahead + min(same, left)] = k0 + i0 + k;
-          ahead += is_up;
-          same += is_eq;
-        }
-      }
-      above += total & 0xffff;
-      equal += total >> 16;
+    const int key0 = k0 - shift;
+    for (int g0 = w0; g0 < w1; g0 += 1024) {
+      uint2 v = make_uint2(0, 0);
+      if (!kHeld)
+        v = vote(g0);
+      else if (g0 + 32 * lane < w0 + part)
+        v = words[g0 / 32 + lane];
+      // of the lane's keys at the threshold, as many as there are places
+      const int eqs = __popc(v.y), eq_incl = warp_incl_scan(eqs);
+      int places = left - (equal + eq_incl - eqs);
+      uint32_t stay = v.x;
+      for (uint32_t e = v.y; e && places > 0; e &= e - 1, --places) stay |= e & (0u - e);
+      const int ups = __popc(v.x), up_incl = warp_incl_scan(ups);
+      int at = lo + above + up_incl - ups + min(equal + eq_incl - eqs, left);
+      for (; stay; stay &= stay - 1) keep[at++] = key0 + g0 + 32 * lane + __ffs(stay) - 1;
+      above += __shfl_sync(0xffffffffu, up_incl, 31);
+      equal += __shfl_sync(0xffffffffu, eq_incl, 31);
     }
   }
   if (ctas > 1) cluster_sync();      // no CTA leaves while its counts are read
@@ -260,11 +283,11 @@ cudaError_t launch_select(const SelectArgs& a, int sm_count, cudaStream_t s) {
   // CTAs a request: a few keys a thread, all requests' on the card at once
   int ctas = 1;
   while (ctas < 8 && (int64_t)a.batch * ctas * 2 <= sm_count && ctas * kThreads * 8 < a.weight_len) ctas *= 2;
-  const int64_t part = (((int64_t)a.weight_len + ctas * kWarps - 1) / (ctas * kWarps) + 127) / 128 * 128;
+  const int64_t part = (((int64_t)a.weight_len + 3 + ctas * kWarps - 1) / (ctas * kWarps) + 127) / 128 * 128;
   const bool held = part * kWarps <= kSliceMax;
-  const size_t smem = held ? (size_t)part * kWarps * 4 : 0;
+  const size_t smem = held ? (size_t)part * kWarps * 4 + part * kWarps / 32 * 8 : 0;   // the codes, and the votes on them
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = held ? allow_smem(select_kernel<true>, kSliceMax * 4, done) : cudaSuccess;
+  cudaError_t e = held ? allow_smem(select_kernel<true>, kSliceMax * 4 + kSliceMax / 4, done) : cudaSuccess;
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.batch * (unsigned)ctas);
