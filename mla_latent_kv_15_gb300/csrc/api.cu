@@ -215,8 +215,8 @@ int decode_impl(const void* q_abs, const void* q_pe, const void* q8, float q_sca
                                 32, kv_box_rows, CU_TENSOR_MAP_SWIZZLE_64B);
     else  // e4m3 codes land unswizzled and are expanded on chip
       enc = enc &&
-            mla::encode_tmap_2d(&tm_kv, cache, CU_TENSOR_MAP_DATA_TYPE_UINT8, mla::kDqk, kv_rows, mla::kDqk, 64,
-                                kv_box_rows, CU_TENSOR_MAP_SWIZZLE_NONE) &&
+            mla::encode_tmap_2d(&tm_kv, cache, CU_TENSOR_MAP_DATA_TYPE_UINT8, mla::kDqk, kv_rows, mla::kDqk,
+                                shared ? 256 : 64, kv_box_rows, CU_TENSOR_MAP_SWIZZLE_NONE) &&
             mla::encode_tmap_2d(&tm_kvr, cache, CU_TENSOR_MAP_DATA_TYPE_UINT8, mla::kDqk, kv_rows, mla::kDqk, 32,
                                 kv_box_rows, CU_TENSOR_MAP_SWIZZLE_NONE);
   }

@@ -337,30 +337,38 @@ __device__ __forceinline__ void e4m3x16_to_bf16(const uint4 v, uint32_t (&o)[8])
 // reads its share of the whole tile, then all write.  e4m3 -> f16 -> f32 ->
 // bf16 is exact: every e4m3 value is a bf16 value.  Runs on the 128 threads of
 // the expansion warps; 9 chunks of 16 codes each.
-// Keys from `live` on become zeros (kClean: the tile reaches past the last key).
-template <bool kClean>
+// kShared: the four latent boxes are one of 256-byte rows, and keys from `live`
+// on (the tile may reach past the last key) become zeros.
+template <bool kShared>
 __device__ __forceinline__ void expand_e4m3_tile(uint32_t stage, int t, int live) {
   constexpr int kPer = kFp8TileBytes / 16 / 128;
   static_assert(kPer == 9, "8 latent chunks and 1 rope chunk per thread");
   uint4 v[kPer];
+  // 16-byte chunk in the row, row (key), box of the thread's k-th piece
+  auto place = [&](int k, int& q, int& r, int& p) {
+    const int i = t + 128 * k;
+    q = i & 3;
+    r = kShared ? i >> 4 : (i >> 2) & 63;
+    p = kShared ? (i >> 2) & 3 : i >> 8;
+  };
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    const int i = t + 128 * k;
-    const int q = i & 3, r = (i >> 2) & 63, p = i >> 8;   // chunk in the row, row (key), box
-    v[k] = lds128(stage + kFp8InPlace + p * kFp8Box + r * 64 + q * 16);
+    int q, r, p;
+    place(k, q, r, p);
+    v[k] = lds128(stage + kFp8InPlace + (kShared ? (t + 128 * k) * 16 : p * kFp8Box + r * 64 + q * 16));
   }
   // rope: row t >> 1, chunk t & 1
   v[8] = lds128(stage + kFp8InPlace + kVBoxes * kFp8Box + (t >> 1) * 32 + (t & 1) * 16);
-  if constexpr (kClean) {
+  if constexpr (kShared) {
 #pragma unroll
     for (int k = 0; k < kPer; ++k)
-      if ((k < 8 ? ((t + 128 * k) >> 2) & 63 : t >> 1) >= live) v[k] = make_uint4(0, 0, 0, 0);
+      if ((k < 8 ? (t + 128 * k) >> 4 : t >> 1) >= live) v[k] = make_uint4(0, 0, 0, 0);
   }
   named_bar_expand();
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    const int i = t + 128 * k;
-    const int q = i & 3, r = (i >> 2) & 63, p = i >> 8;
+    int q, r, p;
+    place(k, q, r, p);
     uint32_t o[8];
     e4m3x16_to_bf16(v[k], o);
     const uint32_t row = stage + p * kBox + r * 128;
@@ -483,7 +491,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kTh
         const int max_pages = prefix ? a.max_prefix_pages : a.max_pages;
         // loads the CTA's columns of tile j (all sub-pages) into dst, counting on `full`:
         //   bf16:           4 latent boxes of 64 x 128 B, then the 64 x 64-B rope box
-        //   e4m3 (v1):      4 latent boxes of 64 x 64 B, then the 64 x 32-B rope box
+        //   e4m3 (v1):      4 latent boxes of 64 x 64 B (kShared: one of 64 x 256 B), then the 64 x 32-B rope box
         //   e4m3 query (v3): 2 latent boxes of 64 x 128 B, then the 64 x 32-B rope box
         // cache row of sub-page sb of tile j (a block-table lookup)
         auto lookup = [&](int j, int sb) {
@@ -574,8 +582,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kTh
 #pragma unroll
               for (int sb = 0; sb < kMaxSub; ++sb) {
                 if (sb >= nsub) break;
-                for (int p = 0; p < kVBoxes; ++p)
-                  tma_load_2d_hint(dst + p * kFp8Box + sb * sub_rows * 64, &tm_kv, xl + 64 * p, ys[sb], full, pol);
+                if constexpr (kShared) {
+                  // (a request's time is the TMA unit's, whatever the size: one
+                  // of 256-byte rows instead of four)
+                  tma_load_2d_hint(dst + sb * sub_rows * 256, &tm_kv, xl, ys[sb], full, pol);
+                } else {
+                  for (int p = 0; p < kVBoxes; ++p)
+                    tma_load_2d_hint(dst + p * kFp8Box + sb * sub_rows * 64, &tm_kv, xl + 64 * p, ys[sb], full, pol);
+                }
                 tma_load_2d_hint(dst + kVBoxes * kFp8Box + sb * sub_rows * 32, &tm_kvr, xr, ys[sb], full, pol);
               }
             }
