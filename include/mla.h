@@ -582,6 +582,9 @@ MLA_API size_t mla_decode_shared_workspace_size(int batch, int prefixes, int tot
  *   q_abs, q_pe, cache (bf16 or e4m3), page_size, query_start_loc, num_heads,
  *   scale, num_splits, out, lse: as for mla_decode.  total_q * num_heads < 2^30,
  *                    and a table's pages * page_size + total_q <= 2^30
+ *                    (and, of the keys and prefix keys that the tables can hold
+ *                    and the tiles of 128 query rows that may see them, fewer
+ *                    than 2^31 tiles of 64 keys)
  *   workspace        >= mla_decode_shared_workspace_size(...) bytes, 256-byte
  *                    aligned.  Calls that may overlap on the GPU need a
  *                    workspace each

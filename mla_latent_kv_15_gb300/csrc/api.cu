@@ -837,6 +837,12 @@ int mla_decode_shared(const void* q_abs, const void* q_pe, const void* cache, in
     return fail(MLA_ERR_UNSUPPORTED, "total_q * num_heads must be below 2^30");
   if (2 * (rows / mla::kRows + batch + 2) * (num_splits > 1 ? num_splits : 1) * mla::kRows >= (int64_t)1 << 31)
     return fail(MLA_ERR_UNSUPPORTED, "total_q * num_heads * num_splits is too large");
+  // the plan's axis: every group of 128 rows with the tiles of its longest keys
+  const int64_t tiles = (rows / mla::kRows + batch + 1) * ((int64_t)max_pages_per_seq * page_size / mla::kTile + 8) +
+                        (rows / mla::kRows + (prefixes < batch ? prefixes : batch) + 1) *
+                            ((int64_t)max_prefix_pages * page_size / mla::kTile + 8);
+  if (tiles >= (int64_t)1 << 31)
+    return fail(MLA_ERR_UNSUPPORTED, "total_q * num_heads / 128 * the keys of a table / 64 is too large");
   const mla::WorkspaceLayout L = mla::workspace_layout(batch, total_q, num_heads, num_splits, prefixes);
   const int esize = cache_dtype == MLA_FP8_E4M3 ? 1 : 2;
   const Extent outputs[] = {dense(out, rows * mla::kLkv * 2), dense(lse, rows * 4), dense(workspace, (int64_t)L.total)};

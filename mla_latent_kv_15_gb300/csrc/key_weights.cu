@@ -514,6 +514,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kFp8>::kThread
           for (int k = 0; k < kPieces; ++k) v[k] = src[lane + 32 * k];
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&bars->raw_empty[mine]));
+          // (This warp's load before this one is seven back: of the next trio of
+          // chunks in the tile before, or of an earlier trio of this tile.  It
+          // was written behind its own wait, and products end in order: so the
+          // barriers here are at most one phase behind.)
 #pragma unroll
           for (int k = 0; k < kRawChunks; ++k) wait(ctx, &bars->k_empty[c + k], (tile & 1) ^ 1);
           __syncwarp();

@@ -64,6 +64,8 @@ def test_decode_shared_refusals(lib):
     refused(-1, "max_pages_per_seq", mp=0)
     refused(-2, "2^30", mpp=1 << 25)
     refused(-2, "2^30", mp=1 << 25)
+    refused(-2, "too large", T=1 << 18, mp=1 << 18, wsb=1 << 62)
+    refused(-2, "too large", T=1 << 18, mpp=1 << 18, wsb=1 << 62)
     refused(-1, "cache_dtype", dtype=2)
     for bad in (0.0, -1.0, float("nan"), float("inf")):
         refused(-1, "kv_scale", dtype=1, kv_scale=bad)
