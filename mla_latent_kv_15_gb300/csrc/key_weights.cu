@@ -111,6 +111,12 @@ __device__ __forceinline__ void wait(const Ctx& c, uint64_t* bar, uint32_t parit
   }
 }
 
+// Whether the CTA has given up (for the whole warp alike).  Loads and products
+// stop then: a barrier that counts bytes would take an arrival too many.
+__device__ __forceinline__ bool stopped(const Ctx& c) {
+  return __any_sync(0xffffffffu, *(volatile int*)&c.bars->abort);
+}
+
 __device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -319,10 +325,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kFp8>::kThread
       // e4m3: 32 keys after 32 keys of three chunks, then of the next three
       for (int c = 0; c < kChunks; c += kFp8 ? kRawChunks : 1) {
         for (int h = 0; h < kKeys / kLoadKeys; ++h, ++n) {
-          if (*abort_flag) return;
           const uint32_t slot = n % kSlots, round = n / kSlots;
           wait(ctx, kFp8 ? &bars->raw_empty[slot] : &bars->k_empty[slot], (round & 1) ^ 1);
-          __syncwarp();
+          if (stopped(ctx)) return;
           if (skip) {      // test aid: the first load never comes
             skip = false;
             continue;
@@ -364,9 +369,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kFp8>::kThread
       for (int rt = 0; rt < r.row_tiles; ++rt) {
         const int row0 = r.q0 * a.num_heads + rt * width + width / 2 * (int)rank;
         for (int c = 0; c < kChunks; ++c, q.next(q_stages)) {
-          if (*abort_flag) return;
           wait(ctx, &bars->q_empty[q.at], (q.round & 1) ^ 1);
-          __syncwarp();
+          if (stopped(ctx)) return;
           if (elect_one()) {
             const uint32_t full = mapa(smem_u32(&bars->q_full[q.at]), 0);
             mbar_expect_tx_remote(full, q_bytes);
@@ -391,12 +395,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kFp8>::kThread
       Turn q{0, 0}, d{0, 0};
       for_tiles([&](int, const Request& r, int) {
         for (int rt = 0; rt < r.row_tiles; ++rt, d.next(accs)) {
-          if (*abort_flag) return;
           wait(ctx, &bars->d_empty[d.at], (d.round & 1) ^ 1);
           for (int c = 0; c < kChunks; ++c, q.next(q_stages)) {
             if (rt == 0) wait(ctx, &bars->k_full[c], tile & 1);
             wait(ctx, &bars->q_full[q.at], q.round & 1);
-            __syncwarp();
+            if (stopped(ctx)) return;
             tc_fence_after();
             if (elect_one()) {
               const uint32_t ka = k_lo + c * (kKBytes >> 4), qa = q_lo + q.at * (q_bytes >> 4);
