@@ -117,6 +117,13 @@ __device__ __forceinline__ bool stopped(const Ctx& c) {
   return __any_sync(0xffffffffu, *(volatile int*)&c.bars->abort);
 }
 
+// A wait of a whole warp; false once the CTA has given up.
+__device__ __forceinline__ bool wait_warp(const Ctx& c, uint64_t* bar, uint32_t parity) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(smem_u32(bar), parity))) return true;
+  wait(c, bar, parity);
+  return !stopped(c);
+}
+
 __device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -326,8 +333,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kFp8>::kThread
       for (int c = 0; c < kChunks; c += kFp8 ? kRawChunks : 1) {
         for (int h = 0; h < kKeys / kLoadKeys; ++h, ++n) {
           const uint32_t slot = n % kSlots, round = n / kSlots;
-          wait(ctx, kFp8 ? &bars->raw_empty[slot] : &bars->k_empty[slot], (round & 1) ^ 1);
-          if (stopped(ctx)) return;
+          if (!wait_warp(ctx, kFp8 ? &bars->raw_empty[slot] : &bars->k_empty[slot], (round & 1) ^ 1)) return;
           if (skip) {      // test aid: the first load never comes
             skip = false;
             continue;
@@ -369,8 +375,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kFp8>::kThread
       for (int rt = 0; rt < r.row_tiles; ++rt) {
         const int row0 = r.q0 * a.num_heads + rt * width + width / 2 * (int)rank;
         for (int c = 0; c < kChunks; ++c, q.next(q_stages)) {
-          wait(ctx, &bars->q_empty[q.at], (q.round & 1) ^ 1);
-          if (stopped(ctx)) return;
+          if (!wait_warp(ctx, &bars->q_empty[q.at], (q.round & 1) ^ 1)) return;
           if (elect_one()) {
             const uint32_t full = mapa(smem_u32(&bars->q_full[q.at]), 0);
             mbar_expect_tx_remote(full, q_bytes);
@@ -395,11 +400,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kFp8>::kThread
       Turn q{0, 0}, d{0, 0};
       for_tiles([&](int, const Request& r, int) {
         for (int rt = 0; rt < r.row_tiles; ++rt, d.next(accs)) {
-          wait(ctx, &bars->d_empty[d.at], (d.round & 1) ^ 1);
+          if (!wait_warp(ctx, &bars->d_empty[d.at], (d.round & 1) ^ 1)) return;
           for (int c = 0; c < kChunks; ++c, q.next(q_stages)) {
-            if (rt == 0) wait(ctx, &bars->k_full[c], tile & 1);
-            wait(ctx, &bars->q_full[q.at], q.round & 1);
-            if (stopped(ctx)) return;
+            if (rt == 0 && !wait_warp(ctx, &bars->k_full[c], tile & 1)) return;
+            if (!wait_warp(ctx, &bars->q_full[q.at], q.round & 1)) return;
             tc_fence_after();
             if (elect_one()) {
               const uint32_t ka = k_lo + c * (kKBytes >> 4), qa = q_lo + q.at * (q_bytes >> 4);
