@@ -857,10 +857,13 @@ int mla_decode_shared(const void* q_abs, const void* q_pe, const void* cache, in
                            dense(query_start_loc, (batch + 1LL) * 4)};
   if (num_blocks > 0 && num_blocks < (1LL << 31) && any_overlap(outputs, 3, inputs, 9))
     return fail(MLA_ERR_INVALID_ARG, "out, lse and the workspace must not overlap each other or the inputs");
-  // A unit's fixed cost in tiles.  A fit of the CTAs' times gives 4.1 us a unit
-  // and 1.0 a tile (e4m3 rows 3.6 and 1.3 to 2.0); 24 drawn batches take 1.7 %
-  // over their best with 5 (3: 3.0 %, 4: 2.2, 6: 1.4; e4m3 3: 3.6, 4: 2.1, 6: 0.7)
-  const mla::SharedArgs sh{prefix_lens, prefix_requests, prefixes, max_prefix_pages, total_q, 5};
+  // A unit's fixed cost in tiles.  A fit of the pairs' times gives 3.5 to 4.6 us a
+  // unit, of few rows and of many, and 1.1 a tile; e4m3 rows 5 and 1.6.  Batches of
+  // all sizes, over the best of 2 to 7 for each: bf16 1.5 % with 3 and one for each
+  // 64 rows (3: 1.9, 4: 2.0, 5: 2.9), e4m3 1.4 with 3 (4: 1.6, 5: 2.6; with one for
+  // each 64 rows 2.2)
+  const mla::SharedArgs sh{prefix_lens, prefix_requests, prefixes, max_prefix_pages, total_q,
+                           3,           cache_dtype == MLA_BF16};
   return decode_impl(q_abs, q_pe, nullptr, 0.f, cache, num_blocks, page_size, cache_dtype, kv_scale, block_table,
                      max_pages_per_seq, seq_lens, batch, query_start_loc, total_q, num_heads, scale, num_splits, out,
                      lse, workspace, workspace_bytes, stream, nullptr, nullptr, &sh, prefix_table);

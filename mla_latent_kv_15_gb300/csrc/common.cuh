@@ -166,7 +166,7 @@ struct SharedArgs {
   int prefixes;
   int max_pages;
   int total_q;
-  int unit_cost;            // of a work unit, in tiles
+  int unit_cost, row_cost;  // of a work unit, in tiles: and for each 64 of its rows
 };
 
 // mla_key_weights: the sum over a request's query rows of exp(score - lse),

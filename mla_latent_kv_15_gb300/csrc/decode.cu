@@ -387,6 +387,18 @@ __device__ __forceinline__ void expand_e4m3_tile(uint32_t stage, int t, int live
 }
 
 // kShared: a plan of launch_shared_plan, in whose units b < 0 is prefix ~b.
+//
+// A prefix's tiles come from L2, for one group of 128 rows after the other, so a
+// tile takes as long as a softmax warp takes over it: 2120 cycles, of which its
+// waits are 480 and the products 1090 (64 requests of 128 heads behind 8192 keys
+// 162 us, 51 % of the tensor cores' rate over all of it; 128 samples of 16 heads
+// behind 32768 keys 180).  Three other forms were built and measured.  Partial
+// scores exchanged as float32, no codes: 173 and 198 (the network between the
+// CTAs), though batches of few rows gain 2 to 6 %.  Sixteen softmax warps, four
+// threads a row: 184 and 202.  A kernel of its own for the prefixes, with 64 whole
+// rows a CTA and no exchange: 143 and 164, but each key is loaded as a key and as
+// a value, 272 KB of L2 reads a 256-key tile and CTA, which bound it; and a call
+// over short prefixes took 5 to 13 us more for the fourth launch.
 template <int kVariant, bool kShared = false>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kThreads, 1)
     decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_qr,

@@ -20,6 +20,14 @@
 // An e4m3 cache lands as codes in a ring of its own and is expanded to bf16 by
 // seven warps.  A stage of that ring is always the same warp's (loads may land
 // out of order, and a wait two phases ahead would not wait).
+//
+// Measured (a launch in a graph): 64 requests of 1024 to 8192 keys, 128 heads,
+// bf16 60.4 us, HBM at 90 % of the copy rate; 32 requests of 2048 to 16384 keys
+// with four verified tokens (512 rows) 105 in bf16, 92 % of the tensor cores'
+// rate, and 131 to 135 over e4m3 rows: there shared memory is the limit, which
+// takes the codes, gives them to the expanding warps, takes the bf16 rows back and
+// gives them to two row tiles' products.  One request of 777 keys and 16 heads
+// 7.0: a chain of loads, nine chunks' products and the sums.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>

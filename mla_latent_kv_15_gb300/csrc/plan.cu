@@ -154,7 +154,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* __res
   __syncthreads();
   const long long kv_cap = (long long)max_pages * page_size;
   const int gshift = __ffs(GR) - 1;   // GR is a power of two
-  const int unit_cost = kShared ? sh.unit_cost : kUnitCostTiles;
+  auto cost_of = [&](const GroupRec& r) {
+    return kShared ? sh.unit_cost + sh.row_cost * (r.nrows / 64) : kUnitCostTiles;
+  };
 
   // 1. groups of every request (kShared: of every prefix, then of every
   //    request; b < 0 marks prefix ~b)
@@ -286,7 +288,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* __res
   for (int base = 0; base < G; base += kPlanThreads) {
     const int g = base + tid;
     const int tl = g < G ? grp[g].tiles : 0;
-    const int t = tl > 0 ? tl + unit_cost : 0;
+    const int t = tl > 0 ? tl + cost_of(grp[g]) : 0;
     int total;
     const int pos = block_excl_scan(t, &total, s_sums, sums_row) + carry;
     if (g < G) grp[g].tpos = pos;
@@ -321,7 +323,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* __res
     if (g < G) {
       const GroupRec r = grp[g];
       if (r.tiles > 0) {
-        const int s0 = r.tpos + unit_cost;   // first real tile on the axis
+        const int s0 = r.tpos + cost_of(r);   // first real tile on the axis
         if (num_splits > 0)
           pieces = min(num_splits, r.tiles);
         else
@@ -398,7 +400,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* __res
         if (grp[mid].ubase <= at) lo = mid; else hi = mid - 1;
       }
       const GroupRec r = grp[lo];
-      const int i = at - r.ubase, s0 = r.tpos + unit_cost;
+      const int i = at - r.ubase, s0 = r.tpos + cost_of(r);
       // a prefix's rows are joined with their own keys, and the other way round
       const bool partial = r.pieces > 1 || lo < own_groups || P.joins[lo].pre_pieces > 0;
       UnitRec u;
@@ -431,7 +433,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* __res
   } else {
     for (int g = tid; g < G; g += kPlanThreads) {
       const GroupRec r = grp[g];
-      const int s0 = r.tpos + unit_cost;           // first real tile on the axis
+      const int s0 = r.tpos + cost_of(r);          // first real tile on the axis
       int kbase = 0;
       const bool partial = r.pieces > 1;
       if (kStaged) {
