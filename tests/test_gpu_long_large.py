@@ -191,3 +191,24 @@ def test_key_weights_of_many_rows(lengths, heads, sq, fp8):
 def test_shared_of_many_heads(fp8):
     Case([(300, 2), (65, 1)], [70, 2, 130], 1024, 1, 64, fp8, seed=51).run().check()
     Case([(300, 2), (65, 1)], [70, 30, 130], 1000, [1, 9, 2], 16, fp8, seed=52).run().check()
+
+
+def test_without_the_optional_arguments():
+    c = Case([(100, 2)], [20, 30], 16, 1, 64, seed=61).run().check()
+    want = c.out.clone()
+    c.out.fill_(float("nan"))
+    c.lse.fill_(7.0)
+    c.run(lse=None)
+    torch.cuda.synchronize()
+    assert torch.equal(c.out, want) and (c.lse == 7).all()
+    w = Weights([300, 64], 16, 1, 64, seed=62)
+    w.run(0.5, status=None)
+    w.check()
+    seq, keep, lens = i32([300, 64]), torch.empty(2, 50, dtype=torch.int32, device="cuda"), i32([0, 0])
+    mla.evict_select(w.weights, seq, keep, lens)
+    before = [w.pages.rows(b) for b in range(2)]
+    mla.cache_compact(w.pages.cache, w.pages.table, keep, lens)
+    torch.cuda.synchronize()
+    for b in range(2):
+        assert torch.equal(w.pages.rows(b, 50), before[b][keep[b].long()])
+    assert lens.tolist() == [50, 50]
