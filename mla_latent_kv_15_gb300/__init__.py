@@ -146,13 +146,27 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+_pytorch = None
+
+
+def _torch():
+    """PyTorch, imported by the first call that takes tensors (asking for the
+    import again costs every call a part of a microsecond)."""
+    global _pytorch
+    if _pytorch is None:
+        import torch
+        _pytorch = torch
+    return _pytorch
+
+
 def _dtype_code(cache):
-    import torch
-    if cache.dtype == torch.bfloat16:
+    torch = _pytorch or _torch()
+    dtype = cache.dtype
+    if dtype is torch.bfloat16:
         return MLA_BF16
-    if cache.dtype in (torch.float8_e4m3fn, torch.uint8):
+    if dtype is torch.float8_e4m3fn or dtype is torch.uint8:
         return MLA_FP8_E4M3
-    raise TypeError(f"cache dtype {cache.dtype} is neither bf16 nor float8_e4m3fn")
+    raise TypeError(f"cache dtype {dtype} is neither bf16 nor float8_e4m3fn")
 
 
 def _dense(t, name: str, dtypes, shape=None, dims=None):
@@ -177,7 +191,7 @@ def _dense(t, name: str, dtypes, shape=None, dims=None):
 
 
 def _cache_checked(cache, name="cache"):
-    import torch
+    torch = _pytorch or _torch()
     dtype, shape = cache.dtype, cache.shape
     if ((dtype is torch.bfloat16 or dtype is torch.float8_e4m3fn) and len(shape) == 3 and shape[2] == DQK and
             cache.is_contiguous()):
@@ -253,11 +267,11 @@ def _head_strides(t, name: str, rows: int, heads, width: int, bf16, writable: bo
 def _on_current_device(*tensors) -> int:
     """Refuse tensors of another device than the current one: the call's
     stream, tensor maps and launch belong to the current device.  Returns it."""
-    import torch
+    torch = _pytorch or _torch()
     found = {t.get_device() for t in tensors if t is not None}
     if len(found) == 1:                      # the usual case
         dev = found.pop()
-        if dev >= 0 and dev == torch.cuda.current_device():
+        if dev >= 0 and dev == torch._C._cuda_getDevice():
             return dev
     dev = None
     for t in tensors:
@@ -274,8 +288,7 @@ def _on_current_device(*tensors) -> int:
 
 
 def _raw_stream(stream, dev: int) -> int:
-    import torch
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    return (_pytorch or _torch())._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def rope_cache_write(kv_c, k_pe, positions, cos_sin, slot_mapping, cache, *, q_pe=None, q_pe_out=None,
@@ -631,7 +644,7 @@ def decode_shared(q_abs, q_pe, cache, prefix_table, prefix_lens, prefix_requests
     ``prefix_table`` [G, pages] int32, and behind them their own keys
     (``block_table``, ``seq_lens``: without the prefix).  ``workspace`` from
     decode_shared_workspace_size; errors by decode_status(workspace)."""
-    import torch
+    torch = _pytorch or _torch()
     bf16, i32 = torch.bfloat16, torch.int32
     T, N = _query(q_abs, q_pe, bf16)
     nb, ps, _ = _cache_checked(cache)
@@ -641,7 +654,8 @@ def decode_shared(q_abs, q_pe, cache, prefix_table, prefix_lens, prefix_requests
     B = _vector(seq_lens, "seq_lens", i32)
     pages = _table(block_table, "block_table", i32, B)[1]
     _dense(out, "out", bf16, (T, N, LKV))
-    _dense(workspace, "workspace", workspace.dtype, workspace.shape)
+    if not workspace.is_contiguous():
+        _dense(workspace, "workspace", workspace.dtype)
     qsl = at_lse = None
     if query_start_loc is not None:
         _vector(query_start_loc, "query_start_loc", i32, B + 1)
@@ -666,7 +680,7 @@ def key_weights(q_abs, q_pe, cache, block_table, seq_lens, lse, weights, *, scal
     the rows' log-sum-exp: decode()'s, or decode_shared()'s with the requests'
     own block table and lengths.  decay 0 does not read the old weights.  Errors
     are OR-ed into ``status`` [1] int32."""
-    import torch
+    torch = _pytorch or _torch()
     i32, f32 = torch.int32, torch.float32
     T, N = _query(q_abs, q_pe, torch.bfloat16)
     nb, ps, _ = _cache_checked(cache)
@@ -695,7 +709,7 @@ def evict_select(weights, seq_lens, keep, keep_lens, *, sinks: int = 0, recent: 
     between them, those of the largest ``weights`` [B, W] (ties: the lowest
     index).  ``keep`` gets their indices, ascending, -1 behind the last, and
     ``keep_lens`` [B] int32 (which may be ``seq_lens`` itself) their number."""
-    import torch
+    torch = _pytorch or _torch()
     i32 = torch.int32
     B = _vector(seq_lens, "seq_lens", i32)
     budget = _table(keep, "keep", i32, B)[1]
@@ -715,7 +729,7 @@ def cache_compact(cache, block_table, keep, keep_lens, *, weights=None, status=N
     (and weights[b, i] weights[b, keep[b, i]]): evict_select's choice moved to
     the front of the request's pages.  keep[b, i] >= i; the pages belong to one
     request alone."""
-    import torch
+    torch = _pytorch or _torch()
     i32 = torch.int32
     nb, ps, _ = _cache_checked(cache)
     B = _vector(keep_lens, "keep_lens", i32)
