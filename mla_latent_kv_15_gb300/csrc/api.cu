@@ -3,6 +3,7 @@
 // here allocates device memory; every buffer belongs to the caller.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -268,6 +269,12 @@ int decode_impl(const void* q_abs, const void* q_pe, const void* q8, float q_sca
   // Sq tokens gives ceil(Sq * N / 32) <= Sq groups.
   const int small_rows = !shared && !q8 && cache_dtype == MLA_BF16 && num_heads <= 32 && total_q == batch;
   const int variant = q8 ? 3 : (cache_dtype == MLA_FP8_E4M3 ? 1 : (small_rows ? 2 : 0));
+  // whether a plan of this call may have long units of many rows (a pair's span of
+  // the axis holds no more tiles than its share)
+  const int long_units =
+      shared && rows > 64 &&
+      (num_splits > 0 ? std::max(max_pages_per_seq, shared->max_pages) * (int64_t)page_size >= mla::kCodedTiles * mla::kTile
+                      : shared->tiles >= (int64_t)mla::kCodedTiles * clusters);
   cudaError_t e = shared ? mla::launch_shared_plan(seq_lens, query_start_loc, batch, num_heads, max_pages_per_seq,
                                                    page_size, num_splits, clusters, a.plan, *shared, s)
                          : mla::launch_plan(seq_lens, query_start_loc, batch, num_heads, max_pages_per_seq, page_size,
@@ -276,7 +283,7 @@ int decode_impl(const void* q_abs, const void* q_pe, const void* q8, float q_sca
   if (e != cudaSuccess) return cuda_fail(e, "plan launch");
   const bool timed = g_timing_start && g_timing_stop;
   if (timed && (e = cudaEventRecord(g_timing_start, s)) != cudaSuccess) return cuda_fail(e, "timing event");
-  e = shared ? mla::launch_decode_shared(tm_q, tm_qr, tm_kv, tm_kvr, tm_out, tm_part, variant, a, clusters, s)
+  e = shared ? mla::launch_decode_shared(tm_q, tm_qr, tm_kv, tm_kvr, tm_out, tm_part, variant, long_units, a, clusters, s)
              : mla::launch_decode(tm_q, tm_qr, tm_kv, tm_kvr, tm_out, tm_part, variant, a, clusters, s);
   if (e != cudaSuccess) return cuda_fail(e, "decode launch");
   if (timed && (e = cudaEventRecord(g_timing_stop, s)) != cudaSuccess) return cuda_fail(e, "timing event");
@@ -863,7 +870,7 @@ int mla_decode_shared(const void* q_abs, const void* q_pe, const void* cache, in
   // 64 rows (3: 1.9, 4: 2.0, 5: 2.9), e4m3 1.4 with 3 (4: 1.6, 5: 2.6; with one for
   // each 64 rows 2.2)
   const mla::SharedArgs sh{prefix_lens, prefix_requests, prefixes, max_prefix_pages, total_q,
-                           3,           cache_dtype == MLA_BF16};
+                           tiles,       3,               cache_dtype == MLA_BF16};
   return decode_impl(q_abs, q_pe, nullptr, 0.f, cache, num_blocks, page_size, cache_dtype, kv_scale, block_table,
                      max_pages_per_seq, seq_lens, batch, query_start_loc, total_q, num_heads, scale, num_splits, out,
                      lse, workspace, workspace_bytes, stream, nullptr, nullptr, &sh, prefix_table);

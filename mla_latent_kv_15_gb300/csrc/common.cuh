@@ -16,6 +16,7 @@ constexpr int kRope = 64;          // decoupled rope width (k_pe, q_pe)
 constexpr int kDqk = kLkv + kRope; // cache row width
 constexpr int kRows = 128;         // query rows per work unit (tcgen05 M)
 constexpr int kTile = 64;          // keys per tile (S MMA N, P.V MMA K)
+constexpr int kCodedTiles = 8;     // mla_decode_shared: tiles of a unit whose partial scores may be exchanged as codes
 constexpr int kMaxClusters = 128;  // upper bound of CTA pairs in the decode grid
 
 // Work-unit plan written by the scheduler kernel into the workspace.
@@ -166,6 +167,7 @@ struct SharedArgs {
   int prefixes;
   int max_pages;
   int total_q;
+  int64_t tiles;            // no plan's axis is longer
   int unit_cost, row_cost;  // of a work unit, in tiles: and for each 64 of its rows
 };
 
@@ -339,10 +341,11 @@ cudaError_t launch_shared_plan(const int32_t* seq_lens, const int32_t* qsl, int 
 cudaError_t launch_decode(const CUtensorMap& tm_q, const CUtensorMap& tm_qr, const CUtensorMap& tm_kv,
                           const CUtensorMap& tm_kvr, const CUtensorMap& tm_out, const CUtensorMap& tm_part,
                           int variant, const DecodeArgs& a, int num_clusters, cudaStream_t s);
-// the same for a plan of launch_shared_plan (variants 0 and 1)
+// the same for a plan of launch_shared_plan (variants 0 and 1); long_units: it may
+// have units of kCodedTiles tiles or more and of more than 64 rows
 cudaError_t launch_decode_shared(const CUtensorMap& tm_q, const CUtensorMap& tm_qr, const CUtensorMap& tm_kv,
                                  const CUtensorMap& tm_kvr, const CUtensorMap& tm_out, const CUtensorMap& tm_part,
-                                 int variant, const DecodeArgs& a, int num_clusters, cudaStream_t s);
+                                 int variant, int long_units, const DecodeArgs& a, int num_clusters, cudaStream_t s);
 cudaError_t launch_combine_shared(const DecodeArgs& a, int sm_count, cudaStream_t s);
 // Tensor maps: query rows (q_abs, q_pe; boxes of 64 columns x a.row_tile / 2
 // rows, 128-B swizzle), cache rows (bf16: 64 x min(page, 128), 128-B swizzle;

@@ -85,6 +85,8 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "ptx.cuh"
 
@@ -131,6 +133,22 @@ struct Layout {
 };
 constexpr int kXBuffers = 4;                      // receive ring (4: reuse needs no handshake)
 constexpr uint32_t kXRowBytes = 2 * (kTile + 8);  // exchanged bytes per row and tile: two halves, codes + header
+// kShared: the partial scores of a unit go over as they are, in float32, or
+// coded, through a ring of two buffers ([2 halves][8 chunks of 4 keys][rows][16 B],
+// or what a buffer of four holds).  Two need no handshake either: what was received
+// from the peer, whole, for a tile left it after it had read the tile before.
+// float32 saves the codes' instructions and their rounding (the log-sum-exp of 100
+// keys is then off by 1e-7 of its size, with codes by up to 2e-6), but its 32 KB a
+// tile of full rows are more than the network between the CTAs carries beside the
+// products: with it alone 64 requests of 128 heads behind 8192 keys take 173 us,
+// with codes alone 162, batches of few rows with it 2 to 6 % less.  So bf16 units of more than 64 rows
+// and kCodedTiles tiles use codes, whose errors cancel over that many keys (7e-7 of
+// 512); a launch that can have none gets the kernel without them, whose code is half
+// as long (4 requests behind 512 keys 14.7, with both 16.1).
+constexpr int kXBuffersShared = 2;
+constexpr int kXBytesShared = kTile * kRows * 4;
+constexpr int kCodedRows = 65;
+enum Exchange { kPlain, kRaw, kMixed };   // not kShared; float32 alone; float32 and codes
 // Warp roles.  Warps 0-7: softmax / exchange / O rescale / epilogue, two
 // threads per query row (warp w: TMEM lanes 32(w%4).., key half and output
 // half w/4).  Warp 8: TMA producer; 9: score-MMA issuer (and TMEM owner);
@@ -186,11 +204,13 @@ struct __align__(8) Barriers {
 // at the end of a unit, their row sums: [2][2][128] + [2][128] floats
 constexpr int kPairFloats = 2 * 2 * kRows + 2 * kRows;
 
-template <int kVariant>
+template <int kVariant, bool kShared = false>
 constexpr size_t smem_bytes() {
   return 1024 + (size_t)Layout<kVariant>::kStages * kStageBytes +
-         kXBuffers * (size_t)Layout<kVariant>::kXBytes + sizeof(Barriers) + 16 + kPairFloats * sizeof(float);
+         (kShared ? kXBuffersShared * (size_t)kXBytesShared : kXBuffers * (size_t)Layout<kVariant>::kXBytes) +
+         sizeof(Barriers) + 16 + kPairFloats * sizeof(float);
 }
+static_assert(smem_bytes<0, true>() <= 232448 && smem_bytes<1, true>() <= 232448, "shared memory per CTA");
 static_assert(smem_bytes<0>() <= 232448 && smem_bytes<1>() <= 232448 && smem_bytes<2>() <= 232448 &&
                   smem_bytes<3>() <= 232448,
               "shared memory per CTA");
@@ -391,20 +411,20 @@ __device__ __forceinline__ void expand_e4m3_tile(uint32_t stage, int t, int live
 // A prefix's tiles come from L2, for one group of 128 rows after the other, so a
 // tile takes as long as a softmax warp takes over it: 2120 cycles, of which its
 // waits are 480 and the products 1090 (64 requests of 128 heads behind 8192 keys
-// 162 us, 51 % of the tensor cores' rate over all of it; 128 samples of 16 heads
-// behind 32768 keys 180).  Three other forms were built and measured.  Partial
-// scores exchanged as float32, no codes: 173 and 198 (the network between the
-// CTAs), though batches of few rows gain 2 to 6 %.  Sixteen softmax warps, four
-// threads a row: 184 and 202.  A kernel of its own for the prefixes, with 64 whole
-// rows a CTA and no exchange: 143 and 164, but each key is loaded as a key and as
+// 164 us, 50 % of the tensor cores' rate over all of it; 128 samples of 16 heads
+// behind 32768 keys 175).  Two other forms were built and measured, where this one
+// took 162 and 188.  Sixteen softmax warps, four threads a row: 184 and 202.  A
+// kernel of its own for the prefixes, with 64 whole rows a CTA and no exchange: 143
+// and 164, but each key is loaded as a key and as
 // a value, 272 KB of L2 reads a 256-key tile and CTA, which bound it; and a call
 // over short prefixes took 5 to 13 us more for the fourth launch.
-template <int kVariant, bool kShared = false>
+template <int kVariant, int kExchange = kPlain>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kThreads, 1)
     decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_qr,
                   const __grid_constant__ CUtensorMap tm_kv, const __grid_constant__ CUtensorMap tm_kvr,
                   const __grid_constant__ CUtensorMap tm_out, const __grid_constant__ CUtensorMap tm_part,
                   const DecodeArgs a) {
+  constexpr bool kShared = kExchange != kPlain;
   constexpr int kCacheFp8 = kVariant == 1 || kVariant == 3;
   constexpr bool kQ8 = kVariant == 3;       // e4m3 query: fp8 x fp8 score MMAs
   // the epilogue's pieces leave by TMA stores (bf16 cache, 128-row units:
@@ -416,13 +436,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kTh
   // (an e4m3 tile's are zeroed as it is expanded)
   constexpr bool kCleans = kShared && !kCacheFp8;
   constexpr int kStages = Layout<kVariant>::kStages;
-  constexpr int kXBytes = Layout<kVariant>::kXBytes;
+  constexpr int kXBytes = kShared ? kXBytesShared : Layout<kVariant>::kXBytes;
+  constexpr int kRing = kShared ? kXBuffersShared : kXBuffers;
   constexpr int kXRows = Layout<kVariant>::kXRows;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t* stages = smem;
   uint8_t* x_recv = stages + kStages * kStageBytes;      // receive ring
-  Barriers* bars = reinterpret_cast<Barriers*>(x_recv + kXBuffers * kXBytes);
+  Barriers* bars = reinterpret_cast<Barriers*>(x_recv + kRing * kXBytes);
   float* pairbuf = reinterpret_cast<float*>(((uintptr_t)(bars + 1) + 15) & ~(uintptr_t)15);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -800,7 +821,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kTh
     // [2][kXRows][8 B]
     constexpr uint32_t kXChunk = (uint32_t)Layout<kVariant>::kXChunk;
     constexpr uint32_t kXHdr = (uint32_t)Layout<kVariant>::kXHdr;
+    constexpr int kEarly = 4;                // kShared: chunks of the next tile that go out while this one's come in
     const uint32_t xcode = (uint32_t)row * 16 + 4 * (uint32_t)hh * kXChunk;
+    const uint32_t xraw = (uint32_t)row * 16 + 8 * (uint32_t)hh * kXChunk;   // kShared: float32
     const uint32_t xhdr = kXHdr + (uint32_t)(hh * kXRows + row) * 8;
     const uint32_t xrecv0 = smem_u32(x_recv);
     const uint32_t xrecv_peer0 = mapa(xrecv0, peer);
@@ -813,13 +836,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kTh
     // Load this half's partial scores of tile `t` from TMEM into `dst` and
     // free the S columns; `hi` and `lo` get their largest and smallest value
     // (the reducing TMEM loads of sm_103a compute them on the way).
-    auto load_s = [&](uint32_t t, float (&dst)[kHalf], float& hi, float& lo) {
+    // `raw` (kShared): the unit's scores go over as float32; then neither.
+    auto load_s = [&](auto raw, uint32_t t, float (&dst)[kHalf], float& hi, float& lo) {
       wait_bar(ctx, &bars->s_full, t & 1);
       __syncwarp();
       tc_fence_after();
       uint32_t r[kHalf];
-      tmem_ld32_max(tl + kTmemS + kHalf * hh, r, hi);
-      tmem_ld32_min(tl + kTmemS + kHalf * hh, r, lo);
+      if constexpr (decltype(raw)::value) {
+        tmem_ld32(tl + kTmemS + kHalf * hh, r);
+      } else {
+        tmem_ld32_max(tl + kTmemS + kHalf * hh, r, hi);
+        tmem_ld32_min(tl + kTmemS + kHalf * hh, r, lo);
+      }
       tmem_wait_ld();
 #pragma unroll
       for (int c = 0; c < kHalf; ++c) dst[c] = __uint_as_float(r[c]);
@@ -862,7 +890,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kTh
     // chunk c (keys 8c..8c+7 of the half) of tile t, valid rows only
     auto send_chunk = [&](uint32_t t, const float (&src)[kHalf], const Enc& e, int c) {
       if (row < nrows_cur) {
-        const uint32_t b = t % kXBuffers;
+        const uint32_t b = t % kRing;
         uint32_t w[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -875,12 +903,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kTh
     };
     auto send_hdr = [&](uint32_t t, const Enc& e) {
       if (row < nrows_cur) {
-        const uint32_t b = t % kXBuffers;
+        const uint32_t b = t % kRing;
         st_async_v2(xrecv_peer0 + b * kXBytes + xhdr, __float_as_uint(e.ctr), __float_as_uint(e.step),
                     xfull_peer0 + b * 8);
       }
     };
-    auto send_s = [&](uint32_t t, const float (&src)[kHalf], int nvis, float hi, float lo) {
+    // kShared: chunk c (keys 4c..4c+3 of the half) of tile t as it is, valid rows only
+    auto send_raw = [&](uint32_t t, const float (&src)[kHalf], int c) {
+      if (row < nrows_cur) {
+        const uint32_t b = t % kRing;
+        st_async_v4(xrecv_peer0 + b * kXBytes + xraw + c * kXChunk, __float_as_uint(src[4 * c]),
+                    __float_as_uint(src[4 * c + 1]), __float_as_uint(src[4 * c + 2]), __float_as_uint(src[4 * c + 3]),
+                    xfull_peer0 + b * 8);
+      }
+    };
+    auto send_s = [&](auto raw, uint32_t t, const float (&src)[kHalf], int nvis, float hi, float lo) {
+      if constexpr (decltype(raw)::value) {
+#pragma unroll
+        for (int c = 0; c < kHalf / 4; ++c) send_raw(t, src, c);
+        return;
+      }
       const Enc e = make_enc(src, nvis, hi, lo);
 #pragma unroll
       for (int c = 0; c < kHalf / 8; ++c) send_chunk(t, src, e, c);
@@ -892,13 +934,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kTh
     // before the barrier, where it overlaps the wait).  `between(c)` runs
     // after chunk c is decoded (the caller sends the next tile's first
     // chunks there, so the network transfer overlaps the decoding).
-    auto recv_s = [&](uint32_t t, float (&acc)[kHalf], uint32_t nbytes, float& amax, auto&& between) -> float {
-      const uint32_t b = t % kXBuffers, use = t / kXBuffers;
+    auto recv_s = [&](auto raw, uint32_t t, float (&acc)[kHalf], uint32_t nbytes, float& amax, auto&& between) -> float {
+      const uint32_t b = t % kRing, use = t / kRing;
       if (tid == 0) mbar_expect_tx(smem_u32(&bars->x_full[b]), nbytes);
       wait_bar_cluster(ctx, &bars->x_full[b], use & 1);
       __syncwarp();
       float ctr = 0.f;
-      if (row < kXRows) {
+      if constexpr (decltype(raw)::value) {
+        const uint32_t base = xrecv0 + b * kXBytes + xraw;
+#pragma unroll
+        for (int c = 0; c < kHalf / 4; ++c) {
+          const uint4 v = lds128(base + c * kXChunk);
+          add2(acc[4 * c], acc[4 * c + 1], __uint_as_float(v.x), __uint_as_float(v.y));
+          add2(acc[4 * c + 2], acc[4 * c + 3], __uint_as_float(v.z), __uint_as_float(v.w));
+          between(c);
+        }
+      } else if (row < kXRows) {
         const uint2 h = lds64(xrecv0 + b * kXBytes + xhdr);
         ctr = __uint_as_float(h.x);
         const float step = __uint_as_float(h.y);
@@ -951,7 +1002,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kTh
       }
       // the warp needs masking only on tiles that reach past its shortest valid row
       const int lmin_warp = __reduce_min_sync(0xffffffffu, Lr);
-      const uint32_t nbytes = (uint32_t)gr.nrows * kXRowBytes;
 
       // the CTA's 288 query dims -> TMEM (A operand of the score MMAs); the
       // two halves of a row write different columns
@@ -1021,6 +1071,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kTh
       }
       tmem_wait_st();
       tc_fence_before();
+      // the previous unit's TMA stores have read their scratch (receive
+      // buffers the peer may write once this unit's first tiles go out; kShared:
+      // that of every warp, before a warp sends)
+      if constexpr (kTmaStore && kShared)
+        if (lane == 0) bulk_wait_group_read<0>();
       named_bar_softmax();
       if (tid == 0) {
         for (int qi = 0; qi < 2; ++qi) {      // two arrivals: the slot's count covers both issuers
@@ -1031,9 +1086,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kTh
       }
       item += 2;
 
-      // the previous unit's TMA stores have read their scratch (receive
-      // buffers the peer may write once this unit's first tiles go out)
-      if constexpr (kTmaStore)
+      if constexpr (kTmaStore && !kShared)
         if (lane == 0) bulk_wait_group_read<0>();
 
       float m = -INFINITY, l = 0.f;          // l: this half's share of the row sum
@@ -1041,15 +1094,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kTh
       // keys of this half of tile jj the row may see (32 on every tile before its last)
       auto nvis = [&](int jj) { return Lr - (ur.tile_begin + jj) * kTile - kHalf * hh; };
       float cur[kHalf], nxt[kHalf];
-      if (ntiles > 0) {
-        float hi, lo;
-        load_s(it, cur, hi, lo);
-        send_s(it, cur, nvis(0), hi, lo);
-      }
       // One tile: `cur` holds this tile's own partials, `nxt` receives the
       // next tile's.  With a bf16 cache the loop runs two tiles per trip with
       // the arrays swapping roles, so no copy moves `nxt` into `cur`.
-      auto tile = [&](int jj, float (&cur)[kHalf], float (&nxt)[kHalf]) {
+      auto tile = [&](auto raw, int jj, float (&cur)[kHalf], float (&nxt)[kHalf]) {
+        const uint32_t nbytes = (uint32_t)gr.nrows * (decltype(raw)::value ? kTile * 4 : kXRowBytes);
         // The next tile's partials are loaded first and sent in pieces while
         // this tile is processed: chunks 0-1 between the decoding steps of
         // this tile's received partials, chunks 2-3 and the header after its
@@ -1058,13 +1107,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kTh
         Enc en{};
         if (has_next) {
           float hi, lo;
-          load_s(it + 1, nxt, hi, lo);
-          en = make_enc(nxt, nvis(jj + 1), hi, lo);
+          load_s(raw, it + 1, nxt, hi, lo);
+          if constexpr (!decltype(raw)::value) en = make_enc(nxt, nvis(jj + 1), hi, lo);
         }
         float hmax;
         // cur = own + peer partial - cpeer
-        const float cpeer = recv_s(it, cur, nbytes, hmax, [&](int c) {
-          if (has_next && c < 2) send_chunk(it + 1, nxt, en, c);
+        const float cpeer = recv_s(raw, it, cur, nbytes, hmax, [&](int c) {
+          if constexpr (decltype(raw)::value) {
+            if (has_next && c < kEarly) send_raw(it + 1, nxt, c);
+          } else if (has_next && c < 2) {
+            send_chunk(it + 1, nxt, en, c);
+          }
         });
 
         // mask on ragged tiles (and take the max again), the max of the
@@ -1113,9 +1166,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kTh
         }
         l += lsum;
         if (has_next) {
-          send_chunk(it + 1, nxt, en, 2);
-          send_chunk(it + 1, nxt, en, 3);
-          send_hdr(it + 1, en);
+          if constexpr (decltype(raw)::value) {
+#pragma unroll
+            for (int c = kEarly; c < kHalf / 4; ++c) send_raw(it + 1, nxt, c);
+          } else {
+            send_chunk(it + 1, nxt, en, 2);
+            send_chunk(it + 1, nxt, en, 3);
+            send_hdr(it + 1, en);
+          }
         }
 
         // P and O may be touched once the P.V of the previous tile has completed
@@ -1140,27 +1198,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kTh
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bars->p_full));
       };
-      if constexpr (kCacheFp8) {
-        // e4m3 cache: one tile per trip (the unrolled form measured 8 %
-        // slower for these variants)
-        for (int jj = 0; jj < ntiles; ++jj, ++item, ++it) {
-          tile(jj, cur, nxt);
+      auto tiles = [&](auto raw) {
+        if (ntiles > 0) {
+          float hi, lo;
+          load_s(raw, it, cur, hi, lo);
+          send_s(raw, it, cur, nvis(0), hi, lo);
+        }
+        if constexpr (kCacheFp8) {
+          // e4m3 cache: one tile per trip (the unrolled form measured 8 %
+          // slower for these variants)
+          for (int jj = 0; jj < ntiles; ++jj, ++item, ++it) {
+            tile(raw, jj, cur, nxt);
 #pragma unroll
-          for (int c = 0; c < kHalf; ++c) cur[c] = nxt[c];
+            for (int c = 0; c < kHalf; ++c) cur[c] = nxt[c];
+          }
+        } else {
+          int jj = 0;
+          for (; jj + 1 < ntiles; jj += 2) {
+            tile(raw, jj, cur, nxt);
+            ++item, ++it;
+            tile(raw, jj + 1, nxt, cur);
+            ++item, ++it;
+          }
+          if (jj < ntiles) {
+            tile(raw, jj, cur, nxt);
+            ++item, ++it;
+          }
         }
-      } else {
-        int jj = 0;
-        for (; jj + 1 < ntiles; jj += 2) {
-          tile(jj, cur, nxt);
-          ++item, ++it;
-          tile(jj + 1, nxt, cur);
-          ++item, ++it;
-        }
-        if (jj < ntiles) {
-          tile(jj, cur, nxt);
-          ++item, ++it;
-        }
-      }
+      };
+      if constexpr (kExchange == kPlain)
+        tiles(std::false_type{});
+      else if constexpr (kExchange == kRaw)
+        tiles(std::true_type{});
+      else if (gr.nrows >= kCodedRows && ntiles >= kCodedTiles)
+        tiles(std::false_type{});
+      else
+        tiles(std::true_type{});
 
       if (u + 1 < uend) prefetch_unit(u + 1);
 
@@ -1180,7 +1253,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kTh
       // before last (h = 0) or of the last tile (h = 1): both are read, and
       // the peer writes into them only after it has received the next
       // unit's first tile, which this CTA sends after its epilogue.
-      const uint32_t scr = xrecv0 + ((it + 2 + (uint32_t)hh) % kXBuffers) * kXBytes + (uint32_t)q4 * 4096u;
+      // kShared: both halves' 32 KB are the last tile's buffer.
+      const uint32_t scr = kShared ? xrecv0 + ((it + 1) % kRing) * kXBytes + (uint32_t)(4 * hh + q4) * 4096u
+                                   : xrecv0 + ((it + 2 + (uint32_t)hh) % kXBuffers) * kXBytes + (uint32_t)q4 * 4096u;
       // Room for the warp's 4 KB: always with 128-row buffers; a 32-row
       // buffer (units of at most 32 rows) holds the one warp quadrant that
       // has rows.
@@ -1372,8 +1447,7 @@ namespace {
 template <class K>
 cudaError_t launch(K* kern, std::atomic<uint64_t>& done, const CUtensorMap& tm_q, const CUtensorMap& tm_qr, const CUtensorMap& tm_kv,
                    const CUtensorMap& tm_kvr, const CUtensorMap& tm_out, const CUtensorMap& tm_part, int variant,
-                   const DecodeArgs& a, int num_clusters, cudaStream_t s) {
-  const size_t smem = decode_smem_bytes(variant);
+                   size_t smem, const DecodeArgs& a, int num_clusters, cudaStream_t s) {
   cudaError_t e = allow_smem(kern, smem, done);
   if (e != cudaSuccess) return e;
   // programmatic dependent launch: the prologue (barriers, TMEM, cluster
@@ -1402,15 +1476,18 @@ cudaError_t launch_decode(const CUtensorMap& tm_q, const CUtensorMap& tm_qr, con
   auto kern = variant == 1 ? decode_kernel<1>
                            : (variant == 2 ? decode_kernel<2> : (variant == 3 ? decode_kernel<3> : decode_kernel<0>));
   static std::atomic<uint64_t> done[4];
-  return launch(kern, done[variant], tm_q, tm_qr, tm_kv, tm_kvr, tm_out, tm_part, variant, a, num_clusters, s);
+  return launch(kern, done[variant], tm_q, tm_qr, tm_kv, tm_kvr, tm_out, tm_part, variant, decode_smem_bytes(variant), a,
+                num_clusters, s);
 }
 
 cudaError_t launch_decode_shared(const CUtensorMap& tm_q, const CUtensorMap& tm_qr, const CUtensorMap& tm_kv,
                                  const CUtensorMap& tm_kvr, const CUtensorMap& tm_out, const CUtensorMap& tm_part,
-                                 int variant, const DecodeArgs& a, int num_clusters, cudaStream_t s) {
-  static std::atomic<uint64_t> done[2];
-  return launch(variant == 1 ? decode_kernel<1, true> : decode_kernel<0, true>, done[variant == 1], tm_q, tm_qr, tm_kv, tm_kvr, tm_out,
-                tm_part, variant, a, num_clusters, s);
+                                 int variant, int long_units, const DecodeArgs& a, int num_clusters, cudaStream_t s) {
+  static std::atomic<uint64_t> done[3];
+  const int which = variant == 1 ? 0 : 1 + (long_units != 0);
+  auto kern = which == 0 ? decode_kernel<1, kRaw> : (which == 1 ? decode_kernel<0, kRaw> : decode_kernel<0, kMixed>);
+  return launch(kern, done[which], tm_q, tm_qr, tm_kv, tm_kvr, tm_out, tm_part, variant,
+                variant == 1 ? smem_bytes<1, true>() : smem_bytes<0, true>(), a, num_clusters, s);
 }
 
 }  // namespace mla

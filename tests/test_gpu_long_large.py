@@ -212,3 +212,21 @@ def test_without_the_optional_arguments():
     for b in range(2):
         assert torch.equal(w.pages.rows(b, 50), before[b][keep[b].long()])
     assert lens.tolist() == [50, 50]
+
+
+@pytest.mark.parametrize("heads,sq,own,splits", [
+    (128, 1, [70, 2, 300], 1),                     # long units of full rows beside short ones, one piece each
+    (40, 2, [5, 130, 64, 1], 1), (16, 1, [100] * 9, 1), (33, 2, [2, 2000], 1),
+    (128, 1, [64] * 9, 0), (128, 1, [64, 3, 700], 2),
+])
+def test_long_units_of_many_rows(heads, sq, own, splits):
+    # units on either side of the choice of how the partial scores are exchanged, in turn on one pair
+    prefix = [(2300, len(own) - 1), (5000, 1)]
+    Case(prefix, own, heads, sq, 64, False, seed=heads, splits=splits).run().check()
+    Case(prefix, own, heads, sq, 64, True, seed=heads, splits=splits).run().check()
+
+
+def test_many_long_units():
+    # several a pair: 20 groups of rows behind 20000 keys, own keys of all sizes
+    rng = np.random.default_rng(71)
+    Case([(20000, 20), (2500, 12)], [int(x) for x in rng.integers(1, 2500, 32)], 128, 1, 64, False, seed=71).run().check()
