@@ -271,7 +271,7 @@ def _on_current_device(*tensors) -> int:
     found = {t.get_device() for t in tensors if t is not None}
     if len(found) == 1:                      # the usual case
         dev = found.pop()
-        if dev >= 0 and dev == torch._C._cuda_getDevice():
+        if dev >= 0 and dev == torch.cuda.current_device():
             return dev
     dev = None
     for t in tensors:
