@@ -137,6 +137,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* __res
   __shared__ int s_sums[2][kPlanThreads / 32];
   // of the first kPlanThreads prefixes: first request, first group, first query row
   __shared__ int s_pbegin[kShared ? kPlanThreads : 1], s_pgroup[kShared ? kPlanThreads : 1], s_prow[kShared ? kPlanThreads : 1];
+  // kShared: groups of own rows that stand behind prefix keys, a bit each
+  __shared__ unsigned s_behind[kShared && kStaged ? kPlanSmemGroups / 32 : 1];
   int sums_row = 0;
   GroupRec* grp = kStaged ? s_groups : P.groups;
   int* ucl = kStaged ? s_ucl : P.unit_cluster;
@@ -151,6 +153,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* __res
   // sync) overlaps the plan; it waits for this grid before reading the plan
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid == 0) s_flags = s_own_rows = 0;
+  if (kShared && kStaged)
+    for (int i = tid; i < kPlanSmemGroups / 32; i += kPlanThreads) s_behind[i] = 0;
   __syncthreads();
   const long long kv_cap = (long long)max_pages * page_size;
   const int gshift = __ffs(GR) - 1;   // GR is a power of two
@@ -169,6 +173,18 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* __res
     q1_ahead = qsl ? qsl[tid + 1] : tid + 1;
     seq_ahead = seq_lens[tid];
   }
+  const bool by_group = kStaged && kShared && np <= kPlanThreads;   // (s_ucl is not in use yet)
+  auto prefix_group = [&](int g, int p, int row0, int nrows, int keys) {
+    if (kStaged) s_kbase[g] = keys;   // every row sees them all
+    GroupRec r;
+    r.b = ~p;
+    r.row0 = row0;
+    r.nrows = nrows;
+    r.lmax = keys;
+    r.tiles = (keys + kTile - 1) / kTile;
+    r.pieces = r.ubase = r.tpos = 0;
+    grp[g] = r;
+  };
   for (int base = 0; base < np; base += kPlanThreads) {
     const int p = base + tid;
     int ng = 0, q0 = 0, rows = 0;
@@ -203,19 +219,28 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* __res
         keys = cap;
       }
       if (keys < 0) keys = 0;
-      for (int g = 0; g < ng && gb + g < P.max_groups; ++g) {
-        if (kStaged) s_kbase[gb + g] = (int)keys;   // every row sees them all
-        GroupRec r;
-        r.b = ~p;
-        r.row0 = q0 * N + g * GR;
-        r.nrows = min(GR, rows - g * GR);
-        r.lmax = (int)keys;
-        r.tiles = (int)((keys + kTile - 1) / kTile);
-        r.pieces = r.ubase = r.tpos = 0;
-        grp[gb + g] = r;
+      if (by_group) {
+        s_ucl[p] = (int)keys;
+        s_ucl[kPlanThreads + p] = rows;
+      } else {
+        for (int g = 0; g < ng && gb + g < P.max_groups; ++g)
+          prefix_group(gb + g, p, q0 * N + g * GR, min(GR, rows - g * GR), (int)keys);
       }
     }
     carry += total;
+  }
+  if (by_group) {
+    // a thread a group: one prefix may have them all
+    __syncthreads();
+    for (int g = tid; g < carry && g < P.max_groups; g += kPlanThreads) {
+      int lo = 0, hi = np - 1;      // the last prefix that begins at or before group g (those after it have none)
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (s_pgroup[mid] <= g) lo = mid; else hi = mid - 1;
+      }
+      const int at = (g - s_pgroup[lo]) * GR;
+      prefix_group(g, lo, s_prow[lo] + at, min(GR, s_ucl[kPlanThreads + lo] - at), s_ucl[lo]);
+    }
   }
   const int own_groups = carry;   // kShared: the first group of a request
   for (int base = 0; base < batch; base += kPlanThreads) {
@@ -390,6 +415,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* __res
         j.pre2_pieces = y.pieces;
       }
       P.joins[g] = j;
+      if (kStaged && j.pre_pieces > 0) atomicOr(&s_behind[g / 32], 1u << g % 32);
     }
     __syncthreads();
     // a unit a thread: a long prefix of few rows is one group of many pieces
@@ -402,7 +428,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* __res
       const GroupRec r = grp[lo];
       const int i = at - r.ubase, s0 = r.tpos + cost_of(r);
       // a prefix's rows are joined with their own keys, and the other way round
-      const bool partial = r.pieces > 1 || lo < own_groups || P.joins[lo].pre_pieces > 0;
+      const bool behind = kStaged ? (s_behind[lo / 32] >> lo % 32 & 1) != 0 : P.joins[lo].pre_pieces > 0;
+      const bool partial = r.pieces > 1 || lo < own_groups || behind;
       UnitRec u;
       int cl;
       u.b = r.b;
@@ -479,9 +506,15 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* __res
   }
   if (kStaged)
     for (int g = tid; g < G; g += kPlanThreads) P.groups[g] = grp[g];
-  if (tid == 0) {
+  if (kShared) {
     const int last = U > 0 ? ucl[U - 1] : -1;
-    for (int k = last + 1; k <= kMaxClusters; ++k) P.cluster_begin[k] = U;
+    for (int k = last + 1 + tid; k <= kMaxClusters; k += kPlanThreads) P.cluster_begin[k] = U;
+  }
+  if (tid == 0) {
+    if (!kShared) {
+      const int last = U > 0 ? ucl[U - 1] : -1;
+      for (int k = last + 1; k <= kMaxClusters; ++k) P.cluster_begin[k] = U;
+    }
     PlanHeader h;
     h.status = s_flags;
     h.num_groups = G;
