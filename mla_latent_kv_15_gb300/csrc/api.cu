@@ -948,6 +948,7 @@ int mla_key_weights(const void* q_abs, const void* q_pe, const void* cache, int6
                               row_tile / 2, CU_TENSOR_MAP_SWIZZLE_128B);
   if (!enc) return fail(MLA_ERR_CUDA, "cuTensorMapEncodeTiled rejected a tensor layout");
   mla::KeyWeightArgs a{};
+  a.cache = static_cast<const uint8_t*>(cache);
   a.block_table = block_table;
   a.seq_lens = seq_lens;
   a.qsl = query_start_loc;
@@ -964,6 +965,7 @@ int mla_key_weights(const void* q_abs, const void* q_pe, const void* cache, int6
   a.scale_log2 = factor;
   a.decay = decay;
   a.row_tile = row_tile;
+  a.many_rows = row_tiles > 1;
   a.status = status;
   a.wait_limit_ns = g_wait_limit_ns;
   a.debug_skip_tile = g_test_skip_tile;

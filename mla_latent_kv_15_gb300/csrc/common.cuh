@@ -174,6 +174,7 @@ struct SharedArgs {
 // mla_key_weights: the sum over a request's query rows of exp(score - lse),
 // for each of its keys.
 struct KeyWeightArgs {
+  const uint8_t* cache;
   const int32_t* block_table;
   const int32_t* seq_lens;
   const int32_t* qsl;         // may be null: one query token per request
@@ -187,6 +188,7 @@ struct KeyWeightArgs {
   float scale_log2;           // scale * log2(e) (* kv_scale for e4m3)
   float decay;
   int row_tile;               // query rows of a product: a multiple of 32, at most 256
+  int many_rows;              // more than one such tile a request, on average
   int* status;                // OR of mla_device_error bits, or null
   unsigned long long wait_limit_ns;
   int debug_skip_tile;        // test aid: the first tile's first chunk never comes

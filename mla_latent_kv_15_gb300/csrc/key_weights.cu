@@ -17,17 +17,21 @@
 // in tensor memory (four of up to 128): a tile's exponentials run under the next
 // products.
 //
-// An e4m3 cache lands as codes in a ring of its own and is expanded to bf16 by
-// seven warps.  A stage of that ring is always the same warp's (loads may land
-// out of order, and a wait two phases ahead would not wait).
+// An e4m3 cache is expanded to bf16 by warps of their own.  Where a request's rows
+// are one tile, codes land in a ring first (kCodes: a stage of it is always the
+// same one of seven warps', since loads may land out of order, and a wait two phases
+// ahead would not wait).  Where they are more, shared memory is what bounds the
+// kernel (see below), and eight warps take the codes from global memory into their
+// registers (kDirect): 512 rows 124 us instead of 135, 1024 rows 94 instead of 116;
+// but 128 rows 101 instead of 79, with too little on its way.
 //
 // Measured (a launch in a graph): 64 requests of 1024 to 8192 keys, 128 heads,
 // bf16 60.4 us, HBM at 90 % of the copy rate; 32 requests of 2048 to 16384 keys
-// with four verified tokens (512 rows) 105 in bf16, 92 % of the tensor cores'
-// rate, and 131 to 135 over e4m3 rows: there shared memory is the limit, which
-// takes the codes, gives them to the expanding warps, takes the bf16 rows back and
-// gives them to two row tiles' products.  One request of 777 keys and 16 heads
-// 7.0: a chain of loads, nine chunks' products and the sums.
+// with four verified tokens (512 rows) 105 in bf16, 92 % of the tensor cores' rate,
+// and 123 over e4m3 rows: there shared memory is the limit, which takes the expanded
+// rows (in kCodes the codes too, and gives them back) and gives them to two row
+// tiles' products beside the queries.  One request of 777 keys and 16 heads 7.0: a
+// chain of loads, nine chunks' products and the sums.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -51,20 +55,25 @@ constexpr uint32_t kRawRow = kRawChunks * 64, kRawBytes = kRawKeys * kRawRow;
 constexpr int kRowTile = 256;                  // query rows of a product at most (its columns)
 constexpr int kMaxQStages = 8;
 constexpr int kWarpK = 0, kWarpQ = 1, kWarpMma = 2, kWarpEpilogue = 4, kWarpExpand = 12;
-constexpr int kExpandWarps = 7;                // each has one stage of the ring of codes to itself
+constexpr int kExpandWarps = 7;                // kCodes: each has one stage of the ring to itself
+constexpr int kDirectWarps = 8;
+static_assert(kDirectWarps % (kKeys / kRawKeys) == 0, "a warp always has the same 32 of a CTA's keys");
 constexpr int kLseRows = 1024;                 // rows of a request whose lse is kept on chip
 // e4m3: registers a thread of the issuing warps, the epilogue's and the
-// expanding ones, of the launch's 96 for each of its five warpgroups
-constexpr uint32_t kRegsIssue = 56, kRegsEpilogue = 112, kRegsExpand = 96;
-static_assert(kRegsIssue + 2 * kRegsEpilogue + 2 * kRegsExpand <= 5 * 96, "register split");
+// expanding ones (kDirect: of both), of the launch's 96 for each of its five warpgroups
+constexpr uint32_t kRegsIssue = 56, kRegsEpilogue = 112, kRegsExpand = 96, kRegsDirect = 104;
+static_assert(kRegsIssue + 2 * kRegsEpilogue + 2 * kRegsExpand <= 5 * 96 && kRegsIssue + 4 * kRegsDirect <= 5 * 96,
+              "register split");
 constexpr float kLog2e = 1.4426950408889634f;
 
-template <bool kFp8>
+enum Kind { kBf16, kCodes, kDirect };   // the cache's rows; e4m3 ones by a ring of codes, or straight into registers
+
+template <int kKind>
 struct Shape {
-  static constexpr int kThreads = kFp8 ? 640 : 384;
+  static constexpr int kThreads = kKind == kBf16 ? 384 : 640;
   static constexpr int kKSlots = kChunks;
-  static constexpr uint32_t kQRegion = kFp8 ? 32768 : 65536;   // as many stages of a CTA's half of a row tile as fit
-  static constexpr int kRawStages = kFp8 ? kExpandWarps : 0;
+  static constexpr uint32_t kQRegion = kKind == kCodes ? 32768 : 65536;   // as many stages of a CTA's half of a row tile as fit
+  static constexpr int kRawStages = kKind == kCodes ? kExpandWarps : 0;
   static constexpr uint32_t kQAt = kKSlots * kKBytes;
   static constexpr uint32_t kRawAt = kQAt + kQRegion;
   static constexpr uint32_t kBarsAt = kRawAt + kRawStages * kRawBytes;
@@ -89,11 +98,12 @@ struct Bars {
   float half[2][kKeys];            // sums of the second half of the columns
 };
 
-template <bool kFp8>
+template <int kKind>
 constexpr size_t smem_bytes() {
-  return 1024 + Shape<kFp8>::kBarsAt + sizeof(Bars);
+  return 1024 + Shape<kKind>::kBarsAt + sizeof(Bars);
 }
-static_assert(smem_bytes<false>() <= 232448 && smem_bytes<true>() <= 232448, "shared memory per CTA");
+static_assert(smem_bytes<kBf16>() <= 232448 && smem_bytes<kCodes>() <= 232448 && smem_bytes<kDirect>() <= 232448,
+              "shared memory per CTA");
 
 struct Ctx {
   Bars* bars;
@@ -140,6 +150,16 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
+// 16 bytes that are read once
+__device__ __forceinline__ uint4 ld_once(const uint8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
 // 16 e4m3 codes -> 16 bf16 values (exact)
 __device__ __forceinline__ void widen16(const uint4 v, uint32_t (&o)[8]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -162,11 +182,12 @@ struct Request {
   int row_tiles;
 };
 
-template <bool kFp8>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kFp8>::kThreads, 1)
+template <int kKind>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kKind>::kThreads, 1)
     key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_qr,
                        const __grid_constant__ CUtensorMap tm_kv, const KeyWeightArgs a) {
-  using S = Shape<kFp8>;
+  using S = Shape<kKind>;
+  constexpr bool kFp8 = kKind != kBf16;
   constexpr int kThreads = S::kThreads;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -320,7 +341,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kFp8>::kThread
     // ------------------------------------------------------------------- keys
     uint32_t n = 0;                                // loads so far
     constexpr int kLoadKeys = kFp8 ? kRawKeys : kKeys;
-    constexpr uint32_t kSlots = kFp8 ? S::kRawStages : S::kKSlots;
+    constexpr uint32_t kSlots = kFp8 ? kExpandWarps : S::kKSlots;
     const int sub_rows = a.page_size < kLoadKeys ? a.page_size : kLoadKeys;
     const int nsub = kLoadKeys / sub_rows;         // boxes of a load
     const uint64_t pol = l2_policy_evict_first();
@@ -369,8 +390,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kFp8>::kThread
     });
     // every load has landed before the CTA ends (the leader's barriers count both CTAs')
     if constexpr (kFp8) {
-      for (uint32_t k = n > S::kRawStages ? n - S::kRawStages : 0; k < n && !*abort_flag; ++k)
-        wait(ctx, &bars->raw_full[k % S::kRawStages], (k / S::kRawStages) & 1);
+      for (uint32_t k = n > kSlots ? n - kSlots : 0; k < n && !*abort_flag; ++k)
+        wait(ctx, &bars->raw_full[k % kSlots], (k / kSlots) & 1);
     } else if (rank == 0) {
       for (uint32_t k = n > S::kKSlots ? n - S::kKSlots : 0; k < n && !*abort_flag; ++k)
         wait(ctx, &bars->k_full[k % S::kKSlots], (k / S::kKSlots) & 1);
@@ -509,6 +530,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kFp8>::kThread
       }
     });
   };
+  // 32 keys' codes of chunks c.. as bf16 into their places, 32 h of the CTA's keys on
+  auto store_widened = [&](const uint4(&v)[kRawBytes / 16 / 32], int c, int h) {
+    uint8_t* dst = smem + c * kKBytes + h * kRawKeys * 128;
+#pragma unroll
+    for (int k = 0; k < kRawBytes / 16 / 32; ++k) {
+      // 16 codes: part q of row `row`, columns 16 (q % 4) of chunk q / 4
+      const int at = lane + 32 * k, row = at / 12, q = at % 12, p = 2 * (q & 3);
+      uint32_t o[8];
+      widen16(v[k], o);
+      uint4* to = reinterpret_cast<uint4*>(dst + (q >> 2) * kKBytes + row * 128);
+      to[p ^ (row & 7)] = make_uint4(o[0], o[1], o[2], o[3]);
+      to[(p + 1) ^ (row & 7)] = make_uint4(o[4], o[5], o[6], o[7]);
+    }
+    // the writes are in this CTA's shared memory, for the tensor cores to read,
+    // before the leader hears of them
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane < kRawChunks) mbar_arrive_remote(mapa(smem_u32(&bars->k_full[c + lane]), 0));
+  };
   auto expand = [&]() {
     // -------------------------------------------------------- e4m3 expansion
     const uint32_t mine = (uint32_t)(warp - kWarpExpand);   // the warp's stage
@@ -536,23 +576,61 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kFp8>::kThread
 #pragma unroll
           for (int k = 0; k < kRawChunks; ++k) wait(ctx, &bars->k_empty[c + k], (tile & 1) ^ 1);
           __syncwarp();
-          uint8_t* dst = smem + c * kKBytes + h * kRawKeys * 128;
-#pragma unroll
-          for (int k = 0; k < kPieces; ++k) {
-            // 16 codes: piece q of row `row`, columns 16 (q % 4) of chunk q / 4
-            const int at = lane + 32 * k, row = at / 12, q = at % 12, p = 2 * (q & 3);
-            uint32_t o[8];
-            widen16(v[k], o);
-            uint4* to = reinterpret_cast<uint4*>(dst + (q >> 2) * kKBytes + row * 128);
-            to[p ^ (row & 7)] = make_uint4(o[0], o[1], o[2], o[3]);
-            to[(p + 1) ^ (row & 7)] = make_uint4(o[4], o[5], o[6], o[7]);
-          }
-          // the writes are in this CTA's shared memory, for the tensor cores to
-          // read, before the leader hears of them
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane < kRawChunks) mbar_arrive_remote(mapa(smem_u32(&bars->k_full[c + lane]), 0));
+          store_widened(v, c, h);
         }
+      }
+      ++tile;
+    });
+  };
+
+  auto expand_direct = [&]() {
+    // -------------------------------------- e4m3 expansion from global memory
+    const uint32_t mine = (uint32_t)(warp - kWarpExpand);
+    const int h = (int)mine % (kKeys / kRawKeys);  // the warp's 32 of the CTA's keys
+    const int shift = __ffs(a.page_size) - 1;      // (page sizes are powers of two)
+    uint32_t piece = 0, tile = 0;                  // pieces of 32 keys x three chunks, and tiles, so far
+    bool skip = a.debug_skip_tile && bars->leads && rank == 0;
+    // the page of the lane's key of a tile, -1 behind the last; the next tile's is
+    // looked up ahead
+    auto page_of = [&](int b, const Request& r, int t) {
+      const int key = t * kPairKeys + kKeys * (int)rank + kRawKeys * h + lane;
+      return key < r.n ? a.block_table[(int64_t)b * a.max_pages + (key >> shift)] : -1;
+    };
+    int ahead_b = -1, ahead_t = 0, ahead = -1;
+    for_tiles([&](int b, const Request& r, int t) {
+      if (r.row_tiles == 0) return;
+      const int key = t * kPairKeys + kKeys * (int)rank + kRawKeys * h + lane;
+      const int blk = ahead_b == b && ahead_t == t ? ahead : page_of(b, r, t);
+      ahead_b = b, ahead_t = t + 1, ahead = page_of(b, r, t + 1);
+      int y = -1;                                  // the lane's cache row: none reads zeros
+      if (key < r.n) {
+        if (blk >= 0 && blk < a.num_blocks)
+          y = (blk << shift) + (key & (a.page_size - 1));
+        else
+          raise(ctx, 4);   // MLA_DEVERR_BAD_BLOCK
+      }
+      for (int i = 0; i < kChunks / kRawChunks * (kKeys / kRawKeys); ++i, ++piece) {
+        if (piece % kDirectWarps != mine) continue;
+        if (skip) {        // test aid: the first piece never comes
+          skip = false;
+          continue;
+        }
+        const int c = i / (kKeys / kRawKeys) * kRawChunks;
+        constexpr int kPieces = kRawBytes / 16 / 32;
+        uint4 v[kPieces];
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k) {
+          // 16 codes: part q of row `row`, columns 16 (q % 4) of chunk q / 4
+          const int at = lane + 32 * k, row = at / 12, q = at % 12;
+          const int from = __shfl_sync(0xffffffffu, y, row);
+          v[k] = make_uint4(0, 0, 0, 0);
+          if (from >= 0) v[k] = ld_once(a.cache + (int64_t)from * kDqk + 64 * c + 16 * q);
+        }
+        // (as above: the warp's piece before this one is eight back)
+#pragma unroll
+        for (int k = 0; k < kRawChunks; ++k) wait(ctx, &bars->k_empty[c + k], (tile & 1) ^ 1);
+        __syncwarp();
+        store_widened(v, c, h);
       }
       ++tile;
     });
@@ -562,15 +640,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kFp8>::kThread
     // each warpgroup sets its register budget
     if (warp < kWarpEpilogue) {
       setmaxnreg_dec<kRegsIssue>();
-      if (warp == kWarpK)
-        load_keys();
-      else if (warp == kWarpQ)
+      if constexpr (kKind == kCodes)
+        if (warp == kWarpK) load_keys();
+      if (warp == kWarpQ)
         load_queries();
       else if (warp == kWarpMma)
         multiply();
     } else if (warp < kWarpExpand) {
-      setmaxnreg_inc<kRegsEpilogue>();
+      setmaxnreg_inc<kKind == kDirect ? kRegsDirect : kRegsEpilogue>();
       epilogue();
+    } else if constexpr (kKind == kDirect) {
+      setmaxnreg_inc<kRegsDirect>();
+      expand_direct();
     } else {
       setmaxnreg_dec<kRegsExpand>();
       expand();
@@ -604,11 +685,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kFp8>::kThread
   }
 }
 
-template <bool kFp8>
+template <int kKind>
 cudaError_t launch(const CUtensorMap& tm_q, const CUtensorMap& tm_qr, const CUtensorMap& tm_kv, const KeyWeightArgs& a,
                    int sm_count, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(key_weights_kernel<kFp8>, smem_bytes<kFp8>(), done);
+  cudaError_t e = allow_smem(key_weights_kernel<kKind>, smem_bytes<kKind>(), done);
   if (e != cudaSuccess) return e;
   // no more pairs than tiles there can be
   const int64_t reach = (int64_t)a.max_pages * a.page_size < a.weight_len ? (int64_t)a.max_pages * a.page_size
@@ -617,15 +698,15 @@ cudaError_t launch(const CUtensorMap& tm_q, const CUtensorMap& tm_qr, const CUte
   const int pairs = sm_count / 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2u * (unsigned)(most < pairs ? (most > 0 ? most : 1) : pairs));
-  cfg.blockDim = dim3(Shape<kFp8>::kThreads);
-  cfg.dynamicSmemBytes = smem_bytes<kFp8>();
+  cfg.blockDim = dim3(Shape<kKind>::kThreads);
+  cfg.dynamicSmemBytes = smem_bytes<kKind>();
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, key_weights_kernel<kFp8>, tm_q, tm_qr, tm_kv, a);
+  e = cudaLaunchKernelEx(&cfg, key_weights_kernel<kKind>, tm_q, tm_qr, tm_kv, a);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
@@ -634,7 +715,9 @@ cudaError_t launch(const CUtensorMap& tm_q, const CUtensorMap& tm_qr, const CUte
 
 cudaError_t launch_key_weights(const CUtensorMap& tm_q, const CUtensorMap& tm_qr, const CUtensorMap& tm_kv, int fp8,
                                const KeyWeightArgs& a, int sm_count, cudaStream_t s) {
-  return fp8 ? launch<true>(tm_q, tm_qr, tm_kv, a, sm_count, s) : launch<false>(tm_q, tm_qr, tm_kv, a, sm_count, s);
+  // (more than one row tile a request, on average: see above)
+  if (fp8 && a.many_rows) return launch<kDirect>(tm_q, tm_qr, tm_kv, a, sm_count, s);
+  return fp8 ? launch<kCodes>(tm_q, tm_qr, tm_kv, a, sm_count, s) : launch<kBf16>(tm_q, tm_qr, tm_kv, a, sm_count, s);
 }
 
 }  // namespace mla

@@ -230,3 +230,34 @@ def test_many_long_units():
     # several a pair: 20 groups of rows behind 20000 keys, own keys of all sizes
     rng = np.random.default_rng(71)
     Case([(20000, 20), (2500, 12)], [int(x) for x in rng.integers(1, 2500, 32)], 128, 1, 64, False, seed=71).run().check()
+
+
+@pytest.mark.parametrize("page", [16, 64, 256])
+def test_key_weights_of_e4m3_rows_and_many_query_rows(page):
+    # on either side of one tile of rows a request, with bad pages, empty and padded requests, waits that run out
+    Weights([700, 0, 129, 1500, 1], 128, 3, page, True, seed=page).run(0.5).check()
+    Weights([700, 0, 129, 1500, 1], 128, [2, 0, 9, 1, 0], page, True, seed=page).run(0.0, status=None)
+    w = Weights([300, 200], 128, 4, page, True, seed=81)
+    w.pages.table[0, 0] = 10 ** 6
+    w.run()
+    torch.cuda.synchronize()
+    assert w.status.item() == 4 and w.weights.isfinite().all()
+    w = Weights([300, 200], 128, 4, page, True, seed=82)
+    try:
+        mla.set_decode_wait_test(True, 2_000_000)
+        w.run()
+    finally:
+        mla.set_decode_wait_test(False, 0)
+    torch.cuda.synchronize()
+    assert w.status.item() & mla.DEVERR_TIMEOUT
+    w.status.zero_()
+    w.run(0.0).check()
+
+
+def test_key_weights_of_many_query_rows_are_the_same_every_time():
+    w = Weights([3000, 2500, 900], 128, 5, 64, True, seed=83).run(0.0).check()
+    want = w.weights.clone()
+    for _ in range(5):
+        w.run(0.0)
+        torch.cuda.synchronize()
+        assert torch.equal(w.weights, want)
