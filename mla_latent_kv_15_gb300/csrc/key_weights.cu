@@ -22,13 +22,14 @@
 // same one of seven warps', since loads may land out of order, and a wait two phases
 // ahead would not wait).  Where they are more, shared memory is what bounds the
 // kernel (see below), and eight warps take the codes from global memory into their
-// registers (kDirect): 512 rows 124 us instead of 135, 1024 rows 94 instead of 116;
-// but 128 rows 101 instead of 79, with too little on its way.
+// registers (kDirect): 512 rows 124 us instead of 135, 1024 rows 94 instead of 116
+// (both less since, see store_widened); but 128 rows 101 instead of 79, with too
+// little on its way.
 //
 // Measured (a launch in a graph): 64 requests of 1024 to 8192 keys, 128 heads,
 // bf16 60.4 us, HBM at 90 % of the copy rate; 32 requests of 2048 to 16384 keys
 // with four verified tokens (512 rows) 105 in bf16, 92 % of the tensor cores' rate,
-// and 123 over e4m3 rows: there shared memory is the limit, which takes the expanded
+// and 116 over e4m3 rows: there shared memory is the limit, which takes the expanded
 // rows (in kCodes the codes too, and gives them back) and gives them to two row
 // tiles' products beside the queries.  One request of 777 keys and 16 heads 7.0: a
 // chain of loads, nine chunks' products and the sums.
