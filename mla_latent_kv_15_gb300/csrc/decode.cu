@@ -367,9 +367,9 @@ __device__ __forceinline__ void expand_e4m3_tile(uint32_t stage, int t, int live
   // 16-byte chunk in the row, row (key), box of the thread's k-th piece
   auto place = [&](int k, int& q, int& r, int& p) {
     const int i = t + 128 * k;
-    q = i & 3;
-    r = kShared ? i >> 4 : (i >> 2) & 63;
-    p = kShared ? (i >> 2) & 3 : i >> 8;
+    q = t & 3;
+    r = kShared ? (t >> 4) + 8 * k : (i >> 2) & 63;
+    p = kShared ? (t >> 2) & 3 : i >> 8;
   };
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
