@@ -22,17 +22,21 @@
 // same one of seven warps', since loads may land out of order, and a wait two phases
 // ahead would not wait).  Where they are more, shared memory is what bounds the
 // kernel (see below), and eight warps take the codes from global memory into their
-// registers (kDirect): 512 rows 124 us instead of 135, 1024 rows 94 instead of 116
-// (both less since, see store_widened); but 128 rows 101 instead of 79, with too
-// little on its way.
+// registers (kDirect).  32 requests of 2048 to 16384 keys, kCodes and kDirect: 128
+// rows 77 and 92 us, 192 80 and 95, 256 84 and 98, with too little on its way; 320
+// rows 117 and 115, 384 129 and 117, 512 136 and 123.
 //
 // Measured (a launch in a graph): 64 requests of 1024 to 8192 keys, 128 heads,
 // bf16 60.4 us, HBM at 90 % of the copy rate; 32 requests of 2048 to 16384 keys
 // with four verified tokens (512 rows) 105 in bf16, 92 % of the tensor cores' rate,
-// and 116 over e4m3 rows: there shared memory is the limit, which takes the expanded
-// rows (in kCodes the codes too, and gives them back) and gives them to two row
-// tiles' products beside the queries.  One request of 777 keys and 16 heads 7.0: a
-// chain of loads, nine chunks' products and the sums.
+// and 124 over e4m3 rows: there shared memory takes the expanded rows (in kCodes the
+// codes too, and gives them back) and gives them to two row tiles' products beside
+// the queries, and what the second CTA expanded is released to the leader (see
+// pass_on).  In kCodes that release is part of a chain: a chunk's place is free,
+// its codes are widened, released, multiplied, and the place is free again once a
+// tile (128 rows 77, 64 requests of 16 heads 143, where bf16 rows take 59 and 108).
+// One request of 777 keys and 16 heads 7.0: a chain of loads, nine chunks' products
+// and the sums.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -84,6 +88,7 @@ struct Shape {
 struct Bars {
   uint64_t k_full[kChunks], q_full[kMaxQStages];  // (lead) both CTAs' halves are there
   uint64_t k_empty[kChunks], q_empty[kMaxQStages];
+  uint64_t k_here[kChunks / kRawChunks];   // e4m3: the second CTA's expanded chunks, three at a time
   uint64_t raw_full[kExpandWarps], raw_empty[kExpandWarps];
   uint64_t d_full[4];
   uint64_t d_empty[4];             // (lead) the epilogue warps of both CTAs
@@ -116,11 +121,13 @@ __device__ __forceinline__ void raise(const Ctx& c, int bit) {
   if (c.status) atomicOr(c.status, bit);
 }
 
+// kCluster: the acquire covers what the other CTA's threads wrote.
+template <bool kCluster = false>
 __device__ __forceinline__ void wait(const Ctx& c, uint64_t* bar, uint32_t parity) {
   const uint32_t at = smem_u32(bar);
-  if (mbar_try_wait(at, parity)) return;
+  if (kCluster ? mbar_try_wait_cluster(at, parity) : mbar_try_wait(at, parity)) return;
   const uint64_t t0 = globaltimer();
-  while (!mbar_try_wait_hint(at, parity, kWaitHintNs)) {
+  while (!(kCluster ? mbar_try_wait_cluster_hint(at, parity, kWaitHintNs) : mbar_try_wait_hint(at, parity, kWaitHintNs))) {
     if (*(volatile int*)&c.bars->abort) return;
     if (globaltimer() - t0 > c.limit_ns) {
       *(volatile int*)&c.bars->abort = 1;
@@ -137,9 +144,11 @@ __device__ __forceinline__ bool stopped(const Ctx& c) {
 }
 
 // A wait of a whole warp; false once the CTA has given up.
+template <bool kCluster = false>
 __device__ __forceinline__ bool wait_warp(const Ctx& c, uint64_t* bar, uint32_t parity) {
-  if (__all_sync(0xffffffffu, mbar_try_wait(smem_u32(bar), parity))) return true;
-  wait(c, bar, parity);
+  const uint32_t at = smem_u32(bar);
+  if (__all_sync(0xffffffffu, kCluster ? mbar_try_wait_cluster(at, parity) : mbar_try_wait(at, parity))) return true;
+  wait<kCluster>(c, bar, parity);
   return !stopped(c);
 }
 
@@ -200,9 +209,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kKind>::kThrea
 
   if (tid == 0) {
     for (int i = 0; i < S::kKSlots; ++i) {
-      mbar_init(smem_u32(&bars->k_full[i]), kFp8 ? 2 * kKeys / kRawKeys : 2);   // each CTA's load, or expanded loads
+      // each CTA's load, or the leader's expanded loads and the other CTA's word of its own
+      mbar_init(smem_u32(&bars->k_full[i]), kFp8 ? kKeys / kRawKeys + 1 : 2);
       mbar_init(smem_u32(&bars->k_empty[i]), 1);
     }
+    for (int i = 0; i < kChunks / kRawChunks; ++i) mbar_init(smem_u32(&bars->k_here[i]), kKeys / kRawKeys);
     for (int i = 0; i < kMaxQStages; ++i) {
       mbar_init(smem_u32(&bars->q_full[i]), 2);
       mbar_init(smem_u32(&bars->q_empty[i]), 1);
@@ -432,7 +443,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kKind>::kThrea
         for (int rt = 0; rt < r.row_tiles; ++rt, d.next(accs)) {
           if (!wait_warp(ctx, &bars->d_empty[d.at], (d.round & 1) ^ 1)) return;
           for (int c = 0; c < kChunks; ++c, q.next(q_stages)) {
-            if (rt == 0 && !wait_warp(ctx, &bars->k_full[c], tile & 1)) return;
+            if (rt == 0 && !wait_warp<kFp8>(ctx, &bars->k_full[c], tile & 1)) return;
             if (!wait_warp(ctx, &bars->q_full[q.at], q.round & 1)) return;
             tc_fence_after();
             if (elect_one()) {
@@ -452,6 +463,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kKind>::kThrea
       if (elect_one()) mma_commit_pair(smem_u32(&bars->drain));
       __syncwarp();
       wait(ctx, &bars->drain, 0);
+    }
+  };
+  auto pass_on = [&]() {
+    // ------------------------- e4m3: the second CTA's expanded keys, to the leader
+    // Plain writes to shared memory that the leader's products read need a release
+    // at the cluster's scope.  It takes some 1700 cycles, so the expanding warps leave
+    // it to this one, which has nothing else to do (a release by each of them: 512
+    // rows 135 us instead of 124, 128 rows 91 instead of 77, 16 heads 158 instead of
+    // 143; three warps that release three chunks each: 128, 85, 157, since releases
+    // of a CTA hold one another up).
+    if (rank == 1) {
+      uint32_t tile = 0;
+      for_tiles([&](int, const Request& r, int) {
+        if (r.row_tiles == 0) return;
+        for (int c = 0; c < kChunks; c += kRawChunks) {
+          if (!wait_warp(ctx, &bars->k_here[c / kRawChunks], tile & 1)) return;
+          if (lane < kRawChunks) mbar_arrive_release_cluster(mapa(smem_u32(&bars->k_full[c + lane]), 0));
+          __syncwarp();
+        }
+        ++tile;
+      });
     }
   };
   auto epilogue = [&]() {
@@ -536,7 +568,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kKind>::kThrea
     uint8_t* dst = smem + c * kKBytes + h * kRawKeys * 128;
     // 16 codes: part q of row `row`, columns 16 (q % 4) of chunk q / 4; eight rows on
     // after every three of them.  (With an address for each of the twelve the code
-    // was a third longer, and 16 heads over e4m3 rows took 144 us instead of 115.)
+    // was a third longer, and 16 heads over e4m3 rows took a quarter more time.)
 #pragma unroll
     for (int m = 0; m < 3; ++m) {
       const int at = lane + 32 * m, row = at / 12, q = at % 12, p = 2 * (q & 3);
@@ -552,10 +584,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kKind>::kThrea
       }
     }
     // the writes are in this CTA's shared memory, for the tensor cores to read,
-    // before the leader hears of them
+    // before the leader hears of them: of the other CTA's by pass_on()
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane < kRawChunks) mbar_arrive_remote(mapa(smem_u32(&bars->k_full[c + lane]), 0));
+    if (rank == 0) {
+      if (lane < kRawChunks) mbar_arrive(smem_u32(&bars->k_full[c + lane]));
+    } else if (lane == 0) {
+      mbar_arrive(smem_u32(&bars->k_here[c / kRawChunks]));
+    }
   };
   auto expand = [&]() {
     // -------------------------------------------------------- e4m3 expansion
@@ -654,10 +690,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kKind>::kThrea
       setmaxnreg_dec<kRegsIssue>();
       if constexpr (kKind == kCodes)
         if (warp == kWarpK) load_keys();
-      if (warp == kWarpQ)
+      if (warp == kWarpQ) {
         load_queries();
-      else if (warp == kWarpMma)
+      } else if (warp == kWarpMma) {
         multiply();
+        pass_on();
+      }
     } else if (warp < kWarpExpand) {
       setmaxnreg_inc<kKind == kDirect ? kRegsDirect : kRegsEpilogue>();
       epilogue();
