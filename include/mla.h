@@ -687,7 +687,10 @@ MLA_API int mla_evict_select(const float* weights, int64_t weight_stride, int we
  *   cache        bf16 or e4m3 rows of 576, any page_size >= 1, num_blocks *
  *                page_size < 2^31
  *   weights      as for mla_key_weights, or NULL
- *   status       one int32 on the device, or NULL: OR-ed into, never cleared
+ *   status       one int32 on the device, or NULL: OR-ed into, never cleared;
+ *                MLA_DEVERR_TIMEOUT too: some rows and weights have then been
+ *                moved and others not, and those of the call's requests are
+ *                undefined
  * cache, weights and status overlap no other argument.  One launch.
  */
 MLA_API int mla_cache_compact(void* cache, int64_t num_blocks, int page_size, int cache_dtype,
@@ -707,8 +710,8 @@ MLA_API int mla_cache_compact(void* cache, int64_t num_blocks, int page_size, in
  * runs out.  The decode still returns; its outputs are then undefined and the
  * error word reports the timeout.  mla_prefill takes both settings in the same
  * way (the skipped tile is the first keys of its first CTA), and so do
- * mla_decode_shared and mla_key_weights.  Call with (0, 0) to restore the
- * defaults.
+ * mla_decode_shared, mla_key_weights and mla_cache_compact (the first
+ * request's first row).  Call with (0, 0) to restore the defaults.
  */
 MLA_API int mla_set_decode_wait_test(int skip_first_tile, unsigned long long wait_limit_ns);
 

@@ -477,7 +477,8 @@ def set_decode_wait_test(skip_first_tile: bool = False, wait_limit_ns: int = 0) 
     run with every wait bounded by ``wait_limit_ns`` (0: the default 1 s) and,
     with ``skip_first_tile``, one CTA never loads its first cache tile, so a
     wait for it runs out and the device error word gets DEVERR_TIMEOUT.
-    Later prefills, shared decodes and key weights of the thread do the same."""
+    Later prefills, shared decodes, key weights and compactions of the thread do
+    the same."""
     _check(load().mla_set_decode_wait_test(int(bool(skip_first_tile)), int(wait_limit_ns)))
 
 
@@ -728,7 +729,8 @@ def cache_compact(cache, block_table, keep, keep_lens, *, weights=None, status=N
     """Row i of request b becomes its row keep[b, i], i < keep_lens[b], in place
     (and weights[b, i] weights[b, keep[b, i]]): evict_select's choice moved to
     the front of the request's pages.  keep[b, i] >= i; the pages belong to one
-    request alone."""
+    request alone.  Errors are OR-ed into ``status`` [1] int32; after
+    DEVERR_TIMEOUT the requests' rows and weights are undefined."""
     torch = _pytorch or _torch()
     i32 = torch.int32
     nb, ps, _ = _cache_checked(cache)

@@ -1036,7 +1036,8 @@ int mla_cache_compact(void* cache, int64_t num_blocks, int page_size, int cache_
   const int sms = sm_count();
   if (sms < 1) return fail(MLA_ERR_CUDA, "cannot query the current device");
   const mla::CompactArgs a{static_cast<uint8_t*>(cache), num_blocks, page_size, block_table, max_pages_per_seq, keep,
-                           keep_lens, batch, max_keep, weights, weight_stride, weight_len, status};
+                           keep_lens, batch, max_keep, weights, weight_stride, weight_len, status,
+                           g_wait_limit_ns, g_test_skip_tile};
   cudaError_t e = mla::launch_compact(a, row_bytes, sms, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "compaction launch");
   return ok();

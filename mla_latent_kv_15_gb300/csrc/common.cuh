@@ -209,6 +209,8 @@ struct CompactArgs {
   int64_t weight_stride;
   int weight_len;
   int* status;                // OR of mla_device_error bits, or null
+  unsigned long long wait_limit_ns;
+  int debug_skip_tile;        // test aid: the first request's first row never comes
 };
 
 // mla_evict_select: the indices of the keys each request keeps.

@@ -67,20 +67,21 @@ __device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t byt
                : "memory");
 }
 
-// A bounded wait; false once some wait of the CTA has run out.
-__device__ __forceinline__ bool wait(Bars* bars, int* status, uint64_t* bar, uint32_t parity) {
+// A bounded wait of a whole warp; false, for all of it alike, once some wait of the
+// CTA has run out.
+__device__ __forceinline__ bool wait(Bars* bars, const CompactArgs& a, uint64_t* bar, uint32_t parity) {
   const uint32_t at = smem_u32(bar);
-  if (mbar_try_wait(at, parity)) return true;
+  if (__all_sync(0xffffffffu, mbar_try_wait(at, parity))) return true;
   const uint64_t t0 = globaltimer();
   while (!mbar_try_wait_hint(at, parity, kWaitHintNs)) {
-    if (*(volatile int*)&bars->abort) return false;
-    if (globaltimer() - t0 > MLA_WAIT_LIMIT_NS) {
+    if (*(volatile int*)&bars->abort) break;
+    if (globaltimer() - t0 > a.wait_limit_ns) {
       *(volatile int*)&bars->abort = 1;
-      if (status) atomicOr(status, 1);        // MLA_DEVERR_TIMEOUT
-      return false;
+      if (a.status) atomicOr(a.status, 1);    // MLA_DEVERR_TIMEOUT
+      break;
     }
   }
-  return true;
+  return !__any_sync(0xffffffffu, *(volatile int*)&bars->abort);
 }
 
 template <int kRowBytes>
@@ -151,7 +152,7 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactArgs a, 
           }
         }
       }
-      if (!wait(bars, a.status, &bars->look_empty[at], ((w / kLook) & 1) ^ 1)) break;
+      if (!wait(bars, a, &bars->look_empty[at], ((w / kLook) & 1) ^ 1)) break;
       bars->src[at][lane] = src;
       bars->dst[at][lane] = dst;
       bars->weight[at][lane] = weight;
@@ -162,12 +163,14 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactArgs a, 
     // ---------------------------------------------------------------- loads
     for (int w = 0; w < waves; ++w) {
       const int at = w % kLook, st = w % kStages;
-      if (!wait(bars, a.status, &bars->look_full[at], (w / kLook) & 1)) break;
-      if (!wait(bars, a.status, &bars->empty[st], ((w / kStages) & 1) ^ 1)) break;
+      if (!wait(bars, a, &bars->look_full[at], (w / kLook) & 1)) break;
+      if (!wait(bars, a, &bars->empty[st], ((w / kStages) & 1) ^ 1)) break;
       __syncwarp();
       const uint32_t bar = smem_u32(&bars->full[st]);
       if (lane < kRowsPerWarp) {
-        if (bars->dst[at][row] >= 0) {
+        if (a.debug_skip_tile && blockIdx.x == 0 && w == 0 && row == 0) {
+          // test aid: the first row never comes
+        } else if (bars->dst[at][row] >= 0) {
           mbar_expect_tx(bar, kRowBytes);
           bulk_load(smem_u32(smem + st * S::kStageBytes + row * kRowBytes),
                     a.cache + (int64_t)bars->src[at][row] * kRowBytes, kRowBytes, bar);
@@ -181,17 +184,17 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactArgs a, 
     // --------------------------------------------------------------- stores
     for (int w = 0; w < waves; ++w) {
       const int at = w % kLook, st = w % kStages;
-      if (!wait(bars, a.status, &bars->look_full[at], (w / kLook) & 1)) break;
+      if (!wait(bars, a, &bars->look_full[at], (w / kLook) & 1)) break;
       const int dst = lane < kRowsPerWarp ? bars->dst[at][row] : -1;
       const float weight = lane < kRowsPerWarp ? bars->weight[at][row] : 0.f;
-      if (!wait(bars, a.status, &bars->full[st], (w / kStages) & 1)) break;
+      if (!wait(bars, a, &bars->full[st], (w / kStages) & 1)) break;
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars->look_empty[at]));
       // every row of the wave is in some CTA's shared memory before one is
       // written (the arrivals order nothing but this: those rows have been read)
       if (ctas > 1) {
         if (warp == kWarpStore && lane < ctas) mbar_arrive_remote(mapa(smem_u32(&bars->go[at]), lane));
-        if (!wait(bars, a.status, &bars->go[at], (w / kLook) & 1)) break;
+        if (!wait(bars, a, &bars->go[at], (w / kLook) & 1)) break;
         __syncwarp();
       }
       if (dst >= 0) {

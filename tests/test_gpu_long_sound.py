@@ -1,6 +1,8 @@
 """Calls of the operators of long contexts whose results hang on an order between
 warps or CTAs, and ways out of a wait.  Plain forms and tolerances are those of
 the operators' own tests."""
+import time
+
 import numpy as np
 import pytest
 import torch
@@ -8,8 +10,9 @@ import torch
 pytestmark = pytest.mark.gpu
 
 if torch.cuda.is_available():
+    import long_ref
     import mla_latent_kv_15_gb300 as mla
-    from test_gpu_evict import SCALE, Weights
+    from test_gpu_evict import SCALE, Weights, check_compact, i32, subset
 
 
 @pytest.mark.parametrize("heads,sq,page", [(16, 1, 64), (40, 2, 32), (128, 1, 16), (128, 3, 64), (128, 8, 256)])
@@ -33,3 +36,46 @@ def test_key_weights_of_e4m3_rows_are_those_of_the_same_rows_in_bf16(heads, sq, 
     w.weights = got["bf16"]
     w.old, w.decay = torch.zeros_like(w.weights), 0.0
     w.check()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("lengths", [[3000], [900, 40], [700] * 160])        # clusters of many CTAs, of some, of one
+def test_compact_wait_that_runs_out(lengths, fp8):
+    rng = np.random.default_rng(len(lengths))
+    keeps = [subset(rng, n, n // 2) for n in lengths]
+    p = long_ref.Pages(lengths, 64, fp8, seed=91)
+    keep = torch.full((len(lengths), max(len(k) for k in keeps)), -1, dtype=torch.int32)
+    for b, k in enumerate(keeps):
+        keep[b, :len(k)] = torch.as_tensor(k.astype(np.int32))
+    keep, lens, status = keep.cuda(), i32([len(k) for k in keeps]), i32([0])
+    raw = p.cache.view(torch.uint8).view(-1, p.cache.element_size() * 576)
+    before = raw.clone()
+    torch.cuda.synchronize()
+    t0 = time.perf_counter()
+    try:
+        mla.set_decode_wait_test(True, 2_000_000)
+        mla.cache_compact(p.cache, p.table, keep, lens, status=status)
+        torch.cuda.synchronize()
+    finally:
+        mla.set_decode_wait_test(False, 0)
+    assert time.perf_counter() - t0 < 5.0
+    assert status.item() == mla.DEVERR_TIMEOUT
+    # only rows of the kept ones' places were written, and with rows of the same request
+    places = torch.cat([p.slots(b, len(k)) for b, k in enumerate(keeps)])
+    left = torch.ones(raw.shape[0], dtype=torch.bool, device="cuda")
+    left[places] = False
+    assert torch.equal(raw[left], before[left])
+    for b, k in enumerate(keeps):
+        at = p.slots(b, len(k))
+        new = before[p.slots(b, lengths[b])[torch.as_tensor(k, device="cuda")]]
+        assert ((raw[at] == new).all(1) | (raw[at] == before[at]).all(1)).all()
+    check_compact(lengths, keeps, 64, fp8)           # the next call
+
+
+def test_compact_takes_no_more_than_its_wait_limit_allows_for():
+    # a limit far above a call's time, no row left out: nothing runs out
+    try:
+        mla.set_decode_wait_test(False, 50_000_000)
+        check_compact([3000, 17], [np.arange(1500, 3000), np.arange(17)], 64)
+    finally:
+        mla.set_decode_wait_test(False, 0)
