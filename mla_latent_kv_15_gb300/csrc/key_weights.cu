@@ -245,6 +245,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kKind>::kThrea
     const int n = a.seq_lens[b];
     return n < 0 ? 0 : (n > cap ? cap : n);
   };
+  // a request's query tokens, -1 where they are not within total_q; the first of them
+  auto tokens_of = [&](int b, int& q0) {
+    q0 = a.qsl ? a.qsl[b] : b;
+    const int q1 = a.qsl ? a.qsl[b + 1] : b + 1;
+    return q0 >= 0 && q0 <= q1 && q1 <= a.total_q ? q1 - q0 : -1;
+  };
   auto tiles_of = [&](int b) { return b < a.batch ? (keys_of(b) + kPairKeys - 1) / kPairKeys : 0; };
   // the pair's share of all tiles: a sum over the batch, then the request that
   // holds the share's first tile
@@ -273,7 +279,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kKind>::kThrea
     long long before0 = 0;                       // of the first kThreads requests, kept for the search
     for (int base = 0; base < a.batch; base += kThreads) {
       const int b = base + tid;
-      if (blockIdx.x == 0 && b < a.batch && a.seq_lens[b] > cap) raise(ctx, 2);   // MLA_DEVERR_BAD_SEQ_LEN
+      if (blockIdx.x == 0 && b < a.batch) {   // every request, those without keys too
+        int q0;
+        if (a.seq_lens[b] > cap) raise(ctx, 2);   // MLA_DEVERR_BAD_SEQ_LEN
+        if (tokens_of(b, q0) < 0) raise(ctx, 8);  // MLA_DEVERR_BAD_QSL
+      }
       total += block_sum(tiles_of(b), before);
       if (base == 0) before0 = before;
     }
@@ -321,12 +331,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kKind>::kThrea
   auto request = [&](int b) {
     Request r;
     r.n = keys_of(b);
-    r.q0 = a.qsl ? a.qsl[b] : b;
-    r.sq = a.qsl ? a.qsl[b + 1] - r.q0 : 1;
-    if (r.sq < 0 || r.q0 < 0 || r.q0 > a.total_q - r.sq) {
-      raise(ctx, 8);   // MLA_DEVERR_BAD_QSL
-      r.sq = 0;
-    }
+    r.sq = max(tokens_of(b, r.q0), 0);
     r.rows = r.sq * a.num_heads;
     r.row_tiles = (r.rows + width - 1) / width;
     return r;

@@ -79,3 +79,37 @@ def test_compact_takes_no_more_than_its_wait_limit_allows_for():
         check_compact([3000, 17], [np.arange(1500, 3000), np.arange(17)], 64)
     finally:
         mla.set_decode_wait_test(False, 0)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("bounds", [[0, 2, 50, 50], [0, 2, 50, 4], [0, -1, 2, 4], [0, 2, 1, 4], [-2147483648, 2, 2, 4],
+                                    [0, 2147483647, -2147483648, 4], [0, 2, 4, 5]])
+def test_key_weights_query_range_of_a_request_without_keys(bounds, fp8):
+    # a request whose tokens are not within the call's counts as without query rows
+    # and is reported, whether it has keys or none
+    for lengths in ([300, 0, 0], [0, 300, 200], [300, 200, 0], [0, 0, 0], [300, -5, 1]):
+        w = Weights([max(n, 0) for n in lengths], 16, [2, 1, 1], 64, fp8, seed=92)
+        w.seq_lens.copy_(torch.tensor(lengths, dtype=torch.int32))
+        w.qsl.copy_(torch.tensor(bounds, dtype=torch.int32))
+        w.run(0.5)
+        torch.cuda.synchronize()
+        assert w.status.item() == 8
+        for b, n in enumerate(lengths):
+            lo, hi = bounds[b:b + 2]
+            assert torch.equal(w.weights[b, max(n, 0):], w.old[b, max(n, 0):])
+            if not 0 <= lo <= hi <= 4 and n > 0:
+                assert torch.equal(w.weights[b, :n], w.old[b, :n] * 0.5)
+    w = Weights([300, 0, 0], 16, [2, 1, 1], 64, fp8, seed=92)
+    w.run(0.5).check()                       # padded requests whose tokens are the call's
+
+
+def test_key_weights_bad_query_range_of_a_late_request():
+    # behind more requests than a block has threads
+    w = Weights([3] * 700 + [0] * 3, 2, [1] * 702 + [2], 16, seed=93)
+    w.qsl[703] = 10 ** 6
+    w.run(0.0)
+    torch.cuda.synchronize()
+    assert w.status.item() == 8
+    w.status.zero_()
+    w.qsl[703] = 704
+    w.run(0.0).check()
