@@ -10,9 +10,11 @@ import torch
 pytestmark = pytest.mark.gpu
 
 if torch.cuda.is_available():
+    import exact_scores
     import long_ref
     import mla_latent_kv_15_gb300 as mla
     from test_gpu_evict import SCALE, Weights, check_compact, i32, subset
+    from test_gpu_shared import Case
 
 
 @pytest.mark.parametrize("heads,sq,page", [(16, 1, 64), (40, 2, 32), (128, 1, 16), (128, 3, 64), (128, 8, 256)])
@@ -113,3 +115,50 @@ def test_key_weights_bad_query_range_of_a_late_request():
     w.status.zero_()
     w.qsl[703] = 704
     w.run(0.0).check()
+
+
+@pytest.mark.parametrize("prefix,own,heads,sq,fp8", [
+    ([(300, 3), (70, 1)], [40, 1, 200, 64], 16, 1, False),
+    ([(450, 2)], [100, 333], 128, 1, False),               # full rows, fewer than 512 keys
+    ([(3000, 4)], [100, 7, 64, 300], 16, 1, False),        # long prefixes of 64 rows
+    ([(2999, 2), (0, 1)], [100, 65, 700], 32, 1, False),
+    ([(3000, 5)], [100, 7, 64, 300, 1], 128, 1, True), ([(513, 3)], [10, 700, 64], 40, 2, True),
+])
+def test_shared_log_sum_exp_where_scores_are_exchanged_as_they_are(prefix, own, heads, sq, fp8):
+    # whole numbers, whose scores are exact in float32: codes in the exchange would
+    # put rows further off (tests/test_exact_scores_cpu.py)
+    c = Case(prefix, own, heads, sq, 64, fp8, seed=len(own) + heads, scale=exact_scores.SCALE)
+    p = c.pages
+    p.kv_scale = 1.0
+    c.q_abs, c.q_pe = (exact_scores.queries(t.shape, p.g) for t in (c.q_abs, c.q_pe))
+    flat = p.cache.view(-1, 576)
+    for i, n in enumerate(p.lengths):
+        if n:
+            rows = exact_scores.keys((n, 576), p.g)
+            if fp8:
+                p.cache.view(torch.uint8).view(-1, 576)[p.slots(i, n)] = rows.float().to(torch.float8_e4m3fn).view(torch.uint8)
+            else:
+                flat[p.slots(i, n)] = rows
+    c.run().check()
+    q = torch.cat([c.q_abs, c.q_pe], dim=2).double()
+    for b, n in enumerate(c.own):
+        g = int(np.searchsorted(c.begin, b, side="right")) - 1
+        keys = torch.cat([p.rows(g), p.rows(len(prefix) + b)])
+        for t in range(c.sq[b]):
+            row = int(c.at[b]) + t
+            s = c.scale * (q[row] @ keys[:c.prefix[g][0] + n - c.sq[b] + 1 + t].t())
+            lse = torch.logsumexp(s, dim=1)
+            err = (c.lse[row].double() - lse).abs()
+            assert (err <= exact_scores.lse_bar(s, lse)).all(), (b, t, (err / exact_scores.lse_bar(s, lse)).max())
+
+
+@pytest.mark.parametrize("decay", [0.0, 0.5])
+@pytest.mark.parametrize("page", [16, 64, 256])
+def test_key_weights_of_requests_with_and_without_query_rows(page, decay):
+    # None, one and several tiles of query rows a request, in either order, where
+    # e4m3 codes go straight into registers: a request without rows or without keys
+    # must leave the turns of those behind it as they are
+    lengths, sq = [700, 0, 129, 1500, 1], [2, 0, 9, 1, 0]
+    for n, t in ((lengths, sq), (lengths[::-1], sq[::-1]), ([300, 700, 0, 900, 257], [0, 9, 3, 0, 9])):
+        for fp8 in (True, False):
+            Weights(n, 128, t, page, fp8, seed=94).run(decay).check()
