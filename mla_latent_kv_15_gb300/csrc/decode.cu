@@ -231,13 +231,15 @@ __device__ __forceinline__ void raise_error(const Ctx& c, int bit) {
 }
 
 // Bounded waits on this CTA's own pipeline; once the CTA has aborted they
-// return at once.
-__device__ __forceinline__ void wait_bar(const Ctx& c, uint64_t* bar, uint32_t parity) {
+// return at once.  True if the phase has completed.
+__device__ __forceinline__ bool wait_bar(const Ctx& c, uint64_t* bar, uint32_t parity) {
   // a completed phase is taken at once (aborted or not); the abort flag is
   // read only when the wait would block
-  if (mbar_try_wait(smem_u32(bar), parity)) return;
-  if (*(volatile int*)&c.bars->abort) return;
-  if (!mbar_wait(smem_u32(bar), parity, c.limit_ns)) raise_error(c, 1);
+  if (mbar_try_wait(smem_u32(bar), parity)) return true;
+  if (*(volatile int*)&c.bars->abort) return false;
+  if (mbar_wait(smem_u32(bar), parity, c.limit_ns)) return true;
+  raise_error(c, 1);
+  return false;
 }
 // Bounded wait for the peer's partial scores.  It is kept after an abort
 // (with a 1 ms bound): the peer's stores into this CTA's receive buffers must
@@ -508,6 +510,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kTh
     const bool leader = lane == 0;
     if (leader) {
       uint32_t item = 0;
+      // A slot is loaded only once it has been handed back, and handed back only
+      // when its last load has landed (`landed` below): a barrier that counts
+      // bytes must not take an arrival before the bytes of the one before.  So
+      // loads stop where the CTA gives up.
+      auto may_load = [&](uint32_t slot, uint32_t round) {
+        return wait_bar(ctx, &bars->kv_empty[slot], (round & 1) ^ 1);
+      };
+      bool go = true;
       const int sub_rows = a.page_size < kTile ? a.page_size : kTile;
       const int nsub = kTile / sub_rows;
       const int oob_row = a.num_blocks * a.page_size;  // first row past the cache: reads zeros
@@ -515,7 +525,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kTh
       // cache lines are read once per pair: evict them first, so that the
       // split-KV partials, queries and block tables stay in L2
       const uint64_t pol = l2_policy_evict_first();
-      for (int u = ubeg; u < uend; ++u) {
+      for (int u = ubeg; u < uend && go; ++u) {
         const UnitRec ur = P.units[u];
         const UnitRec& gr = ur;
         const bool prefix = kShared && gr.b < 0;
@@ -542,10 +552,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kTh
         };
         const int ntiles = ur.tile_end - ur.tile_begin;
         // the CTA's 288 query dims for rows 0-63, then 64-127
-        for (int half = 0; half < 2; ++half, ++item) {
-          if (!leader) continue;
+        for (int half = 0; half < 2 && go; ++half, ++item) {
           const uint32_t slot = item % kStages, round = item / kStages;
-          wait_bar(ctx, &bars->kv_empty[slot], (round & 1) ^ 1);
+          go = may_load(slot, round);
+          if (!go) break;
           const uint32_t st = smem_u32(stages + slot * kStageBytes);
           const int y = gr.row0 + 64 * half;
           if constexpr (kQ8) {
@@ -568,7 +578,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kTh
             if (kCacheFp8) mbar_arrive(smem_u32(&bars->stg_full[slot]));
           }
         }
-        for (int jj = 0; jj < ntiles; ++jj, ++item) {
+        for (int jj = 0; jj < ntiles && go; ++jj, ++item) {
           // test aid: CTA 0 of cluster 0 never loads its first cache tile, so
           // a consumer's bounded wait for it runs out (kShared: the plan's
           // first unit, whichever cluster has it)
@@ -585,7 +595,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kTh
               if (sb >= nsub) break;
               ys[sb] = lookup(ur.tile_begin + jj, sb);
             }
-            wait_bar(ctx, &bars->kv_empty[slot], (round & 1) ^ 1);
+            go = may_load(slot, round);
+            if (!go) break;
             if constexpr (!kCacheFp8) {
               const uint32_t full = smem_u32(&bars->kv_full[slot]);
               mbar_expect_tx(full, kStageBytes);
@@ -630,12 +641,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kTh
         }
       }
       // drain: every issued load has landed before the CTA may exit (with an
-      // e4m3 query every item's loads complete on stg_full)
-      if (leader) {
-        const uint32_t first = item > kStages ? item - kStages : 0;
-        for (uint32_t k = first; k < item; ++k)
-          mbar_wait(smem_u32(kQ8 ? &bars->stg_full[k % kStages] : &bars->kv_full[k % kStages]), (k / kStages) & 1,
-                    a.wait_limit_ns);
+      // e4m3 query every item's loads complete on stg_full).  Given up: loads in
+      // flight finish well within this time
+      const uint32_t first = item > kStages ? item - kStages : 0;
+      for (uint32_t k = first; go && k < item; ++k)
+        wait_bar(ctx, kQ8 ? &bars->stg_full[k % kStages] : &bars->kv_full[k % kStages], (k / kStages) & 1);
+      if (*(volatile int*)&bars->abort) {
+        const uint64_t t0 = globaltimer();
+        while (globaltimer() - t0 < kAbortWaitNs) {
+        }
       }
     }
     __syncwarp();
@@ -668,7 +682,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kTh
           if constexpr (kQ8) {
             // fp8 x fp8: the e4m3 boxes are read as they landed, 9 MMAs of K = 32
             // (8 over the two 128-dim latent boxes, 1 over the 32-dim rope box)
-            wait_bar(ctx, &bars->stg_full[slot], round & 1);
+            const bool landed = wait_bar(ctx, &bars->stg_full[slot], round & 1);
             wait_bar(ctx, &bars->s_free, (it & 1) ^ 1);
             tc_fence_after();
             constexpr uint32_t id_s8 = idesc_e4m3_f32(128, kTile);
@@ -682,11 +696,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kTh
                 mma_ts_f8(d, qa + 32 * p + 8 * k, kd8 + ((p * kQ8Box + k * 32) >> 4), id_s8, (p | k) ? 1u : 0u);
             mma_ts_f8(d, qa + 64, kr8, id_s8, 1u);
             mma_commit(smem_u32(&bars->s_full));
-            mma_commit(smem_u32(&bars->kv_empty[slot]));
+            if (landed) mma_commit(smem_u32(&bars->kv_empty[slot]));
             mma_commit(smem_u32(&bars->kx_free[slot]));
             continue;
           }
-          wait_bar(ctx, &bars->kv_full[slot], round & 1);
+          const bool landed = wait_bar(ctx, &bars->kv_full[slot], round & 1);
           wait_bar(ctx, &bars->s_free, (it & 1) ^ 1);
           tc_fence_after();
           const uint64_t kd = kv_desc0 + slot * kStageDesc;
@@ -699,7 +713,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kTh
 #pragma unroll
           for (int k = 0; k < 2; ++k) mma_ts(d, qa + 128 + k * 8, kr + ((k * 32) >> 4), id_s, 1u);
           mma_commit(smem_u32(&bars->s_full));
-          mma_commit(smem_u32(&bars->kv_empty[slot]));
+          if (landed) mma_commit(smem_u32(&bars->kv_empty[slot]));
         }
       }
       mma_commit(smem_u32(&bars->s_drain));
@@ -721,7 +735,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kTh
         item += 2;
         for (int jj = 0; jj < ntiles; ++jj, ++item, ++it) {
           const uint32_t slot = item % kStages, round = item / kStages;
-          wait_bar(ctx, &bars->kv_full[slot], round & 1);
+          const bool landed = wait_bar(ctx, &bars->kv_full[slot], round & 1);
           if constexpr (kCleans) {
             const int live = ur.lmax - (ur.tile_begin + jj) * kTile;   // keys from here on are behind the last
             if (live < kTile) {
@@ -743,7 +757,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kTh
 #pragma unroll
             for (int k = 1; k < kTile / 16; ++k) mma_ts(tbase + kTmemO, pa + 8 * k, vd + ((k * 2048) >> 4), id_pv, 1);
             mma_commit(smem_u32(&bars->p_free));
-            mma_commit(smem_u32(&bars->kv_empty[slot]));
+            if (landed) mma_commit(smem_u32(&bars->kv_empty[slot]));
           }
         }
         if (!kCleans || lane == 0) mma_commit(smem_u32(&bars->o_full));
@@ -797,9 +811,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kTh
         }
         fence_proxy_async_smem();    // bf16 writes visible to the MMAs
         named_bar_expand();
-        if (te == 0) {
-          mbar_arrive(smem_u32(&bars->kv_full[slot]));
-        }
+        // (not once the CTA has given up: a query's load may be on its way to the slot)
+        if (te == 0 && *(volatile int*)&bars->abort == 0) mbar_arrive(smem_u32(&bars->kv_full[slot]));
       }
     }
   };
@@ -1078,11 +1091,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kVariant>::kTh
         if (lane == 0) bulk_wait_group_read<0>();
       named_bar_softmax();
       if (tid == 0) {
-        for (int qi = 0; qi < 2; ++qi) {      // two arrivals: the slot's count covers both issuers
+        mbar_arrive(smem_u32(&bars->q_ready));
+        // two arrivals: the slot's count covers both issuers (a half of the query
+        // that has not landed: the flag is set)
+        for (int qi = 0; qi < 2 && *(volatile int*)&bars->abort == 0; ++qi) {
           mbar_arrive(smem_u32(&bars->kv_empty[(item + qi) % kStages]));
           mbar_arrive(smem_u32(&bars->kv_empty[(item + qi) % kStages]));
         }
-        mbar_arrive(smem_u32(&bars->q_ready));
       }
       item += 2;
 
