@@ -621,8 +621,14 @@ MLA_API int mla_decode_shared(const void* q_abs, const void* q_pe, const void* c
  *                log-sum-exp, as mla_decode returns it (the weights of a row
  *                then add up to 1) or mla_decode_shared (block_table and
  *                seq_lens the requests' own: the weights of their own keys).
- *                A row with lse = -inf gives no weight
- *   decay        finite, >= 0; 0: the old weights are not read
+ *                A row with lse = -inf gives no weight.  (That of
+ *                mla_decode_fp8q belongs to the scores of the rounded query: the
+ *                weights of the bf16 query's scores are then off by its rounding)
+ *   decay        finite, >= 0; 0: the old weights are not read.  Else every key
+ *                below seq_lens[b] needs one: a key that has come since the last
+ *                call starts from 0, which the caller writes (what stands there
+ *                may be an evicted key's: mla_cache_compact leaves the weights
+ *                behind the kept ones)
  *   weights      float32, weight_len a request at weights + b * weight_stride
  *                elements (weight_stride in [weight_len, 2^32])
  *   q_abs, q_pe, cache (bf16 or e4m3), page_size, block_table, seq_lens,
@@ -674,7 +680,8 @@ MLA_API int mla_evict_select(const float* weights, int64_t weight_stride, int we
  * where row p is cache[block_table[b, p / page_size], p % page_size].  All rows
  * are read as they were before the call.  Afterwards keep_lens are the
  * requests' lengths and the pages behind them are free; rows (and weights) from
- * keep_lens[b] on are left as they were.  Keys keep the rotation of the position
+ * keep_lens[b] on are left as they were: a key written there later starts from the
+ * weight that the caller sets, 0.  Keys keep the rotation of the position
  * they were written at.
  *   keep         [batch, max_keep] int32, keep[b, i] >= i (mla_evict_select's).
  *                An entry below i, or beyond the table or weight_len, sets

@@ -679,8 +679,9 @@ def key_weights(q_abs, q_pe, cache, block_table, seq_lens, lse, weights, *, scal
     of request b gets from all the query rows that see it, for j < seq_lens[b]
     (``weights`` [B, W] float32, rows may be further apart).  ``lse`` [T, N] is
     the rows' log-sum-exp: decode()'s, or decode_shared()'s with the requests'
-    own block table and lengths.  decay 0 does not read the old weights.  Errors
-    are OR-ed into ``status`` [1] int32."""
+    own block table and lengths.  decay 0 does not read the old weights; else a
+    key that has come since the last call needs a weight of 0 in its place (an
+    evicted key's may stand there).  Errors are OR-ed into ``status`` [1] int32."""
     torch = _pytorch or _torch()
     i32, f32 = torch.int32, torch.float32
     T, N = _query(q_abs, q_pe, torch.bfloat16)

@@ -270,7 +270,9 @@ int decode_impl(const void* q_abs, const void* q_pe, const void* q8, float q_sca
   const int small_rows = !shared && !q8 && cache_dtype == MLA_BF16 && num_heads <= 32 && total_q == batch;
   const int variant = q8 ? 3 : (cache_dtype == MLA_FP8_E4M3 ? 1 : (small_rows ? 2 : 0));
   // whether a plan of this call may have long units of many rows (a pair's span of
-  // the axis holds no more tiles than its share)
+  // the axis holds no more tiles than its share).  By the tables' width, since the
+  // lengths are the device's: 8 requests of 16 heads behind 512 keys take 15.9 us,
+  // with tables 32768 keys wide 17.5
   const int long_units =
       shared && rows > 64 &&
       (num_splits > 0 ? std::max(max_pages_per_seq, shared->max_pages) * (int64_t)page_size >= mla::kCodedTiles * mla::kTile

@@ -12,9 +12,11 @@
 // threshold in its part of the slice, and writes its kept indices behind those
 // of the warps before it.
 //
-// A weight is read from memory once.  Bound by the chain of passes: 128 requests
-// of 8192 to 32768 keys take 13.4 us where the weights' bytes need 1.8.  The last of
-// them has its codes and the first histogram after 3.7, the three digits after 4.3,
+// A weight is read from memory once.  128 requests of 8192 to 32768 keys take 13.4
+// us where the weights' bytes need 1.8: a chain of passes in one CTA a request, on
+// 128 of 152 SMs, and as much the passes' instructions (58 % of the issue slots, 4.9
+// M warp instructions for 1.05 M keys; the longest request is the time of all).  The
+// last of them has its codes and the first histogram after 3.7, the three digits after 4.3,
 // 6.7 and 8.1, its votes after 10.8 and its indices after 12.6; one request of 4096
 // keys (7.1) 1.9, 2.5, 3.5, 4.2, 5.0 and 6.2.  Eight loads of four weights are in
 // flight a thread; the kept keys come from votes that a lane holds for 32 keys, so
@@ -286,7 +288,11 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const SelectArgs a,
 }  // namespace
 
 cudaError_t launch_select(const SelectArgs& a, int sm_count, cudaStream_t s) {
-  // CTAs a request: a few keys a thread, all requests' on the card at once
+  // CTAs a request: a few keys a thread, all requests' on the card at once.  Both
+  // this and whether codes are held go by the rows' width, the most keys a request
+  // can have, since the lengths are the device's: rows far wider than their requests
+  // are long cost 7 us (one request of 4096 keys 7.1, in rows of 40960 14.6; 128 of
+  // 8192 to 32768 13.6, in rows of 40960 or 131072 21.1)
   int ctas = 1;
   while (ctas < 8 && (int64_t)a.batch * ctas * 2 <= sm_count && ctas * kThreads * 8 < a.weight_len) ctas *= 2;
   const int64_t part = (((int64_t)a.weight_len + 3 + ctas * kWarps - 1) / (ctas * kWarps) + 127) / 128 * 128;

@@ -13,7 +13,7 @@ if torch.cuda.is_available():
     import exact_scores
     import long_ref
     import mla_latent_kv_15_gb300 as mla
-    from test_gpu_evict import SCALE, Weights, check_compact, i32, subset
+    from test_gpu_evict import SCALE, Weights, check_compact, check_select, i32, subset
     from test_gpu_shared import Case
 
 
@@ -162,3 +162,50 @@ def test_key_weights_of_requests_with_and_without_query_rows(page, decay):
     for n, t in ((lengths, sq), (lengths[::-1], sq[::-1]), ([300, 700, 0, 900, 257], [0, 9, 3, 0, 9])):
         for fp8 in (True, False):
             Weights(n, 128, t, page, fp8, seed=94).run(decay).check()
+
+
+@pytest.mark.parametrize("heads,sq,fp8", [(16, 1, False), (128, 1, False), (128, 1, True), (40, 2, True)])
+def test_shared_results_are_the_same_every_time(heads, sq, fp8):
+    # whatever the workspace held, alone and beside another kernel
+    rng = np.random.default_rng(heads)
+    c = Case([(5000, 20), (700, 12)], [int(x) for x in rng.integers(1, 1500, 32)], heads, sq, 64, fp8, seed=heads + sq).run().check()
+    out, lse = c.out.clone(), c.lse.clone()
+    a, s = torch.randn(2048, 2048, device="cuda", dtype=torch.bfloat16), torch.cuda.Stream()
+    for i in range(20):
+        c.workspace.random_(0, 256) if i % 3 else c.workspace.fill_(255)
+        c.out.fill_(float("nan"))
+        c.lse.fill_(float("nan"))
+        torch.cuda.synchronize()
+        if i % 2:
+            with torch.cuda.stream(s):
+                a @ a
+        c.run()
+        torch.cuda.synchronize()
+        assert mla.decode_status(c.workspace) == 0
+        assert torch.equal(c.out, out) and torch.equal(c.lse, lse)
+
+
+@pytest.mark.parametrize("width", [41000, 131072])
+def test_select_in_rows_far_wider_than_the_requests(width):
+    # the width decides how many CTAs a request has and where its codes are; most
+    # of them then have no key, or none that competes
+    g = torch.Generator(device="cuda").manual_seed(width)
+    for lengths, budget, sinks, recent in (([300], 64, 4, 16), ([9000, 0, 1, 4097, 513, width], 512, 4, 64),
+                                           ([700] * 90, 100, 0, 0), ([130], 129, 100, 28)):
+        w = torch.full((len(lengths), width), 1e9, device="cuda")
+        for b, n in enumerate(lengths):
+            w[b, :n] = torch.rand(n, generator=g, device="cuda").mul(50).round()
+        check_select(w, lengths, budget, sinks, recent)
+
+
+@pytest.mark.parametrize("heads,fp8", [(16, False), (128, False), (16, True)])
+def test_shared_with_tables_far_wider_than_the_requests(heads, fp8):
+    # the width decides which kernel a call gets
+    c = Case([(512, 5), (70, 3)], [10, 64, 1, 200, 333, 7, 90, 129], heads, 1, 64, fp8, seed=95)
+    c.run().check()
+    for name in ("prefix_table", "block_table"):
+        t = getattr(c, name)
+        wide = torch.full((t.shape[0], 600), -1, dtype=torch.int32, device="cuda")
+        wide[:, :t.shape[1]] = t
+        setattr(c, name, wide)
+    c.run().check()
