@@ -23,18 +23,17 @@
 // ahead would not wait).  Where they are more, shared memory is what bounds the
 // kernel (see below), and eight warps take the codes from global memory into their
 // registers (kDirect).  32 requests of 2048 to 16384 keys, kCodes and kDirect: 128
-// rows 77 and 92 us, 192 80 and 95, 256 84 and 98, with too little on its way; 320
-// rows 117 and 115, 384 129 and 117, 512 136 and 123.
+// rows 67 and 92 us, 192 73 and 94, 256 77 and 97, with too little on its way; 320
+// rows 101 and 104, 384 121 and 107, 512 131 and 115.
 //
 // Measured (a launch in a graph): 64 requests of 1024 to 8192 keys, 128 heads,
 // bf16 60.4 us, HBM at 90 % of the copy rate; 32 requests of 2048 to 16384 keys
 // with four verified tokens (512 rows) 105 in bf16, 92 % of the tensor cores' rate,
-// and 124 over e4m3 rows: there shared memory takes the expanded rows (in kCodes the
+// and 115 over e4m3 rows: there shared memory takes the expanded rows (in kCodes the
 // codes too, and gives them back) and gives them to two row tiles' products beside
-// the queries, and what the second CTA expanded is released to the leader (see
-// pass_on).  In kCodes that release is part of a chain: a chunk's place is free,
-// its codes are widened, released, multiplied, and the place is free again once a
-// tile (128 rows 77, 64 requests of 16 heads 143, where bf16 rows take 59 and 108).
+// the queries.  kCodes is bound by a chain: a chunk's place is free, its codes are
+// widened, released to the leader, multiplied, and the place is free again once a
+// tile (128 rows 67, 64 requests of 16 heads 122, where bf16 rows take 59 and 110).
 // One request of 777 keys and 16 heads 7.0: a chain of loads, nine chunks' products
 // and the sums.
 #include <cuda_bf16.h>
@@ -88,7 +87,6 @@ struct Shape {
 struct Bars {
   uint64_t k_full[kChunks], q_full[kMaxQStages];  // (lead) both CTAs' halves are there
   uint64_t k_empty[kChunks], q_empty[kMaxQStages];
-  uint64_t k_here[kChunks / kRawChunks];   // e4m3: the second CTA's expanded chunks, three at a time
   uint64_t raw_full[kExpandWarps], raw_empty[kExpandWarps];
   uint64_t d_full[4];
   uint64_t d_empty[4];             // (lead) the epilogue warps of both CTAs
@@ -209,11 +207,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kKind>::kThrea
 
   if (tid == 0) {
     for (int i = 0; i < S::kKSlots; ++i) {
-      // each CTA's load, or the leader's expanded loads and the other CTA's word of its own
-      mbar_init(smem_u32(&bars->k_full[i]), kFp8 ? kKeys / kRawKeys + 1 : 2);
+      mbar_init(smem_u32(&bars->k_full[i]), kFp8 ? 2 * kKeys / kRawKeys : 2);   // each CTA's load, or expanded loads
       mbar_init(smem_u32(&bars->k_empty[i]), 1);
     }
-    for (int i = 0; i < kChunks / kRawChunks; ++i) mbar_init(smem_u32(&bars->k_here[i]), kKeys / kRawKeys);
     for (int i = 0; i < kMaxQStages; ++i) {
       mbar_init(smem_u32(&bars->q_full[i]), 2);
       mbar_init(smem_u32(&bars->q_empty[i]), 1);
@@ -470,27 +466,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kKind>::kThrea
       wait(ctx, &bars->drain, 0);
     }
   };
-  auto pass_on = [&]() {
-    // ------------------------- e4m3: the second CTA's expanded keys, to the leader
-    // Plain writes to shared memory that the leader's products read need a release
-    // at the cluster's scope.  It takes some 1700 cycles, so the expanding warps leave
-    // it to this one, which has nothing else to do (a release by each of them: 512
-    // rows 135 us instead of 124, 128 rows 91 instead of 77, 16 heads 158 instead of
-    // 143; three warps that release three chunks each: 128, 85, 157, since releases
-    // of a CTA hold one another up).
-    if (rank == 1) {
-      uint32_t tile = 0;
-      for_tiles([&](int, const Request& r, int) {
-        if (r.row_tiles == 0) return;
-        for (int c = 0; c < kChunks; c += kRawChunks) {
-          if (!wait_warp(ctx, &bars->k_here[c / kRawChunks], tile & 1)) return;
-          if (lane < kRawChunks) mbar_arrive_release_cluster(mapa(smem_u32(&bars->k_full[c + lane]), 0));
-          __syncwarp();
-        }
-        ++tile;
-      });
-    }
-  };
   auto epilogue = [&]() {
     // --------------------------------------------------------------- epilogue
     const int e = tid - 32 * kWarpEpilogue;      // 0..255
@@ -589,13 +564,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kKind>::kThrea
       }
     }
     // the writes are in this CTA's shared memory, for the tensor cores to read,
-    // before the leader hears of them: of the other CTA's by pass_on()
+    // before the leader hears of them: of the other CTA's by a release to the
+    // cluster.  (It covers shared memory alone: one of all memory takes some 1700
+    // cycles, 512 rows then 135 us instead of 115, 16 heads 158 instead of 122; by one
+    // warp for all of them 124 and 140.)
     fence_proxy_async_smem();
     __syncwarp();
-    if (rank == 0) {
-      if (lane < kRawChunks) mbar_arrive(smem_u32(&bars->k_full[c + lane]));
-    } else if (lane == 0) {
-      mbar_arrive(smem_u32(&bars->k_here[c / kRawChunks]));
+    if (lane < kRawChunks) {
+      if (rank == 0)
+        mbar_arrive(smem_u32(&bars->k_full[c + lane]));
+      else
+        mbar_arrive_release_smem_cluster(mapa(smem_u32(&bars->k_full[c + lane]), 0));
     }
   };
   auto expand = [&]() {
@@ -695,12 +674,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kKind>::kThrea
       setmaxnreg_dec<kRegsIssue>();
       if constexpr (kKind == kCodes)
         if (warp == kWarpK) load_keys();
-      if (warp == kWarpQ) {
+      if (warp == kWarpQ)
         load_queries();
-      } else if (warp == kWarpMma) {
+      else if (warp == kWarpMma)
         multiply();
-        pass_on();
-      }
     } else if (warp < kWarpExpand) {
       setmaxnreg_inc<kKind == kDirect ? kRegsDirect : kRegsEpilogue>();
       epilogue();

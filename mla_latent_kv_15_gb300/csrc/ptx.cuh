@@ -381,12 +381,19 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
 // Arrivals on a barrier of either CTA of the cluster (a shared::cluster
 // address).  The plain ones order what the tensor cores and the copies do; the
 // cluster-scope release, which also orders plain writes to shared memory for
-// the other CTA, waits for all earlier memory accesses (about 1000 cycles).
+// the other CTA, waits for all earlier memory accesses (about 1000 cycles); the
+// release of the CTA's own shared memory alone does not.
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void mbar_arrive_release_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_release_smem_cluster(uint32_t bar) {
+  asm volatile(
+      "fence.release.sync_restrict::shared::cta.cluster;\n"
+      " mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+      : "memory");
 }
 __device__ __forceinline__ void mbar_expect_tx_remote(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
